@@ -35,6 +35,8 @@ EXPORTED = [
     "eagle_op_lm_head_scratch_bytes", "eagle_op_lm_head",
     "eagle_op_attention_scratch_bytes", "eagle_op_attention", "eagle_plan_budget", "eagle_op_tree_scratch_bytes", "eagle_op_tree_build", "eagle_op_compact",
     "eagle_op_wait_probe",
+    "eagle_op_kv8_write", "eagle_op_kv8_read", "eagle_op_attention_kv8_scratch_bytes", "eagle_op_attention_kv8",
+    "eagle_op_attention_shared_kv8",
 ]
 
 
@@ -67,9 +69,17 @@ class Weights(C.Structure):
                 ("norm_e", C.c_void_p), ("draft", LayerWeights)]
 
 
+class KV8(C.Structure):
+    """eagle_kv8: one layer's 8-bit KV cache."""
+    _fields_ = [("k_code", C.c_void_p), ("v_code", C.c_void_p), ("k_exp", C.c_void_p), ("v_exp", C.c_void_p),
+                ("table", C.c_void_p), ("n_kv_heads", C.c_int), ("head_dim", C.c_int), ("max_batch", C.c_int),
+                ("cap", C.c_int), ("block", C.c_int), ("n_blocks", C.c_int)]
+
+
 _lib: Optional[C.CDLL] = None
 
 vp, i32, u32, u64, f32, sz = C.c_void_p, C.c_int, C.c_uint32, C.c_uint64, C.c_float, C.c_size_t
+i64 = C.c_int64
 
 
 def _declare(lib: C.CDLL) -> None:
@@ -114,6 +124,13 @@ def _declare(lib: C.CDLL) -> None:
         "eagle_op_tree_build": (i32, [vp, i32, i32, i32, i32] + [vp] * 15 + [sz]),
         "eagle_op_compact": (i32, [i32, vp, vp, vp, i32, i32, i32, i32, i32, vp, vp, vp, i32]),
         "eagle_op_wait_probe": (i32, [vp, i32, vp, vp, vp]),
+        "eagle_op_kv8_write": (i32, [vp, P(KV8), i32, vp, i64, vp, i64, i32, vp, vp, vp]),
+        "eagle_op_kv8_read": (i32, [vp, P(KV8), i32, vp, i64, vp, i64, i32, vp, vp, vp]),
+        "eagle_op_attention_kv8_scratch_bytes": (sz, [P(KV8), i32, i32, i32, i32]),
+        "eagle_op_attention_kv8": (i32, [vp, P(KV8), vp, vp, i32, i32, i32, vp, vp, vp, i32, i32, vp, i32, f32, vp,
+                                         sz, vp]),
+        "eagle_op_attention_shared_kv8": (i32, [vp, P(KV8), vp, vp, i32, vp, vp, i32, i32, i32, vp, vp, vp, i32, i32,
+                                                vp, i32, f32, vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)

@@ -381,3 +381,181 @@ def plan_budget(candidates, rows_pts: Sequence[int], verify_us: Sequence[float],
     L.check(lib.eagle_plan_budget(n_k, ks, dr, mm, ex, len(rows_pts), rp, vu, batch, C.byref(bk), C.byref(bm),
                                   C.byref(rate)), "eagle_plan_budget")
     return bk.value, bm.value, rate.value
+
+
+# ---- 8-bit KV cache -----------------------------------------------------------------------------
+def _need(ok: bool, what: str) -> None:
+    if not ok:
+        raise ValueError(what)
+
+
+def _device_guard(t: torch.Tensor):
+    """The tensor's device made current for a launch."""
+    return torch.cuda.device(t.device)
+
+
+class KV8Cache:
+    """One layer's 8-bit KV cache (eagle_kv8) over caller-owned tensors: k, v uint8 e4m3 codes and
+    k_exp, v_exp uint8 exponent bytes. Contiguous: [max_batch][nkv][cap][d] and [max_batch][nkv][cap];
+    with an int32 block table [max_batch][cap / block]: pools [n_blocks][nkv][block][d] and
+    [n_blocks][nkv][block]. The value of a code is code * 2^(byte - 127)."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_exp: torch.Tensor, v_exp: torch.Tensor,
+                 table: Optional[torch.Tensor] = None):
+        for t in (k, v, k_exp, v_exp):
+            _need(t.dtype == torch.uint8 and t.is_contiguous() and t.device == k.device,
+                  "cache tensors must be contiguous uint8 tensors of one device")
+        _need(k.dim() == 4 and k.shape == v.shape and k_exp.shape == k.shape[:3] and v_exp.shape == k.shape[:3],
+              "codes must be [B][nkv][cap][d] (or [n_blocks][nkv][block][d]) and exponents the same without d")
+        self.k, self.v, self.k_exp, self.v_exp, self.table = k, v, k_exp, v_exp, table
+        self.device = k.device
+        n, self.nkv, slots, self.d = k.shape
+        if table is None:
+            self.max_batch, self.cap, self.block, self.n_blocks = n, slots, 0, 0
+        else:
+            _need(table.dtype == torch.int32 and table.dim() == 2 and table.is_contiguous() and
+                  table.device == k.device, "table must be a contiguous int32 [max_batch][blocks] tensor")
+            self.max_batch, self.cap, self.block, self.n_blocks = table.shape[0], table.shape[1] * slots, slots, n
+        self.c = L.KV8(k.data_ptr(), v.data_ptr(), k_exp.data_ptr(), v_exp.data_ptr(), _ptr(table), self.nkv, self.d,
+                       self.max_batch, self.cap, self.block, self.n_blocks)
+        self.ref = C.byref(self.c)
+
+    @classmethod
+    def empty(cls, max_batch: int, nkv: int, cap: int, d: int, device="cuda", block: int = 0,
+              n_blocks: Optional[int] = None) -> "KV8Cache":
+        """A new cache for max_batch sequences of up to cap slots (rounded up to 16, or to whole
+        blocks). block > 0: paged, the table unassigned (-1) and n_blocks pool blocks (default: every
+        sequence's worst case)."""
+        unit = block or 16
+        cap = -(-cap // unit) * unit
+        if block:
+            n_blocks = max_batch * (cap // block) if n_blocks is None else n_blocks
+            table = torch.full((max_batch, cap // block), -1, dtype=torch.int32, device=device)
+            shape = (n_blocks, nkv, block, d)
+        else:
+            table, shape = None, (max_batch, nkv, cap, d)
+        new = lambda s: torch.zeros(s, dtype=torch.uint8, device=device)
+        return cls(new(shape), new(shape), new(shape[:3]), new(shape[:3]), table)
+
+
+def _row_lists(cache: KV8Cache, R: int, **lists: Optional[torch.Tensor]) -> None:
+    for name, t in lists.items():
+        _need(t is None or (t.dtype == torch.int32 and t.is_contiguous() and t.numel() >= R and
+                            t.device == cache.device), f"{name} must be a contiguous int32 tensor of >= {R} entries")
+
+
+def _err_word(cache: KV8Cache, err: Optional[torch.Tensor]) -> None:
+    _need(err is None or (err.dtype == torch.int32 and err.numel() >= 1 and err.device == cache.device),
+          "err must be an int32 tensor on the cache's device")
+
+
+def _kv_rows(cache: KV8Cache, k: torch.Tensor, v: torch.Tensor) -> int:
+    for t in (k, v):
+        _need(t.dtype in (torch.float32, torch.bfloat16) and t.dtype == k.dtype and t.device == cache.device,
+              "k and v must be float32 or bfloat16 tensors of one type on the cache's device")
+        _need(t.dim() == 3 and tuple(t.shape) == (k.shape[0], cache.nkv, cache.d) and
+              (t.shape[0] == 0 or (t.stride(2) == 1 and (t.stride(1) == cache.d or cache.nkv == 1))),
+              "k and v must be [R][nkv][d] with contiguous rows (the row stride is free)")
+    return k.shape[0]
+
+
+def _ld(t: torch.Tensor) -> int:
+    """Row stride in elements (that of a single row is of no account)."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def kv8_write(cache: KV8Cache, k: torch.Tensor, v: torch.Tensor, row_seq: torch.Tensor, row_slot: torch.Tensor,
+              err: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Quantise rows k, v [R][nkv][d] (fp32 or bf16, any row stride of whole 16 bytes) into slot row_slot[r] of
+    sequence row_seq[r] (negative: padding, skipped). err: int32 word that out-of-range rows are latched into."""
+    R = _kv_rows(cache, k, v)
+    _row_lists(cache, R, row_seq=row_seq, row_slot=row_slot)
+    _err_word(cache, err)
+    with _device_guard(cache.k):
+        rc = L.lib().eagle_op_kv8_write(_stream(stream), cache.ref, _dtype_code(k), k.data_ptr(), _ld(k), v.data_ptr(),
+                                        _ld(v), R, row_seq.data_ptr(), row_slot.data_ptr(), _ptr(err))
+    L.check(rc, "eagle_op_kv8_write")
+
+
+def kv8_read(cache: KV8Cache, row_seq: torch.Tensor, row_slot: torch.Tensor, dtype: torch.dtype = torch.bfloat16,
+             out: Optional[Sequence[torch.Tensor]] = None, err: Optional[torch.Tensor] = None,
+             stream: Optional[torch.cuda.Stream] = None):
+    """Entries (row_seq[r], row_slot[r]) as rows k, v [R][nkv][d] of `dtype` (exact), zeros for padding. out:
+    (k, v) to fill, with any row stride of whole 16 bytes."""
+    R = int(row_seq.numel())
+    if out is None:
+        out = tuple(torch.empty(R, cache.nkv, cache.d, dtype=dtype, device=cache.device) for _ in range(2))
+    k, v = out
+    _need(_kv_rows(cache, k, v) == R, "out must have a row for each entry of row_seq")
+    _row_lists(cache, R, row_seq=row_seq, row_slot=row_slot)
+    _err_word(cache, err)
+    with _device_guard(cache.k):
+        rc = L.lib().eagle_op_kv8_read(_stream(stream), cache.ref, _dtype_code(k), k.data_ptr(), _ld(k), v.data_ptr(),
+                                       _ld(v), R, row_seq.data_ptr(), row_slot.data_ptr(), _ptr(err))
+    L.check(rc, "eagle_op_kv8_read")
+    return k, v
+
+
+def attention_kv8_scratch(cache: KV8Cache, R: int, nq: int, rows_per_seq: int, prefix_len: int = 0) -> torch.Tensor:
+    """Scratch for attention_kv8 / attention_shared_kv8 calls of these sizes (calls that may overlap on the GPU
+    need their own)."""
+    nb = L.lib().eagle_op_attention_kv8_scratch_bytes(cache.ref, R, nq, rows_per_seq, prefix_len)
+    _need(nb > 0, "sizes that the 8-bit attention does not take")
+    return torch.empty(nb, dtype=torch.uint8, device=cache.device)
+
+
+def attention_shared_kv8(q: torch.Tensor, prefix_k: Optional[torch.Tensor], prefix_v: Optional[torch.Tensor],
+                         cache: KV8Cache, row_seq: torch.Tensor, row_slot: Optional[torch.Tensor],
+                         ctx_len: Optional[torch.Tensor], rows_per_seq: int, mode: int, tree_T: int = 0,
+                         mask: Optional[torch.Tensor] = None, scale: float = 0.0, out: Optional[torch.Tensor] = None,
+                         scratch: Optional[torch.Tensor] = None, err: Optional[torch.Tensor] = None,
+                         stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """attention_kv8 for sequences behind one shared prefix: prefix_k, prefix_v bf16 [nkv][P][d], which every row
+    sees before its own slots."""
+    _need(q.dim() == 3 and q.shape[2] == cache.d and q.dtype == torch.bfloat16 and q.is_contiguous() and
+          q.device == cache.device, "q must be a contiguous bfloat16 [R][nq][d] tensor on the cache's device")
+    R, nq, d = q.shape
+    P = 0
+    if prefix_k is not None:
+        for t in (prefix_k, prefix_v):
+            _need(t is not None and t.dtype == torch.bfloat16 and t.is_contiguous() and t.device == cache.device and
+                  t.dim() == 3 and t.shape == prefix_k.shape and t.shape[0] == cache.nkv and t.shape[2] == d,
+                  "prefix_k and prefix_v must be contiguous bfloat16 [nkv][P][d] tensors")
+        P = prefix_k.shape[1]
+    _row_lists(cache, R, row_seq=row_seq, row_slot=row_slot)
+    _row_lists(cache, cache.max_batch, ctx_len=ctx_len)
+    _err_word(cache, err)
+    mw = 0
+    if mask is not None:
+        _need(mask.dim() == 2 and mask.shape[0] >= R and mask.dtype in (torch.int64, torch.uint64) and
+              mask.is_contiguous() and mask.device == cache.device, "mask must be a contiguous 64-bit [R][words] tensor")
+        mw = mask.shape[1]
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _need(out.shape == q.shape and out.dtype == q.dtype and out.is_contiguous() and out.device == q.device,
+              "out must be like q")
+    if R == 0:
+        return out
+    if scratch is None:
+        scratch = attention_kv8_scratch(cache, R, nq, rows_per_seq, P)
+    _need(scratch.dtype == torch.uint8 and scratch.is_contiguous() and scratch.device == q.device,
+          "scratch must be a contiguous uint8 tensor on the cache's device")
+    with _device_guard(cache.k):
+        rc = L.lib().eagle_op_attention_shared_kv8(
+            _stream(stream), cache.ref, _ptr(prefix_k) if P else None, _ptr(prefix_v) if P else None, P, q.data_ptr(),
+            out.data_ptr(), R, nq, rows_per_seq, row_seq.data_ptr(), _ptr(row_slot), _ptr(ctx_len), mode, tree_T,
+            _ptr(mask), mw, scale, scratch.data_ptr(), scratch.numel(), _ptr(err))
+    L.check(rc, "eagle_op_attention_shared_kv8")
+    return out
+
+
+def attention_kv8(q: torch.Tensor, cache: KV8Cache, row_seq: torch.Tensor, row_slot: Optional[torch.Tensor],
+                  ctx_len: Optional[torch.Tensor], rows_per_seq: int, mode: int, tree_T: int = 0,
+                  mask: Optional[torch.Tensor] = None, scale: float = 0.0, out: Optional[torch.Tensor] = None,
+                  scratch: Optional[torch.Tensor] = None, err: Optional[torch.Tensor] = None,
+                  stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Tree (mode 1) or causal (mode 0) attention of q [R][nq][d] (bf16) over an 8-bit cache; rows as in
+    attention(), padding rows (row_seq < 0) and rows that see nothing give zeros."""
+    return attention_shared_kv8(q, None, None, cache, row_seq, row_slot, ctx_len, rows_per_seq, mode, tree_T, mask,
+                                scale, out, scratch, err, stream)

@@ -1,0 +1,69 @@
+// The 8-bit KV cache as the kernels see it: e4m3 codes, one exponent byte per (slot, head)
+// vector, contiguous or paged, and the internal launchers of its operators.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "../../include/eagle_ops.h"
+#include "common.cuh"
+
+namespace eagle {
+
+constexpr int KV8_E_LO = -40, KV8_E_HI = 40;   // exponents that a written vector can get
+constexpr int KV8_BIAS = 127;
+constexpr int KV8_BAD = 255;                   // exponent byte of a vector with an entry that is not finite
+
+struct Kv8 {
+  uint8_t *k, *v, *ke, *ve;
+  const int* table;     // nullptr: contiguous
+  int nkv, d, max_batch, cap;
+  int block_log2, tab_w, n_blocks;
+};
+
+// Vector index (in units of d codes, of one exponent byte) of head h of sequence seq at slot; -1 when the
+// slot's block is not assigned or outside the pool. seq and slot are in range. 64-bit: codes of a
+// long cache pass 2^32 bytes.
+__device__ __forceinline__ long long kv8_vec(const Kv8& c, int seq, int h, int slot) {
+  if (!c.table) return ((long long)seq * c.nkv + h) * c.cap + slot;
+  const int blk = c.table[(size_t)seq * c.tab_w + (slot >> c.block_log2)];
+  if (blk < 0 || blk >= c.n_blocks) return -1;
+  return (((long long)blk * c.nkv + h) << c.block_log2) + (slot & ((1 << c.block_log2) - 1));
+}
+
+// 2^(byte - 127), NaN for a vector that held something not finite. Bytes of written vectors are
+// 87 .. 167, so the power is a normal fp32 put together from its exponent bits.
+__device__ __forceinline__ float kv8_pow2(int byte) {
+  return byte == KV8_BAD ? __int_as_float(0x7fffffff) : __int_as_float(byte << 23);
+}
+
+// Two e4m3 codes (low byte first) as two fp16: exact.
+__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t two) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(r) : "r"(two));
+  return r;
+}
+
+struct Kv8Attn {
+  Kv8 c;
+  const void* q;          // bf16 [R][nq][d]
+  void* out;
+  const void *pk, *pv;    // bf16 [nkv][P][d], P == 0: none
+  int P;
+  int R, nq, rows_per_seq, mode, tree_T, mask_words;
+  const int *row_seq, *row_slot, *ctx_len;
+  const uint64_t* mask;
+  float scale;
+  void* scratch;
+  int* err;
+};
+
+int kv8_write(cudaStream_t st, const Kv8& c, bool f32, const void* k, long long ldk, const void* v, long long ldv, int R,
+              const int* row_seq, const int* row_slot, int* err);
+int kv8_read(cudaStream_t st, const Kv8& c, bool f32, void* k, long long ldk, void* v, long long ldv, int R,
+             const int* row_seq, const int* row_slot, int* err);
+size_t kv8_attention_scratch(const Kv8& c, int R, int nq, int rows_per_seq, int P);
+int kv8_attention(cudaStream_t st, const Kv8Attn& a);
+
+}  // namespace eagle

@@ -8,6 +8,7 @@
 #include "common.cuh"
 #include "cycle.h"
 #include "kernels.h"
+#include "kv8.cuh"
 #include "lmhead.cuh"
 
 using namespace eagle;
@@ -220,6 +221,113 @@ int eagle_op_compact(int dtype, void* stream, void* kcache, void* vcache, int la
                            vcache, layers, (size_t)B * nkv * cap * d, B, nkv, cap, d, n_old, acc_len, acc_path,
                            Dmax, KvPage{nullptr, 0, 0});
   return r == 0 ? EAGLE_OK : EAGLE_ECUDA;
+}
+
+// ---- 8-bit KV cache ----------------------------------------------------------------------------
+static bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+// The kernels' view of a cache; EAGLE_EINVAL / EAGLE_ECAPACITY when it breaks the header's rules.
+static int kv8_view(const eagle_kv8* c, Kv8& o) {
+  if (!c || !c->k_code || !c->v_code || !c->k_exp || !c->v_exp || c->n_kv_heads < 1 || c->max_batch < 1 || c->cap < 1 ||
+      (c->head_dim != 64 && c->head_dim != 128))
+    return EAGLE_EINVAL;
+  if (!on16(c->k_code) || !on16(c->v_code) || !on16(c->k_exp) || !on16(c->v_exp)) return EAGLE_EINVAL;
+  o = Kv8{};
+  o.k = (uint8_t*)c->k_code; o.v = (uint8_t*)c->v_code; o.ke = (uint8_t*)c->k_exp; o.ve = (uint8_t*)c->v_exp;
+  o.nkv = c->n_kv_heads; o.d = c->head_dim; o.max_batch = c->max_batch; o.cap = c->cap; o.table = c->table;
+  double vecs;
+  if (c->table) {
+    if (c->block < 16 || c->block > 256 || (c->block & (c->block - 1)) || c->n_blocks < 1 || c->cap % c->block)
+      return EAGLE_EINVAL;
+    while ((1 << o.block_log2) < c->block) ++o.block_log2;
+    o.tab_w = c->cap / c->block;
+    o.n_blocks = c->n_blocks;
+    vecs = (double)c->n_blocks * c->n_kv_heads * c->block;
+  } else {
+    if (c->cap % 16) return EAGLE_EINVAL;
+    vecs = (double)c->max_batch * c->n_kv_heads * c->cap;
+  }
+  return vecs < 2147483648.0 ? EAGLE_OK : EAGLE_ECAPACITY;
+}
+
+static int kv8_rows(const Kv8& c, int dtype, const void* k, int64_t ldk, const void* v, int64_t ldv, int R,
+                    const int32_t* row_seq, const int32_t* row_slot) {
+  if (dtype != EAGLE_DTYPE_F32 && dtype != EAGLE_DTYPE_BF16) return EAGLE_EINVAL;
+  if (R < 0) return EAGLE_EINVAL;
+  if (R == 0) return EAGLE_OK;
+  const int64_t unit = dtype == EAGLE_DTYPE_F32 ? 4 : 8, width = (int64_t)c.nkv * c.d;
+  if (!k || !v || !row_seq || !row_slot || !on16(k) || !on16(v) || ldk < width || ldv < width || ldk % unit ||
+      ldv % unit)
+    return EAGLE_EINVAL;
+  return EAGLE_OK;
+}
+
+int eagle_op_kv8_write(void* stream, const eagle_kv8* cache, int dtype, const void* k, int64_t ldk, const void* v,
+                       int64_t ldv, int R, const int32_t* row_seq, const int32_t* row_slot, int32_t* d_err) {
+  Kv8 c;
+  int r = kv8_view(cache, c);
+  if (r == EAGLE_OK) r = kv8_rows(c, dtype, k, ldk, v, ldv, R, row_seq, row_slot);
+  if (r != EAGLE_OK || R == 0) return r;
+  r = kv8_write(reinterpret_cast<cudaStream_t>(stream), c, dtype == EAGLE_DTYPE_F32, k, ldk, v, ldv, R, row_seq,
+                row_slot, d_err);
+  return r == 0 ? EAGLE_OK : (r == -1 ? EAGLE_ECAPACITY : EAGLE_ECUDA);
+}
+
+int eagle_op_kv8_read(void* stream, const eagle_kv8* cache, int dtype, void* k, int64_t ldk, void* v, int64_t ldv,
+                      int R, const int32_t* row_seq, const int32_t* row_slot, int32_t* d_err) {
+  Kv8 c;
+  int r = kv8_view(cache, c);
+  if (r == EAGLE_OK) r = kv8_rows(c, dtype, k, ldk, v, ldv, R, row_seq, row_slot);
+  if (r != EAGLE_OK || R == 0) return r;
+  r = kv8_read(reinterpret_cast<cudaStream_t>(stream), c, dtype == EAGLE_DTYPE_F32, k, ldk, v, ldv, R, row_seq,
+               row_slot, d_err);
+  return r == 0 ? EAGLE_OK : (r == -1 ? EAGLE_ECAPACITY : EAGLE_ECUDA);
+}
+
+// Sizes that both attention entry points and their scratch size accept.
+static int kv8_attn_sizes(const Kv8& c, int R, int nq, int rows_per_seq, int prefix_len) {
+  if (R < 1 || nq < 1 || nq % c.nkv || nq / c.nkv > 64 || rows_per_seq < 1 || prefix_len < 0) return EAGLE_EINVAL;
+  if ((double)R * nq >= 2147483648.0 / c.d || (double)prefix_len * c.nkv >= 2147483648.0) return EAGLE_ECAPACITY;
+  return EAGLE_OK;
+}
+
+size_t eagle_op_attention_kv8_scratch_bytes(const eagle_kv8* cache, int R, int nq, int rows_per_seq, int prefix_len) {
+  Kv8 c;
+  if (kv8_view(cache, c) != EAGLE_OK || kv8_attn_sizes(c, R, nq, rows_per_seq, prefix_len) != EAGLE_OK) return 0;
+  return al(kv8_attention_scratch(c, R, nq, rows_per_seq, prefix_len));
+}
+
+int eagle_op_attention_shared_kv8(void* stream, const eagle_kv8* cache, const void* prefix_k, const void* prefix_v,
+                                  int prefix_len, const void* q, void* out, int R, int nq, int rows_per_seq,
+                                  const int32_t* row_seq, const int32_t* row_slot, const int32_t* ctx_len, int mode,
+                                  int tree_T, const uint64_t* mask, int mask_words, float scale, void* scratch,
+                                  size_t scratch_bytes, int32_t* d_err) {
+  Kv8Attn a{};
+  int r = kv8_view(cache, a.c);
+  if (r == EAGLE_OK) r = kv8_attn_sizes(a.c, R, nq, rows_per_seq, prefix_len);
+  if (r != EAGLE_OK) return r;
+  if (!q || !out || !on16(q) || !on16(out) || !row_seq || (mode != 0 && mode != 1) || (mode == 0 && !row_slot))
+    return EAGLE_EINVAL;
+  if (mode == 1 && (!ctx_len || !mask || tree_T < 1 || tree_T > 256 || mask_words < (tree_T + 63) / 64)) return EAGLE_EINVAL;
+  if (prefix_len && (!prefix_k || !prefix_v || !on16(prefix_k) || !on16(prefix_v))) return EAGLE_EINVAL;
+  const size_t need = al(kv8_attention_scratch(a.c, R, nq, rows_per_seq, prefix_len));
+  if (!scratch || !on16(scratch) || scratch_bytes < need) return EAGLE_ECAPACITY;
+  a.q = q; a.out = out; a.pk = prefix_k; a.pv = prefix_v; a.P = prefix_len;
+  a.R = R; a.nq = nq; a.rows_per_seq = rows_per_seq; a.mode = mode; a.tree_T = mode == 1 ? tree_T : 0;
+  a.mask_words = mask_words; a.row_seq = row_seq; a.row_slot = row_slot; a.ctx_len = ctx_len; a.mask = mask;
+  a.scale = scale > 0.f ? scale : 1.f / sqrtf((float)a.c.d);
+  a.scratch = scratch; a.err = d_err;
+  r = kv8_attention(reinterpret_cast<cudaStream_t>(stream), a);
+  return r == 0 ? EAGLE_OK : (r == -1 ? EAGLE_ECAPACITY : EAGLE_ECUDA);
+}
+
+int eagle_op_attention_kv8(void* stream, const eagle_kv8* cache, const void* q, void* out, int R, int nq,
+                           int rows_per_seq, const int32_t* row_seq, const int32_t* row_slot, const int32_t* ctx_len,
+                           int mode, int tree_T, const uint64_t* mask, int mask_words, float scale, void* scratch,
+                           size_t scratch_bytes, int32_t* d_err) {
+  return eagle_op_attention_shared_kv8(stream, cache, nullptr, nullptr, 0, q, out, R, nq, rows_per_seq, row_seq,
+                                       row_slot, ctx_len, mode, tree_T, mask, mask_words, scale, scratch, scratch_bytes,
+                                       d_err);
 }
 
 }  // extern "C"

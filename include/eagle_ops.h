@@ -102,6 +102,80 @@ int eagle_op_attention(int dtype, void* stream, const void* q, const void* kcach
                        int tree_T, const uint64_t* mask, int mask_words, float scale, int max_batch,
                        void* scratch, size_t scratch_bytes);
 
+/* ---- 8-bit KV cache ---------------------------------------------------------------------------
+ * One layer's keys and values in e4m3 with one power-of-two exponent byte per (slot, head)
+ * vector: value = code * 2^(byte - 127). A written vector x gets the smallest exponent e in
+ * [-40, 40] with max|x| <= 448 * 2^e (byte e + 127) and codes rounded to nearest even
+ * (magnitudes above 448 * 2^40 saturate); a vector with an entry that is not finite gets byte
+ * 255 and zero codes, and reads back as NaN throughout. Reading is exact in bf16 and fp32, and
+ * writing what was read stores the same values, so entries move (compaction of an accepted path,
+ * a sequence handed to another cache) by eagle_op_kv8_read and eagle_op_kv8_write.
+ *
+ * table == NULL: contiguous, codes [max_batch][n_kv_heads][cap][head_dim] and exponents
+ * [max_batch][n_kv_heads][cap]; cap a multiple of 16. Otherwise paged: pools
+ * [n_blocks][n_kv_heads][block][head_dim] and [n_blocks][n_kv_heads][block], block a power of
+ * two from 16 to 256, and the device block table [max_batch][cap / block] (int32, pool block
+ * of each sequence's slots [j * block, (j + 1) * block), -1 = unassigned); cap a multiple of
+ * block. head_dim 64 or 128. All four arrays start on 16-byte boundaries and hold fewer than
+ * 2^31 vectors each. The struct itself is host memory, read during the call. */
+typedef struct {
+  void *k_code, *v_code; /* e4m3 */
+  void *k_exp, *v_exp;   /* uint8 */
+  const int32_t* table;
+  int n_kv_heads, head_dim, max_batch, cap, block, n_blocks;
+} eagle_kv8;
+
+/* Quantise rows into the cache: k and v hold R rows of [n_kv_heads][head_dim] (dtype
+ * EAGLE_DTYPE_BF16 or EAGLE_DTYPE_F32, 16-byte aligned) with row strides ldk and ldv elements
+ * (multiples of 16 bytes, >= n_kv_heads * head_dim), e.g. the k and v columns of a fused
+ * projection. Row r goes to slot row_slot[r] of sequence row_seq[r]; a row with row_seq[r] < 0 is
+ * padding and is skipped. The rows of one call name different (sequence, slot) pairs. A sequence,
+ * slot or table entry out of range is latched into *d_err (nullable device int32: 2) and its row
+ * skipped; nothing else of the cache changes. R = 0 does nothing. */
+int eagle_op_kv8_write(void* stream, const eagle_kv8* cache, int dtype, const void* k, int64_t ldk, const void* v,
+                       int64_t ldv, int R, const int32_t* row_seq, const int32_t* row_slot, int32_t* d_err);
+
+/* Read cache entries back: row r of k and v (layout, types and strides as above) receives slot
+ * row_slot[r] of sequence row_seq[r], any number of times the same. Padding rows and rows out of
+ * range (latched into *d_err) receive zeros; the gap between row strides is left as it was. */
+int eagle_op_kv8_read(void* stream, const eagle_kv8* cache, int dtype, void* k, int64_t ldk, void* v, int64_t ldv,
+                      int R, const int32_t* row_seq, const int32_t* row_slot, int32_t* d_err);
+
+/* Attention of R query rows over an 8-bit cache, with the row model of eagle_op_attention: q and
+ * out bf16 [R][nq][head_dim] (16-byte aligned), nq a multiple of n_kv_heads with at most 64
+ * query heads per KV head, rows of one sequence contiguous (rows_per_seq each; the last may have
+ * fewer). mode 0 (causal): row r sees slots <= row_slot[r]. mode 1 (tree): row r sees slots <
+ * ctx_len[seq] and slot ctx_len[seq] + t for t < tree_T (1..256) where bit t of
+ * mask[r][t / 64] is set (mask_words >= ceil(tree_T / 64); row_slot is not read). ctx_len is
+ * indexed by sequence ([max_batch]; not read in mode 0). A row that sees nothing, and a padding
+ * row (row_seq[r] < 0), gets zeros. A row whose sequence differs from that of the first
+ * not-padding row among its rows_per_seq, a sequence outside the cache, a visible slot at or
+ * past cap and a table entry out of range are latched into *d_err (nullable): such a row gets
+ * zeros, slots past cap are left out, and a bad table entry makes its slots unspecified. Slots
+ * that no row sees may hold anything. Scale = 1/sqrt(head_dim) when scale <= 0.
+ * Sums, maxima and softmax weights' sums are fp32; the weights enter the value product as fp16.
+ * A row's result does not depend on the values of other rows or sequences; their lengths move
+ * the points where its sum over slots is split, so it can change in the last bits of fp32.
+ * scratch: eagle_op_attention_kv8_scratch_bytes of the same sizes, no initial value needed; two
+ * calls that may overlap on the GPU (graph replays included) need their own. */
+size_t eagle_op_attention_kv8_scratch_bytes(const eagle_kv8* cache, int R, int nq, int rows_per_seq, int prefix_len);
+int eagle_op_attention_kv8(void* stream, const eagle_kv8* cache, const void* q, void* out, int R, int nq,
+                           int rows_per_seq, const int32_t* row_seq, const int32_t* row_slot, const int32_t* ctx_len,
+                           int mode, int tree_T, const uint64_t* mask, int mask_words, float scale, void* scratch,
+                           size_t scratch_bytes, int32_t* d_err);
+
+/* The same for sequences that share a prefix: every row first sees all prefix_len entries of
+ * prefix_k / prefix_v (bf16 [n_kv_heads][prefix_len][head_dim], 16-byte aligned; kept at full
+ * precision, being stored once for the whole batch) and then its own slots as above, in one
+ * softmax. The prefix is one matrix product over all rows of a head, read once per 256 query
+ * vectors rather than once per sequence. Padding rows get zeros. prefix_len = 0 is
+ * eagle_op_attention_kv8. */
+int eagle_op_attention_shared_kv8(void* stream, const eagle_kv8* cache, const void* prefix_k, const void* prefix_v,
+                                  int prefix_len, const void* q, void* out, int R, int nq, int rows_per_seq,
+                                  const int32_t* row_seq, const int32_t* row_slot, const int32_t* ctx_len, int mode,
+                                  int tree_T, const uint64_t* mask, int mask_words, float scale, void* scratch,
+                                  size_t scratch_bytes, int32_t* d_err);
+
 /* EAGLE-2 tree growth and rerank with injected draft confidences, for B sequences:
  * cand_tok/cand_logc [B][k]: the root's children (token, log confidence) in rank order;
  * child_tok/child_logc [B][depth-1][k][k]: children of the r-th node selected at depth

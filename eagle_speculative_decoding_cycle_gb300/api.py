@@ -389,9 +389,25 @@ def _need(ok: bool, what: str) -> None:
         raise ValueError(what)
 
 
-def _device_guard(t: torch.Tensor):
-    """The tensor's device made current for a launch."""
-    return torch.cuda.device(t.device)
+class _Current:
+    """The cache's device made current for a launch (nothing to do where it is already)."""
+    __slots__ = ("index", "before")
+
+    def __init__(self, index: int):
+        self.index = index
+
+    def __enter__(self):
+        self.before = torch.cuda.current_device()
+        if self.before != self.index:
+            torch.cuda.set_device(self.index)
+
+    def __exit__(self, *exc):
+        if self.before != self.index:
+            torch.cuda.set_device(self.before)
+
+
+def _stream_of(index: int, stream: Optional[torch.cuda.Stream]) -> int:
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
 class KV8Cache:
@@ -408,7 +424,7 @@ class KV8Cache:
         _need(k.dim() == 4 and k.shape == v.shape and k_exp.shape == k.shape[:3] and v_exp.shape == k.shape[:3],
               "codes must be [B][nkv][cap][d] (or [n_blocks][nkv][block][d]) and exponents the same without d")
         self.k, self.v, self.k_exp, self.v_exp, self.table = k, v, k_exp, v_exp, table
-        self.device = k.device
+        self.device, self.index = k.device, k.get_device()
         n, self.nkv, slots, self.d = k.shape
         if table is None:
             self.max_batch, self.cap, self.block, self.n_blocks = n, slots, 0, 0
@@ -438,42 +454,50 @@ class KV8Cache:
         return cls(new(shape), new(shape), new(shape[:3]), new(shape[:3]), table)
 
 
-def _row_lists(cache: KV8Cache, R: int, **lists: Optional[torch.Tensor]) -> None:
-    for name, t in lists.items():
-        _need(t is None or (t.dtype == torch.int32 and t.is_contiguous() and t.numel() >= R and
-                            t.device == cache.device), f"{name} must be a contiguous int32 tensor of >= {R} entries")
+def _row_list(cache: KV8Cache, t: torch.Tensor, n: int, name: str) -> int:
+    if t.dtype is not torch.int32 or t.numel() < n or not t.is_contiguous() or t.get_device() != cache.index:
+        raise ValueError(f"{name} must be a contiguous int32 tensor of >= {n} entries on the cache's device")
+    return t.data_ptr()
 
 
-def _err_word(cache: KV8Cache, err: Optional[torch.Tensor]) -> None:
-    _need(err is None or (err.dtype == torch.int32 and err.numel() >= 1 and err.device == cache.device),
+def _err_word(cache: KV8Cache, err: Optional[torch.Tensor]) -> Optional[int]:
+    if err is None:
+        return None
+    _need(err.dtype is torch.int32 and err.numel() >= 1 and err.get_device() == cache.index,
           "err must be an int32 tensor on the cache's device")
+    return err.data_ptr()
 
 
-def _kv_rows(cache: KV8Cache, k: torch.Tensor, v: torch.Tensor) -> int:
+_KV_TYPES = {torch.float32: L.DTYPE_F32, torch.bfloat16: L.DTYPE_BF16}
+
+
+def _kv_rows(cache: KV8Cache, k: torch.Tensor, v: torch.Tensor):
+    """(rows, type code, row strides) of k and v; a single row's stride is of no account."""
+    shape = k.shape
+    code = _KV_TYPES.get(k.dtype)
+    if code is None or v.dtype is not k.dtype or k.get_device() != cache.index or v.get_device() != cache.index:
+        raise ValueError("k and v must be float32 or bfloat16 tensors of one type on the cache's device")
+    if len(shape) != 3 or v.shape != shape or shape[1] != cache.nkv or shape[2] != cache.d:
+        raise ValueError("k and v must be [R][nkv][d]")
+    R, width, ld = shape[0], cache.nkv * cache.d, []
     for t in (k, v):
-        _need(t.dtype in (torch.float32, torch.bfloat16) and t.dtype == k.dtype and t.device == cache.device,
-              "k and v must be float32 or bfloat16 tensors of one type on the cache's device")
-        _need(t.dim() == 3 and tuple(t.shape) == (k.shape[0], cache.nkv, cache.d) and
-              (t.shape[0] == 0 or (t.stride(2) == 1 and (t.stride(1) == cache.d or cache.nkv == 1))),
-              "k and v must be [R][nkv][d] with contiguous rows (the row stride is free)")
-    return k.shape[0]
-
-
-def _ld(t: torch.Tensor) -> int:
-    """Row stride in elements (that of a single row is of no account)."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+        s0, s1, s2 = t.stride()
+        if R and (s2 != 1 or (s1 != cache.d and cache.nkv != 1)):
+            raise ValueError("k and v rows must be contiguous (the row stride is free)")
+        ld.append(s0 if R > 1 else width)
+    return R, code, ld[0], ld[1]
 
 
 def kv8_write(cache: KV8Cache, k: torch.Tensor, v: torch.Tensor, row_seq: torch.Tensor, row_slot: torch.Tensor,
               err: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> None:
     """Quantise rows k, v [R][nkv][d] (fp32 or bf16, any row stride of whole 16 bytes) into slot row_slot[r] of
     sequence row_seq[r] (negative: padding, skipped). err: int32 word that out-of-range rows are latched into."""
-    R = _kv_rows(cache, k, v)
-    _row_lists(cache, R, row_seq=row_seq, row_slot=row_slot)
-    _err_word(cache, err)
-    with _device_guard(cache.k):
-        rc = L.lib().eagle_op_kv8_write(_stream(stream), cache.ref, _dtype_code(k), k.data_ptr(), _ld(k), v.data_ptr(),
-                                        _ld(v), R, row_seq.data_ptr(), row_slot.data_ptr(), _ptr(err))
+    R, code, ldk, ldv = _kv_rows(cache, k, v)
+    seq, slot = _row_list(cache, row_seq, R, "row_seq"), _row_list(cache, row_slot, R, "row_slot")
+    e = _err_word(cache, err)
+    with _Current(cache.index):
+        rc = L.lib().eagle_op_kv8_write(_stream_of(cache.index, stream), cache.ref, code, k.data_ptr(), ldk,
+                                        v.data_ptr(), ldv, R, seq, slot, e)
     L.check(rc, "eagle_op_kv8_write")
 
 
@@ -482,16 +506,20 @@ def kv8_read(cache: KV8Cache, row_seq: torch.Tensor, row_slot: torch.Tensor, dty
              stream: Optional[torch.cuda.Stream] = None):
     """Entries (row_seq[r], row_slot[r]) as rows k, v [R][nkv][d] of `dtype` (exact), zeros for padding. out:
     (k, v) to fill, with any row stride of whole 16 bytes."""
-    R = int(row_seq.numel())
+    n = row_seq.numel()
     if out is None:
-        out = tuple(torch.empty(R, cache.nkv, cache.d, dtype=dtype, device=cache.device) for _ in range(2))
-    k, v = out
-    _need(_kv_rows(cache, k, v) == R, "out must have a row for each entry of row_seq")
-    _row_lists(cache, R, row_seq=row_seq, row_slot=row_slot)
-    _err_word(cache, err)
-    with _device_guard(cache.k):
-        rc = L.lib().eagle_op_kv8_read(_stream(stream), cache.ref, _dtype_code(k), k.data_ptr(), _ld(k), v.data_ptr(),
-                                       _ld(v), R, row_seq.data_ptr(), row_slot.data_ptr(), _ptr(err))
+        _need(dtype in _KV_TYPES, "entries are read as float32 or bfloat16")
+        both = torch.empty((2, n, cache.nkv, cache.d), dtype=dtype, device=cache.device)
+        k, v = both.unbind(0)
+    else:
+        k, v = out
+    R, code, ldk, ldv = _kv_rows(cache, k, v)
+    _need(R == n, "out must have a row for each entry of row_seq")
+    seq, slot = _row_list(cache, row_seq, R, "row_seq"), _row_list(cache, row_slot, R, "row_slot")
+    e = _err_word(cache, err)
+    with _Current(cache.index):
+        rc = L.lib().eagle_op_kv8_read(_stream_of(cache.index, stream), cache.ref, code, k.data_ptr(), ldk,
+                                       v.data_ptr(), ldv, R, seq, slot, e)
     L.check(rc, "eagle_op_kv8_read")
     return k, v
 
@@ -512,40 +540,45 @@ def attention_shared_kv8(q: torch.Tensor, prefix_k: Optional[torch.Tensor], pref
                          stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """attention_kv8 for sequences behind one shared prefix: prefix_k, prefix_v bf16 [nkv][P][d], which every row
     sees before its own slots."""
-    _need(q.dim() == 3 and q.shape[2] == cache.d and q.dtype == torch.bfloat16 and q.is_contiguous() and
-          q.device == cache.device, "q must be a contiguous bfloat16 [R][nq][d] tensor on the cache's device")
-    R, nq, d = q.shape
-    P = 0
+    shape, index = q.shape, cache.index
+    if len(shape) != 3 or shape[2] != cache.d or q.dtype is not torch.bfloat16 or not q.is_contiguous() or \
+            q.get_device() != index:
+        raise ValueError("q must be a contiguous bfloat16 [R][nq][d] tensor on the cache's device")
+    R, nq, d = shape
+    P, pk, pv = 0, None, None
     if prefix_k is not None:
+        _need(prefix_v is not None and prefix_k.shape == prefix_v.shape, "prefix_k and prefix_v must have one shape")
         for t in (prefix_k, prefix_v):
-            _need(t is not None and t.dtype == torch.bfloat16 and t.is_contiguous() and t.device == cache.device and
-                  t.dim() == 3 and t.shape == prefix_k.shape and t.shape[0] == cache.nkv and t.shape[2] == d,
-                  "prefix_k and prefix_v must be contiguous bfloat16 [nkv][P][d] tensors")
+            _need(t.dtype is torch.bfloat16 and t.is_contiguous() and t.get_device() == index and t.dim() == 3 and
+                  t.shape[0] == cache.nkv and t.shape[2] == d,
+                  "prefix_k and prefix_v must be contiguous bfloat16 [nkv][P][d] tensors on the cache's device")
         P = prefix_k.shape[1]
-    _row_lists(cache, R, row_seq=row_seq, row_slot=row_slot)
-    _row_lists(cache, cache.max_batch, ctx_len=ctx_len)
-    _err_word(cache, err)
-    mw = 0
+        if P:
+            pk, pv = prefix_k.data_ptr(), prefix_v.data_ptr()
+    seq = _row_list(cache, row_seq, R, "row_seq")
+    slot = None if row_slot is None else _row_list(cache, row_slot, R, "row_slot")
+    ctx = None if ctx_len is None else _row_list(cache, ctx_len, cache.max_batch, "ctx_len")
+    e = _err_word(cache, err)
+    mp, mw = None, 0
     if mask is not None:
         _need(mask.dim() == 2 and mask.shape[0] >= R and mask.dtype in (torch.int64, torch.uint64) and
-              mask.is_contiguous() and mask.device == cache.device, "mask must be a contiguous 64-bit [R][words] tensor")
-        mw = mask.shape[1]
+              mask.is_contiguous() and mask.get_device() == index, "mask must be a contiguous 64-bit [R][words] tensor")
+        mp, mw = mask.data_ptr(), mask.shape[1]
     if out is None:
         out = torch.empty_like(q)
     else:
-        _need(out.shape == q.shape and out.dtype == q.dtype and out.is_contiguous() and out.device == q.device,
+        _need(out.shape == shape and out.dtype is torch.bfloat16 and out.is_contiguous() and out.get_device() == index,
               "out must be like q")
     if R == 0:
         return out
     if scratch is None:
         scratch = attention_kv8_scratch(cache, R, nq, rows_per_seq, P)
-    _need(scratch.dtype == torch.uint8 and scratch.is_contiguous() and scratch.device == q.device,
-          "scratch must be a contiguous uint8 tensor on the cache's device")
-    with _device_guard(cache.k):
+    if scratch.dtype is not torch.uint8 or not scratch.is_contiguous() or scratch.get_device() != index:
+        raise ValueError("scratch must be a contiguous uint8 tensor on the cache's device")
+    with _Current(index):
         rc = L.lib().eagle_op_attention_shared_kv8(
-            _stream(stream), cache.ref, _ptr(prefix_k) if P else None, _ptr(prefix_v) if P else None, P, q.data_ptr(),
-            out.data_ptr(), R, nq, rows_per_seq, row_seq.data_ptr(), _ptr(row_slot), _ptr(ctx_len), mode, tree_T,
-            _ptr(mask), mw, scale, scratch.data_ptr(), scratch.numel(), _ptr(err))
+            _stream_of(index, stream), cache.ref, pk, pv, P, q.data_ptr(), out.data_ptr(), R, nq, rows_per_seq, seq,
+            slot, ctx, mode, tree_T, mp, mw, scale, scratch.data_ptr(), scratch.numel(), e)
     L.check(rc, "eagle_op_attention_shared_kv8")
     return out
 

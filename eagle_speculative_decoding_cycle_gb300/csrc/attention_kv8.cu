@@ -748,69 +748,6 @@ __global__ void __launch_bounds__(256) kv8_join_k(const Kv8Attn a, const Plan p)
 }
 
 
-// One warp a (row, query head): the lanes share the head dimension, the keys come one by one.
-template <int D>
-__global__ void __launch_bounds__(128) kv8_attn_simple_k(Kv8Attn a) {
-  constexpr int E = D / 32;   // entries a lane
-  PDL_ENTRY();
-  const Kv8& c = a.c;
-  const long long item = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (item >= (long long)a.R * a.nq) return;
-  const int lane = threadIdx.x & 31, row = (int)(item / a.nq), head = (int)(item % a.nq), h = head / (a.nq / c.nkv);
-  __nv_bfloat16* out = (__nv_bfloat16*)a.out + item * D + lane * E;
-  int seq = a.row_seq[row], first = -1;
-  for (int r = row / a.rows_per_seq * a.rows_per_seq; first < 0 && r <= row; ++r) first = a.row_seq[r];
-  const bool live = seq >= 0 && seq == first && seq < c.max_batch;
-  if (seq >= 0 && !live && lane == 0) latch_error(a.err, DEVERR_BOUNDS);
-  float q[E], o[E], m = -INFINITY, l = 0.f;
-  for (int i = 0; i < E; ++i) {
-    q[i] = __bfloat162float(((const __nv_bfloat16*)a.q)[item * D + lane * E + i]);
-    o[i] = 0.f;
-  }
-  auto key = [&](const float* k, const float* v) {
-    float s = 0.f;
-    for (int i = 0; i < E; ++i) s = fmaf(q[i], k[i], s);
-    s = warp_sum(s) * a.scale;
-    const float mn = fmaxf(m, s), base = mn == -INFINITY ? 0.f : mn;
-    const float p = expf(s - base), corr = expf(m - base);
-    m = mn;
-    l = l * corr + p;
-    for (int i = 0; i < E; ++i) o[i] = o[i] * corr + p * v[i];
-  };
-  if (live) {
-    float k[E], v[E];
-    for (int s = 0; s < a.P; ++s) {
-      const size_t at = ((size_t)h * a.P + s) * D + lane * E;
-      for (int i = 0; i < E; ++i) {
-        k[i] = __bfloat162float(((const __nv_bfloat16*)a.pk)[at + i]);
-        v[i] = __bfloat162float(((const __nv_bfloat16*)a.pv)[at + i]);
-      }
-      key(k, v);
-    }
-    const int ctx = a.mode == 1 ? a.ctx_len[seq] : 0;
-    const int end = a.mode == 1 ? ctx + a.tree_T : a.row_slot[row] + 1;
-    for (int s = 0; s < end; ++s) {
-      const int t = s - ctx;
-      if (a.mode == 1 && t >= 0 && !((a.mask[(size_t)row * a.mask_words + (t >> 6)] >> (t & 63)) & 1)) continue;
-      const long long vec = s < c.cap ? kv8_vec(c, seq, h, s) : -1;
-      if (vec < 0) {
-        if (lane == 0) latch_error(a.err, DEVERR_BOUNDS);
-        continue;
-      }
-      const float fk = kv8_pow2(c.ke[vec]), fv = kv8_pow2(c.ve[vec]);
-      for (int i = 0; i < E; i += 2) {
-        const uint32_t hk = e4m3x2_f16x2(*(const uint16_t*)(c.k + vec * D + lane * E + i));
-        const uint32_t hv = e4m3x2_f16x2(*(const uint16_t*)(c.v + vec * D + lane * E + i));
-        const float2 x = __half22float2(*(const __half2*)&hk), y = __half22float2(*(const __half2*)&hv);
-        k[i] = x.x * fk; k[i + 1] = x.y * fk;
-        v[i] = y.x * fv; v[i + 1] = y.y * fv;
-      }
-      key(k, v);
-    }
-  }
-  for (int i = 0; i < E; ++i) out[i] = __float2bfloat16_rn(l == 0.f ? 0.f : o[i] / l);
-}
-
 }  // namespace
 
 // ---- host side ------------------------------------------------------------------------------------------
@@ -886,20 +823,14 @@ cudaError_t launch_d(cudaStream_t st, const Kv8Attn& a, Plan& p, const CUtensorM
 
 }  // namespace
 
-size_t kv8_attention_scratch(const Kv8& c, int, int nq, int rows_per_seq, int) {
+size_t kv8_attention_scratch(const Kv8& c, int R, int nq, int rows_per_seq, int P) {
   Plan p{};
   cut_rows(c, nq, rows_per_seq, p);
-  return own_scratch(c, p);
+  const size_t qv = (size_t)R * nq * (P ? kv8_prefix_splits(c.nkv, R, nq, P) : 0);
+  return own_scratch(c, p) + al256(qv * c.d * sizeof(float)) + al256(qv * 2 * sizeof(float));
 }
 
 int kv8_attention(cudaStream_t st, const Kv8Attn& a) {
-  if (a.P) {
-    const long long blocks = ((long long)a.R * a.nq + 3) / 4;
-    if (blocks > 0x7fffffffll) return -1;
-    if (a.c.d == 128) launch_k(kv8_attn_simple_k<128>, dim3((unsigned)blocks), 128, 0, st, a);
-    else launch_k(kv8_attn_simple_k<64>, dim3((unsigned)blocks), 128, 0, st, a);
-    return cudaGetLastError() == cudaSuccess ? 0 : -4;
-  }
   Plan p{};
   cut_rows(a.c, a.nq, a.rows_per_seq, p);
   uint8_t* s = (uint8_t*)a.scratch;
@@ -908,6 +839,16 @@ int kv8_attention(cudaStream_t st, const Kv8Attn& a) {
   p.part_ml = (float*)s;
   s += al256((size_t)2 * MAX_CTAS * p.qv_pad * 2 * sizeof(float));
   p.pref = (int*)s;
+  if (a.P) {
+    p.n_prefix = kv8_prefix_splits(a.c.nkv, a.R, a.nq, a.P);
+    const size_t qv = (size_t)a.R * a.nq * p.n_prefix;
+    float* o = (float*)(s + al256((MAX_GROUPS + 1) * sizeof(int)));
+    float* ml = (float*)((uint8_t*)o + al256(qv * a.c.d * sizeof(float)));
+    p.pp_o = o;
+    p.pp_ml = ml;
+    const int r = kv8_prefix(st, a, p.n_prefix, o, ml);
+    if (r) return r;
+  }
   const long long rows = a.c.table ? ((long long)a.c.n_blocks * a.c.nkv) << a.c.block_log2
                                    : (long long)a.c.max_batch * a.c.nkv * a.c.cap;
   const int box = a.c.table ? std::min(TK, 1 << a.c.block_log2) : TK;

@@ -1,0 +1,392 @@
+// Attention of all rows of a batch over one shared bf16 prefix, on the 5th-generation tensor cores.
+//
+// Every row sees every prefix key, so the rows of all sequences are one long side: per KV head two dense products,
+// S = Q K^T and O = P V, with M = rows x query heads (hundreds to tens of thousands), N = P keys, and no
+// mask but the prefix's end. 4 M P d flops a head against 4 P d + 6 M d bytes: bound by the tensor cores from
+// some 150 query vectors a head on, and below by reading the prefix once.
+//
+// One CTA takes two tiles of 128 query vectors of one KV head and a range of 128-key tiles, 12 warps:
+//   warps 0-3, 4-7  softmax of tile 0 / 1, one thread a query vector (TMEM lane): S row -> maximum, weights as bf16 back
+//                   into TMEM over S, running sum; O is rescaled only when the maximum moves by more than 2^8;
+//   warp 8          TMA: Q once, K and V tiles through two-stage rings (128-byte swizzle);
+//   warp 9          tcgen05.mma: S_t = Q_t K^T (operands in shared memory), O_t += P_t V (P in TMEM, V read MN-major).
+// While one tile's S is in its softmax warps the tensor cores run the other tile's products, and K and V feed both
+// tiles. TMEM: S0 S1 (128 columns each, P over the first 64), O0 O1 (d each).
+// Weights are rounded to bf16 (2^-8 relative at most, as the bf16 V that they meet; their sum is kept in fp32 of the
+// unrounded weights). Results leave as fp32 partials (o, m, l) of each key range, which the attention over the rows' own slots
+// joins in its epilogue.
+#include "kv8.cuh"
+#include "kernels.h"
+#include "tc_common.cuh"
+
+#include <algorithm>
+#include <cudaTypedefs.h>
+
+namespace eagle {
+namespace {
+
+constexpr int PT = 128;            // keys a tile, query vectors a tile
+constexpr int PF_THREADS = 384;
+constexpr float PF_LAZY = 8.f;
+constexpr int PF_SMS = 152;        // CTAs that run at once (one an SM)
+
+template <int D>
+struct PfShape {
+  static constexpr int HALVES = D / 64, HALF = PT * 128;        // 64 dims of 128 rows
+  static constexpr int OP = HALVES * HALF;                      // one operand tile
+  static constexpr int OFF_Q = 0, OFF_K = 2 * OP, OFF_V = OFF_K + 2 * OP, OFF_BAR = OFF_V + 2 * OP;
+  static constexpr int BYTES = 1024 + OFF_BAR + 256;
+};
+
+__device__ __forceinline__ constexpr uint32_t pf_idesc(int n, bool b_mn) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (b_mn ? (1u << 16) : 0u) | ((uint32_t)(n >> 3) << 17) |
+         ((uint32_t)(PT >> 4) << 24);
+}
+// MN-major operand, 128-byte swizzle: 64 MN-elements a row, one row per k, the next 64 MN-elements mn_stride on.
+__device__ __forceinline__ uint64_t pf_desc_mn(uint32_t saddr, uint32_t mn_stride) {
+  return (uint64_t)((saddr & 0x3FFFF) >> 4) | ((uint64_t)((mn_stride >> 4) & 0x3FFF) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+// D[tmem] (+)= A[tmem] B[smem desc]
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* map, int c0, int c1, int c2, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32u(uint32_t t, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(t),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]),
+      "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]),
+      "r"(v[30]), "r"(v[31])
+      : "memory");
+}
+__device__ __forceinline__ float pf_ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// (x - m) * s of two values. The difference comes first: it is exact where it matters, near the maximum, whatever
+// the size of the scores.
+__device__ __forceinline__ float2 sub_mul2(float2 x, float2 neg_m, float2 s) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "add.rn.f32x2 a, a, b;\n\tmul.rn.f32x2 a, a, c;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(x.x), "f"(x.y), "f"(neg_m.x), "f"(neg_m.y), "f"(s.x), "f"(s.y));
+  return r;
+}
+__device__ __forceinline__ bool lane0_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err) {
+  int ok = 0;
+  if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity, abort_flag, err) ? 1 : 0;
+  ok = __shfl_sync(0xffffffffu, ok, 0);
+  __syncwarp();
+  return ok != 0;
+}
+
+struct PfArgs {
+  int R, nq, G, RB, P;         // rows, query heads, query heads a KV head, rows a tile
+  int splits, tiles, pairs;    // key ranges, key tiles, pairs of query tiles
+  float sl2;                   // scale * log2(e)
+  float *o, *ml;               // [splits][R * nq][D], [splits][R * nq][2]
+  int* err;
+};
+
+template <int D>
+__global__ void __launch_bounds__(PF_THREADS, 1)
+    prefix_k(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+             const __grid_constant__ CUtensorMap tmV, const PfArgs a) {
+  using Sh = PfShape<D>;
+  extern __shared__ uint8_t pf_smem[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(pf_smem) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + Sh::OFF_BAR);
+  uint64_t *q_full = bars, *k_full = bars + 1, *k_empty = bars + 3, *v_full = bars + 5, *v_empty = bars + 7,
+           *s_full = bars + 9, *p_full = bars + 11, *o_done = bars + 13, *drain = bars + 15;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 16);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int split = blockIdx.x % a.splits, pair = blockIdx.x / a.splits % a.pairs, h = blockIdx.x / (a.splits * a.pairs);
+  const int r0 = pair * 2 * a.RB;
+  const int nmt = r0 + a.RB < a.R ? 2 : 1;     // query tiles of this CTA
+  const int t0 = (int)((long long)a.tiles * split / a.splits), t1 = (int)((long long)a.tiles * (split + 1) / a.splits);
+  const int nt = t1 - t0;                      // >= 1: splits <= tiles
+  if (threadIdx.x == 0) {
+    mbar_init(smem_u32(q_full), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(k_full + i), 1);
+      mbar_init(smem_u32(k_empty + i), 1);
+      mbar_init(smem_u32(v_full + i), 1);
+      mbar_init(smem_u32(v_empty + i), 1);
+      mbar_init(smem_u32(s_full + i), 1);
+      mbar_init(smem_u32(p_full + i), PT);
+      mbar_init(smem_u32(o_done + i), 1);
+    }
+    mbar_init(smem_u32(drain), 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 9) tmem_alloc(smem_u32(tmem_slot), 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  PDL_ENTRY();
+
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+    const int mt = warp >> 2, qv = threadIdx.x & 127;
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + mt * PT + lane_off, tO = tmem + 2 * PT + mt * D + lane_off;
+    float m = -INFINITY, l = 0.f;
+    bool ok = mt < nmt;
+    for (int i = 0; ok && i < nt; ++i) {
+      ok = lane0_wait(smem_u32(s_full + mt), (uint32_t)(i & 1), abort_flag, a.err);
+      if (!ok) break;
+      tc_fence_after();
+      float s[PT];
+#pragma unroll
+      for (int c = 0; c < PT; c += 32) tmem_ld32(tS + c, s + c);
+      const int last = a.P - (t0 + i) * PT;    // keys of this tile, 128 but for the prefix's end
+      if (last < PT)
+#pragma unroll
+        for (int c = 0; c < PT; ++c) s[c] = c < last ? s[c] : -INFINITY;
+      float x0 = s[0], x1 = s[1], x2 = s[2], x3 = s[3];
+#pragma unroll
+      for (int c = 4; c < PT; c += 4) {
+        x0 = fmaxf(x0, s[c]);
+        x1 = fmaxf(x1, s[c + 1]);
+        x2 = fmaxf(x2, s[c + 2]);
+        x3 = fmaxf(x3, s[c + 3]);
+      }
+      const float mx = fmaxf(fmaxf(x0, x1), fmaxf(x2, x3));
+      const bool raise = (mx - m) * a.sl2 > PF_LAZY;
+      float corr = 1.f;
+      if (raise) {
+        corr = pf_ex2((m - mx) * a.sl2);
+        m = mx;
+        l *= corr;
+      }
+      if (i > 0 && __any_sync(0xffffffffu, raise)) {
+        // the last product into O must be there before O is rescaled
+        ok = lane0_wait(smem_u32(o_done + mt), (uint32_t)((i - 1) & 1), abort_flag, a.err);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int c = 0; c < D; c += 16) {
+          float o[16];
+          tmem_ld16(tO + c, o);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) o[j] *= corr;
+          tmem_st16(tO + c, o);
+        }
+      }
+      const float2 nm = make_float2(-m, -m), s2 = make_float2(a.sl2, a.sl2);
+      float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+      for (int c0 = 0; c0 < PT; c0 += 64) {
+        uint32_t w[32];
+#pragma unroll
+        for (int c = 0; c < 64; c += 2) {
+          float2 x = sub_mul2(make_float2(s[c0 + c], s[c0 + c + 1]), nm, s2);
+          x.x = pf_ex2(x.x);
+          x.y = pf_ex2(x.y);
+          sum0 += x.x;
+          sum1 += x.y;
+          const __nv_bfloat162 b = __floats2bfloat162_rn(x.x, x.y);
+          w[c / 2] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+        tmem_st32u(tS + c0 / 2, w);
+      }
+      l += sum0 + sum1;
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(smem_u32(p_full + mt));
+    }
+    if (mt < nmt) {
+      const int row = r0 + mt * a.RB + qv / a.G;
+      const bool write = qv < a.RB * a.G && row < a.R;
+      const size_t q = (size_t)split * a.R * a.nq + (size_t)row * a.nq + h * a.G + qv % a.G;
+      if (ok && lane0_wait(smem_u32(o_done + mt), (uint32_t)((nt - 1) & 1), abort_flag, a.err)) {
+        tc_fence_after();
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          float o[32];
+          tmem_ld32(tO + c, o);
+          if (write)
+#pragma unroll
+            for (int j = 0; j < 32; j += 4)
+              *reinterpret_cast<float4*>(a.o + q * D + c + j) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+        }
+        if (write) {
+          a.ml[2 * q] = m * a.sl2;
+          a.ml[2 * q + 1] = l;
+        }
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    if (warp == 8 && lane == 0) {
+      // ---- TMA ----
+      const int qbytes = a.RB * a.G * 128;
+      mbar_expect_tx(smem_u32(q_full), (uint32_t)(nmt * Sh::HALVES * qbytes));
+      for (int mt = 0; mt < nmt; ++mt)
+        for (int x = 0; x < Sh::HALVES; ++x)
+          tma_load_3d(smem_u32(sm + Sh::OFF_Q + mt * Sh::OP + x * Sh::HALF), &tmQ, x * 64, h * a.G, r0 + mt * a.RB,
+                      smem_u32(q_full));
+      int nk = 0, nv = 0;
+      for (int i = 0; i < nt; ++i) {
+        const int st = i & 1;
+        const uint32_t ph = (uint32_t)((i / 2 - 1) & 1);
+        if (i >= 2 && !mbar_wait(smem_u32(k_empty + st), ph, abort_flag, a.err)) break;
+        mbar_expect_tx(smem_u32(k_full + st), Sh::OP);
+        for (int x = 0; x < Sh::HALVES; ++x)
+          tma_load_3d(smem_u32(sm + Sh::OFF_K + st * Sh::OP + x * Sh::HALF), &tmK, x * 64, (t0 + i) * PT, h,
+                      smem_u32(k_full + st));
+        ++nk;
+        if (i >= 2 && !mbar_wait(smem_u32(v_empty + st), ph, abort_flag, a.err)) break;
+        mbar_expect_tx(smem_u32(v_full + st), Sh::OP);
+        for (int x = 0; x < Sh::HALVES; ++x)
+          tma_load_3d(smem_u32(sm + Sh::OFF_V + st * Sh::OP + x * Sh::HALF), &tmV, x * 64, (t0 + i) * PT, h,
+                      smem_u32(v_full + st));
+        ++nv;
+      }
+      if (*abort_flag) {   // copies in flight land before the CTA leaves: the last two of each ring
+        mbar_wait(smem_u32(q_full), 0, abort_flag, a.err, false);
+        for (int j = std::max(0, nk - 2); j < nk; ++j) mbar_wait(smem_u32(k_full + (j & 1)), (uint32_t)((j / 2) & 1), abort_flag, a.err, false);
+        for (int j = std::max(0, nv - 2); j < nv; ++j) mbar_wait(smem_u32(v_full + (j & 1)), (uint32_t)((j / 2) & 1), abort_flag, a.err, false);
+      }
+    } else if (warp == 9 && lane == 0) {
+      // ---- MMA ----
+      constexpr uint32_t IS = pf_idesc(PT, false), IO = pf_idesc(D, true);
+      bool ok = mbar_wait(smem_u32(q_full), 0, abort_flag, a.err);
+      auto issue_s = [&](int mt, int i) {
+        const uint32_t q = smem_u32(sm + Sh::OFF_Q + mt * Sh::OP), k = smem_u32(sm + Sh::OFF_K + (i & 1) * Sh::OP);
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x)
+          tc_mma_bf16(tmem + mt * PT, sdesc_sw128(q + (x >> 2) * Sh::HALF + (x & 3) * 32),
+                      sdesc_sw128(k + (x >> 2) * Sh::HALF + (x & 3) * 32), IS, x ? 1u : 0u);
+        tc_commit(smem_u32(s_full + mt));
+        if (mt == nmt - 1) tc_commit(smem_u32(k_empty + (i & 1)));
+      };
+      if (ok) ok = mbar_wait(smem_u32(k_full), 0, abort_flag, a.err);
+      if (ok) {
+        tc_fence_after();
+        for (int mt = 0; mt < nmt; ++mt) issue_s(mt, 0);
+      }
+      for (int i = 0; ok && i < nt; ++i) {
+        for (int mt = 0; ok && mt < nmt; ++mt) {
+          // P_i V_i, then S_(i+1) over the same columns: the tensor cores take them in this order
+          ok = mbar_wait(smem_u32(p_full + mt), (uint32_t)(i & 1), abort_flag, a.err) &&
+               (mt || mbar_wait(smem_u32(v_full + (i & 1)), (uint32_t)((i / 2) & 1), abort_flag, a.err));
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t v = smem_u32(sm + Sh::OFF_V + (i & 1) * Sh::OP);
+#pragma unroll
+          for (int x = 0; x < PT / 16; ++x)
+            mma_ts(tmem + 2 * PT + mt * D, tmem + mt * PT + x * 8, pf_desc_mn(v + x * 2048, Sh::HALF), IO, (i || x) ? 1u : 0u);
+          tc_commit(smem_u32(o_done + mt));
+          if (mt == nmt - 1) tc_commit(smem_u32(v_empty + (i & 1)));
+          if (i + 1 < nt) {
+            if (mt == 0) ok = mbar_wait(smem_u32(k_full + ((i + 1) & 1)), (uint32_t)(((i + 1) / 2) & 1), abort_flag, a.err);
+            if (ok) {
+              tc_fence_after();
+              issue_s(mt, i + 1);
+            }
+          }
+        }
+      }
+      if (!ok) {   // products in flight end before the CTA frees its TMEM
+        tc_commit(smem_u32(drain));
+        mbar_wait(smem_u32(drain), 0, abort_flag, a.err, false);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 pf_encode() {
+  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  }();
+  return fn;
+}
+
+// bf16 [n2][n1][d] as boxes of 64 x b1 x b2.
+bool map3(CUtensorMap* m, const void* p, int d, int n1, int n2, int b1, int b2) {
+  const auto fn = pf_encode();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)n1, (cuuint64_t)n2};
+  const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)n1 * d * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)b1, (cuuint32_t)b2}, es[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+cudaError_t launch_prefix(cudaStream_t st, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                          const PfArgs& p, int grid) {
+  const cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(prefix_k<D>), PfShape<D>::BYTES);
+  if (e != cudaSuccess) return e;
+  return launch_k(prefix_k<D>, dim3(grid), dim3(PF_THREADS), PfShape<D>::BYTES, st, q, k, v, p);
+}
+
+}  // namespace
+
+// Key ranges: the count that ends first on 152 SMs, a range costing its tiles plus about one and a half for filling the
+// pipeline and writing its partials, which the joining side reads again (a third of a tile each).
+int kv8_prefix_splits(int nkv, int R, int nq, int P) {
+  const int RB = PT / (nq / nkv), tiles = (P + PT - 1) / PT;
+  const long long items = (long long)nkv * ((R + 2 * RB - 1) / (2 * RB));
+  int best = 1;
+  double least = 1e300;
+  for (int s = 1; s <= std::min(tiles, 32); ++s) {
+    const double t = (double)((items * s + PF_SMS - 1) / PF_SMS) * ((tiles + s - 1) / s + 1.5) + s / 3.0;
+    if (t < least) {
+      least = t;
+      best = s;
+    }
+  }
+  return best;
+}
+
+int kv8_prefix(cudaStream_t st, const Kv8Attn& a, int splits, float* o, float* ml) {
+  PfArgs p{};
+  const int nkv = a.c.nkv, d = a.c.d;
+  p.R = a.R; p.nq = a.nq; p.G = a.nq / nkv; p.RB = PT / p.G; p.P = a.P;
+  p.splits = splits; p.tiles = (a.P + PT - 1) / PT; p.pairs = (a.R + 2 * p.RB - 1) / (2 * p.RB);
+  p.sl2 = a.scale * 1.4426950408889634f;
+  p.o = o; p.ml = ml; p.err = a.err;
+  const long long grid = (long long)nkv * p.pairs * splits;
+  if (grid > 0x7fffffffll) return -1;
+  CUtensorMap q, k, v;
+  if (!map3(&q, a.q, d, a.nq, a.R, p.G, p.RB) || !map3(&k, a.pk, d, a.P, nkv, PT, 1) || !map3(&v, a.pv, d, a.P, nkv, PT, 1))
+    return -4;
+  const cudaError_t e = d == 128 ? launch_prefix<128>(st, q, k, v, p, (int)grid) : launch_prefix<64>(st, q, k, v, p, (int)grid);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return -4;
+  }
+  return 0;
+}
+
+}  // namespace eagle

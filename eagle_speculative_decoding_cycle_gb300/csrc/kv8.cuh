@@ -65,5 +65,9 @@ int kv8_read(cudaStream_t st, const Kv8& c, bool f32, void* k, long long ldk, vo
              const int* row_seq, const int* row_slot, int* err);
 size_t kv8_attention_scratch(const Kv8& c, int R, int nq, int rows_per_seq, int P);
 int kv8_attention(cudaStream_t st, const Kv8Attn& a);
+// Partials of all rows over the shared prefix, in `splits` key ranges: o [splits][R * nq][d], ml [splits][R * nq][2]
+// (maximum in log2 units, sum).
+int kv8_prefix_splits(int nkv, int R, int nq, int P);
+int kv8_prefix(cudaStream_t st, const Kv8Attn& a, int splits, float* o, float* ml);
 
 }  // namespace eagle

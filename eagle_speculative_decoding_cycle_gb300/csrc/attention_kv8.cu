@@ -72,12 +72,22 @@ __device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
+// 16 bytes into shared memory; this thread's earlier copies arrive on `bar` once they are there.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
 // 2^n, 0 below the normal range.
 __device__ __forceinline__ float pow2i(int n) { return n < -126 ? 0.f : __int_as_float((min(n, 127) + 127) << 23); }
 
 // How a call's rows are cut and its tiles shared out: the same numbers in both kernels and the scratch size.
 struct Plan {
   int G, RB, nb, QV;      // query heads a KV head; rows a block; blocks a sequence; query vectors a block
+  uint32_t G_inv;         // x / G = x * G_inv >> 16 for x < 128
+  int width;              // lanes that look at one row block
+  int nkv;
   int groups;             // row blocks of this launch, from block g0 on
   int g0;
   int grid, min_tiles;    // CTAs at most; tiles a CTA at least
@@ -89,87 +99,102 @@ struct Plan {
   int n_prefix;
 };
 
-__device__ __forceinline__ int active_ctas(const Plan& p, long long W) {
-  return (int)max(1ll, min((long long)p.grid, W / p.min_tiles));
-}
-__device__ __forceinline__ long long range_start(long long c, long long W, int G) { return c * W / G; }
-__device__ __forceinline__ int cta_of(long long u, long long W, int G) { return (int)(((u + 1) * G - 1) / W); }
+// The tiles W of a launch over its CTAs: the first `more` CTAs take `per` + 1 tiles, the others `per`.
+struct Share {
+  uint32_t ctas, per, more;
+  __device__ __forceinline__ Share(const Plan& p, uint32_t W) {
+    // a CTA takes p.min_tiles tiles at least (one for each key group), or a whole average item where those are shorter
+    const uint32_t items = max(1u, (uint32_t)p.groups * (uint32_t)p.nkv);
+    ctas = max(1u, min((uint32_t)p.grid, W / max(1u, min((uint32_t)p.min_tiles, W / items))));
+    per = W / ctas;
+    more = W - per * ctas;
+  }
+  __device__ __forceinline__ uint32_t start(uint32_t c) const { return c * per + min(c, more); }
+  __device__ __forceinline__ uint32_t cta_of(uint32_t u) const {
+    const uint32_t wide = more * (per + 1);
+    return u < wide ? u / (per + 1) : more + (u - wide) / per;
+  }
+};
 
-// Rows of a block, its sequence (that of the first row that is not padding among the sequence's rows) and the
-// first slot past everything that its rows see. Run by one warp; every lane gets the values.
+// A row block's rows, its sequence (that of the first row that is not padding among the sequence's rows) and the
+// first slot past everything that its rows see.
 struct Group {
   int r0, r1, seq, limit;
 };
-__device__ __forceinline__ Group group_of(const Kv8Attn& a, const Plan& p, int gi, bool latch) {
-  const int lane = threadIdx.x & 31;
+__device__ __forceinline__ int first_seq(const Kv8Attn& a, int s0, int s1) {
+  int seq = a.row_seq[s0];
+  for (int r = s0 + 1; r < s1 && seq < 0; ++r) seq = a.row_seq[r];
+  return seq < 0 ? -1 : seq;
+}
+// By `width` neighbouring lanes (a power of two up to 8); gi out of range gives an empty block. All lanes of a warp call.
+__device__ __forceinline__ Group group_of(const Kv8Attn& a, const Plan& p, int gi, int width, bool latch) {
+  const int sub = threadIdx.x & (width - 1);
   Group o;
-  const int sidx = (p.g0 + gi) / p.nb, rb = (p.g0 + gi) % p.nb;
-  const int s0 = sidx * a.rows_per_seq, s1 = min(s0 + a.rows_per_seq, a.R);
+  const int sidx = (p.g0 + gi) / p.nb, rb = (p.g0 + gi) - sidx * p.nb;
+  const int s0 = sidx * a.rows_per_seq, s1 = (int)min((long long)s0 + a.rows_per_seq, (long long)a.R);
   o.r0 = s0 + rb * p.RB;
-  o.r1 = min(o.r0 + p.RB, s1);
-  o.seq = -1;
-  o.limit = 0;
-  if (o.r0 >= o.r1) return o;
-  for (int r = s0; r < s1 && o.seq < 0; r += 32) {
-    const int s = r + lane < s1 ? a.row_seq[r + lane] : -1;
-    const unsigned any = __ballot_sync(0xffffffffu, s >= 0);
-    if (any) o.seq = __shfl_sync(0xffffffffu, s, __ffs(any) - 1);
-  }
-  if (o.seq < 0) return o;
+  o.r1 = gi < p.groups ? min(o.r0 + p.RB, s1) : o.r0;
+  o.seq = o.r0 < o.r1 ? first_seq(a, s0, s1) : -1;
   bool bad = o.seq >= a.c.max_batch;
-  if (bad) {
-    o.seq = -1;
-  } else {
-    int lim = 0;
-    const int ctx = a.mode == 1 ? a.ctx_len[o.seq] : 0;
-    for (int r = o.r0 + lane; r < o.r1; r += 32) {
-      if (a.row_seq[r] != o.seq) {
-        bad = bad || a.row_seq[r] >= 0;
-        continue;
-      }
-      if (a.mode == 0) {
-        lim = max(lim, min(a.row_slot[r], INT32_MAX - 1) + 1);
-      } else {
-        int top = ctx;
-        for (int w = (a.tree_T - 1) >> 6; w >= 0; --w) {
+  if (bad) o.seq = -1;
+  const int ctx = a.mode == 1 && o.seq >= 0 ? a.ctx_len[o.seq] : 0;
+  int lim = 0;
+  if (o.seq >= 0) {
+    bad = bad || ctx < 0;
+    const int words = (a.tree_T + 63) >> 6;
+    for (int r = o.r0 + sub; r < o.r1; r += width) {
+      const int rs = a.row_seq[r];
+      int end = a.mode == 0 ? min(a.row_slot[r], INT32_MAX - 1) + 1 : ctx;
+      if (a.mode == 1)
+        for (int w = 0; w < words; ++w) {
           uint64_t m = a.mask[(size_t)r * a.mask_words + w];
-          if (w == (a.tree_T - 1) >> 6 && (a.tree_T & 63)) m &= (1ull << (a.tree_T & 63)) - 1;
-          if (m) {
-            top = (int)min((long long)INT32_MAX, (long long)ctx + w * 64 + 64 - __clzll((long long)m));
-            break;
-          }
+          if (w == words - 1 && (a.tree_T & 63)) m &= (1ull << (a.tree_T & 63)) - 1;
+          if (m) end = (int)min((long long)INT32_MAX, (long long)ctx + w * 64 + 64 - __clzll((long long)m));
         }
-        lim = max(lim, top);
-        bad = bad || ctx < 0;
-      }
+      if (rs == o.seq) lim = max(lim, end);
+      else bad = bad || rs >= 0;
     }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) lim = max(lim, __shfl_xor_sync(0xffffffffu, lim, d));
-    bad = bad || lim > a.c.cap;
-    o.limit = min(lim, a.c.cap);
   }
-  if (latch && __any_sync(0xffffffffu, bad) && lane == 0) latch_error(a.err, DEVERR_BOUNDS);
+  for (int d = width >> 1; d > 0; d >>= 1) lim = max(lim, __shfl_xor_sync(0xffffffffu, lim, d));
+  bad = bad || lim > a.c.cap;
+  o.limit = max(0, min(lim, a.c.cap));
+  if (latch && bad) latch_error(a.err, DEVERR_BOUNDS);
   return o;
 }
 
-// out (or partial) values of 8 dims: joined with the prefix's partials.
-__device__ __forceinline__ void join_prefix(const Plan& p, size_t at, size_t stride, int D, int c, float& M, float& L, float* o) {
-  float top = M;
-  for (int s = 0; s < p.n_prefix; ++s) top = fmaxf(top, p.pp_ml[(s * stride + at) * 2]);
-  const float base = top == -INFINITY ? 0.f : top;
-  const float f = ex2(M - base);
+// Adds n partials to (top, L, o), o 8 values of a query vector whose D values are spread over D / 8 neighbouring
+// lanes (sub: this lane's place among them): the lanes share the (m, l) pairs, the sums run in the order of the partials.
+template <int D, typename At>
+__device__ __forceinline__ void fold(int n, At at, const float* ml, const float* po, int sub, float& top, float& L, float* o) {
+  constexpr int GL = D / 8;
+  const unsigned group = ((GL == 32 ? 0u : 1u << GL) - 1u) << ((threadIdx.x & 31) / GL * GL);
+  float mx = top;
+  for (int i = sub; i < n; i += GL) mx = fmaxf(mx, ml[2 * at(i)]);
+#pragma unroll
+  for (int d = GL / 2; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(group, mx, d));
+  const float base = mx == -INFINITY ? 0.f : mx, f = ex2(top - base);
+  top = mx;
   L *= f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) o[i] *= f;
-  for (int s = 0; s < p.n_prefix; ++s) {
-    const float w = ex2(p.pp_ml[(s * stride + at) * 2] - base);
-    L = fmaf(p.pp_ml[(s * stride + at) * 2 + 1], w, L);
-    const float4* x = reinterpret_cast<const float4*>(p.pp_o + (s * stride + at) * D + c);
-    const float4 a = x[0], b = x[1];
-    o[0] = fmaf(a.x, w, o[0]); o[1] = fmaf(a.y, w, o[1]); o[2] = fmaf(a.z, w, o[2]); o[3] = fmaf(a.w, w, o[3]);
-    o[4] = fmaf(b.x, w, o[4]); o[5] = fmaf(b.y, w, o[5]); o[6] = fmaf(b.z, w, o[6]); o[7] = fmaf(b.w, w, o[7]);
+  for (int i0 = 0; i0 < n; i0 += GL) {
+    float w = 0.f, lw = 0.f;
+    if (i0 + sub < n) {
+      const float2 v = *reinterpret_cast<const float2*>(ml + 2 * at(i0 + sub));
+      w = ex2(v.x - base);
+      lw = v.y * w;
+    }
+    const int cnt = min(GL, n - i0);
+#pragma unroll 4
+    for (int j = 0; j < cnt; ++j) {
+      const float4* x = reinterpret_cast<const float4*>(po + at(i0 + j) * D + sub * 8);
+      const float4 a = x[0], b = x[1];
+      const float wj = __shfl_sync(group, w, j, GL);
+      L += __shfl_sync(group, lw, j, GL);
+      o[0] = fmaf(a.x, wj, o[0]); o[1] = fmaf(a.y, wj, o[1]); o[2] = fmaf(a.z, wj, o[2]); o[3] = fmaf(a.w, wj, o[3]);
+      o[4] = fmaf(b.x, wj, o[4]); o[5] = fmaf(b.y, wj, o[5]); o[6] = fmaf(b.z, wj, o[6]); o[7] = fmaf(b.w, wj, o[7]);
+    }
   }
-  M = top;
 }
 
 // 8 finished values of one query vector; nothing seen, or a row that is padding or invalid: zeros.
@@ -190,21 +215,21 @@ template <int D, int NT, int WN, int WK, int NS>
 struct Shape {
   static_assert(NS < 32, "a producer lane has at most one tile in flight");
   static constexpr int QV = 8 * NT * WN, NW = WN * WK;
-  // Eight consumer warps that hold wide accumulators: a producer warpgroup of its own gives its registers to them
-  // (168 a thread at launch; 2 x 128 x 232 + 128 x 40 = 384 x 168).
+  // Eight consumer warps that hold wide accumulators: the other warpgroup (one producer, three row warps) gives its
+  // registers to them (168 a thread at launch; 2 x 128 x 232 + 128 x 40 = 384 x 168).
   static constexpr bool SPLIT_REGS = NW == 8;
-  static constexpr int THREADS = (NW + (SPLIT_REGS ? 4 : 1)) * 32;
+  static constexpr int ROWS_W = SPLIT_REGS ? 3 : 1;       // warps that prepare the rows of the next item
+  static constexpr int THREADS = (NW + 1 + ROWS_W) * 32;
   static constexpr int TILE = 2 * TK * D;                 // K codes, V codes
   static constexpr int Q_LD = 2 * D + 32;                 // bytes a query row: 8-byte reads without bank conflicts
   static constexpr int O_LD = D + 4;
   static constexpr int OFF_EXP = NS * TILE;               // [NS][2][TK] exponent bytes
   static constexpr int OFF_Q = OFF_EXP + NS * 2 * TK;
-  static constexpr int OFF_O = OFF_Q + QV * Q_LD;
-  static constexpr int OFF_COL = OFF_O + QV * O_LD * 4;   // qf, slot limit of each query vector
-  static constexpr int OFF_MLE = OFF_COL + QV * 8;        // m, l of each key group
-  static constexpr int OFF_MASK = OFF_MLE + WK * QV * 8;
-  static constexpr int OFF_BAR = OFF_MASK + MAX_QV * 32;
-  static constexpr int OFF_GROUP = OFF_BAR + NS * 16 + 64;
+  static constexpr int Q_BUF = QV * (Q_LD + 8 + 32);      // query rows, (factor, slot limit) of each, masks
+  static constexpr int OFF_O = OFF_Q + 2 * Q_BUF;
+  static constexpr int OFF_MLE = OFF_O + QV * O_LD * 4;   // m, l of each key group
+  static constexpr int OFF_BAR = OFF_MLE + WK * QV * 8;
+  static constexpr int OFF_GROUP = OFF_BAR + NS * 16 + 192;
   static int bytes(int groups) { return 1024 + OFF_GROUP + (3 * groups + 1) * 4; }
 };
 
@@ -218,8 +243,9 @@ __global__ void __launch_bounds__(Shape<D, NT, WN, WK, NS>::THREADS, CTAS)
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + Sh::OFF_BAR);
   uint64_t* empty = full + NS;
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(empty + NS);
-  int* s_fullvis = reinterpret_cast<int*>(empty + NS) + 1;
+  uint64_t *q_full = empty + NS, *q_empty = q_full + 2;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(q_empty + 2);
+  int* s_fullvis = reinterpret_cast<int*>(q_empty + 2) + 1;   // [2][16], by warp
   int* s_pref = reinterpret_cast<int*>(sm + Sh::OFF_GROUP);
   int* s_lim = s_pref + p.groups + 1;
   int* s_seq = s_lim + p.groups;
@@ -227,16 +253,21 @@ __global__ void __launch_bounds__(Shape<D, NT, WN, WK, NS>::THREADS, CTAS)
   const int nkv = a.c.nkv;
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS; ++s) {
-      mbar_init(smem_u32(full + s), 1);
+      mbar_init(smem_u32(full + s), 33);   // the codes' bytes, and each producer lane's exponent copies
       mbar_init(smem_u32(empty + s), WN);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(smem_u32(q_full + b), Sh::ROWS_W);
+      mbar_init(smem_u32(q_empty + b), NW);
     }
     *abort_flag = 0;
     fence_mbar_init();
   }
   PDL_ENTRY();
-  for (int gi = warp; gi < p.groups; gi += Sh::THREADS / 32) {
-    const Group gr = group_of(a, p, gi, blockIdx.x == 0);
-    if (lane == 0) {
+  for (int g0 = 0; g0 < p.groups; g0 += Sh::THREADS / p.width) {
+    const int gi = g0 + threadIdx.x / p.width;
+    const Group gr = group_of(a, p, gi, p.width, blockIdx.x == 0);
+    if (gi < p.groups && (threadIdx.x & (p.width - 1)) == 0) {
       s_lim[gi] = gr.limit;
       s_seq[gi] = gr.seq;
       s_pref[gi + 1] = gr.r0 < gr.r1 ? max(1, (gr.limit + TK - 1) / TK) : 0;
@@ -260,167 +291,211 @@ __global__ void __launch_bounds__(Shape<D, NT, WN, WK, NS>::THREADS, CTAS)
   __syncthreads();
   if (blockIdx.x == 0)
     for (int i = threadIdx.x; i <= p.groups; i += blockDim.x) p.pref[i] = s_pref[i];
-  const long long W = (long long)s_pref[p.groups] * nkv;
-  const int Gd = active_ctas(p, W);
-  if ((int)blockIdx.x >= Gd) return;
-  const long long w0 = range_start(blockIdx.x, W, Gd), w1 = range_start(blockIdx.x + 1, W, Gd);
-  const int n = (int)(w1 - w0);
+  const Share share(p, (uint32_t)s_pref[p.groups] * nkv);
+  if (blockIdx.x >= share.ctas) return;
+  const uint32_t w0 = share.start(blockIdx.x);
+  const int n = (int)(share.start(blockIdx.x + 1) - w0);
 
   // the item (row block, head) that holds flat tile w
-  auto find = [&](long long w, int& gi, int& h, int& t) {
+  auto find = [&](uint32_t w, int& gi, int& h, int& t) {
     int lo = 0, hi = p.groups;   // the last group with pref * nkv <= w
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if ((long long)s_pref[mid] * nkv <= w) lo = mid;
+      if ((uint32_t)s_pref[mid] * nkv <= w) lo = mid;
       else hi = mid;
     }
     gi = lo;
-    const int nt = s_pref[lo + 1] - s_pref[lo], rem = (int)(w - (long long)s_pref[lo] * nkv);
-    h = rem / nt;
-    t = rem - h * nt;
+    const uint32_t nt = s_pref[lo + 1] - s_pref[lo], rem = w - (uint32_t)s_pref[lo] * nkv;
+    h = (int)(rem / nt);
+    t = (int)(rem - h * nt);
   };
+
+  // The query vectors of an item as fp16 of q 2^-e, the factor that gives its scores in log2 units, what each sees. By
+  // `warps` warps, of which this is number sw.
+  auto prepare = [&](int item, int i, int sw, int warps) -> int {
+    constexpr int LQ = D / 8, PER = 32 / LQ, BATCH = 4;   // lanes a vector, 16 bytes each
+    const int sub = lane % LQ;
+    const float sl2 = a.scale * 1.4426950408889634f;
+    int gi, h, t0;
+    find(w0 + i, gi, h, t0);
+    const int buf = item & 1, seq = s_seq[gi];
+    const int sidx = (p.g0 + gi) / p.nb, rb = (p.g0 + gi) - sidx * p.nb;
+    const int r0 = sidx * a.rows_per_seq + rb * p.RB;
+    const int r1 = min(min(r0 + p.RB, (sidx + 1) * a.rows_per_seq), a.R);
+    const int nqv = (r1 - r0) * p.G;
+    const int ctx = a.mode == 1 && seq >= 0 ? a.ctx_len[seq] : 0;
+    uint8_t* q_rows = sm + Sh::OFF_Q + buf * Sh::Q_BUF;
+    float2* q_cols = reinterpret_cast<float2*>(q_rows + Sh::QV * Sh::Q_LD);
+    uint64_t* q_mask = reinterpret_cast<uint64_t*>(q_cols + Sh::QV);
+    if (item >= 2) kv8_wait(smem_u32(q_empty + buf), (uint32_t)((item / 2 - 1) & 1), abort_flag, a.err);
+    if (a.mode == 1)
+      for (int x = sw * 32 + lane; x < (r1 - r0) * 4; x += warps * 32) {
+        const int r = r0 + x / 4, w = x & 3;
+        uint64_t m = 0;
+        if (w * 64 < a.tree_T) {
+          m = a.mask[(size_t)r * a.mask_words + w];
+          if (w == (a.tree_T - 1) >> 6 && (a.tree_T & 63)) m &= (1ull << (a.tree_T & 63)) - 1;
+        }
+        q_mask[x] = seq >= 0 && a.row_seq[r] == seq ? m : 0ull;
+      }
+    int fullvis = INT32_MAX;   // keys below this are seen by every row that counts
+    for (int x0 = sw * PER; x0 < Sh::QV; x0 += PER * warps * BATCH) {
+      uint4 raw[BATCH];
+      int rs[BATCH], lim[BATCH];
+#pragma unroll
+      for (int b = 0; b < BATCH; ++b) {
+        const int x = x0 + lane / LQ + b * PER * warps;
+        raw[b] = make_uint4(0, 0, 0, 0);
+        rs[b] = -1;
+        lim[b] = 0;
+        if (x < nqv) {
+          const int in = (int)(x * p.G_inv >> 16), row = r0 + in;
+          raw[b] = *reinterpret_cast<const uint4*>((const __nv_bfloat16*)a.q +
+                                                   ((size_t)row * a.nq + h * p.G + x - in * p.G) * D + sub * 8);
+          rs[b] = a.row_seq[row];
+          lim[b] = a.mode == 1 ? ctx : min(a.row_slot[row], INT32_MAX - 1) + 1;
+        }
+      }
+#pragma unroll
+      for (int b = 0; b < BATCH; ++b) {
+        const int x = x0 + lane / LQ + b * PER * warps;
+        const bool live = seq >= 0 && rs[b] == seq;
+        const uint32_t r[4] = {live ? raw[b].x : 0u, live ? raw[b].y : 0u, live ? raw[b].z : 0u, live ? raw[b].w : 0u};
+        uint32_t top = 0;   // the largest magnitude's bits
+#pragma unroll
+        for (int k = 0; k < 4; ++k) top = max(top, max(r[k] << 16 & 0x7fffffffu, r[k] & 0x7fff0000u));
+#pragma unroll
+        for (int d = LQ / 2; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+        // largest entry into [2^13, 2^14); a vector with an entry that is not finite gives NaN
+        const bool fine = top < 0x7f800000u;
+        const int e = top && fine ? max((int)(top >> 23) - 127, -126) - 13 : 0;
+        const float up = pow2i(-e / 2), up2 = pow2i(-e - (-e / 2));   // two factors: -e can pass 127
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          w[k] = fine ? half2_of(__uint_as_float(r[k] << 16) * up * up2, __uint_as_float(r[k] & 0xffff0000u) * up * up2)
+                      : 0x7fff7fffu;
+        if (x < Sh::QV) {
+          const int l = live ? max(0, min(lim[b], a.c.cap)) : 0;
+          *reinterpret_cast<uint4*>(q_rows + x * Sh::Q_LD + sub * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+          if (sub == 0) q_cols[x] = make_float2(sl2 * pow2i(e / 2) * pow2i(e - e / 2), __int_as_float(l));
+          if (live) fullvis = min(fullvis, l);
+        }
+      }
+    }
+    fullvis = __reduce_min_sync(0xffffffffu, fullvis);
+    if (lane == 0) s_fullvis[buf * 16 + sw] = fullvis;
+    __syncwarp();
+    return min(s_pref[gi + 1] - s_pref[gi] - t0, n - i);   // the item's tiles in this range
+  };
+  constexpr int FIRST = (NW + Sh::ROWS_W) * 32;   // threads that prepare the first item
 
   if (warp >= NW) {
     if constexpr (Sh::SPLIT_REGS) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-    if (warp > NW) return;
-    // producer: lane j looks after tiles j, j + 32, ... of the range, so that block-table reads of 32 tiles overlap
-    const int box = a.c.table ? min(TK, 1 << a.c.block_log2) : TK, nbox = TK / box;
+    if (warp > NW) {
+      // row warps: the first item together with the consumers, each later one in the buffer that the consumers are not at
+      const int sw = warp - NW - 1;
+      int i = n ? prepare(0, 0, NW + sw, NW + Sh::ROWS_W) : 0;
+      asm volatile("bar.arrive 2, %0;" ::"n"(FIRST) : "memory");
+      for (int item = 1; i < n; ++item) {
+        i += prepare(item, i, sw, Sh::ROWS_W);
+        if (lane == 0) mbar_arrive(smem_u32(q_full + (item & 1)));
+      }
+      return;
+    }
+    // producer: lane j looks up tiles j, j + 32, ... of the range (block-table reads of 32 tiles overlap); lane 0 issues
+    // the codes of all of them (some 100 clocks a TMA copy), lanes 0-3 copy a tile's exponents, 16 bytes each
+    const int box = a.c.table ? min(TK, 1 << a.c.block_log2) : TK;
     const uint64_t pol = l2_policy_evict_first();
+    int st = 0;
+    uint32_t ph = 1;
     int last = -1;
-    for (int b = 0; b < n; b += 32) {
-      const int i = b + lane;
-      int live = 0, t = 0;
-      long long vec[2] = {0, 0};
-      if (i < n) {
-        int gi, h;
-        find(w0 + i, gi, h, t);
-        live = s_lim[gi] - t * TK;
-        const int seq = s_seq[gi];
-        for (int x = 0; x < nbox && x * box < live; ++x) {
-          vec[x] = kv8_vec(a.c, seq, h, t * TK + x * box);
-          if (vec[x] < 0) {   // not assigned: what is read instead is unspecified
-            latch_error(a.err, DEVERR_BOUNDS);
-            vec[x] = 0;
-          }
+    bool ok = true;
+    for (int b = 0; ok && b < n; b += 32) {
+      int halves = 0, vec0 = 0, vec1 = 0;   // the tile's 16-key halves that hold keys, and where they are
+      if (b + lane < n) {
+        int gi, h, t;
+        find(w0 + b + lane, gi, h, t);
+        const int live = s_lim[gi] - t * TK, seq = s_seq[gi];
+        if (live > 0) {
+          const long long v = kv8_vec(a.c, seq, h, t * TK);
+          long long u = v + 16;
+          halves = 1;
+          if (box == TK ? (a.c.table || t * TK + 16 < a.c.cap) : live > 16) halves = 2;
+          if (box < TK && halves == 2) u = kv8_vec(a.c, seq, h, t * TK + 16);
+          if (v < 0 || (halves == 2 && u < 0)) latch_error(a.err, DEVERR_BOUNDS);   // not assigned: unspecified keys
+          vec0 = (int)max(v, 0ll);
+          vec1 = (int)max(u, 0ll);
         }
       }
-      for (int j = 0; j < 32 && b + j < n; ++j) {
-        if (lane == j) {
-          const int st = i % NS;
-          const uint32_t bar = smem_u32(full + st);
-          bool ok = *abort_flag == 0;
-          if (ok && i >= NS) ok = mbar_wait(smem_u32(empty + st), (uint32_t)((i / NS - 1) & 1), abort_flag, a.err);
-          if (ok) {
-            last = i;
-            if (live <= 0) {
-              mbar_arrive(bar);
-            } else {
-              const int ne = a.c.table ? box : min(TK, a.c.cap - t * TK);   // exponent bytes a box (16 or 32)
-              int boxes = 0;
-              for (int x = 0; x < nbox; ++x) boxes += x * box < live;
-              mbar_expect_tx(bar, (uint32_t)(boxes * 2 * (box * D + ne)));
-              for (int x = 0; x < boxes; ++x) {
-                const uint32_t k = smem_u32(sm + st * Sh::TILE + x * box * D), v = k + TK * D;
-                const uint32_t ke = smem_u32(sm + Sh::OFF_EXP + st * 2 * TK + x * box), ve = ke + TK;
-                tma_load_2d(k, &tmK, 0, (int)vec[x], bar, pol);
-                tma_load_2d(v, &tmV, 0, (int)vec[x], bar, pol);
-                bulk_load(ke, a.c.ke + vec[x], (uint32_t)ne, bar);
-                bulk_load(ve, a.c.ve + vec[x], (uint32_t)ne, bar);
-              }
-            }
+      const int m = min(32, n - b);
+      for (int j = 0; j < m; ++j) {
+        const int nh = __shfl_sync(0xffffffffu, halves, j);
+        const int v0 = __shfl_sync(0xffffffffu, vec0, j), v1 = __shfl_sync(0xffffffffu, vec1, j);
+        if (b + j >= NS && !kv8_wait(smem_u32(empty + st), ph, abort_flag, a.err)) ok = false;
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const uint32_t bar = smem_u32(full + st);
+        last = b + j;
+        if (lane < 2 * nh)
+          copy16(smem_u32(sm + Sh::OFF_EXP + st * 2 * TK) + (lane & 1) * TK + (lane >> 1) * 16,
+                 ((lane & 1) ? a.c.ve : a.c.ke) + (lane < 2 ? v0 : v1));
+        copies_arrive(bar);
+        if (lane == 0) {
+          const int boxes = box == TK ? min(nh, 1) : nh;
+          const uint32_t k = smem_u32(sm + st * Sh::TILE);
+          mbar_expect_tx(bar, (uint32_t)(boxes * 2 * box * D));
+          if (boxes) {
+            tma_load_2d(k, &tmK, 0, v0, bar, pol);
+            tma_load_2d(k + TK * D, &tmV, 0, v0, bar, pol);
+          }
+          if (boxes > 1) {
+            tma_load_2d(k + 16 * D, &tmK, 0, v1, bar, pol);
+            tma_load_2d(k + TK * D + 16 * D, &tmV, 0, v1, bar, pol);
           }
         }
-        __syncwarp();
+        if (++st == NS) {
+          st = 0;
+          ph ^= 1;
+        }
       }
     }
-    // after a timeout the tiles in flight land before the CTA leaves: a tile in flight is the last one of its lane (the
-    // ring has fewer than 32 tiles)
-    if (*abort_flag && last >= 0) mbar_wait(smem_u32(full + last % NS), (uint32_t)((last / NS) & 1), abort_flag, a.err, false);
+    // after a timeout the tiles in flight land before the CTA leaves: the last NS that were issued
+    if (!ok)
+      for (int x = max(0, last - NS + 1); x <= last; ++x)
+        kv8_wait(smem_u32(full + x % NS), (uint32_t)((x / NS) & 1), abort_flag, a.err, false);
   } else {
     if constexpr (Sh::SPLIT_REGS) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
     const int kw = warp / WN, nw = warp % WN;
     const int g = lane >> 2, t4 = lane & 3;
-    float* s_qf = reinterpret_cast<float*>(sm + Sh::OFF_COL);
-    int* s_klim = reinterpret_cast<int*>(s_qf + Sh::QV);
     float* s_m = reinterpret_cast<float*>(sm + Sh::OFF_MLE);
     float* s_l = s_m + WK * Sh::QV;
     float* s_o = reinterpret_cast<float*>(sm + Sh::OFF_O);
-    uint64_t* s_mask = reinterpret_cast<uint64_t*>(sm + Sh::OFF_MASK);
-    const float sl2 = a.scale * 1.4426950408889634f;
+    if (n) prepare(0, 0, warp, NW + Sh::ROWS_W);
+    asm volatile("bar.sync 2, %0;" ::"n"(FIRST) : "memory");
+    // this lane's row of the ldmatrix tiles, with its swizzle, 16-byte column 0: column c is at ^ (16 c)
+    auto swizzled = [&](int row, int col) { return row * D + (D == 128 ? col ^ (row & 7) : col ^ ((row >> 1) & 3)) * 16; };
+    const uint32_t k_at = swizzled(lane, 0), v_at = swizzled(lane & 15, lane >> 4);
     int i = 0;   // tiles of the range that are behind
-    while (i < n) {
+    for (int item = 0; i < n; ++item) {
       int gi, h, t0;
       find(w0 + i, gi, h, t0);
       const int nt = s_pref[gi + 1] - s_pref[gi];
       const int t1 = min(nt, t0 + n - i);
       const int seq = s_seq[gi], limit = s_lim[gi];
-      const int sidx = (p.g0 + gi) / p.nb, rb = (p.g0 + gi) % p.nb;
+      const int sidx = (p.g0 + gi) / p.nb, rb = (p.g0 + gi) - sidx * p.nb;
       const int r0 = sidx * a.rows_per_seq + rb * p.RB;
       const int r1 = min(min(r0 + p.RB, (sidx + 1) * a.rows_per_seq), a.R);
       const int nqv = (r1 - r0) * p.G;
       const int ctx = a.mode == 1 && seq >= 0 ? a.ctx_len[seq] : 0;
 
-      // the rows: query vectors as fp16 of q 2^-e, what they see
-      if (threadIdx.x == 0) *s_fullvis = INT32_MAX;
-      if (a.mode == 1)
-        for (int x = threadIdx.x; x < (r1 - r0) * 4; x += NC) {
-          const int r = r0 + x / 4, w = x & 3;
-          uint64_t m = 0;
-          if (seq >= 0 && a.row_seq[r] == seq && w * 64 < a.tree_T) {
-            m = a.mask[(size_t)r * a.mask_words + w];
-            if (w == (a.tree_T - 1) >> 6 && (a.tree_T & 63)) m &= (1ull << (a.tree_T & 63)) - 1;
-          }
-          s_mask[x] = m;
-        }
-      for (int x = warp; x < Sh::QV; x += NW) {
-        const int row = r0 + x / p.G, head = h * p.G + x % p.G;
-        const bool live = x < nqv && seq >= 0 && a.row_seq[row] == seq;
-        constexpr int E = D / 32;
-        float f[E];
-        float top = 0.f;
-        bool fine = true;
-        if (live) {
-          const __nv_bfloat16* q = (const __nv_bfloat16*)a.q + ((size_t)row * a.nq + head) * D + lane * E;
-#pragma unroll
-          for (int k = 0; k < E; k += 2) {
-            const float2 v = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(q + k));
-            f[k] = v.x;
-            f[k + 1] = v.y;
-          }
-        } else {
-#pragma unroll
-          for (int k = 0; k < E; ++k) f[k] = 0.f;
-        }
-#pragma unroll
-        for (int k = 0; k < E; ++k) {
-          top = fmaxf(top, fabsf(f[k]));
-          fine = fine && isfinite(f[k]);
-        }
-        top = warp_max(top);
-        fine = __all_sync(0xffffffffu, fine);
-        // largest entry into [2^13, 2^14); a vector with an entry that is not finite gives NaN
-        int e = top > 0.f && fine ? max((int)(__float_as_uint(top) >> 23) - 127, -126) - 13 : 0;
-        const float up = pow2i(-e / 2), up2 = pow2i(-e - (-e / 2));   // two factors: -e can pass 127
-        uint32_t w[E / 2];
-#pragma unroll
-        for (int k = 0; k < E / 2; ++k)
-          w[k] = fine ? half2_of(f[2 * k] * up * up2, f[2 * k + 1] * up * up2) : 0x7fff7fffu;
-        uint8_t* dst = sm + Sh::OFF_Q + x * Sh::Q_LD + lane * E * 2;
-        if constexpr (E == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
-        else *reinterpret_cast<uint32_t*>(dst) = w[0];
-        if (lane == 0) {
-          s_qf[x] = sl2 * pow2i(e / 2) * pow2i(e - e / 2);
-          int lim = 0;
-          if (live) lim = a.mode == 1 ? ctx : min(a.row_slot[row], INT32_MAX - 1) + 1;
-          s_klim[x] = max(0, min(lim, a.c.cap));
-        }
-      }
-      named_bar_sync(1, NC);
-      // keys below this are seen by every row that counts
-      for (int x = threadIdx.x; x < nqv; x += NC)
-        if (seq >= 0 && a.row_seq[r0 + x / p.G] == seq) atomicMin(s_fullvis, s_klim[x]);
-      named_bar_sync(1, NC);
-      const int fullvis = *s_fullvis;
+      const int buf = item & 1;
+      const uint8_t* s_q = sm + Sh::OFF_Q + buf * Sh::Q_BUF;
+      const float2* s_col = reinterpret_cast<const float2*>(s_q + Sh::QV * Sh::Q_LD);
+      const uint64_t* s_mask = reinterpret_cast<const uint64_t*>(s_col + Sh::QV);
+      if (item) kv8_wait(smem_u32(q_full + buf), (uint32_t)((item / 2 - (buf == 0)) & 1), abort_flag, a.err);
+      int fullvis = s_fullvis[buf * 16];
+      for (int w = 1; w < (item ? Sh::ROWS_W : NW + Sh::ROWS_W); ++w) fullvis = min(fullvis, s_fullvis[buf * 16 + w]);
 
       float O[D / 16][NT][4], m[NT][2], l[NT][2], qf[NT][2];
 #pragma unroll
@@ -430,52 +505,50 @@ __global__ void __launch_bounds__(Shape<D, NT, WN, WK, NS>::THREADS, CTAS)
         const int col = (nw * NT + x) * 8 + 2 * t4;
         m[x][0] = m[x][1] = -INFINITY;
         l[x][0] = l[x][1] = 0.f;
-        qf[x][0] = s_qf[col];
-        qf[x][1] = s_qf[col + 1];
+        qf[x][0] = s_col[col].x;
+        qf[x][1] = s_col[col + 1].x;
       }
       int E_run = 0;
 
       for (int t = t0; t < t1; ++t, ++i) {
         if (i % WK != kw) continue;
         const int st = i % NS;
-        mbar_wait(smem_u32(full + st), (uint32_t)((i / NS) & 1), abort_flag, a.err);
+        kv8_wait(smem_u32(full + st), (uint32_t)((i / NS) & 1), abort_flag, a.err);
         const int key0 = t * TK;
         if (key0 < limit && !*abort_flag) {
           const uint8_t* s_ke = sm + Sh::OFF_EXP + st * 2 * TK;
           const uint8_t* s_ve = s_ke + TK;
           const uint32_t kb = smem_u32(sm + st * Sh::TILE), vb = kb + TK * D;
           const bool masked = key0 + TK > fullvis;
-          auto visible = [&](int key, int col) -> bool {
-            if (key < s_klim[col]) return true;
-            const int tt = key - ctx;
-            if (a.mode != 1 || tt < 0 || tt >= 256 || col >= nqv || key >= limit) return false;
-            return (s_mask[col / p.G * 4 + (tt >> 6)] >> (tt & 63)) & 1;
+          // the tile's keys that a query vector sees, one bit a key
+          auto sees = [&](int col) -> uint32_t {
+            const int below = __float_as_int(s_col[col].y) - key0;
+            uint32_t v = below >= TK ? 0xffffffffu : below <= 0 ? 0u : (1u << below) - 1;
+            if (a.mode == 1 && col < nqv) {
+              const uint32_t* w = reinterpret_cast<const uint32_t*>(s_mask + (col * p.G_inv >> 16) * 4);
+              const int tt = key0 - ctx;   // tree slot of the tile's first key
+              const uint32_t lo = tt >= 0 && tt < 256 ? w[tt >> 5] : 0u;
+              const uint32_t hi = tt >= -31 && tt < 224 ? w[(tt + 32) >> 5] : 0u;
+              v |= __funnelshift_r(lo, hi, tt & 31);
+            }
+            return limit - key0 >= TK ? v : v & ((1u << (limit - key0)) - 1);
           };
-          // keys that one of this warp's query vectors sees: bit = key in tile
-          uint32_t seen = 0xffffffffu;
-          uint32_t vis[2] = {0xffffffffu, 0xffffffffu};   // [key half of 16][..]: bits of this thread's scores
+          uint32_t seen = 0xffffffffu, vis[NT][2];   // keys that one of this warp's query vectors sees; that each sees
           if (masked) {
             seen = 0;
-            vis[0] = vis[1] = 0;
 #pragma unroll
-            for (int mt = 0; mt < 2; ++mt)
+            for (int x = 0; x < NT; ++x)
 #pragma unroll
-              for (int hf = 0; hf < 2; ++hf) {
-                bool any = false;
-#pragma unroll
-                for (int x = 0; x < NT; ++x)
-#pragma unroll
-                  for (int e = 0; e < 2; ++e) {
-                    const bool v = visible(key0 + mt * 16 + hf * 8 + g, (nw * NT + x) * 8 + 2 * t4 + e);
-                    vis[mt] |= (uint32_t)v << (x * 4 + hf * 2 + e);
-                    any = any || v;
-                  }
-                const uint32_t bal = __ballot_sync(0xffffffffu, any);
-#pragma unroll
-                for (int r = 0; r < 8; ++r) seen |= (((bal >> (4 * r)) & 15u) ? 1u : 0u) << (mt * 16 + hf * 8 + r);
+              for (int e = 0; e < 2; ++e) {
+                vis[x][e] = sees((nw * NT + x) * 8 + 2 * t4 + e);
+                seen |= vis[x][e];
+                vis[x][e] >>= g;   // this thread's keys: bits 0, 8, 16, 24
               }
+            seen |= __shfl_xor_sync(0xffffffffu, seen, 1);
+            seen |= __shfl_xor_sync(0xffffffffu, seen, 2);
           }
-          // exponents of the values: the largest and smallest of the seen ones
+          // exponents, lane = key: of the values, the largest and smallest that count
+          const float fk = kv8_pow2(s_ke[lane]);
           const int vbyte = s_ve[lane];
           const bool counts = ((seen >> lane) & 1u) && vbyte != KV8_BAD;
           int hi = (int)__reduce_max_sync(0xffffffffu, counts ? (uint32_t)vbyte : 0u);
@@ -484,15 +557,9 @@ __global__ void __launch_bounds__(Shape<D, NT, WN, WK, NS>::THREADS, CTAS)
           while (true) {
             const bool one = hi - lo_all <= E_SPAN;
             const int lo = one ? 0 : hi - E_SPAN;
+            float unit = 1.f;   // O from the old reference exponent to the new one
             if (hi > E_run + E_UP || (one ? lo_all : lo) < E_run - E_DOWN) {
-              const float f = pow2i(E_run - hi);   // O is zero before the first tile
-              if (E_run)
-#pragma unroll
-                for (int c = 0; c < D / 16; ++c)
-#pragma unroll
-                  for (int x = 0; x < NT; ++x)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) O[c][x][e] *= f;
+              if (E_run) unit = pow2i(E_run - hi);   // O is zero before the first tile
               E_run = hi;
             }
             float s[2][NT][4];
@@ -503,17 +570,14 @@ __global__ void __launch_bounds__(Shape<D, NT, WN, WK, NS>::THREADS, CTAS)
 #pragma unroll
             for (int c = 0; c < D / 16; ++c) {
               uint32_t r[4], a0[4], a1[4];
-              const int row = (lane >> 3) * 8 + (lane & 7);
-              const int ch = D == 128 ? c ^ (row & 7) : c ^ ((row >> 1) & 3);
-              ldsm4(kb + row * D + ch * 16, r);
-              a0[0] = e4m3x2_f16x2(r[0]); a0[1] = e4m3x2_f16x2(r[1]);
-              a0[2] = e4m3x2_f16x2(r[0] >> 16); a0[3] = e4m3x2_f16x2(r[1] >> 16);
-              a1[0] = e4m3x2_f16x2(r[2]); a1[1] = e4m3x2_f16x2(r[3]);
-              a1[2] = e4m3x2_f16x2(r[2] >> 16); a1[3] = e4m3x2_f16x2(r[3] >> 16);
+              ldsm4(kb + (k_at ^ (c * 16)), r);
+              e4m3x4_f16(r[0], a0[0], a0[2]);
+              e4m3x4_f16(r[1], a0[1], a0[3]);
+              e4m3x4_f16(r[2], a1[0], a1[2]);
+              e4m3x4_f16(r[3], a1[1], a1[3]);
 #pragma unroll
               for (int x = 0; x < NT; ++x) {
-                const uint2 b = *reinterpret_cast<const uint2*>(sm + Sh::OFF_Q + ((nw * NT + x) * 8 + g) * Sh::Q_LD +
-                                                                c * 32 + t4 * 8);
+                const uint2 b = *reinterpret_cast<const uint2*>(s_q + ((nw * NT + x) * 8 + g) * Sh::Q_LD + c * 32 + t4 * 8);
                 mma_f16(s[0][x], a0, b.x, b.y);
                 mma_f16(s[1][x], a1, b.x, b.y);
               }
@@ -523,7 +587,7 @@ __global__ void __launch_bounds__(Shape<D, NT, WN, WK, NS>::THREADS, CTAS)
             for (int x = 0; x < NT; ++x) mx[x][0] = mx[x][1] = -INFINITY;
 #pragma unroll
             for (int mt = 0; mt < 2; ++mt) {
-              const float f0 = kv8_pow2(s_ke[mt * 16 + g]), f1 = kv8_pow2(s_ke[mt * 16 + 8 + g]);
+              const float f0 = __shfl_sync(0xffffffffu, fk, mt * 16 + g), f1 = __shfl_sync(0xffffffffu, fk, mt * 16 + 8 + g);
 #pragma unroll
               for (int x = 0; x < NT; ++x) {
                 // to log2 units here, not inside the subtraction below: a fused x - m would leave the rounding of a
@@ -533,7 +597,7 @@ __global__ void __launch_bounds__(Shape<D, NT, WN, WK, NS>::THREADS, CTAS)
                 if (masked)
 #pragma unroll
                   for (int e = 0; e < 4; ++e)
-                    if (!((vis[mt] >> (x * 4 + e)) & 1u)) s[mt][x][e] = -INFINITY;
+                    if (!((vis[x][e & 1] >> (mt * 16 + (e >> 1) * 8)) & 1u)) s[mt][x][e] = -INFINITY;
                 mx[x][0] = fmaxf(mx[x][0], fmaxf(s[mt][x][0], s[mt][x][2]));
                 mx[x][1] = fmaxf(mx[x][1], fmaxf(s[mt][x][1], s[mt][x][3]));
               }
@@ -543,7 +607,7 @@ __global__ void __launch_bounds__(Shape<D, NT, WN, WK, NS>::THREADS, CTAS)
             for (int x = 0; x < NT; ++x)
 #pragma unroll
               for (int e = 0; e < 2; ++e) raise = raise || mx[x][e] > m[x][e] + LAZY;
-            if (__any_sync(0xffffffffu, raise)) {
+            if (__any_sync(0xffffffffu, raise || unit != 1.f)) {
 #pragma unroll
               for (int x = 0; x < NT; ++x)
 #pragma unroll
@@ -552,26 +616,27 @@ __global__ void __launch_bounds__(Shape<D, NT, WN, WK, NS>::THREADS, CTAS)
                   v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
                   v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
                   v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+                  float corr = 1.f;
                   if (v > m[x][e] + LAZY) {
-                    const float corr = ex2(m[x][e] - v);
+                    corr = ex2(m[x][e] - v);
                     m[x][e] = v;
                     l[x][e] *= corr;
+                  }
+                  corr *= unit;
 #pragma unroll
-                    for (int c = 0; c < D / 16; ++c) {
-                      O[c][x][e] *= corr;
-                      O[c][x][2 + e] *= corr;
-                    }
+                  for (int c = 0; c < D / 16; ++c) {
+                    O[c][x][e] *= corr;
+                    O[c][x][2 + e] *= corr;
                   }
                 }
             }
             // weights, then weights times 2^(exponent - E_run) as the B operand of the value product
             uint32_t pb[2][NT][2];
+            // not finite: NaN where seen; outside this pass's exponents, or seen by nobody: 0
+            const float fv = vbyte == KV8_BAD ? kv8_pow2(vbyte) : vbyte >= lo && vbyte <= hi ? pow2i(vbyte - E_run) : 0.f;
 #pragma unroll
             for (int mt = 0; mt < 2; ++mt) {
-              const int b0 = s_ve[mt * 16 + g], b1 = s_ve[mt * 16 + 8 + g];
-              // not finite: NaN where seen; outside this pass's exponents, or seen by nobody: 0
-              const float v0 = b0 == KV8_BAD ? kv8_pow2(b0) : (b0 >= lo && b0 <= hi ? pow2i(b0 - E_run) : 0.f);
-              const float v1 = b1 == KV8_BAD ? kv8_pow2(b1) : (b1 >= lo && b1 <= hi ? pow2i(b1 - E_run) : 0.f);
+              const float v0 = __shfl_sync(0xffffffffu, fv, mt * 16 + g), v1 = __shfl_sync(0xffffffffu, fv, mt * 16 + 8 + g);
 #pragma unroll
               for (int x = 0; x < NT; ++x) {
                 float w[4];
@@ -581,7 +646,7 @@ __global__ void __launch_bounds__(Shape<D, NT, WN, WK, NS>::THREADS, CTAS)
                   const float pr = ex2(s[mt][x][e] - base);
                   if (first) l[x][e & 1] += pr;
                   w[e] = pr * (e < 2 ? v0 : v1);
-                  if (masked && !((vis[mt] >> (x * 4 + e)) & 1u)) w[e] = 0.f;
+                  if (masked && !((vis[x][e & 1] >> (mt * 16 + (e >> 1) * 8)) & 1u)) w[e] = 0.f;
                 }
                 pb[mt][x][0] = transpose8(half2_of(w[0], w[1]));
                 pb[mt][x][1] = transpose8(half2_of(w[2], w[3]));
@@ -589,24 +654,21 @@ __global__ void __launch_bounds__(Shape<D, NT, WN, WK, NS>::THREADS, CTAS)
             }
 #pragma unroll
             for (int mt = 0; mt < 2; ++mt) {
-              uint32_t z0 = 0xffffffffu, z1 = 0xffffffffu;   // codes of keys that nobody sees are left out
+              // a pair's bytes (k0 d0, k0 d1, k1 d0, k1 d1) to (k0 d0, k1 d0, k0 d1, k1 d1); zeros for keys that nobody sees
+              uint32_t sel0 = 0x3120, sel1 = 0x3120;
               if (masked) {
                 const uint32_t k = seen >> (mt * 16 + 2 * t4);
-                z0 = ((k & 1u) ? 0xffffu : 0u) | ((k & 2u) ? 0xffff0000u : 0u);
-                z1 = ((k & 256u) ? 0xffffu : 0u) | ((k & 512u) ? 0xffff0000u : 0u);
+                sel0 = ((k & 1u) ? 0x0100u : 0x0404u) | ((k & 2u) ? 0x3020u : 0x4040u);
+                sel1 = ((k & 256u) ? 0x0100u : 0x0404u) | ((k & 512u) ? 0x3020u : 0x4040u);
               }
 #pragma unroll
               for (int c = 0; c < D / 16; c += 2) {
                 uint32_t r[4], va[4], vc[4];
-                const int row = mt * 16 + ((lane >> 3) & 1) * 8 + (lane & 7), cc = c + (lane >> 4);
-                const int ch = D == 128 ? cc ^ (row & 7) : cc ^ ((row >> 1) & 3);
-                ldsm4_t(vb + row * D + ch * 16, r);
-                r[0] = __byte_perm(r[0] & z0, 0, 0x3120); r[1] = __byte_perm(r[1] & z1, 0, 0x3120);
-                r[2] = __byte_perm(r[2] & z0, 0, 0x3120); r[3] = __byte_perm(r[3] & z1, 0, 0x3120);
-                va[0] = e4m3x2_f16x2(r[0]); va[1] = e4m3x2_f16x2(r[0] >> 16);
-                va[2] = e4m3x2_f16x2(r[1]); va[3] = e4m3x2_f16x2(r[1] >> 16);
-                vc[0] = e4m3x2_f16x2(r[2]); vc[1] = e4m3x2_f16x2(r[2] >> 16);
-                vc[2] = e4m3x2_f16x2(r[3]); vc[3] = e4m3x2_f16x2(r[3] >> 16);
+                ldsm4_t(vb + mt * 16 * D + (v_at ^ (c * 16)), r);
+                e4m3x4_f16(__byte_perm(r[0], 0, sel0), va[0], va[1]);
+                e4m3x4_f16(__byte_perm(r[1], 0, sel1), va[2], va[3]);
+                e4m3x4_f16(__byte_perm(r[2], 0, sel0), vc[0], vc[1]);
+                e4m3x4_f16(__byte_perm(r[3], 0, sel1), vc[2], vc[3]);
 #pragma unroll
                 for (int x = 0; x < NT; ++x) {
                   mma_f16(O[c][x], va, pb[mt][x][0], pb[mt][x][1]);
@@ -624,6 +686,8 @@ __global__ void __launch_bounds__(Shape<D, NT, WN, WK, NS>::THREADS, CTAS)
         if (lane == 0) mbar_arrive(smem_u32(empty + st));
       }
 
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(q_empty + buf));
       // join the key groups: sums in the order of the groups
 #pragma unroll
       for (int x = 0; x < NT; ++x)
@@ -680,9 +744,9 @@ __global__ void __launch_bounds__(Shape<D, NT, WN, WK, NS>::THREADS, CTAS)
         const float4 v = *reinterpret_cast<const float4*>(s_o + col * Sh::O_LD + c + 4);
         o[0] = u.x; o[1] = u.y; o[2] = u.z; o[3] = u.w; o[4] = v.x; o[5] = v.y; o[6] = v.z; o[7] = v.w;
         if (whole) {
-          const int row = r0 + col / p.G;
-          const size_t at = (size_t)row * a.nq + h * p.G + col % p.G;
-          join_prefix(p, at, (size_t)a.R * a.nq, D, c, top, L, o);
+          const int in = (int)(col * p.G_inv >> 16), row = r0 + in;
+          const size_t at = (size_t)row * a.nq + h * p.G + col - in * p.G;
+          fold<D>(p.n_prefix, [&](int k) { return (size_t)k * a.R * a.nq + at; }, p.pp_ml, p.pp_o, c / 8, top, L, o);
           store8(a, at, D, c, seq >= 0 && a.row_seq[row] == seq, L, o);
         } else {
           const size_t q = (size_t)slot * p.qv_pad + col;
@@ -704,46 +768,34 @@ template <int D>
 __global__ void __launch_bounds__(256) kv8_join_k(const Kv8Attn a, const Plan p) {
   PDL_ENTRY();
   const int nkv = a.c.nkv;
-  const long long W = (long long)p.pref[p.groups] * nkv;
-  const int Gd = active_ctas(p, W), c0 = blockIdx.x;
-  if (c0 + 1 >= Gd) return;
-  const long long w0 = range_start(c0, W, Gd), w1 = range_start(c0 + 1, W, Gd);
+  const Share share(p, (uint32_t)p.pref[p.groups] * nkv);
+  const uint32_t c0 = blockIdx.x;
+  if (c0 + 1 >= share.ctas) return;
+  const uint32_t w0 = share.start(c0), w1 = share.start(c0 + 1);
   int lo = 0, hi = p.groups;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if ((long long)p.pref[mid] * nkv <= w1 - 1) lo = mid;
+    if ((uint32_t)p.pref[mid] * nkv < w1) lo = mid;
     else hi = mid;
   }
-  const int nt = p.pref[lo + 1] - p.pref[lo];
-  const int h = (int)((w1 - 1 - (long long)p.pref[lo] * nkv) / nt);
-  const long long ts = (long long)p.pref[lo] * nkv + (long long)h * nt;
+  const uint32_t nt = p.pref[lo + 1] - p.pref[lo], first = (uint32_t)p.pref[lo] * nkv;
+  const int h = (int)((w1 - 1 - first) / nt);
+  const uint32_t ts = first + h * nt;
   if (ts < w0 || ts + nt <= w1) return;   // begun by an earlier CTA, or finished by this one
-  const int c1 = cta_of(ts + nt - 1, W, Gd);
-  const int sidx = (p.g0 + lo) / p.nb, rb = (p.g0 + lo) % p.nb;
+  const uint32_t c1 = share.cta_of(ts + nt - 1);
+  const int sidx = (p.g0 + lo) / p.nb, rb = (p.g0 + lo) - sidx * p.nb;
   const int s0 = sidx * a.rows_per_seq, s1 = min(s0 + a.rows_per_seq, a.R);
   const int r0 = s0 + rb * p.RB, nqv = (min(r0 + p.RB, s1) - r0) * p.G;
   const int col = blockIdx.y * (256 / (D / 8)) + threadIdx.x / (D / 8), c = threadIdx.x % (D / 8) * 8;
   if (col >= nqv) return;
-  int seq = -1;
-  for (int r = s0; r < s1 && seq < 0; ++r) seq = a.row_seq[r];
+  const int seq = first_seq(a, s0, s1);
   // piece 0 in slot 2 c0 + 1 (it holds the item's start), the others in slot 2 c
-  auto at_of = [&](int k) { return (size_t)(k == c0 ? 2 * k + 1 : 2 * k) * p.qv_pad + col; };
+  auto at_of = [&](uint32_t k) { return (size_t)(k == c0 ? 2 * k + 1 : 2 * k) * p.qv_pad + col; };
   float top = -INFINITY, L = 0.f, o[8] = {};
-  for (int k = c0; k <= c1; ++k) top = fmaxf(top, p.part_ml[2 * at_of(k)]);
-  const float base = top == -INFINITY ? 0.f : top;
-#pragma unroll 4
-  for (int k = c0; k <= c1; ++k) {
-    const size_t q = at_of(k);
-    const float f = ex2(p.part_ml[2 * q] - base);
-    L = fmaf(p.part_ml[2 * q + 1], f, L);
-    const float4 u = *reinterpret_cast<const float4*>(p.part_o + q * D + c);
-    const float4 v = *reinterpret_cast<const float4*>(p.part_o + q * D + c + 4);
-    o[0] = fmaf(u.x, f, o[0]); o[1] = fmaf(u.y, f, o[1]); o[2] = fmaf(u.z, f, o[2]); o[3] = fmaf(u.w, f, o[3]);
-    o[4] = fmaf(v.x, f, o[4]); o[5] = fmaf(v.y, f, o[5]); o[6] = fmaf(v.z, f, o[6]); o[7] = fmaf(v.w, f, o[7]);
-  }
-  const int row = r0 + col / p.G;
-  const size_t at = (size_t)row * a.nq + h * p.G + col % p.G;
-  join_prefix(p, at, (size_t)a.R * a.nq, D, c, top, L, o);
+  fold<D>((int)(c1 - c0) + 1, [&](int k) { return at_of(c0 + k); }, p.part_ml, p.part_o, c / 8, top, L, o);
+  const int in = (int)(col * p.G_inv >> 16), row = r0 + in;
+  const size_t at = (size_t)row * a.nq + h * p.G + col - in * p.G;
+  fold<D>(p.n_prefix, [&](int k) { return (size_t)k * a.R * a.nq + at; }, p.pp_ml, p.pp_o, c / 8, top, L, o);
   store8(a, at, D, c, seq >= 0 && seq < a.c.max_batch && a.row_seq[row] == seq, L, o);
 }
 
@@ -780,12 +832,16 @@ size_t al256(size_t x) { return (x + 255) / 256 * 256; }
 
 // Row blocks: a sequence's rows in one block when their query vectors fit, else in equal blocks.
 void cut_rows(const Kv8& c, int nq, int rows_per_seq, Plan& p) {
+  p.nkv = c.nkv;
   p.G = nq / c.nkv;
   const int most = MAX_QV / p.G;
   p.nb = (rows_per_seq + most - 1) / most;
   p.RB = (rows_per_seq + p.nb - 1) / p.nb;
   p.QV = p.RB * p.G;
   p.qv_pad = (p.QV + 7) / 8 * 8;
+  p.G_inv = 65536u / p.G + 1;
+  p.width = 1;
+  while (p.width < 8 && p.width < p.RB) p.width *= 2;
 }
 
 size_t own_scratch(const Kv8& c, const Plan& p) {
@@ -813,12 +869,12 @@ template <int D>
 cudaError_t launch_d(cudaStream_t st, const Kv8Attn& a, Plan& p, const CUtensorMap& mk, const CUtensorMap& mv) {
   const int t = p.qv_pad / 8;
   if (t <= 1) return launch_own<D, 1, 1, 4, 11, 2>(st, a, p, mk, mv);
-  if (t <= 2) return launch_own<D, 2, 1, 4, 10, 2>(st, a, p, mk, mv);
+  if (t <= 2) return launch_own<D, 2, 1, 4, 9, 2>(st, a, p, mk, mv);
   if (t <= 4) return launch_own<D, 4, 1, 8, 20, 1>(st, a, p, mk, mv);
   if (t <= 6) return launch_own<D, 3, 2, 4, 18, 1>(st, a, p, mk, mv);
   if (t <= 8) return launch_own<D, 4, 2, 4, 16, 1>(st, a, p, mk, mv);
-  if (t <= 12) return launch_own<D, 3, 4, 2, 12, 1>(st, a, p, mk, mv);
-  return launch_own<D, 4, 4, 2, 10, 1>(st, a, p, mk, mv);
+  if (t <= 12) return launch_own<D, 3, 4, 2, 11, 1>(st, a, p, mk, mv);
+  return launch_own<D, 4, 4, 2, 7, 1>(st, a, p, mk, mv);
 }
 
 }  // namespace
@@ -855,7 +911,8 @@ int kv8_attention(cudaStream_t st, const Kv8Attn& a) {
   CUtensorMap mk, mv;
   if (!code_map(&mk, a.c.k, rows, a.c.d, box) || !code_map(&mv, a.c.v, rows, a.c.d, box)) return -4;
   const long long blocks = (((long long)a.R + a.rows_per_seq - 1) / a.rows_per_seq) * p.nb;
-  if (blocks > 0x7fffffffll) return -1;
+  // tiles of a launch and their flat numbers stay in 32 bits
+  if (blocks > 0x7fffffffll || (double)std::min<long long>(blocks, MAX_GROUPS) * (a.c.cap / TK + 1) * a.c.nkv > 4e9) return -1;
   for (long long g0 = 0; g0 < blocks; g0 += MAX_GROUPS) {
     p.g0 = (int)g0;
     p.groups = (int)std::min<long long>(MAX_GROUPS, blocks - g0);

@@ -87,7 +87,7 @@ __device__ __forceinline__ float2 sub_mul2(float2 x, float2 neg_m, float2 s) {
 }
 __device__ __forceinline__ bool lane0_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err) {
   int ok = 0;
-  if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity, abort_flag, err) ? 1 : 0;
+  if ((threadIdx.x & 31) == 0) ok = kv8_wait(bar, parity, abort_flag, err) ? 1 : 0;
   ok = __shfl_sync(0xffffffffu, ok, 0);
   __syncwarp();
   return ok != 0;
@@ -246,13 +246,13 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
       for (int i = 0; i < nt; ++i) {
         const int st = i & 1;
         const uint32_t ph = (uint32_t)((i / 2 - 1) & 1);
-        if (i >= 2 && !mbar_wait(smem_u32(k_empty + st), ph, abort_flag, a.err)) break;
+        if (i >= 2 && !kv8_wait(smem_u32(k_empty + st), ph, abort_flag, a.err)) break;
         mbar_expect_tx(smem_u32(k_full + st), Sh::OP);
         for (int x = 0; x < Sh::HALVES; ++x)
           tma_load_3d(smem_u32(sm + Sh::OFF_K + st * Sh::OP + x * Sh::HALF), &tmK, x * 64, (t0 + i) * PT, h,
                       smem_u32(k_full + st));
         ++nk;
-        if (i >= 2 && !mbar_wait(smem_u32(v_empty + st), ph, abort_flag, a.err)) break;
+        if (i >= 2 && !kv8_wait(smem_u32(v_empty + st), ph, abort_flag, a.err)) break;
         mbar_expect_tx(smem_u32(v_full + st), Sh::OP);
         for (int x = 0; x < Sh::HALVES; ++x)
           tma_load_3d(smem_u32(sm + Sh::OFF_V + st * Sh::OP + x * Sh::HALF), &tmV, x * 64, (t0 + i) * PT, h,
@@ -260,14 +260,14 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
         ++nv;
       }
       if (*abort_flag) {   // copies in flight land before the CTA leaves: the last two of each ring
-        mbar_wait(smem_u32(q_full), 0, abort_flag, a.err, false);
-        for (int j = std::max(0, nk - 2); j < nk; ++j) mbar_wait(smem_u32(k_full + (j & 1)), (uint32_t)((j / 2) & 1), abort_flag, a.err, false);
-        for (int j = std::max(0, nv - 2); j < nv; ++j) mbar_wait(smem_u32(v_full + (j & 1)), (uint32_t)((j / 2) & 1), abort_flag, a.err, false);
+        kv8_wait(smem_u32(q_full), 0, abort_flag, a.err, false);
+        for (int j = std::max(0, nk - 2); j < nk; ++j) kv8_wait(smem_u32(k_full + (j & 1)), (uint32_t)((j / 2) & 1), abort_flag, a.err, false);
+        for (int j = std::max(0, nv - 2); j < nv; ++j) kv8_wait(smem_u32(v_full + (j & 1)), (uint32_t)((j / 2) & 1), abort_flag, a.err, false);
       }
     } else if (warp == 9 && lane == 0) {
       // ---- MMA ----
       constexpr uint32_t IS = pf_idesc(PT, false), IO = pf_idesc(D, true);
-      bool ok = mbar_wait(smem_u32(q_full), 0, abort_flag, a.err);
+      bool ok = kv8_wait(smem_u32(q_full), 0, abort_flag, a.err);
       auto issue_s = [&](int mt, int i) {
         const uint32_t q = smem_u32(sm + Sh::OFF_Q + mt * Sh::OP), k = smem_u32(sm + Sh::OFF_K + (i & 1) * Sh::OP);
 #pragma unroll
@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
         tc_commit(smem_u32(s_full + mt));
         if (mt == nmt - 1) tc_commit(smem_u32(k_empty + (i & 1)));
       };
-      if (ok) ok = mbar_wait(smem_u32(k_full), 0, abort_flag, a.err);
+      if (ok) ok = kv8_wait(smem_u32(k_full), 0, abort_flag, a.err);
       if (ok) {
         tc_fence_after();
         for (int mt = 0; mt < nmt; ++mt) issue_s(mt, 0);
@@ -285,8 +285,8 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
       for (int i = 0; ok && i < nt; ++i) {
         for (int mt = 0; ok && mt < nmt; ++mt) {
           // P_i V_i, then S_(i+1) over the same columns: the tensor cores take them in this order
-          ok = mbar_wait(smem_u32(p_full + mt), (uint32_t)(i & 1), abort_flag, a.err) &&
-               (mt || mbar_wait(smem_u32(v_full + (i & 1)), (uint32_t)((i / 2) & 1), abort_flag, a.err));
+          ok = kv8_wait(smem_u32(p_full + mt), (uint32_t)(i & 1), abort_flag, a.err) &&
+               (mt || kv8_wait(smem_u32(v_full + (i & 1)), (uint32_t)((i / 2) & 1), abort_flag, a.err));
           if (!ok) break;
           tc_fence_after();
           const uint32_t v = smem_u32(sm + Sh::OFF_V + (i & 1) * Sh::OP);
@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
           tc_commit(smem_u32(o_done + mt));
           if (mt == nmt - 1) tc_commit(smem_u32(v_empty + (i & 1)));
           if (i + 1 < nt) {
-            if (mt == 0) ok = mbar_wait(smem_u32(k_full + ((i + 1) & 1)), (uint32_t)(((i + 1) / 2) & 1), abort_flag, a.err);
+            if (mt == 0) ok = kv8_wait(smem_u32(k_full + ((i + 1) & 1)), (uint32_t)(((i + 1) / 2) & 1), abort_flag, a.err);
             if (ok) {
               tc_fence_after();
               issue_s(mt, i + 1);
@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
       }
       if (!ok) {   // products in flight end before the CTA frees its TMEM
         tc_commit(smem_u32(drain));
-        mbar_wait(smem_u32(drain), 0, abort_flag, a.err, false);
+        kv8_wait(smem_u32(drain), 0, abort_flag, a.err, false);
       }
     }
   }

@@ -165,11 +165,15 @@ __global__ void __launch_bounds__(KV8_THREADS)
   for (int j = 0; j < CH; ++j) {
     float x[E];
 #pragma unroll
-    for (int i = 0; i < E / 2; ++i) {
-      const uint32_t h = e4m3x2_f16x2(w[j][i / 2] >> (16 * (i & 1)));
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-      x[2 * i] = f.x * s;
-      x[2 * i + 1] = f.y * s;
+    for (int i = 0; i < E / 4; ++i) {
+      uint32_t h[2];
+      e4m3x4_f16(w[j][i], h[0], h[1]);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[k]));
+        x[4 * i + 2 * k] = f.x * s;
+        x[4 * i + 2 * k + 1] = f.y * s;
+      }
     }
     dst[j * VT + t] = pack((const T*)nullptr, x);
   }

@@ -38,11 +38,30 @@ __device__ __forceinline__ float kv8_pow2(int byte) {
   return byte == KV8_BAD ? __int_as_float(0x7fffffff) : __int_as_float(byte << 23);
 }
 
-// Two e4m3 codes (low byte first) as two fp16: exact.
-__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t two) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(r) : "r"(two));
-  return r;
+// Four e4m3 codes (low byte first) as two pairs of fp16: exact.
+__device__ __forceinline__ void e4m3x4_f16(uint32_t four, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(four));
+}
+
+// Bounded wait for an mbarrier phase by whole warps: as mbar_wait, but the abort flag and the clock are looked at
+// every 64th try only.
+__device__ __forceinline__ bool kv8_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err,
+                                         bool honor_abort = true) {
+  uint64_t t0 = 0;
+  for (uint32_t tries = 1;; ++tries) {
+    if (mbar_try(bar, parity)) return true;
+    if (tries & 63u) continue;
+    if (honor_abort && *abort_flag) return false;
+    const uint64_t now = globaltimer();
+    if (!t0) t0 = now;
+    if (now - t0 > EAGLE_WAIT_LIMIT_NS) {
+      *abort_flag = 1;
+      latch_error(err, DEVERR_MBAR_TIMEOUT);
+      return false;
+    }
+  }
 }
 
 struct Kv8Attn {

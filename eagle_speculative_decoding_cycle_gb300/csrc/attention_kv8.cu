@@ -91,6 +91,7 @@ struct Plan {
   int groups;             // row blocks of this launch, from block g0 on
   int g0;
   int grid, min_tiles;    // CTAs at most; tiles a CTA at least
+  int pad;                // what starting and joining an item costs, in tiles: an item of nt tiles spans pad + nt units
   int qv_pad;             // query vectors of a partial
   float* part_o;          // [2 grid][qv_pad][D]
   float* part_ml;         // [2 grid][qv_pad][2]
@@ -99,13 +100,14 @@ struct Plan {
   int n_prefix;
 };
 
-// The tiles W of a launch over its CTAs: the first `more` CTAs take `per` + 1 tiles, the others `per`.
+// The units W of a launch over its CTAs: the first `more` CTAs take `per` + 1, the others `per`. An item's tiles are its
+// last units, so a range that ends inside its first `pad` units has none of it.
 struct Share {
   uint32_t ctas, per, more;
-  __device__ __forceinline__ Share(const Plan& p, uint32_t W) {
+  __device__ __forceinline__ Share(const Plan& p, uint32_t tiles, int pad) {
     // a CTA takes p.min_tiles tiles at least (one for each key group), or a whole average item where those are shorter
-    const uint32_t items = max(1u, (uint32_t)p.groups * (uint32_t)p.nkv);
-    ctas = max(1u, min((uint32_t)p.grid, W / max(1u, min((uint32_t)p.min_tiles, W / items))));
+    const uint32_t items = (uint32_t)p.groups * p.nkv, W = tiles + items * pad;
+    ctas = max(1u, min((uint32_t)p.grid, tiles / max(1u, min((uint32_t)p.min_tiles, tiles / items))));
     per = W / ctas;
     more = W - per * ctas;
   }
@@ -115,6 +117,8 @@ struct Share {
     return u < wide ? u / (per + 1) : more + (u - wide) / per;
   }
 };
+// The pad of a launch: p.pad, but not more than a CTA's even share of the tiles (few long items: ranges would lie in pads).
+__device__ __forceinline__ int pad_of(const Plan& p, uint32_t tiles) { return (int)min((uint32_t)p.pad, tiles / (uint32_t)p.grid); }
 
 // A row block's rows, its sequence (that of the first row that is not padding among the sequence's rows) and the
 // first slot past everything that its rows see.
@@ -133,7 +137,7 @@ __device__ __forceinline__ Group group_of(const Kv8Attn& a, const Plan& p, int g
   const int sidx = (p.g0 + gi) / p.nb, rb = (p.g0 + gi) - sidx * p.nb;
   const int s0 = sidx * a.rows_per_seq, s1 = (int)min((long long)s0 + a.rows_per_seq, (long long)a.R);
   o.r0 = s0 + rb * p.RB;
-  o.r1 = gi < p.groups ? min(o.r0 + p.RB, s1) : o.r0;
+  o.r1 = gi < p.groups ? min(o.r0 + p.RB, s1) : o.r0;   // a block that exists has rows
   o.seq = o.r0 < o.r1 ? first_seq(a, s0, s1) : -1;
   bool bad = o.seq >= a.c.max_batch;
   if (bad) o.seq = -1;
@@ -270,7 +274,7 @@ __global__ void __launch_bounds__(Shape<D, NT, WN, WK, NS>::THREADS, CTAS)
     if (gi < p.groups && (threadIdx.x & (p.width - 1)) == 0) {
       s_lim[gi] = gr.limit;
       s_seq[gi] = gr.seq;
-      s_pref[gi + 1] = gr.r0 < gr.r1 ? max(1, (gr.limit + TK - 1) / TK) : 0;
+      s_pref[gi + 1] = max(1, (gr.limit + TK - 1) / TK);
     }
   }
   __syncthreads();
@@ -291,33 +295,55 @@ __global__ void __launch_bounds__(Shape<D, NT, WN, WK, NS>::THREADS, CTAS)
   __syncthreads();
   if (blockIdx.x == 0)
     for (int i = threadIdx.x; i <= p.groups; i += blockDim.x) p.pref[i] = s_pref[i];
-  const Share share(p, (uint32_t)s_pref[p.groups] * nkv);
+  const uint32_t tiles = (uint32_t)s_pref[p.groups] * nkv;
+  const int pad = pad_of(p, tiles);
+  const Share share(p, tiles, pad);
   if (blockIdx.x >= share.ctas) return;
-  const uint32_t w0 = share.start(blockIdx.x);
-  const int n = (int)(share.start(blockIdx.x + 1) - w0);
+  const uint32_t w0 = share.start(blockIdx.x), w1 = share.start(blockIdx.x + 1);
 
-  // the item (row block, head) that holds flat tile w
-  auto find = [&](uint32_t w, int& gi, int& h, int& t) {
-    int lo = 0, hi = p.groups;   // the last group with pref * nkv <= w
+  // A walk over the items (row block, head) of the range, in order: tiles [t0, t1) of nt.
+  struct Walk {
+    int gi, h, t0, t1, nt;
+    uint32_t base;   // the item's first unit
+  };
+  auto units = [&](int g) { return (uint32_t)(s_pref[g] + g * pad) * nkv; };   // before row block g
+  auto enter = [&](Walk& k, uint32_t from) {   // the item's tiles in the range, from unit `from` of it on
+    k.nt = s_pref[k.gi + 1] - s_pref[k.gi];
+    k.t0 = max(0, (int)from - pad);
+    k.t1 = min(k.nt, (int)(w1 - k.base) - pad);
+  };
+  auto begin = [&](Walk& k) {   // false: no tiles in the whole range
+    int lo = 0, hi = p.groups;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if ((uint32_t)s_pref[mid] * nkv <= w) lo = mid;
+      if (units(mid) <= w0) lo = mid;
       else hi = mid;
     }
-    gi = lo;
-    const uint32_t nt = s_pref[lo + 1] - s_pref[lo], rem = w - (uint32_t)s_pref[lo] * nkv;
-    h = (int)(rem / nt);
-    t = (int)(rem - h * nt);
+    k.gi = lo;
+    const uint32_t first = units(lo), span = s_pref[lo + 1] - s_pref[lo] + pad;
+    k.h = (int)((w0 - first) / span);
+    k.base = first + k.h * span;
+    enter(k, w0 - k.base);
+    return k.t0 < k.t1;
+  };
+  auto next = [&](Walk& k) {    // false: the range ends
+    k.base += k.nt + pad;
+    if (k.base + pad >= w1) return false;
+    if (++k.h == nkv) {
+      k.h = 0;
+      ++k.gi;
+    }
+    enter(k, 0);
+    return true;
   };
 
   // The query vectors of an item as fp16 of q 2^-e, the factor that gives its scores in log2 units, what each sees. By
   // `warps` warps, of which this is number sw.
-  auto prepare = [&](int item, int i, int sw, int warps) -> int {
+  auto prepare = [&](int item, const Walk& k, int sw, int warps) {
     constexpr int LQ = D / 8, PER = 32 / LQ, BATCH = 4;   // lanes a vector, 16 bytes each
     const int sub = lane % LQ;
     const float sl2 = a.scale * 1.4426950408889634f;
-    int gi, h, t0;
-    find(w0 + i, gi, h, t0);
+    const int gi = k.gi, h = k.h;
     const int buf = item & 1, seq = s_seq[gi];
     const int sidx = (p.g0 + gi) / p.nb, rb = (p.g0 + gi) - sidx * p.nb;
     const int r0 = sidx * a.rows_per_seq + rb * p.RB;
@@ -386,7 +412,6 @@ __global__ void __launch_bounds__(Shape<D, NT, WN, WK, NS>::THREADS, CTAS)
     fullvis = __reduce_min_sync(0xffffffffu, fullvis);
     if (lane == 0) s_fullvis[buf * 16 + sw] = fullvis;
     __syncwarp();
-    return min(s_pref[gi + 1] - s_pref[gi] - t0, n - i);   // the item's tiles in this range
   };
   constexpr int FIRST = (NW + Sh::ROWS_W) * 32;   // threads that prepare the first item
 
@@ -395,74 +420,76 @@ __global__ void __launch_bounds__(Shape<D, NT, WN, WK, NS>::THREADS, CTAS)
     if (warp > NW) {
       // row warps: the first item together with the consumers, each later one in the buffer that the consumers are not at
       const int sw = warp - NW - 1;
-      int i = n ? prepare(0, 0, NW + sw, NW + Sh::ROWS_W) : 0;
+      Walk k;
+      bool more = begin(k);
+      if (more) prepare(0, k, NW + sw, NW + Sh::ROWS_W);
       asm volatile("bar.arrive 2, %0;" ::"n"(FIRST) : "memory");
-      for (int item = 1; i < n; ++item) {
-        i += prepare(item, i, sw, Sh::ROWS_W);
+      more = more && next(k);
+      for (int item = 1; more; ++item, more = next(k)) {
+        prepare(item, k, sw, Sh::ROWS_W);
         if (lane == 0) mbar_arrive(smem_u32(q_full + (item & 1)));
       }
       return;
     }
-    // producer: lane j looks up tiles j, j + 32, ... of the range (block-table reads of 32 tiles overlap); lane 0 issues
-    // the codes of all of them (some 100 clocks a TMA copy), lanes 0-3 copy a tile's exponents, 16 bytes each
+    // producer: lane j looks up every 32nd tile of an item (block-table reads of 32 tiles overlap); lane 0 issues
+    // the codes of all of them, lanes 0-3 copy a tile's exponents, 16 bytes each
     const int box = a.c.table ? min(TK, 1 << a.c.block_log2) : TK;
     const uint64_t pol = l2_policy_evict_first();
-    int st = 0;
+    int st = 0, issued = 0;
     uint32_t ph = 1;
-    int last = -1;
     bool ok = true;
-    for (int b = 0; ok && b < n; b += 32) {
-      int halves = 0, vec0 = 0, vec1 = 0;   // the tile's 16-key halves that hold keys, and where they are
-      if (b + lane < n) {
-        int gi, h, t;
-        find(w0 + b + lane, gi, h, t);
-        const int live = s_lim[gi] - t * TK, seq = s_seq[gi];
-        if (live > 0) {
-          const long long v = kv8_vec(a.c, seq, h, t * TK);
+    Walk k;
+    for (bool more = begin(k); more && ok; more = next(k)) {
+      const int limit = s_lim[k.gi], seq = s_seq[k.gi];
+      for (int b = k.t0; ok && b < k.t1; b += 32) {
+        int halves = 0, vec0 = 0, vec1 = 0;   // the tile's 16-key halves that hold keys, and where they are
+        const int t = b + lane, live = limit - t * TK;
+        if (t < k.t1 && live > 0) {
+          const long long v = kv8_vec(a.c, seq, k.h, t * TK);
           long long u = v + 16;
           halves = 1;
           if (box == TK ? (a.c.table || t * TK + 16 < a.c.cap) : live > 16) halves = 2;
-          if (box < TK && halves == 2) u = kv8_vec(a.c, seq, h, t * TK + 16);
+          if (box < TK && halves == 2) u = kv8_vec(a.c, seq, k.h, t * TK + 16);
           if (v < 0 || (halves == 2 && u < 0)) latch_error(a.err, DEVERR_BOUNDS);   // not assigned: unspecified keys
           vec0 = (int)max(v, 0ll);
           vec1 = (int)max(u, 0ll);
         }
-      }
-      const int m = min(32, n - b);
-      for (int j = 0; j < m; ++j) {
-        const int nh = __shfl_sync(0xffffffffu, halves, j);
-        const int v0 = __shfl_sync(0xffffffffu, vec0, j), v1 = __shfl_sync(0xffffffffu, vec1, j);
-        if (b + j >= NS && !kv8_wait(smem_u32(empty + st), ph, abort_flag, a.err)) ok = false;
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        const uint32_t bar = smem_u32(full + st);
-        last = b + j;
-        if (lane < 2 * nh)
-          copy16(smem_u32(sm + Sh::OFF_EXP + st * 2 * TK) + (lane & 1) * TK + (lane >> 1) * 16,
-                 ((lane & 1) ? a.c.ve : a.c.ke) + (lane < 2 ? v0 : v1));
-        copies_arrive(bar);
-        if (lane == 0) {
-          const int boxes = box == TK ? min(nh, 1) : nh;
-          const uint32_t k = smem_u32(sm + st * Sh::TILE);
-          mbar_expect_tx(bar, (uint32_t)(boxes * 2 * box * D));
-          if (boxes) {
-            tma_load_2d(k, &tmK, 0, v0, bar, pol);
-            tma_load_2d(k + TK * D, &tmV, 0, v0, bar, pol);
+        const int m = min(32, k.t1 - b);
+        for (int j = 0; j < m; ++j) {
+          const int nh = __shfl_sync(0xffffffffu, halves, j);
+          const int v0 = __shfl_sync(0xffffffffu, vec0, j), v1 = __shfl_sync(0xffffffffu, vec1, j);
+          if (issued >= NS && !kv8_wait(smem_u32(empty + st), ph, abort_flag, a.err)) ok = false;
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          const uint32_t bar = smem_u32(full + st);
+          ++issued;
+          if (lane < 2 * nh)
+            copy16(smem_u32(sm + Sh::OFF_EXP + st * 2 * TK) + (lane & 1) * TK + (lane >> 1) * 16,
+                   ((lane & 1) ? a.c.ve : a.c.ke) + (lane < 2 ? v0 : v1));
+          copies_arrive(bar);
+          if (lane == 0) {
+            const int boxes = box == TK ? min(nh, 1) : nh;
+            const uint32_t kd = smem_u32(sm + st * Sh::TILE);
+            mbar_expect_tx(bar, (uint32_t)(boxes * 2 * box * D));
+            if (boxes) {
+              tma_load_2d(kd, &tmK, 0, v0, bar, pol);
+              tma_load_2d(kd + TK * D, &tmV, 0, v0, bar, pol);
+            }
+            if (boxes > 1) {
+              tma_load_2d(kd + 16 * D, &tmK, 0, v1, bar, pol);
+              tma_load_2d(kd + TK * D + 16 * D, &tmV, 0, v1, bar, pol);
+            }
           }
-          if (boxes > 1) {
-            tma_load_2d(k + 16 * D, &tmK, 0, v1, bar, pol);
-            tma_load_2d(k + TK * D + 16 * D, &tmV, 0, v1, bar, pol);
+          if (++st == NS) {
+            st = 0;
+            ph ^= 1;
           }
-        }
-        if (++st == NS) {
-          st = 0;
-          ph ^= 1;
         }
       }
     }
     // after a timeout the tiles in flight land before the CTA leaves: the last NS that were issued
     if (!ok)
-      for (int x = max(0, last - NS + 1); x <= last; ++x)
+      for (int x = max(0, issued - NS); x < issued; ++x)
         kv8_wait(smem_u32(full + x % NS), (uint32_t)((x / NS) & 1), abort_flag, a.err, false);
   } else {
     if constexpr (Sh::SPLIT_REGS) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
@@ -471,17 +498,16 @@ __global__ void __launch_bounds__(Shape<D, NT, WN, WK, NS>::THREADS, CTAS)
     float* s_m = reinterpret_cast<float*>(sm + Sh::OFF_MLE);
     float* s_l = s_m + WK * Sh::QV;
     float* s_o = reinterpret_cast<float*>(sm + Sh::OFF_O);
-    if (n) prepare(0, 0, warp, NW + Sh::ROWS_W);
+    Walk k;
+    bool more = begin(k);
+    if (more) prepare(0, k, warp, NW + Sh::ROWS_W);
     asm volatile("bar.sync 2, %0;" ::"n"(FIRST) : "memory");
     // this lane's row of the ldmatrix tiles, with its swizzle, 16-byte column 0: column c is at ^ (16 c)
     auto swizzled = [&](int row, int col) { return row * D + (D == 128 ? col ^ (row & 7) : col ^ ((row >> 1) & 3)) * 16; };
     const uint32_t k_at = swizzled(lane, 0), v_at = swizzled(lane & 15, lane >> 4);
     int i = 0;   // tiles of the range that are behind
-    for (int item = 0; i < n; ++item) {
-      int gi, h, t0;
-      find(w0 + i, gi, h, t0);
-      const int nt = s_pref[gi + 1] - s_pref[gi];
-      const int t1 = min(nt, t0 + n - i);
+    for (int item = 0; more; ++item, more = next(k)) {
+      const int gi = k.gi, h = k.h, t0 = k.t0, t1 = k.t1, nt = k.nt;
       const int seq = s_seq[gi], limit = s_lim[gi];
       const int sidx = (p.g0 + gi) / p.nb, rb = (p.g0 + gi) - sidx * p.nb;
       const int r0 = sidx * a.rows_per_seq + rb * p.RB;
@@ -768,21 +794,24 @@ template <int D>
 __global__ void __launch_bounds__(256) kv8_join_k(const Kv8Attn a, const Plan p) {
   PDL_ENTRY();
   const int nkv = a.c.nkv;
-  const Share share(p, (uint32_t)p.pref[p.groups] * nkv);
+  const uint32_t tiles = (uint32_t)p.pref[p.groups] * nkv;
+  const int pad = pad_of(p, tiles);
+  const Share share(p, tiles, pad);
   const uint32_t c0 = blockIdx.x;
   if (c0 + 1 >= share.ctas) return;
   const uint32_t w0 = share.start(c0), w1 = share.start(c0 + 1);
+  auto units = [&](int g) { return (uint32_t)(p.pref[g] + g * pad) * nkv; };
   int lo = 0, hi = p.groups;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if ((uint32_t)p.pref[mid] * nkv < w1) lo = mid;
+    if (units(mid) < w1) lo = mid;
     else hi = mid;
   }
-  const uint32_t nt = p.pref[lo + 1] - p.pref[lo], first = (uint32_t)p.pref[lo] * nkv;
-  const int h = (int)((w1 - 1 - first) / nt);
-  const uint32_t ts = first + h * nt;
-  if (ts < w0 || ts + nt <= w1) return;   // begun by an earlier CTA, or finished by this one
-  const uint32_t c1 = share.cta_of(ts + nt - 1);
+  const uint32_t span = p.pref[lo + 1] - p.pref[lo] + pad, first = units(lo);
+  const int h = (int)((w1 - 1 - first) / span);
+  const uint32_t ts = first + h * span + pad, te = first + (h + 1) * span;   // the item's tiles
+  if (ts < w0 || ts >= w1 || te <= w1) return;   // begun by another CTA, or finished by this one
+  const uint32_t c1 = share.cta_of(te - 1);
   const int sidx = (p.g0 + lo) / p.nb, rb = (p.g0 + lo) - sidx * p.nb;
   const int s0 = sidx * a.rows_per_seq, s1 = min(s0 + a.rows_per_seq, a.R);
   const int r0 = s0 + rb * p.RB, nqv = (min(r0 + p.RB, s1) - r0) * p.G;
@@ -855,6 +884,7 @@ cudaError_t launch_own(cudaStream_t st, const Kv8Attn& a, Plan& p, const CUtenso
   const auto fn = kv8_attn_k<D, NT, WN, WK, NS, CTAS>;
   p.grid = std::min(MAX_CTAS, CTAS * device_sm_count());
   p.min_tiles = WK;
+  p.pad = 6 + p.n_prefix / 2;
   const int smem = Sh::bytes(p.groups);
   cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(fn), smem);
   if (e != cudaSuccess) return e;
@@ -910,9 +940,11 @@ int kv8_attention(cudaStream_t st, const Kv8Attn& a) {
   const int box = a.c.table ? std::min(TK, 1 << a.c.block_log2) : TK;
   CUtensorMap mk, mv;
   if (!code_map(&mk, a.c.k, rows, a.c.d, box) || !code_map(&mv, a.c.v, rows, a.c.d, box)) return -4;
-  const long long blocks = (((long long)a.R + a.rows_per_seq - 1) / a.rows_per_seq) * p.nb;
+  // row blocks that hold rows: the last sequence may have fewer
+  const long long seqs = ((long long)a.R + a.rows_per_seq - 1) / a.rows_per_seq;
+  const long long blocks = (seqs - 1) * p.nb + (a.R - (seqs - 1) * a.rows_per_seq + p.RB - 1) / p.RB;
   // tiles of a launch and their flat numbers stay in 32 bits
-  if (blocks > 0x7fffffffll || (double)std::min<long long>(blocks, MAX_GROUPS) * (a.c.cap / TK + 1) * a.c.nkv > 4e9) return -1;
+  if (blocks > 0x7fffffffll || (double)std::min<long long>(blocks, MAX_GROUPS) * (a.c.cap / TK + 32) * a.c.nkv > 2e9) return -1;
   for (long long g0 = 0; g0 < blocks; g0 += MAX_GROUPS) {
     p.g0 = (int)g0;
     p.groups = (int)std::min<long long>(MAX_GROUPS, blocks - g0);

@@ -91,11 +91,12 @@ struct Plan {
   int groups;             // row blocks of this launch, from block g0 on
   int g0;
   int grid, min_tiles;    // CTAs at most; tiles a CTA at least
+  int join_cols;          // query vectors a join CTA takes (a power of two up to 256 / (d / 8))
   int pad;                // what starting and joining an item costs, in tiles: an item of nt tiles spans pad + nt units
   int qv_pad;             // query vectors of a partial
   float* part_o;          // [2 grid][qv_pad][D]
   float* part_ml;         // [2 grid][qv_pad][2]
-  int* pref;              // [groups + 1] tiles a head before each row block (written by CTA 0)
+  int4* cut;              // [grid] the item that CTA c begins and does not finish: row block, head, last CTA (-1: none)
   const float *pp_o, *pp_ml;   // prefix partials [n_prefix][R * nq][D], [..][2]
   int n_prefix;
 };
@@ -293,11 +294,10 @@ __global__ void __launch_bounds__(Shape<D, NT, WN, WK, NS>::THREADS, CTAS)
     if (lane == 0) s_pref[0] = 0;
   }
   __syncthreads();
-  if (blockIdx.x == 0)
-    for (int i = threadIdx.x; i <= p.groups; i += blockDim.x) p.pref[i] = s_pref[i];
   const uint32_t tiles = (uint32_t)s_pref[p.groups] * nkv;
   const int pad = pad_of(p, tiles);
   const Share share(p, tiles, pad);
+  if (threadIdx.x == 0) p.cut[blockIdx.x] = make_int4(0, 0, -1, 0);
   if (blockIdx.x >= share.ctas) return;
   const uint32_t w0 = share.start(blockIdx.x), w1 = share.start(blockIdx.x + 1);
 
@@ -756,6 +756,8 @@ __global__ void __launch_bounds__(Shape<D, NT, WN, WK, NS>::THREADS, CTAS)
         named_bar_sync(1, NC);
       }
       const bool whole = t0 == 0 && t1 == nt;
+      if (threadIdx.x == 0 && t0 == 0 && t1 < nt)
+        p.cut[blockIdx.x] = make_int4(gi, h, (int)share.cta_of(k.base + pad + nt - 1), 0);
       const int slot = 2 * blockIdx.x + (t0 == 0 ? 1 : 0);
       for (int x = threadIdx.x; x < nqv * (D / 8); x += NC) {
         const int col = x / (D / 8), c = x % (D / 8) * 8;
@@ -788,40 +790,49 @@ __global__ void __launch_bounds__(Shape<D, NT, WN, WK, NS>::THREADS, CTAS)
   }
 }
 
-// Joins the pieces of the items that range ends cut: CTA (c, y) takes the item that CTA c's range begins and does
-// not finish, its query vectors from 32 y on; D / 8 threads a query vector, the pieces in order.
+// Joins the pieces of the items that range ends cut: CTA (c, y) takes the item that CTA c began and did not finish, p.join_cols of its
+// query vectors. D / 8 lanes a query vector; where few query vectors leave threads over, they share an item's pieces (every
+// `ways`-th each) and are joined through shared memory, in the order of the threads.
 template <int D>
 __global__ void __launch_bounds__(256) kv8_join_k(const Kv8Attn a, const Plan p) {
   PDL_ENTRY();
-  const int nkv = a.c.nkv;
-  const uint32_t tiles = (uint32_t)p.pref[p.groups] * nkv;
-  const int pad = pad_of(p, tiles);
-  const Share share(p, tiles, pad);
-  const uint32_t c0 = blockIdx.x;
-  if (c0 + 1 >= share.ctas) return;
-  const uint32_t w0 = share.start(c0), w1 = share.start(c0 + 1);
-  auto units = [&](int g) { return (uint32_t)(p.pref[g] + g * pad) * nkv; };
-  int lo = 0, hi = p.groups;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (units(mid) < w1) lo = mid;
-    else hi = mid;
-  }
-  const uint32_t span = p.pref[lo + 1] - p.pref[lo] + pad, first = units(lo);
-  const int h = (int)((w1 - 1 - first) / span);
-  const uint32_t ts = first + h * span + pad, te = first + (h + 1) * span;   // the item's tiles
-  if (ts < w0 || ts >= w1 || te <= w1) return;   // begun by another CTA, or finished by this one
-  const uint32_t c1 = share.cta_of(te - 1);
+  const int c0 = blockIdx.x;
+  const int4 cut = p.cut[c0];
+  if (cut.z < 0) return;
+  const int lo = cut.x, h = cut.y, c1 = cut.z;
   const int sidx = (p.g0 + lo) / p.nb, rb = (p.g0 + lo) - sidx * p.nb;
   const int s0 = sidx * a.rows_per_seq, s1 = min(s0 + a.rows_per_seq, a.R);
   const int r0 = s0 + rb * p.RB, nqv = (min(r0 + p.RB, s1) - r0) * p.G;
-  const int col = blockIdx.y * (256 / (D / 8)) + threadIdx.x / (D / 8), c = threadIdx.x % (D / 8) * 8;
+  constexpr int GL = D / 8;
+  __shared__ float s_part[256 / GL][D + 4];
+  __shared__ float2 s_ml[256 / GL];
+  const int team = threadIdx.x / GL, ways = 256 / GL / p.join_cols, way = team / p.join_cols;
+  const int col = blockIdx.y * p.join_cols + team % p.join_cols, c = threadIdx.x % GL * 8;
+  // piece 0 in slot 2 c0 + 1 (it holds the item's start), the others in slot 2 c
+  auto at_of = [&](int k) { return (size_t)(k ? 2 * (c0 + k) : 2 * c0 + 1) * p.qv_pad + min(col, nqv - 1); };
+  const int pieces = c1 - c0 + 1;
+  float top = -INFINITY, L = 0.f, o[8] = {};
+  fold<D>((pieces - way + ways - 1) / ways, [&](int k) { return at_of(k * ways + way); }, p.part_ml, p.part_o, c / 8, top, L, o);
+  if (ways > 1) {
+    if (way) {
+      *reinterpret_cast<float4*>(&s_part[team][c]) = make_float4(o[0], o[1], o[2], o[3]);
+      *reinterpret_cast<float4*>(&s_part[team][c + 4]) = make_float4(o[4], o[5], o[6], o[7]);
+      if (c == 0) s_ml[team] = make_float2(top, L);
+    }
+    __syncthreads();
+    if (way) return;
+    for (int w = 1; w < ways; ++w) {
+      const int from = team + w * p.join_cols;
+      const float2 ml = s_ml[from];
+      const float mx = fmaxf(top, ml.x), base = mx == -INFINITY ? 0.f : mx, f = ex2(top - base), g = ex2(ml.x - base);
+      top = mx;
+      L = L * f + ml.y * g;
+#pragma unroll
+      for (int x = 0; x < 8; ++x) o[x] = o[x] * f + s_part[from][c + x] * g;
+    }
+  }
   if (col >= nqv) return;
   const int seq = first_seq(a, s0, s1);
-  // piece 0 in slot 2 c0 + 1 (it holds the item's start), the others in slot 2 c
-  auto at_of = [&](uint32_t k) { return (size_t)(k == c0 ? 2 * k + 1 : 2 * k) * p.qv_pad + col; };
-  float top = -INFINITY, L = 0.f, o[8] = {};
-  fold<D>((int)(c1 - c0) + 1, [&](int k) { return at_of(c0 + k); }, p.part_ml, p.part_o, c / 8, top, L, o);
   const int in = (int)(col * p.G_inv >> 16), row = r0 + in;
   const size_t at = (size_t)row * a.nq + h * p.G + col - in * p.G;
   fold<D>(p.n_prefix, [&](int k) { return (size_t)k * a.R * a.nq + at; }, p.pp_ml, p.pp_o, c / 8, top, L, o);
@@ -875,7 +886,7 @@ void cut_rows(const Kv8& c, int nq, int rows_per_seq, Plan& p) {
 
 size_t own_scratch(const Kv8& c, const Plan& p) {
   return al256((size_t)2 * MAX_CTAS * p.qv_pad * c.d * sizeof(float)) +
-         al256((size_t)2 * MAX_CTAS * p.qv_pad * 2 * sizeof(float)) + al256((MAX_GROUPS + 1) * sizeof(int));
+         al256((size_t)2 * MAX_CTAS * p.qv_pad * 2 * sizeof(float)) + al256(MAX_CTAS * sizeof(int4));
 }
 
 template <int D, int NT, int WN, int WK, int NS, int CTAS>
@@ -890,7 +901,9 @@ cudaError_t launch_own(cudaStream_t st, const Kv8Attn& a, Plan& p, const CUtenso
   if (e != cudaSuccess) return e;
   e = launch_k(fn, dim3(p.grid), dim3(Sh::THREADS), smem, st, mk, mv, a, p);
   if (e != cudaSuccess) return e;
-  return launch_k(kv8_join_k<D>, dim3(p.grid, (p.QV + 256 / (D / 8) - 1) / (256 / (D / 8))), dim3(256), 0, st, a, p);
+  p.join_cols = 1;
+  while (p.join_cols < 256 / (D / 8) && p.join_cols * 4 < p.QV) p.join_cols *= 2;
+  return launch_k(kv8_join_k<D>, dim3(p.grid, (p.QV + p.join_cols - 1) / p.join_cols), dim3(256), 0, st, a, p);
 }
 
 // The narrowest configuration that holds a block's query vectors: up to 16 in two small CTAs an SM (one's joins
@@ -924,11 +937,11 @@ int kv8_attention(cudaStream_t st, const Kv8Attn& a) {
   s += al256((size_t)2 * MAX_CTAS * p.qv_pad * a.c.d * sizeof(float));
   p.part_ml = (float*)s;
   s += al256((size_t)2 * MAX_CTAS * p.qv_pad * 2 * sizeof(float));
-  p.pref = (int*)s;
+  p.cut = (int4*)s;
   if (a.P) {
     p.n_prefix = kv8_prefix_splits(a.c.nkv, a.R, a.nq, a.P);
     const size_t qv = (size_t)a.R * a.nq * p.n_prefix;
-    float* o = (float*)(s + al256((MAX_GROUPS + 1) * sizeof(int)));
+    float* o = (float*)(s + al256(MAX_CTAS * sizeof(int4)));
     float* ml = (float*)((uint8_t*)o + al256(qv * a.c.d * sizeof(float)));
     p.pp_o = o;
     p.pp_ml = ml;

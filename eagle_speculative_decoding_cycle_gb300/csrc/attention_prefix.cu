@@ -75,15 +75,49 @@ __device__ __forceinline__ float pf_ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-// (x - m) * s of two values. The difference comes first: it is exact where it matters, near the maximum, whatever
-// the size of the scores.
-__device__ __forceinline__ float2 sub_mul2(float2 x, float2 neg_m, float2 s) {
-  float2 r;
-  asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
-      "add.rn.f32x2 a, a, b;\n\tmul.rn.f32x2 a, a, c;\n\tmov.b64 {%0, %1}, a;\n\t}"
-      : "=f"(r.x), "=f"(r.y)
-      : "f"(x.x), "f"(x.y), "f"(neg_m.x), "f"(neg_m.y), "f"(s.x), "f"(s.y));
+// Pairs of fp32 in 64-bit registers (add.f32x2 and mul.f32x2 take one issue slot for two).
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 two(float a, float b) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
   return r;
+}
+__device__ __forceinline__ float2 one_by_one(f32x2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// 32 columns of this warp's lanes; the values are there after tmem_wait_ld.
+__device__ __forceinline__ void tmem_ld32_async(uint32_t t, float* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
+        "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
+        "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+      : "r"(t));
+}
+// Waits for this thread's TMEM loads; the values pass through, so that nothing of them is used before.
+__device__ __forceinline__ void tmem_wait_ld(float* v) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) asm volatile("" : "+f"(v[i]));
 }
 __device__ __forceinline__ bool lane0_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err) {
   int ok = 0;
@@ -110,8 +144,8 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(pf_smem) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + Sh::OFF_BAR);
   uint64_t *q_full = bars, *k_full = bars + 1, *k_empty = bars + 3, *v_full = bars + 5, *v_empty = bars + 7,
-           *s_full = bars + 9, *p_full = bars + 11, *o_done = bars + 13, *drain = bars + 15;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 16);
+           *s_full = bars + 9, *p_full = bars + 11 /* [tile][half] */, *o_done = bars + 15, *drain = bars + 17;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 18);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int split = blockIdx.x % a.splits, pair = blockIdx.x / a.splits % a.pairs, h = blockIdx.x / (a.splits * a.pairs);
@@ -127,7 +161,8 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
       mbar_init(smem_u32(v_full + i), 1);
       mbar_init(smem_u32(v_empty + i), 1);
       mbar_init(smem_u32(s_full + i), 1);
-      mbar_init(smem_u32(p_full + i), PT);
+      mbar_init(smem_u32(p_full + 2 * i), PT);
+      mbar_init(smem_u32(p_full + 2 * i + 1), PT);
       mbar_init(smem_u32(o_done + i), 1);
     }
     mbar_init(smem_u32(drain), 1);
@@ -154,20 +189,22 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
       tc_fence_after();
       float s[PT];
 #pragma unroll
-      for (int c = 0; c < PT; c += 32) tmem_ld32(tS + c, s + c);
+      for (int c = 0; c < PT; c += 32) tmem_ld32_async(tS + c, s + c);
+#pragma unroll
+      for (int c = 0; c < PT; c += 32) tmem_wait_ld(s + c);
       const int last = a.P - (t0 + i) * PT;    // keys of this tile, 128 but for the prefix's end
       if (last < PT)
 #pragma unroll
         for (int c = 0; c < PT; ++c) s[c] = c < last ? s[c] : -INFINITY;
       float x0 = s[0], x1 = s[1], x2 = s[2], x3 = s[3];
 #pragma unroll
-      for (int c = 4; c < PT; c += 4) {
-        x0 = fmaxf(x0, s[c]);
-        x1 = fmaxf(x1, s[c + 1]);
-        x2 = fmaxf(x2, s[c + 2]);
-        x3 = fmaxf(x3, s[c + 3]);
+      for (int c = 4; c + 7 < PT; c += 8) {
+        x0 = max3(x0, s[c], s[c + 1]);
+        x1 = max3(x1, s[c + 2], s[c + 3]);
+        x2 = max3(x2, s[c + 4], s[c + 5]);
+        x3 = max3(x3, s[c + 6], s[c + 7]);
       }
-      const float mx = fmaxf(fmaxf(x0, x1), fmaxf(x2, x3));
+      const float mx = fmaxf(max3(x0, x1, fmaxf(s[PT - 4], s[PT - 3])), max3(x2, x3, fmaxf(s[PT - 2], s[PT - 1])));
       const bool raise = (mx - m) * a.sl2 > PF_LAZY;
       float corr = 1.f;
       if (raise) {
@@ -189,27 +226,28 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
           tmem_st16(tO + c, o);
         }
       }
-      const float2 nm = make_float2(-m, -m), s2 = make_float2(a.sl2, a.sl2);
-      float sum0 = 0.f, sum1 = 0.f;
+      // the difference comes first: it is exact where it matters, near the maximum, whatever the size of the scores
+      const f32x2 nm = two(-m, -m), s2 = two(a.sl2, a.sl2);
+      f32x2 sum[2] = {two(0.f, 0.f), two(0.f, 0.f)};
 #pragma unroll
-      for (int c0 = 0; c0 < PT; c0 += 64) {
+      for (int hf = 0; hf < 2; ++hf) {
         uint32_t w[32];
 #pragma unroll
         for (int c = 0; c < 64; c += 2) {
-          float2 x = sub_mul2(make_float2(s[c0 + c], s[c0 + c + 1]), nm, s2);
+          float2 x = one_by_one(mul2(add2(two(s[hf * 64 + c], s[hf * 64 + c + 1]), nm), s2));
           x.x = pf_ex2(x.x);
           x.y = pf_ex2(x.y);
-          sum0 += x.x;
-          sum1 += x.y;
+          sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], two(x.x, x.y));
           const __nv_bfloat162 b = __floats2bfloat162_rn(x.x, x.y);
           w[c / 2] = *reinterpret_cast<const uint32_t*>(&b);
         }
-        tmem_st32u(tS + c0 / 2, w);
+        tmem_st32u(tS + hf * 32, w);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(smem_u32(p_full + 2 * mt + hf));   // the first half's product starts under the second half
       }
-      l += sum0 + sum1;
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(smem_u32(p_full + mt));
+      const float2 sums = one_by_one(add2(sum[0], sum[1]));
+      l += sums.x + sums.y;
     }
     if (mt < nmt) {
       const int row = r0 + mt * a.RB + qv / a.G;
@@ -285,14 +323,18 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
       for (int i = 0; ok && i < nt; ++i) {
         for (int mt = 0; ok && mt < nmt; ++mt) {
           // P_i V_i, then S_(i+1) over the same columns: the tensor cores take them in this order
-          ok = kv8_wait(smem_u32(p_full + mt), (uint32_t)(i & 1), abort_flag, a.err) &&
-               (mt || kv8_wait(smem_u32(v_full + (i & 1)), (uint32_t)((i / 2) & 1), abort_flag, a.err));
-          if (!ok) break;
-          tc_fence_after();
+          ok = mt || kv8_wait(smem_u32(v_full + (i & 1)), (uint32_t)((i / 2) & 1), abort_flag, a.err);
           const uint32_t v = smem_u32(sm + Sh::OFF_V + (i & 1) * Sh::OP);
 #pragma unroll
-          for (int x = 0; x < PT / 16; ++x)
-            mma_ts(tmem + 2 * PT + mt * D, tmem + mt * PT + x * 8, pf_desc_mn(v + x * 2048, Sh::HALF), IO, (i || x) ? 1u : 0u);
+          for (int hf = 0; hf < 2; ++hf) {
+            ok = ok && kv8_wait(smem_u32(p_full + 2 * mt + hf), (uint32_t)(i & 1), abort_flag, a.err);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int x = hf * PT / 32; x < (hf + 1) * PT / 32; ++x)
+              mma_ts(tmem + 2 * PT + mt * D, tmem + mt * PT + x * 8, pf_desc_mn(v + x * 2048, Sh::HALF), IO, (i || x) ? 1u : 0u);
+          }
+          if (!ok) break;
           tc_commit(smem_u32(o_done + mt));
           if (mt == nmt - 1) tc_commit(smem_u32(v_empty + (i & 1)));
           if (i + 1 < nt) {

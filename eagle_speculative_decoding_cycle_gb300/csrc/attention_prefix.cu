@@ -60,14 +60,11 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* map, int c
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
       : "memory");
 }
-__device__ __forceinline__ void tmem_st32u(uint32_t t, const uint32_t* v) {
+__device__ __forceinline__ void tmem_st16u(uint32_t t, const uint32_t* v) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(t),
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(t),
       "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]),
-      "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]),
-      "r"(v[30]), "r"(v[31])
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
 }
 __device__ __forceinline__ float pf_ex2(float x) {
@@ -119,6 +116,14 @@ __device__ __forceinline__ void tmem_wait_ld(float* v) {
 #pragma unroll
   for (int i = 0; i < 32; ++i) asm volatile("" : "+f"(v[i]));
 }
+// One lane of a converged warp. The loops of the issuing warps run in all lanes and only the copies and products
+// themselves under this lane: their operands then stay in uniform registers (issued by `lane == 0` of a divergent loop, each
+// product took some 100 clocks to issue against 64 to run).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
 __device__ __forceinline__ bool lane0_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err) {
   int ok = 0;
   if ((threadIdx.x & 31) == 0) ok = kv8_wait(bar, parity, abort_flag, err) ? 1 : 0;
@@ -147,7 +152,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
            *s_full = bars + 9, *p_full = bars + 11 /* [tile][half] */, *o_done = bars + 15, *drain = bars + 17;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 18);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5;
   const int split = blockIdx.x % a.splits, pair = blockIdx.x / a.splits % a.pairs, h = blockIdx.x / (a.splits * a.pairs);
   const int r0 = pair * 2 * a.RB;
   const int nmt = r0 + a.RB < a.R ? 2 : 1;     // query tiles of this CTA
@@ -230,21 +235,23 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
       const f32x2 nm = two(-m, -m), s2 = two(a.sl2, a.sl2);
       f32x2 sum[2] = {two(0.f, 0.f), two(0.f, 0.f)};
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        uint32_t w[32];
+      for (int qt = 0; qt < 4; ++qt) {
+        uint32_t w[16];
 #pragma unroll
-        for (int c = 0; c < 64; c += 2) {
-          float2 x = one_by_one(mul2(add2(two(s[hf * 64 + c], s[hf * 64 + c + 1]), nm), s2));
+        for (int c = 0; c < 32; c += 2) {
+          float2 x = one_by_one(mul2(add2(two(s[qt * 32 + c], s[qt * 32 + c + 1]), nm), s2));
           x.x = pf_ex2(x.x);
           x.y = pf_ex2(x.y);
           sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], two(x.x, x.y));
           const __nv_bfloat162 b = __floats2bfloat162_rn(x.x, x.y);
           w[c / 2] = *reinterpret_cast<const uint32_t*>(&b);
         }
-        tmem_st32u(tS + hf * 32, w);
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(smem_u32(p_full + 2 * mt + hf));   // the first half's product starts under the second half
+        tmem_st16u(tS + qt * 16, w);
+        if (qt & 1) {
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(smem_u32(p_full + 2 * mt + qt / 2));   // the first half's product starts under the second half
+        }
       }
       const float2 sums = one_by_one(add2(sum[0], sum[1]));
       l += sums.x + sums.y;
@@ -272,48 +279,60 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-    if (warp == 8 && lane == 0) {
+    if (warp == 8) {
       // ---- TMA ----
       const int qbytes = a.RB * a.G * 128;
-      mbar_expect_tx(smem_u32(q_full), (uint32_t)(nmt * Sh::HALVES * qbytes));
-      for (int mt = 0; mt < nmt; ++mt)
-        for (int x = 0; x < Sh::HALVES; ++x)
-          tma_load_3d(smem_u32(sm + Sh::OFF_Q + mt * Sh::OP + x * Sh::HALF), &tmQ, x * 64, h * a.G, r0 + mt * a.RB,
-                      smem_u32(q_full));
+      if (elect_one()) {
+        mbar_expect_tx(smem_u32(q_full), (uint32_t)(nmt * Sh::HALVES * qbytes));
+        for (int mt = 0; mt < nmt; ++mt)
+          for (int x = 0; x < Sh::HALVES; ++x)
+            tma_load_3d(smem_u32(sm + Sh::OFF_Q + mt * Sh::OP + x * Sh::HALF), &tmQ, x * 64, h * a.G, r0 + mt * a.RB,
+                        smem_u32(q_full));
+      }
       int nk = 0, nv = 0;
       for (int i = 0; i < nt; ++i) {
         const int st = i & 1;
         const uint32_t ph = (uint32_t)((i / 2 - 1) & 1);
         if (i >= 2 && !kv8_wait(smem_u32(k_empty + st), ph, abort_flag, a.err)) break;
-        mbar_expect_tx(smem_u32(k_full + st), Sh::OP);
-        for (int x = 0; x < Sh::HALVES; ++x)
-          tma_load_3d(smem_u32(sm + Sh::OFF_K + st * Sh::OP + x * Sh::HALF), &tmK, x * 64, (t0 + i) * PT, h,
-                      smem_u32(k_full + st));
+        if (elect_one()) {
+          mbar_expect_tx(smem_u32(k_full + st), Sh::OP);
+          for (int x = 0; x < Sh::HALVES; ++x)
+            tma_load_3d(smem_u32(sm + Sh::OFF_K + st * Sh::OP + x * Sh::HALF), &tmK, x * 64, (t0 + i) * PT, h,
+                        smem_u32(k_full + st));
+        }
         ++nk;
         if (i >= 2 && !kv8_wait(smem_u32(v_empty + st), ph, abort_flag, a.err)) break;
-        mbar_expect_tx(smem_u32(v_full + st), Sh::OP);
-        for (int x = 0; x < Sh::HALVES; ++x)
-          tma_load_3d(smem_u32(sm + Sh::OFF_V + st * Sh::OP + x * Sh::HALF), &tmV, x * 64, (t0 + i) * PT, h,
-                      smem_u32(v_full + st));
+        if (elect_one()) {
+          mbar_expect_tx(smem_u32(v_full + st), Sh::OP);
+          for (int x = 0; x < Sh::HALVES; ++x)
+            tma_load_3d(smem_u32(sm + Sh::OFF_V + st * Sh::OP + x * Sh::HALF), &tmV, x * 64, (t0 + i) * PT, h,
+                        smem_u32(v_full + st));
+        }
         ++nv;
       }
       if (*abort_flag) {   // copies in flight land before the CTA leaves: the last two of each ring
         kv8_wait(smem_u32(q_full), 0, abort_flag, a.err, false);
-        for (int j = std::max(0, nk - 2); j < nk; ++j) kv8_wait(smem_u32(k_full + (j & 1)), (uint32_t)((j / 2) & 1), abort_flag, a.err, false);
-        for (int j = std::max(0, nv - 2); j < nv; ++j) kv8_wait(smem_u32(v_full + (j & 1)), (uint32_t)((j / 2) & 1), abort_flag, a.err, false);
+        for (int j = max(0, nk - 2); j < nk; ++j) kv8_wait(smem_u32(k_full + (j & 1)), (uint32_t)((j / 2) & 1), abort_flag, a.err, false);
+        for (int j = max(0, nv - 2); j < nv; ++j) kv8_wait(smem_u32(v_full + (j & 1)), (uint32_t)((j / 2) & 1), abort_flag, a.err, false);
       }
-    } else if (warp == 9 && lane == 0) {
+    } else if (warp == 9) {
       // ---- MMA ----
       constexpr uint32_t IS = pf_idesc(PT, false), IO = pf_idesc(D, true);
+      // operand descriptors; an offset of n bytes adds n >> 4
+      const uint64_t dq = sdesc_sw128(smem_u32(sm + Sh::OFF_Q)), dk = sdesc_sw128(smem_u32(sm + Sh::OFF_K)),
+                     dv = pf_desc_mn(smem_u32(sm + Sh::OFF_V), Sh::HALF);
       bool ok = kv8_wait(smem_u32(q_full), 0, abort_flag, a.err);
       auto issue_s = [&](int mt, int i) {
-        const uint32_t q = smem_u32(sm + Sh::OFF_Q + mt * Sh::OP), k = smem_u32(sm + Sh::OFF_K + (i & 1) * Sh::OP);
+        if (elect_one()) {
+          const uint64_t q = dq + mt * (Sh::OP >> 4), k = dk + (i & 1) * (Sh::OP >> 4);
 #pragma unroll
-        for (int x = 0; x < D / 16; ++x)
-          tc_mma_bf16(tmem + mt * PT, sdesc_sw128(q + (x >> 2) * Sh::HALF + (x & 3) * 32),
-                      sdesc_sw128(k + (x >> 2) * Sh::HALF + (x & 3) * 32), IS, x ? 1u : 0u);
-        tc_commit(smem_u32(s_full + mt));
-        if (mt == nmt - 1) tc_commit(smem_u32(k_empty + (i & 1)));
+          for (int x = 0; x < D / 16; ++x)
+            tc_mma_bf16(tmem + mt * PT, q + (((x >> 2) * Sh::HALF + (x & 3) * 32) >> 4),
+                        k + (((x >> 2) * Sh::HALF + (x & 3) * 32) >> 4), IS, x ? 1u : 0u);
+          tc_commit(smem_u32(s_full + mt));
+          if (mt == nmt - 1) tc_commit(smem_u32(k_empty + (i & 1)));
+        }
+        __syncwarp();
       };
       if (ok) ok = kv8_wait(smem_u32(k_full), 0, abort_flag, a.err);
       if (ok) {
@@ -324,20 +343,24 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
         for (int mt = 0; ok && mt < nmt; ++mt) {
           // P_i V_i, then S_(i+1) over the same columns: the tensor cores take them in this order
           ok = mt || kv8_wait(smem_u32(v_full + (i & 1)), (uint32_t)((i / 2) & 1), abort_flag, a.err);
-          const uint32_t v = smem_u32(sm + Sh::OFF_V + (i & 1) * Sh::OP);
+          const uint64_t v = dv + (i & 1) * (Sh::OP >> 4);
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
             ok = ok && kv8_wait(smem_u32(p_full + 2 * mt + hf), (uint32_t)(i & 1), abort_flag, a.err);
             if (!ok) break;
             tc_fence_after();
+            if (elect_one()) {
 #pragma unroll
-            for (int x = hf * PT / 32; x < (hf + 1) * PT / 32; ++x)
-              mma_ts(tmem + 2 * PT + mt * D, tmem + mt * PT + x * 8, pf_desc_mn(v + x * 2048, Sh::HALF), IO, (i || x) ? 1u : 0u);
+              for (int x = hf * PT / 32; x < (hf + 1) * PT / 32; ++x)
+                mma_ts(tmem + 2 * PT + mt * D, tmem + mt * PT + x * 8, v + ((x * 2048) >> 4), IO, (i || x) ? 1u : 0u);
+              if (hf) {
+                tc_commit(smem_u32(o_done + mt));
+                if (mt == nmt - 1) tc_commit(smem_u32(v_empty + (i & 1)));
+              }
+            }
+            __syncwarp();
           }
-          if (!ok) break;
-          tc_commit(smem_u32(o_done + mt));
-          if (mt == nmt - 1) tc_commit(smem_u32(v_empty + (i & 1)));
-          if (i + 1 < nt) {
+          if (ok && i + 1 < nt) {
             if (mt == 0) ok = kv8_wait(smem_u32(k_full + ((i + 1) & 1)), (uint32_t)(((i + 1) / 2) & 1), abort_flag, a.err);
             if (ok) {
               tc_fence_after();
@@ -347,7 +370,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
         }
       }
       if (!ok) {   // products in flight end before the CTA frees its TMEM
-        tc_commit(smem_u32(drain));
+        if (elect_one()) tc_commit(smem_u32(drain));
         kv8_wait(smem_u32(drain), 0, abort_flag, a.err, false);
       }
     }

@@ -22,7 +22,7 @@
 // item inside one CTA's range is finished there; the pieces of an item cut by range ends (at most two a
 // CTA) go to scratch as (o, m, l) and a second launch joins them in order. A producer warp streams the tiles (TMA,
 // 128- or 64-byte swizzle) through a ring that runs on across items.
-#include "kv8.cuh"
+#include "kv8_split.cuh"
 #include "kernels.h"
 
 #include <algorithm>
@@ -33,9 +33,7 @@ namespace eagle {
 namespace {
 
 constexpr int TK = 32;            // keys a tile
-constexpr int MAX_QV = 128;       // query vectors a block of rows
-constexpr int MAX_GROUPS = 512;   // row blocks a launch (more: several launches)
-constexpr int MAX_CTAS = 384;     // grid limit that the scratch is sized for
+constexpr int TC_ABOVE = 32;      // head_dim 128 with more query vectors a block goes to tcgen05 (128-key tiles)
 constexpr float LAZY = 8.f;       // how far (log2) a score may pass the reference maximum
 constexpr int E_UP = 4, E_DOWN = 12;   // exponents a tile may have around the reference, E_SPAN within one pass
 constexpr int E_SPAN = 14;
@@ -63,157 +61,10 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
 }
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
 __device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-// 16 bytes into shared memory; this thread's earlier copies arrive on `bar` once they are there.
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copies_arrive(uint32_t bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-}
-// 2^n, 0 below the normal range.
-__device__ __forceinline__ float pow2i(int n) { return n < -126 ? 0.f : __int_as_float((min(n, 127) + 127) << 23); }
-
-// How a call's rows are cut and its tiles shared out: the same numbers in both kernels and the scratch size.
-struct Plan {
-  int G, RB, nb, QV;      // query heads a KV head; rows a block; blocks a sequence; query vectors a block
-  uint32_t G_inv;         // x / G = x * G_inv >> 16 for x < 128
-  int width;              // lanes that look at one row block
-  int nkv;
-  int groups;             // row blocks of this launch, from block g0 on
-  int g0;
-  int grid, min_tiles;    // CTAs at most; tiles a CTA at least
-  int join_cols;          // query vectors a join CTA takes (a power of two up to 256 / (d / 8))
-  int pad;                // what starting and joining an item costs, in tiles: an item of nt tiles spans pad + nt units
-  int qv_pad;             // query vectors of a partial
-  float* part_o;          // [2 grid][qv_pad][D]
-  float* part_ml;         // [2 grid][qv_pad][2]
-  int4* cut;              // [grid] the item that CTA c begins and does not finish: row block, head, last CTA (-1: none)
-  const float *pp_o, *pp_ml;   // prefix partials [n_prefix][R * nq][D], [..][2]
-  int n_prefix;
-};
-
-// The units W of a launch over its CTAs: the first `more` CTAs take `per` + 1, the others `per`. An item's tiles are its
-// last units, so a range that ends inside its first `pad` units has none of it.
-struct Share {
-  uint32_t ctas, per, more;
-  __device__ __forceinline__ Share(const Plan& p, uint32_t tiles, int pad) {
-    // a CTA takes p.min_tiles tiles at least (one for each key group), or a whole average item where those are shorter
-    const uint32_t items = (uint32_t)p.groups * p.nkv, W = tiles + items * pad;
-    ctas = max(1u, min((uint32_t)p.grid, tiles / max(1u, min((uint32_t)p.min_tiles, tiles / items))));
-    per = W / ctas;
-    more = W - per * ctas;
-  }
-  __device__ __forceinline__ uint32_t start(uint32_t c) const { return c * per + min(c, more); }
-  __device__ __forceinline__ uint32_t cta_of(uint32_t u) const {
-    const uint32_t wide = more * (per + 1);
-    return u < wide ? u / (per + 1) : more + (u - wide) / per;
-  }
-};
-// The pad of a launch: p.pad, but not more than a CTA's even share of the tiles (few long items: ranges would lie in pads).
-__device__ __forceinline__ int pad_of(const Plan& p, uint32_t tiles) { return (int)min((uint32_t)p.pad, tiles / (uint32_t)p.grid); }
-
-// A row block's rows, its sequence (that of the first row that is not padding among the sequence's rows) and the
-// first slot past everything that its rows see.
-struct Group {
-  int r0, r1, seq, limit;
-};
-__device__ __forceinline__ int first_seq(const Kv8Attn& a, int s0, int s1) {
-  int seq = a.row_seq[s0];
-  for (int r = s0 + 1; r < s1 && seq < 0; ++r) seq = a.row_seq[r];
-  return seq < 0 ? -1 : seq;
-}
-// By `width` neighbouring lanes (a power of two up to 8); gi out of range gives an empty block. All lanes of a warp call.
-__device__ __forceinline__ Group group_of(const Kv8Attn& a, const Plan& p, int gi, int width, bool latch) {
-  const int sub = threadIdx.x & (width - 1);
-  Group o;
-  const int sidx = (p.g0 + gi) / p.nb, rb = (p.g0 + gi) - sidx * p.nb;
-  const int s0 = sidx * a.rows_per_seq, s1 = (int)min((long long)s0 + a.rows_per_seq, (long long)a.R);
-  o.r0 = s0 + rb * p.RB;
-  o.r1 = gi < p.groups ? min(o.r0 + p.RB, s1) : o.r0;   // a block that exists has rows
-  o.seq = o.r0 < o.r1 ? first_seq(a, s0, s1) : -1;
-  bool bad = o.seq >= a.c.max_batch;
-  if (bad) o.seq = -1;
-  const int ctx = a.mode == 1 && o.seq >= 0 ? a.ctx_len[o.seq] : 0;
-  int lim = 0;
-  if (o.seq >= 0) {
-    bad = bad || ctx < 0;
-    const int words = (a.tree_T + 63) >> 6;
-    for (int r = o.r0 + sub; r < o.r1; r += width) {
-      const int rs = a.row_seq[r];
-      int end = a.mode == 0 ? min(a.row_slot[r], INT32_MAX - 1) + 1 : ctx;
-      if (a.mode == 1)
-        for (int w = 0; w < words; ++w) {
-          uint64_t m = a.mask[(size_t)r * a.mask_words + w];
-          if (w == words - 1 && (a.tree_T & 63)) m &= (1ull << (a.tree_T & 63)) - 1;
-          if (m) end = (int)min((long long)INT32_MAX, (long long)ctx + w * 64 + 64 - __clzll((long long)m));
-        }
-      if (rs == o.seq) lim = max(lim, end);
-      else bad = bad || rs >= 0;
-    }
-  }
-  for (int d = width >> 1; d > 0; d >>= 1) lim = max(lim, __shfl_xor_sync(0xffffffffu, lim, d));
-  bad = bad || lim > a.c.cap;
-  o.limit = max(0, min(lim, a.c.cap));
-  if (latch && bad) latch_error(a.err, DEVERR_BOUNDS);
-  return o;
-}
-
-// Adds n partials to (top, L, o), o 8 values of a query vector whose D values are spread over D / 8 neighbouring
-// lanes (sub: this lane's place among them): the lanes share the (m, l) pairs, the sums run in the order of the partials.
-template <int D, typename At>
-__device__ __forceinline__ void fold(int n, At at, const float* ml, const float* po, int sub, float& top, float& L, float* o) {
-  constexpr int GL = D / 8;
-  const unsigned group = ((GL == 32 ? 0u : 1u << GL) - 1u) << ((threadIdx.x & 31) / GL * GL);
-  float mx = top;
-  for (int i = sub; i < n; i += GL) mx = fmaxf(mx, ml[2 * at(i)]);
-#pragma unroll
-  for (int d = GL / 2; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(group, mx, d));
-  const float base = mx == -INFINITY ? 0.f : mx, f = ex2(top - base);
-  top = mx;
-  L *= f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) o[i] *= f;
-  for (int i0 = 0; i0 < n; i0 += GL) {
-    float w = 0.f, lw = 0.f;
-    if (i0 + sub < n) {
-      const float2 v = *reinterpret_cast<const float2*>(ml + 2 * at(i0 + sub));
-      w = ex2(v.x - base);
-      lw = v.y * w;
-    }
-    const int cnt = min(GL, n - i0);
-#pragma unroll 4
-    for (int j = 0; j < cnt; ++j) {
-      const float4* x = reinterpret_cast<const float4*>(po + at(i0 + j) * D + sub * 8);
-      const float4 a = x[0], b = x[1];
-      const float wj = __shfl_sync(group, w, j, GL);
-      L += __shfl_sync(group, lw, j, GL);
-      o[0] = fmaf(a.x, wj, o[0]); o[1] = fmaf(a.y, wj, o[1]); o[2] = fmaf(a.z, wj, o[2]); o[3] = fmaf(a.w, wj, o[3]);
-      o[4] = fmaf(b.x, wj, o[4]); o[5] = fmaf(b.y, wj, o[5]); o[6] = fmaf(b.z, wj, o[6]); o[7] = fmaf(b.w, wj, o[7]);
-    }
-  }
-}
-
-// 8 finished values of one query vector; nothing seen, or a row that is padding or invalid: zeros.
-__device__ __forceinline__ void store8(const Kv8Attn& a, size_t at, int D, int c, bool live, float L, const float* o) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const bool none = !live || L == 0.f;
-    const __nv_bfloat162 h = __floats2bfloat162_rn(none ? 0.f : o[2 * i] / L, none ? 0.f : o[2 * i + 1] / L);
-    w[i] = *reinterpret_cast<const uint32_t*>(&h);
-  }
-  *reinterpret_cast<uint4*>((__nv_bfloat16*)a.out + at * D + c) = make_uint4(w[0], w[1], w[2], w[3]);
-}
-
 // Shared memory of one configuration: D dims; NT query tiles (of 8) a warp, WN warps side by side over the query
 // tiles, WK groups of them over the keys; NS tiles in the ring.
 template <int D, int NT, int WN, int WK, int NS>
@@ -269,73 +120,13 @@ __global__ void __launch_bounds__(Shape<D, NT, WN, WK, NS>::THREADS, CTAS)
     fence_mbar_init();
   }
   PDL_ENTRY();
-  for (int g0 = 0; g0 < p.groups; g0 += Sh::THREADS / p.width) {
-    const int gi = g0 + threadIdx.x / p.width;
-    const Group gr = group_of(a, p, gi, p.width, blockIdx.x == 0);
-    if (gi < p.groups && (threadIdx.x & (p.width - 1)) == 0) {
-      s_lim[gi] = gr.limit;
-      s_seq[gi] = gr.seq;
-      s_pref[gi + 1] = max(1, (gr.limit + TK - 1) / TK);
-    }
-  }
-  __syncthreads();
-  if (warp == 0) {   // inclusive sums
-    int run = 0;
-    for (int b = 0; b < p.groups; b += 32) {
-      int v = b + lane < p.groups ? s_pref[b + lane + 1] : 0;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, v, d);
-        if (lane >= d) v += u;
-      }
-      if (b + lane < p.groups) s_pref[b + lane + 1] = run + v;
-      run += __shfl_sync(0xffffffffu, v, 31);
-    }
-    if (lane == 0) s_pref[0] = 0;
-  }
-  __syncthreads();
+  lay_out(a, p, s_pref, s_lim, s_seq);
   const uint32_t tiles = (uint32_t)s_pref[p.groups] * nkv;
   const int pad = pad_of(p, tiles);
   const Share share(p, tiles, pad);
   if (threadIdx.x == 0) p.cut[blockIdx.x] = make_int4(0, 0, -1, 0);
   if (blockIdx.x >= share.ctas) return;
-  const uint32_t w0 = share.start(blockIdx.x), w1 = share.start(blockIdx.x + 1);
-
-  // A walk over the items (row block, head) of the range, in order: tiles [t0, t1) of nt.
-  struct Walk {
-    int gi, h, t0, t1, nt;
-    uint32_t base;   // the item's first unit
-  };
-  auto units = [&](int g) { return (uint32_t)(s_pref[g] + g * pad) * nkv; };   // before row block g
-  auto enter = [&](Walk& k, uint32_t from) {   // the item's tiles in the range, from unit `from` of it on
-    k.nt = s_pref[k.gi + 1] - s_pref[k.gi];
-    k.t0 = max(0, (int)from - pad);
-    k.t1 = min(k.nt, (int)(w1 - k.base) - pad);
-  };
-  auto begin = [&](Walk& k) {   // false: no tiles in the whole range
-    int lo = 0, hi = p.groups;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (units(mid) <= w0) lo = mid;
-      else hi = mid;
-    }
-    k.gi = lo;
-    const uint32_t first = units(lo), span = s_pref[lo + 1] - s_pref[lo] + pad;
-    k.h = (int)((w0 - first) / span);
-    k.base = first + k.h * span;
-    enter(k, w0 - k.base);
-    return k.t0 < k.t1;
-  };
-  auto next = [&](Walk& k) {    // false: the range ends
-    k.base += k.nt + pad;
-    if (k.base + pad >= w1) return false;
-    if (++k.h == nkv) {
-      k.h = 0;
-      ++k.gi;
-    }
-    enter(k, 0);
-    return true;
-  };
+  const Range range{s_pref, pad, nkv, p.groups, share.start(blockIdx.x), share.start(blockIdx.x + 1)};
 
   // The query vectors of an item as fp16 of q 2^-e, the factor that gives its scores in log2 units, what each sees. By
   // `warps` warps, of which this is number sw.
@@ -421,11 +212,11 @@ __global__ void __launch_bounds__(Shape<D, NT, WN, WK, NS>::THREADS, CTAS)
       // row warps: the first item together with the consumers, each later one in the buffer that the consumers are not at
       const int sw = warp - NW - 1;
       Walk k;
-      bool more = begin(k);
+      bool more = k.begin(range);
       if (more) prepare(0, k, NW + sw, NW + Sh::ROWS_W);
       asm volatile("bar.arrive 2, %0;" ::"n"(FIRST) : "memory");
-      more = more && next(k);
-      for (int item = 1; more; ++item, more = next(k)) {
+      more = more && k.next(range);
+      for (int item = 1; more; ++item, more = k.next(range)) {
         prepare(item, k, sw, Sh::ROWS_W);
         if (lane == 0) mbar_arrive(smem_u32(q_full + (item & 1)));
       }
@@ -439,7 +230,7 @@ __global__ void __launch_bounds__(Shape<D, NT, WN, WK, NS>::THREADS, CTAS)
     uint32_t ph = 1;
     bool ok = true;
     Walk k;
-    for (bool more = begin(k); more && ok; more = next(k)) {
+    for (bool more = k.begin(range); more && ok; more = k.next(range)) {
       const int limit = s_lim[k.gi], seq = s_seq[k.gi];
       for (int b = k.t0; ok && b < k.t1; b += 32) {
         int halves = 0, vec0 = 0, vec1 = 0;   // the tile's 16-key halves that hold keys, and where they are
@@ -499,14 +290,14 @@ __global__ void __launch_bounds__(Shape<D, NT, WN, WK, NS>::THREADS, CTAS)
     float* s_l = s_m + WK * Sh::QV;
     float* s_o = reinterpret_cast<float*>(sm + Sh::OFF_O);
     Walk k;
-    bool more = begin(k);
+    bool more = k.begin(range);
     if (more) prepare(0, k, warp, NW + Sh::ROWS_W);
     asm volatile("bar.sync 2, %0;" ::"n"(FIRST) : "memory");
     // this lane's row of the ldmatrix tiles, with its swizzle, 16-byte column 0: column c is at ^ (16 c)
     auto swizzled = [&](int row, int col) { return row * D + (D == 128 ? col ^ (row & 7) : col ^ ((row >> 1) & 3)) * 16; };
     const uint32_t k_at = swizzled(lane, 0), v_at = swizzled(lane & 15, lane >> 4);
     int i = 0;   // tiles of the range that are behind
-    for (int item = 0; more; ++item, more = next(k)) {
+    for (int item = 0; more; ++item, more = k.next(range)) {
       const int gi = k.gi, h = k.h, t0 = k.t0, t1 = k.t1, nt = k.nt;
       const int seq = s_seq[gi], limit = s_lim[gi];
       const int sidx = (p.g0 + gi) / p.nb, rb = (p.g0 + gi) - sidx * p.nb;
@@ -873,8 +664,9 @@ size_t al256(size_t x) { return (x + 255) / 256 * 256; }
 // Row blocks: a sequence's rows in one block when their query vectors fit, else in equal blocks.
 void cut_rows(const Kv8& c, int nq, int rows_per_seq, Plan& p) {
   p.nkv = c.nkv;
+  p.tk = TK;
   p.G = nq / c.nkv;
-  const int most = MAX_QV / p.G;
+  const int most = KV8_MAX_QV / p.G;
   p.nb = (rows_per_seq + most - 1) / most;
   p.RB = (rows_per_seq + p.nb - 1) / p.nb;
   p.QV = p.RB * p.G;
@@ -885,39 +677,50 @@ void cut_rows(const Kv8& c, int nq, int rows_per_seq, Plan& p) {
 }
 
 size_t own_scratch(const Kv8& c, const Plan& p) {
-  return al256((size_t)2 * MAX_CTAS * p.qv_pad * c.d * sizeof(float)) +
-         al256((size_t)2 * MAX_CTAS * p.qv_pad * 2 * sizeof(float)) + al256(MAX_CTAS * sizeof(int4));
+  return al256((size_t)2 * KV8_MAX_CTAS * p.qv_pad * c.d * sizeof(float)) +
+         al256((size_t)2 * KV8_MAX_CTAS * p.qv_pad * 2 * sizeof(float)) + al256(KV8_MAX_CTAS * sizeof(int4));
+}
+
+template <int D>
+cudaError_t launch_join(cudaStream_t st, const Kv8Attn& a, Plan& p) {
+  p.join_cols = 1;
+  while (p.join_cols < 256 / (D / 8) && p.join_cols * 4 < p.QV) p.join_cols *= 2;
+  return launch_k(kv8_join_k<D>, dim3(p.grid, (p.QV + p.join_cols - 1) / p.join_cols), dim3(256), 0, st, a, p);
 }
 
 template <int D, int NT, int WN, int WK, int NS, int CTAS>
 cudaError_t launch_own(cudaStream_t st, const Kv8Attn& a, Plan& p, const CUtensorMap& mk, const CUtensorMap& mv) {
   using Sh = Shape<D, NT, WN, WK, NS>;
   const auto fn = kv8_attn_k<D, NT, WN, WK, NS, CTAS>;
-  p.grid = std::min(MAX_CTAS, CTAS * device_sm_count());
+  p.grid = std::min(KV8_MAX_CTAS, CTAS * device_sm_count());
   p.min_tiles = WK;
   p.pad = 6 + p.n_prefix / 2;
   const int smem = Sh::bytes(p.groups);
   cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(fn), smem);
   if (e != cudaSuccess) return e;
   e = launch_k(fn, dim3(p.grid), dim3(Sh::THREADS), smem, st, mk, mv, a, p);
-  if (e != cudaSuccess) return e;
-  p.join_cols = 1;
-  while (p.join_cols < 256 / (D / 8) && p.join_cols * 4 < p.QV) p.join_cols *= 2;
-  return launch_k(kv8_join_k<D>, dim3(p.grid, (p.QV + p.join_cols - 1) / p.join_cols), dim3(256), 0, st, a, p);
+  return e != cudaSuccess ? e : launch_join<D>(st, a, p);
 }
 
 // The narrowest configuration that holds a block's query vectors: up to 16 in two small CTAs an SM (one's joins
 // under the other's loads), more in one CTA whose warps share the query tiles.
 template <int D>
-cudaError_t launch_d(cudaStream_t st, const Kv8Attn& a, Plan& p, const CUtensorMap& mk, const CUtensorMap& mv) {
+cudaError_t launch_mma(cudaStream_t st, const Kv8Attn& a, Plan& p, const CUtensorMap& mk, const CUtensorMap& mv) {
   const int t = p.qv_pad / 8;
   if (t <= 1) return launch_own<D, 1, 1, 4, 11, 2>(st, a, p, mk, mv);
   if (t <= 2) return launch_own<D, 2, 1, 4, 9, 2>(st, a, p, mk, mv);
   if (t <= 4) return launch_own<D, 4, 1, 8, 20, 1>(st, a, p, mk, mv);
-  if (t <= 6) return launch_own<D, 3, 2, 4, 18, 1>(st, a, p, mk, mv);
-  if (t <= 8) return launch_own<D, 4, 2, 4, 16, 1>(st, a, p, mk, mv);
-  if (t <= 12) return launch_own<D, 3, 4, 2, 11, 1>(st, a, p, mk, mv);
-  return launch_own<D, 4, 4, 2, 7, 1>(st, a, p, mk, mv);
+  if constexpr (D == 64) {
+    if (t <= 6) return launch_own<D, 3, 2, 4, 18, 1>(st, a, p, mk, mv);
+    if (t <= 8) return launch_own<D, 4, 2, 4, 16, 1>(st, a, p, mk, mv);
+    if (t <= 12) return launch_own<D, 3, 4, 2, 11, 1>(st, a, p, mk, mv);
+    return launch_own<D, 4, 4, 2, 7, 1>(st, a, p, mk, mv);
+  }
+  p.grid = std::min(KV8_MAX_CTAS, device_sm_count());
+  p.min_tiles = 1;
+  p.pad = 3;
+  const cudaError_t e = kv8_launch_tc(st, a, p, mk, mv);
+  return e != cudaSuccess ? e : launch_join<D>(st, a, p);
 }
 
 }  // namespace
@@ -934,14 +737,14 @@ int kv8_attention(cudaStream_t st, const Kv8Attn& a) {
   cut_rows(a.c, a.nq, a.rows_per_seq, p);
   uint8_t* s = (uint8_t*)a.scratch;
   p.part_o = (float*)s;
-  s += al256((size_t)2 * MAX_CTAS * p.qv_pad * a.c.d * sizeof(float));
+  s += al256((size_t)2 * KV8_MAX_CTAS * p.qv_pad * a.c.d * sizeof(float));
   p.part_ml = (float*)s;
-  s += al256((size_t)2 * MAX_CTAS * p.qv_pad * 2 * sizeof(float));
+  s += al256((size_t)2 * KV8_MAX_CTAS * p.qv_pad * 2 * sizeof(float));
   p.cut = (int4*)s;
   if (a.P) {
     p.n_prefix = kv8_prefix_splits(a.c.nkv, a.R, a.nq, a.P);
     const size_t qv = (size_t)a.R * a.nq * p.n_prefix;
-    float* o = (float*)(s + al256(MAX_CTAS * sizeof(int4)));
+    float* o = (float*)(s + al256(KV8_MAX_CTAS * sizeof(int4)));
     float* ml = (float*)((uint8_t*)o + al256(qv * a.c.d * sizeof(float)));
     p.pp_o = o;
     p.pp_ml = ml;
@@ -950,18 +753,19 @@ int kv8_attention(cudaStream_t st, const Kv8Attn& a) {
   }
   const long long rows = a.c.table ? ((long long)a.c.n_blocks * a.c.nkv) << a.c.block_log2
                                    : (long long)a.c.max_batch * a.c.nkv * a.c.cap;
-  const int box = a.c.table ? std::min(TK, 1 << a.c.block_log2) : TK;
+  if (a.c.d == 128 && p.qv_pad > TC_ABOVE) p.tk = 128;
+  const int box = a.c.table ? std::min(p.tk, 1 << a.c.block_log2) : p.tk;
   CUtensorMap mk, mv;
   if (!code_map(&mk, a.c.k, rows, a.c.d, box) || !code_map(&mv, a.c.v, rows, a.c.d, box)) return -4;
   // row blocks that hold rows: the last sequence may have fewer
   const long long seqs = ((long long)a.R + a.rows_per_seq - 1) / a.rows_per_seq;
   const long long blocks = (seqs - 1) * p.nb + (a.R - (seqs - 1) * a.rows_per_seq + p.RB - 1) / p.RB;
   // tiles of a launch and their flat numbers stay in 32 bits
-  if (blocks > 0x7fffffffll || (double)std::min<long long>(blocks, MAX_GROUPS) * (a.c.cap / TK + 32) * a.c.nkv > 2e9) return -1;
-  for (long long g0 = 0; g0 < blocks; g0 += MAX_GROUPS) {
+  if (blocks > 0x7fffffffll || (double)std::min<long long>(blocks, KV8_MAX_GROUPS) * (a.c.cap / TK + 32) * a.c.nkv > 2e9) return -1;
+  for (long long g0 = 0; g0 < blocks; g0 += KV8_MAX_GROUPS) {
     p.g0 = (int)g0;
-    p.groups = (int)std::min<long long>(MAX_GROUPS, blocks - g0);
-    const cudaError_t e = a.c.d == 128 ? launch_d<128>(st, a, p, mk, mv) : launch_d<64>(st, a, p, mk, mv);
+    p.groups = (int)std::min<long long>(KV8_MAX_GROUPS, blocks - g0);
+    const cudaError_t e = a.c.d == 128 ? launch_mma<128>(st, a, p, mk, mv) : launch_mma<64>(st, a, p, mk, mv);
     if (e != cudaSuccess) {
       cudaGetLastError();
       return -4;

@@ -1,0 +1,242 @@
+// How an 8-bit cache attention call is cut into work and put together again: shared by its kernels.
+//
+// A call is a list of items (row block, KV head), each with the tiles of the slots that its rows see; lengths are
+// read on the device. Laid end to end the tiles are shared out over the CTAs in equal contiguous ranges, so that
+// ragged batches and one long sequence balance alike. An item inside one CTA's range is finished there; the pieces of
+// an item cut by range ends (at most two a CTA) go to scratch as (o, m, l) and a second launch joins them in order.
+#pragma once
+
+#include "kv8.cuh"
+
+#include <cuda.h>
+
+namespace eagle {
+
+constexpr int KV8_MAX_QV = 128;       // query vectors a block of rows
+constexpr int KV8_MAX_GROUPS = 512;   // row blocks a launch (more: several launches)
+constexpr int KV8_MAX_CTAS = 384;     // grid limit that the scratch is sized for
+
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// 16 bytes into shared memory; this thread's earlier copies arrive on `bar` once they are there.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+// 2^n, 0 below the normal range.
+__device__ __forceinline__ float pow2i(int n) { return n < -126 ? 0.f : __int_as_float((min(n, 127) + 127) << 23); }
+
+// How a call's rows are cut and its tiles shared out: the same numbers in both kernels and the scratch size.
+struct Plan {
+  int G, RB, nb, QV;      // query heads a KV head; rows a block; blocks a sequence; query vectors a block
+  uint32_t G_inv;         // x / G = x * G_inv >> 16 for x < 128
+  int width;              // lanes that look at one row block
+  int nkv;
+  int tk;                 // keys a tile
+  int groups;             // row blocks of this launch, from block g0 on
+  int g0;
+  int grid, min_tiles;    // CTAs at most; tiles a CTA at least
+  int join_cols;          // query vectors a join CTA takes (a power of two up to 256 / (d / 8))
+  int pad;                // what starting and joining an item costs, in tiles: an item of nt tiles spans pad + nt units
+  int qv_pad;             // query vectors of a partial
+  float* part_o;          // [2 grid][qv_pad][D]
+  float* part_ml;         // [2 grid][qv_pad][2]
+  int4* cut;              // [grid] the item that CTA c begins and does not finish: row block, head, last CTA (-1: none)
+  const float *pp_o, *pp_ml;   // prefix partials [n_prefix][R * nq][D], [..][2]
+  int n_prefix;
+};
+
+// The units W of a launch over its CTAs: the first `more` CTAs take `per` + 1, the others `per`. An item's tiles are its
+// last units, so a range that ends inside its first `pad` units has none of it.
+struct Share {
+  uint32_t ctas, per, more;
+  __device__ __forceinline__ Share(const Plan& p, uint32_t tiles, int pad) {
+    // a CTA takes p.min_tiles tiles at least (one for each key group), or a whole average item where those are shorter
+    const uint32_t items = (uint32_t)p.groups * p.nkv, W = tiles + items * pad;
+    ctas = max(1u, min((uint32_t)p.grid, tiles / max(1u, min((uint32_t)p.min_tiles, tiles / items))));
+    per = W / ctas;
+    more = W - per * ctas;
+  }
+  __device__ __forceinline__ uint32_t start(uint32_t c) const { return c * per + min(c, more); }
+  __device__ __forceinline__ uint32_t cta_of(uint32_t u) const {
+    const uint32_t wide = more * (per + 1);
+    return u < wide ? u / (per + 1) : more + (u - wide) / per;
+  }
+};
+// The pad of a launch: p.pad, but not more than a CTA's even share of the tiles (few long items: ranges would lie in pads).
+__device__ __forceinline__ int pad_of(const Plan& p, uint32_t tiles) { return (int)min((uint32_t)p.pad, tiles / (uint32_t)p.grid); }
+
+// A row block's rows, its sequence (that of the first row that is not padding among the sequence's rows) and the
+// first slot past everything that its rows see.
+struct Group {
+  int r0, r1, seq, limit;
+};
+__device__ __forceinline__ int first_seq(const Kv8Attn& a, int s0, int s1) {
+  int seq = a.row_seq[s0];
+  for (int r = s0 + 1; r < s1 && seq < 0; ++r) seq = a.row_seq[r];
+  return seq < 0 ? -1 : seq;
+}
+// By `width` neighbouring lanes (a power of two up to 8); gi out of range gives an empty block. All lanes of a warp call.
+__device__ __forceinline__ Group group_of(const Kv8Attn& a, const Plan& p, int gi, int width, bool latch) {
+  const int sub = threadIdx.x & (width - 1);
+  Group o;
+  const int sidx = (p.g0 + gi) / p.nb, rb = (p.g0 + gi) - sidx * p.nb;
+  const int s0 = sidx * a.rows_per_seq, s1 = (int)min((long long)s0 + a.rows_per_seq, (long long)a.R);
+  o.r0 = s0 + rb * p.RB;
+  o.r1 = gi < p.groups ? min(o.r0 + p.RB, s1) : o.r0;   // a block that exists has rows
+  o.seq = o.r0 < o.r1 ? first_seq(a, s0, s1) : -1;
+  bool bad = o.seq >= a.c.max_batch;
+  if (bad) o.seq = -1;
+  const int ctx = a.mode == 1 && o.seq >= 0 ? a.ctx_len[o.seq] : 0;
+  int lim = 0;
+  if (o.seq >= 0) {
+    bad = bad || ctx < 0;
+    const int words = (a.tree_T + 63) >> 6;
+    for (int r = o.r0 + sub; r < o.r1; r += width) {
+      const int rs = a.row_seq[r];
+      int end = a.mode == 0 ? min(a.row_slot[r], INT32_MAX - 1) + 1 : ctx;
+      if (a.mode == 1)
+        for (int w = 0; w < words; ++w) {
+          uint64_t m = a.mask[(size_t)r * a.mask_words + w];
+          if (w == words - 1 && (a.tree_T & 63)) m &= (1ull << (a.tree_T & 63)) - 1;
+          if (m) end = (int)min((long long)INT32_MAX, (long long)ctx + w * 64 + 64 - __clzll((long long)m));
+        }
+      if (rs == o.seq) lim = max(lim, end);
+      else bad = bad || rs >= 0;
+    }
+  }
+  for (int d = width >> 1; d > 0; d >>= 1) lim = max(lim, __shfl_xor_sync(0xffffffffu, lim, d));
+  bad = bad || lim > a.c.cap;
+  o.limit = max(0, min(lim, a.c.cap));
+  if (latch && bad) latch_error(a.err, DEVERR_BOUNDS);
+  return o;
+}
+
+// Adds n partials to (top, L, o), o 8 values of a query vector whose D values are spread over D / 8 neighbouring
+// lanes (sub: this lane's place among them): the lanes share the (m, l) pairs, the sums run in the order of the partials.
+template <int D, typename At>
+__device__ __forceinline__ void fold(int n, At at, const float* ml, const float* po, int sub, float& top, float& L, float* o) {
+  constexpr int GL = D / 8;
+  const unsigned group = ((GL == 32 ? 0u : 1u << GL) - 1u) << ((threadIdx.x & 31) / GL * GL);
+  float mx = top;
+  for (int i = sub; i < n; i += GL) mx = fmaxf(mx, ml[2 * at(i)]);
+#pragma unroll
+  for (int d = GL / 2; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(group, mx, d));
+  const float base = mx == -INFINITY ? 0.f : mx, f = ex2(top - base);
+  top = mx;
+  L *= f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) o[i] *= f;
+  for (int i0 = 0; i0 < n; i0 += GL) {
+    float w = 0.f, lw = 0.f;
+    if (i0 + sub < n) {
+      const float2 v = *reinterpret_cast<const float2*>(ml + 2 * at(i0 + sub));
+      w = ex2(v.x - base);
+      lw = v.y * w;
+    }
+    const int cnt = min(GL, n - i0);
+#pragma unroll 4
+    for (int j = 0; j < cnt; ++j) {
+      const float4* x = reinterpret_cast<const float4*>(po + at(i0 + j) * D + sub * 8);
+      const float4 a = x[0], b = x[1];
+      const float wj = __shfl_sync(group, w, j, GL);
+      L += __shfl_sync(group, lw, j, GL);
+      o[0] = fmaf(a.x, wj, o[0]); o[1] = fmaf(a.y, wj, o[1]); o[2] = fmaf(a.z, wj, o[2]); o[3] = fmaf(a.w, wj, o[3]);
+      o[4] = fmaf(b.x, wj, o[4]); o[5] = fmaf(b.y, wj, o[5]); o[6] = fmaf(b.z, wj, o[6]); o[7] = fmaf(b.w, wj, o[7]);
+    }
+  }
+}
+
+// 8 finished values of one query vector; nothing seen, or a row that is padding or invalid: zeros.
+__device__ __forceinline__ void store8(const Kv8Attn& a, size_t at, int D, int c, bool live, float L, const float* o) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const bool none = !live || L == 0.f;
+    const __nv_bfloat162 h = __floats2bfloat162_rn(none ? 0.f : o[2 * i] / L, none ? 0.f : o[2 * i + 1] / L);
+    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  *reinterpret_cast<uint4*>((__nv_bfloat16*)a.out + at * D + c) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// A CTA's range as a walk over its items, in order.
+struct Range {
+  const int* pref;           // [groups + 1] tiles a head before each row block
+  int pad, nkv, groups;
+  uint32_t w0, w1;
+  __device__ __forceinline__ uint32_t units(int g) const { return (uint32_t)(pref[g] + g * pad) * nkv; }
+};
+struct Walk {
+  int gi, h, t0, t1, nt;     // row block, head, its tiles [t0, t1) of nt
+  uint32_t base;             // the item's first unit
+  __device__ __forceinline__ void enter(const Range& r, uint32_t from) {   // from unit `from` of the item on
+    nt = r.pref[gi + 1] - r.pref[gi];
+    t0 = max(0, (int)from - r.pad);
+    t1 = min(nt, (int)(r.w1 - base) - r.pad);
+  }
+  __device__ __forceinline__ bool begin(const Range& r) {   // false: no tiles in the whole range
+    int lo = 0, hi = r.groups;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (r.units(mid) <= r.w0) lo = mid;
+      else hi = mid;
+    }
+    gi = lo;
+    const uint32_t first = r.units(lo), span = r.pref[lo + 1] - r.pref[lo] + r.pad;
+    h = (int)((r.w0 - first) / span);
+    base = first + h * span;
+    enter(r, r.w0 - base);
+    return t0 < t1;
+  }
+  __device__ __forceinline__ bool next(const Range& r) {    // false: the range ends
+    base += nt + r.pad;
+    if (base + r.pad >= r.w1) return false;
+    if (++h == r.nkv) {
+      h = 0;
+      ++gi;
+    }
+    enter(r, 0);
+    return true;
+  }
+};
+
+// The launch's items as every CTA sees them: s_pref [groups + 1] (tiles a head before each row block), s_lim and s_seq
+// [groups]. By all threads of the CTA; ends with a barrier.
+__device__ __forceinline__ void lay_out(const Kv8Attn& a, const Plan& p, int* s_pref, int* s_lim, int* s_seq) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int g0 = 0; g0 < p.groups; g0 += blockDim.x / p.width) {
+    const int gi = g0 + threadIdx.x / p.width;
+    const Group gr = group_of(a, p, gi, p.width, blockIdx.x == 0);
+    if (gi < p.groups && (threadIdx.x & (p.width - 1)) == 0) {
+      s_lim[gi] = gr.limit;
+      s_seq[gi] = gr.seq;
+      s_pref[gi + 1] = max(1, (gr.limit + p.tk - 1) / p.tk);
+    }
+  }
+  __syncthreads();
+  if (warp == 0) {   // inclusive sums
+    int run = 0;
+    for (int b = 0; b < p.groups; b += 32) {
+      int v = b + lane < p.groups ? s_pref[b + lane + 1] : 0;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, v, d);
+        if (lane >= d) v += u;
+      }
+      if (b + lane < p.groups) s_pref[b + lane + 1] = run + v;
+      run += __shfl_sync(0xffffffffu, v, 31);
+    }
+    if (lane == 0) s_pref[0] = 0;
+  }
+  __syncthreads();
+}
+
+// Host side: the kernel for up to 128 query vectors a block on tcgen05 (head_dim 128).
+cudaError_t kv8_launch_tc(cudaStream_t st, const Kv8Attn& a, Plan& p, const CUtensorMap& k, const CUtensorMap& v);
+
+}  // namespace eagle

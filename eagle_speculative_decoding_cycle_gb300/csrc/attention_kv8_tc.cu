@@ -605,10 +605,15 @@ __global__ void __launch_bounds__(T_THREADS, 1)
         if (ok) {
           tc_fence_after();
           if (elect_one()) {
-            const uint64_t q = dq + buf * (2 * OPB >> 4), kd = dk + st * (OPB >> 4);
-#pragma unroll
-            for (int x = 0; x < 8; ++x)   // high part, low part
-              mma8_ss(tmem + (si & 1) * TT, q + (((x >> 2) * OPB + (x & 3) * 32) >> 4), kd + (((x & 3) * 32) >> 4), IS, x ? 1u : 0u);
+            // rolled loops: unrolled, their operands are hoisted out of the tile loop and spilled (2500 clocks an S)
+            uint64_t q = dq + buf * (2 * OPB >> 4);
+            uint32_t acc = 0;
+#pragma unroll 1
+            for (int part = 0; part < 2; ++part, q += (OPB >> 4) - 8) {   // high part, low part
+              uint64_t kd = dk + st * (OPB >> 4);
+#pragma unroll 1
+              for (int x = 0; x < 4; ++x, q += 2, kd += 2, acc = 1) mma8_ss(tmem + (si & 1) * TT, q, kd, IS, acc);
+            }
             tc_commit(smem_u32(s_full + (si & 1)));
             if (s_tile + 1 == a_head.t1) tc_commit(smem_u32(q_empty + buf));
           }
@@ -635,11 +640,14 @@ __global__ void __launch_bounds__(T_THREADS, 1)
             again = s_more[wg] != 0;
             tc_fence_after();
             if (elect_one()) {
-              const uint64_t v = dv + st * (OPB >> 4);
-              const uint32_t fresh = j < 2 && pass == 0 ? 0u : 1u;   // the warpgroup's first tile of the item begins O
-#pragma unroll
-              for (int x = 0; x < 12; ++x)
-                mma8_ts(tmem + 2 * TT + wg * TT, tmem + wg * TT + x * 8, v + (((x & 3) * 32 * TT) >> 4), IO, x ? 1u : fresh);
+              uint32_t acc = j < 2 && pass == 0 ? 0u : 1u;   // the warpgroup's first tile of the item begins O
+              uint32_t pa = tmem + wg * TT;
+#pragma unroll 1
+              for (int part = 0; part < 3; ++part) {
+                uint64_t v = dv + st * (OPB >> 4);
+#pragma unroll 1
+                for (int x = 0; x < 4; ++x, pa += 8, v += 32 * TT >> 4, acc = 1) mma8_ts(tmem + 2 * TT + wg * TT, pa, v, IO, acc);
+              }
               tc_commit(smem_u32(o_done + wg));
               if (!again) tc_commit(smem_u32(kv_empty + st));
             }

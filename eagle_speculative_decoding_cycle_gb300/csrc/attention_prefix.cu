@@ -324,11 +324,13 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
       bool ok = kv8_wait(smem_u32(q_full), 0, abort_flag, a.err);
       auto issue_s = [&](int mt, int i) {
         if (elect_one()) {
-          const uint64_t q = dq + mt * (Sh::OP >> 4), k = dk + (i & 1) * (Sh::OP >> 4);
-#pragma unroll
-          for (int x = 0; x < D / 16; ++x)
-            tc_mma_bf16(tmem + mt * PT, q + (((x >> 2) * Sh::HALF + (x & 3) * 32) >> 4),
-                        k + (((x >> 2) * Sh::HALF + (x & 3) * 32) >> 4), IS, x ? 1u : 0u);
+          // rolled loops: unrolled, their operands are hoisted out of the tile loop and spilled
+          uint64_t q = dq + mt * (Sh::OP >> 4), k = dk + (i & 1) * (Sh::OP >> 4);
+          uint32_t acc = 0;
+#pragma unroll 1
+          for (int hd = 0; hd < Sh::HALVES; ++hd, q += (Sh::HALF >> 4) - 8, k += (Sh::HALF >> 4) - 8)
+#pragma unroll 1
+            for (int x = 0; x < 4; ++x, q += 2, k += 2, acc = 1) tc_mma_bf16(tmem + mt * PT, q, k, IS, acc);
           tc_commit(smem_u32(s_full + mt));
           if (mt == nmt - 1) tc_commit(smem_u32(k_empty + (i & 1)));
         }
@@ -344,15 +346,16 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
           // P_i V_i, then S_(i+1) over the same columns: the tensor cores take them in this order
           ok = mt || kv8_wait(smem_u32(v_full + (i & 1)), (uint32_t)((i / 2) & 1), abort_flag, a.err);
           const uint64_t v = dv + (i & 1) * (Sh::OP >> 4);
-#pragma unroll
+#pragma unroll 1
           for (int hf = 0; hf < 2; ++hf) {
             ok = ok && kv8_wait(smem_u32(p_full + 2 * mt + hf), (uint32_t)(i & 1), abort_flag, a.err);
             if (!ok) break;
             tc_fence_after();
             if (elect_one()) {
-#pragma unroll
-              for (int x = hf * PT / 32; x < (hf + 1) * PT / 32; ++x)
-                mma_ts(tmem + 2 * PT + mt * D, tmem + mt * PT + x * 8, v + ((x * 2048) >> 4), IO, (i || x) ? 1u : 0u);
+              uint64_t vd = v + hf * (4 * 2048 >> 4);
+              uint32_t pa = tmem + mt * PT + hf * 32, acc = i || hf ? 1u : 0u;
+#pragma unroll 1
+              for (int x = 0; x < 4; ++x, vd += 2048 >> 4, pa += 8, acc = 1) mma_ts(tmem + 2 * PT + mt * D, pa, vd, IO, acc);
               if (hf) {
                 tc_commit(smem_u32(o_done + mt));
                 if (mt == nmt - 1) tc_commit(smem_u32(v_empty + (i & 1)));

@@ -716,9 +716,9 @@ cudaError_t launch_mma(cudaStream_t st, const Kv8Attn& a, Plan& p, const CUtenso
     if (t <= 12) return launch_own<D, 3, 4, 2, 11, 1>(st, a, p, mk, mv);
     return launch_own<D, 4, 4, 2, 7, 1>(st, a, p, mk, mv);
   }
-  p.grid = std::min(KV8_MAX_CTAS, device_sm_count());
+  p.grid = 2 * std::min(KV8_MAX_CTAS / 2, device_sm_count());   // two workers a CTA
   p.min_tiles = 1;
-  p.pad = 3;
+  p.pad = 2;
   const cudaError_t e = kv8_launch_tc(st, a, p, mk, mv);
   return e != cudaSuccess ? e : launch_join<D>(st, a, p);
 }

@@ -155,10 +155,11 @@ __device__ __forceinline__ void fold(int n, At at, const float* ml, const float*
 // 8 finished values of one query vector; nothing seen, or a row that is padding or invalid: zeros.
 __device__ __forceinline__ void store8(const Kv8Attn& a, size_t at, int D, int c, bool live, float L, const float* o) {
   uint32_t w[4];
+  const bool none = !live || L == 0.f;
+  const float inv = 1.f / L;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const bool none = !live || L == 0.f;
-    const __nv_bfloat162 h = __floats2bfloat162_rn(none ? 0.f : o[2 * i] / L, none ? 0.f : o[2 * i + 1] / L);
+    const __nv_bfloat162 h = __floats2bfloat162_rn(none ? 0.f : o[2 * i] * inv, none ? 0.f : o[2 * i + 1] * inv);
     w[i] = *reinterpret_cast<const uint32_t*>(&h);
   }
   *reinterpret_cast<uint4*>((__nv_bfloat16*)a.out + at * D + c) = make_uint4(w[0], w[1], w[2], w[3]);

@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(Shape<D, NT, WN, WK, NS>::THREADS, CTAS)
   using Sh = Shape<D, NT, WN, WK, NS>;
   constexpr int NW = Sh::NW, NC = NW * 32;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sm = smem_raw + (-smem_u32(smem_raw) & 1023u);   // (not by pointer masks: accesses then lose the shared space)
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + Sh::OFF_BAR);
   uint64_t* empty = full + NS;
   uint64_t *q_full = empty + NS, *q_empty = q_full + 2;
@@ -499,12 +499,10 @@ __global__ void __launch_bounds__(Shape<D, NT, WN, WK, NS>::THREADS, CTAS)
             first = false;
           }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(empty + st));
+        warp_arrive(smem_u32(empty + st));
       }
 
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(q_empty + buf));
+      warp_arrive(smem_u32(q_empty + buf));
       // join the key groups: sums in the order of the groups
 #pragma unroll
       for (int x = 0; x < NT; ++x)

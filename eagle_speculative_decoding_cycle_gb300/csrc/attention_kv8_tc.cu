@@ -1,24 +1,25 @@
 // Attention of many query vectors over the 8-bit KV cache on the 5th-generation tensor cores (head_dim 128).
 //
-// A verify pass has tens of query vectors a KV head: per 128-key tile two products of a 128-row tile, which
-// tcgen05 takes with the cache's e4m3 codes as they lie - one TMA copy from HBM to the operand, no conversion. The other
-// operands are brought to 8 bits in parts that add up:
-//   S = (Q_hi + Q_lo) K^T     q scaled by a power of two, each part e4m3: together 8 significant bits, as many as bf16
-//                             has, down to 2^-11 of the vector's largest entry (below, a step of 2^-19 of it);
-//   O += (P_1 + P_2 + P_3) V  the weight times its value's exponent in fp16, cut into e5m2 parts (its upper byte, the
-//                             remainder's, the second remainder rounded): 9 significant bits, down to 2^-20 of the
-//                             largest weight; 5 exponent bits, so that the long tail of a row with one strong key keeps
-//                             its weight (e4m3 parts would flush it).
-// kind::f8f6f4 runs at twice the fp16 rate, so the five products cost 8 x 66 + 12 x 76 clocks a tile (measured), as much as
-// HBM takes to deliver its 33 KB; mma.sync took 3000 clocks for a quarter of the keys.
+// A verify pass has tens of query vectors a KV head: per 128-key tile two products of a 128-row tile.
+//   S = (Q_hi + Q_lo) K^T   kind::f8f6f4 on the cache's e4m3 codes as they lie: one TMA copy from HBM to the operand. q is
+//                           scaled by a power of two and cut into two e4m3 parts, together 8 significant bits, as many as
+//                           bf16 has, down to 2^-9 of the vector's largest entry (below, a step of 2^-17 of it).
+//   O += P V                kind::f16: the weights times their values' exponents as fp16 in TMEM; the codes are widened to
+//                           fp16 (exact) in shared memory, row by row in place, by the softmax threads while they wait
+//                           anyway. (Weights in 8-bit parts, e5m2 for their range, need three products of the codes as
+//                           they lie, but cutting them took twice the arithmetic of the whole softmax: 5000 clocks a
+//                           tile against HBM's 1500.)
+// A key's exponent multiplies its scores; a value's is added to its weights' logarithms, against a running reference E, and
+// taken out again of their sum; a tile whose values' exponents span more than fp16 bears goes through the value product
+// in several passes.
 //
-// One CTA an SM, 24 warps, two workers with a range of items each, so that one's softmax and epilogue run under the other's
+// One CTA an SM, 20 warps, two workers with a range of items each, so that one's softmax and epilogue run under the other's
 // products. A worker has eight softmax warps (two threads a query vector, 64 keys of a tile each: four warps a scheduler
-// hide each other's latencies; S is read twice from TMEM, for the maximum and for the weights, which keeps a thread at 80
-// registers, and each 32 columns of S are overwritten by the weights' parts of their keys), an MMA warp, a producer warp (TMA)
-// and two warps that prepare the next item's query vectors. TMEM: S and O, 128 columns each, of either worker. Exponents: a
-// key's multiplies its scores, a value's its weights, against a running reference E; a tile whose values' exponents span
-// more than fp16 bears goes through the value product in several passes.
+// hide each other's latencies, and prepare the next item's query vectors; S is read twice from TMEM, for the maximum and for the weights, which keeps a thread below 96
+// registers, and each 32 columns of S are overwritten by the weights of their keys), and a producer warp (TMA: keys two tiles
+// ahead, values one). One warp issues both workers' products, each
+// worker's value product and next S together: issued side by side they end together, and the two softmaxes then run in
+// step, with the tensor cores idle. TMEM: S and O, 128 columns each, of either worker.
 #include "kv8_split.cuh"
 #include "kernels.h"
 #include "tc_common.cuh"
@@ -30,20 +31,21 @@ namespace eagle {
 namespace {
 
 constexpr int TT = 128;                 // keys a tile, query vectors a block, dims
-constexpr int NSTAGE = 2;               // tiles in a worker's ring
+constexpr int NSTAGE = 2;               // key tiles in a worker's ring
 constexpr int OPB = TT * TT;            // bytes of an 8-bit operand tile
 constexpr int SOFT = 256;               // softmax threads of a worker
-constexpr int T_THREADS = 2 * SOFT + 256, T_ROWS_W = 2, T_FIRST_W = SOFT / 32 + T_ROWS_W;
-constexpr float T_LAZY = 4.f;           // how far (log2) a score may pass the reference maximum
-constexpr int T_SHIFT = 10;             // weights are held times 2^10: at most 2^(10 + 4 + 1), in fp16's and e5m2's range
-constexpr int TE_UP = 1, TE_DOWN = 8, TE_SPAN = 9;   // exponents around the reference; within one pass
+constexpr int SOFT_W = SOFT / 32;
+constexpr int T_THREADS = 2 * SOFT + 128;
+constexpr float T_LAZY = 8.f;           // how far (log2) a score may pass the reference maximum
+constexpr int T_SHIFT = 3;              // weights are held times 2^3: at most 2^(3 + 8 + 4), inside fp16
+constexpr int TE_UP = 4, TE_DOWN = 12, TE_SPAN = 14;   // exponents around the reference; within one pass
 
 // a worker's shared memory, [2]
-constexpr int TO_K = 0, TO_V = TO_K + 2 * NSTAGE * OPB, TO_Q = TO_V + 2 * NSTAGE * OPB;   // Q: [worker][high, low part]
+constexpr int TO_K = 0, TO_V = TO_K + 2 * NSTAGE * OPB, TO_Q = TO_V + 4 * OPB;   // V: fp16 [worker][half of the dims]; Q: [worker][part]
 constexpr int TO_EXP = TO_Q + 4 * OPB;                    // [worker][stage][K, V][128] exponent bytes
 constexpr int TO_KF = TO_EXP + 2 * NSTAGE * 256;          // [worker][tile parity][128] key factors
-constexpr int TO_VF = TO_KF + 2 * 2 * 512;                // [worker][tile parity][128] value factors
-constexpr int TO_COL = TO_VF + 2 * 2 * 512;               // [worker][item parity][128] (score factor, slot limit)
+constexpr int TO_VF = TO_KF + 2 * 2 * 512;                // [worker][tile parity][2][128] value exponents, inverse factors
+constexpr int TO_COL = TO_VF + 2 * 2 * 1024;              // [worker][item parity][128] (score factor, slot limit)
 constexpr int TO_MASK = TO_COL + 4 * TT * 8;              // [worker][item parity][128 rows][4] tree masks
 constexpr int TO_X = TO_MASK + 4 * TT * 32;               // [worker][tile parity][half][128] maxima; then sums
 constexpr int TO_RED = TO_X + 2 * 2 * 2 * TT * 4;         // [worker] small tables, below
@@ -56,9 +58,13 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
   return r != 0;
 }
-// kind::f8f6f4: A e4m3 (0) or e5m2 (1), B e4m3, fp32 sums, M = N = 128, B K-major or MN-major.
-constexpr uint32_t f8_idesc(int a_fmt, bool b_mn) {
-  return (1u << 4) | ((uint32_t)a_fmt << 7) | (b_mn ? (1u << 16) : 0u) | ((uint32_t)(TT >> 3) << 17) | ((uint32_t)(TT >> 4) << 24);
+// M = N = 128, fp32 sums, A K-major. kind::f8f6f4 with e4m3 operands, B K-major; kind::f16 with fp16 operands, B MN-major.
+constexpr uint32_t S_IDESC = (1u << 4) | ((uint32_t)(TT >> 3) << 17) | ((uint32_t)(TT >> 4) << 24);
+constexpr uint32_t O_IDESC = (1u << 4) | (1u << 16) | ((uint32_t)(TT >> 3) << 17) | ((uint32_t)(TT >> 4) << 24);
+// MN-major operand, 128-byte swizzle: 64 fp16 a row, one row per k, the next 64 dims OPB on.
+__device__ __forceinline__ uint64_t desc_mn(uint32_t saddr) {
+  return (uint64_t)((saddr & 0x3FFFF) >> 4) | ((uint64_t)(OPB >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) |
+         ((uint64_t)2 << 61);
 }
 __device__ __forceinline__ void mma8_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
@@ -66,72 +72,34 @@ __device__ __forceinline__ void mma8_ss(uint32_t d, uint64_t a, uint64_t b, uint
       "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
 }
-__device__ __forceinline__ void mma8_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void mma16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
 }
-__device__ __forceinline__ void ld32_async(uint32_t t, float* v) {
+// Whether an mbarrier phase has ended, without waiting.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
-        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
-        "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
-        "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
-      : "r"(t));
-}
-// Waits for this thread's TMEM loads; the values pass through, so that nothing of them is used before.
-__device__ __forceinline__ void wait_ld(float* v) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < 32; ++i) asm volatile("" : "+f"(v[i]));
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 __device__ __forceinline__ void st8(uint32_t t, const uint32_t* v) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(t), "r"(v[0]), "r"(v[1]),
                "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                : "memory");
 }
-typedef unsigned long long f32x2;
-__device__ __forceinline__ f32x2 two(float a, float b) {
-  f32x2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float2 each(f32x2 v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
-  f32x2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
-  f32x2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-__device__ __forceinline__ uint32_t h2_sub(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-// Two fp16 -> two e5m2, rounded, in the low 16 bits (first in the low byte).
-__device__ __forceinline__ uint32_t h2_e5m2(uint32_t h) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 t;\n\tcvt.rn.satfinite.e5m2x2.f16x2 t, %1;\n\tcvt.u32.u16 %0, t;\n\t}" : "=r"(r) : "r"(h));
-  return r;
-}
-__device__ __forceinline__ uint32_t f32x2_f16x2(float2 v) {
-  const __half2 h = __floats2half2_rn(v.x, v.y);
+__device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
@@ -144,27 +112,19 @@ __device__ __forceinline__ float2 e4m3x2_f32(uint32_t two_codes) {
   e4m3x4_f16(two_codes, lo, hi);
   return __half22float2(*reinterpret_cast<const __half2*>(&lo));
 }
-// A bounded wait taken by lane 0 for its warp: tcgen05.ld / st are collective, so every lane takes the same branch.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err) {
-  int ok = 0;
-  if ((threadIdx.x & 31) == 0) ok = kv8_wait(bar, parity, abort_flag, err) ? 1 : 0;
-  ok = __shfl_sync(0xffffffffu, ok, 0);
-  __syncwarp();
-  return ok != 0;
-}
-
 __global__ void __launch_bounds__(T_THREADS, 1)
     kv8_attn_tc_k(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Kv8Attn a,
                   const Plan p) {
   extern __shared__ uint8_t tc_smem_raw[];
-  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(tc_smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sm = tc_smem_raw + (-smem_u32(tc_smem_raw) & 1023u);   // (not by pointer masks: accesses then lose the shared space)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int wk = warp < 16 ? warp >> 3 : warp < 20 ? warp & 1 : (warp - 20) >> 1;   // this warp's worker
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + TO_BAR + 256);
+  const int wk = warp < 16 ? warp >> 3 : warp & 1;   // this warp's worker (16: MMA of both; 18, 19: producers)
+  uint64_t* drain = reinterpret_cast<uint64_t*>(sm + TO_BAR + 256);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + TO_BAR + wk * 128);
-  uint64_t *kv_full = bars, *kv_empty = bars + 2, *q_full = bars + 4, *q_free = bars + 5, *s_full = bars + 6, *p_full = bars + 7,
-           *o_done = bars + 8, *o_free = bars + 9, *q_first = bars + 10, *drain = bars + 11;
+  uint64_t *k_full = bars, *k_empty = bars + 2, *v_full = bars + 4, *v_empty = bars + 5, *q_full = bars + 6,
+           *s_full = bars + 8, *p_full = bars + 9, *o_done = bars + 10, *o_free = bars + 11;
   int* red = reinterpret_cast<int*>(sm + TO_RED + wk * 512);
   int* r_hi = red;                                            // [tile parity][4 warps] largest exponent
   int* r_lo = red + 8;                                        // smallest
@@ -178,18 +138,20 @@ __global__ void __launch_bounds__(T_THREADS, 1)
   if (warp == 16 || warp == 17) {
     if (lane == 0) {
       for (int i = 0; i < NSTAGE; ++i) {
-        mbar_init(smem_u32(kv_full + i), 33);   // the codes' bytes, and each producer lane's exponent copies
-        mbar_init(smem_u32(kv_empty + i), 1);
+        mbar_init(smem_u32(k_full + i), 33);   // the codes' bytes, and each producer lane's exponent copies
+        mbar_init(smem_u32(k_empty + i), 1);
       }
-      mbar_init(smem_u32(q_full), T_ROWS_W);
-      mbar_init(smem_u32(q_free), 1);
+      mbar_init(smem_u32(v_full), 1);
+      mbar_init(smem_u32(v_empty), 1);
+      mbar_init(smem_u32(q_full), SOFT_W);
       mbar_init(smem_u32(s_full), 1);
-      mbar_init(smem_u32(p_full), SOFT);
+      mbar_init(smem_u32(p_full), SOFT_W);
       mbar_init(smem_u32(o_done), 1);
-      mbar_init(smem_u32(o_free), SOFT);
-      mbar_init(smem_u32(q_first), T_FIRST_W);
-      mbar_init(smem_u32(drain), 1);
-      if (warp == 16) *abort_flag = 0;
+      mbar_init(smem_u32(o_free), SOFT_W);
+      if (warp == 16) {
+        mbar_init(smem_u32(drain), 1);
+        *abort_flag = 0;
+      }
       fence_mbar_init();
     }
     __syncwarp();
@@ -211,8 +173,11 @@ __global__ void __launch_bounds__(T_THREADS, 1)
   Walk k;
   bool more = me < share.ctas && k.begin(range);
 
-  // The query vectors of an item, e4m3 in two parts, and what each sees. By `warps` warps, this being number sw.
-  auto prepare = [&](int item, int sw, int warps) {
+  // The query vectors of an item, e4m3 in two parts, and what each sees. By a worker's softmax warps; the last S of the
+  // item before is done.
+  auto prepare = [&](const Walk& k, int item) {
+    constexpr int warps = SOFT_W;
+    const int sw = warp & 7;
     const int gi = k.gi, h = k.h, buf = item & 1, seq = s_seq[gi];
     const int sidx = (p.g0 + gi) / p.nb, rb = (p.g0 + gi) - sidx * p.nb;
     const int r0 = sidx * a.rows_per_seq + rb * p.RB;
@@ -222,8 +187,6 @@ __global__ void __launch_bounds__(T_THREADS, 1)
     uint8_t* q_hi = sm + TO_Q + wk * 2 * OPB;
     float2* cols = reinterpret_cast<float2*>(sm + TO_COL) + (wk * 2 + buf) * TT;
     uint64_t* masks = reinterpret_cast<uint64_t*>(sm + TO_MASK) + (wk * 2 + buf) * TT * 4;
-    // the last S of the item before is done: the softmax threads are then at that item, and past the one before it
-    if (item) kv8_wait(smem_u32(q_free), (uint32_t)((item - 1) & 1), abort_flag, a.err);
     if (a.mode == 1)
       for (int x = sw * 32 + lane; x < (r1 - r0) * 4; x += warps * 32) {
         const int r = r0 + x / 4, w = x & 3;
@@ -300,17 +263,16 @@ __global__ void __launch_bounds__(T_THREADS, 1)
     fullvis = __reduce_min_sync(0xffffffffu, fullvis);
     if (lane == 0) s_fullvis[buf * 16 + sw] = fullvis;
     fence_proxy_async_all();
-    __syncwarp();
+    warp_arrive(smem_u32(q_full));
   };
 
   if (warp < 16) {
-    if (more) prepare(0, warp & 7, T_FIRST_W);
-    if (lane == 0) mbar_arrive(smem_u32(q_first));
+    if (more) prepare(k, 0);
     const int hf = (warp >> 2) & 1, r = threadIdx.x & 127, c0 = hf * 64;   // half of a tile's keys and of O's columns; row
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tS0 + lane_off + c0, tO = tO0 + lane_off + c0;
     int i = 0, passes = 0;       // tiles of the range; value passes
-    for (int item = 0; more; ++item, more = k.next(range)) {
+    for (int item = 0; more; ++item) {
       const int gi = k.gi, h = k.h, buf = item & 1;
       const int seq = s_seq[gi], limit = s_lim[gi];
       const int sidx = (p.g0 + gi) / p.nb, rb = (p.g0 + gi) - sidx * p.nb;
@@ -318,10 +280,10 @@ __global__ void __launch_bounds__(T_THREADS, 1)
       const int r1 = min(min(r0 + p.RB, (sidx + 1) * a.rows_per_seq), a.R);
       const int nqv = (r1 - r0) * p.G;
       const int ctx = a.mode == 1 && seq >= 0 ? a.ctx_len[seq] : 0;
-      if (item) kv8_wait(smem_u32(q_full), (uint32_t)((item - 1) & 1), abort_flag, a.err);
-      else kv8_wait(smem_u32(q_first), 0, abort_flag, a.err);
+      kv8_wait(smem_u32(q_full), (uint32_t)(item & 1), abort_flag, a.err);
       int fullvis = s_fullvis[buf * 16];
-      for (int w = 1; w < (item ? T_ROWS_W : T_FIRST_W); ++w) fullvis = min(fullvis, s_fullvis[buf * 16 + w]);
+#pragma unroll 1
+      for (int w = 1; w < SOFT_W; ++w) fullvis = min(fullvis, s_fullvis[buf * 16 + w]);
       const float2 col = reinterpret_cast<const float2*>(sm + TO_COL)[(wk * 2 + buf) * TT + r];
       const float qf = r < nqv ? col.x : 0.f;   // a row past the block's never raises its maximum
       const int klim = __float_as_int(col.y);
@@ -331,7 +293,7 @@ __global__ void __launch_bounds__(T_THREADS, 1)
       int E = 0;                 // reference exponent byte
       for (int t = k.t0; t < k.t1; ++t, ++i) {
         const int st = i % NSTAGE, key0 = t * TT, tp = i & 1;
-        kv8_wait(smem_u32(kv_full + st), (uint32_t)((i / NSTAGE) & 1), abort_flag, a.err);
+        kv8_wait(smem_u32(k_full + st), (uint32_t)((i / NSTAGE) & 1), abort_flag, a.err);
         const uint8_t* s_exp = sm + TO_EXP + (wk * NSTAGE + st) * 256;
         const bool masked = key0 + TT > fullvis || limit <= key0;
         uint32_t vis[2] = {0xffffffffu, 0xffffffffu};   // this thread's keys that its row sees
@@ -353,18 +315,14 @@ __global__ void __launch_bounds__(T_THREADS, 1)
             if (lane == 0) r_seen[(warp & 7) * 2 + w] = any;
           }
           named_bar_sync(1 + wk, SOFT);
+          // a slot that no row sees may hold anything: its codes become zeros, 0 * NaN must not come of it
           const uint32_t* any = r_seen + (r >> 6) * 8 + ((r >> 5) & 1);
           seen = ((any[0] | any[2] | any[4] | any[6]) >> (r & 31)) & 1u;
-          if (!seen && hf) {   // a slot that no row sees may hold anything: 0 * NaN must not come of it
-            uint4* z = reinterpret_cast<uint4*>(sm + TO_V + (wk * NSTAGE + st) * OPB + r * TT);
-#pragma unroll
-            for (int x = 0; x < 8; ++x) z[x] = make_uint4(0, 0, 0, 0);
-          }
-          fence_proxy_async_all();
         }
         // exponents of the tile's keys: the first half's threads take the keys', the second's the values'
         float* s_kf = reinterpret_cast<float*>(sm + TO_KF) + (wk * 2 + tp) * TT;
-        float* s_vf = reinterpret_cast<float*>(sm + TO_VF) + (wk * 2 + tp) * TT;
+        float* s_va = reinterpret_cast<float*>(sm + TO_VF) + (wk * 2 + tp) * 2 * TT;   // log2 of a weight's factor
+        float* s_vi = s_va + TT;                                                      // the factor's inverse
         const int vbyte = s_exp[TT + r];
         const bool counts = seen && vbyte != KV8_BAD;
         if (!hf) {
@@ -384,35 +342,35 @@ __global__ void __launch_bounds__(T_THREADS, 1)
         const bool narrow = hi - lo_all <= TE_SPAN;   // one pass does
         float keep[64];                               // the scores, for further passes (local memory, rarely)
 
-        warp_wait(smem_u32(s_full), (uint32_t)(i & 1), abort_flag, a.err);
+        kv8_wait(smem_u32(s_full), (uint32_t)(i & 1), abort_flag, a.err);
         tc_fence_after();
-        // 32 scores in units of q's and the cache's scale
-        auto scores = [&](int c, float* s) {
-          ld32_async(tS + c, s);
-          wait_ld(s);
+        float mx = -INFINITY;
+#pragma unroll 1
+        for (int c = 0; c < 64; c += 16) {   // few live values: a spill goes to L2, next to 220 KB of shared memory
+          float s[16];
+          tmem_ld16(tS + c, s);
+          if (!narrow)   // as they come
+            for (int j = 0; j < 16; ++j) keep[c + j] = s[j];
 #pragma unroll
-          for (int j = 0; j < 32; j += 4) {
+          for (int j = 0; j < 16; j += 4) {
             const float4 f = *reinterpret_cast<const float4*>(s_kf + c0 + c + j);
-            const float2 u = each(mul2(two(s[j], s[j + 1]), two(f.x, f.y))), v = each(mul2(two(s[j + 2], s[j + 3]), two(f.z, f.w)));
-            s[j] = u.x; s[j + 1] = u.y; s[j + 2] = v.x; s[j + 3] = v.y;
+            s[j] *= f.x; s[j + 1] *= f.y; s[j + 2] *= f.z; s[j + 3] *= f.w;
           }
           if (masked)
 #pragma unroll
-            for (int j = 0; j < 32; ++j) s[j] = (vis[c >> 5] >> j) & 1u ? s[j] : -INFINITY;
-        };
-        float mx = -INFINITY;
-#pragma unroll 1
-        for (int c = 0; c < 64; c += 32) {
-          float s[32];
-          scores(c, s);
+            for (int j = 0; j < 16; ++j) s[j] = (vis[c >> 5] >> ((c & 16) + j)) & 1u ? s[j] : -INFINITY;
 #pragma unroll
-          for (int j = 0; j < 32; j += 8)
+          for (int j = 0; j < 16; j += 8)
             mx = max3(mx, max3(s[j], s[j + 1], s[j + 2]), max3(max3(s[j + 3], s[j + 4], s[j + 5]), s[j + 6], s[j + 7]));
-          if (!narrow)
-            for (int j = 0; j < 32; ++j) keep[c + j] = s[j];
         }
         float* x_max = reinterpret_cast<float*>(sm + TO_X) + (wk * 2 + tp) * 2 * TT;
         x_max[hf * TT + r] = mx;
+        // this thread's half of the codes of value r, which lie where the second half's fp16 of the same value go
+        kv8_wait(smem_u32(v_full), (uint32_t)(i & 1), abort_flag, a.err);
+        uint8_t* s_v = sm + TO_V + wk * 2 * OPB + r * TT;
+        uint4 codes[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) codes[c] = *reinterpret_cast<const uint4*>(s_v + OPB + (((hf * 4 + c) ^ (r & 7)) << 4));
         bool first = true;
         float corr = 1.f;
         while (true) {
@@ -423,10 +381,12 @@ __global__ void __launch_bounds__(T_THREADS, 1)
             if (E) unit = pow2i(E - hi);
             E = hi;
           }
-          // not finite: NaN where seen; outside this pass's exponents, or seen by nobody: 0
-          if (hf)
-            s_vf[r] = !seen ? 0.f : vbyte == KV8_BAD ? (first ? kv8_pow2(vbyte) : 0.f)
-                                                     : vbyte >= lo && vbyte <= hi ? pow2i(vbyte - E + T_SHIFT) : 0.f;
+          // not finite: NaN where seen; outside this pass's exponents, or seen by nobody: no weight
+          if (hf) {
+            const bool in = seen && vbyte != KV8_BAD && vbyte >= lo && vbyte <= hi;
+            s_va[r] = in ? (float)(vbyte - E + T_SHIFT) : seen && vbyte == KV8_BAD && first ? kv8_pow2(vbyte) : -INFINITY;
+            s_vi[r] = in ? pow2i(E - vbyte - T_SHIFT) : 0.f;
+          }
           named_bar_sync(1 + wk, SOFT);
           if (first) {
             mx = fmaxf(x_max[r], x_max[TT + r]);
@@ -435,61 +395,77 @@ __global__ void __launch_bounds__(T_THREADS, 1)
               m = mx;
               l *= corr;
             }
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {   // 16 codes to two 16-byte parts of fp16
+              const uint32_t w[4] = {codes[c].x, codes[c].y, codes[c].z, codes[c].w};
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                uint4 f;
+                e4m3x4_f16(seen ? w[2 * j] : 0u, f.x, f.y);
+                e4m3x4_f16(seen ? w[2 * j + 1] : 0u, f.z, f.w);
+                *reinterpret_cast<uint4*>(s_v + hf * OPB + (((2 * c + j) ^ (r & 7)) << 4)) = f;
+              }
+            }
+            fence_proxy_async_all();
           }
           const float scale_o = first ? corr * unit : unit;
           const bool begun = t > k.t0 || !first;      // O holds something
           // a pass before this one must be out of P, and O complete before it is rescaled
           if (begun && (!first || __any_sync(0xffffffffu, scale_o != 1.f))) {
-            warp_wait(smem_u32(o_done), (uint32_t)((passes - 1) & 1), abort_flag, a.err);
+            kv8_wait(smem_u32(o_done), (uint32_t)((passes - 1) & 1), abort_flag, a.err);
             tc_fence_after();
             if (__any_sync(0xffffffffu, scale_o != 1.f)) {
 #pragma unroll 1
-              for (int c = 0; c < 64; c += 32) {
-                float o[32];
-                ld32_async(tO + c, o);
-                wait_ld(o);
+              for (int c = 0; c < 64; c += 16) {
+                float o[16];
+                tmem_ld16(tO + c, o);
 #pragma unroll
-                for (int j = 0; j < 32; ++j) o[j] *= scale_o;
+                for (int j = 0; j < 16; ++j) o[j] *= scale_o;
                 tmem_st16(tO + c, o);
-                tmem_st16(tO + c + 16, o + 16);
               }
             }
           }
           // weights; the difference comes first: it is exact where it matters, whatever the size of the scores
           const float base = m == -INFINITY ? 0.f : -m;
-          const f32x2 nm = two(base, base), q2 = two(qf, qf);
-          f32x2 sum = two(0.f, 0.f);
+          // (scalar arithmetic: pairs of fp32 cost as many moves into aligned registers as they save)
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
-          for (int c = 0; c < 64; c += 32) {
-            float s[32];
+          for (int c = 0; c < 64; c += 16) {
+            float s[16];
             if (first) {
-              scores(c, s);
+              tmem_ld16(tS + c, s);
             } else {
-              for (int j = 0; j < 32; ++j) s[j] = keep[c + j];
+              for (int j = 0; j < 16; ++j) s[j] = keep[c + j];
             }
-            uint32_t p1[8], p2[8], p3[8];
 #pragma unroll
-            for (int j = 0; j < 32; j += 4) {
-              float2 x = each(mul2(add2(two(s[j], s[j + 1]), nm), q2)), y = each(mul2(add2(two(s[j + 2], s[j + 3]), nm), q2));
-              x = make_float2(ex2(x.x), ex2(x.y));
-              y = make_float2(ex2(y.x), ex2(y.y));
-              sum = add2(sum, add2(two(x.x, x.y), two(y.x, y.y)));
-              const float4 f = *reinterpret_cast<const float4*>(s_vf + c0 + c + j);
-              const uint32_t u = f32x2_f16x2(each(mul2(two(x.x, x.y), two(f.x, f.y))));
-              const uint32_t v = f32x2_f16x2(each(mul2(two(y.x, y.y), two(f.z, f.w))));
-              const uint32_t u2 = h2_sub(u, u & 0xff00ff00u), v2 = h2_sub(v, v & 0xff00ff00u);
-              p1[j / 4] = __byte_perm(u, v, 0x7531);          // upper bytes: the fp16 cut to e5m2
-              p2[j / 4] = __byte_perm(u2, v2, 0x7531);
-              p3[j / 4] = __byte_perm(h2_e5m2(h2_sub(u2, u2 & 0xff00ff00u)), h2_e5m2(h2_sub(v2, v2 & 0xff00ff00u)), 0x5410);
+            for (int j = 0; j < 16; j += 4) {
+              const float4 f = *reinterpret_cast<const float4*>(s_kf + c0 + c + j);
+              const float4 v = *reinterpret_cast<const float4*>(s_va + c0 + c + j);
+              // (a key's factor is a power of two: the product is exact)
+              s[j] = ex2(fmaf(fmaf(s[j], f.x, base), qf, v.x));
+              s[j + 1] = ex2(fmaf(fmaf(s[j + 1], f.y, base), qf, v.y));
+              s[j + 2] = ex2(fmaf(fmaf(s[j + 2], f.z, base), qf, v.z));
+              s[j + 3] = ex2(fmaf(fmaf(s[j + 3], f.w, base), qf, v.w));
             }
-            st8(tS + c, p1);        // the parts of 32 keys over the first 24 of their 32 score columns
-            st8(tS + c + 8, p2);
-            st8(tS + c + 16, p3);
+            if (masked) {   // last: what a hidden key holds may be NaN
+              const uint32_t see = vis[c >> 5] >> (c & 16);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) s[j] = (see >> j) & 1u ? s[j] : 0.f;
+            }
+            uint32_t w[8];
+#pragma unroll
+            for (int j = 0; j < 16; j += 4) {
+              const float4 u = *reinterpret_cast<const float4*>(s_vi + c0 + c + j);
+              sum[0] = fmaf(s[j], u.x, sum[0]);
+              sum[1] = fmaf(s[j + 1], u.y, sum[1]);
+              sum[2] = fmaf(s[j + 2], u.z, sum[2]);
+              sum[3] = fmaf(s[j + 3], u.w, sum[3]);
+              w[j / 2] = half2_of(s[j], s[j + 1]);
+              w[j / 2 + 1] = half2_of(s[j + 2], s[j + 3]);
+            }
+            st8(tS + (c & 32) + (c & 16) / 2, w);   // the weights of 32 keys over the first 16 of their 32 score columns
           }
-          if (first) {
-            const float2 u = each(sum);
-            l += u.x + u.y;
-          }
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
           tmem_wait_st();
           if (threadIdx.x % SOFT == 0) *s_more = !one;
           int next_hi = 0;
@@ -501,7 +477,7 @@ __global__ void __launch_bounds__(T_THREADS, 1)
             named_bar_sync(1 + wk, SOFT);
           }
           tc_fence_before();
-          mbar_arrive(smem_u32(p_full));
+          warp_arrive(smem_u32(p_full));
           ++passes;
           if (one) break;
           hi = next_hi;      // > 0: lo_all itself is still to come
@@ -509,19 +485,23 @@ __global__ void __launch_bounds__(T_THREADS, 1)
         }
       }
 
+      // the next item's query vectors, so that its first S runs under this item's end
+      const Walk done = k;
+      more = k.next(range);
+      if (more) prepare(k, item + 1);
       // the item's sum: l of both halves; this thread's 64 dims of its query vector
       float* x_l = reinterpret_cast<float*>(sm + TO_X) + (wk * 2 + (i & 1)) * 2 * TT;   // the parity that the last tile did not use
       x_l[hf * TT + r] = l;
-      warp_wait(smem_u32(o_done), (uint32_t)((passes - 1) & 1), abort_flag, a.err);
+      kv8_wait(smem_u32(o_done), (uint32_t)((passes - 1) & 1), abort_flag, a.err);
       tc_fence_after();
       named_bar_sync(1 + wk, SOFT);
       float L = x_l[r] + x_l[TT + r], top = m * qf;
-      const bool whole = k.t0 == 0 && k.t1 == k.nt;
-      if (threadIdx.x % SOFT == 0 && k.t0 == 0 && k.t1 < k.nt)
-        p.cut[me] = make_int4(gi, h, (int)share.cta_of(k.base + pad + k.nt - 1), 0);
+      const bool whole = done.t0 == 0 && done.t1 == done.nt;
+      if (threadIdx.x % SOFT == 0 && done.t0 == 0 && !whole)
+        p.cut[me] = make_int4(gi, h, (int)share.cta_of(done.base + pad + done.nt - 1), 0);
       const int in = r < nqv ? (int)(r * p.G_inv >> 16) : 0, row = r0 + in;
       const size_t at = (size_t)row * a.nq + h * p.G + (r < nqv ? r - in * p.G : 0), stride = (size_t)a.R * a.nq;
-      const size_t slot = (size_t)(2 * me + (k.t0 == 0 ? 1 : 0)) * p.qv_pad + r;
+      const size_t slot = (size_t)(2 * me + (done.t0 == 0 ? 1 : 0)) * p.qv_pad + r;
       const int n_prefix = whole ? p.n_prefix : 0;
       const float own_top = top;
       for (int s = 0; s < n_prefix; ++s) top = fmaxf(top, p.pp_ml[2 * (s * stride + at)]);
@@ -536,109 +516,158 @@ __global__ void __launch_bounds__(T_THREADS, 1)
       const float inv = whole ? (live && L != 0.f ? 1.f / L : 0.f) : 1.f;
       const float unit = own * pow2i(E ? E - KV8_BIAS - T_SHIFT : 0);
 #pragma unroll 1
-      for (int c = 0; c < 64; c += 32) {
+      for (int c = 0; c < 64; c += 16) {
         __syncwarp();
-        float o[32];
-        ld32_async(tO + c, o);
-        wait_ld(o);
-        if (c == 32) {
+        float o[16];
+        tmem_ld16(tO + c, o);
+        if (c == 48) {
           tc_fence_before();
-          mbar_arrive(smem_u32(o_free));
+          warp_arrive(smem_u32(o_free));
         }
         if (r >= nqv) continue;
 #pragma unroll
-        for (int j = 0; j < 32; ++j) o[j] *= unit;
+        for (int j = 0; j < 16; ++j) o[j] *= unit;
         for (int s = 0; s < n_prefix; ++s) {
           const float g = ex2(p.pp_ml[2 * (s * stride + at)] - tb);
           const float4* x = reinterpret_cast<const float4*>(p.pp_o + (s * stride + at) * TT + c0 + c);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
+          for (int j = 0; j < 4; ++j) {
             const float4 y = x[j];
             o[4 * j] = fmaf(y.x, g, o[4 * j]); o[4 * j + 1] = fmaf(y.y, g, o[4 * j + 1]);
             o[4 * j + 2] = fmaf(y.z, g, o[4 * j + 2]); o[4 * j + 3] = fmaf(y.w, g, o[4 * j + 3]);
           }
         }
         if (whole) {
-          uint32_t w[16];
+          uint32_t w[8];
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
+          for (int j = 0; j < 8; ++j) {
             const __nv_bfloat162 b = inv == 0.f ? __floats2bfloat162_rn(0.f, 0.f) : __floats2bfloat162_rn(o[2 * j] * inv, o[2 * j + 1] * inv);
             w[j] = *reinterpret_cast<const uint32_t*>(&b);
           }
           uint4* dst = reinterpret_cast<uint4*>((__nv_bfloat16*)a.out + at * TT + c0 + c);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) dst[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+          dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+          dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
         } else {
           float4* dst = reinterpret_cast<float4*>(p.part_o + slot * TT + c0 + c);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) dst[j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+          for (int j = 0; j < 4; ++j) dst[j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
           if (hf == 0 && c == 0) *reinterpret_cast<float2*>(p.part_ml + 2 * slot) = make_float2(top, L);
         }
       }
     }
-  } else if (warp < 18) {
-    // ---- MMA: S of a tile, then its value product; the other worker's run under this one's softmax ----
-    constexpr uint32_t IS = f8_idesc(0, false), IO = f8_idesc(1, true);
-    const uint64_t dq = sdesc_sw128(smem_u32(sm + TO_Q + wk * 2 * OPB)), dk = sdesc_sw128(smem_u32(sm + TO_K + wk * NSTAGE * OPB)),
-                   dv = sdesc_sw128(smem_u32(sm + TO_V + wk * NSTAGE * OPB));
-    int i = 0, passes = 0;
+  } else if (warp == 16) {
+    // ---- MMA, both workers: whichever is ready next gets its value product and its next S ----
+    struct Stream {
+      Walk k;
+      bool more, want_s;       // a tile is left; its S is still to come
+      int item, t, i, passes, pass;
+    } w[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const uint32_t id = x * gridDim.x + blockIdx.x;
+      Stream& q = w[x];
+      const Range rx{s_pref, pad, a.c.nkv, p.groups, share.start(id), share.start(id + 1)};
+      q.more = id < share.ctas && q.k.begin(rx);
+      q.want_s = true;
+      q.item = q.i = q.passes = q.pass = 0;
+      q.t = q.more ? q.k.t0 : 0;
+    }
     bool ok = true;
-    for (int item = 0; more && ok; ++item, more = k.next(range)) {
-      ok = item ? kv8_wait(smem_u32(q_full), (uint32_t)((item - 1) & 1), abort_flag, a.err)
-                : kv8_wait(smem_u32(q_first), 0, abort_flag, a.err);
-      for (int t = k.t0; ok && t < k.t1; ++t, ++i) {
-        const int st = i % NSTAGE;
-        ok = kv8_wait(smem_u32(kv_full + st), (uint32_t)((i / NSTAGE) & 1), abort_flag, a.err);
-        if (!ok) break;
-        tc_fence_after();
-        if (elect_one()) {
-          // rolled loops: unrolled, their operands are hoisted out of the tile loop and spilled (2500 clocks an S)
-          uint64_t q = dq;
-          uint32_t acc = 0;
-#pragma unroll 1
-          for (int part = 0; part < 2; ++part, q += (OPB >> 4) - 8) {   // high part, low part
-            uint64_t kd = dk + st * (OPB >> 4);
-#pragma unroll 1
-            for (int x = 0; x < 4; ++x, q += 2, kd += 2, acc = 1) mma8_ss(tS0, q, kd, IS, acc);
-          }
-          tc_commit(smem_u32(s_full));
-          if (t + 1 == k.t1) tc_commit(smem_u32(q_free));
-        }
-        __syncwarp();
-        if (t == k.t0 && item) ok = kv8_wait(smem_u32(o_free), (uint32_t)((item - 1) & 1), abort_flag, a.err);
-        bool again = true;
-        for (int pass = 0; ok && again; ++pass) {
-          ok = kv8_wait(smem_u32(p_full), (uint32_t)(passes & 1), abort_flag, a.err);
-          if (!ok) break;
-          again = *s_more != 0;
+    uint32_t idle = 0;
+    uint64_t since = 0;
+    auto ready = [&](uint32_t bar, uint32_t parity) {   // as one lane sees it
+      return __shfl_sync(0xffffffffu, lane == 0 && mbar_test(bar, parity) ? 1 : 0, 0) != 0;
+    };
+    while (ok && (w[0].more || w[1].more)) {
+      bool moved = false;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        Stream& q = w[x];
+        if (!q.more) continue;
+        uint64_t* b = reinterpret_cast<uint64_t*>(sm + TO_BAR + x * 128);
+        const uint32_t tS = *tmem_slot + x * TT, tO = tS + 2 * TT;
+        const bool begins = q.t == q.k.t0;
+        if (!q.want_s) {
+          // P V: the weights are there, and the last item's O has been read
+          if (!ready(smem_u32(b + 9), (uint32_t)(q.passes & 1))) continue;
+          if (begins && q.pass == 0 && q.item && !ready(smem_u32(b + 11), (uint32_t)((q.item - 1) & 1))) continue;
+          const bool again = *reinterpret_cast<volatile int*>(sm + TO_RED + x * 512 + 160) != 0;
           tc_fence_after();
           if (elect_one()) {
-            uint32_t acc = t == k.t0 && pass == 0 ? 0u : 1u;   // the first product of an item begins O
+            uint64_t v = desc_mn(smem_u32(sm + TO_V + x * 2 * OPB));
+            uint32_t acc = begins && q.pass == 0 ? 0u : 1u;   // the first product of an item begins O
+            // rolled loops: unrolled, their operands are hoisted out of the tile loop and spilled (2500 clocks an S)
 #pragma unroll 1
-            for (int part = 0; part < 3; ++part) {
-              uint64_t v = dv + st * (OPB >> 4);
-              uint32_t pa = tS0 + part * 8;
-#pragma unroll 1
-              for (int x = 0; x < 4; ++x, pa += 32, v += 32 * TT >> 4, acc = 1) mma8_ts(tO0, pa, v, IO, acc);
-            }
-            tc_commit(smem_u32(o_done));
-            if (!again) tc_commit(smem_u32(kv_empty + st));
+            for (int y = 0; y < 8; ++y, v += 16 * TT >> 4, acc = 1) mma16_ts(tO, tS + (y >> 1) * 32 + (y & 1) * 8, v, O_IDESC, acc);
+            tc_commit(smem_u32(b + 10));
+            if (!again) tc_commit(smem_u32(b + 5));
           }
           __syncwarp();
-          ++passes;
+          moved = true;
+          ++q.passes;
+          ++q.pass;
+          if (again) continue;
+          ++q.i;
+          q.pass = 0;
+          q.want_s = true;
+          if (++q.t == q.k.t1) {
+            const uint32_t id = x * gridDim.x + blockIdx.x;
+            q.more = q.k.next(Range{s_pref, pad, a.c.nkv, p.groups, share.start(id), share.start(id + 1)});
+            ++q.item;
+            q.t = q.k.t0;
+          }
         }
+        // S: the query vectors and the keys are there (its columns are free: P V of the tile before comes first)
+        if (!q.more) continue;
+        const bool first = q.t == q.k.t0;
+        const int sn = q.i % NSTAGE;
+        if (first && !ready(smem_u32(b + 6), (uint32_t)(q.item & 1))) continue;
+        if (!ready(smem_u32(b + sn), (uint32_t)((q.i / NSTAGE) & 1))) continue;
+        tc_fence_after();
+        if (elect_one()) {
+          uint64_t qd = sdesc_sw128(smem_u32(sm + TO_Q + x * 2 * OPB));
+          uint32_t acc = 0;
+#pragma unroll 1
+          for (int part = 0; part < 2; ++part, qd += (OPB >> 4) - 8) {   // high part, low part
+            uint64_t kd = sdesc_sw128(smem_u32(sm + TO_K + (x * NSTAGE + sn) * OPB));
+#pragma unroll 1
+            for (int y = 0; y < 4; ++y, qd += 2, kd += 2, acc = 1) mma8_ss(tS, qd, kd, S_IDESC, acc);
+          }
+          tc_commit(smem_u32(b + 8));
+          tc_commit(smem_u32(b + sn + 2));
+        }
+        __syncwarp();
+        moved = true;
+        q.want_s = false;
+      }
+      if (moved) {
+        idle = 0;
+        since = 0;
+        continue;
+      }
+      __nanosleep(32);   // spinning at full rate would take the issue slots of the softmax warps next to this one
+      if ((++idle & 255u) == 0) {   // bounded, as every wait here
+        if (*abort_flag) ok = false;
+        const uint64_t now = globaltimer();
+        if (!since) since = now;
+        if (now - since > EAGLE_WAIT_LIMIT_NS) {
+          *abort_flag = 1;
+          latch_error(a.err, DEVERR_MBAR_TIMEOUT);
+          ok = false;
+        }
+        ok = __all_sync(0xffffffffu, ok);
       }
     }
     if (!ok) {   // products in flight end before the CTA frees its TMEM
       if (elect_one()) tc_commit(smem_u32(drain));
       kv8_wait(smem_u32(drain), 0, abort_flag, a.err, false);
     }
-  } else if (warp < 20) {
+  } else if (warp == 18 || warp == 19) {
     // ---- producer. Lanes 0-7 look after the eight 16-slot parts of a tile's keys, lanes 8-15 of its values ----
     const int box = a.c.table ? min(TT, 1 << a.c.block_log2) : TT, per = box / 16, part = lane & 7;
     const uint8_t* exps = (lane & 8) ? a.c.ve : a.c.ke;
     const uint64_t pol = l2_policy_evict_first();
-    int i = 0;
+    int i = 0, nk = 0, nv = 0;
     bool ok = true;
     auto where = [&](const Walk& w, int t) -> long long {   // this lane's part of a tile; -1: none, or not assigned
       const int slot = t * TT + part * 16;
@@ -653,38 +682,38 @@ __global__ void __launch_bounds__(T_THREADS, 1)
         const int st = i % NSTAGE, parts = max(0, min(8, (limit - t * TT + 15) / 16));
         if (lane < parts && vec < 0) latch_error(a.err, DEVERR_BOUNDS);   // not assigned: unspecified keys
         const int at = (int)max(vec, 0ll);
-        if (i >= NSTAGE && !kv8_wait(smem_u32(kv_empty + st), (uint32_t)((i / NSTAGE - 1) & 1), abort_flag, a.err)) ok = false;
+        if (i >= NSTAGE && !kv8_wait(smem_u32(k_empty + st), (uint32_t)((i / NSTAGE - 1) & 1), abort_flag, a.err)) ok = false;
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        const uint32_t bar = smem_u32(kv_full + st), kd = smem_u32(sm + TO_K + (wk * NSTAGE + st) * OPB),
-                       vd = smem_u32(sm + TO_V + (wk * NSTAGE + st) * OPB);
+        const uint32_t bar = smem_u32(k_full + st), kd = smem_u32(sm + TO_K + (wk * NSTAGE + st) * OPB),
+                       vd = smem_u32(sm + TO_V + wk * 2 * OPB + OPB);
+        ++nk;
         if (lane < 16 && part < parts)
           copy16(smem_u32(sm + TO_EXP + (wk * NSTAGE + st) * 256) + (lane & 8) * 16 + part * 16, exps + at);
         copies_arrive(bar);
         const int boxes = (parts + per - 1) / per;
-        if (lane == 0) mbar_expect_tx(bar, (uint32_t)(boxes * 2 * box * TT));
+        if (lane == 0) mbar_expect_tx(bar, (uint32_t)(boxes * box * TT));
         for (int x = 0; x < boxes; ++x) {
           const int row = __shfl_sync(0xffffffffu, at, x * per);
-          if (lane == 0) {
-            tma_load_2d(kd + x * box * TT, &tmK, 0, row, bar, pol);
-            tma_load_2d(vd + x * box * TT, &tmV, 0, row, bar, pol);
-          }
+          if (lane == 0) tma_load_2d(kd + x * box * TT, &tmK, 0, row, bar, pol);
+        }
+        // the values' buffer is free when the product of the tile before is done
+        if (i && !kv8_wait(smem_u32(v_empty), (uint32_t)((i - 1) & 1), abort_flag, a.err)) ok = false;
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        ++nv;
+        if (lane == 0) mbar_expect_tx(smem_u32(v_full), (uint32_t)(boxes * box * TT));
+        for (int x = 0; x < boxes; ++x) {
+          const int row = __shfl_sync(0xffffffffu, at, x * per);
+          if (lane == 0) tma_load_2d(vd + x * box * TT, &tmV, 0, row, smem_u32(v_full), pol);
         }
         vec = ahead;
       }
     }
-    if (!ok)   // the tiles in flight land before the CTA leaves
-      for (int x = max(0, i - NSTAGE); x < i; ++x)
-        kv8_wait(smem_u32(kv_full + x % NSTAGE), (uint32_t)((x / NSTAGE) & 1), abort_flag, a.err, false);
-  } else {
-    // ---- row warps: the first item together with the softmax warps, each later one ahead of them ----
-    const int sw = warp & 1;
-    if (more) prepare(0, SOFT / 32 + sw, T_FIRST_W);
-    if (lane == 0) mbar_arrive(smem_u32(q_first));
-    more = more && k.next(range);
-    for (int item = 1; more; ++item, more = k.next(range)) {
-      prepare(item, sw, T_ROWS_W);
-      if (lane == 0) mbar_arrive(smem_u32(q_full));
+    if (!ok) {   // the tiles in flight land before the CTA leaves
+      for (int x = max(0, nk - NSTAGE); x < nk; ++x)
+        kv8_wait(smem_u32(k_full + x % NSTAGE), (uint32_t)((x / NSTAGE) & 1), abort_flag, a.err, false);
+      if (nv) kv8_wait(smem_u32(v_full), (uint32_t)((nv - 1) & 1), abort_flag, a.err, false);
     }
   }
   tc_fence_before();

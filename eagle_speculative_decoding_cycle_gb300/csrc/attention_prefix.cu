@@ -72,28 +72,6 @@ __device__ __forceinline__ float pf_ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-// Pairs of fp32 in 64-bit registers (add.f32x2 and mul.f32x2 take one issue slot for two).
-typedef unsigned long long f32x2;
-__device__ __forceinline__ f32x2 two(float a, float b) {
-  f32x2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float2 one_by_one(f32x2 v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
-  f32x2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
-  f32x2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -124,14 +102,6 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
   return r != 0;
 }
-__device__ __forceinline__ bool lane0_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err) {
-  int ok = 0;
-  if ((threadIdx.x & 31) == 0) ok = kv8_wait(bar, parity, abort_flag, err) ? 1 : 0;
-  ok = __shfl_sync(0xffffffffu, ok, 0);
-  __syncwarp();
-  return ok != 0;
-}
-
 struct PfArgs {
   int R, nq, G, RB, P;         // rows, query heads, query heads a KV head, rows a tile
   int splits, tiles, pairs;    // key ranges, key tiles, pairs of query tiles
@@ -146,7 +116,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
              const __grid_constant__ CUtensorMap tmV, const PfArgs a) {
   using Sh = PfShape<D>;
   extern __shared__ uint8_t pf_smem[];
-  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(pf_smem) + 1023) & ~uintptr_t(1023));
+  uint8_t* sm = pf_smem + (-smem_u32(pf_smem) & 1023u);   // (not by pointer masks: accesses then lose the shared space)
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + Sh::OFF_BAR);
   uint64_t *q_full = bars, *k_full = bars + 1, *k_empty = bars + 3, *v_full = bars + 5, *v_empty = bars + 7,
            *s_full = bars + 9, *p_full = bars + 11 /* [tile][half] */, *o_done = bars + 15, *drain = bars + 17;
@@ -166,8 +136,8 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
       mbar_init(smem_u32(v_full + i), 1);
       mbar_init(smem_u32(v_empty + i), 1);
       mbar_init(smem_u32(s_full + i), 1);
-      mbar_init(smem_u32(p_full + 2 * i), PT);
-      mbar_init(smem_u32(p_full + 2 * i + 1), PT);
+      mbar_init(smem_u32(p_full + 2 * i), 4);
+      mbar_init(smem_u32(p_full + 2 * i + 1), 4);
       mbar_init(smem_u32(o_done + i), 1);
     }
     mbar_init(smem_u32(drain), 1);
@@ -189,7 +159,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
     float m = -INFINITY, l = 0.f;
     bool ok = mt < nmt;
     for (int i = 0; ok && i < nt; ++i) {
-      ok = lane0_wait(smem_u32(s_full + mt), (uint32_t)(i & 1), abort_flag, a.err);
+      ok = kv8_wait(smem_u32(s_full + mt), (uint32_t)(i & 1), abort_flag, a.err);
       if (!ok) break;
       tc_fence_after();
       float s[PT];
@@ -219,7 +189,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
       }
       if (i > 0 && __any_sync(0xffffffffu, raise)) {
         // the last product into O must be there before O is rescaled
-        ok = lane0_wait(smem_u32(o_done + mt), (uint32_t)((i - 1) & 1), abort_flag, a.err);
+        ok = kv8_wait(smem_u32(o_done + mt), (uint32_t)((i - 1) & 1), abort_flag, a.err);
         if (!ok) break;
         tc_fence_after();
 #pragma unroll 1
@@ -232,35 +202,32 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
         }
       }
       // the difference comes first: it is exact where it matters, near the maximum, whatever the size of the scores
-      const f32x2 nm = two(-m, -m), s2 = two(a.sl2, a.sl2);
-      f32x2 sum[2] = {two(0.f, 0.f), two(0.f, 0.f)};
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int qt = 0; qt < 4; ++qt) {
         uint32_t w[16];
 #pragma unroll
         for (int c = 0; c < 32; c += 2) {
-          float2 x = one_by_one(mul2(add2(two(s[qt * 32 + c], s[qt * 32 + c + 1]), nm), s2));
-          x.x = pf_ex2(x.x);
-          x.y = pf_ex2(x.y);
-          sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], two(x.x, x.y));
-          const __nv_bfloat162 b = __floats2bfloat162_rn(x.x, x.y);
+          const float x = pf_ex2((s[qt * 32 + c] - m) * a.sl2), y = pf_ex2((s[qt * 32 + c + 1] - m) * a.sl2);
+          sum[c & 2] += x;
+          sum[(c & 2) + 1] += y;
+          const __nv_bfloat162 b = __floats2bfloat162_rn(x, y);
           w[c / 2] = *reinterpret_cast<const uint32_t*>(&b);
         }
         tmem_st16u(tS + qt * 16, w);
         if (qt & 1) {
           tmem_wait_st();
           tc_fence_before();
-          mbar_arrive(smem_u32(p_full + 2 * mt + qt / 2));   // the first half's product starts under the second half
+          warp_arrive(smem_u32(p_full + 2 * mt + qt / 2));   // the first half's product starts under the second half
         }
       }
-      const float2 sums = one_by_one(add2(sum[0], sum[1]));
-      l += sums.x + sums.y;
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
     }
     if (mt < nmt) {
       const int row = r0 + mt * a.RB + qv / a.G;
       const bool write = qv < a.RB * a.G && row < a.R;
       const size_t q = (size_t)split * a.R * a.nq + (size_t)row * a.nq + h * a.G + qv % a.G;
-      if (ok && lane0_wait(smem_u32(o_done + mt), (uint32_t)((nt - 1) & 1), abort_flag, a.err)) {
+      if (ok && kv8_wait(smem_u32(o_done + mt), (uint32_t)((nt - 1) & 1), abort_flag, a.err)) {
         tc_fence_after();
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {

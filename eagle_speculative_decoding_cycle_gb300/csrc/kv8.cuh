@@ -45,23 +45,32 @@ __device__ __forceinline__ void e4m3x4_f16(uint32_t four, uint32_t& lo, uint32_t
       : "r"(four));
 }
 
-// Bounded wait for an mbarrier phase by whole warps: as mbar_wait, but the abort flag and the clock are looked at
-// every 64th try only.
+// Bounded wait of a converged warp for an mbarrier phase: lane 0 tries (a try by 32 lanes is 32 accesses to the barrier:
+// waiting warps then took half of the shared-memory pipe), looking at the abort flag and the clock every 64th time. Gives
+// up as mbar_wait does. Every lane gets the same answer: whether the CTA goes on.
 __device__ __forceinline__ bool kv8_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err,
                                          bool honor_abort = true) {
-  uint64_t t0 = 0;
-  for (uint32_t tries = 1;; ++tries) {
-    if (mbar_try(bar, parity)) return true;
-    if (tries & 63u) continue;
-    if (honor_abort && *abort_flag) return false;
-    const uint64_t now = globaltimer();
-    if (!t0) t0 = now;
-    if (now - t0 > EAGLE_WAIT_LIMIT_NS) {
-      *abort_flag = 1;
-      latch_error(err, DEVERR_MBAR_TIMEOUT);
-      return false;
+  if ((threadIdx.x & 31) == 0) {
+    uint64_t t0 = 0;
+    for (uint32_t tries = 1; !mbar_try(bar, parity); ++tries) {
+      if (tries & 63u) continue;
+      if (honor_abort && *abort_flag) break;
+      const uint64_t now = globaltimer();
+      if (!t0) t0 = now;
+      if (now - t0 > EAGLE_WAIT_LIMIT_NS) {
+        *abort_flag = 1;
+        latch_error(err, DEVERR_MBAR_TIMEOUT);
+        break;
+      }
     }
   }
+  __syncwarp();
+  return *abort_flag == 0;
+}
+// One arrival for the warp, after what all its lanes did.
+__device__ __forceinline__ void warp_arrive(uint32_t bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
 struct Kv8Attn {

@@ -5,8 +5,7 @@
 //                           scaled by a power of two and cut into two e4m3 parts, together 8 significant bits, as many as
 //                           bf16 has, down to 2^-9 of the vector's largest entry (below, a step of 2^-17 of it).
 //   O += P V                kind::f16: the weights times their values' exponents as fp16 in TMEM; the codes are widened to
-//                           fp16 (exact) in shared memory, row by row in place, by the softmax threads while they wait
-//                           anyway. (Weights in 8-bit parts, e5m2 for their range, need three products of the codes as
+//                           fp16 (exact) in shared memory by the softmax threads while they wait for S. (Weights in 8-bit parts, e5m2 for their range, need three products of the codes as
 //                           they lie, but cutting them took twice the arithmetic of the whole softmax: 5000 clocks a
 //                           tile against HBM's 1500.)
 // A key's exponent multiplies its scores; a value's is added to its weights' logarithms, against a running reference E, and
@@ -16,10 +15,9 @@
 // One CTA an SM, 20 warps, two workers with a range of items each, so that one's softmax and epilogue run under the other's
 // products. A worker has eight softmax warps (two threads a query vector, 64 keys of a tile each: four warps a scheduler
 // hide each other's latencies, and prepare the next item's query vectors; S is read twice from TMEM, for the maximum and for the weights, which keeps a thread below 96
-// registers, and each 32 columns of S are overwritten by the weights of their keys), and a producer warp (TMA: keys two tiles
-// ahead, values one). One warp issues both workers' products, each
-// worker's value product and next S together: issued side by side they end together, and the two softmaxes then run in
-// step, with the tensor cores idle. TMEM: S and O, 128 columns each, of either worker.
+// registers, and each 32 columns of S are overwritten by the weights of their keys), an MMA warp and a producer warp (TMA: the
+// next tile's keys under this one's softmax, its values as soon as these are widened). TMEM: S and O, 128 columns each, of
+// either worker.
 #include "kv8_split.cuh"
 #include "kernels.h"
 #include "tc_common.cuh"
@@ -31,7 +29,6 @@ namespace eagle {
 namespace {
 
 constexpr int TT = 128;                 // keys a tile, query vectors a block, dims
-constexpr int NSTAGE = 2;               // key tiles in a worker's ring
 constexpr int OPB = TT * TT;            // bytes of an 8-bit operand tile
 constexpr int SOFT = 256;               // softmax threads of a worker
 constexpr int SOFT_W = SOFT / 32;
@@ -41,9 +38,10 @@ constexpr int T_SHIFT = 3;              // weights are held times 2^3: at most 2
 constexpr int TE_UP = 4, TE_DOWN = 12, TE_SPAN = 14;   // exponents around the reference; within one pass
 
 // a worker's shared memory, [2]
-constexpr int TO_K = 0, TO_V = TO_K + 2 * NSTAGE * OPB, TO_Q = TO_V + 4 * OPB;   // V: fp16 [worker][half of the dims]; Q: [worker][part]
-constexpr int TO_EXP = TO_Q + 4 * OPB;                    // [worker][stage][K, V][128] exponent bytes
-constexpr int TO_KF = TO_EXP + 2 * NSTAGE * 256;          // [worker][tile parity][128] key factors
+constexpr int TO_K = 0, TO_V8 = TO_K + 2 * OPB, TO_V = TO_V8 + 2 * OPB, TO_Q = TO_V + 4 * OPB;   // keys; values: codes, fp16
+                                                          // [half of the dims]; query vectors [part]
+constexpr int TO_EXP = TO_Q + 4 * OPB;                    // [worker][tile parity][K, V][128] exponent bytes
+constexpr int TO_KF = TO_EXP + 2 * 2 * 256;               // [worker][tile parity][128] key factors
 constexpr int TO_VF = TO_KF + 2 * 2 * 512;                // [worker][tile parity][2][128] value exponents, inverse factors
 constexpr int TO_COL = TO_VF + 2 * 2 * 1024;              // [worker][item parity][128] (score factor, slot limit)
 constexpr int TO_MASK = TO_COL + 4 * TT * 8;              // [worker][item parity][128 rows][4] tree masks
@@ -78,16 +76,6 @@ __device__ __forceinline__ void mma16_ts(uint32_t d, uint32_t a, uint64_t b, uin
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
 }
-// Whether an mbarrier phase has ended, without waiting.
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
 __device__ __forceinline__ void st8(uint32_t t, const uint32_t* v) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(t), "r"(v[0]), "r"(v[1]),
                "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
@@ -118,13 +106,12 @@ __global__ void __launch_bounds__(T_THREADS, 1)
   extern __shared__ uint8_t tc_smem_raw[];
   uint8_t* sm = tc_smem_raw + (-smem_u32(tc_smem_raw) & 1023u);   // (not by pointer masks: accesses then lose the shared space)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int wk = warp < 16 ? warp >> 3 : warp & 1;   // this warp's worker (16: MMA of both; 18, 19: producers)
-  uint64_t* drain = reinterpret_cast<uint64_t*>(sm + TO_BAR + 256);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  const int wk = warp < 16 ? warp >> 3 : warp & 1;   // this warp's worker (16, 17: MMA; 18, 19: producers)
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + TO_BAR + 256);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + TO_BAR + wk * 128);
-  uint64_t *k_full = bars, *k_empty = bars + 2, *v_full = bars + 4, *v_empty = bars + 5, *q_full = bars + 6,
-           *s_full = bars + 8, *p_full = bars + 9, *o_done = bars + 10, *o_free = bars + 11;
+  uint64_t *k_full = bars, *k_empty = bars + 1, *v_full = bars + 2, *v_empty = bars + 3, *q_full = bars + 4, *s_full = bars + 5,
+           *p_full = bars + 6, *o_done = bars + 7, *o_free = bars + 8, *drain = bars + 9;
   int* red = reinterpret_cast<int*>(sm + TO_RED + wk * 512);
   int* r_hi = red;                                            // [tile parity][4 warps] largest exponent
   int* r_lo = red + 8;                                        // smallest
@@ -137,21 +124,17 @@ __global__ void __launch_bounds__(T_THREADS, 1)
   int* s_seq = s_lim + p.groups;
   if (warp == 16 || warp == 17) {
     if (lane == 0) {
-      for (int i = 0; i < NSTAGE; ++i) {
-        mbar_init(smem_u32(k_full + i), 33);   // the codes' bytes, and each producer lane's exponent copies
-        mbar_init(smem_u32(k_empty + i), 1);
-      }
+      mbar_init(smem_u32(k_full), 33);   // the codes' bytes, and each producer lane's exponent copies
+      mbar_init(smem_u32(k_empty), 1 + SOFT_W);   // S of the tile, and its exponents read by each softmax warp
       mbar_init(smem_u32(v_full), 1);
-      mbar_init(smem_u32(v_empty), 1);
+      mbar_init(smem_u32(v_empty), SOFT_W);
       mbar_init(smem_u32(q_full), SOFT_W);
       mbar_init(smem_u32(s_full), 1);
       mbar_init(smem_u32(p_full), SOFT_W);
       mbar_init(smem_u32(o_done), 1);
       mbar_init(smem_u32(o_free), SOFT_W);
-      if (warp == 16) {
-        mbar_init(smem_u32(drain), 1);
-        *abort_flag = 0;
-      }
+      mbar_init(smem_u32(drain), 1);
+      if (warp == 16) *abort_flag = 0;
       fence_mbar_init();
     }
     __syncwarp();
@@ -292,9 +275,9 @@ __global__ void __launch_bounds__(T_THREADS, 1)
       float m = -INFINITY, l = 0.f;
       int E = 0;                 // reference exponent byte
       for (int t = k.t0; t < k.t1; ++t, ++i) {
-        const int st = i % NSTAGE, key0 = t * TT, tp = i & 1;
-        kv8_wait(smem_u32(k_full + st), (uint32_t)((i / NSTAGE) & 1), abort_flag, a.err);
-        const uint8_t* s_exp = sm + TO_EXP + (wk * NSTAGE + st) * 256;
+        const int key0 = t * TT, tp = i & 1;
+        kv8_wait(smem_u32(k_full), (uint32_t)(i & 1), abort_flag, a.err);
+        const uint8_t* s_exp = sm + TO_EXP + (wk * 2 + tp) * 256;
         const bool masked = key0 + TT > fullvis || limit <= key0;
         uint32_t vis[2] = {0xffffffffu, 0xffffffffu};   // this thread's keys that its row sees
         bool seen = true;                               // key r of the tile, by any row
@@ -335,6 +318,9 @@ __global__ void __launch_bounds__(T_THREADS, 1)
             r_lo[tp * 4 + (warp & 3)] = (int)wlo;
           }
         }
+        // (without this arrival the next tile's keys could be there before a warp still at the item's end has seen this
+        // phase of k_full end, and it would wait for the phase after)
+        warp_arrive(smem_u32(k_empty));
         named_bar_sync(1 + wk, SOFT);
         const int4 rh = *reinterpret_cast<const int4*>(r_hi + tp * 4), rl = *reinterpret_cast<const int4*>(r_lo + tp * 4);
         int hi = max(max(rh.x, rh.y), max(rh.z, rh.w));
@@ -342,6 +328,29 @@ __global__ void __launch_bounds__(T_THREADS, 1)
         const bool narrow = hi - lo_all <= TE_SPAN;   // one pass does
         float keep[64];                               // the scores, for further passes (local memory, rarely)
 
+        // value r's codes to fp16, this thread's half of the dims, under S: the product of the tile before must be done
+        if (i) kv8_wait(smem_u32(o_done), (uint32_t)((passes - 1) & 1), abort_flag, a.err);
+        kv8_wait(smem_u32(v_full), (uint32_t)(i & 1), abort_flag, a.err);
+        {
+          const uint8_t* from = sm + TO_V8 + wk * OPB + r * TT;
+          uint8_t* to = sm + TO_V + (wk * 2 + hf) * OPB + r * TT;
+          uint4 codes[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) codes[c] = *reinterpret_cast<const uint4*>(from + (((hf * 4 + c) ^ (r & 7)) << 4));
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {   // 16 codes to two 16-byte parts of fp16
+            const uint32_t w[4] = {codes[c].x, codes[c].y, codes[c].z, codes[c].w};
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              uint4 f;
+              e4m3x4_f16(seen ? w[2 * j] : 0u, f.x, f.y);
+              e4m3x4_f16(seen ? w[2 * j + 1] : 0u, f.z, f.w);
+              *reinterpret_cast<uint4*>(to + (((2 * c + j) ^ (r & 7)) << 4)) = f;
+            }
+          }
+          fence_proxy_async_all();
+          warp_arrive(smem_u32(v_empty));
+        }
         kv8_wait(smem_u32(s_full), (uint32_t)(i & 1), abort_flag, a.err);
         tc_fence_after();
         float mx = -INFINITY;
@@ -365,12 +374,6 @@ __global__ void __launch_bounds__(T_THREADS, 1)
         }
         float* x_max = reinterpret_cast<float*>(sm + TO_X) + (wk * 2 + tp) * 2 * TT;
         x_max[hf * TT + r] = mx;
-        // this thread's half of the codes of value r, which lie where the second half's fp16 of the same value go
-        kv8_wait(smem_u32(v_full), (uint32_t)(i & 1), abort_flag, a.err);
-        uint8_t* s_v = sm + TO_V + wk * 2 * OPB + r * TT;
-        uint4 codes[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) codes[c] = *reinterpret_cast<const uint4*>(s_v + OPB + (((hf * 4 + c) ^ (r & 7)) << 4));
         bool first = true;
         float corr = 1.f;
         while (true) {
@@ -395,18 +398,6 @@ __global__ void __launch_bounds__(T_THREADS, 1)
               m = mx;
               l *= corr;
             }
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {   // 16 codes to two 16-byte parts of fp16
-              const uint32_t w[4] = {codes[c].x, codes[c].y, codes[c].z, codes[c].w};
-#pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                uint4 f;
-                e4m3x4_f16(seen ? w[2 * j] : 0u, f.x, f.y);
-                e4m3x4_f16(seen ? w[2 * j + 1] : 0u, f.z, f.w);
-                *reinterpret_cast<uint4*>(s_v + hf * OPB + (((2 * c + j) ^ (r & 7)) << 4)) = f;
-              }
-            }
-            fence_proxy_async_all();
           }
           const float scale_o = first ? corr * unit : unit;
           const bool begun = t > k.t0 || !first;      // O holds something
@@ -555,112 +546,48 @@ __global__ void __launch_bounds__(T_THREADS, 1)
         }
       }
     }
-  } else if (warp == 16) {
-    // ---- MMA, both workers: whichever is ready next gets its value product and its next S ----
-    struct Stream {
-      Walk k;
-      bool more, want_s;       // a tile is left; its S is still to come
-      int item, t, i, passes, pass;
-    } w[2];
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const uint32_t id = x * gridDim.x + blockIdx.x;
-      Stream& q = w[x];
-      const Range rx{s_pref, pad, a.c.nkv, p.groups, share.start(id), share.start(id + 1)};
-      q.more = id < share.ctas && q.k.begin(rx);
-      q.want_s = true;
-      q.item = q.i = q.passes = q.pass = 0;
-      q.t = q.more ? q.k.t0 : 0;
-    }
+  } else if (warp < 18) {
+    // ---- MMA: S of a tile, then its value product ----
+    const uint64_t dq = sdesc_sw128(smem_u32(sm + TO_Q + wk * 2 * OPB)), dk = sdesc_sw128(smem_u32(sm + TO_K + wk * OPB)),
+                   dv = desc_mn(smem_u32(sm + TO_V + wk * 2 * OPB));
+    int i = 0, passes = 0;
     bool ok = true;
-    uint32_t idle = 0;
-    uint64_t since = 0;
-    auto ready = [&](uint32_t bar, uint32_t parity) {   // as one lane sees it
-      return __shfl_sync(0xffffffffu, lane == 0 && mbar_test(bar, parity) ? 1 : 0, 0) != 0;
-    };
-    while (ok && (w[0].more || w[1].more)) {
-      bool moved = false;
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        Stream& q = w[x];
-        if (!q.more) continue;
-        uint64_t* b = reinterpret_cast<uint64_t*>(sm + TO_BAR + x * 128);
-        const uint32_t tS = *tmem_slot + x * TT, tO = tS + 2 * TT;
-        const bool begins = q.t == q.k.t0;
-        if (!q.want_s) {
-          // P V: the weights are there, and the last item's O has been read
-          if (!ready(smem_u32(b + 9), (uint32_t)(q.passes & 1))) continue;
-          if (begins && q.pass == 0 && q.item && !ready(smem_u32(b + 11), (uint32_t)((q.item - 1) & 1))) continue;
-          const bool again = *reinterpret_cast<volatile int*>(sm + TO_RED + x * 512 + 160) != 0;
-          tc_fence_after();
-          if (elect_one()) {
-            uint64_t v = desc_mn(smem_u32(sm + TO_V + x * 2 * OPB));
-            uint32_t acc = begins && q.pass == 0 ? 0u : 1u;   // the first product of an item begins O
-            // rolled loops: unrolled, their operands are hoisted out of the tile loop and spilled (2500 clocks an S)
-#pragma unroll 1
-            for (int y = 0; y < 8; ++y, v += 16 * TT >> 4, acc = 1) mma16_ts(tO, tS + (y >> 1) * 32 + (y & 1) * 8, v, O_IDESC, acc);
-            tc_commit(smem_u32(b + 10));
-            if (!again) tc_commit(smem_u32(b + 5));
-          }
-          __syncwarp();
-          moved = true;
-          ++q.passes;
-          ++q.pass;
-          if (again) continue;
-          ++q.i;
-          q.pass = 0;
-          q.want_s = true;
-          if (++q.t == q.k.t1) {
-            const uint32_t id = x * gridDim.x + blockIdx.x;
-            q.more = q.k.next(Range{s_pref, pad, a.c.nkv, p.groups, share.start(id), share.start(id + 1)});
-            ++q.item;
-            q.t = q.k.t0;
-          }
-        }
-        // S: the query vectors and the keys are there (its columns are free: P V of the tile before comes first)
-        if (!q.more) continue;
-        const bool first = q.t == q.k.t0;
-        const int sn = q.i % NSTAGE;
-        if (first && !ready(smem_u32(b + 6), (uint32_t)(q.item & 1))) continue;
-        if (!ready(smem_u32(b + sn), (uint32_t)((q.i / NSTAGE) & 1))) continue;
+    for (int item = 0; more && ok; ++item, more = k.next(range)) {
+      ok = kv8_wait_all(smem_u32(q_full), (uint32_t)(item & 1), abort_flag, a.err);
+      for (int t = k.t0; ok && t < k.t1; ++t, ++i) {
+        ok = kv8_wait_all(smem_u32(k_full), (uint32_t)(i & 1), abort_flag, a.err);
+        if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
-          uint64_t qd = sdesc_sw128(smem_u32(sm + TO_Q + x * 2 * OPB));
-          uint32_t acc = 0;
-#pragma unroll 1
-          for (int part = 0; part < 2; ++part, qd += (OPB >> 4) - 8) {   // high part, low part
-            uint64_t kd = sdesc_sw128(smem_u32(sm + TO_K + (x * NSTAGE + sn) * OPB));
-#pragma unroll 1
-            for (int y = 0; y < 4; ++y, qd += 2, kd += 2, acc = 1) mma8_ss(tS, qd, kd, S_IDESC, acc);
-          }
-          tc_commit(smem_u32(b + 8));
-          tc_commit(smem_u32(b + sn + 2));
+#pragma unroll
+          for (int x = 0; x < 8; ++x)   // high part, low part
+            mma8_ss(tS0, dq + (((x >> 2) * OPB + (x & 3) * 32) >> 4), dk + (((x & 3) * 32) >> 4), S_IDESC, x ? 1u : 0u);
+          tc_commit(smem_u32(s_full));
+          tc_commit(smem_u32(k_empty));
         }
         __syncwarp();
-        moved = true;
-        q.want_s = false;
-      }
-      if (moved) {
-        idle = 0;
-        since = 0;
-        continue;
-      }
-      __nanosleep(32);   // spinning at full rate would take the issue slots of the softmax warps next to this one
-      if ((++idle & 255u) == 0) {   // bounded, as every wait here
-        if (*abort_flag) ok = false;
-        const uint64_t now = globaltimer();
-        if (!since) since = now;
-        if (now - since > EAGLE_WAIT_LIMIT_NS) {
-          *abort_flag = 1;
-          latch_error(a.err, DEVERR_MBAR_TIMEOUT);
-          ok = false;
+        if (t == k.t0 && item) ok = kv8_wait_all(smem_u32(o_free), (uint32_t)((item - 1) & 1), abort_flag, a.err);
+        bool again = true;
+        for (int pass = 0; ok && again; ++pass) {
+          ok = kv8_wait_all(smem_u32(p_full), (uint32_t)(passes & 1), abort_flag, a.err);
+          if (!ok) break;
+          again = *s_more != 0;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint32_t fresh = t == k.t0 && pass == 0 ? 0u : 1u;   // the first product of an item begins O
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+              mma16_ts(tO0, tS0 + (x >> 1) * 32 + (x & 1) * 8, dv + ((x * 16 * TT) >> 4), O_IDESC, x ? 1u : fresh);
+            tc_commit(smem_u32(o_done));
+          }
+          __syncwarp();
+          ++passes;
         }
-        ok = __all_sync(0xffffffffu, ok);
       }
     }
     if (!ok) {   // products in flight end before the CTA frees its TMEM
       if (elect_one()) tc_commit(smem_u32(drain));
-      kv8_wait(smem_u32(drain), 0, abort_flag, a.err, false);
+      kv8_wait_all(smem_u32(drain), 0, abort_flag, a.err, false);
     }
   } else if (warp == 18 || warp == 19) {
     // ---- producer. Lanes 0-7 look after the eight 16-slot parts of a tile's keys, lanes 8-15 of its values ----
@@ -679,41 +606,35 @@ __global__ void __launch_bounds__(T_THREADS, 1)
       long long vec = where(k, k.t0);
       for (int t = k.t0; ok && t < k.t1; ++t, ++i) {
         const long long ahead = t + 1 < k.t1 ? where(k, t + 1) : -1;   // the next tile's table entries, a tile early
-        const int st = i % NSTAGE, parts = max(0, min(8, (limit - t * TT + 15) / 16));
+        const int parts = max(0, min(8, (limit - t * TT + 15) / 16));
         if (lane < parts && vec < 0) latch_error(a.err, DEVERR_BOUNDS);   // not assigned: unspecified keys
         const int at = (int)max(vec, 0ll);
-        if (i >= NSTAGE && !kv8_wait(smem_u32(k_empty + st), (uint32_t)((i / NSTAGE - 1) & 1), abort_flag, a.err)) ok = false;
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        const uint32_t bar = smem_u32(k_full + st), kd = smem_u32(sm + TO_K + (wk * NSTAGE + st) * OPB),
-                       vd = smem_u32(sm + TO_V + wk * 2 * OPB + OPB);
-        ++nk;
-        if (lane < 16 && part < parts)
-          copy16(smem_u32(sm + TO_EXP + (wk * NSTAGE + st) * 256) + (lane & 8) * 16 + part * 16, exps + at);
-        copies_arrive(bar);
         const int boxes = (parts + per - 1) / per;
-        if (lane == 0) mbar_expect_tx(bar, (uint32_t)(boxes * box * TT));
-        for (int x = 0; x < boxes; ++x) {
-          const int row = __shfl_sync(0xffffffffu, at, x * per);
-          if (lane == 0) tma_load_2d(kd + x * box * TT, &tmK, 0, row, bar, pol);
-        }
-        // the values' buffer is free when the product of the tile before is done
-        if (i && !kv8_wait(smem_u32(v_empty), (uint32_t)((i - 1) & 1), abort_flag, a.err)) ok = false;
-        ok = __all_sync(0xffffffffu, ok);
+        auto load = [&](const CUtensorMap* map, uint32_t dst, uint32_t bar) {
+          if (lane == 0) mbar_expect_tx(bar, (uint32_t)(boxes * box * TT));
+          for (int x = 0; x < boxes; ++x) {
+            const int row = __shfl_sync(0xffffffffu, at, x * per);
+            if (lane == 0) tma_load_2d(dst + x * box * TT, map, 0, row, bar, pol);
+          }
+        };
+        // the keys' buffer is free when S of the tile before is done, the values' when they are widened
+        if (i) ok = kv8_wait_all(smem_u32(k_empty), (uint32_t)((i - 1) & 1), abort_flag, a.err);
         if (!ok) break;
+        if (lane < 16 && part < parts)
+          copy16(smem_u32(sm + TO_EXP + (wk * 2 + (i & 1)) * 256) + (lane & 8) * 16 + part * 16, exps + at);
+        copies_arrive(smem_u32(k_full));
+        load(&tmK, smem_u32(sm + TO_K + wk * OPB), smem_u32(k_full));
+        ++nk;
+        if (i) ok = kv8_wait_all(smem_u32(v_empty), (uint32_t)((i - 1) & 1), abort_flag, a.err);
+        if (!ok) break;
+        load(&tmV, smem_u32(sm + TO_V8 + wk * OPB), smem_u32(v_full));
         ++nv;
-        if (lane == 0) mbar_expect_tx(smem_u32(v_full), (uint32_t)(boxes * box * TT));
-        for (int x = 0; x < boxes; ++x) {
-          const int row = __shfl_sync(0xffffffffu, at, x * per);
-          if (lane == 0) tma_load_2d(vd + x * box * TT, &tmV, 0, row, smem_u32(v_full), pol);
-        }
         vec = ahead;
       }
     }
     if (!ok) {   // the tiles in flight land before the CTA leaves
-      for (int x = max(0, nk - NSTAGE); x < nk; ++x)
-        kv8_wait(smem_u32(k_full + x % NSTAGE), (uint32_t)((x / NSTAGE) & 1), abort_flag, a.err, false);
-      if (nv) kv8_wait(smem_u32(v_full), (uint32_t)((nv - 1) & 1), abort_flag, a.err, false);
+      if (nk) kv8_wait_all(smem_u32(k_full), (uint32_t)((nk - 1) & 1), abort_flag, a.err, false);
+      if (nv) kv8_wait_all(smem_u32(v_full), (uint32_t)((nv - 1) & 1), abort_flag, a.err, false);
     }
   }
   tc_fence_before();

@@ -72,6 +72,28 @@ __device__ __forceinline__ float pf_ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+// Pairs of fp32 in 64-bit registers (add.f32x2 and mul.f32x2 take one issue slot for two).
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 two(float a, float b) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 one_by_one(f32x2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -202,16 +224,18 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
         }
       }
       // the difference comes first: it is exact where it matters, near the maximum, whatever the size of the scores
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      const f32x2 nm = two(-m, -m), s2 = two(a.sl2, a.sl2);
+      f32x2 sum[2] = {two(0.f, 0.f), two(0.f, 0.f)};
 #pragma unroll
       for (int qt = 0; qt < 4; ++qt) {
         uint32_t w[16];
 #pragma unroll
         for (int c = 0; c < 32; c += 2) {
-          const float x = pf_ex2((s[qt * 32 + c] - m) * a.sl2), y = pf_ex2((s[qt * 32 + c + 1] - m) * a.sl2);
-          sum[c & 2] += x;
-          sum[(c & 2) + 1] += y;
-          const __nv_bfloat162 b = __floats2bfloat162_rn(x, y);
+          float2 x = one_by_one(mul2(add2(two(s[qt * 32 + c], s[qt * 32 + c + 1]), nm), s2));
+          x.x = pf_ex2(x.x);
+          x.y = pf_ex2(x.y);
+          sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], two(x.x, x.y));
+          const __nv_bfloat162 b = __floats2bfloat162_rn(x.x, x.y);
           w[c / 2] = *reinterpret_cast<const uint32_t*>(&b);
         }
         tmem_st16u(tS + qt * 16, w);
@@ -221,7 +245,8 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
           warp_arrive(smem_u32(p_full + 2 * mt + qt / 2));   // the first half's product starts under the second half
         }
       }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      const float2 sums = one_by_one(add2(sum[0], sum[1]));
+      l += sums.x + sums.y;
     }
     if (mt < nmt) {
       const int row = r0 + mt * a.RB + qv / a.G;
@@ -260,7 +285,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
       for (int i = 0; i < nt; ++i) {
         const int st = i & 1;
         const uint32_t ph = (uint32_t)((i / 2 - 1) & 1);
-        if (i >= 2 && !kv8_wait(smem_u32(k_empty + st), ph, abort_flag, a.err)) break;
+        if (i >= 2 && !kv8_wait_all(smem_u32(k_empty + st), ph, abort_flag, a.err)) break;
         if (elect_one()) {
           mbar_expect_tx(smem_u32(k_full + st), Sh::OP);
           for (int x = 0; x < Sh::HALVES; ++x)
@@ -268,7 +293,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
                         smem_u32(k_full + st));
         }
         ++nk;
-        if (i >= 2 && !kv8_wait(smem_u32(v_empty + st), ph, abort_flag, a.err)) break;
+        if (i >= 2 && !kv8_wait_all(smem_u32(v_empty + st), ph, abort_flag, a.err)) break;
         if (elect_one()) {
           mbar_expect_tx(smem_u32(v_full + st), Sh::OP);
           for (int x = 0; x < Sh::HALVES; ++x)
@@ -278,9 +303,9 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
         ++nv;
       }
       if (*abort_flag) {   // copies in flight land before the CTA leaves: the last two of each ring
-        kv8_wait(smem_u32(q_full), 0, abort_flag, a.err, false);
-        for (int j = max(0, nk - 2); j < nk; ++j) kv8_wait(smem_u32(k_full + (j & 1)), (uint32_t)((j / 2) & 1), abort_flag, a.err, false);
-        for (int j = max(0, nv - 2); j < nv; ++j) kv8_wait(smem_u32(v_full + (j & 1)), (uint32_t)((j / 2) & 1), abort_flag, a.err, false);
+        kv8_wait_all(smem_u32(q_full), 0, abort_flag, a.err, false);
+        for (int j = max(0, nk - 2); j < nk; ++j) kv8_wait_all(smem_u32(k_full + (j & 1)), (uint32_t)((j / 2) & 1), abort_flag, a.err, false);
+        for (int j = max(0, nv - 2); j < nv; ++j) kv8_wait_all(smem_u32(v_full + (j & 1)), (uint32_t)((j / 2) & 1), abort_flag, a.err, false);
       }
     } else if (warp == 9) {
       // ---- MMA ----
@@ -288,22 +313,21 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
       // operand descriptors; an offset of n bytes adds n >> 4
       const uint64_t dq = sdesc_sw128(smem_u32(sm + Sh::OFF_Q)), dk = sdesc_sw128(smem_u32(sm + Sh::OFF_K)),
                      dv = pf_desc_mn(smem_u32(sm + Sh::OFF_V), Sh::HALF);
-      bool ok = kv8_wait(smem_u32(q_full), 0, abort_flag, a.err);
+      bool ok = kv8_wait_all(smem_u32(q_full), 0, abort_flag, a.err);
       auto issue_s = [&](int mt, int i) {
         if (elect_one()) {
-          // rolled loops: unrolled, their operands are hoisted out of the tile loop and spilled
           uint64_t q = dq + mt * (Sh::OP >> 4), k = dk + (i & 1) * (Sh::OP >> 4);
           uint32_t acc = 0;
-#pragma unroll 1
+#pragma unroll
           for (int hd = 0; hd < Sh::HALVES; ++hd, q += (Sh::HALF >> 4) - 8, k += (Sh::HALF >> 4) - 8)
-#pragma unroll 1
+#pragma unroll
             for (int x = 0; x < 4; ++x, q += 2, k += 2, acc = 1) tc_mma_bf16(tmem + mt * PT, q, k, IS, acc);
           tc_commit(smem_u32(s_full + mt));
           if (mt == nmt - 1) tc_commit(smem_u32(k_empty + (i & 1)));
         }
         __syncwarp();
       };
-      if (ok) ok = kv8_wait(smem_u32(k_full), 0, abort_flag, a.err);
+      if (ok) ok = kv8_wait_all(smem_u32(k_full), 0, abort_flag, a.err);
       if (ok) {
         tc_fence_after();
         for (int mt = 0; mt < nmt; ++mt) issue_s(mt, 0);
@@ -311,17 +335,17 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
       for (int i = 0; ok && i < nt; ++i) {
         for (int mt = 0; ok && mt < nmt; ++mt) {
           // P_i V_i, then S_(i+1) over the same columns: the tensor cores take them in this order
-          ok = mt || kv8_wait(smem_u32(v_full + (i & 1)), (uint32_t)((i / 2) & 1), abort_flag, a.err);
+          ok = mt || kv8_wait_all(smem_u32(v_full + (i & 1)), (uint32_t)((i / 2) & 1), abort_flag, a.err);
           const uint64_t v = dv + (i & 1) * (Sh::OP >> 4);
 #pragma unroll 1
           for (int hf = 0; hf < 2; ++hf) {
-            ok = ok && kv8_wait(smem_u32(p_full + 2 * mt + hf), (uint32_t)(i & 1), abort_flag, a.err);
+            ok = ok && kv8_wait_all(smem_u32(p_full + 2 * mt + hf), (uint32_t)(i & 1), abort_flag, a.err);
             if (!ok) break;
             tc_fence_after();
             if (elect_one()) {
               uint64_t vd = v + hf * (4 * 2048 >> 4);
               uint32_t pa = tmem + mt * PT + hf * 32, acc = i || hf ? 1u : 0u;
-#pragma unroll 1
+#pragma unroll
               for (int x = 0; x < 4; ++x, vd += 2048 >> 4, pa += 8, acc = 1) mma_ts(tmem + 2 * PT + mt * D, pa, vd, IO, acc);
               if (hf) {
                 tc_commit(smem_u32(o_done + mt));
@@ -331,7 +355,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
             __syncwarp();
           }
           if (ok && i + 1 < nt) {
-            if (mt == 0) ok = kv8_wait(smem_u32(k_full + ((i + 1) & 1)), (uint32_t)(((i + 1) / 2) & 1), abort_flag, a.err);
+            if (mt == 0) ok = kv8_wait_all(smem_u32(k_full + ((i + 1) & 1)), (uint32_t)(((i + 1) / 2) & 1), abort_flag, a.err);
             if (ok) {
               tc_fence_after();
               issue_s(mt, i + 1);
@@ -341,7 +365,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
       }
       if (!ok) {   // products in flight end before the CTA frees its TMEM
         if (elect_one()) tc_commit(smem_u32(drain));
-        kv8_wait(smem_u32(drain), 0, abort_flag, a.err, false);
+        kv8_wait_all(smem_u32(drain), 0, abort_flag, a.err, false);
       }
     }
   }

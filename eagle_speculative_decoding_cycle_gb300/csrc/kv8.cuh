@@ -67,6 +67,25 @@ __device__ __forceinline__ bool kv8_wait(uint32_t bar, uint32_t parity, volatile
   __syncwarp();
   return *abort_flag == 0;
 }
+// The same, every lane trying: for the single warps that issue copies and products, which go on some hundred clocks earlier
+// without the divergence (4096 shared tokens, 64 x 17 rows: 147 -> 134 us).
+__device__ __forceinline__ bool kv8_wait_all(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err,
+                                             bool honor_abort = true) {
+  uint64_t t0 = 0;
+  for (uint32_t tries = 1; !mbar_try(bar, parity); ++tries) {
+    if (tries & 63u) continue;
+    if (honor_abort && *abort_flag) break;
+    const uint64_t now = globaltimer();
+    if (!t0) t0 = now;
+    if (now - t0 > EAGLE_WAIT_LIMIT_NS) {
+      *abort_flag = 1;
+      latch_error(err, DEVERR_MBAR_TIMEOUT);
+      break;
+    }
+  }
+  __syncwarp();
+  return *abort_flag == 0;
+}
 // One arrival for the warp, after what all its lanes did.
 __device__ __forceinline__ void warp_arrive(uint32_t bar) {
   __syncwarp();

@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(T_THREADS, 1)
     }
     fullvis = __reduce_min_sync(0xffffffffu, fullvis);
     if (lane == 0) s_fullvis[buf * 16 + sw] = fullvis;
-    fence_proxy_async_all();
+    fence_async_shared();
     warp_arrive(smem_u32(q_full));
   };
 
@@ -348,7 +348,7 @@ __global__ void __launch_bounds__(T_THREADS, 1)
               *reinterpret_cast<uint4*>(to + (((2 * c + j) ^ (r & 7)) << 4)) = f;
             }
           }
-          fence_proxy_async_all();
+          fence_async_shared();
           warp_arrive(smem_u32(v_empty));
         }
         kv8_wait(smem_u32(s_full), (uint32_t)(i & 1), abort_flag, a.err);

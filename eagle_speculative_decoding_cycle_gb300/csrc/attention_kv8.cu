@@ -65,6 +65,12 @@ __device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
+// Partial k of the prefix for query vector `at` of all (row, query head).
+template <int D>
+__device__ __forceinline__ Part prefix_part(const Kv8Attn& a, const Plan& p, int k, size_t at) {
+  const size_t q = (size_t)k * a.R * a.nq + at;
+  return Part{p.pp_ml + 2 * q, p.pp_o + q * D};
+}
 // Shared memory of one configuration: D dims; NT query tiles (of 8) a warp, WN warps side by side over the query
 // tiles, WK groups of them over the keys; NS tiles in the ring.
 template <int D, int NT, int WN, int WK, int NS>
@@ -124,7 +130,7 @@ __global__ void __launch_bounds__(Shape<D, NT, WN, WK, NS>::THREADS, CTAS)
   const uint32_t tiles = (uint32_t)s_pref[p.groups] * nkv;
   const int pad = pad_of(p, tiles);
   const Share share(p, tiles, pad);
-  if (threadIdx.x == 0) p.cut[blockIdx.x] = make_int4(0, 0, -1, 0);
+  if (threadIdx.x == 0) cut_none(p, blockIdx.x);
   if (blockIdx.x >= share.ctas) return;
   const Range range{s_pref, pad, nkv, p.groups, share.start(blockIdx.x), share.start(blockIdx.x + 1)};
 
@@ -545,8 +551,7 @@ __global__ void __launch_bounds__(Shape<D, NT, WN, WK, NS>::THREADS, CTAS)
         named_bar_sync(1, NC);
       }
       const bool whole = t0 == 0 && t1 == nt;
-      if (threadIdx.x == 0 && t0 == 0 && t1 < nt)
-        p.cut[blockIdx.x] = make_int4(gi, h, (int)share.cta_of(k.base + pad + nt - 1), 0);
+      if (threadIdx.x == 0 && t0 == 0) cut_begin(p, blockIdx.x, k, (int)share.cta_of(k.base + pad + nt - 1));
       const int slot = 2 * blockIdx.x + (t0 == 0 ? 1 : 0);
       for (int x = threadIdx.x; x < nqv * (D / 8); x += NC) {
         const int col = x / (D / 8), c = x % (D / 8) * 8;
@@ -563,7 +568,7 @@ __global__ void __launch_bounds__(Shape<D, NT, WN, WK, NS>::THREADS, CTAS)
         if (whole) {
           const int in = (int)(col * p.G_inv >> 16), row = r0 + in;
           const size_t at = (size_t)row * a.nq + h * p.G + col - in * p.G;
-          fold<D>(p.n_prefix, [&](int k) { return (size_t)k * a.R * a.nq + at; }, p.pp_ml, p.pp_o, c / 8, top, L, o);
+          fold<D>(p.n_prefix, [&](int k) { return prefix_part<D>(a, p, k, at); }, c / 8, top, L, o);
           store8(a, at, D, c, seq >= 0 && a.row_seq[row] == seq, L, o);
         } else {
           const size_t q = (size_t)slot * p.qv_pad + col;
@@ -579,29 +584,36 @@ __global__ void __launch_bounds__(Shape<D, NT, WN, WK, NS>::THREADS, CTAS)
   }
 }
 
-// Joins the pieces of the items that range ends cut: CTA (c, y) takes the item that CTA c began and did not finish, p.join_cols of its
-// query vectors. D / 8 lanes a query vector; where few query vectors leave threads over, they share an item's pieces (every
-// `ways`-th each) and are joined through shared memory, in the order of the threads.
+// Joins the pieces of the items that range ends cut, and the prefix's partials with them: CTA (x, y) takes the
+// item of p.cut[x], p.join_cols of its query vectors. D / 8 lanes a query vector and p.join_ways such
+// teams, which take every join_ways-th partial each and are joined through shared memory, in the order of the teams.
 template <int D>
 __global__ void __launch_bounds__(256) kv8_join_k(const Kv8Attn a, const Plan p) {
-  PDL_ENTRY();
-  const int c0 = blockIdx.x;
-  const int4 cut = p.cut[c0];
-  if (cut.z < 0) return;
-  const int lo = cut.x, h = cut.y, c1 = cut.z;
-  const int sidx = (p.g0 + lo) / p.nb, rb = (p.g0 + lo) - sidx * p.nb;
-  const int s0 = sidx * a.rows_per_seq, s1 = min(s0 + a.rows_per_seq, a.R);
-  const int r0 = s0 + rb * p.RB, nqv = (min(r0 + p.RB, s1) - r0) * p.G;
   constexpr int GL = D / 8;
   __shared__ float s_part[256 / GL][D + 4];
   __shared__ float2 s_ml[256 / GL];
-  const int team = threadIdx.x / GL, ways = 256 / GL / p.join_cols, way = team / p.join_cols;
+  PDL_ENTRY();
+  const int4 cut = p.cut[blockIdx.x];
+  const int lo = cut.x, h = cut.y, c0 = cut.z, c1 = cut.w;
+  if (c1 < 0) return;
+  if (lo < 0 || lo >= p.groups || h < 0 || h >= p.nkv || c0 < 0 || c1 < c0 || c1 >= p.grid) return;   // a wait gave up
+  const int sidx = (p.g0 + lo) / p.nb, rb = (p.g0 + lo) - sidx * p.nb;
+  const int s0 = sidx * a.rows_per_seq, s1 = (int)min((long long)s0 + a.rows_per_seq, (long long)a.R);
+  const int r0 = s0 + rb * p.RB, nqv = (min(r0 + p.RB, s1) - r0) * p.G;
+  const int team = threadIdx.x / GL, ways = p.join_ways, way = team / p.join_cols;
   const int col = blockIdx.y * p.join_cols + team % p.join_cols, c = threadIdx.x % GL * 8;
-  // piece 0 in slot 2 c0 + 1 (it holds the item's start), the others in slot 2 c
-  auto at_of = [&](int k) { return (size_t)(k ? 2 * (c0 + k) : 2 * c0 + 1) * p.qv_pad + min(col, nqv - 1); };
-  const int pieces = c1 - c0 + 1;
+  const int col_in = min(col, nqv - 1), in = (int)(col_in * p.G_inv >> 16), row = r0 + in;
+  const size_t at = (size_t)row * a.nq + h * p.G + col_in - in * p.G;
+  const int seq = first_seq(a, s0, s1), own = a.row_seq[row];
+  // piece 0 in slot 2 c0 + 1 (it holds the item's start), the others in slot 2 c, then the prefix's
+  const int pieces = c1 - c0 + 1, n = pieces + p.n_prefix;
   float top = -INFINITY, L = 0.f, o[8] = {};
-  fold<D>((pieces - way + ways - 1) / ways, [&](int k) { return at_of(k * ways + way); }, p.part_ml, p.part_o, c / 8, top, L, o);
+  fold<D>((n - way + ways - 1) / ways, [&](int i) {
+    const int k = i * ways + way;
+    if (k >= pieces) return prefix_part<D>(a, p, k - pieces, at);
+    const size_t q = (size_t)(k ? 2 * (c0 + k) : 2 * c0 + 1) * p.qv_pad + col_in;
+    return Part{p.part_ml + 2 * q, p.part_o + q * D};
+  }, c / 8, top, L, o);
   if (ways > 1) {
     if (way) {
       *reinterpret_cast<float4*>(&s_part[team][c]) = make_float4(o[0], o[1], o[2], o[3]);
@@ -620,12 +632,7 @@ __global__ void __launch_bounds__(256) kv8_join_k(const Kv8Attn a, const Plan p)
       for (int x = 0; x < 8; ++x) o[x] = o[x] * f + s_part[from][c + x] * g;
     }
   }
-  if (col >= nqv) return;
-  const int seq = first_seq(a, s0, s1);
-  const int in = (int)(col * p.G_inv >> 16), row = r0 + in;
-  const size_t at = (size_t)row * a.nq + h * p.G + col - in * p.G;
-  fold<D>(p.n_prefix, [&](int k) { return (size_t)k * a.R * a.nq + at; }, p.pp_ml, p.pp_o, c / 8, top, L, o);
-  store8(a, at, D, c, seq >= 0 && seq < a.c.max_batch && a.row_seq[row] == seq, L, o);
+  if (col < nqv) store8(a, at, D, c, seq >= 0 && seq < a.c.max_batch && own == seq, L, o);
 }
 
 
@@ -679,11 +686,19 @@ size_t own_scratch(const Kv8& c, const Plan& p) {
          al256((size_t)2 * KV8_MAX_CTAS * p.qv_pad * 2 * sizeof(float)) + al256(KV8_MAX_CTAS * sizeof(int4));
 }
 
+// A join CTA holds up to 256 / (D / 8) teams: as many on one query vector as leave each about four partials, if the
+// grid's ranges are spread evenly over the items, the others on further query vectors.
 template <int D>
 cudaError_t launch_join(cudaStream_t st, const Kv8Attn& a, Plan& p) {
-  p.join_cols = 1;
-  while (p.join_cols < 256 / (D / 8) && p.join_cols * 4 < p.QV) p.join_cols *= 2;
-  return launch_k(kv8_join_k<D>, dim3(p.grid, (p.QV + p.join_cols - 1) / p.join_cols), dim3(256), 0, st, a, p);
+  constexpr int TEAMS = 256 / (D / 8);
+  const int items = p.groups * p.nkv, partials = p.grid / items + 2 + p.n_prefix;
+  p.join_ways = 1;
+  while (p.join_ways < TEAMS && p.join_ways * 4 < partials) p.join_ways *= 2;
+  p.join_cols = 32 / (D / 8);   // whole warps
+  while (p.join_cols * p.join_ways < TEAMS && p.join_cols < p.QV) p.join_cols *= 2;
+  if (p.join_cols * p.join_ways > TEAMS) p.join_ways = TEAMS / p.join_cols;
+  return launch_k(kv8_join_k<D>, dim3(p.by_item ? items : p.grid, (p.QV + p.join_cols - 1) / p.join_cols),
+                  dim3(p.join_cols * p.join_ways * (D / 8)), 0, st, a, p);
 }
 
 template <int D, int NT, int WN, int WK, int NS, int CTAS>
@@ -691,6 +706,7 @@ cudaError_t launch_own(cudaStream_t st, const Kv8Attn& a, Plan& p, const CUtenso
   using Sh = Shape<D, NT, WN, WK, NS>;
   const auto fn = kv8_attn_k<D, NT, WN, WK, NS, CTAS>;
   p.grid = std::min(KV8_MAX_CTAS, CTAS * device_sm_count());
+  p.by_item = p.groups * p.nkv <= p.grid;
   p.min_tiles = WK;
   p.pad = 6 + p.n_prefix / 2;
   const int smem = Sh::bytes(p.groups);
@@ -715,6 +731,7 @@ cudaError_t launch_mma(cudaStream_t st, const Kv8Attn& a, Plan& p, const CUtenso
     return launch_own<D, 4, 4, 2, 7, 1>(st, a, p, mk, mv);
   }
   p.grid = 2 * std::min(KV8_MAX_CTAS / 2, device_sm_count());   // two workers a CTA
+  p.by_item = p.groups * p.nkv <= p.grid;
   p.min_tiles = 1;
   p.pad = 2;
   const cudaError_t e = kv8_launch_tc(st, a, p, mk, mv);

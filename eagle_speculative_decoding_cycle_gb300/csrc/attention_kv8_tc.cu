@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(T_THREADS, 1)
   const int pad = pad_of(p, tiles);
   const Share share(p, tiles, pad);                          // over the workers: all first ones, then all second ones
   const uint32_t me = wk * gridDim.x + blockIdx.x;
-  if (threadIdx.x < 2) p.cut[threadIdx.x * gridDim.x + blockIdx.x] = make_int4(0, 0, -1, 0);
+  if (threadIdx.x < 2) cut_none(p, threadIdx.x * gridDim.x + blockIdx.x);
   __syncthreads();
   const Range range{s_pref, pad, a.c.nkv, p.groups, share.start(me), share.start(me + 1)};
   Walk k;
@@ -488,8 +488,7 @@ __global__ void __launch_bounds__(T_THREADS, 1)
       named_bar_sync(1 + wk, SOFT);
       float L = x_l[r] + x_l[TT + r], top = m * qf;
       const bool whole = done.t0 == 0 && done.t1 == done.nt;
-      if (threadIdx.x % SOFT == 0 && done.t0 == 0 && !whole)
-        p.cut[me] = make_int4(gi, h, (int)share.cta_of(done.base + pad + done.nt - 1), 0);
+      if (threadIdx.x % SOFT == 0 && done.t0 == 0) cut_begin(p, me, done, (int)share.cta_of(done.base + pad + done.nt - 1));
       const int in = r < nqv ? (int)(r * p.G_inv >> 16) : 0, row = r0 + in;
       const size_t at = (size_t)row * a.nq + h * p.G + (r < nqv ? r - in * p.G : 0), stride = (size_t)a.R * a.nq;
       const size_t slot = (size_t)(2 * me + (done.t0 == 0 ? 1 : 0)) * p.qv_pad + r;

@@ -41,12 +41,13 @@ struct Plan {
   int groups;             // row blocks of this launch, from block g0 on
   int g0;
   int grid, min_tiles;    // CTAs at most; tiles a CTA at least
-  int join_cols;          // query vectors a join CTA takes (a power of two up to 256 / (d / 8))
+  int join_cols, join_ways;   // a join CTA: query vectors, threads' teams that share one's pieces (powers of two)
   int pad;                // what starting and joining an item costs, in tiles: an item of nt tiles spans pad + nt units
   int qv_pad;             // query vectors of a partial
   float* part_o;          // [2 grid][qv_pad][D]
   float* part_ml;         // [2 grid][qv_pad][2]
-  int4* cut;              // [grid] the item that CTA c begins and does not finish: row block, head, last CTA (-1: none)
+  int4* cut;              // items that range ends cut: row block, head, first CTA, last CTA (-1: not cut)
+  int by_item;            // cut is indexed by item (no more items than CTAs), else by the item's first CTA
   const float *pp_o, *pp_ml;   // prefix partials [n_prefix][R * nq][D], [..][2]
   int n_prefix;
 };
@@ -117,32 +118,31 @@ __device__ __forceinline__ Group group_of(const Kv8Attn& a, const Plan& p, int g
   return o;
 }
 
+// A partial of one query vector: its maximum and sum (ml), its D values (o).
+struct Part {
+  const float *ml, *o;
+};
 // Adds n partials to (top, L, o), o 8 values of a query vector whose D values are spread over D / 8 neighbouring
 // lanes (sub: this lane's place among them): the lanes share the (m, l) pairs, the sums run in the order of the partials.
 template <int D, typename At>
-__device__ __forceinline__ void fold(int n, At at, const float* ml, const float* po, int sub, float& top, float& L, float* o) {
+__device__ __forceinline__ void fold(int n, At at, int sub, float& top, float& L, float* o) {
   constexpr int GL = D / 8;
-  const unsigned group = ((GL == 32 ? 0u : 1u << GL) - 1u) << ((threadIdx.x & 31) / GL * GL);
-  float mx = top;
-  for (int i = sub; i < n; i += GL) mx = fmaxf(mx, ml[2 * at(i)]);
+  const unsigned group = ((1u << GL) - 1u) << ((threadIdx.x & 31) / GL * GL);
+  for (int i0 = 0; i0 < n; i0 += GL) {   // GL partials at a time
+    float2 ml = make_float2(-INFINITY, 0.f);
+    if (i0 + sub < n) ml = *reinterpret_cast<const float2*>(at(i0 + sub).ml);
+    float mx = fmaxf(top, ml.x);
 #pragma unroll
-  for (int d = GL / 2; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(group, mx, d));
-  const float base = mx == -INFINITY ? 0.f : mx, f = ex2(top - base);
-  top = mx;
-  L *= f;
+    for (int d = GL / 2; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(group, mx, d));
+    const float base = mx == -INFINITY ? 0.f : mx, f = ex2(top - base), w = ex2(ml.x - base), lw = ml.y * w;
+    top = mx;
+    L *= f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) o[i] *= f;
-  for (int i0 = 0; i0 < n; i0 += GL) {
-    float w = 0.f, lw = 0.f;
-    if (i0 + sub < n) {
-      const float2 v = *reinterpret_cast<const float2*>(ml + 2 * at(i0 + sub));
-      w = ex2(v.x - base);
-      lw = v.y * w;
-    }
+    for (int i = 0; i < 8; ++i) o[i] *= f;
     const int cnt = min(GL, n - i0);
 #pragma unroll 4
     for (int j = 0; j < cnt; ++j) {
-      const float4* x = reinterpret_cast<const float4*>(po + at(i0 + j) * D + sub * 8);
+      const float4* x = reinterpret_cast<const float4*>(at(i0 + j).o + sub * 8);
       const float4 a = x[0], b = x[1];
       const float wj = __shfl_sync(group, w, j, GL);
       L += __shfl_sync(group, lw, j, GL);
@@ -205,6 +205,16 @@ struct Walk {
     return true;
   }
 };
+
+// Who writes p.cut: by CTA, each CTA at its start (none) and for the item that it begins and does not finish; by item,
+// the CTA that begins the item.
+__device__ __forceinline__ void cut_none(const Plan& p, int cta) {
+  if (!p.by_item) p.cut[cta] = make_int4(0, 0, 0, -1);
+}
+__device__ __forceinline__ void cut_begin(const Plan& p, int cta, const Walk& k, int last) {   // of an item with t0 = 0
+  if (k.t1 < k.nt) p.cut[p.by_item ? k.gi * p.nkv + k.h : cta] = make_int4(k.gi, k.h, cta, last);
+  else if (p.by_item) p.cut[k.gi * p.nkv + k.h] = make_int4(0, 0, 0, -1);
+}
 
 // The launch's items as every CTA sees them: s_pref [groups + 1] (tiles a head before each row block), s_lim and s_seq
 // [groups]. By all threads of the CTA; ends with a barrier.

@@ -125,13 +125,16 @@ __global__ void __launch_bounds__(Shape<D, NT, WN, WK, NS>::THREADS, CTAS)
     *abort_flag = 0;
     fence_mbar_init();
   }
-  PDL_ENTRY();
+  late_entry(p);
   lay_out(a, p, s_pref, s_lim, s_seq);
   const uint32_t tiles = (uint32_t)s_pref[p.groups] * nkv;
   const int pad = pad_of(p, tiles);
   const Share share(p, tiles, pad);
   if (threadIdx.x == 0) cut_none(p, blockIdx.x);
-  if (blockIdx.x >= share.ctas) return;
+  if (blockIdx.x >= share.ctas) {
+    if (threadIdx.x == 0) late_wait(p);
+    return;
+  }
   const Range range{s_pref, pad, nkv, p.groups, share.start(blockIdx.x), share.start(blockIdx.x + 1)};
 
   // The query vectors of an item as fp16 of q 2^-e, the factor that gives its scores in log2 units, what each sees. By
@@ -551,6 +554,7 @@ __global__ void __launch_bounds__(Shape<D, NT, WN, WK, NS>::THREADS, CTAS)
         named_bar_sync(1, NC);
       }
       const bool whole = t0 == 0 && t1 == nt;
+      if (whole) late_wait(p);
       if (threadIdx.x == 0 && t0 == 0) cut_begin(p, blockIdx.x, k, (int)share.cta_of(k.base + pad + nt - 1));
       const int slot = 2 * blockIdx.x + (t0 == 0 ? 1 : 0);
       for (int x = threadIdx.x; x < nqv * (D / 8); x += NC) {
@@ -581,6 +585,7 @@ __global__ void __launch_bounds__(Shape<D, NT, WN, WK, NS>::THREADS, CTAS)
         }
       }
     }
+    if (threadIdx.x == 0) late_wait(p);
   }
 }
 
@@ -779,6 +784,7 @@ int kv8_attention(cudaStream_t st, const Kv8Attn& a) {
   if (blocks > 0x7fffffffll || (double)std::min<long long>(blocks, KV8_MAX_GROUPS) * (a.c.cap / TK + 32) * a.c.nkv > 2e9) return -1;
   for (long long g0 = 0; g0 < blocks; g0 += KV8_MAX_GROUPS) {
     p.g0 = (int)g0;
+    p.late = a.P && g0 == 0;
     p.groups = (int)std::min<long long>(KV8_MAX_GROUPS, blocks - g0);
     const cudaError_t e = a.c.d == 128 ? launch_mma<128>(st, a, p, mk, mv) : launch_mma<64>(st, a, p, mk, mv);
     if (e != cudaSuccess) {

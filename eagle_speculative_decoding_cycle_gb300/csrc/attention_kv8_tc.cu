@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(T_THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tS0 = *tmem_slot + wk * TT, tO0 = *tmem_slot + 2 * TT + wk * TT;
-  PDL_ENTRY();
+  late_entry(p);
   lay_out(a, p, s_pref, s_lim, s_seq);
   const uint32_t tiles = (uint32_t)s_pref[p.groups] * a.c.nkv;
   const int pad = pad_of(p, tiles);
@@ -493,6 +493,7 @@ __global__ void __launch_bounds__(T_THREADS, 1)
       const size_t at = (size_t)row * a.nq + h * p.G + (r < nqv ? r - in * p.G : 0), stride = (size_t)a.R * a.nq;
       const size_t slot = (size_t)(2 * me + (done.t0 == 0 ? 1 : 0)) * p.qv_pad + r;
       const int n_prefix = whole ? p.n_prefix : 0;
+      if (whole) late_wait(p);
       const float own_top = top;
       for (int s = 0; s < n_prefix; ++s) top = fmaxf(top, p.pp_ml[2 * (s * stride + at)]);
       const float tb = top == -INFINITY ? 0.f : top, own = ex2(own_top - tb);
@@ -636,6 +637,7 @@ __global__ void __launch_bounds__(T_THREADS, 1)
       if (nv) kv8_wait_all(smem_u32(v_full), (uint32_t)((nv - 1) & 1), abort_flag, a.err, false);
     }
   }
+  if (threadIdx.x == 0) late_wait(p);
   tc_fence_before();
   __syncthreads();
   if (warp == 18) {

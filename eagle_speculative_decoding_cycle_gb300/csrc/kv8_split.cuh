@@ -50,7 +50,19 @@ struct Plan {
   int by_item;            // cut is indexed by item (no more items than CTAs), else by the item's first CTA
   const float *pp_o, *pp_ml;   // prefix partials [n_prefix][R * nq][D], [..][2]
   int n_prefix;
+  int late;               // the launch just before this one makes the prefix's partials: wait for it where they are read
 };
+
+// Behind the prefix kernel the own slots' kernel starts as soon as that one's last CTAs have started (they trigger it
+// after their own wait, so all that came before the call is complete), and waits for its partials where it reads them.
+// One thread of each CTA waits before it ends, so that the join finds both kernels complete.
+__device__ __forceinline__ void late_entry(const Plan& p) {
+  if (!p.late) pdl_wait();
+  pdl_trigger();
+}
+__device__ __forceinline__ void late_wait(const Plan& p) {
+  if (p.late) pdl_wait();
+}
 
 // The units W of a launch over its CTAs: the first `more` CTAs take `per` + 1, the others `per`. An item's tiles are its
 // last units, so a range that ends inside its first `pad` units has none of it.

@@ -73,7 +73,7 @@ __device__ __forceinline__ Part prefix_part(const Kv8Attn& a, const Plan& p, int
 }
 // Shared memory of one configuration: D dims; NT query tiles (of 8) a warp, WN warps side by side over the query
 // tiles, WK groups of them over the keys; NS tiles in the ring.
-template <int D, int NT, int WN, int WK, int NS>
+template <int D, int NT, int WN, int WK, int NS, int CTAS>
 struct Shape {
   static_assert(NS < 32, "a producer lane has at most one tile in flight");
   static constexpr int QV = 8 * NT * WN, NW = WN * WK;
@@ -89,17 +89,26 @@ struct Shape {
   static constexpr int OFF_Q = OFF_EXP + NS * 2 * TK;
   static constexpr int Q_BUF = QV * (Q_LD + 8 + 32);      // query rows, (factor, slot limit) of each, masks
   static constexpr int OFF_O = OFF_Q + 2 * Q_BUF;
-  static constexpr int OFF_MLE = OFF_O + QV * O_LD * 4;   // m, l of each key group
-  static constexpr int OFF_BAR = OFF_MLE + WK * QV * 8;
+  // Key groups that write their O side by side: all of them where shared memory lasts for NS tiles and 512 row blocks
+  static constexpr int O_BUF = QV * O_LD * 4, MLE = 2 * WK * QV * 8;   // m, l of each key group, by item parity
+  static constexpr int bytes_with(int nr, int groups) {
+    return 1024 + OFF_O + nr * O_BUF + MLE + NS * 16 + 192 + (3 * groups + 1) * 4;
+  }
+  static constexpr int ROOM = (228 / CTAS - 1) * 1024;
+  static constexpr int regions(int nr) { return nr == 1 || bytes_with(nr, KV8_MAX_GROUPS) <= ROOM ? nr : regions(nr / 2); }
+  static constexpr int NR = regions(WK);
+  static_assert(bytes_with(NR, KV8_MAX_GROUPS) <= ROOM, "shared memory");
+  static constexpr int OFF_MLE = OFF_O + NR * O_BUF;
+  static constexpr int OFF_BAR = OFF_MLE + MLE;
   static constexpr int OFF_GROUP = OFF_BAR + NS * 16 + 192;
-  static int bytes(int groups) { return 1024 + OFF_GROUP + (3 * groups + 1) * 4; }
+  static int bytes(int groups) { return bytes_with(NR, groups); }
 };
 
 template <int D, int NT, int WN, int WK, int NS, int CTAS>
-__global__ void __launch_bounds__(Shape<D, NT, WN, WK, NS>::THREADS, CTAS)
+__global__ void __launch_bounds__(Shape<D, NT, WN, WK, NS, CTAS>::THREADS, CTAS)
     kv8_attn_k(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Kv8Attn a,
                const Plan p) {
-  using Sh = Shape<D, NT, WN, WK, NS>;
+  using Sh = Shape<D, NT, WN, WK, NS, CTAS>;
   constexpr int NW = Sh::NW, NC = NW * 32;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = smem_raw + (-smem_u32(smem_raw) & 1023u);   // (not by pointer masks: accesses then lose the shared space)
@@ -107,7 +116,7 @@ __global__ void __launch_bounds__(Shape<D, NT, WN, WK, NS>::THREADS, CTAS)
   uint64_t* empty = full + NS;
   uint64_t *q_full = empty + NS, *q_empty = q_full + 2;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(q_empty + 2);
-  int* s_fullvis = reinterpret_cast<int*>(q_empty + 2) + 1;   // [2][16], by warp
+  int* s_fullvis = reinterpret_cast<int*>(q_empty + 2) + 1;   // [2][16], by warp; [15] the context's length
   int* s_pref = reinterpret_cast<int*>(sm + Sh::OFF_GROUP);
   int* s_lim = s_pref + p.groups + 1;
   int* s_seq = s_lim + p.groups;
@@ -202,7 +211,7 @@ __global__ void __launch_bounds__(Shape<D, NT, WN, WK, NS>::THREADS, CTAS)
           w[k] = fine ? half2_of(__uint_as_float(r[k] << 16) * up * up2, __uint_as_float(r[k] & 0xffff0000u) * up * up2)
                       : 0x7fff7fffu;
         if (x < Sh::QV) {
-          const int l = live ? max(0, min(lim[b], a.c.cap)) : 0;
+          const int l = live ? max(0, min(lim[b], a.c.cap)) : -1;   // -1: padding
           *reinterpret_cast<uint4*>(q_rows + x * Sh::Q_LD + sub * 16) = make_uint4(w[0], w[1], w[2], w[3]);
           if (sub == 0) q_cols[x] = make_float2(sl2 * pow2i(e / 2) * pow2i(e - e / 2), __int_as_float(l));
           if (live) fullvis = min(fullvis, l);
@@ -211,6 +220,7 @@ __global__ void __launch_bounds__(Shape<D, NT, WN, WK, NS>::THREADS, CTAS)
     }
     fullvis = __reduce_min_sync(0xffffffffu, fullvis);
     if (lane == 0) s_fullvis[buf * 16 + sw] = fullvis;
+    if (sw == 0 && lane == 0) s_fullvis[buf * 16 + 15] = ctx;
     __syncwarp();
   };
   constexpr int FIRST = (NW + Sh::ROWS_W) * 32;   // threads that prepare the first item
@@ -295,8 +305,6 @@ __global__ void __launch_bounds__(Shape<D, NT, WN, WK, NS>::THREADS, CTAS)
     if constexpr (Sh::SPLIT_REGS) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
     const int kw = warp / WN, nw = warp % WN;
     const int g = lane >> 2, t4 = lane & 3;
-    float* s_m = reinterpret_cast<float*>(sm + Sh::OFF_MLE);
-    float* s_l = s_m + WK * Sh::QV;
     float* s_o = reinterpret_cast<float*>(sm + Sh::OFF_O);
     Walk k;
     bool more = k.begin(range);
@@ -308,18 +316,18 @@ __global__ void __launch_bounds__(Shape<D, NT, WN, WK, NS>::THREADS, CTAS)
     int i = 0;   // tiles of the range that are behind
     for (int item = 0; more; ++item, more = k.next(range)) {
       const int gi = k.gi, h = k.h, t0 = k.t0, t1 = k.t1, nt = k.nt;
-      const int seq = s_seq[gi], limit = s_lim[gi];
+      const int limit = s_lim[gi];
       const int sidx = (p.g0 + gi) / p.nb, rb = (p.g0 + gi) - sidx * p.nb;
       const int r0 = sidx * a.rows_per_seq + rb * p.RB;
       const int r1 = min(min(r0 + p.RB, (sidx + 1) * a.rows_per_seq), a.R);
       const int nqv = (r1 - r0) * p.G;
-      const int ctx = a.mode == 1 && seq >= 0 ? a.ctx_len[seq] : 0;
 
       const int buf = item & 1;
       const uint8_t* s_q = sm + Sh::OFF_Q + buf * Sh::Q_BUF;
       const float2* s_col = reinterpret_cast<const float2*>(s_q + Sh::QV * Sh::Q_LD);
       const uint64_t* s_mask = reinterpret_cast<const uint64_t*>(s_col + Sh::QV);
       if (item) kv8_wait(smem_u32(q_full + buf), (uint32_t)((item / 2 - (buf == 0)) & 1), abort_flag, a.err);
+      const int ctx = s_fullvis[buf * 16 + 15];
       int fullvis = s_fullvis[buf * 16];
       for (int w = 1; w < (item ? Sh::ROWS_W : NW + Sh::ROWS_W); ++w) fullvis = min(fullvis, s_fullvis[buf * 16 + w]);
 
@@ -511,8 +519,9 @@ __global__ void __launch_bounds__(Shape<D, NT, WN, WK, NS>::THREADS, CTAS)
         warp_arrive(smem_u32(empty + st));
       }
 
-      warp_arrive(smem_u32(q_empty + buf));
       // join the key groups: sums in the order of the groups
+      float* s_m = reinterpret_cast<float*>(sm + Sh::OFF_MLE) + buf * 2 * WK * Sh::QV;
+      float* s_l = s_m + WK * Sh::QV;
 #pragma unroll
       for (int x = 0; x < NT; ++x)
 #pragma unroll
@@ -527,21 +536,22 @@ __global__ void __launch_bounds__(Shape<D, NT, WN, WK, NS>::THREADS, CTAS)
             s_l[at] = v;
           }
         }
-      named_bar_sync(1, NC);
+      named_bar_sync(1, NC);   // (and the item before has been read from s_o)
       const float unit = E_run ? pow2i(E_run - KV8_BIAS) : 1.f;
 #pragma unroll 1
-      for (int r = 0; r < WK; ++r) {
-        if (r == kw) {
+      for (int r = 0; r < WK; r += Sh::NR) {
+        if (r == kw / Sh::NR * Sh::NR) {
 #pragma unroll
           for (int x = 0; x < NT; ++x)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const int col = (nw * NT + x) * 8 + 2 * t4 + e;
+              if (col >= nqv) continue;
               float top = s_m[col];
 #pragma unroll
               for (int k = 1; k < WK; ++k) top = fmaxf(top, s_m[k * Sh::QV + col]);
               const float f = ex2(m[x][e] - (top == -INFINITY ? 0.f : top)) * unit;
-              float* o = s_o + col * Sh::O_LD + 2 * g;
+              float* o = s_o + (kw % Sh::NR * Sh::QV + col) * Sh::O_LD + 2 * g;
 #pragma unroll
               for (int c = 0; c < D / 16; ++c) {
                 float2 v = r ? *reinterpret_cast<float2*>(o + 16 * c) : make_float2(0.f, 0.f);
@@ -566,24 +576,27 @@ __global__ void __launch_bounds__(Shape<D, NT, WN, WK, NS>::THREADS, CTAS)
 #pragma unroll
         for (int k = 0; k < WK; ++k)
           L += s_l[k * Sh::QV + col] * ex2(s_m[k * Sh::QV + col] - (top == -INFINITY ? 0.f : top));
-        const float4 u = *reinterpret_cast<const float4*>(s_o + col * Sh::O_LD + c);
-        const float4 v = *reinterpret_cast<const float4*>(s_o + col * Sh::O_LD + c + 4);
-        o[0] = u.x; o[1] = u.y; o[2] = u.z; o[3] = u.w; o[4] = v.x; o[5] = v.y; o[6] = v.z; o[7] = v.w;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = 0.f;
+#pragma unroll
+        for (int k = 0; k < Sh::NR; ++k) {
+          const float* src = s_o + (k * Sh::QV + col) * Sh::O_LD + c;
+          const float4 u = *reinterpret_cast<const float4*>(src), v = *reinterpret_cast<const float4*>(src + 4);
+          o[0] += u.x; o[1] += u.y; o[2] += u.z; o[3] += u.w; o[4] += v.x; o[5] += v.y; o[6] += v.z; o[7] += v.w;
+        }
         if (whole) {
           const int in = (int)(col * p.G_inv >> 16), row = r0 + in;
           const size_t at = (size_t)row * a.nq + h * p.G + col - in * p.G;
           fold<D>(p.n_prefix, [&](int k) { return prefix_part<D>(a, p, k, at); }, c / 8, top, L, o);
-          store8(a, at, D, c, seq >= 0 && a.row_seq[row] == seq, L, o);
+          store8(a, at, D, c, __float_as_int(s_col[col].y) >= 0, L, o);
         } else {
           const size_t q = (size_t)slot * p.qv_pad + col;
-          *reinterpret_cast<float4*>(p.part_o + q * D + c) = u;
-          *reinterpret_cast<float4*>(p.part_o + q * D + c + 4) = v;
-          if (c == 0) {
-            p.part_ml[2 * q] = top;
-            p.part_ml[2 * q + 1] = L;
-          }
+          *reinterpret_cast<float4*>(p.part_o + q * D + c) = make_float4(o[0], o[1], o[2], o[3]);
+          *reinterpret_cast<float4*>(p.part_o + q * D + c + 4) = make_float4(o[4], o[5], o[6], o[7]);
+          if (c == 0) *reinterpret_cast<float2*>(p.part_ml + 2 * q) = make_float2(top, L);
         }
       }
+      warp_arrive(smem_u32(q_empty + buf));
     }
     if (threadIdx.x == 0) late_wait(p);
   }
@@ -708,7 +721,7 @@ cudaError_t launch_join(cudaStream_t st, const Kv8Attn& a, Plan& p) {
 
 template <int D, int NT, int WN, int WK, int NS, int CTAS>
 cudaError_t launch_own(cudaStream_t st, const Kv8Attn& a, Plan& p, const CUtensorMap& mk, const CUtensorMap& mv) {
-  using Sh = Shape<D, NT, WN, WK, NS>;
+  using Sh = Shape<D, NT, WN, WK, NS, CTAS>;
   const auto fn = kv8_attn_k<D, NT, WN, WK, NS, CTAS>;
   p.grid = std::min(KV8_MAX_CTAS, CTAS * device_sm_count());
   p.by_item = p.groups * p.nkv <= p.grid;
@@ -726,7 +739,7 @@ cudaError_t launch_own(cudaStream_t st, const Kv8Attn& a, Plan& p, const CUtenso
 template <int D>
 cudaError_t launch_mma(cudaStream_t st, const Kv8Attn& a, Plan& p, const CUtensorMap& mk, const CUtensorMap& mv) {
   const int t = p.qv_pad / 8;
-  if (t <= 1) return launch_own<D, 1, 1, 4, 11, 2>(st, a, p, mk, mv);
+  if (t <= 1) return launch_own<D, 1, 1, 4, 10, 2>(st, a, p, mk, mv);
   if (t <= 2) return launch_own<D, 2, 1, 4, 9, 2>(st, a, p, mk, mv);
   if (t <= 4) return launch_own<D, 4, 1, 8, 20, 1>(st, a, p, mk, mv);
   if constexpr (D == 64) {

@@ -26,7 +26,9 @@ namespace eagle {
 namespace {
 
 constexpr int PT = 128;            // keys a tile, query vectors a tile
-constexpr int PF_THREADS = 384;
+constexpr int PH = PT / 2;         // keys a thread
+constexpr int PF_SOFT = 16;        // softmax warps
+constexpr int PF_THREADS = 640;
 constexpr float PF_LAZY = 8.f;
 constexpr int PF_SMS = 152;        // CTAs that run at once (one an SM)
 
@@ -34,7 +36,8 @@ template <int D>
 struct PfShape {
   static constexpr int HALVES = D / 64, HALF = PT * 128;        // 64 dims of 128 rows
   static constexpr int OP = HALVES * HALF;                      // one operand tile
-  static constexpr int OFF_Q = 0, OFF_K = 2 * OP, OFF_V = OFF_K + 2 * OP, OFF_BAR = OFF_V + 2 * OP;
+  static constexpr int OFF_Q = 0, OFF_K = 2 * OP, OFF_V = OFF_K + 2 * OP, OFF_X = OFF_V + 2 * OP;
+  static constexpr int OFF_BAR = OFF_X + 2 * 2 * 2 * PT * 4;   // [parity][tile][half][query vector]
   static constexpr int BYTES = 1024 + OFF_BAR + 256;
 };
 
@@ -166,42 +169,46 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 9) tmem_alloc(smem_u32(tmem_slot), 512);
+  if (warp == PF_SOFT + 1) tmem_alloc(smem_u32(tmem_slot), 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   PDL_ENTRY();
 
-  if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
-    const int mt = warp >> 2, qv = threadIdx.x & 127;
+  if (warp < PF_SOFT) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+    const int mt = warp >> 3, hf = (warp >> 2) & 1, qv = threadIdx.x & 127;
+    float* s_x = reinterpret_cast<float*>(sm + Sh::OFF_X) + mt * 2 * PT + qv;   // this query vector's maxima, by half
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + mt * PT + lane_off, tO = tmem + 2 * PT + mt * D + lane_off;
     float m = -INFINITY, l = 0.f;
-    bool ok = mt < nmt;
-    for (int i = 0; ok && i < nt; ++i) {
-      ok = kv8_wait(smem_u32(s_full + mt), (uint32_t)(i & 1), abort_flag, a.err);
-      if (!ok) break;
+    // (a wait that gave up ends no loop here: the two warps of a query vector meet at barriers)
+    for (int i = 0; mt < nmt && i < nt; ++i) {
+      kv8_wait(smem_u32(s_full + mt), (uint32_t)(i & 1), abort_flag, a.err);
       tc_fence_after();
-      float s[PT];
+      float s[PH];
 #pragma unroll
-      for (int c = 0; c < PT; c += 32) tmem_ld32_async(tS + c, s + c);
+      for (int c = 0; c < PH; c += 32) tmem_ld32_async(tS + hf * PH + c, s + c);
 #pragma unroll
-      for (int c = 0; c < PT; c += 32) tmem_wait_ld(s + c);
-      const int last = a.P - (t0 + i) * PT;    // keys of this tile, 128 but for the prefix's end
-      if (last < PT)
+      for (int c = 0; c < PH; c += 32) tmem_wait_ld(s + c);
+      const int last = a.P - (t0 + i) * PT - hf * PH;    // keys of this half, 64 but at the prefix's end
+      if (last < PH)
 #pragma unroll
-        for (int c = 0; c < PT; ++c) s[c] = c < last ? s[c] : -INFINITY;
+        for (int c = 0; c < PH; ++c) s[c] = c < last ? s[c] : -INFINITY;
       float x0 = s[0], x1 = s[1], x2 = s[2], x3 = s[3];
 #pragma unroll
-      for (int c = 4; c + 7 < PT; c += 8) {
+      for (int c = 4; c + 7 < PH; c += 8) {
         x0 = max3(x0, s[c], s[c + 1]);
         x1 = max3(x1, s[c + 2], s[c + 3]);
         x2 = max3(x2, s[c + 4], s[c + 5]);
         x3 = max3(x3, s[c + 6], s[c + 7]);
       }
-      const float mx = fmaxf(max3(x0, x1, fmaxf(s[PT - 4], s[PT - 3])), max3(x2, x3, fmaxf(s[PT - 2], s[PT - 1])));
+      float mx = fmaxf(max3(x0, x1, fmaxf(s[PH - 4], s[PH - 3])), max3(x2, x3, fmaxf(s[PH - 2], s[PH - 1])));
+      float* x = s_x + (i & 1) * 4 * PT;
+      x[hf * PT] = mx;
+      named_bar_sync(1 + mt * 4 + (warp & 3), 64);   // the two warps of these query vectors
+      mx = fmaxf(mx, x[(hf ^ 1) * PT]);
       const bool raise = (mx - m) * a.sl2 > PF_LAZY;
       float corr = 1.f;
       if (raise) {
@@ -210,12 +217,11 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
         l *= corr;
       }
       if (i > 0 && __any_sync(0xffffffffu, raise)) {
-        // the last product into O must be there before O is rescaled
-        ok = kv8_wait(smem_u32(o_done + mt), (uint32_t)((i - 1) & 1), abort_flag, a.err);
-        if (!ok) break;
+        // the last product into O must be there before O is rescaled, half of its columns by either warp
+        kv8_wait(smem_u32(o_done + mt), (uint32_t)((i - 1) & 1), abort_flag, a.err);
         tc_fence_after();
 #pragma unroll 1
-        for (int c = 0; c < D; c += 16) {
+        for (int c = hf * (D / 2); c < (hf + 1) * (D / 2); c += 16) {
           float o[16];
           tmem_ld16(tO + c, o);
 #pragma unroll
@@ -227,7 +233,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
       const f32x2 nm = two(-m, -m), s2 = two(a.sl2, a.sl2);
       f32x2 sum[2] = {two(0.f, 0.f), two(0.f, 0.f)};
 #pragma unroll
-      for (int qt = 0; qt < 4; ++qt) {
+      for (int qt = 0; qt < PH / 32; ++qt) {
         uint32_t w[16];
 #pragma unroll
         for (int c = 0; c < 32; c += 2) {
@@ -238,13 +244,11 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
           const __nv_bfloat162 b = __floats2bfloat162_rn(x.x, x.y);
           w[c / 2] = *reinterpret_cast<const uint32_t*>(&b);
         }
-        tmem_st16u(tS + qt * 16, w);
-        if (qt & 1) {
-          tmem_wait_st();
-          tc_fence_before();
-          warp_arrive(smem_u32(p_full + 2 * mt + qt / 2));   // the first half's product starts under the second half
-        }
+        tmem_st16u(tS + hf * PH + qt * 16, w);
       }
+      tmem_wait_st();
+      tc_fence_before();
+      warp_arrive(smem_u32(p_full + 2 * mt + hf));
       const float2 sums = one_by_one(add2(sum[0], sum[1]));
       l += sums.x + sums.y;
     }
@@ -252,10 +256,14 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
       const int row = r0 + mt * a.RB + qv / a.G;
       const bool write = qv < a.RB * a.G && row < a.R;
       const size_t q = (size_t)split * a.R * a.nq + (size_t)row * a.nq + h * a.G + qv % a.G;
-      if (ok && kv8_wait(smem_u32(o_done + mt), (uint32_t)((nt - 1) & 1), abort_flag, a.err)) {
+      float* x = s_x + (nt & 1) * 4 * PT;   // the parity that the last tile did not use
+      x[hf * PT] = l;
+      named_bar_sync(1 + mt * 4 + (warp & 3), 64);
+      l = x[0] + x[PT];
+      if (kv8_wait(smem_u32(o_done + mt), (uint32_t)((nt - 1) & 1), abort_flag, a.err)) {
         tc_fence_after();
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
+        for (int c = hf * (D / 2); c < (hf + 1) * (D / 2); c += 32) {
           float o[32];
           tmem_ld32(tO + c, o);
           if (write)
@@ -263,15 +271,15 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
             for (int j = 0; j < 32; j += 4)
               *reinterpret_cast<float4*>(a.o + q * D + c + j) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
         }
-        if (write) {
+        if (write && hf == 0) {
           a.ml[2 * q] = m * a.sl2;
           a.ml[2 * q + 1] = l;
         }
       }
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-    if (warp == 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if (warp == PF_SOFT) {
       // ---- TMA ----
       const int qbytes = a.RB * a.G * 128;
       if (elect_one()) {
@@ -307,7 +315,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
         for (int j = max(0, nk - 2); j < nk; ++j) kv8_wait_all(smem_u32(k_full + (j & 1)), (uint32_t)((j / 2) & 1), abort_flag, a.err, false);
         for (int j = max(0, nv - 2); j < nv; ++j) kv8_wait_all(smem_u32(v_full + (j & 1)), (uint32_t)((j / 2) & 1), abort_flag, a.err, false);
       }
-    } else if (warp == 9) {
+    } else if (warp == PF_SOFT + 1) {
       // ---- MMA ----
       constexpr uint32_t IS = pf_idesc(PT, false), IO = pf_idesc(D, true);
       // operand descriptors; an offset of n bytes adds n >> 4
@@ -344,7 +352,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
             tc_fence_after();
             if (elect_one()) {
               uint64_t vd = v + hf * (4 * 2048 >> 4);
-              uint32_t pa = tmem + mt * PT + hf * 32, acc = i || hf ? 1u : 0u;
+              uint32_t pa = tmem + mt * PT + hf * PH, acc = i || hf ? 1u : 0u;
 #pragma unroll
               for (int x = 0; x < 4; ++x, vd += 2048 >> 4, pa += 8, acc = 1) mma_ts(tmem + 2 * PT + mt * D, pa, vd, IO, acc);
               if (hf) {
@@ -371,7 +379,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == PF_SOFT + 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }

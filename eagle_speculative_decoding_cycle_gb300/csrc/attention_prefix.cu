@@ -26,9 +26,8 @@ namespace eagle {
 namespace {
 
 constexpr int PT = 128;            // keys a tile, query vectors a tile
-constexpr int PH = PT / 2;         // keys a thread
-constexpr int PF_SOFT = 16;        // softmax warps
-constexpr int PF_THREADS = 640;
+constexpr int PH = PT / 2;         // keys of one S: half a tile
+constexpr int PF_THREADS = 384;
 constexpr float PF_LAZY = 8.f;
 constexpr int PF_SMS = 152;        // CTAs that run at once (one an SM)
 
@@ -36,8 +35,7 @@ template <int D>
 struct PfShape {
   static constexpr int HALVES = D / 64, HALF = PT * 128;        // 64 dims of 128 rows
   static constexpr int OP = HALVES * HALF;                      // one operand tile
-  static constexpr int OFF_Q = 0, OFF_K = 2 * OP, OFF_V = OFF_K + 2 * OP, OFF_X = OFF_V + 2 * OP;
-  static constexpr int OFF_BAR = OFF_X + 2 * 2 * 2 * PT * 4;   // [parity][tile][half][query vector]
+  static constexpr int OFF_Q = 0, OFF_K = 2 * OP, OFF_V = OFF_K + 2 * OP, OFF_BAR = OFF_V + 2 * OP;
   static constexpr int BYTES = 1024 + OFF_BAR + 256;
 };
 
@@ -144,8 +142,8 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
   uint8_t* sm = pf_smem + (-smem_u32(pf_smem) & 1023u);   // (not by pointer masks: accesses then lose the shared space)
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + Sh::OFF_BAR);
   uint64_t *q_full = bars, *k_full = bars + 1, *k_empty = bars + 3, *v_full = bars + 5, *v_empty = bars + 7,
-           *s_full = bars + 9, *p_full = bars + 11 /* [tile][half] */, *o_done = bars + 15, *drain = bars + 17;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 18);
+           *s_full = bars + 9 /* [tile][half] */, *p_full = bars + 13 /* [tile][half] */, *o_done = bars + 17 /* [tile][half] */, *drain = bars + 21 /* [tile] */;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 23);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5;
   const int split = blockIdx.x % a.splits, pair = blockIdx.x / a.splits % a.pairs, h = blockIdx.x / (a.splits * a.pairs);
@@ -157,39 +155,42 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
     mbar_init(smem_u32(q_full), 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(k_full + i), 1);
-      mbar_init(smem_u32(k_empty + i), 1);
+      mbar_init(smem_u32(k_empty + i), nmt);
       mbar_init(smem_u32(v_full + i), 1);
-      mbar_init(smem_u32(v_empty + i), 1);
-      mbar_init(smem_u32(s_full + i), 1);
-      mbar_init(smem_u32(p_full + 2 * i), 4);
-      mbar_init(smem_u32(p_full + 2 * i + 1), 4);
-      mbar_init(smem_u32(o_done + i), 1);
+      mbar_init(smem_u32(v_empty + i), nmt);
+      mbar_init(smem_u32(drain + i), 1);
+      for (int hf = 0; hf < 2; ++hf) {
+        mbar_init(smem_u32(s_full + 2 * i + hf), 1);
+        mbar_init(smem_u32(p_full + 2 * i + hf), 4);
+        mbar_init(smem_u32(o_done + 2 * i + hf), 1);
+      }
     }
-    mbar_init(smem_u32(drain), 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == PF_SOFT + 1) tmem_alloc(smem_u32(tmem_slot), 512);
+  if (warp == 9) tmem_alloc(smem_u32(tmem_slot), 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   PDL_ENTRY();
 
-  if (warp < PF_SOFT) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
-    const int mt = warp >> 3, hf = (warp >> 2) & 1, qv = threadIdx.x & 127;
-    float* s_x = reinterpret_cast<float*>(sm + Sh::OFF_X) + mt * 2 * PT + qv;   // this query vector's maxima, by half
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+    const int mt = warp >> 2, qv = threadIdx.x & 127;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + mt * PT + lane_off, tO = tmem + 2 * PT + mt * D + lane_off;
     float m = -INFINITY, l = 0.f;
-    // (a wait that gave up ends no loop here: the two warps of a query vector meet at barriers)
-    for (int i = 0; mt < nmt && i < nt; ++i) {
-      kv8_wait(smem_u32(s_full + mt), (uint32_t)(i & 1), abort_flag, a.err);
+    bool ok = mt < nmt;
+    for (int j = 0; ok && j < 2 * nt; ++j) {   // halves of the key tiles
+      const int i = j >> 1, hf = j & 1;
+      const uint32_t tP = tS + hf * PH;
+      ok = kv8_wait(smem_u32(s_full + 2 * mt + hf), (uint32_t)(i & 1), abort_flag, a.err);
+      if (!ok) break;
       tc_fence_after();
       float s[PH];
 #pragma unroll
-      for (int c = 0; c < PH; c += 32) tmem_ld32_async(tS + hf * PH + c, s + c);
+      for (int c = 0; c < PH; c += 32) tmem_ld32_async(tP + c, s + c);
 #pragma unroll
       for (int c = 0; c < PH; c += 32) tmem_wait_ld(s + c);
       const int last = a.P - (t0 + i) * PT - hf * PH;    // keys of this half, 64 but at the prefix's end
@@ -204,11 +205,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
         x2 = max3(x2, s[c + 4], s[c + 5]);
         x3 = max3(x3, s[c + 6], s[c + 7]);
       }
-      float mx = fmaxf(max3(x0, x1, fmaxf(s[PH - 4], s[PH - 3])), max3(x2, x3, fmaxf(s[PH - 2], s[PH - 1])));
-      float* x = s_x + (i & 1) * 4 * PT;
-      x[hf * PT] = mx;
-      named_bar_sync(1 + mt * 4 + (warp & 3), 64);   // the two warps of these query vectors
-      mx = fmaxf(mx, x[(hf ^ 1) * PT]);
+      const float mx = fmaxf(max3(x0, x1, fmaxf(s[PH - 4], s[PH - 3])), max3(x2, x3, fmaxf(s[PH - 2], s[PH - 1])));
       const bool raise = (mx - m) * a.sl2 > PF_LAZY;
       float corr = 1.f;
       if (raise) {
@@ -216,16 +213,17 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
         m = mx;
         l *= corr;
       }
-      if (i > 0 && __any_sync(0xffffffffu, raise)) {
-        // the last product into O must be there before O is rescaled, half of its columns by either warp
-        kv8_wait(smem_u32(o_done + mt), (uint32_t)((i - 1) & 1), abort_flag, a.err);
+      if (j > 0 && __any_sync(0xffffffffu, raise)) {
+        // the last product into O must be there before O is rescaled (the one before it is: this S came behind it)
+        ok = kv8_wait(smem_u32(o_done + 2 * mt + (hf ^ 1)), (uint32_t)(((j - 1) >> 1) & 1), abort_flag, a.err);
+        if (!ok) break;
         tc_fence_after();
 #pragma unroll 1
-        for (int c = hf * (D / 2); c < (hf + 1) * (D / 2); c += 16) {
+        for (int c = 0; c < D; c += 16) {
           float o[16];
           tmem_ld16(tO + c, o);
 #pragma unroll
-          for (int j = 0; j < 16; ++j) o[j] *= corr;
+          for (int x = 0; x < 16; ++x) o[x] *= corr;
           tmem_st16(tO + c, o);
         }
       }
@@ -244,7 +242,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
           const __nv_bfloat162 b = __floats2bfloat162_rn(x.x, x.y);
           w[c / 2] = *reinterpret_cast<const uint32_t*>(&b);
         }
-        tmem_st16u(tS + hf * PH + qt * 16, w);
+        tmem_st16u(tP + qt * 16, w);
       }
       tmem_wait_st();
       tc_fence_before();
@@ -256,14 +254,10 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
       const int row = r0 + mt * a.RB + qv / a.G;
       const bool write = qv < a.RB * a.G && row < a.R;
       const size_t q = (size_t)split * a.R * a.nq + (size_t)row * a.nq + h * a.G + qv % a.G;
-      float* x = s_x + (nt & 1) * 4 * PT;   // the parity that the last tile did not use
-      x[hf * PT] = l;
-      named_bar_sync(1 + mt * 4 + (warp & 3), 64);
-      l = x[0] + x[PT];
-      if (kv8_wait(smem_u32(o_done + mt), (uint32_t)((nt - 1) & 1), abort_flag, a.err)) {
+      if (ok && kv8_wait(smem_u32(o_done + 2 * mt + 1), (uint32_t)((nt - 1) & 1), abort_flag, a.err)) {
         tc_fence_after();
 #pragma unroll 1
-        for (int c = hf * (D / 2); c < (hf + 1) * (D / 2); c += 32) {
+        for (int c = 0; c < D; c += 32) {
           float o[32];
           tmem_ld32(tO + c, o);
           if (write)
@@ -271,15 +265,15 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
             for (int j = 0; j < 32; j += 4)
               *reinterpret_cast<float4*>(a.o + q * D + c + j) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
         }
-        if (write && hf == 0) {
+        if (write) {
           a.ml[2 * q] = m * a.sl2;
           a.ml[2 * q + 1] = l;
         }
       }
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-    if (warp == PF_SOFT) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    if (warp == 8) {
       // ---- TMA ----
       const int qbytes = a.RB * a.G * 128;
       if (elect_one()) {
@@ -315,71 +309,66 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
         for (int j = max(0, nk - 2); j < nk; ++j) kv8_wait_all(smem_u32(k_full + (j & 1)), (uint32_t)((j / 2) & 1), abort_flag, a.err, false);
         for (int j = max(0, nv - 2); j < nv; ++j) kv8_wait_all(smem_u32(v_full + (j & 1)), (uint32_t)((j / 2) & 1), abort_flag, a.err, false);
       }
-    } else if (warp == PF_SOFT + 1) {
-      // ---- MMA ----
-      constexpr uint32_t IS = pf_idesc(PT, false), IO = pf_idesc(D, true);
+    } else if (warp <= 8 + nmt) {
+      // ---- MMA: one warp a query tile (both by one warp: 4 waits a tile, some 250 clocks each though what they wait for is
+      // there, held the tensor cores up) ----
+      constexpr uint32_t IS = pf_idesc(PH, false), IO = pf_idesc(D, true);
+      const int mt = warp - 9;
+      const uint32_t tS = tmem + mt * PT, tO = tmem + 2 * PT + mt * D;
       // operand descriptors; an offset of n bytes adds n >> 4
-      const uint64_t dq = sdesc_sw128(smem_u32(sm + Sh::OFF_Q)), dk = sdesc_sw128(smem_u32(sm + Sh::OFF_K)),
+      const uint64_t dq = sdesc_sw128(smem_u32(sm + Sh::OFF_Q + mt * Sh::OP)), dk = sdesc_sw128(smem_u32(sm + Sh::OFF_K)),
                      dv = pf_desc_mn(smem_u32(sm + Sh::OFF_V), Sh::HALF);
-      bool ok = kv8_wait_all(smem_u32(q_full), 0, abort_flag, a.err);
-      auto issue_s = [&](int mt, int i) {
-        if (elect_one()) {
-          uint64_t q = dq + mt * (Sh::OP >> 4), k = dk + (i & 1) * (Sh::OP >> 4);
-          uint32_t acc = 0;
+      auto issue_s = [&](int i, int hf) {   // by one lane
+        const uint64_t k = dk + (((i & 1) * Sh::OP + hf * PH * 128) >> 4);
 #pragma unroll
-          for (int hd = 0; hd < Sh::HALVES; ++hd, q += (Sh::HALF >> 4) - 8, k += (Sh::HALF >> 4) - 8)
-#pragma unroll
-            for (int x = 0; x < 4; ++x, q += 2, k += 2, acc = 1) tc_mma_bf16(tmem + mt * PT, q, k, IS, acc);
-          tc_commit(smem_u32(s_full + mt));
-          if (mt == nmt - 1) tc_commit(smem_u32(k_empty + (i & 1)));
+        for (int x = 0; x < D / 16; ++x) {
+          const int at = ((x >> 2) * Sh::HALF + (x & 3) * 32) >> 4;
+          tc_mma_bf16(tS + hf * PH, dq + at, k + at, IS, x ? 1u : 0u);
         }
-        __syncwarp();
+        tc_commit(smem_u32(s_full + 2 * mt + hf));
+        if (hf) tc_commit(smem_u32(k_empty + (i & 1)));
       };
-      if (ok) ok = kv8_wait_all(smem_u32(k_full), 0, abort_flag, a.err);
+      bool ok = kv8_wait_all(smem_u32(q_full), 0, abort_flag, a.err) && kv8_wait_all(smem_u32(k_full), 0, abort_flag, a.err);
       if (ok) {
         tc_fence_after();
-        for (int mt = 0; mt < nmt; ++mt) issue_s(mt, 0);
+        if (elect_one()) {
+          issue_s(0, 0);
+          issue_s(0, 1);
+        }
+        __syncwarp();
       }
       for (int i = 0; ok && i < nt; ++i) {
-        for (int mt = 0; ok && mt < nmt; ++mt) {
-          // P_i V_i, then S_(i+1) over the same columns: the tensor cores take them in this order
-          ok = mt || kv8_wait_all(smem_u32(v_full + (i & 1)), (uint32_t)((i / 2) & 1), abort_flag, a.err);
-          const uint64_t v = dv + (i & 1) * (Sh::OP >> 4);
-#pragma unroll 1
-          for (int hf = 0; hf < 2; ++hf) {
-            ok = ok && kv8_wait_all(smem_u32(p_full + 2 * mt + hf), (uint32_t)(i & 1), abort_flag, a.err);
-            if (!ok) break;
-            tc_fence_after();
-            if (elect_one()) {
-              uint64_t vd = v + hf * (4 * 2048 >> 4);
-              uint32_t pa = tmem + mt * PT + hf * PH, acc = i || hf ? 1u : 0u;
+        // P V of a half, then the next tile's S over the same columns: the tensor cores take them in this order. The operands
+        // are waited for before the weights, so that nothing stands between these and the products.
+        const bool next = i + 1 < nt;
+        ok = kv8_wait_all(smem_u32(v_full + (i & 1)), (uint32_t)((i / 2) & 1), abort_flag, a.err);
+        if (ok && next) ok = kv8_wait_all(smem_u32(k_full + ((i + 1) & 1)), (uint32_t)(((i + 1) / 2) & 1), abort_flag, a.err);
+        const uint64_t v = dv + (i & 1) * (Sh::OP >> 4);
 #pragma unroll
-              for (int x = 0; x < 4; ++x, vd += 2048 >> 4, pa += 8, acc = 1) mma_ts(tmem + 2 * PT + mt * D, pa, vd, IO, acc);
-              if (hf) {
-                tc_commit(smem_u32(o_done + mt));
-                if (mt == nmt - 1) tc_commit(smem_u32(v_empty + (i & 1)));
-              }
-            }
-            __syncwarp();
+        for (int hf = 0; hf < 2; ++hf) {
+          ok = ok && kv8_wait_all(smem_u32(p_full + 2 * mt + hf), (uint32_t)(i & 1), abort_flag, a.err);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              mma_ts(tO, tS + hf * PH + x * 8, v + ((hf * 4 + x) * 2048 >> 4), IO, i || hf || x ? 1u : 0u);
+            tc_commit(smem_u32(o_done + 2 * mt + hf));
+            if (hf) tc_commit(smem_u32(v_empty + (i & 1)));
+            if (next) issue_s(i + 1, hf);
           }
-          if (ok && i + 1 < nt) {
-            if (mt == 0) ok = kv8_wait_all(smem_u32(k_full + ((i + 1) & 1)), (uint32_t)(((i + 1) / 2) & 1), abort_flag, a.err);
-            if (ok) {
-              tc_fence_after();
-              issue_s(mt, i + 1);
-            }
-          }
+          __syncwarp();
         }
       }
       if (!ok) {   // products in flight end before the CTA frees its TMEM
-        if (elect_one()) tc_commit(smem_u32(drain));
-        kv8_wait_all(smem_u32(drain), 0, abort_flag, a.err, false);
+        if (elect_one()) tc_commit(smem_u32(drain + mt));
+        kv8_wait_all(smem_u32(drain + mt), 0, abort_flag, a.err, false);
       }
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == PF_SOFT + 1) {
+  if (warp == 9) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }

@@ -509,8 +509,8 @@ def kv8_read(cache: KV8Cache, row_seq: torch.Tensor, row_slot: torch.Tensor, dty
     n = row_seq.numel()
     if out is None:
         _need(dtype in _KV_TYPES, "entries are read as float32 or bfloat16")
-        both = torch.empty((2, n, cache.nkv, cache.d), dtype=dtype, device=cache.device)
-        k, v = both.unbind(0)
+        k = torch.empty((n, cache.nkv, cache.d), dtype=dtype, device=cache.device)
+        v = torch.empty_like(k)
     else:
         k, v = out
     R, code, ldk, ldv = _kv_rows(cache, k, v)

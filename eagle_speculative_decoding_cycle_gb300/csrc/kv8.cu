@@ -55,30 +55,14 @@ __device__ __forceinline__ uint32_t f32x2_e4m3x2(float lo, float hi) {
   return r;
 }
 
-// The vector that this thread's group of VT threads works on: (row, K or V, head), in the order of
-// the input rows.
-struct Place {
-  int row, head, seq;
-  bool is_v, pad;
-  long long vec;        // index in the cache; -1: none (padding, or out of range: latched)
-};
-
-__device__ __forceinline__ Place place_of(const Kv8& c, long long g, const int* row_seq, const int* row_slot, int* err,
-                                          bool leader) {
-  Place p;
-  p.row = (int)(g / (2 * c.nkv));
-  const int rem = (int)(g - (long long)p.row * 2 * c.nkv);
-  p.is_v = rem >= c.nkv;
-  p.head = p.is_v ? rem - c.nkv : rem;
-  p.seq = row_seq[p.row];
-  p.pad = p.seq < 0;
-  p.vec = -1;
-  if (!p.pad) {
-    const int slot = row_slot[p.row];
-    if (p.seq < c.max_batch && slot >= 0 && slot < c.cap) p.vec = kv8_vec(c, p.seq, p.head, slot);
-    if (p.vec < 0 && leader) latch_error(err, DEVERR_BOUNDS);
-  }
-  return p;
+// A row's vector in the cache; -1: none (padding, or out of range: latched).
+__device__ __forceinline__ long long vec_of(const Kv8& c, int row, int head, const int* row_seq, const int* row_slot,
+                                            int* err, bool leader) {
+  const int seq = row_seq[row], slot = row_slot[row];
+  if (seq < 0) return -1;
+  const long long vec = seq < c.max_batch && slot >= 0 && slot < c.cap ? kv8_vec(c, seq, head, slot) : -1;
+  if (vec < 0 && leader) latch_error(err, DEVERR_BOUNDS);
+  return vec;
 }
 
 template <typename T, int D>
@@ -90,10 +74,13 @@ __global__ void __launch_bounds__(KV8_THREADS)
   const long long g = ((long long)blockIdx.x * KV8_THREADS + threadIdx.x) / VT;
   if (g >= n) return;
   const int t = threadIdx.x % VT;
-  const Place p = place_of(c, g, row_seq, row_slot, err, t == 0);
+  const int row = (int)(g / (2 * c.nkv)), part = (int)(g - (long long)row * 2 * c.nkv);   // K heads, V heads
+  const bool is_v = part >= c.nkv;
+  const int head = is_v ? part - c.nkv : part;
+  const uint4* src = reinterpret_cast<const uint4*>((is_v ? v + row * ldv : k + row * ldk) + (size_t)head * D);
+  const long long vec = vec_of(c, row, head, row_seq, row_slot, err, t == 0);
   const unsigned group = ((1u << VT) - 1) << ((threadIdx.x & 31) / VT * VT);
-  if (p.vec < 0) return;   // the whole group
-  const uint4* src = reinterpret_cast<const uint4*>((p.is_v ? v + p.row * ldv : k + p.row * ldk) + (size_t)p.head * D);
+  if (vec < 0) return;   // the whole group
   uint4 raw[CH];
 #pragma unroll
   for (int j = 0; j < CH; ++j) raw[j] = src[j * VT + t];
@@ -117,7 +104,7 @@ __global__ void __launch_bounds__(KV8_THREADS)
   int e = (int)(b >> 23) - 127 - 8 + ((b & 0x7fffffu) > 0x600000u ? 1 : 0);
   e = max(KV8_E_LO, min(KV8_E_HI, e));
   const float inv = __int_as_float((KV8_BIAS - e) << 23);
-  uint8_t* dst = (p.is_v ? c.v : c.k) + p.vec * D;
+  uint8_t* dst = (is_v ? c.v : c.k) + vec * D;
 #pragma unroll
   for (int j = 0; j < CH; ++j) {
     uint32_t w[E / 4];
@@ -129,9 +116,10 @@ __global__ void __launch_bounds__(KV8_THREADS)
     if constexpr (E == 4) reinterpret_cast<uint32_t*>(dst)[j * VT + t] = w[0];
     else reinterpret_cast<uint2*>(dst)[j * VT + t] = make_uint2(w[0], w[1]);
   }
-  if (t == 0) (p.is_v ? c.ve : c.ke)[p.vec] = fine ? (uint8_t)(e + KV8_BIAS) : (uint8_t)KV8_BAD;
+  if (t == 0) (is_v ? c.ve : c.ke)[vec] = fine ? (uint8_t)(e + KV8_BIAS) : (uint8_t)KV8_BAD;
 }
 
+// K and V of a (row, head) by the same threads: one look-up for both and twice the loads in flight.
 template <typename T, int D>
 __global__ void __launch_bounds__(KV8_THREADS)
     kv8_read_k(Kv8 c, T* k, long long ldk, T* v, long long ldv, long long n, const int* row_seq, const int* row_slot,
@@ -141,41 +129,53 @@ __global__ void __launch_bounds__(KV8_THREADS)
   const long long g = ((long long)blockIdx.x * KV8_THREADS + threadIdx.x) / VT;
   if (g >= n) return;
   const int t = threadIdx.x % VT;
-  const Place p = place_of(c, g, row_seq, row_slot, err, t == 0);
-  uint4* dst = reinterpret_cast<uint4*>((p.is_v ? v + p.row * ldv : k + p.row * ldk) + (size_t)p.head * D);
-  if (p.vec < 0) {
+  const int row = (int)(g / c.nkv), head = (int)(g - (long long)row * c.nkv);
+  const long long vec = vec_of(c, row, head, row_seq, row_slot, err, t == 0);
+  uint4* dst[2] = {reinterpret_cast<uint4*>(k + row * ldk + (size_t)head * D),
+                   reinterpret_cast<uint4*>(v + row * ldv + (size_t)head * D)};
+  if (vec < 0) {
 #pragma unroll
-    for (int j = 0; j < CH; ++j) dst[j * VT + t] = make_uint4(0, 0, 0, 0);
+    for (int y = 0; y < 2; ++y)
+#pragma unroll
+      for (int j = 0; j < CH; ++j) dst[y][j * VT + t] = make_uint4(0, 0, 0, 0);
     return;
   }
-  const uint8_t* src = (p.is_v ? c.v : c.k) + p.vec * D;
-  uint32_t w[CH][E / 4];
+  uint32_t w[2][CH][E / 4];
+  uint8_t byte[2];
 #pragma unroll
-  for (int j = 0; j < CH; ++j) {
-    if constexpr (E == 4) {
-      w[j][0] = reinterpret_cast<const uint32_t*>(src)[j * VT + t];
-    } else {
-      const uint2 u = reinterpret_cast<const uint2*>(src)[j * VT + t];
-      w[j][0] = u.x;
-      w[j][1] = u.y;
-    }
-  }
-  const float s = kv8_pow2((p.is_v ? c.ve : c.ke)[p.vec]);
+  for (int y = 0; y < 2; ++y) {
+    const uint8_t* src = (y ? c.v : c.k) + vec * D;
 #pragma unroll
-  for (int j = 0; j < CH; ++j) {
-    float x[E];
-#pragma unroll
-    for (int i = 0; i < E / 4; ++i) {
-      uint32_t h[2];
-      e4m3x4_f16(w[j][i], h[0], h[1]);
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[k]));
-        x[4 * i + 2 * k] = f.x * s;
-        x[4 * i + 2 * k + 1] = f.y * s;
+    for (int j = 0; j < CH; ++j) {
+      if constexpr (E == 4) {
+        w[y][j][0] = reinterpret_cast<const uint32_t*>(src)[j * VT + t];
+      } else {
+        const uint2 u = reinterpret_cast<const uint2*>(src)[j * VT + t];
+        w[y][j][0] = u.x;
+        w[y][j][1] = u.y;
       }
     }
-    dst[j * VT + t] = pack((const T*)nullptr, x);
+    byte[y] = (y ? c.ve : c.ke)[vec];
+  }
+#pragma unroll
+  for (int y = 0; y < 2; ++y) {
+    const float s = kv8_pow2(byte[y]);
+#pragma unroll
+    for (int j = 0; j < CH; ++j) {
+      float x[E];
+#pragma unroll
+      for (int i = 0; i < E / 4; ++i) {
+        uint32_t h[2];
+        e4m3x4_f16(w[y][j][i], h[0], h[1]);
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[z]));
+          x[4 * i + 2 * z] = f.x * s;
+          x[4 * i + 2 * z + 1] = f.y * s;
+        }
+      }
+      dst[y][j * VT + t] = pack((const T*)nullptr, x);
+    }
   }
 }
 
@@ -198,7 +198,7 @@ static int write_t(cudaStream_t st, const Kv8& c, const void* k, long long ldk, 
 template <typename T>
 static int read_t(cudaStream_t st, const Kv8& c, void* k, long long ldk, void* v, long long ldv, int R,
                   const int* row_seq, const int* row_slot, int* err) {
-  const long long n = 2ll * R * c.nkv, blocks = (n * (c.d / 16) + KV8_THREADS - 1) / KV8_THREADS;
+  const long long n = (long long)R * c.nkv, blocks = (n * (c.d / 16) + KV8_THREADS - 1) / KV8_THREADS;
   if (blocks > 0x7fffffffll) return -1;
   if (c.d == 128)
     launch_k(kv8_read_k<T, 128>, dim3((unsigned)blocks), KV8_THREADS, 0, st, c, (T*)k, ldk, (T*)v, ldv, n, row_seq,

@@ -1,27 +1,27 @@
-// Attention over the 8-bit KV cache, behind an optional bf16 prefix that all rows share.
+// Attention over the 8-bit KV cache, behind an optional bf16 prefix that all rows share: up to 32 query vectors a block
+// of rows (all of head_dim 64), the join of what range ends cut, and the host side.
 //
 //   o = sum_s p_s v_s / sum_s p_s,  p_s = 2^(x_s - m),  x_s = log2(e) scale q.k_s,  m near the maximum,
 // over the prefix and the slots that the row sees: one softmax, in one pass over the keys.
 //
-// Own slots (kv8_attn_k). A decoding step or a verify pass has few query vectors (rows x query heads of a KV
+// Own slots (kv8_attn_k). A decoding step or a small verify pass has few query vectors (rows x query heads of a KV
 // head) and many keys, so the keys are the long side of both products, on mma.sync m16n8k16 (fp16, fp32 sums):
 //   S^T [16 keys x 8 query vectors] = K Q^T,   O^T [16 dims x 8 query vectors] += V^T P^T.
 // With the query vectors on the 8-wide side four of them cost half an instruction, where a 128-row tcgen05 tile
 // would be 3% full; and both operands that come from the cache are A fragments, which a warp converts from e4m3
 // right after ldmatrix (fp16 holds every code exactly; cvt runs at 128 codes a clock and SM against the 23 bytes a
-// clock that HBM delivers). tcgen05 would need the fp16 tiles back in shared memory: 64 KB written and
-// read again for each 32 KB of codes, as much time as the load itself.
+// clock that HBM delivers).
 //   - A key's exponent multiplies its score, a value's exponent its weight: the codes are never scaled.
 //   - q is scaled by a power of two into fp16's range (exact down to 2^-38 of its largest entry).
 //   - Weights enter the value product as fp16 (2^-11), scaled by 2^(e_s - E), E the warp's running
 //     reference exponent; a tile whose exponents span more than fp16 bears is taken in several passes.
 //   - The maximum is raised only when a score passes it by 2^8: fp16 holds weights up to 2^16, and most tiles
 //     then need no reduction across lanes and no rescaling of O. Each column decides for itself.
-// Work is split over CTAs by tiles of 32 keys: CTA c takes tiles [c W / G, (c + 1) W / G) of all (sequence, head)
-// items laid end to end, lengths read on the device, so ragged batches and one long sequence balance alike. An
-// item inside one CTA's range is finished there; the pieces of an item cut by range ends (at most two a
-// CTA) go to scratch as (o, m, l) and a second launch joins them in order. A producer warp streams the tiles (TMA,
-// 128- or 64-byte swizzle) through a ring that runs on across items.
+// A producer warp streams the tiles (TMA, 128- or 64-byte swizzle) through a ring that runs on across items, row warps
+// prepare the next item's query vectors, and the key groups' sums meet in shared memory, side by side where it lasts.
+// Bound by HBM once a range is long: one sequence of 32768 slots (8 KV heads of 128, 4 query heads each) 24 us, of them
+// some 12 us of loads at 5.6 TB/s, 4 us until the first tile is there and 6 us for the join's launch; 64 ragged sequences
+// of up to 2048 slots 43 us (21 us of bytes at the copy rate).
 #include "kv8_split.cuh"
 #include "kernels.h"
 

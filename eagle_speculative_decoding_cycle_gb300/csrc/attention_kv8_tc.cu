@@ -4,20 +4,23 @@
 //   S = (Q_hi + Q_lo) K^T   kind::f8f6f4 on the cache's e4m3 codes as they lie: one TMA copy from HBM to the operand. q is
 //                           scaled by a power of two and cut into two e4m3 parts, together 8 significant bits, as many as
 //                           bf16 has, down to 2^-9 of the vector's largest entry (below, a step of 2^-17 of it).
-//   O += P V                kind::f16: the weights times their values' exponents as fp16 in TMEM; the codes are widened to
-//                           fp16 (exact) in shared memory by the softmax threads while they wait for S. (Weights in 8-bit parts, e5m2 for their range, need three products of the codes as
-//                           they lie, but cutting them took twice the arithmetic of the whole softmax: 5000 clocks a
-//                           tile against HBM's 1500.)
+//   O += P V                kind::f16: the weights times their values' exponents as fp16 (2^-11) in TMEM; the codes are
+//                           widened to fp16 (exact) in shared memory by the softmax threads while they wait for S. (Weights
+//                           in 8-bit parts, e5m2 for their range, need three products of the codes as they lie, but cutting
+//                           them took twice the arithmetic of the whole softmax: 5000 clocks a tile against HBM's 1500.)
 // A key's exponent multiplies its scores; a value's is added to its weights' logarithms, against a running reference E, and
 // taken out again of their sum; a tile whose values' exponents span more than fp16 bears goes through the value product
 // in several passes.
 //
 // One CTA an SM, 20 warps, two workers with a range of items each, so that one's softmax and epilogue run under the other's
-// products. A worker has eight softmax warps (two threads a query vector, 64 keys of a tile each: four warps a scheduler
-// hide each other's latencies, and prepare the next item's query vectors; S is read twice from TMEM, for the maximum and for the weights, which keeps a thread below 96
-// registers, and each 32 columns of S are overwritten by the weights of their keys), an MMA warp and a producer warp (TMA: the
-// next tile's keys under this one's softmax, its values as soon as these are widened). TMEM: S and O, 128 columns each, of
-// either worker.
+// products (one worker: 151 us instead of 118 at the time). A worker has eight softmax warps (two threads a query vector,
+// 64 keys of a tile each: four warps a scheduler hide each other's latencies, and prepare the next item's query vectors; S is
+// read twice from TMEM, for the maximum and for the weights, which keeps a thread below 96 registers, and each 32 columns of
+// S are overwritten by the weights of their keys), an MMA warp and a producer warp (TMA: the next tile's keys under this one's
+// softmax, its values as soon as these are widened). TMEM: S and O, 128 columns each, of either worker.
+// 64 ragged sequences of up to 2048 slots, 17 tree rows of 32 heads over 8 KV heads: 92 us (24 us of bytes at the copy rate),
+// 180 us on mma.sync. Bound by the softmax warps: of a tile's some 7000 clocks the weights take 2400 to 3400, the maximum
+// 1500, widening the values 1300, the two products and their hand-overs the rest.
 #include "kv8_split.cuh"
 #include "kernels.h"
 #include "tc_common.cuh"
@@ -44,12 +47,14 @@ constexpr int TO_EXP = TO_Q + 4 * OPB;                    // [worker][tile parit
 constexpr int TO_KF = TO_EXP + 2 * 2 * 256;               // [worker][tile parity][128] key factors
 constexpr int TO_VF = TO_KF + 2 * 2 * 512;                // [worker][tile parity][2][128] value exponents, inverse factors
 constexpr int TO_COL = TO_VF + 2 * 2 * 1024;              // [worker][item parity][128] (score factor, slot limit)
-constexpr int TO_MASK = TO_COL + 4 * TT * 8;              // [worker][item parity][128 rows][4] tree masks
-constexpr int TO_X = TO_MASK + 4 * TT * 32;               // [worker][tile parity][half][128] maxima; then sums
+constexpr int TO_MASK = TO_COL + 4 * TT * 8;              // [worker][128 rows][4] tree masks: the last tile's barrier on its
+                                                          // exponents comes after their last use in an item
+constexpr int TO_X = TO_MASK + 2 * TT * 32;               // [worker][tile parity][half][128] maxima; then sums
 constexpr int TO_RED = TO_X + 2 * 2 * 2 * TT * 4;         // [worker] small tables, below
 constexpr int TO_BAR = TO_RED + 2 * 512;
 constexpr int TO_GROUP = TO_BAR + 2 * 128 + 64;
 constexpr int tc_smem(int groups) { return 1024 + TO_GROUP + (3 * groups + 1) * 4; }
+static_assert(tc_smem(KV8_MAX_GROUPS) <= 227 * 1024, "shared memory");
 
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
@@ -169,7 +174,7 @@ __global__ void __launch_bounds__(T_THREADS, 1)
     const int ctx = a.mode == 1 && seq >= 0 ? a.ctx_len[seq] : 0;
     uint8_t* q_hi = sm + TO_Q + wk * 2 * OPB;
     float2* cols = reinterpret_cast<float2*>(sm + TO_COL) + (wk * 2 + buf) * TT;
-    uint64_t* masks = reinterpret_cast<uint64_t*>(sm + TO_MASK) + (wk * 2 + buf) * TT * 4;
+    uint64_t* masks = reinterpret_cast<uint64_t*>(sm + TO_MASK) + wk * TT * 4;
     if (a.mode == 1)
       for (int x = sw * 32 + lane; x < (r1 - r0) * 4; x += warps * 32) {
         const int r = r0 + x / 4, w = x & 3;
@@ -271,7 +276,7 @@ __global__ void __launch_bounds__(T_THREADS, 1)
       const float qf = r < nqv ? col.x : 0.f;   // a row past the block's never raises its maximum
       const int klim = __float_as_int(col.y);
       const uint32_t* my_mask =
-          reinterpret_cast<const uint32_t*>(sm + TO_MASK) + ((wk * 2 + buf) * TT + (r < nqv ? (r * p.G_inv >> 16) : 0)) * 8;
+          reinterpret_cast<const uint32_t*>(sm + TO_MASK) + (wk * TT + (r < nqv ? (r * p.G_inv >> 16) : 0)) * 8;
       float m = -INFINITY, l = 0.f;
       int E = 0;                 // reference exponent byte
       for (int t = k.t0; t < k.t1; ++t, ++i) {

@@ -9,12 +9,17 @@
 //   warps 0-3, 4-7  softmax of tile 0 / 1, one thread a query vector (TMEM lane): S row -> maximum, weights as bf16 back
 //                   into TMEM over S, running sum; O is rescaled only when the maximum moves by more than 2^8;
 //   warp 8          TMA: Q once, K and V tiles through two-stage rings (128-byte swizzle);
-//   warp 9          tcgen05.mma: S_t = Q_t K^T (operands in shared memory), O_t += P_t V (P in TMEM, V read MN-major).
-// While one tile's S is in its softmax warps the tensor cores run the other tile's products, and K and V feed both
-// tiles. TMEM: S0 S1 (128 columns each, P over the first 64), O0 O1 (d each).
+//   warps 9, 10     tcgen05.mma of tile 0 / 1: S = Q K^T (operands in shared memory), O += P V (P in TMEM, V read MN-major).
+// S comes in halves of 64 keys, each with its own barriers: while one half is in its softmax warps the tensor cores run the
+// other half's value product and next S, and the other tile's. (S of 128 keys at once leaves a chain of product, softmax,
+// product: 119 us in all for 4096 shared tokens under 64 x 17 rows of 32 heads, against 106; its two threads a query vector
+// 118; halves with one issuing warp for both tiles 135, each of its waits taking some 250 clocks.)
+// TMEM: S0 S1 (128 columns each, P over the first half of each 64), O0 O1 (d each). Bound by the tensor cores: a pair of
+// tiles takes some 3300 clocks of 128 keys, where products of 128 columns (64 clocks each) would take 2048; a product of 64
+// columns is not much faster than one of 128.
 // Weights are rounded to bf16 (2^-8 relative at most, as the bf16 V that they meet; their sum is kept in fp32 of the
-// unrounded weights). Results leave as fp32 partials (o, m, l) of each key range, which the attention over the rows' own slots
-// joins in its epilogue.
+// unrounded weights). Results leave as fp32 partials (o, m, l) of each key range, which the attention over the rows' own
+// slots joins in its epilogue.
 #include "kv8.cuh"
 #include "kernels.h"
 #include "tc_common.cuh"
@@ -119,7 +124,7 @@ __device__ __forceinline__ void tmem_wait_ld(float* v) {
 }
 // One lane of a converged warp. The loops of the issuing warps run in all lanes and only the copies and products
 // themselves under this lane: their operands then stay in uniform registers (issued by `lane == 0` of a divergent loop, each
-// product took some 100 clocks to issue against 64 to run).
+// product took some 100 clocks to issue).
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));

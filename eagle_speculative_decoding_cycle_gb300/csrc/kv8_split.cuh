@@ -4,6 +4,8 @@
 // read on the device. Laid end to end the tiles are shared out over the CTAs in equal contiguous ranges, so that
 // ragged batches and one long sequence balance alike. An item inside one CTA's range is finished there; the pieces of
 // an item cut by range ends (at most two a CTA) go to scratch as (o, m, l) and a second launch joins them in order.
+// An item also costs its start and its end, counted as `pad` tiles (64 ragged sequences, one row each: 52 us with none,
+// 48 with 2, 44 with 3 to 6, 46 with 8).
 #pragma once
 
 #include "kv8.cuh"
@@ -125,7 +127,7 @@ __device__ __forceinline__ Group group_of(const Kv8Attn& a, const Plan& p, int g
   }
   for (int d = width >> 1; d > 0; d >>= 1) lim = max(lim, __shfl_xor_sync(0xffffffffu, lim, d));
   bad = bad || lim > a.c.cap;
-  o.limit = max(0, min(lim, a.c.cap));
+  o.limit = ctx < 0 ? 0 : max(0, min(lim, a.c.cap));
   if (latch && bad) latch_error(a.err, DEVERR_BOUNDS);
   return o;
 }

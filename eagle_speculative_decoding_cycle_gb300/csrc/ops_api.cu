@@ -1,5 +1,6 @@
 // Kernel-level C ABI (eagle_ops.h): each entry point runs one of the cycle's kernels on
 // caller-provided device buffers.
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 
@@ -227,6 +228,9 @@ int eagle_op_compact(int dtype, void* stream, void* kcache, void* vcache, int la
 static bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 // The kernels' view of a cache; EAGLE_EINVAL / EAGLE_ECAPACITY when it breaks the header's rules.
+// Vectors of a cache, slots of a prefix: their numbers, rounded up to whole tiles, stay in 32 bits.
+constexpr double KV8_MOST = 2147483648.0 - 4096;
+
 static int kv8_view(const eagle_kv8* c, Kv8& o) {
   if (!c || !c->k_code || !c->v_code || !c->k_exp || !c->v_exp || c->n_kv_heads < 1 || c->max_batch < 1 || c->cap < 1 ||
       (c->head_dim != 64 && c->head_dim != 128))
@@ -247,7 +251,7 @@ static int kv8_view(const eagle_kv8* c, Kv8& o) {
     if (c->cap % 16) return EAGLE_EINVAL;
     vecs = (double)c->max_batch * c->n_kv_heads * c->cap;
   }
-  return vecs < 2147483648.0 ? EAGLE_OK : EAGLE_ECAPACITY;
+  return vecs < KV8_MOST ? EAGLE_OK : EAGLE_ECAPACITY;
 }
 
 static int kv8_rows(const Kv8& c, int dtype, const void* k, int64_t ldk, const void* v, int64_t ldv, int R,
@@ -287,14 +291,14 @@ int eagle_op_kv8_read(void* stream, const eagle_kv8* cache, int dtype, void* k, 
 // Sizes that both attention entry points and their scratch size accept.
 static int kv8_attn_sizes(const Kv8& c, int R, int nq, int rows_per_seq, int prefix_len) {
   if (R < 1 || nq < 1 || nq % c.nkv || nq / c.nkv > 64 || rows_per_seq < 1 || prefix_len < 0) return EAGLE_EINVAL;
-  if ((double)R * nq >= 2147483648.0 / c.d || (double)prefix_len * c.nkv >= 2147483648.0) return EAGLE_ECAPACITY;
+  if ((double)R * nq >= 2147483648.0 / c.d || (double)prefix_len * c.nkv >= KV8_MOST) return EAGLE_ECAPACITY;
   return EAGLE_OK;
 }
 
 size_t eagle_op_attention_kv8_scratch_bytes(const eagle_kv8* cache, int R, int nq, int rows_per_seq, int prefix_len) {
   Kv8 c;
   if (kv8_view(cache, c) != EAGLE_OK || kv8_attn_sizes(c, R, nq, rows_per_seq, prefix_len) != EAGLE_OK) return 0;
-  return al(kv8_attention_scratch(c, R, nq, rows_per_seq, prefix_len));
+  return al(kv8_attention_scratch(c, R, nq, std::min(rows_per_seq, R), prefix_len));
 }
 
 int eagle_op_attention_shared_kv8(void* stream, const eagle_kv8* cache, const void* prefix_k, const void* prefix_v,
@@ -310,8 +314,11 @@ int eagle_op_attention_shared_kv8(void* stream, const eagle_kv8* cache, const vo
     return EAGLE_EINVAL;
   if (mode == 1 && (!ctx_len || !mask || tree_T < 1 || tree_T > 256 || mask_words < (tree_T + 63) / 64)) return EAGLE_EINVAL;
   if (prefix_len && (!prefix_k || !prefix_v || !on16(prefix_k) || !on16(prefix_v))) return EAGLE_EINVAL;
+  rows_per_seq = std::min(rows_per_seq, R);
   const size_t need = al(kv8_attention_scratch(a.c, R, nq, rows_per_seq, prefix_len));
   if (!scratch || !on16(scratch) || scratch_bytes < need) return EAGLE_ECAPACITY;
+  const uintptr_t q0 = (uintptr_t)q, o0 = (uintptr_t)out, len = (uintptr_t)R * nq * a.c.d * 2;
+  if (q0 != o0 && q0 < o0 + len && o0 < q0 + len) return EAGLE_EINVAL;   // (out = q: a block's rows are read before they are written)
   a.q = q; a.out = out; a.pk = prefix_k; a.pv = prefix_v; a.P = prefix_len;
   a.R = R; a.nq = nq; a.rows_per_seq = rows_per_seq; a.mode = mode; a.tree_T = mode == 1 ? tree_T : 0;
   a.mask_words = mask_words; a.row_seq = row_seq; a.row_slot = row_slot; a.ctx_len = ctx_len; a.mask = mask;

@@ -149,11 +149,17 @@ int eagle_op_kv8_read(void* stream, const eagle_kv8* cache, int dtype, void* k, 
  * mask[r][t / 64] is set (mask_words >= ceil(tree_T / 64); row_slot is not read). ctx_len is
  * indexed by sequence ([max_batch]; not read in mode 0). A row that sees nothing, and a padding
  * row (row_seq[r] < 0), gets zeros. A row whose sequence differs from that of the first
- * not-padding row among its rows_per_seq, a sequence outside the cache, a visible slot at or
- * past cap and a table entry out of range are latched into *d_err (nullable): such a row gets
- * zeros, slots past cap are left out, and a bad table entry makes its slots unspecified. Slots
+ * not-padding row among its rows_per_seq, a sequence outside the cache, a negative ctx_len, a
+ * visible slot at or past cap and a table entry out of range are latched into *d_err (nullable):
+ * such a row gets zeros, a negative ctx_len hides all slots of its sequence, slots past cap are
+ * left out, and a bad table entry makes its slots unspecified (every entry up to the last slot that
+ * a sequence's rows see is looked up, those of slots in between that no row sees too). Slots
  * that no row sees may hold anything. Scale = 1/sqrt(head_dim) when scale <= 0.
- * Sums, maxima and softmax weights' sums are fp32; the weights enter the value product as fp16.
+ * out may be q itself; otherwise the two do not overlap (refused).
+ * Sums, maxima and softmax weights' sums are fp32; the weights enter the value product as fp16
+ * (2^-11). q is used exactly (fp16 times a power of two, entries down to 2^-38 of its largest), but
+ * with head_dim 128 and more than 32 query vectors a block (rows x query heads of a KV head, up
+ * to 128 together) it is held in two e4m3 parts: each entry to 2^-17 of the vector's largest.
  * A row's result does not depend on the values of other rows or sequences; their lengths move
  * the points where its sum over slots is split, so it can change in the last bits of fp32.
  * scratch: eagle_op_attention_kv8_scratch_bytes of the same sizes, no initial value needed; two
@@ -168,7 +174,8 @@ int eagle_op_attention_kv8(void* stream, const eagle_kv8* cache, const void* q, 
  * prefix_k / prefix_v (bf16 [n_kv_heads][prefix_len][head_dim], 16-byte aligned; kept at full
  * precision, being stored once for the whole batch) and then its own slots as above, in one
  * softmax. The prefix is one matrix product over all rows of a head, read once per 256 query
- * vectors rather than once per sequence. Padding rows get zeros. prefix_len = 0 is
+ * vectors rather than once per sequence; its weights enter the value product as bf16 (2^-8), the
+ * type of the values that they meet. Padding rows get zeros. prefix_len = 0 is
  * eagle_op_attention_kv8. */
 int eagle_op_attention_shared_kv8(void* stream, const eagle_kv8* cache, const void* prefix_k, const void* prefix_v,
                                   int prefix_len, const void* q, void* out, int R, int nq, int rows_per_seq,

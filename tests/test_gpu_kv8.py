@@ -490,3 +490,81 @@ def test_a_serving_run():
             hist[b] = hist[b] + [(deq(k)[b], deq(v)[b])]
             want, tol = expect(q[b].double().cpu().numpy(), b, [])
             assert np.all(np.abs(out[b] - want) <= tol)
+
+
+# ---- more shapes of work --------------------------------------------------------------------------
+@pytest.mark.parametrize("B,T,nq,nkv,d,most,mode,block,P", [
+    (600, 1, 4, 2, 64, 40, 0, 16, 0),        # more row blocks than one launch takes
+    (600, 1, 4, 2, 64, 40, 0, 0, 50),        # the same behind a prefix
+    (530, 9, 8, 1, 128, 70, 1, 16, 130),     # 72 query vectors a block
+    (64, 1, 16, 8, 128, 200, 0, 16, 0),      # more (block, head) items than CTAs
+    (64, 12, 32, 8, 128, 150, 1, 32, 0),     # the same with 48 query vectors
+])
+def test_many_sequences(B, T, nq, nkv, d, most, mode, block, P):
+    ctx = np.random.default_rng(B + T).integers(0, most, size=B)
+    k = Case(B, T, nq, nkv, d, ctx, mode, block, P, seed=30)
+    pick = sorted({0, B * T - 1, 511 * T % (B * T), 512 * T % (B * T)} | set(k.g.integers(0, B * T, 25).tolist()))
+    a = k.check(rows=pick)
+    assert torch.equal(k.run(), a)
+
+
+@pytest.mark.parametrize("B,T,nq,nkv,d,ctx,mode,block,vspread,P", [
+    (1, 9, 4, 1, 128, 3, 1, 0, 0.7, 0),             # a cache shorter than a tile, 36 query vectors
+    (2, 200, 4, 2, 128, [5, 60], 0, 16, 0.7, 0),    # a causal chunk in four row blocks
+    (2, 60, 4, 2, 64, [131, 20], 0, 0, 0.7, 90),    # 120 query vectors of 64
+    (2, 9, 8, 2, 64, [100, 300], 1, 16, 6.0, 0),    # values of many sizes in one tile
+    (1, 30, 8, 2, 128, [250], 0, 64, 6.0, 0),
+    (2, 12, 16, 2, 128, [0, 140], 1, 0, 6.0, 200),
+])
+def test_row_blocks_of_many_query_vectors(B, T, nq, nkv, d, ctx, mode, block, vspread, P):
+    Case(B, T, nq, nkv, d, ctx, mode, block, P, seed=31, vspread=vspread).check()
+
+
+@pytest.mark.parametrize("T,P", [(1, 0), (12, 0), (12, 140)])
+def test_results_over_the_queries(T, P):
+    """out = q is allowed: the same bits as into a tensor of its own."""
+    k = Case(5, T, 16, 4, 128, [300, 0, 77, 128, 3], 1, 16, P, seed=32)
+    want = k.run()
+    assert k.run(out=k.q) is k.q and torch.equal(k.q, want) and int(k.err) == 0
+
+
+@pytest.mark.parametrize("T,d,P", [(1, 64, 0), (12, 128, 0), (12, 128, 140)])
+def test_two_graphs_and_a_side_stream(T, d, P):
+    k = Case(6, T, 16, 4, d, [300, 0, 77, 128, 3, 64], 1, 16, P, seed=33)
+    want = k.run()
+    mask, rs, cx = bits_of(k.trees, T), i32(k.row_seq), i32(k.ctx)
+    call = lambda **kw: api.attention_shared_kv8(k.q, k.pk, k.pv, k.c, rs, None, cx, T, 1, T, mask, **kw)
+    outs, graphs, streams = [], [], [torch.cuda.Stream() for _ in range(2)]
+    for st in streams:
+        s = api.attention_kv8_scratch(k.c, 6 * T, 16, T, P)
+        s.fill_(0xff)
+        o = torch.empty_like(k.q)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=st):
+            call(out=o, scratch=s)
+        outs.append((o, s)), graphs.append(g)
+    for _ in range(20):
+        for g, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o, _ in outs)
+    side = torch.cuda.Stream()
+    got = [call(stream=side) for _ in range(8)]       # results and scratch are made for the side stream
+    kk = api.kv8_read(k.c, rs, rs, stream=side)
+    side.synchronize()
+    assert all(torch.equal(o, want) for o in got)
+    assert all(torch.equal(a, b) for a, b in zip(kk, api.kv8_read(k.c, rs, rs)))
+
+
+@pytest.mark.parametrize("P", [0, 33])
+def test_a_negative_context_hides_its_sequence(P):
+    k = Case(3, 12, 8, 2, 128, [40, 25, 9], 1, P=P, seed=34)
+    k.ctx = np.asarray([40, -5, 9])
+    out = k.run()
+    assert int(k.err) == 2
+    k.ctx = np.asarray([40, 0, 9])
+    k.trees[12:24] = False                             # the prefix alone, or nothing
+    want, tol = k.want()
+    assert np.all(np.abs(out.double().cpu().numpy() - want) <= tol)

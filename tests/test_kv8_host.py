@@ -126,3 +126,18 @@ def test_binding_refuses_wrong_tensors():
             a["prefix_v"] = kw["prefix_k"]
         with pytest.raises(ValueError):
             api.attention_shared_kv8(**a)
+
+
+def test_sizes_at_their_limits(lib):
+    size = lambda rps, P=0, **kw: lib.eagle_op_attention_kv8_scratch_bytes(cache(**kw), 8, 32, rps, P)
+    assert size((1 << 31) - 1) == size(8) > 0            # more rows a sequence than rows: one sequence
+    assert size(4, (1 << 28) - 513) > 0
+    assert size(4, (1 << 28) - 512) == 0                 # 8 heads: prefix slots past 32 bits once rounded up
+    assert size(4, max_batch=1, cap=(1 << 28) - 528) > 0
+    assert size(4, max_batch=1, cap=(1 << 28) - 512) == 0
+
+
+def test_out_may_be_q_but_not_overlap_it(lib):
+    step = 32 * 128 * 2
+    for out in (FAKE + step, FAKE + 8 * step - 16, FAKE - 16):
+        assert attn(lib, cache(), q=FAKE, out=out) == L.EAGLE_EINVAL

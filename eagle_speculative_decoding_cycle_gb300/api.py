@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes as C
 import dataclasses
+from contextlib import nullcontext
 from typing import Dict, List, Optional, Sequence
 
 import torch
@@ -406,12 +407,12 @@ class _Current:
             torch.cuda.set_device(self.before)
 
 
-def _empty_for(stream: Optional[torch.cuda.Stream], shape, dtype, device) -> torch.Tensor:
-    """A new tensor that belongs to the stream its kernel runs on: freed early, its memory is not handed to others."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+_HERE = nullcontext()
+
+
+def _owned_by(stream: Optional[torch.cuda.Stream]):
+    """New tensors belong to the stream that their kernel runs on: freed early, their memory is not handed to others."""
+    return _HERE if stream is None else torch.cuda.stream(stream)
 
 
 def _stream_of(index: int, stream: Optional[torch.cuda.Stream]) -> int:
@@ -517,8 +518,9 @@ def kv8_read(cache: KV8Cache, row_seq: torch.Tensor, row_slot: torch.Tensor, dty
     n = row_seq.numel()
     if out is None:
         _need(dtype in _KV_TYPES, "entries are read as float32 or bfloat16")
-        shape = (n, cache.nkv, cache.d)
-        k, v = (_empty_for(stream, shape, dtype, cache.device) for _ in range(2))
+        with _owned_by(stream):
+            k = torch.empty((n, cache.nkv, cache.d), dtype=dtype, device=cache.device)
+            v = torch.empty_like(k)
     else:
         k, v = out
     R, code, ldk, ldv = _kv_rows(cache, k, v)
@@ -535,14 +537,9 @@ def kv8_read(cache: KV8Cache, row_seq: torch.Tensor, row_slot: torch.Tensor, dty
 def attention_kv8_scratch(cache: KV8Cache, R: int, nq: int, rows_per_seq: int, prefix_len: int = 0) -> torch.Tensor:
     """Scratch for attention_kv8 / attention_shared_kv8 calls of these sizes (calls that may overlap on the GPU
     need their own)."""
-    return _scratch_of(cache, R, nq, rows_per_seq, prefix_len, None)
-
-
-def _scratch_of(cache: KV8Cache, R: int, nq: int, rows_per_seq: int, prefix_len: int,
-                stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
     nb = L.lib().eagle_op_attention_kv8_scratch_bytes(cache.ref, R, nq, rows_per_seq, prefix_len)
     _need(nb > 0, "sizes that the 8-bit attention does not take")
-    return _empty_for(stream, nb, torch.uint8, cache.device)
+    return torch.empty(nb, dtype=torch.uint8, device=cache.device)
 
 
 def attention_shared_kv8(q: torch.Tensor, prefix_k: Optional[torch.Tensor], prefix_v: Optional[torch.Tensor],
@@ -578,14 +575,16 @@ def attention_shared_kv8(q: torch.Tensor, prefix_k: Optional[torch.Tensor], pref
               mask.is_contiguous() and mask.get_device() == index, "mask must be a contiguous 64-bit [R][words] tensor")
         mp, mw = mask.data_ptr(), mask.shape[1]
     if out is None:
-        out = _empty_for(stream, shape, torch.bfloat16, cache.device)
+        with _owned_by(stream):
+            out = torch.empty_like(q)
     else:
         _need(out.shape == shape and out.dtype is torch.bfloat16 and out.is_contiguous() and out.get_device() == index,
               "out must be like q")
     if R == 0:
         return out
     if scratch is None:
-        scratch = _scratch_of(cache, R, nq, rows_per_seq, P, stream)
+        with _owned_by(stream):
+            scratch = attention_kv8_scratch(cache, R, nq, rows_per_seq, P)
     if scratch.dtype is not torch.uint8 or not scratch.is_contiguous() or scratch.get_device() != index:
         raise ValueError("scratch must be a contiguous uint8 tensor on the cache's device")
     with _Current(index):

@@ -1,4 +1,4 @@
-// Attention over the 8-bit KV cache, behind an optional bf16 prefix that all rows share: up to 32 query vectors a block
+// Attention over the 8-bit KV cache, behind an optional bf16 prefix that all rows share: up to 16 query vectors a block
 // of rows (all of head_dim 64), the join of what range ends cut, and the host side.
 //
 //   o = sum_s p_s v_s / sum_s p_s,  p_s = 2^(x_s - m),  x_s = log2(e) scale q.k_s,  m near the maximum,
@@ -33,7 +33,9 @@ namespace eagle {
 namespace {
 
 constexpr int TK = 32;            // keys a tile
-constexpr int TC_ABOVE = 32;      // head_dim 128 with more query vectors a block goes to tcgen05 (128-key tiles)
+// head_dim 128 with more query vectors a block goes to tcgen05 (128-key tiles). 64 ragged sequences of up to 2048 slots, 8 KV
+// heads, T rows of 4 query heads a KV head (mma.sync, tcgen05): T = 1 45, 82 us; 2 45, 82; 4 65, 83; 8 182, 84; 17 180, 92.
+constexpr int TC_ABOVE = 16;
 constexpr float LAZY = 8.f;       // how far (log2) a score may pass the reference maximum
 constexpr int E_UP = 4, E_DOWN = 12;   // exponents a tile may have around the reference, E_SPAN within one pass
 constexpr int E_SPAN = 14;
@@ -734,26 +736,32 @@ cudaError_t launch_own(cudaStream_t st, const Kv8Attn& a, Plan& p, const CUtenso
   return e != cudaSuccess ? e : launch_join<D>(st, a, p);
 }
 
-// The narrowest configuration that holds a block's query vectors: up to 16 in two small CTAs an SM (one's joins
-// under the other's loads), more in one CTA whose warps share the query tiles.
+// The narrowest configuration that holds a block's query vectors: small ones in two CTAs an SM (one's joins under the
+// other's loads), large ones in one CTA of eight warps. 64 ragged sequences of up to 2048 slots, 8 KV heads of 64: 32 query
+// vectors a block 60 us (two query tiles a warp, two CTAs; 96 with four a warp in one CTA, whose registers spill), 48 86 us
+// (94 in two CTAs of 64), 64 96 us (104 and 116 in one CTA), 96 126 us, 128 162 us.
 template <int D>
 cudaError_t launch_mma(cudaStream_t st, const Kv8Attn& a, Plan& p, const CUtensorMap& mk, const CUtensorMap& mv) {
   const int t = p.qv_pad / 8;
   if (t <= 1) return launch_own<D, 1, 1, 4, 10, 2>(st, a, p, mk, mv);
   if (t <= 2) return launch_own<D, 2, 1, 4, 9, 2>(st, a, p, mk, mv);
-  if (t <= 4) return launch_own<D, 4, 1, 8, 20, 1>(st, a, p, mk, mv);
   if constexpr (D == 64) {
+    if (t <= 4) return launch_own<D, 2, 2, 2, 9, 2>(st, a, p, mk, mv);
     if (t <= 6) return launch_own<D, 3, 2, 4, 18, 1>(st, a, p, mk, mv);
-    if (t <= 8) return launch_own<D, 4, 2, 4, 16, 1>(st, a, p, mk, mv);
+    if (t <= 8) return launch_own<D, 2, 4, 1, 7, 2>(st, a, p, mk, mv);
     if (t <= 12) return launch_own<D, 3, 4, 2, 11, 1>(st, a, p, mk, mv);
     return launch_own<D, 4, 4, 2, 7, 1>(st, a, p, mk, mv);
   }
+  return cudaErrorInvalidValue;   // (head_dim 128 with more goes to launch_tc)
+}
+
+cudaError_t launch_tc(cudaStream_t st, const Kv8Attn& a, Plan& p, const CUtensorMap& mk, const CUtensorMap& mv) {
   p.grid = 2 * std::min(KV8_MAX_CTAS / 2, device_sm_count());   // two workers a CTA
   p.by_item = p.groups * p.nkv <= p.grid;
   p.min_tiles = 1;
   p.pad = 2;
   const cudaError_t e = kv8_launch_tc(st, a, p, mk, mv);
-  return e != cudaSuccess ? e : launch_join<D>(st, a, p);
+  return e != cudaSuccess ? e : launch_join<128>(st, a, p);
 }
 
 }  // namespace
@@ -786,7 +794,8 @@ int kv8_attention(cudaStream_t st, const Kv8Attn& a) {
   }
   const long long rows = a.c.table ? ((long long)a.c.n_blocks * a.c.nkv) << a.c.block_log2
                                    : (long long)a.c.max_batch * a.c.nkv * a.c.cap;
-  if (a.c.d == 128 && p.qv_pad > TC_ABOVE) p.tk = 128;
+  const bool tc = a.c.d == 128 && p.qv_pad > TC_ABOVE;
+  if (tc) p.tk = 128;
   const int box = a.c.table ? std::min(p.tk, 1 << a.c.block_log2) : p.tk;
   CUtensorMap mk, mv;
   if (!code_map(&mk, a.c.k, rows, a.c.d, box) || !code_map(&mv, a.c.v, rows, a.c.d, box)) return -4;
@@ -799,7 +808,9 @@ int kv8_attention(cudaStream_t st, const Kv8Attn& a) {
     p.g0 = (int)g0;
     p.late = a.P && g0 == 0;
     p.groups = (int)std::min<long long>(KV8_MAX_GROUPS, blocks - g0);
-    const cudaError_t e = a.c.d == 128 ? launch_mma<128>(st, a, p, mk, mv) : launch_mma<64>(st, a, p, mk, mv);
+    const cudaError_t e = tc ? launch_tc(st, a, p, mk, mv)
+                          : a.c.d == 128 ? launch_mma<128>(st, a, p, mk, mv)
+                                         : launch_mma<64>(st, a, p, mk, mv);
     if (e != cudaSuccess) {
       cudaGetLastError();
       return -4;

@@ -10,7 +10,7 @@ W = sum p |v| / sum p and A the largest sum_i |q_i k_i| * scale that the row see
                               its own and, through the sum, everybody's;
   W * (n + 64) * 2^-23        n fp32 additions of the value product and of the sum, exp2 and the joins.
 fp16 weights below 2^-14 round to a step of 2^-24, against a largest weight of at least 1 a row: n * 2^-25 * max|v|.
-With head_dim 128 and more than 32 query vectors a block (rows x query heads of a KV head) q is held in 8-bit parts:
+With head_dim 128 and more than 16 query vectors a block (rows x query heads of a KV head) q is held in 8-bit parts:
   W * 2 * 2^-17 * Q           q as two e4m3 parts, its largest entry in [2^7, 2^8): each entry is off by at most half of
                               their smallest step, 2^-10, so 2^-17 of the largest entry; Q = max|q| sum_i |k_i| * scale.
 """
@@ -231,7 +231,7 @@ class Case:
                 count = int(s.sum())
                 top = np.abs(V[s]).max() if count else 0.0
                 nb = -(-T // (128 // G))
-                parts = d == 128 and -(-T // nb) * G > 32
+                parts = d == 128 and -(-T // nb) * G > 16
                 Q = np.abs(q[r, h * G:(h + 1) * G]).max(-1) * np.abs(K[s]).sum(-1).max(initial=0.0) * scale
                 tol[r, h * G:(h + 1) * G] = 2.0 ** -8 * np.abs(o) + count * 2.0 ** -25 * top + \
                     W * ((2.0 ** -8 if P else 2.0 ** -11) + 2 * (d + 8) * 2.0 ** -23 * A[:, None] +

@@ -12,11 +12,12 @@
 //   warps 9, 10     tcgen05.mma of tile 0 / 1: S = Q K^T (operands in shared memory), O += P V (P in TMEM, V read MN-major).
 // S comes in halves of 64 keys, each with its own barriers: while one half is in its softmax warps the tensor cores run the
 // other half's value product and next S, and the other tile's. (S of 128 keys at once leaves a chain of product, softmax,
-// product: 119 us in all for 4096 shared tokens under 64 x 17 rows of 32 heads, against 106; its two threads a query vector
+// product: 121 us in all for 4096 shared tokens under 64 x 17 rows of 32 heads, against 106; with two threads a query vector
 // 118; halves with one issuing warp for both tiles 135, each of its waits taking some 250 clocks.)
-// TMEM: S0 S1 (128 columns each, P over the first half of each 64), O0 O1 (d each). Bound by the tensor cores: a pair of
-// tiles takes some 3300 clocks of 128 keys, where products of 128 columns (64 clocks each) would take 2048; a product of 64
-// columns is not much faster than one of 128.
+// TMEM: S0 S1 (128 columns each, P over the first half of each 64), O0 O1 (d each). That prefix alone: 66 us under the
+// profiler, tensor pipe 46% active; 38 us of products at the rate of a large GEMM. 128 keys of a pair of tiles take some 3300
+// clocks, 2048 of them products at full width: products of 64 columns read their operands twice as often, and the
+// hand-overs between the warps do the rest.
 // Weights are rounded to bf16 (2^-8 relative at most, as the bf16 V that they meet; their sum is kept in fp32 of the
 // unrounded weights). Results leave as fp32 partials (o, m, l) of each key range, which the attention over the rows' own
 // slots joins in its epilogue.

@@ -589,7 +589,7 @@ __global__ void __launch_bounds__(Shape<D, NT, WN, WK, NS, CTAS>::THREADS, CTAS)
         if (whole) {
           const int in = (int)(col * p.G_inv >> 16), row = r0 + in;
           const size_t at = (size_t)row * a.nq + h * p.G + col - in * p.G;
-          fold<D>(p.n_prefix, [&](int k) { return prefix_part<D>(a, p, k, at); }, c / 8, top, L, o);
+          fold<D, 6>(p.n_prefix, [&](int k) { return prefix_part<D>(a, p, k, at); }, c / 8, top, L, o);
           store8(a, at, D, c, __float_as_int(s_col[col].y) >= 0, L, o);
         } else {
           const size_t q = (size_t)slot * p.qv_pad + col;
@@ -628,7 +628,7 @@ __global__ void __launch_bounds__(256) kv8_join_k(const Kv8Attn a, const Plan p)
   // piece 0 in slot 2 c0 + 1 (it holds the item's start), the others in slot 2 c, then the prefix's
   const int pieces = c1 - c0 + 1, n = pieces + p.n_prefix;
   float top = -INFINITY, L = 0.f, o[8] = {};
-  fold<D>((n - way + ways - 1) / ways, [&](int i) {
+  fold<D, 3>((n - way + ways - 1) / ways, [&](int i) {
     const int k = i * ways + way;
     if (k >= pieces) return prefix_part<D>(a, p, k - pieces, at);
     const size_t q = (size_t)(k ? 2 * (c0 + k) : 2 * c0 + 1) * p.qv_pad + col_in;
@@ -642,14 +642,19 @@ __global__ void __launch_bounds__(256) kv8_join_k(const Kv8Attn a, const Plan p)
     }
     __syncthreads();
     if (way) return;
+    float mx = top;
+    for (int w = 1; w < ways; ++w) mx = fmaxf(mx, s_ml[team + w * p.join_cols].x);
+    const float base = mx == -INFINITY ? 0.f : mx, f = ex2(top - base);
+    L *= f;
+#pragma unroll
+    for (int x = 0; x < 8; ++x) o[x] *= f;
     for (int w = 1; w < ways; ++w) {
       const int from = team + w * p.join_cols;
       const float2 ml = s_ml[from];
-      const float mx = fmaxf(top, ml.x), base = mx == -INFINITY ? 0.f : mx, f = ex2(top - base), g = ex2(ml.x - base);
-      top = mx;
-      L = L * f + ml.y * g;
+      const float g = ex2(ml.x - base);
+      L = fmaf(ml.y, g, L);
 #pragma unroll
-      for (int x = 0; x < 8; ++x) o[x] = o[x] * f + s_part[from][c + x] * g;
+      for (int x = 0; x < 8; ++x) o[x] = fmaf(s_part[from][c + x], g, o[x]);
     }
   }
   if (col < nqv) store8(a, at, D, c, seq >= 0 && seq < a.c.max_batch && own == seq, L, o);
@@ -707,7 +712,8 @@ size_t own_scratch(const Kv8& c, const Plan& p) {
 }
 
 // A join CTA holds up to 256 / (D / 8) teams: as many on one query vector as leave each about four partials, if the
-// grid's ranges are spread evenly over the items, the others on further query vectors.
+// grid's ranges are spread evenly over the items, the others on further query vectors; fewer where items that are all cut
+// would make more than two CTAs an SM (61 rows of one sequence: 25.4 us with 992 CTAs, 19.5 with 248).
 template <int D>
 cudaError_t launch_join(cudaStream_t st, const Kv8Attn& a, Plan& p) {
   constexpr int TEAMS = 256 / (D / 8);
@@ -717,6 +723,10 @@ cudaError_t launch_join(cudaStream_t st, const Kv8Attn& a, Plan& p) {
   p.join_cols = 32 / (D / 8);   // whole warps
   while (p.join_cols * p.join_ways < TEAMS && p.join_cols < p.QV) p.join_cols *= 2;
   if (p.join_cols * p.join_ways > TEAMS) p.join_ways = TEAMS / p.join_cols;
+  while (p.join_ways > 1 && p.by_item && items * ((p.QV + p.join_cols - 1) / p.join_cols) > 2 * device_sm_count()) {
+    p.join_ways /= 2;
+    p.join_cols *= 2;
+  }
   return launch_k(kv8_join_k<D>, dim3(p.by_item ? items : p.grid, (p.QV + p.join_cols - 1) / p.join_cols),
                   dim3(p.join_cols * p.join_ways * (D / 8)), 0, st, a, p);
 }

@@ -104,6 +104,9 @@ __device__ __forceinline__ Group group_of(const Kv8Attn& a, const Plan& p, int g
   const int s0 = sidx * a.rows_per_seq, s1 = (int)min((long long)s0 + a.rows_per_seq, (long long)a.R);
   o.r0 = s0 + rb * p.RB;
   o.r1 = gi < p.groups ? min(o.r0 + p.RB, s1) : o.r0;   // a block that exists has rows
+  // (the first rows' numbers are on their way while the sequence's is)
+  const int first = o.r0 + sub;
+  const int first_rs = first < o.r1 ? a.row_seq[first] : -1, first_slot = first < o.r1 && a.mode == 0 ? a.row_slot[first] : 0;
   o.seq = o.r0 < o.r1 ? first_seq(a, s0, s1) : -1;
   bool bad = o.seq >= a.c.max_batch;
   if (bad) o.seq = -1;
@@ -113,8 +116,8 @@ __device__ __forceinline__ Group group_of(const Kv8Attn& a, const Plan& p, int g
     bad = bad || ctx < 0;
     const int words = (a.tree_T + 63) >> 6;
     for (int r = o.r0 + sub; r < o.r1; r += width) {
-      const int rs = a.row_seq[r];
-      int end = a.mode == 0 ? min(a.row_slot[r], INT32_MAX - 1) + 1 : ctx;
+      const int rs = r == first ? first_rs : a.row_seq[r];
+      int end = a.mode == 0 ? min(r == first ? first_slot : a.row_slot[r], INT32_MAX - 1) + 1 : ctx;
       if (a.mode == 1)
         for (int w = 0; w < words; ++w) {
           uint64_t m = a.mask[(size_t)r * a.mask_words + w];
@@ -137,14 +140,24 @@ struct Part {
   const float *ml, *o;
 };
 // Adds n partials to (top, L, o), o 8 values of a query vector whose D values are spread over D / 8 neighbouring
-// lanes (sub: this lane's place among them): the lanes share the (m, l) pairs, the sums run in the order of the partials.
-template <int D, typename At>
+// lanes (sub: this lane's place among them): the lanes share the (m, l) pairs, the sums run in the order of the partials,
+// the values of FB partials are in flight at a time.
+__device__ __forceinline__ void load8(const float* p, float4* x) {
+  x[0] = reinterpret_cast<const float4*>(p)[0];
+  x[1] = reinterpret_cast<const float4*>(p)[1];
+}
+template <int D, int FB, typename At>
 __device__ __forceinline__ void fold(int n, At at, int sub, float& top, float& L, float* o) {
   constexpr int GL = D / 8;
   const unsigned group = ((1u << GL) - 1u) << ((threadIdx.x & 31) / GL * GL);
   for (int i0 = 0; i0 < n; i0 += GL) {   // GL partials at a time
     float2 ml = make_float2(-INFINITY, 0.f);
     if (i0 + sub < n) ml = *reinterpret_cast<const float2*>(at(i0 + sub).ml);
+    const int cnt = min(GL, n - i0);
+    float4 x[FB][2];   // the first partials' values come under the maximum's way through the lanes
+#pragma unroll
+    for (int j = 0; j < FB; ++j)
+      if (j < cnt) load8(at(i0 + j).o + sub * 8, x[j]);
     float mx = fmaxf(top, ml.x);
 #pragma unroll
     for (int d = GL / 2; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(group, mx, d));
@@ -153,15 +166,19 @@ __device__ __forceinline__ void fold(int n, At at, int sub, float& top, float& L
     L *= f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) o[i] *= f;
-    const int cnt = min(GL, n - i0);
-#pragma unroll 4
-    for (int j = 0; j < cnt; ++j) {
-      const float4* x = reinterpret_cast<const float4*>(at(i0 + j).o + sub * 8);
-      const float4 a = x[0], b = x[1];
-      const float wj = __shfl_sync(group, w, j, GL);
-      L += __shfl_sync(group, lw, j, GL);
-      o[0] = fmaf(a.x, wj, o[0]); o[1] = fmaf(a.y, wj, o[1]); o[2] = fmaf(a.z, wj, o[2]); o[3] = fmaf(a.w, wj, o[3]);
-      o[4] = fmaf(b.x, wj, o[4]); o[5] = fmaf(b.y, wj, o[5]); o[6] = fmaf(b.z, wj, o[6]); o[7] = fmaf(b.w, wj, o[7]);
+    for (int j0 = 0; j0 < cnt; j0 += FB) {
+#pragma unroll
+      for (int j = 0; j < FB; ++j)
+        if (j0 && j0 + j < cnt) load8(at(i0 + j0 + j).o + sub * 8, x[j]);
+#pragma unroll
+      for (int j = 0; j < FB; ++j)
+        if (j0 + j < cnt) {
+          const float4 a = x[j][0], b = x[j][1];
+          const float wj = __shfl_sync(group, w, j0 + j, GL);
+          L += __shfl_sync(group, lw, j0 + j, GL);
+          o[0] = fmaf(a.x, wj, o[0]); o[1] = fmaf(a.y, wj, o[1]); o[2] = fmaf(a.z, wj, o[2]); o[3] = fmaf(a.w, wj, o[3]);
+          o[4] = fmaf(b.x, wj, o[4]); o[5] = fmaf(b.y, wj, o[5]); o[6] = fmaf(b.z, wj, o[6]); o[7] = fmaf(b.w, wj, o[7]);
+        }
     }
   }
 }

@@ -34,7 +34,7 @@ namespace {
 
 constexpr int TK = 32;            // keys a tile
 // head_dim 128 with more query vectors a block goes to tcgen05 (128-key tiles). 64 ragged sequences of up to 2048 slots, 8 KV
-// heads, T rows of 4 query heads a KV head (mma.sync, tcgen05): T = 1 45, 82 us; 2 45, 82; 4 65, 83; 8 182, 84; 17 180, 92.
+// heads, T rows of 4 query heads a KV head (mma.sync, tcgen05): T = 1 45, 82 us; 2 45, 82; 4 58, 81; 6 94, 82; 8 96, 83.
 constexpr int TC_ABOVE = 16;
 constexpr float LAZY = 8.f;       // how far (log2) a score may pass the reference maximum
 constexpr int E_UP = 4, E_DOWN = 12;   // exponents a tile may have around the reference, E_SPAN within one pass
@@ -589,7 +589,7 @@ __global__ void __launch_bounds__(Shape<D, NT, WN, WK, NS, CTAS>::THREADS, CTAS)
         if (whole) {
           const int in = (int)(col * p.G_inv >> 16), row = r0 + in;
           const size_t at = (size_t)row * a.nq + h * p.G + col - in * p.G;
-          fold<D, 6>(p.n_prefix, [&](int k) { return prefix_part<D>(a, p, k, at); }, c / 8, top, L, o);
+          fold<D, (NT == 1 ? 6 : 2)>(p.n_prefix, [&](int k) { return prefix_part<D>(a, p, k, at); }, c / 8, top, L, o);
           store8(a, at, D, c, __float_as_int(s_col[col].y) >= 0, L, o);
         } else {
           const size_t q = (size_t)slot * p.qv_pad + col;
@@ -747,14 +747,15 @@ cudaError_t launch_own(cudaStream_t st, const Kv8Attn& a, Plan& p, const CUtenso
 }
 
 // The narrowest configuration that holds a block's query vectors: small ones in two CTAs an SM (one's joins under the
-// other's loads), large ones in one CTA of eight warps. 64 ragged sequences of up to 2048 slots, 8 KV heads of 64: 32 query
+// other's loads), large ones in one CTA of eight warps. A second query tile goes to other warps, not to the same: they widen
+// the codes once more, but nothing spills (16 query vectors of 128: 58 us, 65 with both in a warp). 64 ragged sequences of up to 2048 slots, 8 KV heads of 64: 32 query
 // vectors a block 60 us (two query tiles a warp, two CTAs; 96 with four a warp in one CTA, whose registers spill), 48 86 us
 // (94 in two CTAs of 64), 64 96 us (104 and 116 in one CTA), 96 126 us, 128 162 us.
 template <int D>
 cudaError_t launch_mma(cudaStream_t st, const Kv8Attn& a, Plan& p, const CUtensorMap& mk, const CUtensorMap& mv) {
   const int t = p.qv_pad / 8;
   if (t <= 1) return launch_own<D, 1, 1, 4, 10, 2>(st, a, p, mk, mv);
-  if (t <= 2) return launch_own<D, 2, 1, 4, 9, 2>(st, a, p, mk, mv);
+  if (t <= 2) return launch_own<D, 1, 2, 2, 10, 2>(st, a, p, mk, mv);
   if constexpr (D == 64) {
     if (t <= 4) return launch_own<D, 2, 2, 2, 9, 2>(st, a, p, mk, mv);
     if (t <= 6) return launch_own<D, 3, 2, 4, 18, 1>(st, a, p, mk, mv);

@@ -19,9 +19,9 @@
 //     then need no reduction across lanes and no rescaling of O. Each column decides for itself.
 // A producer warp streams the tiles (TMA, 128- or 64-byte swizzle) through a ring that runs on across items, row warps
 // prepare the next item's query vectors, and the key groups' sums meet in shared memory, side by side where it lasts.
-// Bound by HBM once a range is long: one sequence of 32768 slots (8 KV heads of 128, 4 query heads each) 24 us, of them
-// some 12 us of loads at 5.6 TB/s, 4 us until the first tile is there and 6 us for the join's launch; 64 ragged sequences
-// of up to 2048 slots 43 us (21 us of bytes at the copy rate).
+// Bound by HBM once a range is long: one sequence of 32768 slots (8 KV heads of 128, 4 query heads each) 23 us, of them
+// some 12 us of loads at 5.6 TB/s, 4 us until the first tile is there and 5 us for the join's launch; 64 ragged sequences
+// of up to 2048 slots 41 us (21 us of bytes at the copy rate).
 #include "kv8_split.cuh"
 #include "kernels.h"
 

@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(Shape<D, NT, WN, WK, NS, CTAS>::THREADS, CTAS)
     const int r0 = sidx * a.rows_per_seq + rb * p.RB;
     const int r1 = min(min(r0 + p.RB, (sidx + 1) * a.rows_per_seq), a.R);
     const int nqv = (r1 - r0) * p.G;
-    const int ctx = a.mode == 1 && seq >= 0 ? a.ctx_len[seq] : 0;
+    const int ctx = a.mode == 1 && seq >= 0 ? __ldcg(a.ctx_len + seq) : 0;
     uint8_t* q_rows = sm + Sh::OFF_Q + buf * Sh::Q_BUF;
     float2* q_cols = reinterpret_cast<float2*>(q_rows + Sh::QV * Sh::Q_LD);
     uint64_t* q_mask = reinterpret_cast<uint64_t*>(q_cols + Sh::QV);
@@ -170,10 +170,10 @@ __global__ void __launch_bounds__(Shape<D, NT, WN, WK, NS, CTAS>::THREADS, CTAS)
         const int r = r0 + x / 4, w = x & 3;
         uint64_t m = 0;
         if (w * 64 < a.tree_T) {
-          m = a.mask[(size_t)r * a.mask_words + w];
+          m = __ldcg(a.mask + (size_t)r * a.mask_words + w);
           if (w == (a.tree_T - 1) >> 6 && (a.tree_T & 63)) m &= (1ull << (a.tree_T & 63)) - 1;
         }
-        q_mask[x] = seq >= 0 && a.row_seq[r] == seq ? m : 0ull;
+        q_mask[x] = seq >= 0 && __ldcg(a.row_seq + r) == seq ? m : 0ull;
       }
     int fullvis = INT32_MAX;   // keys below this are seen by every row that counts
     for (int x0 = sw * PER; x0 < Sh::QV; x0 += PER * warps * BATCH) {
@@ -187,10 +187,10 @@ __global__ void __launch_bounds__(Shape<D, NT, WN, WK, NS, CTAS>::THREADS, CTAS)
         lim[b] = 0;
         if (x < nqv) {
           const int in = (int)(x * p.G_inv >> 16), row = r0 + in;
-          raw[b] = *reinterpret_cast<const uint4*>((const __nv_bfloat16*)a.q +
-                                                   ((size_t)row * a.nq + h * p.G + x - in * p.G) * D + sub * 8);
-          rs[b] = a.row_seq[row];
-          lim[b] = a.mode == 1 ? ctx : min(a.row_slot[row], INT32_MAX - 1) + 1;
+          raw[b] = __ldcg(reinterpret_cast<const uint4*>((const __nv_bfloat16*)a.q +
+                                                         ((size_t)row * a.nq + h * p.G + x - in * p.G) * D + sub * 8));
+          rs[b] = __ldcg(a.row_seq + row);
+          lim[b] = a.mode == 1 ? ctx : min(__ldcg(a.row_slot + row), INT32_MAX - 1) + 1;
         }
       }
 #pragma unroll
@@ -624,7 +624,7 @@ __global__ void __launch_bounds__(256) kv8_join_k(const Kv8Attn a, const Plan p)
   const int col = blockIdx.y * p.join_cols + team % p.join_cols, c = threadIdx.x % GL * 8;
   const int col_in = min(col, nqv - 1), in = (int)(col_in * p.G_inv >> 16), row = r0 + in;
   const size_t at = (size_t)row * a.nq + h * p.G + col_in - in * p.G;
-  const int seq = first_seq(a, s0, s1), own = a.row_seq[row];
+  const int seq = first_seq(a, s0, s1), own = __ldcg(a.row_seq + row);
   // piece 0 in slot 2 c0 + 1 (it holds the item's start), the others in slot 2 c, then the prefix's
   const int pieces = c1 - c0 + 1, n = pieces + p.n_prefix;
   float top = -INFINITY, L = 0.f, o[8] = {};

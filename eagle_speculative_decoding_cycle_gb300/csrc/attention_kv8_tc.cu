@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(T_THREADS, 1)
     const int r0 = sidx * a.rows_per_seq + rb * p.RB;
     const int r1 = min(min(r0 + p.RB, (sidx + 1) * a.rows_per_seq), a.R);
     const int nqv = (r1 - r0) * p.G;
-    const int ctx = a.mode == 1 && seq >= 0 ? a.ctx_len[seq] : 0;
+    const int ctx = a.mode == 1 && seq >= 0 ? __ldcg(a.ctx_len + seq) : 0;
     uint8_t* q_hi = sm + TO_Q + wk * 2 * OPB;
     float2* cols = reinterpret_cast<float2*>(sm + TO_COL) + (wk * 2 + buf) * TT;
     uint64_t* masks = reinterpret_cast<uint64_t*>(sm + TO_MASK) + wk * TT * 4;
@@ -180,10 +180,10 @@ __global__ void __launch_bounds__(T_THREADS, 1)
         const int r = r0 + x / 4, w = x & 3;
         uint64_t m = 0;
         if (w * 64 < a.tree_T) {
-          m = a.mask[(size_t)r * a.mask_words + w];
+          m = __ldcg(a.mask + (size_t)r * a.mask_words + w);
           if (w == (a.tree_T - 1) >> 6 && (a.tree_T & 63)) m &= (1ull << (a.tree_T & 63)) - 1;
         }
-        masks[x] = seq >= 0 && a.row_seq[r] == seq ? m : 0ull;
+        masks[x] = seq >= 0 && __ldcg(a.row_seq + r) == seq ? m : 0ull;
       }
     int fullvis = INT32_MAX;   // keys below this are seen by every row that counts
     const float sl2 = a.scale * 1.4426950408889634f;
@@ -201,10 +201,10 @@ __global__ void __launch_bounds__(T_THREADS, 1)
           const int in = (int)(x * p.G_inv >> 16), row = r0 + in;
           const uint4* q = reinterpret_cast<const uint4*>((const __nv_bfloat16*)a.q +
                                                           ((size_t)row * a.nq + h * p.G + x - in * p.G) * TT + sub * 16);
-          raw[b][0] = q[0];
-          raw[b][1] = q[1];
-          rs[b] = a.row_seq[row];
-          lim[b] = a.mode == 1 ? ctx : min(a.row_slot[row], INT32_MAX - 1) + 1;
+          raw[b][0] = __ldcg(q);
+          raw[b][1] = __ldcg(q + 1);
+          rs[b] = __ldcg(a.row_seq + row);
+          lim[b] = a.mode == 1 ? ctx : min(__ldcg(a.row_slot + row), INT32_MAX - 1) + 1;
         }
       }
 #pragma unroll
@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(T_THREADS, 1)
       const int r0 = sidx * a.rows_per_seq + rb * p.RB;
       const int r1 = min(min(r0 + p.RB, (sidx + 1) * a.rows_per_seq), a.R);
       const int nqv = (r1 - r0) * p.G;
-      const int ctx = a.mode == 1 && seq >= 0 ? a.ctx_len[seq] : 0;
+      const int ctx = a.mode == 1 && seq >= 0 ? __ldcg(a.ctx_len + seq) : 0;
       kv8_wait(smem_u32(q_full), (uint32_t)(item & 1), abort_flag, a.err);
       int fullvis = s_fullvis[buf * 16];
 #pragma unroll 1
@@ -508,7 +508,7 @@ __global__ void __launch_bounds__(T_THREADS, 1)
         L = fmaf(v.y, ex2(v.x - tb), L);
       }
       // (E = 0: no value counted, O is zero or NaN)
-      const bool live = whole && r < nqv && seq >= 0 && a.row_seq[row] == seq;
+      const bool live = whole && r < nqv && seq >= 0 && __ldcg(a.row_seq + row) == seq;
       const float inv = whole ? (live && L != 0.f ? 1.f / L : 0.f) : 1.f;
       const float unit = own * pow2i(E ? E - KV8_BIAS - T_SHIFT : 0);
 #pragma unroll 1

@@ -27,7 +27,7 @@ struct Kv8 {
 // long cache pass 2^32 bytes.
 __device__ __forceinline__ long long kv8_vec(const Kv8& c, int seq, int h, int slot) {
   if (!c.table) return ((long long)seq * c.nkv + h) * c.cap + slot;
-  const int blk = c.table[(size_t)seq * c.tab_w + (slot >> c.block_log2)];
+  const int blk = __ldcg(c.table + (size_t)seq * c.tab_w + (slot >> c.block_log2));
   if (blk < 0 || blk >= c.n_blocks) return -1;
   return (((long long)blk * c.nkv + h) << c.block_log2) + (slot & ((1 << c.block_log2) - 1));
 }

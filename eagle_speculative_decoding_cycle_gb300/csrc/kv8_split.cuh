@@ -58,6 +58,8 @@ struct Plan {
 // Behind the prefix kernel the own slots' kernel starts as soon as that one's last CTAs have started (they trigger it
 // after their own wait, so all that came before the call is complete), and waits for its partials where it reads them.
 // One thread of each CTA waits before it ends, so that the join finds both kernels complete.
+// What it reads before that (rows, lengths, masks, tables, q) comes from L2 by __ldcg, cp.async.cg or TMA: no line that an
+// earlier kernel left in an SM's L1.
 __device__ __forceinline__ void late_entry(const Plan& p) {
   if (!p.late) pdl_wait();
   pdl_trigger();
@@ -92,8 +94,8 @@ struct Group {
   int r0, r1, seq, limit;
 };
 __device__ __forceinline__ int first_seq(const Kv8Attn& a, int s0, int s1) {
-  int seq = a.row_seq[s0];
-  for (int r = s0 + 1; r < s1 && seq < 0; ++r) seq = a.row_seq[r];
+  int seq = __ldcg(a.row_seq + s0);
+  for (int r = s0 + 1; r < s1 && seq < 0; ++r) seq = __ldcg(a.row_seq + r);
   return seq < 0 ? -1 : seq;
 }
 // By `width` neighbouring lanes (a power of two up to 8); gi out of range gives an empty block. All lanes of a warp call.
@@ -106,21 +108,21 @@ __device__ __forceinline__ Group group_of(const Kv8Attn& a, const Plan& p, int g
   o.r1 = gi < p.groups ? min(o.r0 + p.RB, s1) : o.r0;   // a block that exists has rows
   // (the first rows' numbers are on their way while the sequence's is)
   const int first = o.r0 + sub;
-  const int first_rs = first < o.r1 ? a.row_seq[first] : -1, first_slot = first < o.r1 && a.mode == 0 ? a.row_slot[first] : 0;
+  const int first_rs = first < o.r1 ? __ldcg(a.row_seq + first) : -1, first_slot = first < o.r1 && a.mode == 0 ? __ldcg(a.row_slot + first) : 0;
   o.seq = o.r0 < o.r1 ? first_seq(a, s0, s1) : -1;
   bool bad = o.seq >= a.c.max_batch;
   if (bad) o.seq = -1;
-  const int ctx = a.mode == 1 && o.seq >= 0 ? a.ctx_len[o.seq] : 0;
+  const int ctx = a.mode == 1 && o.seq >= 0 ? __ldcg(a.ctx_len + o.seq) : 0;
   int lim = 0;
   if (o.seq >= 0) {
     bad = bad || ctx < 0;
     const int words = (a.tree_T + 63) >> 6;
     for (int r = o.r0 + sub; r < o.r1; r += width) {
-      const int rs = r == first ? first_rs : a.row_seq[r];
-      int end = a.mode == 0 ? min(r == first ? first_slot : a.row_slot[r], INT32_MAX - 1) + 1 : ctx;
+      const int rs = r == first ? first_rs : __ldcg(a.row_seq + r);
+      int end = a.mode == 0 ? min(r == first ? first_slot : __ldcg(a.row_slot + r), INT32_MAX - 1) + 1 : ctx;
       if (a.mode == 1)
         for (int w = 0; w < words; ++w) {
-          uint64_t m = a.mask[(size_t)r * a.mask_words + w];
+          uint64_t m = __ldcg(a.mask + (size_t)r * a.mask_words + w);
           if (w == words - 1 && (a.tree_T & 63)) m &= (1ull << (a.tree_T & 63)) - 1;
           if (m) end = (int)min((long long)INT32_MAX, (long long)ctx + w * 64 + 64 - __clzll((long long)m));
         }

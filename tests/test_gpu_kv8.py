@@ -568,3 +568,29 @@ def test_a_negative_context_hides_its_sequence(P):
     k.trees[12:24] = False                             # the prefix alone, or nothing
     want, tol = k.want()
     assert np.all(np.abs(out.double().cpu().numpy() - want) <= tol)
+
+
+@pytest.mark.parametrize("T,P", [(1, 200), (12, 200), (12, 0)])
+def test_inputs_changed_between_calls(T, P):
+    """Queries, lengths, masks and cache entries rewritten in place on the stream just before each call."""
+    k = Case(6, T, 16, 4, 128, [300, 0, 77, 128, 3, 64], 1, 16, P, seed=35)
+    rs, qs = i32(k.row_seq), [k.q.roll(j, 0).clone() for j in range(6)]
+    cs = [i32((k.ctx + 37 * j) % 290) for j in range(6)]
+    ms = [bits_of(np.roll(k.trees, j * T, 0), T) for j in range(6)]
+    ks = [torch.randn(6, 4, 128, device=DEV) for _ in range(6)]
+    slot = i32(np.zeros(6))
+    seqs = i32(np.arange(6))
+    q, cx, mask = k.q.clone(), cs[0].clone(), ms[0].clone()
+
+    def step(j):
+        q.copy_(qs[j]), mask.copy_(ms[j])
+        api.kv8_write(k.c, ks[j], ks[j], seqs, slot)
+        cx.copy_(cs[j])
+        return api.attention_shared_kv8(q, k.pk, k.pv, k.c, rs, None, cx, T, 1, T, mask)
+
+    alone = []
+    for j in range(6):
+        alone.append(step(j))
+        torch.cuda.synchronize()
+    for _ in range(4):
+        assert all(torch.equal(a, b) for a, b in zip(alone, [step(j) for j in range(6)]))

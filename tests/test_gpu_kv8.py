@@ -594,3 +594,24 @@ def test_inputs_changed_between_calls(T, P):
         torch.cuda.synchronize()
     for _ in range(4):
         assert all(torch.equal(a, b) for a, b in zip(alone, [step(j) for j in range(6)]))
+
+
+@pytest.mark.parametrize("T,R,d,P", [(9, 24, 128, 0), (9, 19, 128, 60), (3, 7, 64, 0), (40, 95, 128, 0)])
+def test_a_last_sequence_with_fewer_rows(T, R, d, P):
+    k = Case(3, T, 16, 4, d, [50, 200, 7], 1, 16, P, seed=36)
+    k.err = err_word()
+    mask = bits_of(k.trees, T)
+    big = torch.full_like(k.q, 9.0)
+    out = api.attention_shared_kv8(k.q[:R], k.pk, k.pv, k.c, i32(k.row_seq[:R]), None, i32(k.ctx), T, 1, T, mask[:R],
+                                   out=big[:R], err=k.err)
+    want, tol = k.want(range(R))
+    assert int(k.err) == 0 and torch.all(big[R:] == 9)
+    assert np.all(np.abs(out.double().cpu().numpy() - want[:R]) <= tol[:R])
+
+
+def test_one_sequence_of_more_rows_than_there_are():
+    k = Case(1, 5, 8, 2, 128, 90, 0, 16, seed=37)
+    a = k.check()
+    k.T = 1 << 20
+    b = k.run()
+    assert int(k.err) == 0 and torch.equal(a, b)

@@ -390,21 +390,9 @@ def _need(ok: bool, what: str) -> None:
         raise ValueError(what)
 
 
-class _Current:
-    """The cache's device made current for a launch (nothing to do where it is already)."""
-    __slots__ = ("index", "before")
-
-    def __init__(self, index: int):
-        self.index = index
-
-    def __enter__(self):
-        self.before = torch.cuda.current_device()
-        if self.before != self.index:
-            torch.cuda.set_device(self.index)
-
-    def __exit__(self, *exc):
-        if self.before != self.index:
-            torch.cuda.set_device(self.before)
+def _elsewhere(index: int) -> bool:
+    """Whether another device than the cache's is current: a launch then goes under torch.cuda.device."""
+    return torch._C._cuda_getDevice() != index
 
 
 _HERE = nullcontext()
@@ -504,9 +492,11 @@ def kv8_write(cache: KV8Cache, k: torch.Tensor, v: torch.Tensor, row_seq: torch.
     R, code, ldk, ldv = _kv_rows(cache, k, v)
     seq, slot = _row_list(cache, row_seq, R, "row_seq"), _row_list(cache, row_slot, R, "row_slot")
     e = _err_word(cache, err)
-    with _Current(cache.index):
-        rc = L.lib().eagle_op_kv8_write(_stream_of(cache.index, stream), cache.ref, code, k.data_ptr(), ldk,
-                                        v.data_ptr(), ldv, R, seq, slot, e)
+    if _elsewhere(cache.index):
+        with torch.cuda.device(cache.index):
+            return kv8_write(cache, k, v, row_seq, row_slot, err, stream)
+    rc = L.lib().eagle_op_kv8_write(_stream_of(cache.index, stream), cache.ref, code, k.data_ptr(), ldk, v.data_ptr(),
+                                    ldv, R, seq, slot, e)
     L.check(rc, "eagle_op_kv8_write")
 
 
@@ -527,9 +517,11 @@ def kv8_read(cache: KV8Cache, row_seq: torch.Tensor, row_slot: torch.Tensor, dty
     _need(R == n, "out must have a row for each entry of row_seq")
     seq, slot = _row_list(cache, row_seq, R, "row_seq"), _row_list(cache, row_slot, R, "row_slot")
     e = _err_word(cache, err)
-    with _Current(cache.index):
-        rc = L.lib().eagle_op_kv8_read(_stream_of(cache.index, stream), cache.ref, code, k.data_ptr(), ldk,
-                                       v.data_ptr(), ldv, R, seq, slot, e)
+    if _elsewhere(cache.index):
+        with torch.cuda.device(cache.index):
+            return kv8_read(cache, row_seq, row_slot, dtype, (k, v), err, stream)
+    rc = L.lib().eagle_op_kv8_read(_stream_of(cache.index, stream), cache.ref, code, k.data_ptr(), ldk, v.data_ptr(),
+                                   ldv, R, seq, slot, e)
     L.check(rc, "eagle_op_kv8_read")
     return k, v
 
@@ -587,10 +579,13 @@ def attention_shared_kv8(q: torch.Tensor, prefix_k: Optional[torch.Tensor], pref
             scratch = attention_kv8_scratch(cache, R, nq, rows_per_seq, P)
     if scratch.dtype is not torch.uint8 or not scratch.is_contiguous() or scratch.get_device() != index:
         raise ValueError("scratch must be a contiguous uint8 tensor on the cache's device")
-    with _Current(index):
-        rc = L.lib().eagle_op_attention_shared_kv8(
-            _stream_of(index, stream), cache.ref, pk, pv, P, q.data_ptr(), out.data_ptr(), R, nq, rows_per_seq, seq,
-            slot, ctx, mode, tree_T, mp, mw, scale, scratch.data_ptr(), scratch.numel(), e)
+    if _elsewhere(index):
+        with torch.cuda.device(index):
+            return attention_shared_kv8(q, prefix_k, prefix_v, cache, row_seq, row_slot, ctx_len, rows_per_seq, mode,
+                                        tree_T, mask, scale, out, scratch, err, stream)
+    rc = L.lib().eagle_op_attention_shared_kv8(
+        _stream_of(index, stream), cache.ref, pk, pv, P, q.data_ptr(), out.data_ptr(), R, nq, rows_per_seq, seq, slot,
+        ctx, mode, tree_T, mp, mw, scale, scratch.data_ptr(), scratch.numel(), e)
     L.check(rc, "eagle_op_attention_shared_kv8")
     return out
 

@@ -360,21 +360,21 @@ __global__ void __launch_bounds__(T_THREADS, 1)
         tc_fence_after();
         float mx = -INFINITY;
 #pragma unroll 1
-        for (int c = 0; c < 64; c += 16) {   // few live values: a spill goes to L2, next to 220 KB of shared memory
-          float s[16];
-          tmem_ld16(tS + c, s);
+        for (int c = 0; c < 64; c += 32) {
+          float s[32];
+          tmem_ld32(tS + c, s);
           if (!narrow)   // as they come
-            for (int j = 0; j < 16; ++j) keep[c + j] = s[j];
+            for (int j = 0; j < 32; ++j) keep[c + j] = s[j];
 #pragma unroll
-          for (int j = 0; j < 16; j += 4) {
+          for (int j = 0; j < 32; j += 4) {
             const float4 f = *reinterpret_cast<const float4*>(s_kf + c0 + c + j);
             s[j] *= f.x; s[j + 1] *= f.y; s[j + 2] *= f.z; s[j + 3] *= f.w;
           }
           if (masked)
 #pragma unroll
-            for (int j = 0; j < 16; ++j) s[j] = (vis[c >> 5] >> ((c & 16) + j)) & 1u ? s[j] : -INFINITY;
+            for (int j = 0; j < 32; ++j) s[j] = (vis[c >> 5] >> j) & 1u ? s[j] : -INFINITY;
 #pragma unroll
-          for (int j = 0; j < 16; j += 8)
+          for (int j = 0; j < 32; j += 8)
             mx = max3(mx, max3(s[j], s[j + 1], s[j + 2]), max3(max3(s[j + 3], s[j + 4], s[j + 5]), s[j + 6], s[j + 7]));
         }
         float* x_max = reinterpret_cast<float*>(sm + TO_X) + (wk * 2 + tp) * 2 * TT;

@@ -14,10 +14,10 @@
 // other half's value product and next S, and the other tile's. (S of 128 keys at once leaves a chain of product, softmax,
 // product: 121 us in all for 4096 shared tokens under 64 x 17 rows of 32 heads, against 106; with two threads a query vector
 // 118; halves with one issuing warp for both tiles 135, each of its waits taking some 250 clocks.)
-// TMEM: S0 S1 (128 columns each, P over the first half of each 64), O0 O1 (d each). That prefix alone: 66 us under the
-// profiler, tensor pipe 46% active; 38 us of products at the rate of a large GEMM. 128 keys of a pair of tiles take some 3300
-// clocks, 2048 of them products at full width: products of 64 columns read their operands twice as often, and the
-// hand-overs between the warps do the rest.
+// TMEM: S0 S1 (128 columns each, P over the first half of each 64), O0 O1 (d each). That prefix alone: 62 us, of them 38 us
+// of products at the rate of a large GEMM; tensor pipe 46% active. 128 keys of a pair of tiles take some 3300 clocks where
+// their products take 2048: bound by the way of a half through its warps and back (softmax 900 clocks, hand-overs and issue
+// some 1500, two halves under way a tile; with an eighth of the products 8 us less, without the ex2 2 us less).
 // Weights are rounded to bf16 (2^-8 relative at most, as the bf16 V that they meet; their sum is kept in fp32 of the
 // unrounded weights). Results leave as fp32 partials (o, m, l) of each key range, which the attention over the rows' own
 // slots joins in its epilogue.

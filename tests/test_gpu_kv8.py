@@ -615,3 +615,14 @@ def test_one_sequence_of_more_rows_than_there_are():
     k.T = 1 << 20
     b = k.run()
     assert int(k.err) == 0 and torch.equal(a, b)
+
+
+@pytest.mark.parametrize("T,block", [(1, 0), (12, 0), (1, 256), (12, 256)])
+def test_a_cache_of_more_than_four_gigabytes(T, block):
+    """Codes past 2^32 bytes: the last heads of a long contiguous cache, blocks from all over a large pool."""
+    k = Case(1, T, 16, 4, 128, 600, 1, block, seed=38, cap=1 << 24)
+    assert k.c.k.numel() > 2 ** 32
+    k.check()
+    n = 600 + T
+    got, _ = api.kv8_read(k.c, i32(np.zeros(n)), i32(np.arange(n)), dtype=torch.float32)
+    assert np.array_equal(got.double().cpu().numpy(), k.K[0])

@@ -258,10 +258,11 @@ __global__ void __launch_bounds__(Shape<D, NT, WN, WK, NS, CTAS>::THREADS, CTAS)
         const int t = b + lane, live = limit - t * TK;
         if (t < k.t1 && live > 0) {
           const long long v = kv8_vec(a.c, seq, k.h, t * TK);
-          long long u = v + 16;
           halves = 1;
           if (box == TK ? (a.c.table || t * TK + 16 < a.c.cap) : live > 16) halves = 2;
-          if (box < TK && halves == 2) u = kv8_vec(a.c, seq, k.h, t * TK + 16);
+          // the second half's vector: of its own block, or 16 on from the first, if that one has a block at all
+          // (every start stays a multiple of 16: its exponents are copied 16 bytes at a time)
+          const long long u = halves == 2 && box < TK ? kv8_vec(a.c, seq, k.h, t * TK + 16) : v < 0 ? v : v + 16;
           if (v < 0 || (halves == 2 && u < 0)) latch_error(a.err, DEVERR_BOUNDS);   // not assigned: unspecified keys
           vec0 = (int)max(v, 0ll);
           vec1 = (int)max(u, 0ll);

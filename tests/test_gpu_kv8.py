@@ -626,3 +626,25 @@ def test_a_cache_of_more_than_four_gigabytes(T, block):
     n = 600 + T
     got, _ = api.kv8_read(k.c, i32(np.zeros(n)), i32(np.arange(n)), dtype=torch.float32)
     assert np.array_equal(got.double().cpu().numpy(), k.K[0])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("T", [1, 12])
+@pytest.mark.parametrize("block", [16, 32, 64, 256])
+@pytest.mark.parametrize("P", [0, 40])
+def test_blocks_that_are_not_assigned(block, T, d, P):
+    """Table entries below a sequence's length that are -1 or past the pool, one or all of them: latched, and the other
+    sequences' rows keep their bits."""
+    k = Case(3, T, 16, 4, d, [150, 300, 77], 1, block, P, seed=40)
+    want = k.check()
+    good = k.c.table.clone()
+    others = [r for r in range(3 * T) if r // T != 1]
+    for at, entry in ((0, -1), (299 // block, k.c.n_blocks), (100 // block, -2 ** 31), (64 // block, 2 ** 31 - 1),
+                      (slice(None), -1)):
+        k.c.table.copy_(good)
+        k.c.table[1, at] = entry
+        out = k.run()
+        assert int(k.err) == 2, (at, entry)
+        assert torch.equal(out[others], want[others]), (at, entry)
+    k.c.table.copy_(good)
+    assert torch.equal(k.run(), want) and int(k.err) == 0

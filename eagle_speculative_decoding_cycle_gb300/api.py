@@ -391,7 +391,9 @@ def _need(ok: bool, what: str) -> None:
 
 
 def _elsewhere(index: int) -> bool:
-    """Whether another device than the cache's is current: a launch then goes under torch.cuda.device."""
+    """Whether another device than the cache's is current: a launch then goes under torch.cuda.device. A cache
+    of the CPU (index -1, as of all the CPU's tensors) is refused here."""
+    _need(index >= 0, "the cache and its call's tensors must be on a GPU")
     return torch._C._cuda_getDevice() != index
 
 

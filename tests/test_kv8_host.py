@@ -141,3 +141,17 @@ def test_out_may_be_q_but_not_overlap_it(lib):
     step = 32 * 128 * 2
     for out in (FAKE + step, FAKE + 8 * step - 16, FAKE - 16):
         assert attn(lib, cache(), q=FAKE, out=out) == L.EAGLE_EINVAL
+
+
+def test_tensors_of_the_cpu_are_refused():
+    """Calls whose tensors agree with one another but lie on the CPU: refused before any launch."""
+    c = cpu_cache()
+    rows, i32 = torch.zeros(4, 3, 64), torch.zeros(4, dtype=torch.int32)
+    q = torch.zeros(4, 6, 64, dtype=torch.bfloat16)
+    for call in (lambda: api.kv8_write(c, rows, rows, i32, i32), lambda: api.kv8_read(c, i32, i32),
+                 lambda: api.kv8_read(c, i32, i32, out=(rows, rows)),
+                 lambda: api.attention_kv8(q, c, i32, i32, i32, 2, 0),
+                 lambda: api.attention_shared_kv8(q, torch.zeros(3, 5, 64, dtype=torch.bfloat16),
+                                                  torch.zeros(3, 5, 64, dtype=torch.bfloat16), c, i32, i32, i32, 2, 0)):
+        with pytest.raises(ValueError, match="GPU"):
+            call()

@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(Shape<D, NT, WN, WK, NS, CTAS>::THREADS, CTAS)
           }
           // exponents, lane = key: of the values, the largest and smallest that count
           const float fk = kv8_pow2(s_ke[lane]);
-          const int vbyte = s_ve[lane];
+          const int vbyte = max((int)s_ve[lane], KV8_LOWEST);
           const bool counts = ((seen >> lane) & 1u) && vbyte != KV8_BAD;
           int hi = (int)__reduce_max_sync(0xffffffffu, counts ? (uint32_t)vbyte : 0u);
           const int lo_all = (int)__reduce_min_sync(0xffffffffu, counts ? (uint32_t)vbyte : 255u);

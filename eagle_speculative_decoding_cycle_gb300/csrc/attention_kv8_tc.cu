@@ -311,7 +311,7 @@ __global__ void __launch_bounds__(T_THREADS, 1)
         float* s_kf = reinterpret_cast<float*>(sm + TO_KF) + (wk * 2 + tp) * TT;
         float* s_va = reinterpret_cast<float*>(sm + TO_VF) + (wk * 2 + tp) * 2 * TT;   // log2 of a weight's factor
         float* s_vi = s_va + TT;                                                      // the factor's inverse
-        const int vbyte = s_exp[TT + r];
+        const int vbyte = max((int)s_exp[TT + r], KV8_LOWEST);
         const bool counts = seen && vbyte != KV8_BAD;
         if (!hf) {
           s_kf[r] = kv8_pow2(s_exp[r]);

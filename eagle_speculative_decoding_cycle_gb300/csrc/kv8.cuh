@@ -13,6 +13,8 @@ namespace eagle {
 
 constexpr int KV8_E_LO = -40, KV8_E_HI = 40;   // exponents that a written vector can get
 constexpr int KV8_BIAS = 127;
+constexpr int KV8_LOWEST = KV8_E_LO + KV8_BIAS;   // the lowest byte that is written; attention takes the byte 0 of cleared
+                                               // memory (zero codes) for it, so that 0 can mean "none" beside the bytes
 constexpr int KV8_BAD = 255;                   // exponent byte of a vector with an entry that is not finite
 
 struct Kv8 {

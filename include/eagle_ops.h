@@ -109,7 +109,9 @@ int eagle_op_attention(int dtype, void* stream, const void* q, const void* kcach
  * (magnitudes above 448 * 2^40 saturate); a vector with an entry that is not finite gets byte
  * 255 and zero codes, and reads back as NaN throughout. Reading is exact in bf16 and fp32, and
  * writing what was read stores the same values, so entries move (compaction of an accepted path,
- * a sequence handed to another cache) by eagle_op_kv8_read and eagle_op_kv8_write.
+ * a sequence handed to another cache) by eagle_op_kv8_read and eagle_op_kv8_write. Cleared memory
+ * (codes and bytes zero) counts as zero vectors. A slot that is read or that an attention row sees
+ * holds what was written, or cleared memory; other bytes give unspecified values there.
  *
  * table == NULL: contiguous, codes [max_batch][n_kv_heads][cap][head_dim] and exponents
  * [max_batch][n_kv_heads][cap]; cap a multiple of 16. Otherwise paged: pools

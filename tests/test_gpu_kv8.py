@@ -648,3 +648,36 @@ def test_blocks_that_are_not_assigned(block, T, d, P):
         assert torch.equal(out[others], want[others]), (at, entry)
     k.c.table.copy_(good)
     assert torch.equal(k.run(), want) and int(k.err) == 0
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("T", [1, 12])
+@pytest.mark.parametrize("P", [0, 40])
+def test_slots_that_were_never_written(T, d, P):
+    """Cleared memory (KV8Cache.empty) in slots that rows see, between written ones and before them: zero keys and
+    values, as kv8_read gives them."""
+    k = Case(3, T, 16, 4, d, [300, 290, 70], 1, 0, P, seed=41)
+    for b, lo, hi in ((0, 100, 200), (0, 17, 18), (1, 0, 45), (1, 60, 64), (1, 289, 290), (2, 0, 70 + T)):
+        for t in (k.c.k, k.c.v, k.c.k_exp, k.c.v_exp):
+            t[b, :, lo:hi] = 0
+        k.K[b, lo:hi] = 0
+        k.V[b, lo:hi] = 0
+    kk, vv = api.kv8_read(k.c, i32([0] * 100), i32(np.arange(100, 200)))
+    assert not kk.any() and not vv.any()
+    out = k.check()
+    if not P:
+        assert not out[2 * T:].any()
+    assert torch.equal(k.run(), out)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("T", [1, 12])
+def test_written_and_cleared_bands(T, d):
+    """Long ranges a CTA in which written and cleared bands of 128 slots take turns."""
+    k = Case(12, T, 16, 8, d, 2000, 1, seed=42)
+    off = np.nonzero(np.arange(2000) // 128 % 2)[0]
+    for t in (k.c.k, k.c.v, k.c.k_exp, k.c.v_exp):
+        t[:, :, torch.from_numpy(off).to(DEV)] = 0
+    k.K[:, off] = 0
+    k.V[:, off] = 0
+    k.check(rows=[0, T, 12 * T - 1])

@@ -11,12 +11,11 @@
 // would be 3% full; and both operands that come from the cache are A fragments, which a warp converts from e4m3
 // right after ldmatrix (fp16 holds every code exactly; cvt runs at 128 codes a clock and SM against the 23 bytes a
 // clock that HBM delivers).
-//   - A key's exponent multiplies its score, a value's exponent its weight: the codes are never scaled.
+//   - A key's factor multiplies its score, a value's exponent is added to it: the codes are never scaled.
 //   - q is scaled by a power of two into fp16's range (exact down to 2^-38 of its largest entry).
-//   - Weights enter the value product as fp16 (2^-11), scaled by 2^(e_s - E), E the warp's running
-//     reference exponent; a tile whose exponents span more than fp16 bears is taken in several passes.
-//   - The maximum is raised only when a score passes it by 2^8: fp16 holds weights up to 2^16, and most tiles
-//     then need no reduction across lanes and no rescaling of O. Each column decides for itself.
+//   - Weights times their values' factors enter the value product as fp16 (2^-11), against a reference of each query
+//     vector that is raised only when a product passes it by 2^15: most tiles then need no reduction across lanes and no
+//     rescaling of O. Each column decides for itself.
 // A producer warp streams the tiles (TMA, 128- or 64-byte swizzle) through a ring that runs on across items, row warps
 // prepare the next item's query vectors, and the key groups' sums meet in shared memory, side by side where it lasts.
 // Bound by HBM once a range is long: one sequence of 32768 slots (8 KV heads of 128, 4 query heads each) 23 us, of them
@@ -36,9 +35,6 @@ constexpr int TK = 32;            // keys a tile
 // head_dim 128 with more query vectors a block goes to tcgen05 (128-key tiles). 64 ragged sequences of up to 2048 slots, 8 KV
 // heads, T rows of 4 query heads a KV head (mma.sync, tcgen05): T = 1 45, 82 us; 2 45, 82; 4 58, 81; 6 94, 82; 8 96, 83.
 constexpr int TC_ABOVE = 16;
-constexpr float LAZY = 8.f;       // how far (log2) a score may pass the reference maximum
-constexpr int E_UP = 4, E_DOWN = 12;   // exponents a tile may have around the reference, E_SPAN within one pass
-constexpr int E_SPAN = 14;
 
 __device__ __forceinline__ void mma_f16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -334,18 +330,17 @@ __global__ void __launch_bounds__(Shape<D, NT, WN, WK, NS, CTAS>::THREADS, CTAS)
       int fullvis = s_fullvis[buf * 16];
       for (int w = 1; w < (item ? Sh::ROWS_W : NW + Sh::ROWS_W); ++w) fullvis = min(fullvis, s_fullvis[buf * 16 + w]);
 
-      float O[D / 16][NT][4], m[NT][2], l[NT][2], qf[NT][2];
+      float O[D / 16][NT][4], ref[NT][2], l[NT][2], qf[NT][2];
 #pragma unroll
       for (int x = 0; x < NT; ++x) {
 #pragma unroll
         for (int c = 0; c < D / 16; ++c) O[c][x][0] = O[c][x][1] = O[c][x][2] = O[c][x][3] = 0.f;
         const int col = (nw * NT + x) * 8 + 2 * t4;
-        m[x][0] = m[x][1] = -INFINITY;
+        ref[x][0] = ref[x][1] = -INFINITY;
         l[x][0] = l[x][1] = 0.f;
         qf[x][0] = s_col[col].x;
         qf[x][1] = s_col[col + 1].x;
       }
-      int E_run = 0;
 
       for (int t = t0; t < t1; ++t, ++i) {
         if (i % WK != kw) continue;
@@ -384,139 +379,115 @@ __global__ void __launch_bounds__(Shape<D, NT, WN, WK, NS, CTAS>::THREADS, CTAS)
             seen |= __shfl_xor_sync(0xffffffffu, seen, 1);
             seen |= __shfl_xor_sync(0xffffffffu, seen, 2);
           }
-          // exponents, lane = key: of the values, the largest and smallest that count
-          const float fk = kv8_pow2(s_ke[lane]);
-          const int vbyte = max((int)s_ve[lane], KV8_LOWEST);
-          const bool counts = ((seen >> lane) & 1u) && vbyte != KV8_BAD;
-          int hi = (int)__reduce_max_sync(0xffffffffu, counts ? (uint32_t)vbyte : 0u);
-          const int lo_all = (int)__reduce_min_sync(0xffffffffu, counts ? (uint32_t)vbyte : 255u);
-          bool first = true;
-          while (true) {
-            const bool one = hi - lo_all <= E_SPAN;
-            const int lo = one ? 0 : hi - E_SPAN;
-            float unit = 1.f;   // O from the old reference exponent to the new one
-            if (hi > E_run + E_UP || (one ? lo_all : lo) < E_run - E_DOWN) {
-              if (E_run) unit = pow2i(E_run - hi);   // O is zero before the first tile
-              E_run = hi;
+          // lane = key: its factor, its value's exponent and the inverse of that one's power
+          const float fk = kv8_pow2(s_ke[lane]), ev = kv8_exponent(s_ve[lane]), iv = kv8_inverse(s_ve[lane]);
+          float s[2][NT][4];
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+            for (int x = 0; x < NT; ++x) s[mt][x][0] = s[mt][x][1] = s[mt][x][2] = s[mt][x][3] = 0.f;
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) {
+            uint32_t r[4], a0[4], a1[4];
+            ldsm4(kb + (k_at ^ (c * 16)), r);
+            e4m3x4_f16(r[0], a0[0], a0[2]);
+            e4m3x4_f16(r[1], a0[1], a0[3]);
+            e4m3x4_f16(r[2], a1[0], a1[2]);
+            e4m3x4_f16(r[3], a1[1], a1[3]);
+#pragma unroll
+            for (int x = 0; x < NT; ++x) {
+              const uint2 b = *reinterpret_cast<const uint2*>(s_q + ((nw * NT + x) * 8 + g) * Sh::Q_LD + c * 32 + t4 * 8);
+              mma_f16(s[0][x], a0, b.x, b.y);
+              mma_f16(s[1][x], a1, b.x, b.y);
             }
-            float s[2][NT][4];
+          }
+          float mx[NT][2];
 #pragma unroll
-            for (int mt = 0; mt < 2; ++mt)
+          for (int x = 0; x < NT; ++x) mx[x][0] = mx[x][1] = -INFINITY;
 #pragma unroll
-              for (int x = 0; x < NT; ++x) s[mt][x][0] = s[mt][x][1] = s[mt][x][2] = s[mt][x][3] = 0.f;
+          for (int mt = 0; mt < 2; ++mt) {
+            const float f0 = __shfl_sync(0xffffffffu, fk, mt * 16 + g), f1 = __shfl_sync(0xffffffffu, fk, mt * 16 + 8 + g);
+            const float e0 = __shfl_sync(0xffffffffu, ev, mt * 16 + g), e1 = __shfl_sync(0xffffffffu, ev, mt * 16 + 8 + g);
 #pragma unroll
-            for (int c = 0; c < D / 16; ++c) {
-              uint32_t r[4], a0[4], a1[4];
-              ldsm4(kb + (k_at ^ (c * 16)), r);
-              e4m3x4_f16(r[0], a0[0], a0[2]);
-              e4m3x4_f16(r[1], a0[1], a0[3]);
-              e4m3x4_f16(r[2], a1[0], a1[2]);
-              e4m3x4_f16(r[3], a1[1], a1[3]);
+            for (int x = 0; x < NT; ++x) {
+              // a rounded sum here, and the reference taken off it below: that difference is exact near the reference,
+              // where a fused one would leave the rounding of a huge score over, and a weight of 2^(that)
+              s[mt][x][0] = s[mt][x][0] * f0 * qf[x][0] + e0; s[mt][x][1] = s[mt][x][1] * f0 * qf[x][1] + e0;
+              s[mt][x][2] = s[mt][x][2] * f1 * qf[x][0] + e1; s[mt][x][3] = s[mt][x][3] * f1 * qf[x][1] + e1;
+              if (masked)
 #pragma unroll
-              for (int x = 0; x < NT; ++x) {
-                const uint2 b = *reinterpret_cast<const uint2*>(s_q + ((nw * NT + x) * 8 + g) * Sh::Q_LD + c * 32 + t4 * 8);
-                mma_f16(s[0][x], a0, b.x, b.y);
-                mma_f16(s[1][x], a1, b.x, b.y);
-              }
+                for (int e = 0; e < 4; ++e)
+                  if (!((vis[x][e & 1] >> (mt * 16 + (e >> 1) * 8)) & 1u)) s[mt][x][e] = -INFINITY;
+              mx[x][0] = fmaxf(mx[x][0], fmaxf(s[mt][x][0], s[mt][x][2]));
+              mx[x][1] = fmaxf(mx[x][1], fmaxf(s[mt][x][1], s[mt][x][3]));
             }
-            float mx[NT][2];
+          }
+          bool raise = false;
 #pragma unroll
-            for (int x = 0; x < NT; ++x) mx[x][0] = mx[x][1] = -INFINITY;
+          for (int x = 0; x < NT; ++x)
 #pragma unroll
-            for (int mt = 0; mt < 2; ++mt) {
-              const float f0 = __shfl_sync(0xffffffffu, fk, mt * 16 + g), f1 = __shfl_sync(0xffffffffu, fk, mt * 16 + 8 + g);
-#pragma unroll
-              for (int x = 0; x < NT; ++x) {
-                // to log2 units here, not inside the subtraction below: a fused x - m would leave the rounding of a
-                // huge m over, and a weight of 2^(that)
-                s[mt][x][0] = s[mt][x][0] * f0 * qf[x][0]; s[mt][x][1] = s[mt][x][1] * f0 * qf[x][1];
-                s[mt][x][2] = s[mt][x][2] * f1 * qf[x][0]; s[mt][x][3] = s[mt][x][3] * f1 * qf[x][1];
-                if (masked)
-#pragma unroll
-                  for (int e = 0; e < 4; ++e)
-                    if (!((vis[x][e & 1] >> (mt * 16 + (e >> 1) * 8)) & 1u)) s[mt][x][e] = -INFINITY;
-                mx[x][0] = fmaxf(mx[x][0], fmaxf(s[mt][x][0], s[mt][x][2]));
-                mx[x][1] = fmaxf(mx[x][1], fmaxf(s[mt][x][1], s[mt][x][3]));
-              }
-            }
-            bool raise = false;
+            for (int e = 0; e < 2; ++e) raise = raise || mx[x][e] - ref[x][e] > KV8_TOP;
+          if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
             for (int x = 0; x < NT; ++x)
 #pragma unroll
-              for (int e = 0; e < 2; ++e) raise = raise || mx[x][e] > m[x][e] + LAZY;
-            if (__any_sync(0xffffffffu, raise || unit != 1.f)) {
+              for (int e = 0; e < 2; ++e) {
+                float v = mx[x][e];
+                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+                if (!(v - ref[x][e] > KV8_TOP)) continue;
+                const float corr = ex2(ref[x][e] - (v - KV8_HEAD));
+                ref[x][e] = v - KV8_HEAD;
+                l[x][e] *= corr;
 #pragma unroll
-              for (int x = 0; x < NT; ++x)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  float v = mx[x][e];
-                  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
-                  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
-                  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-                  float corr = 1.f;
-                  if (v > m[x][e] + LAZY) {
-                    corr = ex2(m[x][e] - v);
-                    m[x][e] = v;
-                    l[x][e] *= corr;
-                  }
-                  corr *= unit;
-#pragma unroll
-                  for (int c = 0; c < D / 16; ++c) {
-                    O[c][x][e] *= corr;
-                    O[c][x][2 + e] *= corr;
-                  }
+                for (int c = 0; c < D / 16; ++c) {
+                  O[c][x][e] *= corr;
+                  O[c][x][2 + e] *= corr;
                 }
-            }
-            // weights, then weights times 2^(exponent - E_run) as the B operand of the value product
-            uint32_t pb[2][NT][2];
-            // not finite: NaN where seen; outside this pass's exponents, or seen by nobody: 0
-            const float fv = vbyte == KV8_BAD ? kv8_pow2(vbyte) : vbyte >= lo && vbyte <= hi ? pow2i(vbyte - E_run) : 0.f;
+              }
+          }
+          // weights, as the B operand of the value product
+          uint32_t pb[2][NT][2];
 #pragma unroll
-            for (int mt = 0; mt < 2; ++mt) {
-              const float v0 = __shfl_sync(0xffffffffu, fv, mt * 16 + g), v1 = __shfl_sync(0xffffffffu, fv, mt * 16 + 8 + g);
+          for (int mt = 0; mt < 2; ++mt) {
+            const float i0 = __shfl_sync(0xffffffffu, iv, mt * 16 + g), i1 = __shfl_sync(0xffffffffu, iv, mt * 16 + 8 + g);
+#pragma unroll
+            for (int x = 0; x < NT; ++x) {
+              float w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float base = ref[x][e & 1] == -INFINITY ? 0.f : ref[x][e & 1];
+                w[e] = ex2(s[mt][x][e] - base);
+                l[x][e & 1] = fmaf(w[e], e < 2 ? i0 : i1, l[x][e & 1]);
+              }
+              pb[mt][x][0] = transpose8(half2_of(w[0], w[1]));
+              pb[mt][x][1] = transpose8(half2_of(w[2], w[3]));
+            }
+          }
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt) {
+            // a pair's bytes (k0 d0, k0 d1, k1 d0, k1 d1) to (k0 d0, k1 d0, k0 d1, k1 d1); zeros for keys that nobody sees
+            uint32_t sel0 = 0x3120, sel1 = 0x3120;
+            if (masked) {
+              const uint32_t k = seen >> (mt * 16 + 2 * t4);
+              sel0 = ((k & 1u) ? 0x0100u : 0x0404u) | ((k & 2u) ? 0x3020u : 0x4040u);
+              sel1 = ((k & 256u) ? 0x0100u : 0x0404u) | ((k & 512u) ? 0x3020u : 0x4040u);
+            }
+#pragma unroll
+            for (int c = 0; c < D / 16; c += 2) {
+              uint32_t r[4], va[4], vc[4];
+              ldsm4_t(vb + mt * 16 * D + (v_at ^ (c * 16)), r);
+              e4m3x4_f16(__byte_perm(r[0], 0, sel0), va[0], va[1]);
+              e4m3x4_f16(__byte_perm(r[1], 0, sel1), va[2], va[3]);
+              e4m3x4_f16(__byte_perm(r[2], 0, sel0), vc[0], vc[1]);
+              e4m3x4_f16(__byte_perm(r[3], 0, sel1), vc[2], vc[3]);
 #pragma unroll
               for (int x = 0; x < NT; ++x) {
-                float w[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const float base = m[x][e & 1] == -INFINITY ? 0.f : m[x][e & 1];
-                  const float pr = ex2(s[mt][x][e] - base);
-                  if (first) l[x][e & 1] += pr;
-                  w[e] = pr * (e < 2 ? v0 : v1);
-                  if (masked && !((vis[x][e & 1] >> (mt * 16 + (e >> 1) * 8)) & 1u)) w[e] = 0.f;
-                }
-                pb[mt][x][0] = transpose8(half2_of(w[0], w[1]));
-                pb[mt][x][1] = transpose8(half2_of(w[2], w[3]));
+                mma_f16(O[c][x], va, pb[mt][x][0], pb[mt][x][1]);
+                mma_f16(O[c + 1][x], vc, pb[mt][x][0], pb[mt][x][1]);
               }
             }
-#pragma unroll
-            for (int mt = 0; mt < 2; ++mt) {
-              // a pair's bytes (k0 d0, k0 d1, k1 d0, k1 d1) to (k0 d0, k1 d0, k0 d1, k1 d1); zeros for keys that nobody sees
-              uint32_t sel0 = 0x3120, sel1 = 0x3120;
-              if (masked) {
-                const uint32_t k = seen >> (mt * 16 + 2 * t4);
-                sel0 = ((k & 1u) ? 0x0100u : 0x0404u) | ((k & 2u) ? 0x3020u : 0x4040u);
-                sel1 = ((k & 256u) ? 0x0100u : 0x0404u) | ((k & 512u) ? 0x3020u : 0x4040u);
-              }
-#pragma unroll
-              for (int c = 0; c < D / 16; c += 2) {
-                uint32_t r[4], va[4], vc[4];
-                ldsm4_t(vb + mt * 16 * D + (v_at ^ (c * 16)), r);
-                e4m3x4_f16(__byte_perm(r[0], 0, sel0), va[0], va[1]);
-                e4m3x4_f16(__byte_perm(r[1], 0, sel1), va[2], va[3]);
-                e4m3x4_f16(__byte_perm(r[2], 0, sel0), vc[0], vc[1]);
-                e4m3x4_f16(__byte_perm(r[3], 0, sel1), vc[2], vc[3]);
-#pragma unroll
-                for (int x = 0; x < NT; ++x) {
-                  mma_f16(O[c][x], va, pb[mt][x][0], pb[mt][x][1]);
-                  mma_f16(O[c + 1][x], vc, pb[mt][x][0], pb[mt][x][1]);
-                }
-              }
-            }
-            if (one) break;
-            hi = (int)__reduce_max_sync(0xffffffffu, counts && vbyte < lo ? (uint32_t)vbyte : 0u);
-            if (hi == 0) break;
-            first = false;
           }
         }
         warp_arrive(smem_u32(empty + st));
@@ -535,12 +506,11 @@ __global__ void __launch_bounds__(Shape<D, NT, WN, WK, NS, CTAS>::THREADS, CTAS)
           v += __shfl_xor_sync(0xffffffffu, v, 16);
           if (g == 0) {
             const int at = kw * Sh::QV + (nw * NT + x) * 8 + 2 * t4 + e;
-            s_m[at] = m[x][e];
+            s_m[at] = ref[x][e];
             s_l[at] = v;
           }
         }
       named_bar_sync(1, NC);   // (and the item before has been read from s_o)
-      const float unit = E_run ? pow2i(E_run - KV8_BIAS) : 1.f;
 #pragma unroll 1
       for (int r = 0; r < WK; r += Sh::NR) {
         if (r == kw / Sh::NR * Sh::NR) {
@@ -553,7 +523,7 @@ __global__ void __launch_bounds__(Shape<D, NT, WN, WK, NS, CTAS>::THREADS, CTAS)
               float top = s_m[col];
 #pragma unroll
               for (int k = 1; k < WK; ++k) top = fmaxf(top, s_m[k * Sh::QV + col]);
-              const float f = ex2(m[x][e] - (top == -INFINITY ? 0.f : top)) * unit;
+              const float f = ex2(ref[x][e] - (top == -INFINITY ? 0.f : top));
               float* o = s_o + (kw % Sh::NR * Sh::QV + col) * Sh::O_LD + 2 * g;
 #pragma unroll
               for (int c = 0; c < D / 16; ++c) {

@@ -8,15 +8,13 @@
 //                           widened to fp16 (exact) in shared memory by the softmax threads while they wait for S. (Weights
 //                           in 8-bit parts, e5m2 for their range, need three products of the codes as they lie, but cutting
 //                           them took twice the arithmetic of the whole softmax: 5000 clocks a tile against HBM's 1500.)
-// A key's exponent multiplies its scores; a value's is added to its weights' logarithms, against a running reference E, and
-// taken out again of their sum; a tile whose values' exponents span more than fp16 bears goes through the value product
-// in several passes.
+// A key's factor multiplies its scores; a value's exponent is added to them and taken out again of the weights' sum.
 //
 // One CTA an SM, 20 warps, two workers with a range of items each, so that one's softmax and epilogue run under the other's
 // products (one worker: 151 us instead of 118 at the time). A worker has eight softmax warps (two threads a query vector,
 // 64 keys of a tile each: four warps a scheduler hide each other's latencies, and prepare the next item's query vectors; S is
-// read twice from TMEM, for the maximum and for the weights, which keeps a thread below 96 registers, and each 32 columns of
-// S are overwritten by the weights of their keys), an MMA warp and a producer warp (TMA: the next tile's keys under this one's
+// read twice from TMEM, for the maximum, which leaves scores plus exponents there, and for the weights, which keeps a thread
+// below 96 registers, and each 32 columns of S are overwritten by the weights of their keys), an MMA warp and a producer warp (TMA: the next tile's keys under this one's
 // softmax, its values as soon as these are widened). TMEM: S and O, 128 columns each, of either worker.
 // 64 ragged sequences of up to 2048 slots, 17 tree rows of 32 heads over 8 KV heads: 91 us (24 us of bytes at the copy rate),
 // 180 us on mma.sync. Bound by the softmax warps: of a tile's some 7000 clocks the weights take 2400 to 3400, the maximum
@@ -36,16 +34,13 @@ constexpr int OPB = TT * TT;            // bytes of an 8-bit operand tile
 constexpr int SOFT = 256;               // softmax threads of a worker
 constexpr int SOFT_W = SOFT / 32;
 constexpr int T_THREADS = 2 * SOFT + 128;
-constexpr float T_LAZY = 8.f;           // how far (log2) a score may pass the reference maximum
-constexpr int T_SHIFT = 3;              // weights are held times 2^3: at most 2^(3 + 8 + 4), inside fp16
-constexpr int TE_UP = 4, TE_DOWN = 12, TE_SPAN = 14;   // exponents around the reference; within one pass
 
 // a worker's shared memory, [2]
 constexpr int TO_K = 0, TO_V8 = TO_K + 2 * OPB, TO_V = TO_V8 + 2 * OPB, TO_Q = TO_V + 4 * OPB;   // keys; values: codes, fp16
                                                           // [half of the dims]; query vectors [part]
 constexpr int TO_EXP = TO_Q + 4 * OPB;                    // [worker][tile parity][K, V][128] exponent bytes
 constexpr int TO_KF = TO_EXP + 2 * 2 * 256;               // [worker][tile parity][128] key factors
-constexpr int TO_VF = TO_KF + 2 * 2 * 512;                // [worker][tile parity][2][128] value exponents, inverse factors
+constexpr int TO_VF = TO_KF + 2 * 2 * 512;                // [worker][tile parity][2][128] value exponents, inverses of their powers
 constexpr int TO_COL = TO_VF + 2 * 2 * 1024;              // [worker][item parity][128] (score factor, slot limit)
 constexpr int TO_MASK = TO_COL + 4 * TT * 8;              // [worker][128 rows][4] tree masks: the last tile's barrier on its
                                                           // exponents comes after their last use in an item
@@ -118,12 +113,8 @@ __global__ void __launch_bounds__(T_THREADS, 1)
   uint64_t *k_full = bars, *k_empty = bars + 1, *v_full = bars + 2, *v_empty = bars + 3, *q_full = bars + 4, *s_full = bars + 5,
            *p_full = bars + 6, *o_done = bars + 7, *o_free = bars + 8, *drain = bars + 9;
   int* red = reinterpret_cast<int*>(sm + TO_RED + wk * 512);
-  int* r_hi = red;                                            // [tile parity][4 warps] largest exponent
-  int* r_lo = red + 8;                                        // smallest
-  uint32_t* r_seen = reinterpret_cast<uint32_t*>(red + 16);   // [8 warps][2] keys seen
-  int* r_next = red + 32;                                     // [4 warps] largest exponent of the next pass
-  volatile int* s_more = red + 40;                            // another pass of the same tile follows
-  int* s_fullvis = red + 48;                                  // [item parity][16 warps]
+  uint32_t* r_seen = reinterpret_cast<uint32_t*>(red);        // [8 warps][2] keys seen
+  int* s_fullvis = red + 16;                                  // [item parity][16 warps]
   int* s_pref = reinterpret_cast<int*>(sm + TO_GROUP);
   int* s_lim = s_pref + p.groups + 1;
   int* s_seq = s_lim + p.groups;
@@ -259,7 +250,7 @@ __global__ void __launch_bounds__(T_THREADS, 1)
     const int hf = (warp >> 2) & 1, r = threadIdx.x & 127, c0 = hf * 64;   // half of a tile's keys and of O's columns; row
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tS0 + lane_off + c0, tO = tO0 + lane_off + c0;
-    int i = 0, passes = 0;       // tiles of the range; value passes
+    int i = 0;                   // tiles of the range
     for (int item = 0; more; ++item) {
       const int gi = k.gi, h = k.h, buf = item & 1;
       const int seq = s_seq[gi], limit = s_lim[gi];
@@ -277,8 +268,7 @@ __global__ void __launch_bounds__(T_THREADS, 1)
       const int klim = __float_as_int(col.y);
       const uint32_t* my_mask =
           reinterpret_cast<const uint32_t*>(sm + TO_MASK) + (wk * TT + (r < nqv ? (r * p.G_inv >> 16) : 0)) * 8;
-      float m = -INFINITY, l = 0.f;
-      int E = 0;                 // reference exponent byte
+      float ref = -INFINITY, l = 0.f;
       for (int t = k.t0; t < k.t1; ++t, ++i) {
         const int key0 = t * TT, tp = i & 1;
         kv8_wait(smem_u32(k_full), (uint32_t)(i & 1), abort_flag, a.err);
@@ -307,34 +297,22 @@ __global__ void __launch_bounds__(T_THREADS, 1)
           const uint32_t* any = r_seen + (r >> 6) * 8 + ((r >> 5) & 1);
           seen = ((any[0] | any[2] | any[4] | any[6]) >> (r & 31)) & 1u;
         }
-        // exponents of the tile's keys: the first half's threads take the keys', the second's the values'
+        // the tile's keys: the first half's threads take their factors, the second's their values'
         float* s_kf = reinterpret_cast<float*>(sm + TO_KF) + (wk * 2 + tp) * TT;
-        float* s_va = reinterpret_cast<float*>(sm + TO_VF) + (wk * 2 + tp) * 2 * TT;   // log2 of a weight's factor
-        float* s_vi = s_va + TT;                                                      // the factor's inverse
-        const int vbyte = max((int)s_exp[TT + r], KV8_LOWEST);
-        const bool counts = seen && vbyte != KV8_BAD;
+        float* s_va = reinterpret_cast<float*>(sm + TO_VF) + (wk * 2 + tp) * 2 * TT;   // exponents
+        float* s_vi = s_va + TT;                                                      // the inverses of their powers
         if (!hf) {
           s_kf[r] = kv8_pow2(s_exp[r]);
         } else {
-          const uint32_t whi = __reduce_max_sync(0xffffffffu, counts ? (uint32_t)vbyte : 0u);
-          const uint32_t wlo = __reduce_min_sync(0xffffffffu, counts ? (uint32_t)vbyte : 255u);
-          if (lane == 0) {
-            r_hi[tp * 4 + (warp & 3)] = (int)whi;
-            r_lo[tp * 4 + (warp & 3)] = (int)wlo;
-          }
+          s_va[r] = kv8_exponent(s_exp[TT + r]);
+          s_vi[r] = kv8_inverse(s_exp[TT + r]);
         }
         // (without this arrival the next tile's keys could be there before a warp still at the item's end has seen this
         // phase of k_full end, and it would wait for the phase after)
         warp_arrive(smem_u32(k_empty));
         named_bar_sync(1 + wk, SOFT);
-        const int4 rh = *reinterpret_cast<const int4*>(r_hi + tp * 4), rl = *reinterpret_cast<const int4*>(r_lo + tp * 4);
-        int hi = max(max(rh.x, rh.y), max(rh.z, rh.w));
-        const int lo_all = min(min(rl.x, rl.y), min(rl.z, rl.w));
-        const bool narrow = hi - lo_all <= TE_SPAN;   // one pass does
-        float keep[64];                               // the scores, for further passes (local memory, rarely)
-
         // value r's codes to fp16, this thread's half of the dims, under S: the product of the tile before must be done
-        if (i) kv8_wait(smem_u32(o_done), (uint32_t)((passes - 1) & 1), abort_flag, a.err);
+        if (i) kv8_wait(smem_u32(o_done), (uint32_t)((i - 1) & 1), abort_flag, a.err);
         kv8_wait(smem_u32(v_full), (uint32_t)(i & 1), abort_flag, a.err);
         {
           const uint8_t* from = sm + TO_V8 + wk * OPB + r * TT;
@@ -363,122 +341,74 @@ __global__ void __launch_bounds__(T_THREADS, 1)
         for (int c = 0; c < 64; c += 32) {
           float s[32];
           tmem_ld32(tS + c, s);
-          if (!narrow)   // as they come
-            for (int j = 0; j < 32; ++j) keep[c + j] = s[j];
 #pragma unroll
-          for (int j = 0; j < 32; j += 4) {
+          for (int j = 0; j < 32; j += 4) {   // (a key's factor is a power of two: that product is exact)
             const float4 f = *reinterpret_cast<const float4*>(s_kf + c0 + c + j);
-            s[j] *= f.x; s[j + 1] *= f.y; s[j + 2] *= f.z; s[j + 3] *= f.w;
+            const float4 v = *reinterpret_cast<const float4*>(s_va + c0 + c + j);
+            s[j] = fmaf(s[j] * f.x, qf, v.x);
+            s[j + 1] = fmaf(s[j + 1] * f.y, qf, v.y);
+            s[j + 2] = fmaf(s[j + 2] * f.z, qf, v.z);
+            s[j + 3] = fmaf(s[j + 3] * f.w, qf, v.w);
           }
           if (masked)
 #pragma unroll
-            for (int j = 0; j < 32; ++j) s[j] = (vis[c >> 5] >> j) & 1u ? s[j] : -INFINITY;
+            for (int j = 0; j < 32; ++j) s[j] = (vis[c >> 5] >> j) & 1u ? s[j] : -INFINITY;   // last: a hidden key may hold NaN
 #pragma unroll
           for (int j = 0; j < 32; j += 8)
             mx = max3(mx, max3(s[j], s[j + 1], s[j + 2]), max3(max3(s[j + 3], s[j + 4], s[j + 5]), s[j + 6], s[j + 7]));
+          tmem_st16(tS + c, s);
+          tmem_st16(tS + c + 16, s + 16);
         }
+        tmem_wait_st();
         float* x_max = reinterpret_cast<float*>(sm + TO_X) + (wk * 2 + tp) * 2 * TT;
         x_max[hf * TT + r] = mx;
-        bool first = true;
+        named_bar_sync(1 + wk, SOFT);
+        mx = fmaxf(x_max[r], x_max[TT + r]);
         float corr = 1.f;
-        while (true) {
-          const bool one = hi - lo_all <= TE_SPAN;
-          const int lo = one ? 0 : hi - TE_SPAN;
-          float unit = 1.f;    // O from the old reference exponent to the new one
-          if (hi > E + TE_UP || (one ? lo_all : lo) < E - TE_DOWN) {
-            if (E) unit = pow2i(E - hi);
-            E = hi;
-          }
-          // not finite: NaN where seen; outside this pass's exponents, or seen by nobody: no weight
-          if (hf) {
-            const bool in = seen && vbyte != KV8_BAD && vbyte >= lo && vbyte <= hi;
-            s_va[r] = in ? (float)(vbyte - E + T_SHIFT) : seen && vbyte == KV8_BAD && first ? kv8_pow2(vbyte) : -INFINITY;
-            s_vi[r] = in ? pow2i(E - vbyte - T_SHIFT) : 0.f;
-          }
-          named_bar_sync(1 + wk, SOFT);
-          if (first) {
-            mx = fmaxf(x_max[r], x_max[TT + r]);
-            if ((mx - m) * qf > T_LAZY) {
-              corr = ex2((m - mx) * qf);
-              m = mx;
-              l *= corr;
-            }
-          }
-          const float scale_o = first ? corr * unit : unit;
-          const bool begun = t > k.t0 || !first;      // O holds something
-          // a pass before this one must be out of P, and O complete before it is rescaled
-          if (begun && (!first || __any_sync(0xffffffffu, scale_o != 1.f))) {
-            kv8_wait(smem_u32(o_done), (uint32_t)((passes - 1) & 1), abort_flag, a.err);
-            tc_fence_after();
-            if (__any_sync(0xffffffffu, scale_o != 1.f)) {
-#pragma unroll 1
-              for (int c = 0; c < 64; c += 16) {
-                float o[16];
-                tmem_ld16(tO + c, o);
-#pragma unroll
-                for (int j = 0; j < 16; ++j) o[j] *= scale_o;
-                tmem_st16(tO + c, o);
-              }
-            }
-          }
-          // weights; the difference comes first: it is exact where it matters, whatever the size of the scores
-          const float base = m == -INFINITY ? 0.f : -m;
-          // (scalar arithmetic: pairs of fp32 cost as many moves into aligned registers as they save)
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        if (r < nqv && mx - ref > KV8_TOP) {
+          corr = ex2(ref - (mx - KV8_HEAD));
+          ref = mx - KV8_HEAD;
+          l *= corr;
+        }
+        if (t > k.t0 && __any_sync(0xffffffffu, corr != 1.f)) {   // (the product of the tile before is done)
 #pragma unroll 1
           for (int c = 0; c < 64; c += 16) {
-            float s[16];
-            if (first) {
-              tmem_ld16(tS + c, s);
-            } else {
-              for (int j = 0; j < 16; ++j) s[j] = keep[c + j];
-            }
+            float o[16];
+            tmem_ld16(tO + c, o);
 #pragma unroll
-            for (int j = 0; j < 16; j += 4) {
-              const float4 f = *reinterpret_cast<const float4*>(s_kf + c0 + c + j);
-              const float4 v = *reinterpret_cast<const float4*>(s_va + c0 + c + j);
-              // (a key's factor is a power of two: the product is exact)
-              s[j] = ex2(fmaf(fmaf(s[j], f.x, base), qf, v.x));
-              s[j + 1] = ex2(fmaf(fmaf(s[j + 1], f.y, base), qf, v.y));
-              s[j + 2] = ex2(fmaf(fmaf(s[j + 2], f.z, base), qf, v.z));
-              s[j + 3] = ex2(fmaf(fmaf(s[j + 3], f.w, base), qf, v.w));
-            }
-            if (masked) {   // last: what a hidden key holds may be NaN
-              const uint32_t see = vis[c >> 5] >> (c & 16);
-#pragma unroll
-              for (int j = 0; j < 16; ++j) s[j] = (see >> j) & 1u ? s[j] : 0.f;
-            }
-            uint32_t w[8];
-#pragma unroll
-            for (int j = 0; j < 16; j += 4) {
-              const float4 u = *reinterpret_cast<const float4*>(s_vi + c0 + c + j);
-              sum[0] = fmaf(s[j], u.x, sum[0]);
-              sum[1] = fmaf(s[j + 1], u.y, sum[1]);
-              sum[2] = fmaf(s[j + 2], u.z, sum[2]);
-              sum[3] = fmaf(s[j + 3], u.w, sum[3]);
-              w[j / 2] = half2_of(s[j], s[j + 1]);
-              w[j / 2 + 1] = half2_of(s[j + 2], s[j + 3]);
-            }
-            st8(tS + (c & 32) + (c & 16) / 2, w);   // the weights of 32 keys over the first 16 of their 32 score columns
+            for (int j = 0; j < 16; ++j) o[j] *= corr;
+            tmem_st16(tO + c, o);
           }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-          tmem_wait_st();
-          if (threadIdx.x % SOFT == 0) *s_more = !one;
-          int next_hi = 0;
-          if (!one) {   // the next pass's exponents
-            const uint32_t below = __reduce_max_sync(0xffffffffu, counts && vbyte < lo ? (uint32_t)vbyte : 0u);
-            if (lane == 0) r_next[warp & 3] = (int)below;      // (both halves hold the same)
-            named_bar_sync(1 + wk, SOFT);
-            next_hi = max(max(r_next[0], r_next[1]), max(r_next[2], r_next[3]));
-            named_bar_sync(1 + wk, SOFT);
-          }
-          tc_fence_before();
-          warp_arrive(smem_u32(p_full));
-          ++passes;
-          if (one) break;
-          hi = next_hi;      // > 0: lo_all itself is still to come
-          first = false;
         }
+        // weights: a difference of two rounded numbers, exact near the reference, whatever the size of the scores
+        const float base = ref == -INFINITY ? 0.f : ref;
+        // (scalar arithmetic: pairs of fp32 cost as many moves into aligned registers as they save)
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+        for (int c = 0; c < 64; c += 16) {
+          float s[16];
+          tmem_ld16(tS + c, s);
+          uint32_t w[8];
+#pragma unroll
+          for (int j = 0; j < 16; j += 4) {
+            const float4 u = *reinterpret_cast<const float4*>(s_vi + c0 + c + j);
+            s[j] = ex2(s[j] - base);
+            s[j + 1] = ex2(s[j + 1] - base);
+            s[j + 2] = ex2(s[j + 2] - base);
+            s[j + 3] = ex2(s[j + 3] - base);
+            sum[0] = fmaf(s[j], u.x, sum[0]);
+            sum[1] = fmaf(s[j + 1], u.y, sum[1]);
+            sum[2] = fmaf(s[j + 2], u.z, sum[2]);
+            sum[3] = fmaf(s[j + 3], u.w, sum[3]);
+            w[j / 2] = half2_of(s[j], s[j + 1]);
+            w[j / 2 + 1] = half2_of(s[j + 2], s[j + 3]);
+          }
+          st8(tS + (c & 32) + (c & 16) / 2, w);   // the weights of 32 keys over the first 16 of their 32 score columns
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        tmem_wait_st();
+        tc_fence_before();
+        warp_arrive(smem_u32(p_full));
       }
 
       // the next item's query vectors, so that its first S runs under this item's end
@@ -488,10 +418,10 @@ __global__ void __launch_bounds__(T_THREADS, 1)
       // the item's sum: l of both halves; this thread's 64 dims of its query vector
       float* x_l = reinterpret_cast<float*>(sm + TO_X) + (wk * 2 + (i & 1)) * 2 * TT;   // the parity that the last tile did not use
       x_l[hf * TT + r] = l;
-      kv8_wait(smem_u32(o_done), (uint32_t)((passes - 1) & 1), abort_flag, a.err);
+      kv8_wait(smem_u32(o_done), (uint32_t)((i - 1) & 1), abort_flag, a.err);
       tc_fence_after();
       named_bar_sync(1 + wk, SOFT);
-      float L = x_l[r] + x_l[TT + r], top = m * qf;
+      float L = x_l[r] + x_l[TT + r], top = ref;
       const bool whole = done.t0 == 0 && done.t1 == done.nt;
       if (threadIdx.x % SOFT == 0 && done.t0 == 0) cut_begin(p, me, done, (int)share.cta_of(done.base + pad + done.nt - 1));
       const int in = r < nqv ? (int)(r * p.G_inv >> 16) : 0, row = r0 + in;
@@ -507,10 +437,8 @@ __global__ void __launch_bounds__(T_THREADS, 1)
         const float2 v = *reinterpret_cast<const float2*>(p.pp_ml + 2 * (s * stride + at));
         L = fmaf(v.y, ex2(v.x - tb), L);
       }
-      // (E = 0: no value counted, O is zero or NaN)
       const bool live = whole && r < nqv && seq >= 0 && __ldcg(a.row_seq + row) == seq;
       const float inv = whole ? (live && L != 0.f ? 1.f / L : 0.f) : 1.f;
-      const float unit = own * pow2i(E ? E - KV8_BIAS - T_SHIFT : 0);
 #pragma unroll 1
       for (int c = 0; c < 64; c += 16) {
         __syncwarp();
@@ -522,7 +450,7 @@ __global__ void __launch_bounds__(T_THREADS, 1)
         }
         if (r >= nqv) continue;
 #pragma unroll
-        for (int j = 0; j < 16; ++j) o[j] *= unit;
+        for (int j = 0; j < 16; ++j) o[j] *= own;
         for (int s = 0; s < n_prefix; ++s) {
           const float g = ex2(p.pp_ml[2 * (s * stride + at)] - tb);
           const float4* x = reinterpret_cast<const float4*>(p.pp_o + (s * stride + at) * TT + c0 + c);
@@ -555,7 +483,7 @@ __global__ void __launch_bounds__(T_THREADS, 1)
     // ---- MMA: S of a tile, then its value product ----
     const uint64_t dq = sdesc_sw128(smem_u32(sm + TO_Q + wk * 2 * OPB)), dk = sdesc_sw128(smem_u32(sm + TO_K + wk * OPB)),
                    dv = desc_mn(smem_u32(sm + TO_V + wk * 2 * OPB));
-    int i = 0, passes = 0;
+    int i = 0;
     bool ok = true;
     for (int item = 0; more && ok; ++item, more = k.next(range)) {
       ok = kv8_wait_all(smem_u32(q_full), (uint32_t)(item & 1), abort_flag, a.err);
@@ -572,22 +500,17 @@ __global__ void __launch_bounds__(T_THREADS, 1)
         }
         __syncwarp();
         if (t == k.t0 && item) ok = kv8_wait_all(smem_u32(o_free), (uint32_t)((item - 1) & 1), abort_flag, a.err);
-        bool again = true;
-        for (int pass = 0; ok && again; ++pass) {
-          ok = kv8_wait_all(smem_u32(p_full), (uint32_t)(passes & 1), abort_flag, a.err);
-          if (!ok) break;
-          again = *s_more != 0;
-          tc_fence_after();
-          if (elect_one()) {
-            const uint32_t fresh = t == k.t0 && pass == 0 ? 0u : 1u;   // the first product of an item begins O
+        ok = ok && kv8_wait_all(smem_u32(p_full), (uint32_t)(i & 1), abort_flag, a.err);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t fresh = t == k.t0 ? 0u : 1u;   // the first product of an item begins O
 #pragma unroll
-            for (int x = 0; x < 8; ++x)
-              mma16_ts(tO0, tS0 + (x >> 1) * 32 + (x & 1) * 8, dv + ((x * 16 * TT) >> 4), O_IDESC, x ? 1u : fresh);
-            tc_commit(smem_u32(o_done));
-          }
-          __syncwarp();
-          ++passes;
+          for (int x = 0; x < 8; ++x)
+            mma16_ts(tO0, tS0 + (x >> 1) * 32 + (x & 1) * 8, dv + ((x * 16 * TT) >> 4), O_IDESC, x ? 1u : fresh);
+          tc_commit(smem_u32(o_done));
         }
+        __syncwarp();
       }
     }
     if (!ok) {   // products in flight end before the CTA frees its TMEM

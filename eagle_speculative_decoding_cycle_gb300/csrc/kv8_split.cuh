@@ -30,8 +30,21 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
 __device__ __forceinline__ void copies_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
+// Weights of own slots. With x a score (log2 units) and 2^e its value's factor, the B operand of the value product is
+// w = 2^(x + e - ref) of each query vector, fp16, and the sum takes w 2^-e in fp32. ref is set KV8_HEAD below the largest
+// x + e and moved once one passes it by more than KV8_TOP: w is at most 2^15, the largest at least 2^7 (fp16 holds 2^-24 to
+// 2^16), so that what a weight loses to fp16's smallest step, 2^-25, is 2^-32 of the largest product of a weight and its
+// value's size, whatever the sizes of values that the query vector gives no weight. (One reference exponent for all values of
+// a tile lost small weights beside them: 6000 keys, most of weight 2^-16 beside values 2^12 times theirs, 7% off.)
+constexpr float KV8_HEAD = 7.f, KV8_TOP = 15.f;
+
+// A value's e and 2^-e from its byte. A vector that held something not finite makes NaN of the weight.
+__device__ __forceinline__ float kv8_exponent(int byte) {
+  return byte == KV8_BAD ? __int_as_float(0x7fffffff) : (float)(max(byte, KV8_LOWEST) - KV8_BIAS);
+}
 // 2^n, 0 below the normal range.
 __device__ __forceinline__ float pow2i(int n) { return n < -126 ? 0.f : __int_as_float((min(n, 127) + 127) << 23); }
+__device__ __forceinline__ float kv8_inverse(int byte) { return pow2i(KV8_BIAS - max(byte, KV8_LOWEST)); }
 
 // How a call's rows are cut and its tiles shared out: the same numbers in both kernels and the scratch size.
 struct Plan {

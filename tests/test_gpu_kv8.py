@@ -681,3 +681,67 @@ def test_written_and_cleared_bands(T, d):
     k.K[:, off] = 0
     k.V[:, off] = 0
     k.check(rows=[0, T, 12 * T - 1])
+
+
+@pytest.mark.parametrize("T,d", [(1, 64), (12, 64), (1, 128), (12, 128)])
+@pytest.mark.parametrize("P", [0, 40])
+def test_many_small_weights_beside_large_values(T, d, P):
+    """Thousands of keys of weight 2^-16 next to one of weight 1, and in every tile a value 2^12 times the others' size
+    whose weight is nothing: the small ones' sum counts. Tolerance: as above, but a weight's absolute step is at most
+    2^-24 of a largest one of at least 2^7 (each product p |v| against the row's largest), so n * 2^-31 * max p |v| / sum p
+    in the place of n * 2^-25 * max|V|."""
+    k = Case(1, T, 16, 4, d, 6000, 1, 16, P, seed=43)
+    n, g = 6000 + T, k.g
+    x = np.full(n, -16.3)                                # scores in log2 units
+    x[::32] = -200.0
+    x[5] = 0.0
+    V = 1 + 0.1 * g.normal(size=(n, 4, d))
+    V[::32] = 6000.0
+    V[5] = g.normal(size=(4, d))
+    K = np.broadcast_to((x * d ** -0.5 * np.log(2))[:, None, None], (n, 4, d))
+    k.q.fill_(1.0)
+    if P:                                                # a prefix that weighs 2^-20 at most in all
+        k.pk.fill_(-4.0)
+    rows = lambda y: torch.from_numpy(np.ascontiguousarray(y)).float().to(DEV)
+    api.kv8_write(k.c, rows(K), rows(V), i32(np.zeros(n)), i32(np.arange(n)))
+    k.K, k.V = (O.dequantise(*O.quantise(y.astype(np.float32).astype(np.float64)))[None] for y in (K, V))
+    B = 40                                               # as many sequences over the same blocks: long ranges a CTA
+    c = api.KV8Cache(k.c.k, k.c.v, k.c.k_exp, k.c.v_exp, k.c.table.expand(B, -1).contiguous())
+    err = err_word()
+    got = api.attention_shared_kv8(k.q.repeat(B, 1, 1), k.pk, k.pv, c, i32(np.repeat(np.arange(B), T)), None, i32([6000] * B),
+                                   T, 1, T, bits_of(k.trees, T).repeat(B, 1), err=err).double().cpu().numpy()
+    assert int(err) == 0
+    got = got.reshape(B, T, 4, 4, d)
+    for r in range(T):
+        see = np.concatenate([np.ones(6000, bool), k.trees[r]])
+        for h in range(4):
+            Kh, Vh = k.K[0, see, h], k.V[0, see, h]
+            if P:
+                Kh = np.concatenate([k.pk[h].double().cpu().numpy(), Kh])
+                Vh = np.concatenate([k.pv[h].double().cpu().numpy(), Vh])
+            count = len(Kh)
+            s = Kh.sum(-1) * d ** -0.5
+            p = np.exp(s - s.max())
+            o, W = p @ Vh / p.sum(), p @ np.abs(Vh) / p.sum()
+            A = np.abs(s).max()
+            tol = 2.0 ** -8 * np.abs(o) + W * ((2.0 ** -8 if P else 2.0 ** -11) + 2 * (d + 8) * 2.0 ** -23 * A +
+                                               (count + 64) * 2.0 ** -23 + (d == 128) * 2 * 2.0 ** -17 * A) + \
+                count * 2.0 ** -31 * (p * np.abs(Vh).max(-1)).max() / p.sum()
+            off = np.abs(got[:, r, h] - o) / tol
+            assert off.max() <= 1, f"row {r} head {h}: {off.max()} times the tolerance"
+
+
+@pytest.mark.parametrize("T,d", [(2, 64), (12, 64), (2, 128), (12, 128)])
+def test_rows_do_not_depend_on_values_that_others_see(T, d):
+    """A value of 2^14 times the others' size in a tree slot: rows that do not see it keep their bits."""
+    k = Case(2, T, 16, 4, d, [500, 77], 1, 16, seed=44)
+    k.trees[:, T - 1] = False
+    k.trees[T - 1, T - 1] = k.trees[2 * T - 1, T - 1] = True
+    a = k.run()
+    x = k.g.normal(size=(2, 4, d))
+    api.kv8_write(k.c, torch.from_numpy(x).float().to(DEV), torch.from_numpy(2.0 ** 14 * x).float().to(DEV), i32([0, 1]),
+                  i32(k.ctx + T - 1))
+    b = k.run()
+    keep = [r for r in range(2 * T) if r % T != T - 1]
+    same = torch.equal(a[keep], b[keep])
+    assert same

@@ -595,7 +595,8 @@ __global__ void __launch_bounds__(256) kv8_join_k(const Kv8Attn a, const Plan p)
   const int col = blockIdx.y * p.join_cols + team % p.join_cols, c = threadIdx.x % GL * 8;
   const int col_in = min(col, nqv - 1), in = (int)(col_in * p.G_inv >> 16), row = r0 + in;
   const size_t at = (size_t)row * a.nq + h * p.G + col_in - in * p.G;
-  const int seq = first_seq(a, s0, s1), own = __ldcg(a.row_seq + row);
+  const int lead = __ldcg(a.row_seq + s0), own = __ldcg(a.row_seq + row);
+  const int seq = lead >= 0 ? lead : seq_behind_padding(a.row_seq, s0, s1, r0, s1, 32);
   // piece 0 in slot 2 c0 + 1 (it holds the item's start), the others in slot 2 c, then the prefix's
   const int pieces = c1 - c0 + 1, n = pieces + p.n_prefix;
   float top = -INFINITY, L = 0.f, o[8] = {};

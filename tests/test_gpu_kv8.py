@@ -745,3 +745,41 @@ def test_rows_do_not_depend_on_values_that_others_see(T, d):
     keep = [r for r in range(2 * T) if r % T != T - 1]
     same = torch.equal(a[keep], b[keep])
     assert same
+
+
+@pytest.mark.parametrize("T,d,P", [(300, 64, 0), (300, 128, 0), (70, 128, 40)])
+def test_padding_in_front_of_long_chunks(T, d, P):
+    """Chunks whose first rows are padding, up to all but the last and all, in several row blocks."""
+    k = Case(5, T, 8, 4, d, [40, 0, 9, 77, 130], 0, 16, P, seed=45)
+    rows = k.row_seq.reshape(5, T)
+    for b, n in enumerate((1, T - 1, T, 2 * T // 3, 0)):
+        rows[b, :n] = -1
+    rows[4, T // 2:] = -1                         # and behind
+    out = k.check(rows=[0, 1, T - 1, 2 * T - 2, 2 * T - 1, 2 * T, 3 * T - 1, 3 * T + 2 * T // 3 - 1, 3 * T + 2 * T // 3,
+                        4 * T - 1, 4 * T, 4 * T + T // 2 - 1, 4 * T + T // 2, 5 * T - 1])
+    assert not out[torch.from_numpy(k.row_seq < 0).to(DEV)].any()
+
+
+def test_padding_costs_no_more_than_rows():
+    """A chunk that is padding throughout, or nearly so, beside one that is not: no slower than two that are not."""
+    k = Case(2, 4096, 8, 4, 64, [10, 20], 0, seed=46)
+    full = i32(k.row_seq)
+    slot, ctx, out = i32(k.row_slot), i32(k.ctx), torch.empty_like(k.q)
+    scratch = api.attention_kv8_scratch(k.c, 8192, 8, 4096)
+
+    def best(row_seq):
+        times = []
+        for _ in range(8):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            for _ in range(4):
+                api.attention_kv8(k.q, k.c, row_seq, slot, ctx, 4096, 0, out=out, scratch=scratch)
+            b.record()
+            torch.cuda.synchronize()
+            times.append(a.elapsed_time(b))
+        return min(times)
+
+    for n in (4096, 4095):
+        padded = full.clone()
+        padded[:n] = -1
+        assert best(padded) < 1.3 * best(full), n

@@ -338,11 +338,11 @@ __global__ void __launch_bounds__(T_THREADS, 1)
         tc_fence_after();
         float mx = -INFINITY;
 #pragma unroll 1
-        for (int c = 0; c < 64; c += 32) {
-          float s[32];
-          tmem_ld32(tS + c, s);
+        for (int c = 0; c < 64; c += 16) {
+          float s[16];
+          tmem_ld16(tS + c, s);
 #pragma unroll
-          for (int j = 0; j < 32; j += 4) {   // (a key's factor is a power of two: that product is exact)
+          for (int j = 0; j < 16; j += 4) {   // (a key's factor is a power of two: that product is exact)
             const float4 f = *reinterpret_cast<const float4*>(s_kf + c0 + c + j);
             const float4 v = *reinterpret_cast<const float4*>(s_va + c0 + c + j);
             s[j] = fmaf(s[j] * f.x, qf, v.x);
@@ -352,12 +352,11 @@ __global__ void __launch_bounds__(T_THREADS, 1)
           }
           if (masked)
 #pragma unroll
-            for (int j = 0; j < 32; ++j) s[j] = (vis[c >> 5] >> j) & 1u ? s[j] : -INFINITY;   // last: a hidden key may hold NaN
+            for (int j = 0; j < 16; ++j) s[j] = (vis[c >> 5] >> ((c & 16) + j)) & 1u ? s[j] : -INFINITY;   // last: a hidden key may hold NaN
 #pragma unroll
-          for (int j = 0; j < 32; j += 8)
+          for (int j = 0; j < 16; j += 8)
             mx = max3(mx, max3(s[j], s[j + 1], s[j + 2]), max3(max3(s[j + 3], s[j + 4], s[j + 5]), s[j + 6], s[j + 7]));
           tmem_st16(tS + c, s);
-          tmem_st16(tS + c + 16, s + 16);
         }
         tmem_wait_st();
         float* x_max = reinterpret_cast<float*>(sm + TO_X) + (wk * 2 + tp) * 2 * TT;

@@ -12,7 +12,7 @@
 // right after ldmatrix (fp16 holds every code exactly; cvt runs at 128 codes a clock and SM against the 23 bytes a
 // clock that HBM delivers).
 //   - A key's factor multiplies its score, a value's exponent is added to it: the codes are never scaled.
-//   - q is scaled by a power of two into fp16's range (exact down to 2^-38 of its largest entry).
+//   - q is scaled by a power of two into fp16's range (entries down to 2^-30 of its largest exactly, others to 2^-38 of it).
 //   - Weights times their values' factors enter the value product as fp16 (2^-11), against a reference of each query
 //     vector that is raised only when a product passes it by 2^15: most tiles then need no reduction across lanes and no
 //     rescaling of O. Each column decides for itself.

@@ -159,8 +159,8 @@ int eagle_op_kv8_read(void* stream, const eagle_kv8* cache, int dtype, void* k, 
  * that no row sees may hold anything. Scale = 1/sqrt(head_dim) when scale <= 0.
  * out may be q itself; otherwise the two do not overlap (refused).
  * Sums, maxima and softmax weights' sums are fp32; the weights enter the value product as fp16
- * (2^-11). q is used exactly (fp16 times a power of two, entries down to 2^-38 of its largest), but
- * with head_dim 128 and more than 16 query vectors a block (rows x query heads of a KV head, up
+ * (2^-11). q is used as fp16 times a power of two (entries down to 2^-30 of its largest exactly, smaller
+ * ones to within 2^-38 of the largest), but with head_dim 128 and more than 16 query vectors a block (rows x query heads of a KV head, up
  * to 128 together) it is held in two e4m3 parts: each entry to 2^-17 of the vector's largest.
  * A row's result does not depend on the values of other rows or sequences; their lengths move
  * the points where its sum over slots is split, so it can change in the last bits of fp32.

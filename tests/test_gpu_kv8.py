@@ -783,3 +783,60 @@ def test_padding_costs_no_more_than_rows():
         padded = full.clone()
         padded[:n] = -1
         assert best(padded) < 1.3 * best(full), n
+
+
+@pytest.mark.parametrize("qscale", [1e6, 1e12, 1e25])
+@pytest.mark.parametrize("T,d,P", [(1, 64, 0), (12, 64, 0), (1, 128, 0), (12, 128, 0), (1, 128, 20), (12, 128, 20)])
+def test_scores_of_any_size(T, d, P, qscale):
+    """Scores so large that a row is its best key's value, far past where fp32 holds a score and an exponent apart. Rows
+    whose two best scores are closer than 2^-10 of the largest one's terms are left out: d + 8 fp32 roundings of 2^-24 and
+    q's 2^-17 (twice: both keys) are less."""
+    k = Case(3, T, 16, 4, d, [1, 40, 300], 1, 16, P, seed=47, qscale=qscale)
+    out = k.run().double().cpu().numpy()
+    assert int(k.err) == 0 and np.isfinite(out).all()
+    q, some = k.q.double().cpu().numpy(), 0
+    for r in range(3 * T):
+        b = r // T
+        see = np.concatenate([np.ones(k.ctx[b], bool), k.trees[r]])
+        at = np.nonzero(see)[0]
+        for h in range(16):
+            K, V = k.K[b, at, h // 4], k.V[b, at, h // 4]
+            if P:
+                K = np.concatenate([k.pk[h // 4].double().cpu().numpy(), K])
+                V = np.concatenate([k.pv[h // 4].double().cpu().numpy(), V])
+            s = K @ q[r, h]
+            order = np.argsort(s)
+            if len(s) > 1 and s[order[-1]] - s[order[-2]] < 2.0 ** -10 * np.max(np.abs(K) @ np.abs(q[r, h])):
+                continue
+            v = V[order[-1]]
+            some += 1
+            assert np.all(np.abs(out[r, h] - v) <= (2.0 ** -8 + 2.0 ** -8 * (P > 0) + 2.0 ** -11 + 2.0 ** -20) * np.abs(v))
+    assert some > 10 * T
+
+
+def test_small_entries_of_a_query():
+    """A query whose scores come from entries 2^-31 of its largest one (that one meets zeros in every key): each entry is
+    within 2^-38 of the largest, so a score within sum_i |k_i| * 2^-38 * max|q| * scale; entries of 2^-30 and more are exact."""
+    for low, exact in ((2.0 ** -30, True), (2.0 ** -33, False)):
+        k = Case(2, 1, 4, 1, 64, [50, 90], 0, seed=48, qscale=1.0)
+        q = low * (1 + k.g.integers(0, 128, size=(2, 4, 64)) / 128)
+        q[:, :, 0] = 1.0
+        k.q.copy_(torch.from_numpy(q).to(torch.bfloat16))
+        assert np.array_equal(k.q.double().cpu().numpy(), q)
+        n = k.K.shape[1]
+        K = k.g.normal(size=(2, n, 1, 64)) / low / 4
+        K[..., 0] = 0
+        for b in range(2):
+            m = k.ctx[b] + 1
+            x = torch.from_numpy(K[b, :m]).float().to(DEV)
+            v = torch.from_numpy(k.v[b, :m]).float().to(DEV)
+            api.kv8_write(k.c, x, v, i32([b] * m), i32(np.arange(m)))
+        k.K = O.dequantise(*O.quantise(K.astype(np.float32).astype(np.float64)))
+        out = k.run().double().cpu().numpy()
+        want, tol = k.want()
+        if not exact:
+            for r in range(2):
+                m = k.ctx[r] + 1
+                reach = np.abs(k.K[r, :m, 0]).sum(-1).max() * 2.0 ** -38 * 64 ** -0.5
+                tol[r] += 2 * reach * np.abs(k.V[r, :m]).max()
+        assert np.all(np.abs(out - want) <= tol)

@@ -32,8 +32,11 @@ namespace eagle {
 namespace {
 
 constexpr int TK = 32;            // keys a tile
-// head_dim 128 with more query vectors a block goes to tcgen05 (128-key tiles). 64 ragged sequences of up to 2048 slots, 8 KV
-// heads, T rows of 4 query heads a KV head (mma.sync, tcgen05): T = 1 45, 82 us; 2 45, 82; 4 58, 81; 6 94, 82; 8 96, 83.
+// head_dim 128 with more query vectors a block goes to tcgen05 (128-key tiles), on either side of which (mma.sync, tcgen05):
+// 64 ragged sequences of up to 2048 slots, 8 KV heads, T rows of 4 query heads each: T = 1 41, 70 us; 2 41, 70; 4 49, 71; 6 -,
+// 72; 8 -, 72 (when mma.sync still had forms for these it took 14% more than tcgen05 there). One sequence of 32768 slots:
+// T = 1 23, 36 us; 4 27, 36; 6 -, 37. 64 sequences of up to 1024, 32 KV heads of one query head: T = 1 81, 152 us; 8 85, 154;
+// 16 104, 158; 17 -, 159.
 constexpr int TC_ABOVE = 16;
 
 __device__ __forceinline__ void mma_f16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
@@ -75,8 +78,9 @@ template <int D, int NT, int WN, int WK, int NS, int CTAS>
 struct Shape {
   static_assert(NS < 32, "a producer lane has at most one tile in flight");
   static constexpr int QV = 8 * NT * WN, NW = WN * WK;
-  // Eight consumer warps that hold wide accumulators: the other warpgroup (one producer, three row warps) gives its
-  // registers to them (168 a thread at launch; 2 x 128 x 232 + 128 x 40 = 384 x 168).
+  // Eight consumer warps that hold wide accumulators: the other warpgroup (one producer, three row warps) gives
+  // registers to them (168 a thread at launch; 2 x 128 x 216 + 128 x 72 = 384 x 168; the row warps spill some 250 bytes a
+  // thread with 40, 10 with 72).
   static constexpr bool SPLIT_REGS = NW == 8;
   static constexpr int ROWS_W = SPLIT_REGS ? 3 : 1;       // warps that prepare the rows of the next item
   static constexpr int THREADS = (NW + 1 + ROWS_W) * 32;
@@ -224,7 +228,7 @@ __global__ void __launch_bounds__(Shape<D, NT, WN, WK, NS, CTAS>::THREADS, CTAS)
   constexpr int FIRST = (NW + Sh::ROWS_W) * 32;   // threads that prepare the first item
 
   if (warp >= NW) {
-    if constexpr (Sh::SPLIT_REGS) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    if constexpr (Sh::SPLIT_REGS) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp > NW) {
       // row warps: the first item together with the consumers, each later one in the buffer that the consumers are not at
       const int sw = warp - NW - 1;
@@ -301,7 +305,7 @@ __global__ void __launch_bounds__(Shape<D, NT, WN, WK, NS, CTAS>::THREADS, CTAS)
       for (int x = max(0, issued - NS); x < issued; ++x)
         kv8_wait(smem_u32(full + x % NS), (uint32_t)((x / NS) & 1), abort_flag, a.err, false);
   } else {
-    if constexpr (Sh::SPLIT_REGS) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+    if constexpr (Sh::SPLIT_REGS) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     const int kw = warp / WN, nw = warp % WN;
     const int g = lane >> 2, t4 = lane & 3;
     float* s_o = reinterpret_cast<float*>(sm + Sh::OFF_O);
@@ -718,11 +722,11 @@ cudaError_t launch_own(cudaStream_t st, const Kv8Attn& a, Plan& p, const CUtenso
   return e != cudaSuccess ? e : launch_join<D>(st, a, p);
 }
 
-// The narrowest configuration that holds a block's query vectors: small ones in two CTAs an SM (one's joins under the
-// other's loads), large ones in one CTA of eight warps. A second query tile goes to other warps, not to the same: they widen
-// the codes once more, but nothing spills (16 query vectors of 128: 58 us, 65 with both in a warp). 64 ragged sequences of up to 2048 slots, 8 KV heads of 64: 32 query
-// vectors a block 60 us (two query tiles a warp, two CTAs; 96 with four a warp in one CTA, whose registers spill), 48 86 us
-// (94 in two CTAs of 64), 64 96 us (104 and 116 in one CTA), 96 126 us, 128 162 us.
+// A configuration that holds a block's query vectors: up to 64 in two CTAs an SM (one's joins under the other's loads), more
+// in one CTA of eight warps. A second query tile goes to other warps, not to the same: they widen
+// the codes once more, but nothing spills (16 query vectors of 128: 58 us at the time, 65 with both in a warp). 64 ragged
+// sequences of up to 2048 slots, 8 KV heads of 64: 16 query vectors a block 43 us, 32 48 us, 48 76 us (82 in one CTA of three
+// query tiles a warp), 64 77 us, 96 102 us (123 in the form for 128), 128 128 us. (The last two spill 8 and 12 bytes a thread.)
 template <int D>
 cudaError_t launch_mma(cudaStream_t st, const Kv8Attn& a, Plan& p, const CUtensorMap& mk, const CUtensorMap& mv) {
   const int t = p.qv_pad / 8;
@@ -730,7 +734,6 @@ cudaError_t launch_mma(cudaStream_t st, const Kv8Attn& a, Plan& p, const CUtenso
   if (t <= 2) return launch_own<D, 1, 2, 2, 10, 2>(st, a, p, mk, mv);
   if constexpr (D == 64) {
     if (t <= 4) return launch_own<D, 2, 2, 2, 9, 2>(st, a, p, mk, mv);
-    if (t <= 6) return launch_own<D, 3, 2, 4, 18, 1>(st, a, p, mk, mv);
     if (t <= 8) return launch_own<D, 2, 4, 1, 7, 2>(st, a, p, mk, mv);
     if (t <= 12) return launch_own<D, 3, 4, 2, 11, 1>(st, a, p, mk, mv);
     return launch_own<D, 4, 4, 2, 7, 1>(st, a, p, mk, mv);

@@ -16,9 +16,9 @@
 // read twice from TMEM, for the maximum, which leaves scores plus exponents there, and for the weights, which keeps a thread
 // below 96 registers, and each 32 columns of S are overwritten by the weights of their keys), an MMA warp and a producer warp (TMA: the next tile's keys under this one's
 // softmax, its values as soon as these are widened). TMEM: S and O, 128 columns each, of either worker.
-// 64 ragged sequences of up to 2048 slots, 17 tree rows of 32 heads over 8 KV heads: 91 us (24 us of bytes at the copy rate),
-// 180 us on mma.sync. Bound by the softmax warps: of a tile's some 7000 clocks the weights take 2400 to 3400, the maximum
-// 1500, widening the values 1300, the two products and their hand-overs the rest.
+// 64 ragged sequences of up to 2048 slots, 17 tree rows of 32 heads over 8 KV heads: 83 us (24 us of bytes at the copy rate),
+// 180 us on mma.sync at the time. Bound by the softmax warps: of a tile's some 5700 clocks the weights take 1400, the maximum
+// 1400, widening the values 1000, the two products, the barriers and their hand-overs the rest.
 #include "kv8_split.cuh"
 #include "kernels.h"
 #include "tc_common.cuh"

@@ -12,7 +12,7 @@
 //   warps 9, 10     tcgen05.mma of tile 0 / 1: S = Q K^T (operands in shared memory), O += P V (P in TMEM, V read MN-major).
 // S comes in halves of 64 keys, each with its own barriers: while one half is in its softmax warps the tensor cores run the
 // other half's value product and next S, and the other tile's. (S of 128 keys at once leaves a chain of product, softmax,
-// product: 121 us in all for 4096 shared tokens under 64 x 17 rows of 32 heads, against 106; with two threads a query vector
+// product: 121 us in all for 4096 shared tokens under 64 x 17 rows of 32 heads, against 106 (103 since); with two threads a query vector
 // 118; halves with one issuing warp for both tiles 135, each of its waits taking some 250 clocks.)
 // TMEM: S0 S1 (128 columns each, P over the first half of each 64), O0 O1 (d each). That prefix alone: 62 us, of them 38 us
 // of products at the rate of a large GEMM; tensor pipe 46% active. 128 keys of a pair of tiles take some 3300 clocks where
@@ -35,7 +35,9 @@ constexpr int PT = 128;            // keys a tile, query vectors a tile
 constexpr int PH = PT / 2;         // keys of one S: half a tile
 constexpr int PF_THREADS = 384;
 constexpr float PF_LAZY = 8.f;
-constexpr int PF_SMS = 152;        // CTAs that run at once (one an SM)
+// CTAs that run at once, one an SM. A number, not the current device's count: the scratch size is asked for without a
+// device in hand, and both must cut alike. With another count the results are the same, the cut is only a worse guess.
+constexpr int PF_SMS = 152;
 
 template <int D>
 struct PfShape {
@@ -182,7 +184,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
   PDL_ENTRY();
 
   if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
     const int mt = warp >> 2, qv = threadIdx.x & 127;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + mt * PT + lane_off, tO = tmem + 2 * PT + mt * D + lane_off;
@@ -278,7 +280,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
       }
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == 8) {
       // ---- TMA ----
       const int qbytes = a.RB * a.G * 128;

@@ -4,8 +4,9 @@
 // read on the device. Laid end to end the tiles are shared out over the CTAs in equal contiguous ranges, so that
 // ragged batches and one long sequence balance alike. An item inside one CTA's range is finished there; the pieces of
 // an item cut by range ends (at most two a CTA) go to scratch as (o, m, l) and a second launch joins them in order.
-// An item also costs its start and its end, counted as `pad` tiles (64 ragged sequences, one row each: 52 us with none,
-// 48 with 2, 44 with 3 to 6, 46 with 8).
+// An item also costs its start and its end, counted as `pad` tiles (with 0, 2, 4, 6, 8 of them: 64 ragged sequences, one row
+// each, 44.8, 39.9, 40.2, 40.9, 41.4 us; one of 32768 slots 23.8, 23.0, 22.2, 22.3, 22.3; 64 behind 8192 shared slots 43.9,
+// 43.3, 43.2, 42.9, 43.7).
 #pragma once
 
 #include "kv8.cuh"

@@ -18,7 +18,7 @@
 //     rescaling of O. Each column decides for itself.
 // A producer warp streams the tiles (TMA, 128- or 64-byte swizzle) through a ring that runs on across items, row warps
 // prepare the next item's query vectors, and the key groups' sums meet in shared memory, side by side where it lasts.
-// Bound by HBM once a range is long: one sequence of 32768 slots (8 KV heads of 128, 4 query heads each) 23 us, of them
+// Bound by HBM once a range is long: one sequence of 32768 slots (8 KV heads of 128, 4 query heads each) 22 us, of them
 // some 12 us of loads at 5.6 TB/s, 4 us until the first tile is there and 5 us for the join's launch; 64 ragged sequences
 // of up to 2048 slots 41 us (21 us of bytes at the copy rate).
 #include "kv8_split.cuh"
@@ -689,7 +689,7 @@ size_t own_scratch(const Kv8& c, const Plan& p) {
 
 // A join CTA holds up to 256 / (D / 8) teams: as many on one query vector as leave each about four partials, if the
 // grid's ranges are spread evenly over the items, the others on further query vectors; fewer where items that are all cut
-// would make more than two CTAs an SM (61 rows of one sequence: 25.4 us with 992 CTAs, 19.5 with 248).
+// would make more than two CTAs an SM (61 rows of one sequence: 25.4 us with 992 CTAs, 19.5 with 248 at the time).
 template <int D>
 cudaError_t launch_join(cudaStream_t st, const Kv8Attn& a, Plan& p) {
   constexpr int TEAMS = 256 / (D / 8);

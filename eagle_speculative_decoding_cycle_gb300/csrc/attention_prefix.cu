@@ -19,7 +19,9 @@
 // their products take 2048: bound by the way of a half through its warps and back (softmax 900 clocks, hand-overs and issue
 // some 1500, two halves under way a tile; with an eighth of the products 8 us less, without the ex2 2 us less).
 // Weights are rounded to bf16 (2^-8 relative at most, as the bf16 V that they meet; their sum is kept in fp32 of the
-// unrounded weights). Results leave as fp32 partials (o, m, l) of each key range, which the attention over the rows' own
+// unrounded weights). A second part, as the attention over the bf16 cache has it, takes half of the products again: 120 us
+// instead of 103 for that case and 46 instead of 42 for 8192 shared tokens under 64 rows, for 0.0016 relative off the 64-bit
+// results instead of 0.0021 (0.0015 of it the weights', 0.0016 the rounding of the results to bf16). Results leave as fp32 partials (o, m, l) of each key range, which the attention over the rows' own
 // slots joins in its epilogue.
 #include "kv8.cuh"
 #include "kernels.h"

@@ -158,12 +158,16 @@ int eagle_op_kv8_read(void* stream, const eagle_kv8* cache, int dtype, void* k, 
  * a sequence's rows see is looked up, those of slots in between that no row sees too). Slots
  * that no row sees may hold anything. Scale = 1/sqrt(head_dim) when scale <= 0.
  * out may be q itself; otherwise the two do not overlap (refused).
- * Sums, maxima and softmax weights' sums are fp32; the weights enter the value product as fp16
- * (2^-11). q is used as fp16 times a power of two (entries down to 2^-30 of its largest exactly, smaller
- * ones to within 2^-38 of the largest), but with head_dim 128 and more than 16 query vectors a block (rows x query heads of a KV head, up
- * to 128 together) it is held in two e4m3 parts: each entry to 2^-17 of the vector's largest.
+ * Sums, maxima and softmax weights' sums are fp32. A weight times its value's power of two enters
+ * the value product as fp16: to 2^-11 of itself, and to 2^-32 of the query vector's largest such
+ * product at least. q is used as fp16 times a power of two (entries down to 2^-30 of its largest
+ * exactly, smaller ones to within 2^-38 of the largest), but with head_dim 128 and more than 16 query
+ * vectors a block (rows x query heads of a KV head, up to 128 together) it is held in two e4m3 parts:
+ * entries down to 2^-9 of the vector's largest exactly, others to within 2^-17 of it.
  * A row's result does not depend on the values of other rows or sequences; their lengths move
- * the points where its sum over slots is split, so it can change in the last bits of fp32.
+ * the points where its sum over slots is split, so it can change in the last bits of fp32. Nor do
+ * a decoding step's rows and a verify pass's agree bit for bit, as eagle_op_attention's do: the
+ * number of rows chooses the kernel.
  * scratch: eagle_op_attention_kv8_scratch_bytes of the same sizes, no initial value needed; two
  * calls that may overlap on the GPU (graph replays included) need their own. */
 size_t eagle_op_attention_kv8_scratch_bytes(const eagle_kv8* cache, int R, int nq, int rows_per_seq, int prefix_len);
@@ -177,7 +181,7 @@ int eagle_op_attention_kv8(void* stream, const eagle_kv8* cache, const void* q, 
  * precision, being stored once for the whole batch) and then its own slots as above, in one
  * softmax. The prefix is one matrix product over all rows of a head, read once per 256 query
  * vectors rather than once per sequence; its weights enter the value product as bf16 (2^-8), the
- * type of the values that they meet. Padding rows get zeros. prefix_len = 0 is
+ * type of the values that they meet, in one part (eagle_op_attention takes two). Padding rows get zeros. prefix_len = 0 is
  * eagle_op_attention_kv8. */
 int eagle_op_attention_shared_kv8(void* stream, const eagle_kv8* cache, const void* prefix_k, const void* prefix_v,
                                   int prefix_len, const void* q, void* out, int R, int nq, int rows_per_seq,

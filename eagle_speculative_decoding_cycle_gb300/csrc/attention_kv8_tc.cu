@@ -11,11 +11,12 @@
 // A key's factor multiplies its scores; a value's exponent is added to them and taken out again of the weights' sum.
 //
 // One CTA an SM, 20 warps, two workers with a range of items each, so that one's softmax and epilogue run under the other's
-// products (one worker: 151 us instead of 118 at the time). A worker has eight softmax warps (two threads a query vector,
-// 64 keys of a tile each: four warps a scheduler hide each other's latencies, and prepare the next item's query vectors; S is
+// products (one worker: 151 us instead of 118 at the time). A worker has eight softmax warps (two threads a query vector, 64
+// keys of a tile each: four warps a scheduler hide each other's latencies, and prepare the next item's query vectors; S is
 // read twice from TMEM, for the maximum, which leaves scores plus exponents there, and for the weights, which keeps a thread
-// below 96 registers, and each 32 columns of S are overwritten by the weights of their keys), an MMA warp and a producer warp (TMA: the next tile's keys under this one's
-// softmax, its values as soon as these are widened). TMEM: S and O, 128 columns each, of either worker.
+// below 96 registers, and each 32 columns of S are overwritten by the weights of their keys), an MMA warp and a producer
+// warp (TMA: the next tile's keys under this one's softmax, its values as soon as these are widened). TMEM: S and O, 128
+// columns each, of either worker.
 // 64 ragged sequences of up to 2048 slots, 17 tree rows of 32 heads over 8 KV heads: 83 us (24 us of bytes at the copy rate),
 // 180 us on mma.sync at the time. Bound by the softmax warps: of a tile's some 5700 clocks the weights take 1400, the maximum
 // 1400, widening the values 1000, the two products, the barriers and their hand-overs the rest.
@@ -352,7 +353,8 @@ __global__ void __launch_bounds__(T_THREADS, 1)
           }
           if (masked)
 #pragma unroll
-            for (int j = 0; j < 16; ++j) s[j] = (vis[c >> 5] >> ((c & 16) + j)) & 1u ? s[j] : -INFINITY;   // last: a hidden key may hold NaN
+            for (int j = 0; j < 16; ++j)   // last: a hidden key may hold NaN
+              s[j] = (vis[c >> 5] >> ((c & 16) + j)) & 1u ? s[j] : -INFINITY;
 #pragma unroll
           for (int j = 0; j < 16; j += 8)
             mx = max3(mx, max3(s[j], s[j + 1], s[j + 2]), max3(max3(s[j + 3], s[j + 4], s[j + 5]), s[j + 6], s[j + 7]));

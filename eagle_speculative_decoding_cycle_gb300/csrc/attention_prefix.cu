@@ -12,8 +12,8 @@
 //   warps 9, 10     tcgen05.mma of tile 0 / 1: S = Q K^T (operands in shared memory), O += P V (P in TMEM, V read MN-major).
 // S comes in halves of 64 keys, each with its own barriers: while one half is in its softmax warps the tensor cores run the
 // other half's value product and next S, and the other tile's. (S of 128 keys at once leaves a chain of product, softmax,
-// product: 121 us in all for 4096 shared tokens under 64 x 17 rows of 32 heads, against 106 (103 since); with two threads a query vector
-// 118; halves with one issuing warp for both tiles 135, each of its waits taking some 250 clocks.)
+// product: 121 us in all for 4096 shared tokens under 64 x 17 rows of 32 heads, against 106 (103 since); with two threads a
+// query vector 118; halves with one issuing warp for both tiles 135, each of its waits taking some 250 clocks.)
 // TMEM: S0 S1 (128 columns each, P over the first half of each 64), O0 O1 (d each). That prefix alone: 62 us, of them 38 us
 // of products at the rate of a large GEMM; tensor pipe 46% active. 128 keys of a pair of tiles take some 3300 clocks where
 // their products take 2048: bound by the way of a half through its warps and back (softmax 900 clocks, hand-overs and issue
@@ -21,8 +21,8 @@
 // Weights are rounded to bf16 (2^-8 relative at most, as the bf16 V that they meet; their sum is kept in fp32 of the
 // unrounded weights). A second part, as the attention over the bf16 cache has it, takes half of the products again: 120 us
 // instead of 103 for that case and 46 instead of 42 for 8192 shared tokens under 64 rows, for 0.0016 relative off the 64-bit
-// results instead of 0.0021 (0.0015 of it the weights', 0.0016 the rounding of the results to bf16). Results leave as fp32 partials (o, m, l) of each key range, which the attention over the rows' own
-// slots joins in its epilogue.
+// results instead of 0.0021 (0.0015 of it the weights', 0.0016 the rounding of the results to bf16). Results leave as fp32
+// partials (o, m, l) of each key range, which the attention over the rows' own slots joins in its epilogue.
 #include "kv8.cuh"
 #include "kernels.h"
 #include "tc_common.cuh"

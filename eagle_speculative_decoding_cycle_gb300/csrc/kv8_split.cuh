@@ -109,8 +109,8 @@ struct Group {
 };
 // For a sequence whose first row is padding: that of its first row in [s0, s1) that is not, -1 if [r0, r1) is all padding. By
 // `width` neighbouring lanes (a power of two), eight rows a lane in flight (one after another they cost a load's latency a row:
-// two chunks of 4096 rows, one of them all padding, 1912 us; now 346, and 560 with none padding). Not inline: its rare call then costs the others
-// nothing.
+// two chunks of 4096 rows, one of them all padding, 1912 us; now 346, and 560 with none padding). Not inline: its rare call
+// then costs the others nothing.
 static __device__ __noinline__ int seq_behind_padding(const int* row_seq, int s0, int s1, int r0, int r1, int width) {
   const int lane = threadIdx.x & 31, sub = lane & (width - 1);
   const unsigned group = (width == 32 ? 0xffffffffu : (1u << width) - 1u) << (lane - sub);

@@ -37,6 +37,8 @@ EXPORTED = [
     "eagle_op_wait_probe",
     "eagle_op_kv8_write", "eagle_op_kv8_read", "eagle_op_attention_kv8_scratch_bytes", "eagle_op_attention_kv8",
     "eagle_op_attention_shared_kv8",
+    "eagle_op_kv8_compact", "eagle_op_kv8_resize_scratch_bytes", "eagle_op_kv8_resize",
+    "eagle_rope_frequencies", "eagle_rope_turns", "eagle_op_rope", "eagle_op_attention_prompt",
 ]
 
 
@@ -74,6 +76,15 @@ class KV8(C.Structure):
     _fields_ = [("k_code", C.c_void_p), ("v_code", C.c_void_p), ("k_exp", C.c_void_p), ("v_exp", C.c_void_p),
                 ("table", C.c_void_p), ("n_kv_heads", C.c_int), ("head_dim", C.c_int), ("max_batch", C.c_int),
                 ("cap", C.c_int), ("block", C.c_int), ("n_blocks", C.c_int)]
+
+
+class RopeScaling(C.Structure):
+    """eagle_rope_scaling: a rule for rotary frequencies beyond the trained context."""
+    _fields_ = [("kind", C.c_int), ("factor", C.c_double), ("original", C.c_double), ("low", C.c_double),
+                ("high", C.c_double), ("attention", C.c_double)]
+
+
+ROPE_KINDS = {"linear": 1, "ntk": 2, "llama3": 3, "yarn": 4}
 
 
 _lib: Optional[C.CDLL] = None
@@ -131,6 +142,15 @@ def _declare(lib: C.CDLL) -> None:
                                          sz, vp]),
         "eagle_op_attention_shared_kv8": (i32, [vp, P(KV8), vp, vp, i32, vp, vp, i32, i32, i32, vp, vp, vp, i32, i32,
                                                 vp, i32, f32, vp, sz, vp]),
+        "eagle_op_kv8_compact": (i32, [vp, P(KV8), i32, i32, vp, vp, vp, i32, vp]),
+        "eagle_op_kv8_resize_scratch_bytes": (sz, [P(KV8)]),
+        "eagle_op_kv8_resize": (i32, [vp, P(KV8), i32, i32, vp, vp, vp, vp, sz, vp]),
+        "eagle_rope_frequencies": (i32, [i32, C.c_double, P(RopeScaling), P(C.c_double), P(f32)]),
+        "eagle_rope_turns": (i32, [i32, P(C.c_double), P(u64)]),
+        "eagle_op_rope": (i32, [vp, i32, i32, vp, i64, vp, i64, i32, vp, i64, vp, i64, i32, i32, i32, i32, i32, vp, vp, f32,
+                                i32]),
+        "eagle_op_attention_prompt": (i32, [vp, vp, i64, vp, i64, vp, i64, vp, i64, vp, i32, i32, i32, i32, i32, i32, vp, vp,
+                                            f32, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)

@@ -601,3 +601,219 @@ def attention_kv8(q: torch.Tensor, cache: KV8Cache, row_seq: torch.Tensor, row_s
     attention(), padding rows (row_seq < 0) and rows that see nothing give zeros."""
     return attention_shared_kv8(q, None, None, cache, row_seq, row_slot, ctx_len, rows_per_seq, mode, tree_T, mask,
                                 scale, out, scratch, err, stream)
+
+
+# ---- layers of an 8-bit cache: blocks and accepted paths -----------------------------------------------
+class KV8Layers:
+    """The 8-bit caches of a model's layers (KV8Cache, one shape), contiguous or over one block table. Paged: refs int32
+    [n_blocks] counts the table entries that hold each block (None: counted from the table here)."""
+
+    def __init__(self, caches: Sequence[KV8Cache], refs: Optional[torch.Tensor] = None):
+        _need(len(caches) > 0, "at least one layer")
+        c = caches[0]
+        for x in caches:
+            _need(x.index == c.index and x.k.shape == c.k.shape and _ptr(x.table) == _ptr(c.table) and
+                  x.max_batch == c.max_batch, "the layers must have one shape, device and block table")
+        self.caches, self.n = list(caches), len(caches)
+        self.device, self.index, self.max_batch, self.table, self.n_blocks = c.device, c.index, c.max_batch, c.table, c.n_blocks
+        self.c = (L.KV8 * self.n)(*[x.c for x in caches])
+        self.refs = self.scratch = None
+        if c.table is None:
+            _need(refs is None, "a contiguous cache has no blocks")
+            return
+        if refs is None:
+            held = c.table[c.table >= 0].long()
+            refs = torch.bincount(held, minlength=c.n_blocks)[:c.n_blocks].to(torch.int32)
+        _need(refs.dtype is torch.int32 and refs.numel() == c.n_blocks and refs.is_contiguous() and
+              refs.get_device() == c.index, "refs must be a contiguous int32 [n_blocks] tensor on the caches' device")
+        self.refs = refs
+        nb = L.lib().eagle_op_kv8_resize_scratch_bytes(c.ref)
+        _need(nb > 0, "a cache that the library does not take")
+        self.scratch = torch.empty(nb, dtype=torch.uint8, device=c.device)
+
+
+def _seq_list(layers: KV8Layers, t: torch.Tensor, n: Optional[int], name: str) -> int:
+    """Entries of a per-sequence list: as many as `n` where that is given, and at most max_batch."""
+    if t.dtype is not torch.int32 or t.dim() != 1 or not t.is_contiguous() or t.get_device() != layers.index or \
+            t.numel() > layers.max_batch or (n is not None and t.numel() != n):
+        raise ValueError(f"{name} must be a contiguous int32 list, one entry a sequence, on the caches' device")
+    return t.numel()
+
+
+def kv8_compact(layers: KV8Layers, n_old: torch.Tensor, acc_len: torch.Tensor, acc_path: torch.Tensor,
+                err: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Accepted paths to their committed slots in all layers: slot n_old[b] + j takes what slot n_old[b] +
+    acc_path[b][j - 1] held, j = 1 .. acc_len[b] (int32 [B], [B], [B][Dmax <= 16]; B sequences from 0 on)."""
+    B = _seq_list(layers, n_old, None, "n_old")
+    _seq_list(layers, acc_len, B, "acc_len")
+    _need(acc_path.dtype is torch.int32 and acc_path.dim() == 2 and acc_path.shape[0] == B and acc_path.is_contiguous() and
+          acc_path.get_device() == layers.index, "acc_path must be a contiguous int32 [B][Dmax] tensor on the caches' device")
+    e = _err_word(layers, err)
+    if _elsewhere(layers.index):
+        with torch.cuda.device(layers.index):
+            return kv8_compact(layers, n_old, acc_len, acc_path, err, stream)
+    rc = L.lib().eagle_op_kv8_compact(_stream_of(layers.index, stream), layers.c, layers.n, B, n_old.data_ptr(),
+                                      acc_len.data_ptr(), acc_path.data_ptr(), acc_path.shape[1], e)
+    L.check(rc, "eagle_op_kv8_compact")
+
+
+def kv8_fork(layers: KV8Layers, parent: Optional[torch.Tensor], length: torch.Tensor, err: Optional[torch.Tensor] = None,
+             stream: Optional[torch.cuda.Stream] = None) -> None:
+    """kv8_resize in which sequences with parent[b] >= 0 first give up their blocks and share those of their parent's first
+    length[b] slots; a partly filled last one is copied, so that both may go on writing. Parents have length -1."""
+    _need(layers.refs is not None, "a contiguous cache has no blocks")
+    B = _seq_list(layers, length, None, "length")
+    if parent is not None:
+        _seq_list(layers, parent, B, "parent")
+    e = _err_word(layers, err)
+    if _elsewhere(layers.index):
+        with torch.cuda.device(layers.index):
+            return kv8_fork(layers, parent, length, err, stream)
+    rc = L.lib().eagle_op_kv8_resize(_stream_of(layers.index, stream), layers.c, layers.n, B, layers.refs.data_ptr(),
+                                     _ptr(parent), length.data_ptr(), layers.scratch.data_ptr(), layers.scratch.numel(), e)
+    L.check(rc, "eagle_op_kv8_resize")
+
+
+def kv8_resize(layers: KV8Layers, length: torch.Tensor, err: Optional[torch.Tensor] = None,
+               stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Give each sequence b the blocks of its slots [0, length[b]) and no others (int32 [B]; negative: left as it is, 0: all
+    its blocks released). New blocks are the lowest-numbered free ones. Calls on one table are ordered by the caller."""
+    kv8_fork(layers, None, length, err, stream)
+
+
+# ---- rotary positions ---------------------------------------------------------------------------------
+class Rope:
+    """Rotary positions of heads of head_dim: the first `rot` entries (default: all) turned, pairs (x[i], x[i + rot/2]) or,
+    interleaved, (x[2i], x[2i + 1]). scaling: None, or a rule for long contexts, dict(kind="linear" | "ntk", factor),
+    dict(kind="llama3", factor, low_freq_factor, high_freq_factor, original), dict(kind="yarn", factor, original,
+    beta_fast, beta_slow, attention); freq: angles per position of the pairs (radians) instead of a rule."""
+
+    def __init__(self, head_dim: int, theta: float = 1e4, rot: Optional[int] = None, interleaved: bool = False,
+                 scaling: Optional[dict] = None, freq: Optional[Sequence[float]] = None, factor: Optional[float] = None,
+                 device="cuda"):
+        lib = L.lib()
+        self.head_dim, self.rot, self.interleaved = head_dim, head_dim if rot is None else rot, bool(interleaved)
+        _need(self.rot >= 2 and self.rot % 2 == 0, "rot must be a positive even number")
+        n = self.rot // 2
+        f, m = (C.c_double * n)(), C.c_float(1.0)
+        if freq is None:
+            s = None
+            if scaling is not None:
+                x = dict(scaling)
+                kind = x.pop("kind", None)
+                _need(kind in L.ROPE_KINDS, "scaling must name a rule: " + ", ".join(L.ROPE_KINDS))
+                names = {"linear": (), "ntk": (), "llama3": ("original", "low_freq_factor", "high_freq_factor"),
+                         "yarn": ("original",)}[kind]
+                _need(all(k in x for k in ("factor",) + names), f"scaling {kind} needs factor " + " ".join(names))
+                if kind == "yarn":
+                    lo, hi = x.pop("beta_slow", 1.0), x.pop("beta_fast", 32.0)
+                else:
+                    lo, hi = x.pop("low_freq_factor", 0.0), x.pop("high_freq_factor", 0.0)
+                s = L.RopeScaling(L.ROPE_KINDS[kind], x.pop("factor"), x.pop("original", 0.0), lo, hi, x.pop("attention", 0.0))
+                _need(not x, "scaling has entries that the rule does not: " + ", ".join(map(str, x)))
+            L.check(lib.eagle_rope_frequencies(self.rot, theta, None if s is None else C.byref(s), f, C.byref(m)),
+                    "eagle_rope_frequencies")
+        else:
+            _need(scaling is None and len(freq) == n, "freq must have rot / 2 angles, and stands in place of a rule")
+            f[:] = [float(x) for x in freq]
+        t = (C.c_uint64 * n)()
+        L.check(lib.eagle_rope_turns(n, f, t), "eagle_rope_turns")
+        self.freq = list(f)
+        self.factor = m.value if factor is None else float(factor)
+        self.turns = torch.tensor([x - (1 << 64) if x >> 63 else x for x in t], dtype=torch.int64).to(device)
+        self.device, self.index = self.turns.device, self.turns.get_device()
+
+
+def _head_rows(t: torch.Tensor, index: int, d: int, name: str) -> int:
+    """Row stride of [R][heads][d] rows, each row in one piece; a single row's is of no account."""
+    if t.dim() != 3 or t.shape[2] != d or t.get_device() != index:
+        raise ValueError(f"{name} must be [R][heads][{d}] on the same device")
+    s0, s1, s2 = t.stride()
+    R, h, _ = t.shape
+    if R and h and (s2 != 1 or (s1 != d and h != 1)):
+        raise ValueError(f"{name}'s rows must be contiguous (the row stride is free)")
+    return s0 if R > 1 else h * d
+
+
+def rope(plan: Rope, q: torch.Tensor, k: Optional[torch.Tensor], pos: torch.Tensor, dtype: Optional[torch.dtype] = None,
+         out: Optional[Sequence[Optional[torch.Tensor]]] = None, inverse: bool = False,
+         stream: Optional[torch.cuda.Stream] = None):
+    """Rows q [R][nq][d] and k [R][nkv][d] (or None; fp32 or bf16, any row stride of whole 16 bytes) turned to positions
+    pos [R] (int32); inverse: turned back. Returns (q, k) of `dtype` (default: q's), contiguous, or written to `out`,
+    which may be (q, k) themselves."""
+    d, index = plan.head_dim, plan.index
+    src = _KV_TYPES.get(q.dtype)
+    _need(src is not None and (k is None or (k.dtype is q.dtype and k.dim() == 3 and k.shape[0] == q.shape[0])),
+          "q and k must be float32 or bfloat16 rows of one type and number")
+    _need(index >= 0, "the plan and its call's tensors must be on a GPU")
+    ldq = _head_rows(q, index, d, "q")
+    ldk = 0 if k is None else _head_rows(k, index, d, "k")
+    R, nq, _ = q.shape
+    nkv = 0 if k is None else k.shape[1]
+    if pos.dtype is not torch.int32 or pos.numel() != R or not pos.is_contiguous() or pos.get_device() != index:
+        raise ValueError("pos must be a contiguous int32 tensor of an entry a row")
+    if out is None:
+        dtype = q.dtype if dtype is None else dtype
+        _need(dtype in _KV_TYPES, "rows are written as float32 or bfloat16")
+        with _owned_by(stream):
+            qo = torch.empty((R, nq, d), dtype=dtype, device=q.device)
+            ko = None if k is None else torch.empty((R, nkv, d), dtype=dtype, device=q.device)
+    else:
+        qo, ko = out
+        _need(qo.shape == q.shape and (ko is None) == (k is None) and (k is None or ko.shape == k.shape) and
+              qo.dtype in _KV_TYPES and (ko is None or ko.dtype is qo.dtype) and (dtype is None or dtype is qo.dtype),
+              "out must be rows like q and k, float32 or bfloat16")
+    ldqo = _head_rows(qo, index, d, "out")
+    ldko = 0 if k is None else _head_rows(ko, index, d, "out")
+    if _elsewhere(index):
+        with torch.cuda.device(index):
+            return rope(plan, q, k, pos, None, (qo, ko), inverse, stream)
+    rc = L.lib().eagle_op_rope(_stream_of(index, stream), src, _KV_TYPES[qo.dtype], q.data_ptr(), ldq, qo.data_ptr(), ldqo, nq,
+                               _ptr(k), ldk, _ptr(ko), ldko, nkv, d, plan.rot, int(plan.interleaved), R, pos.data_ptr(),
+                               plan.turns.data_ptr(), plan.factor, int(inverse))
+    L.check(rc, "eagle_op_rope")
+    return qo, ko
+
+
+# ---- attention over whole prompts -----------------------------------------------------------------------
+def attention_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_start: torch.Tensor,
+                     k_start: Optional[torch.Tensor] = None, scale: float = 0.0, out: Optional[torch.Tensor] = None,
+                     lse: Optional[torch.Tensor] = None, err: Optional[torch.Tensor] = None,
+                     stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Causal attention of packed sequences: rows q[q_start[b]:q_start[b + 1]] ([R][nq][d] bf16) over keys and values
+    k, v[k_start[b]:k_start[b + 1]] ([Rk][nkv][d]; default: the rows' starts), the last row seeing all of them. Row strides
+    are free. q_start, k_start: int32 [B + 1] on the device. lse: float32 [R][nq] to fill with the rows' log-sum-exps. Rows
+    of no sequence are not written."""
+    index = q.get_device()
+    _need(index >= 0, "q, k and v must be on a GPU")
+    d = q.shape[-1]
+    for t in (q, k, v):
+        _need(t.dtype is torch.bfloat16, "q, k and v must be bfloat16")
+    ldq, ldk, ldv = _head_rows(q, index, d, "q"), _head_rows(k, index, d, "k"), _head_rows(v, index, d, "v")
+    _need(k.shape == v.shape, "k and v must have one shape")
+    R, nq, _ = q.shape
+    k_start = q_start if k_start is None else k_start
+    for t in (q_start, k_start):
+        if t.dtype is not torch.int32 or t.dim() != 1 or t.numel() < 1 or not t.is_contiguous() or t.get_device() != index or \
+                t.numel() != q_start.numel():
+            raise ValueError("q_start and k_start must be contiguous int32 lists of one more entry than sequences")
+    if out is None:
+        with _owned_by(stream):
+            out = torch.empty((R, nq, d), dtype=torch.bfloat16, device=q.device)
+    else:
+        _need(out.shape == q.shape and out.dtype is torch.bfloat16, "out must be bfloat16 rows like q")
+    ldo = _head_rows(out, index, d, "out")
+    if lse is not None:
+        _need(lse.dtype is torch.float32 and lse.shape == (R, nq) and lse.is_contiguous() and lse.get_device() == index,
+              "lse must be a contiguous float32 [R][nq] tensor on q's device")
+    if err is not None:
+        _need(err.dtype is torch.int32 and err.numel() >= 1 and err.get_device() == index,
+              "err must be an int32 tensor on q's device")
+    if _elsewhere(index):
+        with torch.cuda.device(index):
+            return attention_prompt(q, k, v, q_start, k_start, scale, out, lse, err, stream)
+    rc = L.lib().eagle_op_attention_prompt(_stream_of(index, stream), q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv,
+                                           out.data_ptr(), ldo, _ptr(lse), R, k.shape[0], nq, k.shape[1], d,
+                                           q_start.numel() - 1, q_start.data_ptr(), k_start.data_ptr(), scale, _ptr(err))
+    L.check(rc, "eagle_op_attention_prompt")
+    return out

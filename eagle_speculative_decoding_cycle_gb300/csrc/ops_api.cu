@@ -3,6 +3,8 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <new>
+#include <vector>
 
 #include "../../include/eagle.h"
 #include "../../include/eagle_ops.h"
@@ -11,6 +13,7 @@
 #include "kernels.h"
 #include "kv8.cuh"
 #include "lmhead.cuh"
+#include "ops_ext.h"
 
 using namespace eagle;
 
@@ -335,6 +338,194 @@ int eagle_op_attention_kv8(void* stream, const eagle_kv8* cache, const void* q, 
   return eagle_op_attention_shared_kv8(stream, cache, nullptr, nullptr, 0, q, out, R, nq, rows_per_seq, row_seq,
                                        row_slot, ctx_len, mode, tree_T, mask, mask_words, scale, scratch, scratch_bytes,
                                        d_err);
+}
+
+
+// ---- blocks and accepted paths of an 8-bit cache's layers -----------------------------------------
+// The layers' common shape and their arrays. They must agree in everything but the four arrays.
+static int kv8_layers(const eagle_kv8* caches, int layers, Kv8& c, std::vector<Kv8Layer>& l) {
+  if (!caches || layers < 1) return EAGLE_EINVAL;
+  if (layers > 4096) return EAGLE_ECAPACITY;
+  l.resize(layers);
+  for (int i = 0; i < layers; ++i) {
+    Kv8 x;
+    const int r = kv8_view(caches + i, x);
+    if (r != EAGLE_OK) return r;
+    if (i == 0) c = x;
+    if (x.nkv != c.nkv || x.d != c.d || x.max_batch != c.max_batch || x.cap != c.cap || x.table != c.table ||
+        x.block_log2 != c.block_log2 || x.n_blocks != c.n_blocks)
+      return EAGLE_EINVAL;
+    l[i] = Kv8Layer{{x.k, x.v, x.ke, x.ve}};
+  }
+  return EAGLE_OK;
+}
+
+int eagle_op_kv8_compact(void* stream, const eagle_kv8* caches, int layers, int B, const int32_t* n_old,
+                         const int32_t* acc_len, const int32_t* acc_path, int Dmax, int32_t* d_err) try {
+  Kv8 c;
+  std::vector<Kv8Layer> l;
+  int r = kv8_layers(caches, layers, c, l);
+  if (r != EAGLE_OK) return r;
+  if (B < 0 || B > c.max_batch || Dmax < 1 || Dmax > 16) return EAGLE_EINVAL;
+  if (B == 0) return EAGLE_OK;
+  if (!n_old || !acc_len || !acc_path) return EAGLE_EINVAL;
+  r = kv8_compact(reinterpret_cast<cudaStream_t>(stream), c, l.data(), layers, B, n_old, acc_len, acc_path, Dmax, d_err);
+  return r == 0 ? EAGLE_OK : (r == -1 ? EAGLE_ECAPACITY : EAGLE_ECUDA);
+} catch (const std::bad_alloc&) {
+  return EAGLE_ECAPACITY;
+}
+
+size_t eagle_op_kv8_resize_scratch_bytes(const eagle_kv8* cache) {
+  Kv8 c;
+  if (kv8_view(cache, c) != EAGLE_OK || !c.table) return 0;
+  return kv8_resize_scratch(c);
+}
+
+int eagle_op_kv8_resize(void* stream, const eagle_kv8* caches, int layers, int B, int32_t* refs, const int32_t* parent,
+                        const int32_t* length, void* scratch, size_t scratch_bytes, int32_t* d_err) try {
+  Kv8 c;
+  std::vector<Kv8Layer> l;
+  int r = kv8_layers(caches, layers, c, l);
+  if (r != EAGLE_OK) return r;
+  if (!c.table || B < 0 || B > c.max_batch) return EAGLE_EINVAL;
+  if (B == 0) return EAGLE_OK;
+  if (!refs || !length) return EAGLE_EINVAL;
+  if (!scratch || !on16(scratch) || scratch_bytes < kv8_resize_scratch(c)) return EAGLE_ECAPACITY;
+  r = kv8_resize(reinterpret_cast<cudaStream_t>(stream), c, l.data(), layers, B, refs, parent, length, scratch, d_err);
+  return r == 0 ? EAGLE_OK : (r == -1 ? EAGLE_ECAPACITY : EAGLE_ECUDA);
+} catch (const std::bad_alloc&) {
+  return EAGLE_ECAPACITY;
+}
+
+// ---- rotary positions -------------------------------------------------------------------------------
+int eagle_rope_frequencies(int rot, double theta, const eagle_rope_scaling* s, double* freq, float* factor) {
+  if (!freq || !factor || rot < 2 || rot % 2 || rot > 65536 || !(theta > 1.0) || !std::isfinite(theta)) return EAGLE_EINVAL;
+  const double pi2 = 6.283185307179586476925286766559;
+  const int kind = s ? s->kind : EAGLE_ROPE_PLAIN;
+  if (kind < EAGLE_ROPE_PLAIN || kind > EAGLE_ROPE_YARN) return EAGLE_EINVAL;
+  if (kind != EAGLE_ROPE_PLAIN && !(s->factor >= 1.0 && std::isfinite(s->factor))) return EAGLE_EINVAL;
+  *factor = 1.f;
+  double base = theta, lo = 0, hi = 0;
+  if (kind == EAGLE_ROPE_NTK) {
+    if (rot < 4) return EAGLE_EINVAL;
+    base = theta * std::pow(s->factor, (double)rot / (rot - 2));
+  } else if (kind == EAGLE_ROPE_LLAMA3) {
+    if (!(s->original > 0 && s->low >= 0 && s->high > s->low && std::isfinite(s->high) && std::isfinite(s->original)))
+      return EAGLE_EINVAL;
+  } else if (kind == EAGLE_ROPE_YARN) {
+    // the pairs (as real numbers) that make `high` and `low` turns over the original context
+    if (!(s->original > 0 && s->low > 0 && s->high >= s->low && std::isfinite(s->high) && std::isfinite(s->original)))
+      return EAGLE_EINVAL;
+    const double unit = rot / (2 * std::log(theta));
+    lo = std::max(0.0, std::floor(unit * std::log(s->original / (s->high * pi2))));
+    hi = std::min(rot - 1.0, std::ceil(unit * std::log(s->original / (s->low * pi2))));
+    *factor = s->attention > 0 ? (float)s->attention : (float)(0.1 * std::log(s->factor) + 1);
+  }
+  for (int i = 0; i < rot / 2; ++i) {
+    double f = std::pow(base, -2.0 * i / rot);
+    if (kind == EAGLE_ROPE_LINEAR) {
+      f /= s->factor;
+    } else if (kind == EAGLE_ROPE_LLAMA3) {
+      const double turns = s->original * f / pi2;
+      const double keep = std::min(1.0, std::max(0.0, (turns - s->low) / (s->high - s->low)));
+      f = keep * f + (1 - keep) * (f / s->factor);
+    } else if (kind == EAGLE_ROPE_YARN) {
+      const double slow = i <= lo ? 0.0 : i >= hi ? 1.0 : (i - lo) / (hi - lo);
+      f = (1 - slow) * f + slow * (f / s->factor);
+    }
+    freq[i] = f;
+  }
+  return EAGLE_OK;
+}
+
+int eagle_rope_turns(int n, const double* freq, uint64_t* turns) {
+  if (n < 1 || !freq || !turns) return EAGLE_EINVAL;
+  for (int i = 0; i < n; ++i) {
+    const double t = freq[i] / 6.283185307179586476925286766559;
+    if (!std::isfinite(t) || std::fabs(t) > 4503599627370496.0) return EAGLE_EINVAL;
+    const double part = t - std::floor(t);
+    turns[i] = part < 1.0 ? (uint64_t)std::ldexp(part, 64) : 0;      // (a tiny negative angle's part rounds to 1: no turn)
+  }
+  return EAGLE_OK;
+}
+
+// Whether rows of wa bytes, lda bytes apart, and rows of wb bytes, ldb apart, share a byte. With different strides: whether
+// the spans that they lie in do.
+static bool rows_meet(const void* pa, int64_t lda, int64_t wa, int Ra, const void* pb, int64_t ldb, int64_t wb, int Rb) {
+  const intptr_t a = (intptr_t)pa, b = (intptr_t)pb;
+  if (a + (Ra - 1) * lda + wa <= b || b + (Rb - 1) * ldb + wb <= a) return false;
+  if (lda != ldb) return true;
+  int64_t by = (b - a) % lda;      // b's rows from a's, within a row
+  if (by < 0) by += lda;
+  return by < wa || by + wb > lda;
+}
+
+int eagle_op_rope(void* stream, int dtype_in, int dtype_out, const void* q, int64_t ldq, void* q_out, int64_t ldqo, int nq,
+                  const void* k, int64_t ldk, void* k_out, int64_t ldko, int nkv, int head_dim, int rot, int interleaved,
+                  int R, const int32_t* pos, const uint64_t* turns, float factor, int inverse) {
+  if ((dtype_in != EAGLE_DTYPE_F32 && dtype_in != EAGLE_DTYPE_BF16) ||
+      (dtype_out != EAGLE_DTYPE_F32 && dtype_out != EAGLE_DTYPE_BF16))
+    return EAGLE_EINVAL;
+  if (R < 0 || nq < 0 || nkv < 0 || nq + (int64_t)nkv < 1 || head_dim < 16 || head_dim > 256 || head_dim % 16 || rot < 16 ||
+      rot > head_dim || rot % 16 || !std::isfinite(factor))
+    return EAGLE_EINVAL;
+  if (R == 0) return EAGLE_OK;
+  if (nq > 65536 || nkv > 65536) return EAGLE_ECAPACITY;
+  if (!pos || !turns) return EAGLE_EINVAL;
+  const int64_t ei = dtype_in == EAGLE_DTYPE_F32 ? 4 : 2, eo = dtype_out == EAGLE_DTYPE_F32 ? 4 : 2;
+  const struct { const void* p; int64_t ld, e, w; } rows[4] = {{q, ldq, ei, (int64_t)nq * head_dim}, {k, ldk, ei, (int64_t)nkv * head_dim},
+                                                               {q_out, ldqo, eo, (int64_t)nq * head_dim}, {k_out, ldko, eo, (int64_t)nkv * head_dim}};
+  for (const auto& r : rows) {
+    if (!r.w) continue;
+    if (!r.p || !on16(r.p) || r.ld < r.w || r.ld * r.e % 16 || r.ld > ((int64_t)1 << 40)) return EAGLE_EINVAL;
+  }
+  // an output is the input that it comes from, with the same rows and type, or meets no input and no other output
+  for (int o = 2; o < 4; ++o) {
+    if (!rows[o].w) continue;
+    for (int i = 0; i < o; ++i) {
+      if (!rows[i].w || i == o) continue;
+      if (i == o - 2 && rows[i].p == rows[o].p && rows[i].e == rows[o].e && rows[i].ld == rows[o].ld) continue;
+      if (rows_meet(rows[o].p, rows[o].ld * rows[o].e, rows[o].w * rows[o].e, R, rows[i].p, rows[i].ld * rows[i].e,
+                    rows[i].w * rows[i].e, R))
+        return EAGLE_EINVAL;
+    }
+  }
+  RopeArgs a{};
+  a.q = q; a.k = k; a.qo = q_out; a.ko = k_out;
+  a.ldq = ldq; a.ldk = ldk; a.ldqo = ldqo; a.ldko = ldko;
+  a.R = R; a.nq = nq; a.nkv = nkv; a.d = head_dim; a.rot = rot;
+  a.pos = pos; a.turns = reinterpret_cast<const unsigned long long*>(turns); a.factor = factor; a.inverse = inverse != 0;
+  const int r = rope_rows(reinterpret_cast<cudaStream_t>(stream), a, dtype_in == EAGLE_DTYPE_F32, dtype_out == EAGLE_DTYPE_F32,
+                          interleaved != 0);
+  return r == 0 ? EAGLE_OK : (r == -1 ? EAGLE_ECAPACITY : EAGLE_ECUDA);
+}
+
+// ---- attention over whole prompts ---------------------------------------------------------------------
+int eagle_op_attention_prompt(void* stream, const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v, int64_t ldv,
+                              void* out, int64_t ldo, float* lse, int R, int Rk, int nq, int nkv, int head_dim, int B,
+                              const int32_t* q_start, const int32_t* k_start, float scale, int32_t* d_err) {
+  if (R < 0 || Rk < 0 || nkv < 1 || nq < nkv || nq % nkv || nq / nkv > 64 || (head_dim != 64 && head_dim != 128) || B < 0)
+    return EAGLE_EINVAL;
+  if (R == 0 || B == 0) return EAGLE_OK;
+  if ((double)R * nq >= 2147483648.0 || (double)Rk + 256 >= 2147483648.0 || nq > 65536 || B > (1 << 24)) return EAGLE_ECAPACITY;
+  const int64_t wq = (int64_t)nq * head_dim, wk = (int64_t)nkv * head_dim, most = (int64_t)1 << 36;
+  if (!q || !out || !q_start || !k_start || (Rk && (!k || !v))) return EAGLE_EINVAL;
+  if (!on16(q) || !on16(k) || !on16(v) || !on16(out)) return EAGLE_EINVAL;
+  if (ldq < wq || ldo < wq || ldq % 8 || ldo % 8 || ldq > most || ldo > most) return EAGLE_EINVAL;
+  if (Rk && (ldk < wk || ldv < wk || ldk % 8 || ldv % 8 || ldk > most || ldv > most)) return EAGLE_EINVAL;
+  // results go out while other items still read: none of the inputs may be their place
+  if (rows_meet(out, ldo * 2, wq * 2, R, q, ldq * 2, wq * 2, R)) return EAGLE_EINVAL;
+  if (Rk && (rows_meet(out, ldo * 2, wq * 2, R, k, ldk * 2, wk * 2, Rk) || rows_meet(out, ldo * 2, wq * 2, R, v, ldv * 2, wk * 2, Rk)))
+    return EAGLE_EINVAL;
+  PromptArgs a{};
+  a.q = q; a.k = k; a.v = v; a.out = out; a.lse = lse;
+  a.ldq = ldq; a.ldk = ldk; a.ldv = ldv; a.ldo = ldo;
+  a.R = R; a.Rk = Rk; a.nq = nq; a.nkv = nkv; a.d = head_dim; a.B = B;
+  a.start = q_start; a.kstart = k_start;
+  a.scale = scale > 0.f ? scale : 1.f / sqrtf((float)head_dim);
+  a.err = d_err;
+  const int r = prompt_attention(reinterpret_cast<cudaStream_t>(stream), a);
+  return r == 0 ? EAGLE_OK : EAGLE_ECUDA;
 }
 
 }  // extern "C"

@@ -189,6 +189,93 @@ int eagle_op_attention_shared_kv8(void* stream, const eagle_kv8* cache, const vo
                                   int tree_T, const uint64_t* mask, int mask_words, float scale, void* scratch,
                                   size_t scratch_bytes, int32_t* d_err);
 
+/* ---- blocks and accepted paths of an 8-bit cache's layers -----------------------------------------
+ * caches: HOST array of one eagle_kv8 a layer, read during the call; all layers have one shape and
+ * one table. Calls on one table (and writes of the cache) change it and are ordered by the caller.
+ *
+ * Accepted paths to their committed slots, in all layers and heads: slot n_old[b] + j receives what
+ * slot n_old[b] + acc_path[b][j - 1] held, j = 1..acc_len[b], for sequences b < B (n_old, acc_len [B],
+ * acc_path [B][Dmax], Dmax <= 16; codes and exponents are copied, so values stay exactly). A sequence's
+ * moves take effect at once, whatever their order. acc_len <= 0: nothing to do. A length above Dmax
+ * is taken for Dmax; it, a slot outside the cache and a block that is not assigned are latched
+ * into *d_err (2), such a slot's move is left out. Paged or contiguous. The slots that are written
+ * must be the sequence's own (eagle_op_kv8_resize sees to that). */
+int eagle_op_kv8_compact(void* stream, const eagle_kv8* caches, int layers, int B, const int32_t* n_old,
+                         const int32_t* acc_len, const int32_t* acc_path, int Dmax, int32_t* d_err);
+
+/* Block bookkeeping of a paged cache. State: the table and refs [n_blocks], for each pool block the number of
+ * table entries that hold it (zero: free). After the call sequence b < B has blocks for slots
+ * [0, length[b]) and no others; length[b] < 0 leaves it as it is. (a) Surplus entries are
+ * released: -1 in the table, one off the count. (b) A fork, a sequence with parent[b] >= 0 (parent
+ * nullable: no forks), releases all its entries and takes those of its parent's first length[b] slots: the
+ * blocks are shared. Any number of sequences may fork one parent; the parent has length < 0 in
+ * this call and blocks for all those slots. (c) Missing entries get free blocks, the lowest-numbered
+ * first, in the order of sequences and slots. (d) A last block that is partly filled and that other entries
+ * hold too is replaced by a free one (counted in the same order) and its filled slots are copied
+ * in all layers: what a sequence writes at length[b] and behind is never seen by another. A block
+ * that loses its last holder by (d) is free from the next call on.
+ * length[b] past cap, and a parent that is out of range, is b itself, takes part in the call or lacks a
+ * block, are latched into *d_err (2) and leave b as it was; so is an entry outside the pool or a
+ * count that does not match the table (the entry is cleared). Too few free blocks: latched (3); the entries that come
+ * first in the order have theirs, the others stay -1, and a block that should have been copied
+ * stays shared. scratch: no initial value, not shared with a call that may overlap on the GPU. */
+size_t eagle_op_kv8_resize_scratch_bytes(const eagle_kv8* cache);
+int eagle_op_kv8_resize(void* stream, const eagle_kv8* caches, int layers, int B, int32_t* refs, const int32_t* parent,
+                        const int32_t* length, void* scratch, size_t scratch_bytes, int32_t* d_err);
+
+/* ---- rotary positions ------------------------------------------------------------------------------
+ * Frequencies on the host: freq[i], i < rot / 2, the angle that pair i turns by from one position to the next,
+ * theta^(-2i / rot) under one of these rules for contexts beyond the trained one (scaling nullable: plain):
+ * LINEAR: divided by factor. NTK: base theta * factor^(rot / (rot - 2)). LLAMA3: pairs of at most
+ * `low` turns in the original context divided by factor, of `high` and more unchanged, between them a
+ * blend, linear in the turns. YARN: unchanged up to the pair of `high` turns, divided by factor from the pair of
+ * `low` turns on (both rounded outwards to whole pairs), a ramp over the pairs between; *factor
+ * receives `attention`, or 0.1 ln(factor) + 1 when that is not positive, by which the op scales turned
+ * entries; it is 1 otherwise. */
+enum { EAGLE_ROPE_PLAIN = 0, EAGLE_ROPE_LINEAR = 1, EAGLE_ROPE_NTK = 2, EAGLE_ROPE_LLAMA3 = 3, EAGLE_ROPE_YARN = 4 };
+typedef struct {
+  int kind;
+  double factor;       /* >= 1 */
+  double original;     /* trained context (LLAMA3, YARN) */
+  double low, high;    /* turns (LLAMA3, YARN) */
+  double attention;    /* YARN */
+} eagle_rope_scaling;
+int eagle_rope_frequencies(int rot, double theta, const eagle_rope_scaling* scaling, double* freq, float* factor);
+
+/* The op's table from angles per position (radians, of any rule): turns[i] = freq[i] / 2 pi modulo 1, in
+ * 2^-64. Host memory; copy it to the device. */
+int eagle_rope_turns(int n, const double* freq, uint64_t* turns);
+
+/* Turn the first `rot` entries of each head of R rows of q ([nq][head_dim]) and k ([nkv][head_dim]; either count may be
+ * 0), row r by pos[r] * freq: pairs (x[i], x[i + rot / 2]), or (x[2i], x[2i + 1]) when interleaved, become
+ * factor * (a cos - b sin, b cos + a sin), with `inverse` the same by the negative angle. Entries behind
+ * `rot` are copied. head_dim 16..256 and rot 16..head_dim, multiples of 16. Types EAGLE_DTYPE_F32 or
+ * _BF16, in and out independently; 16-byte aligned rows of free stride (elements, whole 16 bytes), so q
+ * and k may be columns of a fused projection. An output may be the input it comes from (same type, rows
+ * and stride); otherwise outputs meet neither an input nor each other (refused). turns: device [rot / 2].
+ * Positions are any int32: the angle is taken modulo a turn without rounding, then rounded to fp32 (2^-24
+ * relative), arithmetic is fp32 and the result is rounded once. */
+int eagle_op_rope(void* stream, int dtype_in, int dtype_out, const void* q, int64_t ldq, void* q_out, int64_t ldqo, int nq,
+                  const void* k, int64_t ldk, void* k_out, int64_t ldko, int nkv, int head_dim, int rot, int interleaved,
+                  int R, const int32_t* pos, const uint64_t* turns, float factor, int inverse);
+
+/* Causal attention over whole prompts, packed: sequence b < B has rows q[q_start[b] .. q_start[b + 1]) and keys and values
+ * k, v[k_start[b] .. k_start[b + 1]). Its last row sees all its keys, each row before it one fewer: with as many rows as
+ * keys a whole prompt, with fewer the last chunk of one, with more the first rows see nothing (zeros, lse
+ * -inf). q, out bf16 [R][nq][head_dim], k, v bf16 [Rk][nkv][head_dim], 16-byte aligned with free row strides (elements,
+ * multiples of 8), head_dim 64 or 128, at most 64 query heads a KV head. lse (nullable): fp32 [R][nq], the natural
+ * logarithm of each row's sum of exp(score), by which results over different keys can be joined. Scale =
+ * 1/sqrt(head_dim) when scale <= 0. q_start, k_start: device [B + 1], read by the kernel, so that a captured call serves
+ * any lengths; a sequence whose starts fall, or lie outside [0, R] or [0, Rk], is latched into *d_err (nullable) and
+ * skipped. Rows of no sequence are left as they were. out meets none of q, k, v (refused).
+ * Products are bf16 with fp32 sums; weights enter the value product as bf16 (2^-8 relative, the type of the values);
+ * maxima, sums and lse are fp32. A row's result depends on its own keys alone, bit for bit whatever other sequences
+ * hold: keys and values that it does not see, of its own sequence too, may be anything, NaN and infinities
+ * among it. */
+int eagle_op_attention_prompt(void* stream, const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v, int64_t ldv,
+                              void* out, int64_t ldo, float* lse, int R, int Rk, int nq, int nkv, int head_dim, int B,
+                              const int32_t* q_start, const int32_t* k_start, float scale, int32_t* d_err);
+
 /* EAGLE-2 tree growth and rerank with injected draft confidences, for B sequences:
  * cand_tok/cand_logc [B][k]: the root's children (token, log confidence) in rank order;
  * child_tok/child_logc [B][depth-1][k][k]: children of the r-th node selected at depth

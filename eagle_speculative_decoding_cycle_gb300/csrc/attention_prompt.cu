@@ -8,18 +8,19 @@
 // The query heads of a KV head read the same keys, so a tile of 128 query vectors is RB = 128 / G positions times the G
 // heads: one TMA box lays them out so, and grouped heads need neither copies nor masks of their own. An item is a pair of such
 // tiles (2 RB positions of one KV head) with all the keys that its rows see, 128 at a time. A CTA an SM takes items in
-// turn, the ones with the most keys first. 12 warps:
-//   warps 0-3, 4-7  softmax of tile 0 / 1, one thread a query vector (TMEM lane): S row -> maximum, weights as bf16 back into
-//                   TMEM over S, running sum; O is rescaled only when the maximum moves by more than 2^8; results;
-//   warp 8          finds the items; TMA: Q of each tile, K and V tiles through one ring;
-//   warps 9, 10     tcgen05.mma of tile 0 / 1: S = Q K^T (operands in shared memory), O += P V (P in TMEM, V read MN-major);
-//   warp 11         looks through value tiles that not all rows see (below).
+// turn, the ones with the most keys first. 20 warps:
+//   warps 0-7, 8-15 softmax of tile 0 / 1, four threads a query vector (16 TMEM lanes a warp): S row -> maximum, weights as bf16
+//                   back into TMEM over S, running sum; O is rescaled only when the maximum moves by more than 2^8; results;
+//   warp 16         finds the items; TMA: Q of each tile, K and V tiles through one ring;
+//   warps 17, 18    tcgen05.mma of tile 0 / 1, in turn: S = Q K^T (operands in shared memory), O += P V (P in TMEM, V read
+//                   MN-major);
+//   warp 19         looks through value tiles that not all rows see (below).
 // TMEM: S0 S1 (128 columns each, P over the first 64), O0 O1 (d each). While one tile is in its softmax warps the tensor cores
 // run the other's products. Weights are rounded to bf16 (2^-8 relative at most, as the values that they meet); maxima, sums
 // and outputs are fp32, the sum of the unrounded weights.
 //
 // A weight of zero does not hide a value that is not finite (0 * inf = NaN). In the tiles that some rows see only in part
-// warp 11 replaces such values by zero and keeps, for each column, the first key that held a NaN, +inf and -inf: rows that
+// warp 19 replaces such values by zero and keeps, for each column, the first key that held a NaN, +inf and -inf: rows that
 // see it get that value in their results, the others are left alone.
 #include "attn_tc.cuh"
 #include "kernels.h"
@@ -31,7 +32,8 @@ namespace eagle {
 namespace {
 
 constexpr int AT = 128;              // keys a tile, query vectors a tile
-constexpr int AP_THREADS = 384;
+constexpr int AP_SOFT = 16;          // softmax warps, eight a tile
+constexpr int AP_THREADS = (AP_SOFT + 4) * 32;
 constexpr float AP_LAZY = 8.f;       // binary orders that a maximum may pass its reference by
 constexpr uint32_t AP_NONE = 0x3fffffffu;      // three fields of ten bits, "no key"
 
@@ -169,6 +171,52 @@ __device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
   return r;
 }
 
+// A warp's 16 lanes of TMEM as fragments: thread t gets of row t / 4 and of row t / 4 + 8 the columns 2 (t % 4) and one more of
+// every eight (v[4 i .. 4 i + 3]: the two of the first row, the two of the second).
+__device__ __forceinline__ void frag_ld64(uint32_t t, float* v) {      // 64 columns
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
+        "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
+        "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+      : "r"(t));
+}
+// 64 bf16 a row as 32 columns of pairs: w[2 i] of the first row, w[2 i + 1] of the second, in frag_ld64's order.
+__device__ __forceinline__ void frag_st_pairs(uint32_t t, const uint32_t* w) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(t),
+      "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]), "r"(w[8]), "r"(w[9]),
+      "r"(w[10]), "r"(w[11]), "r"(w[12]), "r"(w[13]), "r"(w[14]), "r"(w[15])
+      : "memory");
+}
+// The maximum over the four threads that share a row.
+__device__ __forceinline__ float quad_max(float x) {
+  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+  return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+}
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// w[j]: word q of piece j (q = the thread's place among the four of its row) -> word j of piece q.
+__device__ __forceinline__ void quad_transpose(uint32_t* w, int q) {
+  const bool odd = q & 1, high = q & 2;
+#pragma unroll
+  for (int j = 0; j < 4; j += 2) {
+    const uint32_t y = __shfl_xor_sync(0xffffffffu, odd ? w[j] : w[j + 1], 1);
+    if (odd) w[j] = y;
+    else w[j + 1] = y;
+  }
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const uint32_t y = __shfl_xor_sync(0xffffffffu, high ? w[j] : w[j + 2], 2);
+    if (high) w[j] = y;
+    else w[j + 2] = y;
+  }
+}
+
 // Values that are not finite in rows [r0, 128) of a value tile (16-byte pieces, 128-byte swizzle): replaced by zero, the
 // first key (of those after the first row's last, 0: seen by all) kept for each column. By a converged warp.
 template <int D>
@@ -232,7 +280,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
   uint64_t *full = bars, *empty = bars + ST /* ring */, *q_full = bars + 2 * ST /* [tile] */, *q_empty = q_full + 2,
            *s_full = q_full + 4 /* [tile] */, *p_full = q_full + 6 /* [tile][half] */, *o_done = q_full + 10 /* [tile] */,
            *o_free = q_full + 12 /* [tile] */, *item_full = q_full + 14 /* [slot] */, *item_empty = q_full + 16 /* [slot] */,
-           *drain = q_full + 18 /* [tile] */, *looked = q_full + 20 /* ring */;
+           *drain = q_full + 18 /* [tile] */, *turn = q_full + 20 /* [tile] */, *looked = q_full + 22 /* ring */;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(looked + ST);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* has_bad = abort_flag + 1;      // [slot]
@@ -249,168 +297,218 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
       mbar_init(smem_u32(q_full + i), 1);
       mbar_init(smem_u32(q_empty + i), 1);
       mbar_init(smem_u32(s_full + i), 1);
-      mbar_init(smem_u32(p_full + 2 * i), 4);
-      mbar_init(smem_u32(p_full + 2 * i + 1), 4);
+      mbar_init(smem_u32(p_full + 2 * i), AP_SOFT / 2);
+      mbar_init(smem_u32(p_full + 2 * i + 1), AP_SOFT / 2);
       mbar_init(smem_u32(o_done + i), 1);
-      mbar_init(smem_u32(o_free + i), 4);
+      mbar_init(smem_u32(o_free + i), AP_SOFT / 2);
+      mbar_init(smem_u32(turn + i), 1);
       mbar_init(smem_u32(item_full + i), 1);
-      mbar_init(smem_u32(item_empty + i), 11);
+      mbar_init(smem_u32(item_empty + i), AP_SOFT + 3);
       mbar_init(smem_u32(drain + i), 1);
       has_bad[i] = 0;
     }
     *abort_flag = 0;
     fence_mbar_init();
+    mbar_arrive(smem_u32(turn));      // tile 0 begins
   }
-  if (warp == 9) tmem_alloc(smem_u32(tmem_slot), 512);
+  if (warp == AP_SOFT + 1) tmem_alloc(smem_u32(tmem_slot), 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   PDL_ENTRY();
 
-  if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
-    const int mt = warp >> 2, qv = threadIdx.x & 127;
-    const int pos = qv / a.G, g = qv - pos * a.G;      // of the tile's 128 query vectors
-    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t tS = tmem + mt * AT + lane_off, tO = tmem + 2 * AT + mt * D + lane_off;
+  if (warp < AP_SOFT) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+    // a warp has 16 rows of its tile, of its own quarter of the TMEM lanes: threads 4 r .. 4 r + 3 rows r and r + 8
+    const int mt = warp >> 3, quad = threadIdx.x & 3, lane0 = (warp & 3) * 32 + (warp >> 2 & 1) * 16;
+    const int qv = lane0 + ((threadIdx.x & 31) >> 2);
+    const uint32_t tS = tmem + mt * AT + ((uint32_t)lane0 << 16), tO = tmem + 2 * AT + mt * D + ((uint32_t)lane0 << 16);
+    int pos[2], g[2];
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      pos[y] = (qv + 8 * y) / a.G;
+      g[y] = qv + 8 * y - pos[y] * a.G;
+    }
     uint32_t s_phase = 0, o_phase = 0;
     bool ok = true;
     for (int n = 0; ok; ++n) {
       ok = kv8_wait(smem_u32(item_full + (n & 1)), (uint32_t)((n >> 1) & 1), abort_flag, a.err);
       if (!ok) break;
-      const ApItem it = items[n & 1];
+      const ApItem& it = items[n & 1];
       if (it.h < 0) break;
-      const int nt = it.n[mt];
-      const int lim = it.lim0 + mt * a.RB + pos;      // last key that this row sees
-      float m2 = -INFINITY, l = 0.f;
+      const int nt = it.n[mt], first = it.lim0 + mt * a.RB;      // the last key that the tile's first row sees
+      float m2[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};      // l: this thread's part
       for (int j = 0; j < nt; ++j) {
         ok = kv8_wait(smem_u32(s_full + mt), s_phase, abort_flag, a.err);
         if (!ok) break;
         s_phase ^= 1;
         tc_fence_after();
-        float s[AT];
+        float s[64];
+        frag_ld64(tS, s);
+        tmem_wait_ld(s);
+        frag_ld64(tS + 64, s + 32);
+        const bool partial = j * AT + AT - 1 > first;      // some row of the tile does not see all of these keys
+        float mx[2];
 #pragma unroll
-        for (int c = 0; c < AT; c += 32) tmem_ld32_async(tS + c, s + c);
+        for (int hf = 0; hf < 2; ++hf) {      // (the second half arrives under the first one's maximum)
+          if (hf) tmem_wait_ld(s + 32);
+          if (partial) {
 #pragma unroll
-        for (int c = 0; c < AT; c += 32) tmem_wait_ld(s + c);
-        if (j * AT + AT - 1 > it.lim0 + mt * a.RB) {      // some row of the tile does not see all of these keys
-          const int last = lim - j * AT;
+            for (int y = 0; y < 2; ++y) {
+              const int last = first + pos[y] - j * AT - hf * 64 - 2 * quad;
 #pragma unroll
-          for (int c = 0; c < AT; ++c) s[c] = c <= last ? s[c] : -INFINITY;
+              for (int c = 0; c < 8; ++c) {
+                s[hf * 32 + 4 * c + 2 * y] = 8 * c <= last ? s[hf * 32 + 4 * c + 2 * y] : -INFINITY;
+                s[hf * 32 + 4 * c + 2 * y + 1] = 8 * c + 1 <= last ? s[hf * 32 + 4 * c + 2 * y + 1] : -INFINITY;
+              }
+            }
+          }
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const float* x = s + hf * 32 + 2 * y;
+            float x0 = hf ? max3(mx[y], x[0], x[1]) : fmaxf(x[0], x[1]), x1 = fmaxf(x[4], x[5]);
+#pragma unroll
+            for (int c = 2; c < 8; c += 2) {
+              x0 = max3(x0, x[4 * c], x[4 * c + 1]);
+              x1 = max3(x1, x[4 * c + 4], x[4 * c + 5]);
+            }
+            mx[y] = fmaxf(x0, x1);
+          }
         }
-        float x0 = s[0], x1 = s[1], x2 = s[2], x3 = s[3];
+        float corr[2] = {1.f, 1.f};
+        bool raise = false;
 #pragma unroll
-        for (int c = 4; c + 7 < AT; c += 8) {
-          x0 = max3(x0, s[c], s[c + 1]);
-          x1 = max3(x1, s[c + 2], s[c + 3]);
-          x2 = max3(x2, s[c + 4], s[c + 5]);
-          x3 = max3(x3, s[c + 6], s[c + 7]);
-        }
-        const float mx = fmaxf(max3(x0, x1, fmaxf(s[AT - 4], s[AT - 3])), max3(x2, x3, fmaxf(s[AT - 2], s[AT - 1]))) * a.sl2;
-        const bool raise = mx > m2 + AP_LAZY;
-        float corr = 1.f;
-        if (raise) {
-          corr = pf_ex2(m2 - mx);
-          m2 = mx;
-          l *= corr;
+        for (int y = 0; y < 2; ++y) {
+          mx[y] = quad_max(mx[y]) * a.sl2;
+          if (mx[y] > m2[y] + AP_LAZY) {
+            corr[y] = pf_ex2(m2[y] - mx[y]);
+            m2[y] = mx[y];
+            l[y] *= corr[y];
+            raise = true;
+          }
         }
         // (this S came behind the product into O before it, so O is there)
         if (j > 0 && __any_sync(0xffffffffu, raise)) {
 #pragma unroll 1
           for (int c = 0; c < D; c += 16) {
-            float o[16];
-            tmem_ld16(tO + c, o);
+            float o[8];
+            asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                         : "=f"(o[0]), "=f"(o[1]), "=f"(o[2]), "=f"(o[3]), "=f"(o[4]), "=f"(o[5]), "=f"(o[6]), "=f"(o[7])
+                         : "r"(tO + c));
+            asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-            for (int x = 0; x < 16; ++x) o[x] *= corr;
-            tmem_st16(tO + c, o);
+            for (int x = 0; x < 8; ++x) {
+              asm volatile("" : "+f"(o[x]));
+              o[x] *= corr[x >> 1 & 1];
+            }
+            asm volatile("tcgen05.st.sync.aligned.16x256b.x2.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(tO + c), "f"(o[0]),
+                         "f"(o[1]), "f"(o[2]), "f"(o[3]), "f"(o[4]), "f"(o[5]), "f"(o[6]), "f"(o[7])
+                         : "memory");
           }
         }
         // One rounding of the reference for the whole row, then one of each difference: near the maximum, where weights
         // count, that is exact whatever the size of the scores.
-        const float ref = m2 == -INFINITY ? 0.f : m2;
-        const f32x2 nm = two(-ref, -ref), s2 = two(a.sl2, a.sl2);
-        f32x2 sum[2] = {two(0.f, 0.f), two(0.f, 0.f)};
+        f32x2 nm[2], sum[2];
+        const f32x2 s2 = two(a.sl2, a.sl2);
 #pragma unroll
-        for (int qt = 0; qt < AT / 32; ++qt) {
+        for (int y = 0; y < 2; ++y) {
+          const float ref = m2[y] == -INFINITY ? 0.f : m2[y];
+          nm[y] = two(-ref, -ref);
+          sum[y] = two(0.f, 0.f);
+        }
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
           uint32_t w[16];
 #pragma unroll
-          for (int c = 0; c < 32; c += 2) {
-            float2 x = one_by_one(fma2(two(s[qt * 32 + c], s[qt * 32 + c + 1]), s2, nm));
-            x.x = pf_ex2(x.x);
-            x.y = pf_ex2(x.y);
-            sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], two(x.x, x.y));
-            const __nv_bfloat162 b = __floats2bfloat162_rn(x.x, x.y);
-            w[c / 2] = *reinterpret_cast<const uint32_t*>(&b);
+          for (int c = 0; c < 16; ++c) {      // 2 c': first row, 2 c' + 1: second row
+            const float* x = s + hf * 32 + 2 * c;
+            float2 e = one_by_one(fma2(two(x[0], x[1]), s2, nm[c & 1]));
+            e.x = pf_ex2(e.x);
+            e.y = pf_ex2(e.y);
+            sum[c & 1] = add2(sum[c & 1], two(e.x, e.y));
+            w[c] = bf16_pair(e.x, e.y);
           }
-          tmem_st16u(tS + qt * 16, w);
-          if (qt & 1) {
-            tmem_wait_st();
-            tc_fence_before();
-            warp_arrive(smem_u32(p_full + 2 * mt + (qt >> 1)));
-          }
+          frag_st_pairs(tS + hf * 32, w);
+          tmem_wait_st();
+          tc_fence_before();
+          warp_arrive(smem_u32(p_full + 2 * mt + hf));
         }
-        const float2 sums = one_by_one(add2(sum[0], sum[1]));
-        l += sums.x + sums.y;
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const float2 sums = one_by_one(sum[y]);
+          l[y] += sums.x + sums.y;
+        }
       }
       if (!ok) break;
       if (it.rows[mt] > 0) {
-        const int row = it.row0 + mt * a.RB + pos, head = it.h * a.G + g;
-        const bool write = pos < it.rows[mt];      // (so pos < RB: not the vectors behind the last head)
-        __nv_bfloat16* dst = a.out + (long long)row * a.ldo + (long long)head * D;
-        if (write && a.lse) {
-          const float ref = m2 == -INFINITY ? 0.f : m2;
-          a.lse[(long long)row * a.nq + head] = l == 0.f ? -INFINITY : (ref + log2f(l)) * 0.693147180559945309f;
+        float inv[2];
+        __nv_bfloat16* dst[2];
+        bool write[2];
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          l[y] += __shfl_xor_sync(0xffffffffu, l[y], 1);
+          l[y] += __shfl_xor_sync(0xffffffffu, l[y], 2);
+          const int row = it.row0 + mt * a.RB + pos[y], head = it.h * a.G + g[y];
+          write[y] = pos[y] < it.rows[mt];      // (so pos < RB: not the vectors behind the last head)
+          dst[y] = a.out + (long long)row * a.ldo + (long long)head * D;
+          inv[y] = l[y] == 0.f ? 0.f : 1.f / l[y];
+          if (write[y] && a.lse && quad == 0) {
+            const float ref = m2[y] == -INFINITY ? 0.f : m2[y];
+            a.lse[(long long)row * a.nq + head] = l[y] == 0.f ? -INFINITY : (ref + log2f(l[y])) * 0.693147180559945309f;
+          }
         }
         if (nt == 0) {      // rows that see no key
-          if (write)
 #pragma unroll
-            for (int c = 0; c < D; c += 8) *reinterpret_cast<uint4*>(dst + c) = make_uint4(0, 0, 0, 0);
+          for (int y = 0; y < 2; ++y)
+            if (write[y])
+              for (int c = quad * 8; c < D; c += 32) *reinterpret_cast<uint4*>(dst[y] + c) = make_uint4(0, 0, 0, 0);
         } else {
           ok = kv8_wait(smem_u32(o_done + mt), o_phase, abort_flag, a.err);
           if (!ok) break;
           o_phase ^= 1;
           tc_fence_after();
-          const float inv = l == 0.f ? 0.f : 1.f / l;
           const bool poisoned = has_bad[n & 1] != 0;
-          const int i = mt * a.RB + pos;
 #pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
+          for (int c = 0; c < D; c += 64) {
             float o[32];
-            tmem_ld32(tO + c, o);
+            frag_ld64(tO + c, o);
+            tmem_wait_ld(o);
+            if (c + 64 == D) {      // O is read: the next item's products may begin
+              tc_fence_before();
+              warp_arrive(smem_u32(o_free + mt));
+            }
 #pragma unroll
-            for (int x = 0; x < 32; ++x) o[x] *= inv;
+            for (int x = 0; x < 32; ++x) o[x] *= inv[x >> 1 & 1];
             if (poisoned) {
-#pragma unroll 1
-              for (int x = 0; x < 32; ++x) {
-                const uint32_t w = bad[(n & 1) * D + c + x];
-                const bool nan = i >= (int)(w & 1023), up = i >= (int)((w >> 10) & 1023), down = i >= (int)((w >> 20) & 1023);
-                const float add = nan || (up && down) ? __int_as_float(0x7fffffff) : up ? INFINITY : down ? -INFINITY : 0.f;
+              const uint32_t* from = bad + (n & 1) * D + c + 2 * quad;
 #pragma unroll
-                for (int y = 0; y < 32; ++y) o[y] += y == x ? add : 0.f;
+              for (int x = 0; x < 32; ++x) {
+                const uint32_t w = from[(x >> 2) * 8 + (x & 1)];
+                const int i = mt * a.RB + pos[x >> 1 & 1];
+                const bool nan = i >= (int)(w & 1023), up = i >= (int)((w >> 10) & 1023), down = i >= (int)((w >> 20) & 1023);
+                if (nan || up || down) o[x] = nan || (up && down) ? __int_as_float(0x7fffffff) : up ? o[x] + INFINITY : o[x] - INFINITY;
               }
             }
-            if (write)
+            // a thread gets whole 16-byte pieces: the four of a row write 64 bytes in one go
 #pragma unroll
-              for (int x = 0; x < 32; x += 8) {
+            for (int y = 0; y < 2; ++y)
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
                 uint32_t w[4];
 #pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                  const __nv_bfloat162 b = __floats2bfloat162_rn(o[x + 2 * y], o[x + 2 * y + 1]);
-                  w[y] = *reinterpret_cast<const uint32_t*>(&b);
-                }
-                *reinterpret_cast<uint4*>(dst + c + x) = make_uint4(w[0], w[1], w[2], w[3]);
+                for (int z = 0; z < 4; ++z) w[z] = bf16_pair(o[(x * 4 + z) * 4 + 2 * y], o[(x * 4 + z) * 4 + 2 * y + 1]);
+                quad_transpose(w, quad);
+                if (write[y]) *reinterpret_cast<uint4*>(dst[y] + c + x * 32 + quad * 8) = make_uint4(w[0], w[1], w[2], w[3]);
               }
           }
-          tc_fence_before();
-          warp_arrive(smem_u32(o_free + mt));
         }
       }
       warp_arrive(smem_u32(item_empty + (n & 1)));
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    if (warp == 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if (warp == AP_SOFT) {
       // ---- items, TMA ----
       ApList list = ap_begin(a, blockIdx.x == 0);
       const uint32_t qbytes = (uint32_t)(a.RB * a.G * 128);
@@ -443,7 +541,9 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
         return true;
       };
       for (int n = 0; ok; ++n) {
-        const ApItem it = ap_item(a, list, blockIdx.x + (long long)n * gridDim.x);
+        // to and fro over the CTAs: who takes the largest of one round takes the smallest of the next
+        const int turn = n & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
+        const ApItem it = ap_item(a, list, turn + (long long)n * gridDim.x);
         if (n >= 2) ok = kv8_wait_all(smem_u32(item_empty + (n & 1)), (uint32_t)(((n >> 1) - 1) & 1), abort_flag, a.err);
         if (!ok) break;
         if (elect_one()) {
@@ -469,19 +569,19 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
         for (int x = max(0, s - ST); x < s; ++x)
           kv8_wait_all(smem_u32(full + x % ST), (uint32_t)((x / ST) & 1), abort_flag, a.err, false);
       }
-    } else if (warp < 11) {
+    } else if (warp < AP_SOFT + 3) {
       // ---- MMA: one warp a query tile ----
       constexpr uint32_t IS = pf_idesc(AT, false), IO = pf_idesc(D, true);
-      const int mt = warp - 9;
+      const int mt = warp - AP_SOFT - 1;
       const uint32_t tS = tmem + mt * AT, tO = tmem + 2 * AT + mt * D;
       // operand descriptors; an offset of n bytes adds n >> 4
       const uint64_t dq = sdesc_sw128(smem_u32(sm + mt * Sh::OP)), dk = sdesc_sw128(smem_u32(sm + Sh::OFF_RING)),
                      dv = pf_desc_mn(smem_u32(sm + Sh::OFF_RING), Sh::HALF);
       int s = 0, used = 0;
-      uint32_t p_phase = 0;
+      uint32_t p_phase = 0, t_phase = 0;
       bool ok = true;
       auto wait_stage = [&](int x) { return kv8_wait_all(smem_u32(full + x % ST), (uint32_t)((x / ST) & 1), abort_flag, a.err); };
-      // (behind wait_stage: warp 11 has then passed the stage's use before, so this phase is the current one)
+      // (behind wait_stage: warp 19 has then passed the stage's use before, so this phase is the current one)
       auto wait_looked = [&](int x) { return kv8_wait_all(smem_u32(looked + x % ST), (uint32_t)((x / ST) & 1), abort_flag, a.err); };
       auto issue_s = [&](int x, bool last) {      // by one lane
         const uint64_t k = dk + ((uint64_t)(x % ST) * Sh::OP >> 4);
@@ -517,9 +617,11 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
           int seen;
           const bool partial = ap_partial(it, a.RB, j, seen);
           if (j >= mine) {      // the other tile's keys alone
-            ok = wait_stage(s) && wait_stage(s + 1);
+            ok = wait_stage(s) && wait_stage(s + 1) && kv8_wait_all(smem_u32(turn + mt), t_phase, abort_flag, a.err);
+            t_phase ^= 1;
             if (!ok) break;
             if (elect_one()) {
+              mbar_arrive(smem_u32(turn + (mt ^ 1)));
               mbar_arrive(smem_u32(empty + s % ST));
               mbar_arrive(smem_u32(empty + (s + 1) % ST));
             }
@@ -531,7 +633,9 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
           if (ok && partial) ok = wait_looked(s + 1);
           if (ok && next) ok = wait_stage(s + 2);
           if (ok && j == 0 && used) ok = kv8_wait_all(smem_u32(o_free + mt), (uint32_t)((used - 1) & 1), abort_flag, a.err);
-          ok = ok && kv8_wait_all(smem_u32(p_full + 2 * mt), p_phase, abort_flag, a.err);
+          ok = ok && kv8_wait_all(smem_u32(p_full + 2 * mt), p_phase, abort_flag, a.err) &&
+               kv8_wait_all(smem_u32(turn + mt), t_phase, abort_flag, a.err);
+          t_phase ^= 1;
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) issue_o(s + 1, 0, j == 0);
@@ -545,6 +649,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
             tc_commit(smem_u32(empty + (s + 1) % ST));
             if (next) issue_s(s + 2, j + 2 == mine);
             else tc_commit(smem_u32(o_done + mt));
+            mbar_arrive(smem_u32(turn + (mt ^ 1)));
           }
           __syncwarp();
         }
@@ -597,7 +702,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == AP_SOFT + 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }

@@ -7,20 +7,25 @@
 //
 // The query heads of a KV head read the same keys, so a tile of 128 query vectors is RB = 128 / G positions times the G
 // heads: one TMA box lays them out so, and grouped heads need neither copies nor masks of their own. An item is a pair of such
-// tiles (2 RB positions of one KV head) with all the keys that its rows see, 128 at a time. A CTA an SM takes items in
-// turn, the ones with the most keys first. 20 warps:
-//   warps 0-7, 8-15 softmax of tile 0 / 1, four threads a query vector (16 TMEM lanes a warp): S row -> maximum, weights as bf16
-//                   back into TMEM over S, running sum; O is rescaled only when the maximum moves by more than 2^8; results;
-//   warp 16         finds the items; TMA: Q of each tile, K and V tiles through one ring;
-//   warps 17, 18    tcgen05.mma of tile 0 / 1, in turn: S = Q K^T (operands in shared memory), O += P V (P in TMEM, V read
-//                   MN-major);
-//   warp 19         looks through value tiles that not all rows see (below).
-// TMEM: S0 S1 (128 columns each, P over the first 64), O0 O1 (d each). While one tile is in its softmax warps the tensor cores
-// run the other's products. Weights are rounded to bf16 (2^-8 relative at most, as the values that they meet); maxima, sums
-// and outputs are fp32, the sum of the unrounded weights.
+// tiles (2 RB positions of one KV head) with all the keys that its rows see, KT at a time. A CTA an SM takes items in
+// turn, the ones with the most keys first. 16 warps:
+//   warps 0-3, 4-7  softmax of tile 0 / 1, one thread a query vector (TMEM lane): S row -> weights as bf16 in TMEM, running sum;
+//                   O is rescaled only when the maximum moves by more than 2^8;
+//   warps 8-11      results: O of both tiles from TMEM, divided by the sums;
+//   warp 12         finds the items; TMA: Q of each tile, K and V tiles through one ring;
+//   warps 13, 14    tcgen05.mma of tile 0 / 1: S = Q K^T (operands in shared memory), O += P V (P in TMEM, V read MN-major);
+//   warp 15         looks through value tiles that not all rows see (below).
+//
+// TMEM decides the tile. With S, then P over it, of 128 keys (256 columns for two tiles, 256 for their O) a tile's chain of
+// S, softmax, P V, S ... has no overlap but the other tile's: 1.7 us for 128 keys of a pair, of them 1.06 of products and 0.54 of
+// softmax; the hand-overs between softmax and products, some 0.6 us a round, are in nobody's shadow. So P has columns of its
+// own: S of the next keys is computed as soon as the softmax warps hold this one in registers. For d = 128 that leaves
+// 80 keys a tile (S 80, P 40 of a tile's 128 columns beside O), for d = 64 128 keys (O 64, S 128, P 64 of 256).
+// Weights are rounded to bf16 (2^-8 relative at most, as the values that they meet); maxima, sums and outputs are fp32, the
+// sum of the unrounded weights.
 //
 // A weight of zero does not hide a value that is not finite (0 * inf = NaN). In the tiles that some rows see only in part
-// warp 19 replaces such values by zero and keeps, for each column, the first key that held a NaN, +inf and -inf: rows that
+// warp 15 replaces such values by zero and keeps, for each column, the first key that held a NaN, +inf and -inf: rows that
 // see it get that value in their results, the others are left alone.
 #include "attn_tc.cuh"
 #include "kernels.h"
@@ -31,20 +36,28 @@
 namespace eagle {
 namespace {
 
-constexpr int AT = 128;              // keys a tile, query vectors a tile
-constexpr int AP_SOFT = 16;          // softmax warps, eight a tile
-constexpr int AP_THREADS = (AP_SOFT + 4) * 32;
+constexpr int AT = 128;              // query vectors a tile
+constexpr int AP_SOFT = 8;           // softmax warps, four a tile; behind them four that write results, then four single ones
+constexpr int AP_TMA = AP_SOFT + 4, AP_MMA = AP_TMA + 1, AP_LOOK = AP_TMA + 3;
+constexpr int AP_THREADS = (AP_SOFT + 8) * 32;
 constexpr float AP_LAZY = 8.f;       // binary orders that a maximum may pass its reference by
 constexpr uint32_t AP_NONE = 0x3fffffffu;      // three fields of ten bits, "no key"
 
 template <int D>
 struct ApShape {
-  static constexpr int HALVES = D / 64, HALF = AT * 128;        // 64 dims of 128 rows
-  static constexpr int OP = HALVES * HALF;                      // one operand tile
-  static constexpr int STAGES = D == 128 ? 5 : 8;
-  static constexpr int OFF_RING = 2 * OP, OFF_BAR = OFF_RING + STAGES * OP;
-  static constexpr int OFF_ITEM = OFF_BAR + 400, OFF_BAD = OFF_ITEM + 2 * 48;
-  static constexpr int BYTES = 1024 + OFF_BAD + 2 * D * 4;
+  static constexpr int KT = D == 128 ? 80 : 128;                          // keys a tile
+  static constexpr int HALVES = D / 64, QHALF = AT * 128, KHALF = KT * 128;   // 64 dims of all rows
+  static constexpr int QB = HALVES * QHALF, KB = HALVES * KHALF;          // a tile of Q, of K or V
+  static constexpr int STAGES = 8;
+  static constexpr int OFF_RING = 2 * QB, OFF_BAR = OFF_RING + STAGES * KB;
+  static constexpr int OFF_ITEM = OFF_BAR + 448, OFF_BAD = OFF_ITEM + 2 * 32, OFF_INV = OFF_BAD + 2 * D * 4;
+  static constexpr int BYTES = OFF_INV + 2 * AT * 4;
+  // TMEM columns: O of both tiles, then S and P of each
+  static constexpr int T_S = 2 * D, T_P = T_S + KT, T_STEP = (512 - 2 * D) / 2;
+  static_assert(KT + KT / 2 <= T_STEP, "S and P of a tile beside O");
+  // registers a thread of the softmax warps, the result warps, the single ones: together those of the launch, 128 each
+  static constexpr int R_SOFT = D == 128 ? 152 : 176, R_OUT = D == 128 ? 144 : 104, R_ONE = D == 128 ? 64 : 56;
+  static_assert(2 * R_SOFT + R_OUT + R_ONE <= 4 * 128, "registers of the launch");
 };
 
 // What a CTA does next. lim0: the last key that the first row sees (negative: none); rows of tile 0 and 1; key tiles of each.
@@ -70,7 +83,7 @@ __device__ __forceinline__ ApSeq ap_seq(const ApArgs& a, int b, bool& bad) {
   return bad ? ApSeq{0, 0, 0, 0} : ApSeq{r0, r1 - r0, k0, k1 - k0};
 }
 
-// The items' order. Pair t of a sequence has level t + (off >> log2 of a pair's positions): about its number of key tiles.
+// The items' order. Pair t of a sequence has level t + off / (a pair's positions): proportional to its keys, nearly.
 // Items go by falling level, then sequence, then head: the last ones are the short ones, so the CTAs end together.
 struct ApList {
   int level, above, upto;      // pairs of higher levels, of this and higher ones
@@ -107,6 +120,7 @@ __device__ __forceinline__ ApList ap_begin(const ApArgs& a, bool latch) {
   return l;
 }
 // Item i; h = -1 behind the last one. i rises from call to call.
+template <int KT>
 __device__ __forceinline__ ApItem ap_item(const ApArgs& a, ApList& l, long long i) {
   ApItem it{};
   it.h = -1;
@@ -143,7 +157,7 @@ __device__ __forceinline__ ApItem ap_item(const ApArgs& a, ApList& l, long long 
 #pragma unroll
     for (int y = 0; y < 2; ++y) {
       const int last = x.lim0 + y * a.RB + x.rows[y] - 1;      // (a sequence's last row sees its last key, none further)
-      x.n[y] = x.rows[y] > 0 && last >= 0 ? last / AT + 1 : 0;
+      x.n[y] = x.rows[y] > 0 && last >= 0 ? last / KT + 1 : 0;
     }
     it.h = __shfl_sync(0xffffffffu, x.h, src);
     it.row0 = __shfl_sync(0xffffffffu, x.row0, src);
@@ -160,9 +174,18 @@ __device__ __forceinline__ ApItem ap_item(const ApArgs& a, ApList& l, long long 
 }
 
 // Whether key tile j holds keys that a row of the tiles that use it does not see, and the last one that all of them see.
+template <int KT>
 __device__ __forceinline__ bool ap_partial(const ApItem& it, int RB, int j, int& seen) {
   seen = j < it.n[0] ? it.lim0 : it.lim0 + RB;
-  return j * AT + AT - 1 > seen;
+  return j * KT + KT - 1 > seen;
+}
+
+// Bounded waits of a converged warp that go on at once when the phase is over.
+__device__ __forceinline__ bool ap_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err) {
+  return __all_sync(0xffffffffu, mbar_try(bar, parity)) || kv8_wait(bar, parity, abort_flag, err);
+}
+__device__ __forceinline__ bool ap_wait_one(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err) {
+  return __all_sync(0xffffffffu, mbar_try(bar, parity)) || kv8_wait_all(bar, parity, abort_flag, err);
 }
 
 __device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
@@ -171,6 +194,25 @@ __device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
   return r;
 }
 
+// 16 columns of this warp's lanes; the values are there after tmem_wait_ld_n.
+__device__ __forceinline__ void tmem_ld16_async(uint32_t t, float* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+      : "r"(t));
+}
+template <int N>
+__device__ __forceinline__ void tmem_wait_ld_n(float* v) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i]));
+}
+__device__ __forceinline__ void tmem_st8u(uint32_t t, const uint32_t* v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(t), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
 // A warp's 16 lanes of TMEM as fragments: thread t gets of row t / 4 and of row t / 4 + 8 the columns 2 (t % 4) and one more of
 // every eight (v[4 i .. 4 i + 3]: the two of the first row, the two of the second).
 __device__ __forceinline__ void frag_ld64(uint32_t t, float* v) {      // 64 columns
@@ -182,19 +224,6 @@ __device__ __forceinline__ void frag_ld64(uint32_t t, float* v) {      // 64 col
         "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
         "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
       : "r"(t));
-}
-// 64 bf16 a row as 32 columns of pairs: w[2 i] of the first row, w[2 i + 1] of the second, in frag_ld64's order.
-__device__ __forceinline__ void frag_st_pairs(uint32_t t, const uint32_t* w) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(t),
-      "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]), "r"(w[8]), "r"(w[9]),
-      "r"(w[10]), "r"(w[11]), "r"(w[12]), "r"(w[13]), "r"(w[14]), "r"(w[15])
-      : "memory");
-}
-// The maximum over the four threads that share a row.
-__device__ __forceinline__ float quad_max(float x) {
-  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-  return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
 }
 __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
@@ -217,7 +246,7 @@ __device__ __forceinline__ void quad_transpose(uint32_t* w, int q) {
   }
 }
 
-// Values that are not finite in rows [r0, 128) of a value tile (16-byte pieces, 128-byte swizzle): replaced by zero, the
+// Values that are not finite in rows from r0 on of a value tile (16-byte pieces, 128-byte swizzle): replaced by zero, the
 // first key (of those after the first row's last, 0: seen by all) kept for each column. By a converged warp.
 template <int D>
 __device__ __forceinline__ bool ap_clean(uint8_t* v, int r0, int key0, int lim0, uint32_t* bad, bool fresh) {
@@ -229,8 +258,8 @@ __device__ __forceinline__ bool ap_clean(uint8_t* v, int r0, int key0, int lim0,
 #pragma unroll 1
   for (int x = 0; x < Sh::HALVES; ++x)
 #pragma unroll 4
-    for (int i = r0 * 8 + lane; i < AT * 8; i += 32) {
-      const uint4 w = *reinterpret_cast<const uint4*>(v + x * Sh::HALF + i * 16);
+    for (int i = r0 * 8 + lane; i < Sh::KT * 8; i += 32) {
+      const uint4 w = *reinterpret_cast<const uint4*>(v + x * Sh::KHALF + i * 16);
       const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
       for (int y = 0; y < 4; ++y) acc = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&u[y]), zero, acc);   // inf * 0 = NaN
@@ -244,9 +273,9 @@ __device__ __forceinline__ bool ap_clean(uint8_t* v, int r0, int key0, int lim0,
 #pragma unroll 1
   for (int x = 0; x < Sh::HALVES; ++x)
 #pragma unroll 1
-    for (int i = r0 * 8 + lane; i < AT * 8; i += 32) {
+    for (int i = r0 * 8 + lane; i < Sh::KT * 8; i += 32) {
       const int row = i >> 3, piece = (i & 7) ^ (row & 7);
-      __nv_bfloat16* p = reinterpret_cast<__nv_bfloat16*>(v + x * Sh::HALF + i * 16);
+      __nv_bfloat16* p = reinterpret_cast<__nv_bfloat16*>(v + x * Sh::KHALF + i * 16);
       const int rel = max(0, key0 + row - lim0);
 #pragma unroll 1
       for (int y = 0; y < 8; ++y) {
@@ -273,19 +302,20 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
     prompt_k(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
              const __grid_constant__ CUtensorMap tmV, const ApArgs a) {
   using Sh = ApShape<D>;
-  constexpr int ST = Sh::STAGES;
-  extern __shared__ uint8_t ap_smem[];
-  uint8_t* sm = ap_smem + (-smem_u32(ap_smem) & 1023u);
+  constexpr int ST = Sh::STAGES, KT = Sh::KT;
+  extern __shared__ __align__(1024) uint8_t sm[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + Sh::OFF_BAR);
-  uint64_t *full = bars, *empty = bars + ST /* ring */, *q_full = bars + 2 * ST /* [tile] */, *q_empty = q_full + 2,
-           *s_full = q_full + 4 /* [tile] */, *p_full = q_full + 6 /* [tile][half] */, *o_done = q_full + 10 /* [tile] */,
-           *o_free = q_full + 12 /* [tile] */, *item_full = q_full + 14 /* [slot] */, *item_empty = q_full + 16 /* [slot] */,
-           *drain = q_full + 18 /* [tile] */, *turn = q_full + 20 /* [tile] */, *looked = q_full + 22 /* ring */;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(looked + ST);
+  uint64_t *full = bars, *empty = bars + ST, *looked = bars + 2 * ST /* ring */, *q_full = bars + 3 * ST /* [tile] */,
+           *q_empty = q_full + 2 /* [tile] */, *s_full = q_full + 4 /* [tile] */, *s_free = q_full + 6 /* [tile] */,
+           *p_full = q_full + 8 /* [tile] */, *p_free = q_full + 10 /* [tile] */, *o_done = q_full + 12 /* [tile] */,
+           *o_free = q_full + 14 /* [tile] */, *l_full = q_full + 16 /* [tile] */, *l_free = q_full + 18 /* [tile] */,
+           *item_full = q_full + 20 /* [slot] */, *item_empty = q_full + 22 /* [slot] */, *drain = q_full + 24 /* [tile] */;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(q_full + 26);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* has_bad = abort_flag + 1;      // [slot]
   ApItem* items = reinterpret_cast<ApItem*>(sm + Sh::OFF_ITEM);
   uint32_t* bad = reinterpret_cast<uint32_t*>(sm + Sh::OFF_BAD);      // [slot][D]
+  float* inv = reinterpret_cast<float*>(sm + Sh::OFF_INV);            // [tile][query vector]: 1 / sum of the weights
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
     for (int i = 0; i < ST; ++i) {
@@ -297,218 +327,229 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
       mbar_init(smem_u32(q_full + i), 1);
       mbar_init(smem_u32(q_empty + i), 1);
       mbar_init(smem_u32(s_full + i), 1);
-      mbar_init(smem_u32(p_full + 2 * i), AP_SOFT / 2);
-      mbar_init(smem_u32(p_full + 2 * i + 1), AP_SOFT / 2);
+      mbar_init(smem_u32(s_free + i), 4);
+      mbar_init(smem_u32(p_full + i), 4);
+      mbar_init(smem_u32(p_free + i), 1);
       mbar_init(smem_u32(o_done + i), 1);
-      mbar_init(smem_u32(o_free + i), AP_SOFT / 2);
-      mbar_init(smem_u32(turn + i), 1);
+      mbar_init(smem_u32(o_free + i), 4);
+      mbar_init(smem_u32(l_full + i), 4);
+      mbar_init(smem_u32(l_free + i), 4);
       mbar_init(smem_u32(item_full + i), 1);
-      mbar_init(smem_u32(item_empty + i), AP_SOFT + 3);
+      mbar_init(smem_u32(item_empty + i), AP_SOFT + 4 + 3);
       mbar_init(smem_u32(drain + i), 1);
       has_bad[i] = 0;
     }
     *abort_flag = 0;
     fence_mbar_init();
-    mbar_arrive(smem_u32(turn));      // tile 0 begins
   }
-  if (warp == AP_SOFT + 1) tmem_alloc(smem_u32(tmem_slot), 512);
+  if (warp == AP_MMA) tmem_alloc(smem_u32(tmem_slot), 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   PDL_ENTRY();
 
+  // Phases: a waiter passes every phase of a barrier that it waits on, in order, and no phase can end twice before its waiters
+  // have passed it: what ends it next comes behind something that they do after. (Waits that depend on the case, `looked`,
+  // come behind one that vouches for the phase before.)
   if (warp < AP_SOFT) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
-    // a warp has 16 rows of its tile, of its own quarter of the TMEM lanes: threads 4 r .. 4 r + 3 rows r and r + 8
-    const int mt = warp >> 3, quad = threadIdx.x & 3, lane0 = (warp & 3) * 32 + (warp >> 2 & 1) * 16;
-    const int qv = lane0 + ((threadIdx.x & 31) >> 2);
-    const uint32_t tS = tmem + mt * AT + ((uint32_t)lane0 << 16), tO = tmem + 2 * AT + mt * D + ((uint32_t)lane0 << 16);
-    int pos[2], g[2];
-#pragma unroll
-    for (int y = 0; y < 2; ++y) {
-      pos[y] = (qv + 8 * y) / a.G;
-      g[y] = qv + 8 * y - pos[y] * a.G;
-    }
-    uint32_t s_phase = 0, o_phase = 0;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Sh::R_SOFT));
+    const int mt = warp >> 2, qv = threadIdx.x & 127;
+    const int pos = qv / a.G, low = ((warp & 3) * 32) / a.G;      // this thread's position in the tile, its warp's first
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + Sh::T_S + mt * Sh::T_STEP + lane_off, tP = tS + KT, tO = tmem + mt * D + lane_off;
+    uint32_t s_phase = 0, p_phase = 1, l_phase = 1;      // (1: a barrier's first wait passes, nobody holds what it guards)
     bool ok = true;
     for (int n = 0; ok; ++n) {
-      ok = kv8_wait(smem_u32(item_full + (n & 1)), (uint32_t)((n >> 1) & 1), abort_flag, a.err);
+      ok = ap_wait(smem_u32(item_full + (n & 1)), (uint32_t)((n >> 1) & 1), abort_flag, a.err);
       if (!ok) break;
       const ApItem& it = items[n & 1];
       if (it.h < 0) break;
       const int nt = it.n[mt], first = it.lim0 + mt * a.RB;      // the last key that the tile's first row sees
-      float m2[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};      // l: this thread's part
+      float m2 = -INFINITY, l = 0.f;
       for (int j = 0; j < nt; ++j) {
-        ok = kv8_wait(smem_u32(s_full + mt), s_phase, abort_flag, a.err);
+        ok = ap_wait(smem_u32(s_full + mt), s_phase, abort_flag, a.err);
         if (!ok) break;
         s_phase ^= 1;
         tc_fence_after();
-        float s[64];
-        frag_ld64(tS, s);
-        tmem_wait_ld(s);
-        frag_ld64(tS + 64, s + 32);
-        const bool partial = j * AT + AT - 1 > first;      // some row of the tile does not see all of these keys
-        float mx[2];
+        float s[KT];
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {      // (the second half arrives under the first one's maximum)
-          if (hf) tmem_wait_ld(s + 32);
-          if (partial) {
+        for (int c = 0; c < KT / 32 * 32; c += 32) tmem_ld32_async(tS + c, s + c);
+        if constexpr (KT % 32) tmem_ld16_async(tS + KT - 16, s + KT - 16);
+        tmem_wait_ld_n<KT>(s);
+        tc_fence_before();
+        warp_arrive(smem_u32(s_free + mt));      // S of the next keys may come
+        const int last = first + pos - j * KT, all = first + low - j * KT;      // last keys seen by this row, by all of the warp's
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              const int last = first + pos[y] - j * AT - hf * 64 - 2 * quad;
+        for (int c0 = 0; c0 < KT; c0 += 16)
+          if (c0 + 15 > all)
 #pragma unroll
-              for (int c = 0; c < 8; ++c) {
-                s[hf * 32 + 4 * c + 2 * y] = 8 * c <= last ? s[hf * 32 + 4 * c + 2 * y] : -INFINITY;
-                s[hf * 32 + 4 * c + 2 * y + 1] = 8 * c + 1 <= last ? s[hf * 32 + 4 * c + 2 * y + 1] : -INFINITY;
-              }
-            }
-          }
+            for (int c = c0; c < c0 + 16; ++c) s[c] = c <= last ? s[c] : -INFINITY;
+        float x0 = fmaxf(s[0], s[1]), x1 = fmaxf(s[2], s[3]), x2 = fmaxf(s[4], s[5]), x3 = fmaxf(s[6], s[7]);
 #pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            const float* x = s + hf * 32 + 2 * y;
-            float x0 = hf ? max3(mx[y], x[0], x[1]) : fmaxf(x[0], x[1]), x1 = fmaxf(x[4], x[5]);
-#pragma unroll
-            for (int c = 2; c < 8; c += 2) {
-              x0 = max3(x0, x[4 * c], x[4 * c + 1]);
-              x1 = max3(x1, x[4 * c + 4], x[4 * c + 5]);
-            }
-            mx[y] = fmaxf(x0, x1);
-          }
+        for (int c = 8; c < KT; c += 8) {
+          x0 = max3(x0, s[c], s[c + 1]);
+          x1 = max3(x1, s[c + 2], s[c + 3]);
+          x2 = max3(x2, s[c + 4], s[c + 5]);
+          x3 = max3(x3, s[c + 6], s[c + 7]);
         }
-        float corr[2] = {1.f, 1.f};
-        bool raise = false;
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          mx[y] = quad_max(mx[y]) * a.sl2;
-          if (mx[y] > m2[y] + AP_LAZY) {
-            corr[y] = pf_ex2(m2[y] - mx[y]);
-            m2[y] = mx[y];
-            l[y] *= corr[y];
-            raise = true;
-          }
+        const float mx = fmaxf(max3(x0, x1, x2), x3) * a.sl2;
+        const bool raise = mx > m2 + AP_LAZY;
+        float corr = 1.f;
+        if (raise) {
+          corr = pf_ex2(m2 - mx);
+          m2 = mx;
+          l *= corr;
         }
-        // (this S came behind the product into O before it, so O is there)
+        // the product into O before this one is done: P may be written, and O rescaled
+        ok = ap_wait(smem_u32(p_free + mt), p_phase, abort_flag, a.err);
+        if (!ok) break;
+        p_phase ^= 1;
+        tc_fence_after();
         if (j > 0 && __any_sync(0xffffffffu, raise)) {
 #pragma unroll 1
           for (int c = 0; c < D; c += 16) {
-            float o[8];
-            asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                         : "=f"(o[0]), "=f"(o[1]), "=f"(o[2]), "=f"(o[3]), "=f"(o[4]), "=f"(o[5]), "=f"(o[6]), "=f"(o[7])
-                         : "r"(tO + c));
-            asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+            float o[16];
+            tmem_ld16(tO + c, o);
 #pragma unroll
-            for (int x = 0; x < 8; ++x) {
-              asm volatile("" : "+f"(o[x]));
-              o[x] *= corr[x >> 1 & 1];
-            }
-            asm volatile("tcgen05.st.sync.aligned.16x256b.x2.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(tO + c), "f"(o[0]),
-                         "f"(o[1]), "f"(o[2]), "f"(o[3]), "f"(o[4]), "f"(o[5]), "f"(o[6]), "f"(o[7])
-                         : "memory");
+            for (int x = 0; x < 16; ++x) o[x] *= corr;
+            tmem_st16(tO + c, o);
           }
         }
         // One rounding of the reference for the whole row, then one of each difference: near the maximum, where weights
         // count, that is exact whatever the size of the scores.
-        f32x2 nm[2], sum[2];
-        const f32x2 s2 = two(a.sl2, a.sl2);
+        const float ref = m2 == -INFINITY ? 0.f : m2;
+        const f32x2 nm = two(-ref, -ref), s2 = two(a.sl2, a.sl2);
+        f32x2 sum[2] = {two(0.f, 0.f), two(0.f, 0.f)};
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          const float ref = m2[y] == -INFINITY ? 0.f : m2[y];
-          nm[y] = two(-ref, -ref);
-          sum[y] = two(0.f, 0.f);
-        }
+        for (int c0 = 0; c0 < KT; c0 += 16) {
+          uint32_t w[8];
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          uint32_t w[16];
-#pragma unroll
-          for (int c = 0; c < 16; ++c) {      // 2 c': first row, 2 c' + 1: second row
-            const float* x = s + hf * 32 + 2 * c;
-            float2 e = one_by_one(fma2(two(x[0], x[1]), s2, nm[c & 1]));
-            e.x = pf_ex2(e.x);
-            e.y = pf_ex2(e.y);
-            sum[c & 1] = add2(sum[c & 1], two(e.x, e.y));
-            w[c] = bf16_pair(e.x, e.y);
+          for (int c = 0; c < 16; c += 2) {
+            float2 x = one_by_one(fma2(two(s[c0 + c], s[c0 + c + 1]), s2, nm));
+            x.x = pf_ex2(x.x);
+            x.y = pf_ex2(x.y);
+            sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], two(x.x, x.y));
+            w[c / 2] = bf16_pair(x.x, x.y);
           }
-          frag_st_pairs(tS + hf * 32, w);
-          tmem_wait_st();
-          tc_fence_before();
-          warp_arrive(smem_u32(p_full + 2 * mt + hf));
+          tmem_st8u(tP + c0 / 2, w);
         }
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          const float2 sums = one_by_one(sum[y]);
-          l[y] += sums.x + sums.y;
-        }
+        tmem_wait_st();
+        tc_fence_before();
+        warp_arrive(smem_u32(p_full + mt));
+        const float2 sums = one_by_one(add2(sum[0], sum[1]));
+        l += sums.x + sums.y;
       }
       if (!ok) break;
       if (it.rows[mt] > 0) {
-        float inv[2];
-        __nv_bfloat16* dst[2];
-        bool write[2];
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          l[y] += __shfl_xor_sync(0xffffffffu, l[y], 1);
-          l[y] += __shfl_xor_sync(0xffffffffu, l[y], 2);
-          const int row = it.row0 + mt * a.RB + pos[y], head = it.h * a.G + g[y];
-          write[y] = pos[y] < it.rows[mt];      // (so pos < RB: not the vectors behind the last head)
-          dst[y] = a.out + (long long)row * a.ldo + (long long)head * D;
-          inv[y] = l[y] == 0.f ? 0.f : 1.f / l[y];
-          if (write[y] && a.lse && quad == 0) {
-            const float ref = m2[y] == -INFINITY ? 0.f : m2[y];
-            a.lse[(long long)row * a.nq + head] = l[y] == 0.f ? -INFINITY : (ref + log2f(l[y])) * 0.693147180559945309f;
-          }
+        if (pos < it.rows[mt] && a.lse) {      // (so pos < RB: not the vectors behind the last head)
+          const float ref = m2 == -INFINITY ? 0.f : m2;
+          a.lse[(long long)(it.row0 + mt * a.RB + pos) * a.nq + it.h * a.G + qv - pos * a.G] =
+              l == 0.f ? -INFINITY : (ref + log2f(l)) * 0.693147180559945309f;
         }
-        if (nt == 0) {      // rows that see no key
-#pragma unroll
-          for (int y = 0; y < 2; ++y)
-            if (write[y])
-              for (int c = quad * 8; c < D; c += 32) *reinterpret_cast<uint4*>(dst[y] + c) = make_uint4(0, 0, 0, 0);
-        } else {
-          ok = kv8_wait(smem_u32(o_done + mt), o_phase, abort_flag, a.err);
+        if (nt) {
+          ok = ap_wait(smem_u32(l_free + mt), l_phase, abort_flag, a.err);
           if (!ok) break;
-          o_phase ^= 1;
-          tc_fence_after();
-          const bool poisoned = has_bad[n & 1] != 0;
-#pragma unroll 1
-          for (int c = 0; c < D; c += 64) {
-            float o[32];
-            frag_ld64(tO + c, o);
-            tmem_wait_ld(o);
-            if (c + 64 == D) {      // O is read: the next item's products may begin
-              tc_fence_before();
-              warp_arrive(smem_u32(o_free + mt));
-            }
-#pragma unroll
-            for (int x = 0; x < 32; ++x) o[x] *= inv[x >> 1 & 1];
-            if (poisoned) {
-              const uint32_t* from = bad + (n & 1) * D + c + 2 * quad;
-#pragma unroll
-              for (int x = 0; x < 32; ++x) {
-                const uint32_t w = from[(x >> 2) * 8 + (x & 1)];
-                const int i = mt * a.RB + pos[x >> 1 & 1];
-                const bool nan = i >= (int)(w & 1023), up = i >= (int)((w >> 10) & 1023), down = i >= (int)((w >> 20) & 1023);
-                if (nan || up || down) o[x] = nan || (up && down) ? __int_as_float(0x7fffffff) : up ? o[x] + INFINITY : o[x] - INFINITY;
-              }
-            }
-            // a thread gets whole 16-byte pieces: the four of a row write 64 bytes in one go
-#pragma unroll
-            for (int y = 0; y < 2; ++y)
-#pragma unroll
-              for (int x = 0; x < 2; ++x) {
-                uint32_t w[4];
-#pragma unroll
-                for (int z = 0; z < 4; ++z) w[z] = bf16_pair(o[(x * 4 + z) * 4 + 2 * y], o[(x * 4 + z) * 4 + 2 * y + 1]);
-                quad_transpose(w, quad);
-                if (write[y]) *reinterpret_cast<uint4*>(dst[y] + c + x * 32 + quad * 8) = make_uint4(w[0], w[1], w[2], w[3]);
-              }
-          }
+          l_phase ^= 1;
+          inv[mt * AT + qv] = l == 0.f ? 0.f : 1.f / l;
+          warp_arrive(smem_u32(l_full + mt));
         }
       }
       warp_arrive(smem_u32(item_empty + (n & 1)));
     }
+  } else if (warp < AP_TMA) {
+    // ---- results: both tiles' in turn, a quarter of the lanes a warp, while the softmax warps are at the next item ----
+    if constexpr (Sh::R_OUT > 128) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Sh::R_OUT));
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Sh::R_OUT));
+    const int lane = threadIdx.x & 31, quad = lane & 3, lane0 = (warp & 3) * 32;
+    // position and head (of the tile, of the group) of the four query vectors of this thread's fragments
+    uint32_t at[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const int v = lane0 + x * 8 + (lane >> 2);
+      at[x] = (uint32_t)(v / a.G) << 16 | (uint32_t)(v % a.G);
+    }
+    uint32_t phase = 0;      // a bit a tile
+    bool ok = true;
+    for (int n = 0; ok; ++n) {
+      ok = ap_wait(smem_u32(item_full + (n & 1)), (uint32_t)((n >> 1) & 1), abort_flag, a.err);
+      if (!ok) break;
+      const ApItem& it = items[n & 1];
+      if (it.h < 0) break;
+#pragma unroll 1
+      for (int mt = 0; mt < 2; ++mt) {
+        const int rows = it.rows[mt], nt = it.n[mt];
+        if (rows <= 0) continue;
+        __nv_bfloat16* base = a.out + (long long)(it.row0 + mt * a.RB) * a.ldo + (long long)it.h * a.G * D;
+        // fragments of 16 rows, four threads a row; O leaves TMEM before anything is written, the next item's products wait
+        uint32_t w[D / 2];
+        if (nt) {
+          ok = ap_wait(smem_u32(l_full + mt), phase >> mt & 1, abort_flag, a.err) &&
+               ap_wait(smem_u32(o_done + mt), phase >> mt & 1, abort_flag, a.err);
+          if (!ok) break;
+          phase ^= 1u << mt;
+          tc_fence_after();
+          float part[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) part[x] = inv[mt * AT + lane0 + x * 8 + (lane >> 2)];
+#pragma unroll
+          for (int f = 0; f < 2; ++f)
+#pragma unroll
+            for (int c = 0; c < D; c += 64) {
+              float o[32];
+              frag_ld64(tmem + ((uint32_t)(lane0 + f * 16) << 16) + mt * D + c, o);
+              tmem_wait_ld(o);
+#pragma unroll
+              for (int x = 0; x < 16; ++x)
+                w[f * (D / 4) + c / 4 + x] = bf16_pair(o[2 * x] * part[2 * f + (x & 1)], o[2 * x + 1] * part[2 * f + (x & 1)]);
+            }
+          tc_fence_before();
+          warp_arrive(smem_u32(o_free + mt));
+          warp_arrive(smem_u32(l_free + mt));
+        } else {      // rows that see no key
+#pragma unroll
+          for (int x = 0; x < D / 2; ++x) w[x] = 0;
+        }
+        // a row's 64 bytes go out together
+#pragma unroll
+        for (int f = 0; f < 2; ++f)
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const int p = at[2 * f + y] >> 16;
+            __nv_bfloat16* dst = base + (long long)p * a.ldo + (int)(at[2 * f + y] & 0xffff) * D + quad * 8;
+#pragma unroll
+            for (int x = 0; x < D / 32; ++x) {
+              uint32_t z[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) z[i] = w[f * (D / 4) + (x * 4 + i) * 2 + y];
+              quad_transpose(z, quad);
+              if (p < rows)      // (so p < RB: not the vectors behind the last head)
+                *reinterpret_cast<uint4*>(dst + x * 32) = make_uint4(z[0], z[1], z[2], z[3]);
+            }
+          }
+        if (nt && has_bad[n & 1]) {      // (rare: over what this warp has just written, a row a thread)
+          __syncwarp();
+          const int p = (lane0 + lane) / a.G, i = mt * a.RB + p;
+          if (p < rows) {
+            __nv_bfloat16* o = base + (long long)p * a.ldo + (lane0 + lane - p * a.G) * D;
+#pragma unroll 1
+            for (int c = 0; c < D; ++c) {
+              const uint32_t x = bad[(n & 1) * D + c];
+              float add = 0.f;
+              if (i >= (int)((x >> 10) & 1023)) add += INFINITY;
+              if (i >= (int)((x >> 20) & 1023)) add -= INFINITY;      // (both: NaN)
+              if (i >= (int)(x & 1023)) add = __int_as_float(0x7fffffff);
+              if (add != 0.f) o[c] = __float2bfloat16_rn(__bfloat162float(o[c]) + add);
+            }
+          }
+        }
+      }
+      if (ok) warp_arrive(smem_u32(item_empty + (n & 1)));
+    }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-    if (warp == AP_SOFT) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Sh::R_ONE));
+    // The ring's order of an item of n key tiles: K 0, then K j + 1 and V j for j = 0 .. n - 1 (no K n).
+    if (warp == AP_TMA) {
       // ---- items, TMA ----
       ApList list = ap_begin(a, blockIdx.x == 0);
       const uint32_t qbytes = (uint32_t)(a.RB * a.G * 128);
@@ -517,11 +558,11 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
       // K or V tile j into the ring's next stage
       auto load = [&](const CUtensorMap* map, const ApItem& it, int j) {
         const int st = s % ST;
-        if (s >= ST && !kv8_wait_all(smem_u32(empty + st), (uint32_t)((s / ST - 1) & 1), abort_flag, a.err)) return false;
+        if (s >= ST && !ap_wait_one(smem_u32(empty + st), (uint32_t)((s / ST - 1) & 1), abort_flag, a.err)) return false;
         if (elect_one()) {
-          mbar_expect_tx(smem_u32(full + st), Sh::OP);
+          mbar_expect_tx(smem_u32(full + st), Sh::KB);
           for (int x = 0; x < Sh::HALVES; ++x)
-            tma_load_3d(smem_u32(sm + Sh::OFF_RING + st * Sh::OP + x * Sh::HALF), map, x * 64, it.h, it.k0 + j * AT,
+            tma_load_3d(smem_u32(sm + Sh::OFF_RING + st * Sh::KB + x * Sh::KHALF), map, x * 64, it.h, it.k0 + j * KT,
                         smem_u32(full + st));
         }
         __syncwarp();
@@ -529,11 +570,11 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
         return true;
       };
       auto load_q = [&](const ApItem& it, int t) {
-        if (used[t] && !kv8_wait_all(smem_u32(q_empty + t), (uint32_t)((used[t] - 1) & 1), abort_flag, a.err)) return false;
+        if (used[t] && !ap_wait_one(smem_u32(q_empty + t), (uint32_t)((used[t] - 1) & 1), abort_flag, a.err)) return false;
         if (elect_one()) {
           mbar_expect_tx(smem_u32(q_full + t), Sh::HALVES * qbytes);
           for (int x = 0; x < Sh::HALVES; ++x)
-            tma_load_3d(smem_u32(sm + t * Sh::OP + x * Sh::HALF), &tmQ, x * 64, it.h * a.G, it.row0 + t * a.RB,
+            tma_load_3d(smem_u32(sm + t * Sh::QB + x * Sh::QHALF), &tmQ, x * 64, it.h * a.G, it.row0 + t * a.RB,
                         smem_u32(q_full + t));
         }
         __syncwarp();
@@ -542,9 +583,9 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
       };
       for (int n = 0; ok; ++n) {
         // to and fro over the CTAs: who takes the largest of one round takes the smallest of the next
-        const int turn = n & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
-        const ApItem it = ap_item(a, list, turn + (long long)n * gridDim.x);
-        if (n >= 2) ok = kv8_wait_all(smem_u32(item_empty + (n & 1)), (uint32_t)(((n >> 1) - 1) & 1), abort_flag, a.err);
+        const int at = n & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
+        const ApItem it = ap_item<KT>(a, list, at + (long long)n * gridDim.x);
+        if (n >= 2) ok = ap_wait_one(smem_u32(item_empty + (n & 1)), (uint32_t)(((n >> 1) - 1) & 1), abort_flag, a.err);
         if (!ok) break;
         if (elect_one()) {
           items[n & 1] = it;
@@ -559,8 +600,8 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
         ok = ok && load(&tmK, it, 0);
         if (it.n[1]) ok = ok && load_q(it, 1);
         for (int j = 0; ok && j < nt; ++j) {
-          ok = load(&tmV, it, j);
-          if (j + 1 < nt) ok = ok && load(&tmK, it, j + 1);
+          if (j + 1 < nt) ok = load(&tmK, it, j + 1);
+          ok = ok && load(&tmV, it, j);
         }
       }
       if (*abort_flag) {      // copies in flight land before the CTA leaves: the last ones of the ring and of Q
@@ -569,89 +610,92 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
         for (int x = max(0, s - ST); x < s; ++x)
           kv8_wait_all(smem_u32(full + x % ST), (uint32_t)((x / ST) & 1), abort_flag, a.err, false);
       }
-    } else if (warp < AP_SOFT + 3) {
+    } else if (warp < AP_LOOK) {
       // ---- MMA: one warp a query tile ----
-      constexpr uint32_t IS = pf_idesc(AT, false), IO = pf_idesc(D, true);
-      const int mt = warp - AP_SOFT - 1;
-      const uint32_t tS = tmem + mt * AT, tO = tmem + 2 * AT + mt * D;
+      constexpr uint32_t IS = pf_idesc(KT, false), IO = pf_idesc(D, true);
+      const int mt = warp - AP_MMA;
+      const uint32_t tS = tmem + Sh::T_S + mt * Sh::T_STEP, tP = tS + KT, tO = tmem + mt * D;
       // operand descriptors; an offset of n bytes adds n >> 4
-      const uint64_t dq = sdesc_sw128(smem_u32(sm + mt * Sh::OP)), dk = sdesc_sw128(smem_u32(sm + Sh::OFF_RING)),
-                     dv = pf_desc_mn(smem_u32(sm + Sh::OFF_RING), Sh::HALF);
-      int s = 0, used = 0;
-      uint32_t p_phase = 0, t_phase = 0;
+      const uint64_t dq = sdesc_sw128(smem_u32(sm + mt * Sh::QB)), dk = sdesc_sw128(smem_u32(sm + Sh::OFF_RING)),
+                     dv = pf_desc_mn(smem_u32(sm + Sh::OFF_RING), Sh::KHALF);
+      int s = 0, used = 0, units = 0;      // stages, items and key tiles with products of this tile so far
       bool ok = true;
-      auto wait_stage = [&](int x) { return kv8_wait_all(smem_u32(full + x % ST), (uint32_t)((x / ST) & 1), abort_flag, a.err); };
-      // (behind wait_stage: warp 19 has then passed the stage's use before, so this phase is the current one)
-      auto wait_looked = [&](int x) { return kv8_wait_all(smem_u32(looked + x % ST), (uint32_t)((x / ST) & 1), abort_flag, a.err); };
-      auto issue_s = [&](int x, bool last) {      // by one lane
-        const uint64_t k = dk + ((uint64_t)(x % ST) * Sh::OP >> 4);
+      auto wait_stage = [&](int x) { return ap_wait_one(smem_u32(full + x % ST), (uint32_t)((x / ST) & 1), abort_flag, a.err); };
+      auto give_back = [&](int x) {
+        if (elect_one()) mbar_arrive(smem_u32(empty + x % ST));
+        __syncwarp();
+      };
+      // S of the keys in stage x, once the softmax warps hold the S before
+      auto scores = [&](int x, bool last) {
+        if (!wait_stage(x)) return false;
+        if (units && !ap_wait_one(smem_u32(s_free + mt), (uint32_t)((units - 1) & 1), abort_flag, a.err)) return false;
+        ++units;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t k = dk + ((uint64_t)(x % ST) * Sh::KB >> 4);
 #pragma unroll
-        for (int y = 0; y < D / 16; ++y) {
-          const int at = ((y >> 2) * Sh::HALF + (y & 3) * 32) >> 4;
-          tc_mma_bf16(tS, dq + at, k + at, IS, y ? 1u : 0u);
+          for (int y = 0; y < D / 16; ++y)
+            tc_mma_bf16(tS, dq + (((y >> 2) * Sh::QHALF + (y & 3) * 32) >> 4), k + (((y >> 2) * Sh::KHALF + (y & 3) * 32) >> 4), IS,
+                        y ? 1u : 0u);
+          tc_commit(smem_u32(s_full + mt));
+          tc_commit(smem_u32(empty + x % ST));
+          if (last) tc_commit(smem_u32(q_empty + mt));
         }
-        tc_commit(smem_u32(s_full + mt));
-        tc_commit(smem_u32(empty + x % ST));
-        if (last) tc_commit(smem_u32(q_empty + mt));
+        __syncwarp();
+        return true;
       };
-      auto issue_o = [&](int x, int half, bool first) {      // by one lane
-        const uint64_t v = dv + ((uint64_t)(x % ST) * Sh::OP >> 4);
-#pragma unroll
-        for (int y = 0; y < 4; ++y)
-          mma_ts(tO, tS + (half * 4 + y) * 8, v + ((half * 4 + y) * 2048 >> 4), IO, first && !half && !y ? 0u : 1u);
-      };
+      uint32_t p_phase = 0;
       for (int n = 0; ok; ++n) {
-        ok = kv8_wait_all(smem_u32(item_full + (n & 1)), (uint32_t)((n >> 1) & 1), abort_flag, a.err);
+        ok = ap_wait_one(smem_u32(item_full + (n & 1)), (uint32_t)((n >> 1) & 1), abort_flag, a.err);
         if (!ok) break;
         const ApItem it = items[n & 1];
         if (it.h < 0) break;
         const int mine = it.n[mt], nt = max(it.n[0], it.n[1]);
-        if (mine) {
-          ok = kv8_wait_all(smem_u32(q_full + mt), (uint32_t)(used & 1), abort_flag, a.err) && wait_stage(s);
-          if (!ok) break;
-          tc_fence_after();
-          if (elect_one()) issue_s(s, mine == 1);
-          __syncwarp();
+        if (nt) {
+          if (mine) {
+            ok = ap_wait_one(smem_u32(q_full + mt), (uint32_t)(used & 1), abort_flag, a.err) && scores(s, mine == 1);
+          } else {
+            ok = wait_stage(s);
+            if (ok) give_back(s);
+          }
+          ++s;
         }
-        for (int j = 0; ok && j < nt; ++j, s += 2) {      // stages s: K of this tile, s + 1: V
-          int seen;
-          const bool partial = ap_partial(it, a.RB, j, seen);
-          if (j >= mine) {      // the other tile's keys alone
-            ok = wait_stage(s) && wait_stage(s + 1) && kv8_wait_all(smem_u32(turn + mt), t_phase, abort_flag, a.err);
-            t_phase ^= 1;
-            if (!ok) break;
-            if (elect_one()) {
-              mbar_arrive(smem_u32(turn + (mt ^ 1)));
-              mbar_arrive(smem_u32(empty + s % ST));
-              mbar_arrive(smem_u32(empty + (s + 1) % ST));
+        for (int j = 0; ok && j < nt; ++j) {
+          if (j + 1 < nt) {
+            if (j + 1 < mine) {
+              ok = scores(s, j + 2 == mine);
+            } else {      // the other tile's keys alone
+              ok = wait_stage(s);
+              if (ok) give_back(s);
             }
-            __syncwarp();
+            if (!ok) break;
+            ++s;
+          }
+          ok = wait_stage(s);
+          if (!ok) break;
+          if (j >= mine) {
+            give_back(s++);
             continue;
           }
-          const bool next = j + 1 < mine;
-          ok = wait_stage(s + 1);
-          if (ok && partial) ok = wait_looked(s + 1);
-          if (ok && next) ok = wait_stage(s + 2);
-          if (ok && j == 0 && used) ok = kv8_wait_all(smem_u32(o_free + mt), (uint32_t)((used - 1) & 1), abort_flag, a.err);
-          ok = ok && kv8_wait_all(smem_u32(p_full + 2 * mt), p_phase, abort_flag, a.err) &&
-               kv8_wait_all(smem_u32(turn + mt), t_phase, abort_flag, a.err);
-          t_phase ^= 1;
+          int seen;
+          if (ap_partial<KT>(it, a.RB, j, seen))      // (behind wait_stage: warp 15 has passed the stage's use before)
+            ok = ap_wait_one(smem_u32(looked + s % ST), (uint32_t)((s / ST) & 1), abort_flag, a.err);
+          if (ok && j == 0 && used) ok = ap_wait_one(smem_u32(o_free + mt), (uint32_t)((used - 1) & 1), abort_flag, a.err);
+          ok = ok && ap_wait_one(smem_u32(p_full + mt), p_phase, abort_flag, a.err);
           if (!ok) break;
-          tc_fence_after();
-          if (elect_one()) issue_o(s + 1, 0, j == 0);
-          __syncwarp();
-          ok = kv8_wait_all(smem_u32(p_full + 2 * mt + 1), p_phase, abort_flag, a.err);
           p_phase ^= 1;
-          if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
-            issue_o(s + 1, 1, false);
-            tc_commit(smem_u32(empty + (s + 1) % ST));
-            if (next) issue_s(s + 2, j + 2 == mine);
-            else tc_commit(smem_u32(o_done + mt));
-            mbar_arrive(smem_u32(turn + (mt ^ 1)));
+            const uint64_t v = dv + ((uint64_t)(s % ST) * Sh::KB >> 4);
+#pragma unroll
+            for (int y = 0; y < KT / 16; ++y)      // 16 keys a product
+              mma_ts(tO, tP + y * 8, v + (y * 2048 >> 4), IO, j || y ? 1u : 0u);
+            tc_commit(smem_u32(p_free + mt));
+            tc_commit(smem_u32(empty + s % ST));
+            if (j + 1 == mine) tc_commit(smem_u32(o_done + mt));
           }
           __syncwarp();
+          ++s;
         }
         if (mine) ++used;
         if (ok && elect_one()) mbar_arrive(smem_u32(item_empty + (n & 1)));
@@ -667,33 +711,32 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
       int s = 0;
       bool ok = true;
       for (int n = 0; ok; ++n) {
-        ok = kv8_wait_all(smem_u32(item_full + (n & 1)), (uint32_t)((n >> 1) & 1), abort_flag, a.err);
+        ok = ap_wait_one(smem_u32(item_full + (n & 1)), (uint32_t)((n >> 1) & 1), abort_flag, a.err);
         if (!ok) break;
         const ApItem it = items[n & 1];
         if (it.h < 0) break;
         const int nt = max(it.n[0], it.n[1]);
         bool found = false;
-        for (int j = 0; ok && j < nt; ++j) {
-          // every stage is waited for and given back, so that this warp is never a turn of the ring behind
-          for (int y = 0; ok && y < 2; ++y, ++s) {
-            ok = kv8_wait_all(smem_u32(full + s % ST), (uint32_t)((s / ST) & 1), abort_flag, a.err);
-            int seen;
-            if (ok && y == 1 && ap_partial(it, a.RB, j, seen)) {
-              const bool here = ap_clean<D>(sm + Sh::OFF_RING + (s % ST) * Sh::OP, max(0, seen + 1 - j * AT), j * AT, it.lim0,
-                                            bad + (n & 1) * D, !found);
-              found |= here;
-              if (here) {
-                if (elect_one()) has_bad[n & 1] = 1;
-                fence_async_shared();
-              }
-              __syncwarp();
-            }
-            if (ok && elect_one()) {
-              mbar_arrive(smem_u32(looked + s % ST));
-              mbar_arrive(smem_u32(empty + s % ST));
+        // every stage is waited for and given back, so that this warp is never a turn of the ring behind
+        for (int x = 0; ok && x < 2 * nt; ++x, ++s) {
+          ok = ap_wait_one(smem_u32(full + s % ST), (uint32_t)((s / ST) & 1), abort_flag, a.err);
+          const bool is_v = x && (!(x & 1) || x + 1 == 2 * nt);
+          const int j = (x - 1) >> 1;
+          int seen;
+          if (ok && is_v && ap_partial<KT>(it, a.RB, j, seen)) {
+            if (ap_clean<D>(sm + Sh::OFF_RING + (s % ST) * Sh::KB, max(0, seen + 1 - j * KT), j * KT, it.lim0, bad + (n & 1) * D,
+                            !found)) {
+              found = true;
+              if (elect_one()) has_bad[n & 1] = 1;
+              fence_async_shared();
             }
             __syncwarp();
           }
+          if (ok && elect_one()) {
+            mbar_arrive(smem_u32(looked + s % ST));
+            mbar_arrive(smem_u32(empty + s % ST));
+          }
+          __syncwarp();
         }
         if (ok && elect_one()) mbar_arrive(smem_u32(item_empty + (n & 1)));
         __syncwarp();
@@ -702,7 +745,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == AP_SOFT + 1) {
+  if (warp == AP_MMA) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -745,9 +788,10 @@ int prompt_attention(cudaStream_t st, const PromptArgs& a) {
   CUtensorMap q, k, v;
   // without keys K and V are not read; their maps still need memory
   const bool none = a.Rk == 0;
+  const int KT = a.d == 128 ? ApShape<128>::KT : ApShape<64>::KT;
   if (!ap_map(&q, a.q, a.d, a.nq, a.R, a.ldq, p.G, p.RB) ||
-      !ap_map(&k, none ? a.q : a.k, a.d, none ? a.nq : a.nkv, none ? a.R : a.Rk, none ? a.ldq : a.ldk, 1, AT) ||
-      !ap_map(&v, none ? a.q : a.v, a.d, none ? a.nq : a.nkv, none ? a.R : a.Rk, none ? a.ldq : a.ldv, 1, AT))
+      !ap_map(&k, none ? a.q : a.k, a.d, none ? a.nq : a.nkv, none ? a.R : a.Rk, none ? a.ldq : a.ldk, 1, KT) ||
+      !ap_map(&v, none ? a.q : a.v, a.d, none ? a.nq : a.nkv, none ? a.R : a.Rk, none ? a.ldq : a.ldv, 1, KT))
     return -4;
   const cudaError_t e = a.d == 128 ? launch_prompt<128>(st, q, k, v, p, grid) : launch_prompt<64>(st, q, k, v, p, grid);
   if (e != cudaSuccess) {

@@ -56,7 +56,7 @@ struct ApShape {
   static constexpr int T_S = 2 * D, T_P = T_S + KT, T_STEP = (512 - 2 * D) / 2;
   static_assert(KT + KT / 2 <= T_STEP, "S and P of a tile beside O");
   // registers a thread of the softmax warps, the result warps, the single ones: together those of the launch, 128 each
-  static constexpr int R_SOFT = D == 128 ? 152 : 176, R_OUT = D == 128 ? 144 : 104, R_ONE = D == 128 ? 64 : 56;
+  static constexpr int R_SOFT = 176, R_OUT = 88, R_ONE = 72;
   static_assert(2 * R_SOFT + R_OUT + R_ONE <= 4 * 128, "registers of the launch");
 };
 
@@ -94,6 +94,7 @@ __device__ __forceinline__ int ap_first(const ApArgs& a, const ApSeq& s) { retur
 // pairs of level e and higher (a converged warp)
 __device__ __forceinline__ int ap_count(const ApArgs& a, int e) {
   int n = 0;
+#pragma unroll 1
   for (int b = threadIdx.x & 31; b < a.B; b += 32) {
     bool bad;
     const ApSeq s = ap_seq(a, b, bad);
@@ -104,6 +105,7 @@ __device__ __forceinline__ int ap_count(const ApArgs& a, int e) {
 }
 __device__ __forceinline__ ApList ap_begin(const ApArgs& a, bool latch) {
   int total = 0, top = 0;
+#pragma unroll 1
   for (int b = threadIdx.x & 31; b < a.B; b += 32) {
     bool bad;
     const ApSeq s = ap_seq(a, b, bad);
@@ -115,8 +117,8 @@ __device__ __forceinline__ ApList ap_begin(const ApArgs& a, bool latch) {
   ApList l;
   l.total = __reduce_add_sync(0xffffffffu, total);
   l.level = __reduce_max_sync(0xffffffffu, top);
-  l.above = 0;
-  l.upto = ap_count(a, l.level);
+  ++l.level;      // nothing counted yet
+  l.above = l.upto = 0;
   return l;
 }
 // Item i; h = -1 behind the last one. i rises from call to call.
@@ -126,12 +128,14 @@ __device__ __forceinline__ ApItem ap_item(const ApArgs& a, ApList& l, long long 
   it.h = -1;
   const long long rank = i / a.nkv;
   if (rank >= l.total) return it;
+#pragma unroll 1
   while (rank >= l.upto) {      // (ends: all pairs are of level zero or higher)
     l.above = l.upto;
     l.upto = ap_count(a, --l.level);
   }
   int k = (int)rank - l.above;
   const int lane = threadIdx.x & 31;
+#pragma unroll 1
   for (int b0 = 0; b0 < a.B; b0 += 32) {
     const int b = b0 + lane;
     ApSeq s{0, 0, 0, 0};
@@ -180,18 +184,53 @@ __device__ __forceinline__ bool ap_partial(const ApItem& it, int RB, int j, int&
   return j * KT + KT - 1 > seen;
 }
 
-// Bounded waits of a converged warp that go on at once when the phase is over.
-__device__ __forceinline__ bool ap_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err) {
-  return __all_sync(0xffffffffu, mbar_try(bar, parity)) || kv8_wait(bar, parity, abort_flag, err);
-}
-__device__ __forceinline__ bool ap_wait_one(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err) {
-  return __all_sync(0xffffffffu, mbar_try(bar, parity)) || kv8_wait_all(bar, parity, abort_flag, err);
+__device__ __forceinline__ void tma_prefetch_3d(const void* map, int c0, int c1, int c2) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(reinterpret_cast<uint64_t>(map)), "r"(c0),
+               "r"(c1), "r"(c2)
+               : "memory");
 }
 
+// D[tmem] (+)= A B, the operands' descriptors given by their low halves (128-byte swizzle, rows of eight 1024 bytes apart).
+constexpr uint32_t AP_DESC_HIGH = (1024 >> 4) | 1u << 14 | 2u << 29;
+__device__ __forceinline__ void ap_mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(AP_DESC_HIGH)
+      : "memory");
+}
+__device__ __forceinline__ void ap_mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 y, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(AP_DESC_HIGH)
+      : "memory");
+}
 __device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
   f32x2 r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
+}
+
+// Bounded wait of a converged warp for an mbarrier phase, on at once when it is over; lane 0 tries again, looking at the abort flag
+// and, every 64th time, at the clock. Gives up as mbar_wait does; every lane gets the same answer. (Short: it is inlined some
+// twenty times, and the instruction cache is what bounds the ends of items.)
+__device__ __forceinline__ bool ap_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err, bool honor_abort = true) {
+  if (__all_sync(0xffffffffu, mbar_try(bar, parity))) return true;
+  uint64_t t0 = 0;
+  bool done = false;
+#pragma unroll 1
+  for (uint32_t tries = 1;; ++tries) {
+    if ((threadIdx.x & 31) == 0) done = mbar_try(bar, parity);
+    if (__any_sync(0xffffffffu, done)) return true;
+    if (tries & 63u) continue;
+    if (honor_abort && *abort_flag) return false;
+    const uint64_t now = globaltimer();
+    if (!t0) t0 = now;
+    if (__any_sync(0xffffffffu, now - t0 > EAGLE_WAIT_LIMIT_NS)) {
+      *abort_flag = 1;
+      latch_error(err, DEVERR_MBAR_TIMEOUT);
+      return false;
+    }
+  }
 }
 
 // 16 columns of this warp's lanes; the values are there after tmem_wait_ld_n.
@@ -257,7 +296,7 @@ __device__ __forceinline__ bool ap_clean(uint8_t* v, int r0, int key0, int lim0,
   r0 &= ~3;      // (rows before the first that is hidden from some: seen by all, and looked at for nothing)
 #pragma unroll 1
   for (int x = 0; x < Sh::HALVES; ++x)
-#pragma unroll 4
+#pragma unroll 2
     for (int i = r0 * 8 + lane; i < Sh::KT * 8; i += 32) {
       const uint4 w = *reinterpret_cast<const uint4*>(v + x * Sh::KHALF + i * 16);
       const uint32_t u[4] = {w.x, w.y, w.z, w.w};
@@ -367,6 +406,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
       if (it.h < 0) break;
       const int nt = it.n[mt], first = it.lim0 + mt * a.RB;      // the last key that the tile's first row sees
       float m2 = -INFINITY, l = 0.f;
+#pragma unroll 1
       for (int j = 0; j < nt; ++j) {
         ok = ap_wait(smem_u32(s_full + mt), s_phase, abort_flag, a.err);
         if (!ok) break;
@@ -459,8 +499,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
     }
   } else if (warp < AP_TMA) {
     // ---- results: both tiles' in turn, a quarter of the lanes a warp, while the softmax warps are at the next item ----
-    if constexpr (Sh::R_OUT > 128) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Sh::R_OUT));
-    else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Sh::R_OUT));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Sh::R_OUT));
     const int lane = threadIdx.x & 31, quad = lane & 3, lane0 = (warp & 3) * 32;
     // position and head (of the tile, of the group) of the four query vectors of this thread's fragments
     uint32_t at[4];
@@ -481,52 +520,51 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
         const int rows = it.rows[mt], nt = it.n[mt];
         if (rows <= 0) continue;
         __nv_bfloat16* base = a.out + (long long)(it.row0 + mt * a.RB) * a.ldo + (long long)it.h * a.G * D;
-        // fragments of 16 rows, four threads a row; O leaves TMEM before anything is written, the next item's products wait
-        uint32_t w[D / 2];
         if (nt) {
           ok = ap_wait(smem_u32(l_full + mt), phase >> mt & 1, abort_flag, a.err) &&
                ap_wait(smem_u32(o_done + mt), phase >> mt & 1, abort_flag, a.err);
           if (!ok) break;
           phase ^= 1u << mt;
           tc_fence_after();
-          float part[4];
-#pragma unroll
-          for (int x = 0; x < 4; ++x) part[x] = inv[mt * AT + lane0 + x * 8 + (lane >> 2)];
-#pragma unroll
-          for (int f = 0; f < 2; ++f)
-#pragma unroll
-            for (int c = 0; c < D; c += 64) {
-              float o[32];
-              frag_ld64(tmem + ((uint32_t)(lane0 + f * 16) << 16) + mt * D + c, o);
-              tmem_wait_ld(o);
-#pragma unroll
-              for (int x = 0; x < 16; ++x)
-                w[f * (D / 4) + c / 4 + x] = bf16_pair(o[2 * x] * part[2 * f + (x & 1)], o[2 * x + 1] * part[2 * f + (x & 1)]);
-            }
-          tc_fence_before();
-          warp_arrive(smem_u32(o_free + mt));
-          warp_arrive(smem_u32(l_free + mt));
-        } else {      // rows that see no key
-#pragma unroll
-          for (int x = 0; x < D / 2; ++x) w[x] = 0;
         }
-        // a row's 64 bytes go out together
+        // Fragments of 16 rows, four threads a row, 64 columns at a time: a row's 64 bytes go out together. Rolled, as all
+        // that runs once an item: what falls out of the instruction cache comes back at some ten clocks an instruction.
+#pragma unroll 1
+        for (int fc = 0; fc < 2 * D / 64; ++fc) {
+          const int f = fc / (D / 64), c = fc % (D / 64) * 64;
+          float o[32], part[2];
+          if (nt) {
+            frag_ld64(tmem + ((uint32_t)(lane0 + f * 16) << 16) + mt * D + c, o);
+            tmem_wait_ld(o);
 #pragma unroll
-        for (int f = 0; f < 2; ++f)
+            for (int y = 0; y < 2; ++y) part[y] = inv[mt * AT + lane0 + f * 16 + y * 8 + (lane >> 2)];
+            if (fc == 2 * D / 64 - 1) {      // O is read: the next item's products may begin
+              tc_fence_before();
+              warp_arrive(smem_u32(o_free + mt));
+              warp_arrive(smem_u32(l_free + mt));
+            }
+          } else {      // rows that see no key
+            part[0] = part[1] = 0.f;
+#pragma unroll
+            for (int x = 0; x < 32; ++x) o[x] = 0.f;
+          }
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
-            const int p = at[2 * f + y] >> 16;
-            __nv_bfloat16* dst = base + (long long)p * a.ldo + (int)(at[2 * f + y] & 0xffff) * D + quad * 8;
+            const uint32_t v = f ? at[2 + y] : at[y];
+            const int p = v >> 16;
+            __nv_bfloat16* dst = base + (long long)p * a.ldo + (int)(v & 0xffff) * D + c + quad * 8;
 #pragma unroll
-            for (int x = 0; x < D / 32; ++x) {
-              uint32_t z[4];
+            for (int x = 0; x < 2; ++x) {
+              uint32_t w[4];
 #pragma unroll
-              for (int i = 0; i < 4; ++i) z[i] = w[f * (D / 4) + (x * 4 + i) * 2 + y];
-              quad_transpose(z, quad);
+              for (int i = 0; i < 4; ++i)
+                w[i] = bf16_pair(o[(x * 4 + i) * 4 + 2 * y] * part[y], o[(x * 4 + i) * 4 + 2 * y + 1] * part[y]);
+              quad_transpose(w, quad);
               if (p < rows)      // (so p < RB: not the vectors behind the last head)
-                *reinterpret_cast<uint4*>(dst + x * 32) = make_uint4(z[0], z[1], z[2], z[3]);
+                *reinterpret_cast<uint4*>(dst + x * 32) = make_uint4(w[0], w[1], w[2], w[3]);
             }
           }
+        }
         if (nt && has_bad[n & 1]) {      // (rare: over what this warp has just written, a row a thread)
           __syncwarp();
           const int p = (lane0 + lane) / a.G, i = mt * a.RB + p;
@@ -552,150 +590,145 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
     if (warp == AP_TMA) {
       // ---- items, TMA ----
       ApList list = ap_begin(a, blockIdx.x == 0);
-      const uint32_t qbytes = (uint32_t)(a.RB * a.G * 128);
-      int used[2] = {0, 0}, s = 0;      // tiles of Q and stages of the ring so far
+      const uint32_t qbytes = (uint32_t)(Sh::HALVES * a.RB * a.G * 128);
+      uint32_t used = 0;                // loads of Q: of tile 0 in the low half, of tile 1 in the high half
+      int s = 0;                        // stages of the ring so far
+      ApItem it{}, next{};
       bool ok = true;
-      // K or V tile j into the ring's next stage
-      auto load = [&](const CUtensorMap* map, const ApItem& it, int j) {
-        const int st = s % ST;
-        if (s >= ST && !ap_wait_one(smem_u32(empty + st), (uint32_t)((s / ST - 1) & 1), abort_flag, a.err)) return false;
-        if (elect_one()) {
-          mbar_expect_tx(smem_u32(full + st), Sh::KB);
-          for (int x = 0; x < Sh::HALVES; ++x)
-            tma_load_3d(smem_u32(sm + Sh::OFF_RING + st * Sh::KB + x * Sh::KHALF), map, x * 64, it.h, it.k0 + j * KT,
-                        smem_u32(full + st));
-        }
-        __syncwarp();
-        ++s;
-        return true;
-      };
-      auto load_q = [&](const ApItem& it, int t) {
-        if (used[t] && !ap_wait_one(smem_u32(q_empty + t), (uint32_t)((used[t] - 1) & 1), abort_flag, a.err)) return false;
-        if (elect_one()) {
-          mbar_expect_tx(smem_u32(q_full + t), Sh::HALVES * qbytes);
-          for (int x = 0; x < Sh::HALVES; ++x)
-            tma_load_3d(smem_u32(sm + t * Sh::QB + x * Sh::QHALF), &tmQ, x * 64, it.h * a.G, it.row0 + t * a.RB,
-                        smem_u32(q_full + t));
-        }
-        __syncwarp();
-        ++used[t];
-        return true;
-      };
-      for (int n = 0; ok; ++n) {
+      // Item n is found, its Q brought into L2, and published while the products of item n - 1 run, whose loads come between.
+#pragma unroll 1
+      for (int n = 0;; ++n) {
         // to and fro over the CTAs: who takes the largest of one round takes the smallest of the next
         const int at = n & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
-        const ApItem it = ap_item<KT>(a, list, at + (long long)n * gridDim.x);
-        if (n >= 2) ok = ap_wait_one(smem_u32(item_empty + (n & 1)), (uint32_t)(((n >> 1) - 1) & 1), abort_flag, a.err);
+        next = ap_item<KT>(a, list, at + (long long)n * gridDim.x);
+        if (next.h >= 0 && elect_one())
+#pragma unroll 1
+          for (int x = 0; x < 2 * Sh::HALVES; ++x)
+            if (x & 1 ? next.n[1] : next.n[0]) tma_prefetch_3d(&tmQ, (x >> 1) * 64, next.h * a.G, next.row0 + (x & 1) * a.RB);
+        __syncwarp();
+        const int nt = max(it.n[0], it.n[1]);
+#pragma unroll 1
+        for (int x = 0; ok && x < 2 * nt; ++x, ++s) {
+          const int st = s % ST;
+          const bool is_v = x && (!(x & 1) || x + 1 == 2 * nt);
+          if (s >= ST) ok = ap_wait(smem_u32(empty + st), (uint32_t)((s / ST - 1) & 1), abort_flag, a.err);
+          if (!ok) break;
+          if (elect_one()) {
+            mbar_expect_tx(smem_u32(full + st), Sh::KB);
+            for (int y = 0; y < Sh::HALVES; ++y)
+              tma_load_3d(smem_u32(sm + Sh::OFF_RING + st * Sh::KB + y * Sh::KHALF), is_v ? &tmV : &tmK, y * 64, it.h,
+                          it.k0 + (x ? is_v ? (x - 1) >> 1 : (x + 1) >> 1 : 0) * KT, smem_u32(full + st));
+          }
+          __syncwarp();
+          if (x == 0)      // behind the first keys: Q, when the item before has done with its place
+#pragma unroll 1
+            for (int t = 0; ok && t < 2; ++t) {
+              if (!(t ? it.n[1] : it.n[0])) continue;
+              const uint32_t u = used >> 16 * t & 0xffff;
+              if (u) ok = ap_wait(smem_u32(q_empty + t), (u - 1) & 1, abort_flag, a.err);
+              if (!ok) break;
+              if (elect_one()) {
+                mbar_expect_tx(smem_u32(q_full + t), qbytes);
+                for (int y = 0; y < Sh::HALVES; ++y)
+                  tma_load_3d(smem_u32(sm + t * Sh::QB + y * Sh::QHALF), &tmQ, y * 64, it.h * a.G, it.row0 + t * a.RB,
+                              smem_u32(q_full + t));
+              }
+              __syncwarp();
+              used = (used & ~(0xffffu << 16 * t)) | ((u + 1 == 0x10000 ? 2 : u + 1) & 0xffff) << 16 * t;
+            }
+        }
+        if (ok && n >= 2) ok = ap_wait(smem_u32(item_empty + (n & 1)), (uint32_t)(((n >> 1) - 1) & 1), abort_flag, a.err);
         if (!ok) break;
         if (elect_one()) {
-          items[n & 1] = it;
+          items[n & 1] = next;
           has_bad[n & 1] = 0;
           mbar_arrive(smem_u32(item_full + (n & 1)));
         }
         __syncwarp();
-        if (it.h < 0) break;
-        const int nt = max(it.n[0], it.n[1]);
-        if (nt == 0) continue;
-        if (it.n[0]) ok = load_q(it, 0);
-        ok = ok && load(&tmK, it, 0);
-        if (it.n[1]) ok = ok && load_q(it, 1);
-        for (int j = 0; ok && j < nt; ++j) {
-          if (j + 1 < nt) ok = load(&tmK, it, j + 1);
-          ok = ok && load(&tmV, it, j);
-        }
+        if (next.h < 0) break;
+        it = next;
       }
       if (*abort_flag) {      // copies in flight land before the CTA leaves: the last ones of the ring and of Q
-        for (int t = 0; t < 2; ++t)
-          if (used[t]) kv8_wait_all(smem_u32(q_full + t), (uint32_t)((used[t] - 1) & 1), abort_flag, a.err, false);
-        for (int x = max(0, s - ST); x < s; ++x)
-          kv8_wait_all(smem_u32(full + x % ST), (uint32_t)((x / ST) & 1), abort_flag, a.err, false);
+#pragma unroll 1
+        for (int x = max(0, s - ST) - 2; x < s; ++x) {
+          const int t = x - (max(0, s - ST) - 2);
+          if (t < 2 && !(used >> 16 * t & 0xffff)) continue;
+          const uint32_t bar = t < 2 ? smem_u32(q_full + t) : smem_u32(full + x % ST);
+          ap_wait(bar, t < 2 ? ((used >> 16 * t & 0xffff) - 1) & 1 : (uint32_t)((x / ST) & 1), abort_flag, a.err, false);
+        }
       }
     } else if (warp < AP_LOOK) {
       // ---- MMA: one warp a query tile ----
       constexpr uint32_t IS = pf_idesc(KT, false), IO = pf_idesc(D, true);
-      const int mt = warp - AP_MMA;
-      const uint32_t tS = tmem + Sh::T_S + mt * Sh::T_STEP, tP = tS + KT, tO = tmem + mt * D;
-      // operand descriptors; an offset of n bytes adds n >> 4
-      const uint64_t dq = sdesc_sw128(smem_u32(sm + mt * Sh::QB)), dk = sdesc_sw128(smem_u32(sm + Sh::OFF_RING)),
-                     dv = pf_desc_mn(smem_u32(sm + Sh::OFF_RING), Sh::KHALF);
+      // What the products are issued with goes through a warp reduction, whose result is in a uniform register: from there
+      // descriptors are one addition each (held in the threads' registers, each product waits for several moves).
+      const int mt = (int)__reduce_max_sync(0xffffffffu, (uint32_t)(warp - AP_MMA));
+      const uint32_t base = __reduce_max_sync(0xffffffffu, tmem);
+      const uint32_t tS = base + Sh::T_S + mt * Sh::T_STEP, tP = tS + KT, tO = base + mt * D;
+      // low halves of the operand descriptors; an offset of n bytes adds n >> 4
+      const uint32_t dq = (uint32_t)sdesc_sw128(smem_u32(sm + mt * Sh::QB)), dk = (uint32_t)sdesc_sw128(smem_u32(sm + Sh::OFF_RING)),
+                     dv = (uint32_t)pf_desc_mn(smem_u32(sm + Sh::OFF_RING), Sh::KHALF);
       int s = 0, used = 0, units = 0;      // stages, items and key tiles with products of this tile so far
-      bool ok = true;
-      auto wait_stage = [&](int x) { return ap_wait_one(smem_u32(full + x % ST), (uint32_t)((x / ST) & 1), abort_flag, a.err); };
-      auto give_back = [&](int x) {
-        if (elect_one()) mbar_arrive(smem_u32(empty + x % ST));
-        __syncwarp();
-      };
-      // S of the keys in stage x, once the softmax warps hold the S before
-      auto scores = [&](int x, bool last) {
-        if (!wait_stage(x)) return false;
-        if (units && !ap_wait_one(smem_u32(s_free + mt), (uint32_t)((units - 1) & 1), abort_flag, a.err)) return false;
-        ++units;
-        tc_fence_after();
-        if (elect_one()) {
-          const uint64_t k = dk + ((uint64_t)(x % ST) * Sh::KB >> 4);
-#pragma unroll
-          for (int y = 0; y < D / 16; ++y)
-            tc_mma_bf16(tS, dq + (((y >> 2) * Sh::QHALF + (y & 3) * 32) >> 4), k + (((y >> 2) * Sh::KHALF + (y & 3) * 32) >> 4), IS,
-                        y ? 1u : 0u);
-          tc_commit(smem_u32(s_full + mt));
-          tc_commit(smem_u32(empty + x % ST));
-          if (last) tc_commit(smem_u32(q_empty + mt));
-        }
-        __syncwarp();
-        return true;
-      };
       uint32_t p_phase = 0;
+      bool ok = true;
+#pragma unroll 1
       for (int n = 0; ok; ++n) {
-        ok = ap_wait_one(smem_u32(item_full + (n & 1)), (uint32_t)((n >> 1) & 1), abort_flag, a.err);
+        ok = ap_wait(smem_u32(item_full + (n & 1)), (uint32_t)((n >> 1) & 1), abort_flag, a.err);
         if (!ok) break;
         const ApItem it = items[n & 1];
         if (it.h < 0) break;
-        const int mine = it.n[mt], nt = max(it.n[0], it.n[1]);
-        if (nt) {
-          if (mine) {
-            ok = ap_wait_one(smem_u32(q_full + mt), (uint32_t)(used & 1), abort_flag, a.err) && scores(s, mine == 1);
-          } else {
-            ok = wait_stage(s);
-            if (ok) give_back(s);
-          }
-          ++s;
-        }
-        for (int j = 0; ok && j < nt; ++j) {
-          if (j + 1 < nt) {
-            if (j + 1 < mine) {
-              ok = scores(s, j + 2 == mine);
-            } else {      // the other tile's keys alone
-              ok = wait_stage(s);
-              if (ok) give_back(s);
-            }
-            if (!ok) break;
-            ++s;
-          }
-          ok = wait_stage(s);
+        const int mine = mt ? it.n[1] : it.n[0], nt = max(it.n[0], it.n[1]);
+        // stage by stage: S of the keys in it, or O of the values in it; those of the other tile alone are given back
+#pragma unroll 1
+        for (int x = 0; ok && x < 2 * nt; ++x, ++s) {
+          const int st = s % ST;
+          const bool is_v = x && (!(x & 1) || x + 1 == 2 * nt);
+          const int j = x ? is_v ? (x - 1) >> 1 : (x + 1) >> 1 : 0;
+          const uint32_t turn = (uint32_t)((s / ST) & 1);
+          ok = ap_wait(smem_u32(full + st), turn, abort_flag, a.err);
           if (!ok) break;
           if (j >= mine) {
-            give_back(s++);
-            continue;
-          }
-          int seen;
-          if (ap_partial<KT>(it, a.RB, j, seen))      // (behind wait_stage: warp 15 has passed the stage's use before)
-            ok = ap_wait_one(smem_u32(looked + s % ST), (uint32_t)((s / ST) & 1), abort_flag, a.err);
-          if (ok && j == 0 && used) ok = ap_wait_one(smem_u32(o_free + mt), (uint32_t)((used - 1) & 1), abort_flag, a.err);
-          ok = ok && ap_wait_one(smem_u32(p_full + mt), p_phase, abort_flag, a.err);
-          if (!ok) break;
-          p_phase ^= 1;
-          tc_fence_after();
-          if (elect_one()) {
-            const uint64_t v = dv + ((uint64_t)(s % ST) * Sh::KB >> 4);
+            if (elect_one()) mbar_arrive(smem_u32(empty + st));
+            __syncwarp();
+          } else if (!is_v) {
+            if (x == 0) ok = ap_wait(smem_u32(q_full + mt), (uint32_t)(used & 1), abort_flag, a.err);
+            // the softmax warps hold the S before
+            if (ok && units) ok = ap_wait(smem_u32(s_free + mt), (uint32_t)((units - 1) & 1), abort_flag, a.err);
+            if (!ok) break;
+            ++units;
+            tc_fence_after();
+            const uint32_t k = __reduce_max_sync(0xffffffffu, dk + ((uint32_t)(st * Sh::KB) >> 4));
+            if (elect_one()) {
 #pragma unroll
-            for (int y = 0; y < KT / 16; ++y)      // 16 keys a product
-              mma_ts(tO, tP + y * 8, v + (y * 2048 >> 4), IO, j || y ? 1u : 0u);
-            tc_commit(smem_u32(p_free + mt));
-            tc_commit(smem_u32(empty + s % ST));
-            if (j + 1 == mine) tc_commit(smem_u32(o_done + mt));
+              for (int y = 0; y < D / 16; ++y)
+                ap_mma_ss(tS, dq + (((y >> 2) * Sh::QHALF + (y & 3) * 32) >> 4), k + (((y >> 2) * Sh::KHALF + (y & 3) * 32) >> 4),
+                          IS, y ? 1u : 0u);
+              tc_commit(smem_u32(s_full + mt));
+              tc_commit(smem_u32(empty + st));
+              if (j + 1 == mine) tc_commit(smem_u32(q_empty + mt));
+            }
+            __syncwarp();
+          } else {
+            int seen;
+            if (ap_partial<KT>(it, a.RB, j, seen))      // (behind the wait for the stage: warp 15 has passed its use before)
+              ok = ap_wait(smem_u32(looked + st), turn, abort_flag, a.err);
+            if (ok && j == 0 && used) ok = ap_wait(smem_u32(o_free + mt), (uint32_t)((used - 1) & 1), abort_flag, a.err);
+            ok = ok && ap_wait(smem_u32(p_full + mt), p_phase, abort_flag, a.err);
+            if (!ok) break;
+            p_phase ^= 1;
+            tc_fence_after();
+            const uint32_t v = __reduce_max_sync(0xffffffffu, dv + ((uint32_t)(st * Sh::KB) >> 4));
+            const uint32_t more = __reduce_max_sync(0xffffffffu, (uint32_t)j);
+            if (elect_one()) {
+#pragma unroll
+              for (int y = 0; y < KT / 16; ++y)      // 16 keys a product
+                ap_mma_ts(tO, tP + y * 8, v + (y * 2048 >> 4), IO, y ? 1u : more);
+              tc_commit(smem_u32(p_free + mt));
+              tc_commit(smem_u32(empty + st));
+              if (j + 1 == mine) tc_commit(smem_u32(o_done + mt));
+            }
+            __syncwarp();
           }
-          __syncwarp();
-          ++s;
         }
         if (mine) ++used;
         if (ok && elect_one()) mbar_arrive(smem_u32(item_empty + (n & 1)));
@@ -704,22 +737,23 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
       if (!ok) {      // products in flight end before the CTA frees its TMEM
         if (elect_one()) tc_commit(smem_u32(drain + mt));
         __syncwarp();
-        kv8_wait_all(smem_u32(drain + mt), 0, abort_flag, a.err, false);
+        ap_wait(smem_u32(drain + mt), 0, abort_flag, a.err, false);
       }
     } else {
       // ---- value tiles that some rows see only in part ----
       int s = 0;
       bool ok = true;
       for (int n = 0; ok; ++n) {
-        ok = ap_wait_one(smem_u32(item_full + (n & 1)), (uint32_t)((n >> 1) & 1), abort_flag, a.err);
+        ok = ap_wait(smem_u32(item_full + (n & 1)), (uint32_t)((n >> 1) & 1), abort_flag, a.err);
         if (!ok) break;
         const ApItem it = items[n & 1];
         if (it.h < 0) break;
         const int nt = max(it.n[0], it.n[1]);
         bool found = false;
         // every stage is waited for and given back, so that this warp is never a turn of the ring behind
+#pragma unroll 1
         for (int x = 0; ok && x < 2 * nt; ++x, ++s) {
-          ok = ap_wait_one(smem_u32(full + s % ST), (uint32_t)((s / ST) & 1), abort_flag, a.err);
+          ok = ap_wait(smem_u32(full + s % ST), (uint32_t)((s / ST) & 1), abort_flag, a.err);
           const bool is_v = x && (!(x & 1) || x + 1 == 2 * nt);
           const int j = (x - 1) >> 1;
           int seen;

@@ -630,14 +630,16 @@ class KV8Layers:
         nb = L.lib().eagle_op_kv8_resize_scratch_bytes(c.ref)
         _need(nb > 0, "a cache that the library does not take")
         self.scratch = torch.empty(nb, dtype=torch.uint8, device=c.device)
+        self.work = (self.scratch.data_ptr(), nb)
 
 
 def _seq_list(layers: KV8Layers, t: torch.Tensor, n: Optional[int], name: str) -> int:
     """Entries of a per-sequence list: as many as `n` where that is given, and at most max_batch."""
+    m = t.numel()
     if t.dtype is not torch.int32 or t.dim() != 1 or not t.is_contiguous() or t.get_device() != layers.index or \
-            t.numel() > layers.max_batch or (n is not None and t.numel() != n):
+            m > layers.max_batch or (n is not None and m != n):
         raise ValueError(f"{name} must be a contiguous int32 list, one entry a sequence, on the caches' device")
-    return t.numel()
+    return m
 
 
 def kv8_compact(layers: KV8Layers, n_old: torch.Tensor, acc_len: torch.Tensor, acc_path: torch.Tensor,
@@ -670,7 +672,7 @@ def kv8_fork(layers: KV8Layers, parent: Optional[torch.Tensor], length: torch.Te
         with torch.cuda.device(layers.index):
             return kv8_fork(layers, parent, length, err, stream)
     rc = L.lib().eagle_op_kv8_resize(_stream_of(layers.index, stream), layers.c, layers.n, B, layers.refs.data_ptr(),
-                                     _ptr(parent), length.data_ptr(), layers.scratch.data_ptr(), layers.scratch.numel(), e)
+                                     _ptr(parent), length.data_ptr(), *layers.work, e)
     L.check(rc, "eagle_op_kv8_resize")
 
 
@@ -721,16 +723,17 @@ class Rope:
         self.freq = list(f)
         self.factor = m.value if factor is None else float(factor)
         self.turns = torch.tensor([x - (1 << 64) if x >> 63 else x for x in t], dtype=torch.int64).to(device)
-        self.device, self.index = self.turns.device, self.turns.get_device()
+        self.device, self.index, self.table = self.turns.device, self.turns.get_device(), self.turns.data_ptr()
 
 
 def _head_rows(t: torch.Tensor, index: int, d: int, name: str) -> int:
     """Row stride of [R][heads][d] rows, each row in one piece; a single row's is of no account."""
-    if t.dim() != 3 or t.shape[2] != d or t.get_device() != index:
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != d or t.get_device() != index:
         raise ValueError(f"{name} must be [R][heads][{d}] on the same device")
+    R, h, _ = shape
     s0, s1, s2 = t.stride()
-    R, h, _ = t.shape
-    if R and h and (s2 != 1 or (s1 != d and h != 1)):
+    if (s2 != 1 or (s1 != d and h != 1)) and R and h:
         raise ValueError(f"{name}'s rows must be contiguous (the row stride is free)")
     return s0 if R > 1 else h * d
 
@@ -741,36 +744,42 @@ def rope(plan: Rope, q: torch.Tensor, k: Optional[torch.Tensor], pos: torch.Tens
     """Rows q [R][nq][d] and k [R][nkv][d] (or None; fp32 or bf16, any row stride of whole 16 bytes) turned to positions
     pos [R] (int32); inverse: turned back. Returns (q, k) of `dtype` (default: q's), contiguous, or written to `out`,
     which may be (q, k) themselves."""
-    d, index = plan.head_dim, plan.index
-    src = _KV_TYPES.get(q.dtype)
-    _need(src is not None and (k is None or (k.dtype is q.dtype and k.dim() == 3 and k.shape[0] == q.shape[0])),
-          "q and k must be float32 or bfloat16 rows of one type and number")
-    _need(index >= 0, "the plan and its call's tensors must be on a GPU")
+    d, index, qt = plan.head_dim, plan.index, q.dtype
+    src = _KV_TYPES.get(qt)
+    if src is None or index < 0:
+        raise ValueError("q must be float32 or bfloat16 rows, and the plan and its call's tensors on a GPU")
     ldq = _head_rows(q, index, d, "q")
-    ldk = 0 if k is None else _head_rows(k, index, d, "k")
     R, nq, _ = q.shape
-    nkv = 0 if k is None else k.shape[1]
+    nkv = ldk = 0
+    if k is not None:
+        if k.dtype is not qt or k.dim() != 3 or k.shape[0] != R:
+            raise ValueError("q and k must be rows of one type and number")
+        ldk, nkv = _head_rows(k, index, d, "k"), k.shape[1]
     if pos.dtype is not torch.int32 or pos.numel() != R or not pos.is_contiguous() or pos.get_device() != index:
         raise ValueError("pos must be a contiguous int32 tensor of an entry a row")
     if out is None:
-        dtype = q.dtype if dtype is None else dtype
-        _need(dtype in _KV_TYPES, "rows are written as float32 or bfloat16")
+        to = qt if dtype is None else dtype
+        dst = _KV_TYPES.get(to)
+        _need(dst is not None, "rows are written as float32 or bfloat16")
+        dev = q.device
         with _owned_by(stream):
-            qo = torch.empty((R, nq, d), dtype=dtype, device=q.device)
-            ko = None if k is None else torch.empty((R, nkv, d), dtype=dtype, device=q.device)
+            qo = torch.empty((R, nq, d), dtype=to, device=dev)
+            ko = None if k is None else torch.empty((R, nkv, d), dtype=to, device=dev)
+        ldqo, ldko = nq * d, nkv * d
     else:
         qo, ko = out
+        dst = _KV_TYPES.get(qo.dtype)
         _need(qo.shape == q.shape and (ko is None) == (k is None) and (k is None or ko.shape == k.shape) and
-              qo.dtype in _KV_TYPES and (ko is None or ko.dtype is qo.dtype) and (dtype is None or dtype is qo.dtype),
+              dst is not None and (ko is None or ko.dtype is qo.dtype) and (dtype is None or dtype is qo.dtype),
               "out must be rows like q and k, float32 or bfloat16")
-    ldqo = _head_rows(qo, index, d, "out")
-    ldko = 0 if k is None else _head_rows(ko, index, d, "out")
+        ldqo = _head_rows(qo, index, d, "out")
+        ldko = 0 if k is None else _head_rows(ko, index, d, "out")
     if _elsewhere(index):
         with torch.cuda.device(index):
             return rope(plan, q, k, pos, None, (qo, ko), inverse, stream)
-    rc = L.lib().eagle_op_rope(_stream_of(index, stream), src, _KV_TYPES[qo.dtype], q.data_ptr(), ldq, qo.data_ptr(), ldqo, nq,
-                               _ptr(k), ldk, _ptr(ko), ldko, nkv, d, plan.rot, int(plan.interleaved), R, pos.data_ptr(),
-                               plan.turns.data_ptr(), plan.factor, int(inverse))
+    rc = L.lib().eagle_op_rope(_stream_of(index, stream), src, dst, q.data_ptr(), ldq, qo.data_ptr(), ldqo, nq,
+                               _ptr(k), ldk, _ptr(ko), ldko, nkv, d, plan.rot, plan.interleaved, R, pos.data_ptr(),
+                               plan.table, plan.factor, inverse)
     L.check(rc, "eagle_op_rope")
     return qo, ko
 
@@ -784,25 +793,28 @@ def attention_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_start:
     k, v[k_start[b]:k_start[b + 1]] ([Rk][nkv][d]; default: the rows' starts), the last row seeing all of them. Row strides
     are free. q_start, k_start: int32 [B + 1] on the device. lse: float32 [R][nq] to fill with the rows' log-sum-exps. Rows
     of no sequence are not written."""
-    index = q.get_device()
-    _need(index >= 0, "q, k and v must be on a GPU")
-    d = q.shape[-1]
-    for t in (q, k, v):
-        _need(t.dtype is torch.bfloat16, "q, k and v must be bfloat16")
+    index, shape = q.get_device(), q.shape
+    if index < 0 or q.dtype is not torch.bfloat16 or k.dtype is not torch.bfloat16 or v.dtype is not torch.bfloat16:
+        raise ValueError("q, k and v must be bfloat16 tensors of a GPU")
+    d = shape[-1]
     ldq, ldk, ldv = _head_rows(q, index, d, "q"), _head_rows(k, index, d, "k"), _head_rows(v, index, d, "v")
-    _need(k.shape == v.shape, "k and v must have one shape")
-    R, nq, _ = q.shape
-    k_start = q_start if k_start is None else k_start
+    kshape = k.shape
+    _need(kshape == v.shape, "k and v must have one shape")
+    R, nq, _ = shape
+    n = q_start.numel()
+    if k_start is None:
+        k_start = q_start
     for t in (q_start, k_start):
-        if t.dtype is not torch.int32 or t.dim() != 1 or t.numel() < 1 or not t.is_contiguous() or t.get_device() != index or \
-                t.numel() != q_start.numel():
+        if t.dtype is not torch.int32 or t.dim() != 1 or n < 1 or t.numel() != n or not t.is_contiguous() or \
+                t.get_device() != index:
             raise ValueError("q_start and k_start must be contiguous int32 lists of one more entry than sequences")
     if out is None:
         with _owned_by(stream):
             out = torch.empty((R, nq, d), dtype=torch.bfloat16, device=q.device)
+        ldo = nq * d
     else:
-        _need(out.shape == q.shape and out.dtype is torch.bfloat16, "out must be bfloat16 rows like q")
-    ldo = _head_rows(out, index, d, "out")
+        _need(out.shape == shape and out.dtype is torch.bfloat16, "out must be bfloat16 rows like q")
+        ldo = _head_rows(out, index, d, "out")
     if lse is not None:
         _need(lse.dtype is torch.float32 and lse.shape == (R, nq) and lse.is_contiguous() and lse.get_device() == index,
               "lse must be a contiguous float32 [R][nq] tensor on q's device")
@@ -813,7 +825,6 @@ def attention_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_start:
         with torch.cuda.device(index):
             return attention_prompt(q, k, v, q_start, k_start, scale, out, lse, err, stream)
     rc = L.lib().eagle_op_attention_prompt(_stream_of(index, stream), q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv,
-                                           out.data_ptr(), ldo, _ptr(lse), R, k.shape[0], nq, k.shape[1], d,
-                                           q_start.numel() - 1, q_start.data_ptr(), k_start.data_ptr(), scale, _ptr(err))
+                                           out.data_ptr(), ldo, _ptr(lse), R, kshape[0], nq, kshape[1], d, n - 1, q_start.data_ptr(), k_start.data_ptr(), scale, _ptr(err))
     L.check(rc, "eagle_op_attention_prompt")
     return out

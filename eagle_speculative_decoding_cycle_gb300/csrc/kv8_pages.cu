@@ -6,13 +6,15 @@
 // counts, so the result of a call depends on the table and counts alone, not on the order of earlier calls.
 //
 // kv8_plan_k, one CTA, phases with a barrier between them:
-//   check     which sequences take part; a fork's parent keeps its entries during the call and has all that are shared;
-//   release   entries past a sequence's last block, and all that a fork held: counts down (integer atomics: any order);
-//   share     a fork's entries from its parent's: counts up;
-//   count     missing entries of each sequence, plus its last block if that is partly filled and others hold it too: the
-//             sequence would write where they read. Then exclusive sums over the sequences;
-//   find      that many free blocks in rising order;
+//   rows      a warp a sequence: which take part (a fork's parent keeps its entries during the call and has all that are
+//             shared); entries past the last block, and all that a fork held, released; a fork's taken from its parent's;
+//             counts down and up (integer atomics: any order). Entries that are missing are counted;
+//   last      a thread a sequence: its last block, if that is partly filled and others hold it too, is to be replaced: the
+//             sequence would write where they read. Exclusive sums of the entries wanted over the sequences;
+//   find      that many free blocks in rising order, 16 counts a thread at a time;
 //   assign    the n-th missing entry, in the order of sequences and slots, gets the n-th free block.
+// Up to 2048 sequences and 4096 new blocks what the phases hand on is in shared memory. A call of 64 sequences and 8400 blocks: 
+// MEASURED (was 11 us with a phase for each step, all through L2).
 // kv8_copy_k then copies the filled slots of the blocks that were replaced, in all layers and heads, a warp for each
 // (copy, layer, K or V, head): the slots of a head are next to each other in a block.
 //
@@ -29,19 +31,22 @@ constexpr int COPY_THREADS = 256;
 
 struct LayerSet { Kv8Layer l[MAX_LAYERS]; };
 
+constexpr int PLAN_SEQS = 2048, PLAN_FOUND = 4096, PLAN_COUNTS = 16;
+
 struct PlanArgs {
   int* table;
   int* refs;
   const int *parent, *length;
   int B, max_batch, tab_w, n_blocks, block_log2, cap;
   int* err;
-  // scratch
-  int* state;      // [B]: blocks wanted, -1: takes no part
+  // scratch, for what does not fit into shared memory
+  int* state;      // [B]: blocks wanted, -1: takes no part; bit 30: the last one is to be replaced
   int* need;       // [B]: missing entries, then the sum of those of earlier sequences
-  int* shared;     // [B]: the last block is to be replaced
+  int* tail;       // [B]: the block that ends the sequence, if it is partly filled; -1: none
   int* copies;     // [0]: their number, then (from, to, slots) each
   int* found;      // free blocks, rising
 };
+constexpr int PLAN_LAST = 1 << 30;
 
 // Sum over the threads before this one, and the total.
 __device__ __forceinline__ int block_scan(int v, int* warp_sums, int& total) {
@@ -54,37 +59,42 @@ __device__ __forceinline__ int block_scan(int v, int* warp_sums, int& total) {
   }
   if (lane == 31) warp_sums[warp] = x;
   __syncthreads();
-  if (warp == 0) {
-    int w = warp_sums[lane];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, w, o);
-      if (lane >= o) w += y;
-    }
-    warp_sums[lane] = w;
-  }
-  __syncthreads();
-  total = warp_sums[PLAN_WARPS - 1];
-  const int before = warp ? warp_sums[warp - 1] : 0;
+  const int w = warp_sums[lane];      // (32 warps)
+  const int before = __reduce_add_sync(0xffffffffu, lane < warp ? w : 0);
+  total = __reduce_add_sync(0xffffffffu, w);
   __syncthreads();      // warp_sums may be written again
   return before + x - v;
 }
 
+__device__ __forceinline__ void release(const PlanArgs& a, int e) {
+  if (e >= a.n_blocks) {
+    latch_error(a.err, DEVERR_BOUNDS);
+  } else if (atomicSub(a.refs + e, 1) <= 0) {      // a count that did not match the table
+    atomicAdd(a.refs + e, 1);
+    latch_error(a.err, DEVERR_BOUNDS);
+  }
+}
+
 __global__ void __launch_bounds__(PLAN_THREADS, 1) kv8_plan_k(const PlanArgs a) {
-  __shared__ int warp_sums[PLAN_WARPS];
+  __shared__ int warp_sums[PLAN_WARPS], sh_state[PLAN_SEQS], sh_need[PLAN_SEQS], sh_tail[PLAN_SEQS], sh_found[PLAN_FOUND];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, block = 1 << a.block_log2;
+  volatile int* state = a.B <= PLAN_SEQS ? sh_state : a.state;
+  volatile int* need = a.B <= PLAN_SEQS ? sh_need : a.need;
+  volatile int* tail = a.B <= PLAN_SEQS ? sh_tail : a.tail;
   PDL_ENTRY();
-  // ---- check ----
+  // ---- rows ----
   if (threadIdx.x == 0) a.copies[0] = 0;
   for (int b = warp; b < a.B; b += PLAN_WARPS) {
-    const int n = a.length[b], p = a.parent ? a.parent[b] : -1;
+    const int n = __ldcg(a.length + b), p = a.parent ? __ldcg(a.parent + b) : -1;
+    const int nb = n > 0 ? (int)(((long long)n + block - 1) >> a.block_log2) : 0;
+    const int end = n & (block - 1) ? nb - 1 : -1;      // the entry of a partly filled last block
+    int missing = 0, last = -1;
     bool ok = n >= 0, bad = n > a.cap;
-    int nb = n > 0 ? (int)(((long long)n + block - 1) >> a.block_log2) : 0;
     if (ok && !bad && p >= 0) {
-      // the parent takes no part itself, and holds what is shared
-      bad = p >= a.max_batch || p == b || (p < a.B && a.length[p] >= 0);
+      bad = p >= a.max_batch || p == b || (p < a.B && __ldcg(a.length + p) >= 0);      // the parent takes no part itself
       if (!bad) {
         bool holes = false;
+#pragma unroll 4
         for (int j = lane; j < nb; j += 32) {
           const int e = __ldcg(a.table + (size_t)p * a.tab_w + j);
           holes |= e < 0 || e >= a.n_blocks;
@@ -96,93 +106,94 @@ __global__ void __launch_bounds__(PLAN_THREADS, 1) kv8_plan_k(const PlanArgs a) 
       if (lane == 0) latch_error(a.err, DEVERR_BOUNDS);
       ok = false;
     }
-    if (lane == 0) a.state[b] = ok ? nb : -1;
-  }
-  __syncthreads();
-  // ---- release ----
-  for (int b = warp; b < a.B; b += PLAN_WARPS) {
-    const int nb = __ldcg(a.state + b);
-    if (nb < 0) continue;
-    const bool fork = a.parent && a.parent[b] >= 0;
-    int* row = a.table + (size_t)b * a.tab_w;
+    if (ok) {
+      int* row = a.table + (size_t)b * a.tab_w;
+      if (p >= 0) {
+        const int* from = a.table + (size_t)p * a.tab_w;
 #pragma unroll 4
-    for (int j = (fork ? 0 : nb) + lane; j < a.tab_w; j += 32) {
-      const int e = __ldcg(row + j);
-      if (e < 0) continue;
-      row[j] = -1;
-      if (e >= a.n_blocks) {
-        latch_error(a.err, DEVERR_BOUNDS);
-      } else if (atomicSub(a.refs + e, 1) <= 0) {      // a count that did not match the table
-        atomicAdd(a.refs + e, 1);
-        latch_error(a.err, DEVERR_BOUNDS);
-      }
-    }
-  }
-  __syncthreads();
-  // ---- share ----
-  if (a.parent) {
-    for (int b = warp; b < a.B; b += PLAN_WARPS) {
-      const int nb = __ldcg(a.state + b), p = a.parent[b];
-      if (nb < 0 || p < 0) continue;
-#pragma unroll 4
-      for (int j = lane; j < nb; j += 32) {
-        const int e = __ldcg(a.table + (size_t)p * a.tab_w + j);
-        a.table[(size_t)b * a.tab_w + j] = e;
-        atomicAdd(a.refs + e, 1);
-      }
-    }
-    __syncthreads();
-  }
-  // ---- count ----
-  for (int b = warp; b < a.B; b += PLAN_WARPS) {
-    const int nb = __ldcg(a.state + b);
-    int missing = 0, last = 0;
-    if (nb > 0) {
-      const int* row = a.table + (size_t)b * a.tab_w;
-#pragma unroll 4
-      for (int j = lane; j < nb; j += 32) missing += __ldcg(row + j) < 0;
-      missing = __reduce_add_sync(0xffffffffu, missing);
-      const int e = __ldcg(row + nb - 1);
-      if ((a.length[b] & (block - 1)) && e >= 0) {
-        if (e >= a.n_blocks) {
-          if (lane == 0) latch_error(a.err, DEVERR_BOUNDS);
-        } else {
-          last = __ldcg(a.refs + e) > 1;
+        for (int j = lane; j < a.tab_w; j += 32) {
+          const int e = __ldcg(row + j), x = j < nb ? __ldcg(from + j) : -1;
+          row[j] = x;
+          last = j == end ? x : last;
+          if (x >= 0) atomicAdd(a.refs + x, 1);
+          if (e >= 0) release(a, e);
         }
+      } else {
+#pragma unroll 8
+        for (int j = lane; j < a.tab_w; j += 32) {
+          const int e = __ldcg(row + j);
+          if (j < nb) {
+            missing += e < 0;
+            last = j == end ? e : last;
+          } else if (e >= 0) {
+            row[j] = -1;
+            release(a, e);
+          }
+        }
+        missing = __reduce_add_sync(0xffffffffu, missing);
       }
     }
+    last = __reduce_max_sync(0xffffffffu, last);
     if (lane == 0) {
-      a.need[b] = missing + last;
-      a.shared[b] = last;
+      state[b] = ok ? nb : -1;
+      need[b] = missing;
+      tail[b] = last;
     }
   }
   __syncthreads();
+  // ---- last; the first counts are on their way meanwhile ----
+  int counts[PLAN_COUNTS];
+  auto load_counts = [&](int b0) {
+    const int at = b0 + PLAN_COUNTS * threadIdx.x;
+#pragma unroll
+    for (int i = 0; i < PLAN_COUNTS; i += 4) {
+      int4 v = make_int4(1, 1, 1, 1);
+      if (at + i + 3 < a.n_blocks && !(reinterpret_cast<uintptr_t>(a.refs) & 15)) {
+        v = __ldcg(reinterpret_cast<const int4*>(a.refs + at + i));
+      } else {
+        if (at + i < a.n_blocks) v.x = __ldcg(a.refs + at + i);
+        if (at + i + 1 < a.n_blocks) v.y = __ldcg(a.refs + at + i + 1);
+        if (at + i + 2 < a.n_blocks) v.z = __ldcg(a.refs + at + i + 2);
+        if (at + i + 3 < a.n_blocks) v.w = __ldcg(a.refs + at + i + 3);
+      }
+      counts[i] = v.x; counts[i + 1] = v.y; counts[i + 2] = v.z; counts[i + 3] = v.w;
+    }
+  };
+  load_counts(0);
   int wanted = 0;
   for (int b0 = 0; b0 < a.B; b0 += PLAN_THREADS) {
     const int b = b0 + threadIdx.x;
-    const int v = b < a.B ? __ldcg(a.need + b) : 0;
+    int v = 0;
+    if (b < a.B) {
+      const int e = tail[b];
+      v = need[b];
+      if (e >= a.n_blocks) {
+        latch_error(a.err, DEVERR_BOUNDS);
+      } else if (e >= 0 && __ldcg(a.refs + e) > 1) {
+        state[b] = state[b] | PLAN_LAST;
+        ++v;
+      }
+    }
     int total;
     const int before = block_scan(v, warp_sums, total);
-    if (b < a.B) a.need[b] = wanted + before;
+    if (b < a.B) need[b] = wanted + before;
     wanted += total;
   }
   if (wanted == 0) return;      // (the same in all threads)
   // ---- find ----
+  volatile int* found_at = wanted <= PLAN_FOUND ? sh_found : a.found;
   int found = 0;
-  for (int b0 = 0; b0 < a.n_blocks && found < wanted; b0 += 4 * PLAN_THREADS) {
-    int free_[4], n = 0;
-    const int at = b0 + 4 * threadIdx.x;
+  for (int b0 = 0; b0 < a.n_blocks && found < wanted; b0 += PLAN_COUNTS * PLAN_THREADS) {
+    if (b0) load_counts(b0);
+    int n = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      free_[i] = at + i < a.n_blocks && __ldcg(a.refs + at + i) == 0;
-      n += free_[i];
-    }
+    for (int i = 0; i < PLAN_COUNTS; ++i) n += counts[i] == 0;
     int total;
     int rank = found + block_scan(n, warp_sums, total);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (free_[i]) {
-        if (rank < wanted) a.found[rank] = at + i;
+    for (int i = 0; i < PLAN_COUNTS; ++i)
+      if (counts[i] == 0) {
+        if (rank < wanted) found_at[rank] = b0 + PLAN_COUNTS * threadIdx.x + i;
         ++rank;
       }
     found += total;
@@ -191,12 +202,13 @@ __global__ void __launch_bounds__(PLAN_THREADS, 1) kv8_plan_k(const PlanArgs a) 
   __syncthreads();
   // ---- assign ----
   for (int b = warp; b < a.B; b += PLAN_WARPS) {
-    const int nb = __ldcg(a.state + b);
-    if (nb <= 0) continue;
-    const int rank0 = __ldcg(a.need + b), last = __ldcg(a.shared + b);
-    if (b + 1 < a.B ? __ldcg(a.need + b + 1) == rank0 : wanted == rank0) continue;
+    const int st = state[b], rank0 = need[b];
+    if (st <= 0 || (b + 1 < a.B ? need[b + 1] == rank0 : wanted == rank0)) continue;
+    const int nb = st & (PLAN_LAST - 1);
+    const bool last = st & PLAN_LAST;
     int* row = a.table + (size_t)b * a.tab_w;
     int rank = rank0;
+#pragma unroll 4
     for (int j0 = 0; j0 < nb; j0 += 32) {
       const int j = j0 + lane;
       const int e = j < nb ? __ldcg(row + j) : 0;
@@ -205,7 +217,7 @@ __global__ void __launch_bounds__(PLAN_THREADS, 1) kv8_plan_k(const PlanArgs a) 
       const int mine = rank + __popc(who & ((1u << lane) - 1));
       rank += __popc(who);
       if (!take || mine >= found) continue;
-      const int blk = __ldcg(a.found + mine);
+      const int blk = found_at[mine];
       row[j] = blk;
       a.refs[blk] = 1;
       if (replace) {
@@ -213,7 +225,7 @@ __global__ void __launch_bounds__(PLAN_THREADS, 1) kv8_plan_k(const PlanArgs a) 
         const int c = atomicAdd(a.copies, 1);
         a.copies[1 + 3 * c] = e;
         a.copies[2 + 3 * c] = blk;
-        a.copies[3 + 3 * c] = a.length[b] & (block - 1);
+        a.copies[3 + 3 * c] = __ldcg(a.length + b) & (block - 1);
       }
     }
   }
@@ -258,10 +270,11 @@ __global__ void __launch_bounds__(COPY_THREADS)
   const int b = blockIdx.x / parts, part = blockIdx.x % parts;
   if (threadIdx.x < 32) {
     const int lane = threadIdx.x;
-    const int len = min(acc_len[b], min(Dmax, MOST)), n = n_old[b];
-    bool bad = acc_len[b] > Dmax;
+    const int took = acc_len[b], n = n_old[b], node = lane < Dmax ? acc_path[(size_t)b * Dmax + lane] : 0;
+    const int len = min(took, min(Dmax, MOST));
+    bool bad = took > Dmax;
     if (lane < len) {
-      const long long f = (long long)n + acc_path[(size_t)b * Dmax + lane], t = (long long)n + lane + 1;
+      const long long f = (long long)n + node, t = (long long)n + lane + 1;
       const bool in = n >= 0 && f >= 0 && f < c.cap && t < c.cap;
       const long long fv = in ? kv8_vec(c, b, 0, (int)f) : -1, tv = in ? kv8_vec(c, b, 0, (int)t) : -1;
       const bool ok = fv >= 0 && tv >= 0;
@@ -346,7 +359,7 @@ int kv8_resize(cudaStream_t st, const Kv8& c, const Kv8Layer* layers, int n_laye
   int* s = static_cast<int*>(scratch);
   a.state = s;
   a.need = s + c.max_batch;
-  a.shared = s + 2 * (size_t)c.max_batch;
+  a.tail = s + 2 * (size_t)c.max_batch;
   a.copies = s + 3 * (size_t)c.max_batch;
   a.found = reinterpret_cast<int*>(static_cast<char*>(scratch) + align256((size_t)c.max_batch * 6 * 4 + 4));
   cudaError_t e = launch_k(kv8_plan_k, dim3(1), dim3(PLAN_THREADS), 0, st, a);
@@ -356,7 +369,7 @@ int kv8_resize(cudaStream_t st, const Kv8& c, const Kv8Layer* layers, int n_laye
     const LayerSet set = layer_set(layers, l0, n);
     // at most one copy a sequence; CTAs past the copies that there are end at once
     const long long most = ((long long)B * n * 2 * c.nkv + COPY_THREADS / 32 - 1) / (COPY_THREADS / 32);
-    const unsigned grid = (unsigned)(most < 152 * 4 ? most : 152 * 4);
+    const unsigned grid = (unsigned)(most < 152 * 8 ? most : 152 * 8);
     e = launch_k(kv8_copy_k, dim3(grid), dim3(COPY_THREADS), 0, st, set, n, c.nkv, c.d, c.block_log2, (const int*)a.copies);
     if (e != cudaSuccess || cudaGetLastError() != cudaSuccess) return -4;
   }

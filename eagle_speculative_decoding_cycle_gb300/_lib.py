@@ -38,7 +38,7 @@ EXPORTED = [
     "eagle_op_kv8_write", "eagle_op_kv8_read", "eagle_op_attention_kv8_scratch_bytes", "eagle_op_attention_kv8",
     "eagle_op_attention_shared_kv8",
     "eagle_op_kv8_compact", "eagle_op_kv8_resize_scratch_bytes", "eagle_op_kv8_resize",
-    "eagle_rope_frequencies", "eagle_rope_turns", "eagle_op_rope", "eagle_op_attention_prompt",
+    "eagle_rope_frequencies", "eagle_rope_turns", "eagle_op_rope", "eagle_op_attention_prompt_scratch_bytes", "eagle_op_attention_prompt",
 ]
 
 
@@ -149,8 +149,9 @@ def _declare(lib: C.CDLL) -> None:
         "eagle_rope_turns": (i32, [i32, P(C.c_double), P(u64)]),
         "eagle_op_rope": (i32, [vp, i32, i32, vp, i64, vp, i64, i32, vp, i64, vp, i64, i32, i32, i32, i32, i32, vp, vp, f32,
                                 i32]),
+        "eagle_op_attention_prompt_scratch_bytes": (sz, [i32] * 6),
         "eagle_op_attention_prompt": (i32, [vp, vp, i64, vp, i64, vp, i64, vp, i64, vp, i32, i32, i32, i32, i32, i32, vp, vp,
-                                            f32, vp]),
+                                            f32, vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)

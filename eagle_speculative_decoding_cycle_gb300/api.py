@@ -788,11 +788,12 @@ def rope(plan: Rope, q: torch.Tensor, k: Optional[torch.Tensor], pos: torch.Tens
 def attention_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_start: torch.Tensor,
                      k_start: Optional[torch.Tensor] = None, scale: float = 0.0, out: Optional[torch.Tensor] = None,
                      lse: Optional[torch.Tensor] = None, err: Optional[torch.Tensor] = None,
-                     stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+                     stream: Optional[torch.cuda.Stream] = None, scratch: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Causal attention of packed sequences: rows q[q_start[b]:q_start[b + 1]] ([R][nq][d] bf16) over keys and values
     k, v[k_start[b]:k_start[b + 1]] ([Rk][nkv][d]; default: the rows' starts), the last row seeing all of them. Row strides
     are free. q_start, k_start: int32 [B + 1] on the device. lse: float32 [R][nq] to fill with the rows' log-sum-exps. Rows
-    of no sequence are not written."""
+    of no sequence are not written. scratch: uint8, made here where it is of use and none is given; an empty one keeps a
+    row's result independent of the batch, bit for bit (calls of few rows over many keys are slower so)."""
     index, shape = q.get_device(), q.shape
     if index < 0 or q.dtype is not torch.bfloat16 or k.dtype is not torch.bfloat16 or v.dtype is not torch.bfloat16:
         raise ValueError("q, k and v must be bfloat16 tensors of a GPU")
@@ -823,8 +824,19 @@ def attention_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_start:
               "err must be an int32 tensor on q's device")
     if _elsewhere(index):
         with torch.cuda.device(index):
-            return attention_prompt(q, k, v, q_start, k_start, scale, out, lse, err, stream)
-    rc = L.lib().eagle_op_attention_prompt(_stream_of(index, stream), q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv,
-                                           out.data_ptr(), ldo, _ptr(lse), R, kshape[0], nq, kshape[1], d, n - 1, q_start.data_ptr(), k_start.data_ptr(), scale, _ptr(err))
+            return attention_prompt(q, k, v, q_start, k_start, scale, out, lse, err, stream, scratch)
+    lib, work, nb = L.lib(), None, 0
+    if scratch is None:
+        nb = lib.eagle_op_attention_prompt_scratch_bytes(R, kshape[0], nq, kshape[1], d, n - 1)
+        if nb:
+            with _owned_by(stream):
+                scratch = torch.empty(nb, dtype=torch.uint8, device=q.device)
+            work = scratch.data_ptr()
+    elif scratch.numel():
+        _need(scratch.dtype is torch.uint8 and scratch.is_contiguous() and scratch.get_device() == index,
+              "scratch must be a contiguous uint8 tensor on q's device")
+        work, nb = scratch.data_ptr(), scratch.numel()
+    rc = lib.eagle_op_attention_prompt(_stream_of(index, stream), q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv,
+                                           out.data_ptr(), ldo, _ptr(lse), R, kshape[0], nq, kshape[1], d, n - 1, q_start.data_ptr(), k_start.data_ptr(), scale, work, nb, _ptr(err))
     L.check(rc, "eagle_op_attention_prompt")
     return out

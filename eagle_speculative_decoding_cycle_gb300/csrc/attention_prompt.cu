@@ -33,6 +33,7 @@
 #include "kernels.h"
 #include "ops_ext.h"
 
+#include <algorithm>
 #include <cuda_bf16.h>
 
 namespace eagle {
@@ -52,7 +53,7 @@ struct ApShape {
   static constexpr int QB = HALVES * QHALF, KB = HALVES * KHALF;          // a tile of Q, of K or V
   static constexpr int STAGES = 8;
   static constexpr int OFF_RING = 2 * QB, OFF_BAR = OFF_RING + STAGES * KB;
-  static constexpr int OFF_ITEM = OFF_BAR + 448, OFF_BAD = OFF_ITEM + 2 * 32, OFF_INV = OFF_BAD + 2 * D * 4;
+  static constexpr int OFF_ITEM = OFF_BAR + 448, OFF_BAD = OFF_ITEM + 2 * 48, OFF_INV = OFF_BAD + 2 * D * 4;
   static constexpr int BYTES = OFF_INV + 2 * AT * 4;
   // TMEM columns: O of both tiles, then S and P of each
   static constexpr int T_S = 2 * D, T_P = T_S + KT, T_STEP = (512 - 2 * D) / 2;
@@ -62,9 +63,10 @@ struct ApShape {
   static_assert(2 * R_SOFT + R_OUT + R_ONE <= 4 * 128, "registers of the launch");
 };
 
-// What a CTA does next. lim0: the last key that the first row sees (negative: none); rows of tile 0 and 1; key tiles of each.
+// What a CTA does next. lim0: the last key, from k0 on, that the first row sees (negative: none); rows of tile 0 and 1; key tiles
+// of each; slot: where the sums of a piece of an item go, -1 for a whole one.
 struct ApItem {
-  int h, row0, rows[2], n[2], k0, lim0;
+  int h, row0, rows[2], n[2], k0, lim0, slot;
 };
 
 struct ApArgs {
@@ -75,6 +77,9 @@ struct ApArgs {
   long long ldo;
   float* lse;
   int* err;
+  float *part_o, *part_ml;     // split: [slot][2 tiles][128][D], [slot][2 tiles][128][2]
+  struct ApStart* starts;      // split: [CTA]
+  struct ApJoin* joins;        // split: [CTA]
 };
 
 // One sequence's rows and keys; none where the starts are not in order or out of range.
@@ -177,6 +182,113 @@ __device__ __forceinline__ ApItem ap_item(const ApArgs& a, ApList& l, long long 
     return it;
   }
   return it;      // not reached
+}
+
+// ---- few items: their key tiles, laid end to end, cut into equal ranges, one a CTA -------------------------------------
+// The items in order: pairs of tiles of the sequences one after another, the heads of a pair side by side. An item has as
+// many units as key tiles, one where its rows see nothing. prompt_plan_k finds where each range starts.
+struct ApStart { int b, t, h, j, units, pad[3]; };      // sequence, pair, head, key tile; units of the range
+struct ApJoin { int row0, rows[2], h, first, last, pad[2]; };   // the item that starts in a range and ends behind it: its first
+                                                       // piece's slot, the CTA of its last one; h = -1: none
+constexpr int AP_LEAST = 4;         // units that a range has at least: its ends cost as much
+constexpr int AP_PLAN = 512;        // threads of the plan: pairs, sequences and CTAs are fewer
+
+template <int KT>
+__device__ __forceinline__ int ap_tiles(const ApArgs& a, const ApSeq& s, int t) {
+  const int last = s.lk - s.lq + min((t + 1) * 2 * a.RB, s.lq) - 1;
+  return last >= 0 ? last / KT + 1 : 1;
+}
+__device__ __forceinline__ void ap_rows(const ApArgs& a, const ApSeq& s, int t, int* rows) {
+  const int left = s.lq - t * 2 * a.RB;
+  rows[0] = min(a.RB, left);
+  rows[1] = max(0, min(a.RB, left - a.RB));
+}
+
+// Exclusive sums of a value a thread, and the total.
+__device__ __forceinline__ int ap_block_scan(int v, int* sums, int& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) sums[warp] = x;
+  __syncthreads();
+  const int w = lane < AP_PLAN / 32 ? sums[lane] : 0;
+  total = __reduce_add_sync(0xffffffffu, w);
+  const int before = __reduce_add_sync(0xffffffffu, lane < warp ? w : 0);
+  __syncthreads();
+  return before + x - v;
+}
+// The last of n rising values that is at most u.
+__device__ __forceinline__ int ap_find(const int* v, int n, int u) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (v[mid] <= u) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+template <int KT>
+__global__ void __launch_bounds__(AP_PLAN) prompt_plan_k(const ApArgs a, int grid) {
+  __shared__ int sums[32], pair0[AP_PLAN], unit0[AP_PLAN];
+  PDL_ENTRY();
+  const int i = threadIdx.x;
+  ApSeq s{0, 0, 0, 0};
+  bool bad = false;
+  if (i < a.B) s = ap_seq(a, i, bad);
+  if (bad) latch_error(a.err, DEVERR_BOUNDS);
+  int pairs, units;
+  pair0[i] = ap_block_scan(ap_pairs(a, s.lq), sums, pairs);
+  __syncthreads();
+  // (equal values: the last one, so the sequence that has the pair)
+  int b = 0, t = 0, n = 0;
+  if (i < pairs) {
+    b = ap_find(pair0, a.B, i);
+    t = i - pair0[b];
+    s = ap_seq(a, b, bad);
+    n = ap_tiles<KT>(a, s, t);
+  }
+  unit0[i] = ap_block_scan(n * a.nkv, sums, units);
+  __syncthreads();
+  const int shares = max(1, min(grid, units / AP_LEAST));
+  if (i >= grid) return;
+  ApStart st{};
+  ApJoin jn{};
+  jn.h = -1;
+  if (i < shares && units > 0) {
+    const int u0 = (int)((long long)units * i / shares), u1 = (int)((long long)units * (i + 1) / shares);
+    int p = ap_find(unit0, pairs, u0);
+    st.b = ap_find(pair0, a.B, p);
+    st.t = p - pair0[st.b];
+    s = ap_seq(a, st.b, bad);
+    n = ap_tiles<KT>(a, s, st.t);
+    st.h = (u0 - unit0[p]) / n;
+    st.j = (u0 - unit0[p]) % n;
+    st.units = u1 - u0;
+    if (u1 > u0) {
+      p = ap_find(unit0, pairs, u1 - 1);
+      b = ap_find(pair0, a.B, p);
+      t = p - pair0[b];
+      s = ap_seq(a, b, bad);
+      n = ap_tiles<KT>(a, s, t);
+      const int h = (u1 - 1 - unit0[p]) / n, from = unit0[p] + h * n;
+      if (from >= u0 && from + n > u1) {
+        jn.h = h;
+        jn.row0 = s.r0 + t * 2 * a.RB;
+        ap_rows(a, s, t, jn.rows);
+        jn.first = 2 * i + (from == u0 ? 0 : 1);
+        int y = i + 1;
+        while (y + 1 < shares && (int)((long long)units * (y + 1) / shares) < from + n) ++y;
+        jn.last = y;
+      }
+    }
+  }
+  a.starts[i] = st;
+  a.joins[i] = jn;
 }
 
 // Whether key tile j holds keys that a row of the tiles that use it does not see, and the last one that all of them see.
@@ -337,7 +449,7 @@ __device__ __forceinline__ bool ap_clean(uint8_t* v, int r0, int key0, int lim0,
   return true;
 }
 
-template <int D>
+template <int D, bool SPLIT>
 __global__ void __launch_bounds__(AP_THREADS, 1)
     prompt_k(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
              const __grid_constant__ CUtensorMap tmV, const ApArgs a) {
@@ -485,7 +597,11 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
       }
       if (!ok) break;
       if (it.rows[mt] > 0) {
-        if (pos < it.rows[mt] && a.lse) {      // (so pos < RB: not the vectors behind the last head)
+        const bool piece = SPLIT && it.slot >= 0;
+        if (piece) {
+          float2* ml = reinterpret_cast<float2*>(a.part_ml) + (size_t)(it.slot * 2 + mt) * AT + qv;
+          *ml = make_float2(m2, l);
+        } else if (pos < it.rows[mt] && a.lse) {      // (so pos < RB: not the vectors behind the last head)
           const float ref = m2 == -INFINITY ? 0.f : m2;
           a.lse[(long long)(it.row0 + mt * a.RB + pos) * a.nq + it.h * a.G + qv - pos * a.G] =
               l == 0.f ? -INFINITY : (ref + log2f(l)) * 0.693147180559945309f;
@@ -494,7 +610,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
           ok = ap_wait(smem_u32(l_free + mt), l_phase, abort_flag, a.err);
           if (!ok) break;
           l_phase ^= 1;
-          inv[mt * AT + qv] = l == 0.f ? 0.f : 1.f / l;
+          inv[mt * AT + qv] = piece ? 1.f : l == 0.f ? 0.f : 1.f / l;
           warp_arrive(smem_u32(l_full + mt));
         }
       }
@@ -521,7 +637,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
 #pragma unroll 1
       for (int mt = 0; mt < 2; ++mt) {
         const int rows = it.rows[mt], nt = it.n[mt];
-        if (rows <= 0) continue;
+        if (rows <= 0 || (SPLIT && it.slot >= 0 && !nt)) continue;
         __nv_bfloat16* base = a.out + (long long)(it.row0 + mt * a.RB) * a.ldo + (long long)it.h * a.G * D;
         if (nt) {
           ok = ap_wait(smem_u32(l_full + mt), phase >> mt & 1, abort_flag, a.err) &&
@@ -550,6 +666,18 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
             part[0] = part[1] = 0.f;
 #pragma unroll
             for (int x = 0; x < 32; ++x) o[x] = 0.f;
+          }
+          if (SPLIT && it.slot >= 0) {
+            // two neighbours exchange pairs: 16 bytes a thread, of the first eight rows or of the other
+            const int odd = quad & 1;
+            float* part = a.part_o + ((size_t)(it.slot * 2 + mt) * AT + lane0 + f * 16 + (lane >> 2) + 8 * odd) * D + c + (quad >> 1) * 4;
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+              const float* v = o + 4 * x;
+              const float g0 = __shfl_xor_sync(0xffffffffu, odd ? v[0] : v[2], 1), g1 = __shfl_xor_sync(0xffffffffu, odd ? v[1] : v[3], 1);
+              *reinterpret_cast<float4*>(part + x * 8) = odd ? make_float4(g0, g1, v[2], v[3]) : make_float4(v[0], v[1], g0, g1);
+            }
+            continue;
           }
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
@@ -580,7 +708,9 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
               if (i >= (int)((x >> 10) & 1023)) add += INFINITY;
               if (i >= (int)((x >> 20) & 1023)) add -= INFINITY;      // (both: NaN)
               if (i >= (int)(x & 1023)) add = __int_as_float(0x7fffffff);
-              if (add != 0.f) o[c] = __float2bfloat16_rn(__bfloat162float(o[c]) + add);
+              if (add == 0.f) continue;
+              if (SPLIT && it.slot >= 0) a.part_o[((size_t)(it.slot * 2 + mt) * AT + lane0 + lane) * D + c] += add;
+              else o[c] = __float2bfloat16_rn(__bfloat162float(o[c]) + add);
             }
           }
         }
@@ -593,6 +723,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
     if (warp == AP_TMA) {
       // ---- items, TMA ----
       ApList list{};
+      ApStart at0{};      // split: where this CTA goes on
       const uint32_t qbytes = (uint32_t)(Sh::HALVES * a.RB * a.G * 128);
       uint32_t used = 0;                // loads of Q: of tile 0 in the low half, of tile 1 in the high half
       int s = 0;                        // stages of the ring so far
@@ -601,14 +732,54 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
       // The loads of item n - 1; halfway item n is found and its Q brought into L2, behind them it is published.
 #pragma unroll 1
       for (int n = 0, m = 0;; ++n, ++m) {      // slots, items of this pass
-        if (m == 0) list = ap_begin(a, n == 0 && blockIdx.x == 0);
+        if (m == 0) {
+          if constexpr (SPLIT) {
+            at0 = a.starts[blockIdx.x];
+          } else {
+            list = ap_begin(a, n == 0 && blockIdx.x == 0);
+          }
+        }
         const int nt = max(it.n[0], it.n[1]);
 #pragma unroll 1
         for (int x = 0; ok && x < max(1, 2 * nt); ++x) {
           if (x == nt) {
-            // to and fro over the CTAs: who takes the largest of one round takes the smallest of the next
-            const int at = m & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
-            next = ap_item<KT>(a, list, at + (long long)m * gridDim.x);
+            if constexpr (SPLIT) {
+              next.h = -1;
+              if (at0.units > 0) {
+                bool bad_;
+                ApSeq q = ap_seq(a, at0.b, bad_);
+#pragma unroll 1
+                while (at0.t >= ap_pairs(a, q.lq)) {      // (ends: there are units left)
+                  q = ap_seq(a, ++at0.b, bad_);
+                  at0.t = 0;
+                }
+                const int tiles = ap_tiles<KT>(a, q, at0.t), j0 = at0.j, j1 = min(tiles, j0 + at0.units);
+                next.h = at0.h;
+                next.row0 = q.r0 + at0.t * 2 * a.RB;
+                ap_rows(a, q, at0.t, next.rows);
+                // slot 0 for a piece at the start of the CTA's range, 1 for one at its end
+                next.slot = j0 == 0 && j1 == tiles ? -1 : 2 * blockIdx.x + (m == 0 ? 0 : 1);
+                next.k0 = q.k0 + j0 * KT;
+                const int lim = q.lk - q.lq + at0.t * 2 * a.RB;
+                next.lim0 = lim - j0 * KT;
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                  const int last = lim + y * a.RB + next.rows[y] - 1, all = next.rows[y] > 0 && last >= 0 ? last / KT + 1 : 0;
+                  next.n[y] = max(0, min(all, j1) - j0);
+                }
+                at0.units -= j1 - j0;
+                at0.j = 0;
+                if (++at0.h == a.nkv) {
+                  at0.h = 0;
+                  ++at0.t;
+                }
+              }
+            } else {
+              // to and fro over the CTAs: who takes the largest of one round takes the smallest of the next
+              const int at = m & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
+              next = ap_item<KT>(a, list, at + (long long)m * gridDim.x);
+              next.slot = -1;
+            }
             if (next.h >= 0 && elect_one())
 #pragma unroll 1
               for (int y = 0; y < 2 * Sh::HALVES; ++y)
@@ -809,6 +980,74 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
   }
 }
 
+// The pieces of the item that starts in CTA x's range and ends behind it: 16 of its 256 query vectors a block, a warp for
+// each, D / 32 columns a lane. The weights of up to 32 pieces come first, a piece a lane, so that the sums' loads wait for
+// nothing.
+constexpr int AP_JOIN = 16;      // blocks an item
+template <int D>
+__global__ void __launch_bounds__(256) prompt_join_k(const ApArgs a) {
+  constexpr int C = D / 32;
+  PDL_ENTRY();
+  const int x = blockIdx.x / AP_JOIN, lane = threadIdx.x & 31;
+  const ApJoin r = a.joins[x];
+  if (r.h < 0) return;
+#pragma unroll 1
+  for (int i = 0; i < 256 / AP_JOIN; i += 8) {
+    const int v = blockIdx.x % AP_JOIN * (256 / AP_JOIN) + i + (threadIdx.x >> 5), mt = v / AT, qv = v % AT;
+    const int pos = qv / a.G;
+    if (pos >= r.rows[mt]) continue;
+    const int pieces = r.last - x + 1;
+    auto place = [&](int y) { return (size_t)((y ? 2 * (x + y) : r.first) * 2 + mt) * AT + qv; };
+    // (a piece with no key that this row sees has no sum, and its columns are not written)
+    float m = -INFINITY, l = 0.f, o[C];
+#pragma unroll 1
+    for (int y = lane; y < pieces; y += 32) {
+      const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + place(y));
+      if (ml.y != 0.f) m = fmaxf(m, ml.x);
+    }
+    m = warp_max(m);
+#pragma unroll
+    for (int c = 0; c < C; ++c) o[c] = 0.f;
+#pragma unroll 1
+    for (int y0 = 0; y0 < pieces; y0 += 32) {
+      float2 ml = make_float2(0.f, 0.f);
+      if (y0 + lane < pieces) ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + place(y0 + lane));
+      const float w = ml.y != 0.f ? exp2f(ml.x - m) : 0.f;
+      l += warp_sum(ml.y != 0.f ? ml.y * w : 0.f);
+      const unsigned there = __ballot_sync(0xffffffffu, ml.y != 0.f);
+      const int n = min(32, pieces - y0);
+#pragma unroll 8
+      for (int y = 0; y < n; ++y) {
+        const float f = __shfl_sync(0xffffffffu, w, y);
+        const float* at = a.part_o + place(y0 + y) * D;
+        float p[C];
+#pragma unroll
+        for (int c = 0; c < C; ++c) p[c] = 0.f;
+        if (there >> y & 1) {
+          if constexpr (C == 4) {
+            const float4 q = __ldcg(reinterpret_cast<const float4*>(at) + lane);
+            p[0] = q.x; p[1] = q.y; p[2] = q.z; p[3] = q.w;
+          } else {
+            const float2 q = __ldcg(reinterpret_cast<const float2*>(at) + lane);
+            p[0] = q.x; p[1] = q.y;
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < C; ++c) o[c] += p[c] * f;
+      }
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const int row = r.row0 + mt * a.RB + pos, head = r.h * a.G + qv - pos * a.G;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + (long long)row * a.ldo + (long long)head * D + lane * C);
+    if constexpr (C == 4)
+      *reinterpret_cast<uint2*>(dst) = make_uint2(bf16_pair(o[0] * inv, o[1] * inv), bf16_pair(o[2] * inv, o[3] * inv));
+    else
+      *dst = bf16_pair(o[0] * inv, o[1] * inv);
+    if (a.lse && lane == 0)
+      a.lse[(long long)row * a.nq + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.693147180559945309f;
+  }
+}
+
 // bf16 rows of `heads` vectors of d, ld elements from a row to the next, as boxes of 64 x b1 heads x b2 rows.
 bool ap_map(CUtensorMap* m, const void* p, int d, int heads, long long rows, long long ld, int b1, int b2) {
   const auto fn = pf_encode();
@@ -821,16 +1060,39 @@ bool ap_map(CUtensorMap* m, const void* p, int d, int heads, long long rows, lon
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D>
+template <int D, bool SPLIT>
 cudaError_t launch_prompt(cudaStream_t st, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                           const ApArgs& p, int grid) {
   static_assert(ApShape<D>::BYTES <= 227 * 1024, "shared memory of a CTA");
-  const cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(prompt_k<D>), ApShape<D>::BYTES);
+  cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(prompt_k<D, SPLIT>), ApShape<D>::BYTES);
   if (e != cudaSuccess) return e;
-  return launch_k(prompt_k<D>, dim3(grid), dim3(AP_THREADS), ApShape<D>::BYTES, st, q, k, v, p);
+  if (SPLIT) e = launch_k(prompt_plan_k<ApShape<D>::KT>, dim3(1), dim3(AP_PLAN), 0, st, p, grid);
+  if (e != cudaSuccess) return e;
+  e = launch_k(prompt_k<D, SPLIT>, dim3(grid), dim3(AP_THREADS), ApShape<D>::BYTES, st, q, k, v, p);
+  if (e == cudaSuccess && SPLIT) e = launch_k(prompt_join_k<D>, dim3(grid * AP_JOIN), dim3(256), 0, st, p);
+  return e;
 }
 
 }  // namespace
+
+// Whether to split, from what the host knows, the rows and keys in all. A whole item takes its key tiles (1 us each), a range
+// its share of all items' and some AP_EXTRA more: the plan, the pieces' sums (up to 40 MB through L2) and the join. Heads of 128, 32
+// over 8, whole / split: 1 row behind 4096 keys 56 / 21 us, 61 rows 61 / 28, 512 rows behind 3584 64 / 49, 8 x 1 row behind 2048
+// (15 by the rule) 32 / 27; 4 x 200 rows behind 1800 (8) 39 / 52, a whole prompt of 1024 (2) 23 / 38.
+constexpr int AP_EXTRA = 14;
+static bool prompt_split(int R, int Rk, int G, int nkv, int d, int B, int sms) {
+  const int RB = AT / G, KT = d == 128 ? ApShape<128>::KT : ApShape<64>::KT;
+  const long long most = (long long)R / (2 * RB) + B;      // pairs
+  if (most > AP_PLAN || sms > AP_PLAN || most * nkv > 8 * sms) return false;
+  const double items = (double)std::max((long long)B, ((long long)R + 2 * RB - 1) / (2 * RB)) * nkv, tiles = (double)Rk / B / KT;
+  return most * nkv * ((double)Rk / KT + 1) < 1 << 30 && tiles - items * tiles / sms > AP_EXTRA;
+}
+
+size_t prompt_attention_scratch(int R, int Rk, int nq, int nkv, int d, int B) {
+  const int sms = device_sm_count();
+  if (sms < 1 || !prompt_split(R, Rk, nq / nkv, nkv, d, B, sms)) return 0;
+  return (size_t)2 * sms * 2 * AT * (d + 2) * sizeof(float) + (size_t)sms * (sizeof(ApStart) + sizeof(ApJoin));
+}
 
 int prompt_attention(cudaStream_t st, const PromptArgs& a) {
   ApArgs p{};
@@ -842,7 +1104,15 @@ int prompt_attention(cudaStream_t st, const PromptArgs& a) {
   const long long most = ((long long)a.R / (2 * p.RB) + a.B) * a.nkv;
   const int sms = device_sm_count();
   if (sms < 1) return -4;
-  const int grid = (int)(most < sms ? most : sms);
+  const size_t need = prompt_attention_scratch(a.R, a.Rk, a.nq, a.nkv, a.d, a.B);
+  const bool split = need && a.scratch && a.scratch_bytes >= need;
+  if (split) {
+    p.part_o = static_cast<float*>(a.scratch);
+    p.part_ml = p.part_o + (size_t)2 * sms * 2 * AT * a.d;
+    p.starts = reinterpret_cast<ApStart*>(p.part_ml + (size_t)2 * sms * 2 * AT * 2);
+    p.joins = reinterpret_cast<ApJoin*>(p.starts + sms);
+  }
+  const int grid = split ? sms : (int)(most < sms ? most : sms);
   CUtensorMap q, k, v;
   // without keys K and V are not read; their maps still need memory
   const bool none = a.Rk == 0;
@@ -851,7 +1121,8 @@ int prompt_attention(cudaStream_t st, const PromptArgs& a) {
       !ap_map(&k, none ? a.q : a.k, a.d, none ? a.nq : a.nkv, none ? a.R : a.Rk, none ? a.ldq : a.ldk, 1, KT) ||
       !ap_map(&v, none ? a.q : a.v, a.d, none ? a.nq : a.nkv, none ? a.R : a.Rk, none ? a.ldq : a.ldv, 1, KT))
     return -4;
-  const cudaError_t e = a.d == 128 ? launch_prompt<128>(st, q, k, v, p, grid) : launch_prompt<64>(st, q, k, v, p, grid);
+  const cudaError_t e = a.d == 128 ? (split ? launch_prompt<128, true>(st, q, k, v, p, grid) : launch_prompt<128, false>(st, q, k, v, p, grid))
+                                   : (split ? launch_prompt<64, true>(st, q, k, v, p, grid) : launch_prompt<64, false>(st, q, k, v, p, grid));
   if (e != cudaSuccess) {
     cudaGetLastError();
     return -4;

@@ -501,13 +501,27 @@ int eagle_op_rope(void* stream, int dtype_in, int dtype_out, const void* q, int6
 }
 
 // ---- attention over whole prompts ---------------------------------------------------------------------
-int eagle_op_attention_prompt(void* stream, const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v, int64_t ldv,
-                              void* out, int64_t ldo, float* lse, int R, int Rk, int nq, int nkv, int head_dim, int B,
-                              const int32_t* q_start, const int32_t* k_start, float scale, int32_t* d_err) {
+static int prompt_sizes(int R, int Rk, int nq, int nkv, int head_dim, int B) {
   if (R < 0 || Rk < 0 || nkv < 1 || nq < nkv || nq % nkv || nq / nkv > 64 || (head_dim != 64 && head_dim != 128) || B < 0)
     return EAGLE_EINVAL;
-  if (R == 0 || B == 0) return EAGLE_OK;
   if ((double)R * nq >= 2147483648.0 || (double)Rk + 256 >= 2147483648.0 || nq > 65536 || B > (1 << 24)) return EAGLE_ECAPACITY;
+  return EAGLE_OK;
+}
+
+size_t eagle_op_attention_prompt_scratch_bytes(int R, int Rk, int nq, int nkv, int head_dim, int B) {
+  if (prompt_sizes(R, Rk, nq, nkv, head_dim, B) != EAGLE_OK || R == 0 || B == 0) return 0;
+  return prompt_attention_scratch(R, Rk, nq, nkv, head_dim, B);
+}
+
+int eagle_op_attention_prompt(void* stream, const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v, int64_t ldv,
+                              void* out, int64_t ldo, float* lse, int R, int Rk, int nq, int nkv, int head_dim, int B,
+                              const int32_t* q_start, const int32_t* k_start, float scale, void* scratch, size_t scratch_bytes,
+                              int32_t* d_err) {
+  const int sizes = prompt_sizes(R, Rk, nq, nkv, head_dim, B);
+  if (sizes == EAGLE_EINVAL) return sizes;
+  if (R == 0 || B == 0) return EAGLE_OK;
+  if (sizes != EAGLE_OK) return sizes;
+  if (scratch && !on16(scratch)) return EAGLE_EINVAL;
   const int64_t wq = (int64_t)nq * head_dim, wk = (int64_t)nkv * head_dim, most = (int64_t)1 << 36;
   if (!q || !out || !q_start || !k_start || (Rk && (!k || !v))) return EAGLE_EINVAL;
   if (!on16(q) || !on16(k) || !on16(v) || !on16(out)) return EAGLE_EINVAL;
@@ -523,6 +537,7 @@ int eagle_op_attention_prompt(void* stream, const void* q, int64_t ldq, const vo
   a.R = R; a.Rk = Rk; a.nq = nq; a.nkv = nkv; a.d = head_dim; a.B = B;
   a.start = q_start; a.kstart = k_start;
   a.scale = scale > 0.f ? scale : 1.f / sqrtf((float)head_dim);
+  a.scratch = scratch; a.scratch_bytes = scratch ? scratch_bytes : 0;
   a.err = d_err;
   const int r = prompt_attention(reinterpret_cast<cudaStream_t>(stream), a);
   return r == 0 ? EAGLE_OK : EAGLE_ECUDA;

@@ -30,9 +30,12 @@ struct PromptArgs {
   int R, Rk, nq, nkv, d, B;
   const int *start, *kstart;           // [B + 1]
   float scale;
+  void* scratch;                       // of prompt_attention_scratch's size, or less: then items are not split
+  size_t scratch_bytes;
   int* err;
 };
 int prompt_attention(cudaStream_t st, const PromptArgs& a);
+size_t prompt_attention_scratch(int R, int Rk, int nq, int nkv, int d, int B);      // 0: no use for it
 
 // Code and exponent arrays of one layer: k, v, ke, ve.
 struct Kv8Layer { uint8_t* p[4]; };

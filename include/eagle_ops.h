@@ -269,12 +269,17 @@ int eagle_op_rope(void* stream, int dtype_in, int dtype_out, const void* q, int6
  * any lengths; a sequence whose starts fall, or lie outside [0, R] or [0, Rk], is latched into *d_err (nullable) and
  * skipped. Rows of no sequence are left as they were. out meets none of q, k, v (refused).
  * Products are bf16 with fp32 sums; weights enter the value product as bf16 (2^-8 relative, the type of the values);
- * maxima, sums and lse are fp32. A row's result depends on its own keys alone, bit for bit whatever other sequences
- * hold: keys and values that it does not see, of its own sequence too, may be anything, NaN and infinities
- * among it. */
+ * maxima, sums and lse are fp32. Keys and values that a row does not see, of its own sequence too, may be anything,
+ * NaN and infinities among it: its result is the same bits.
+ * scratch (nullable, 16-byte aligned, no initial value, not shared with a call that may overlap on the GPU): with the bytes that
+ * eagle_op_attention_prompt_scratch_bytes gives for these sizes (0 where there is no use for it) calls of few rows over many
+ * keys have their keys shared out over the GPU, at points that all sequences' lengths move; a row's result can then change in
+ * the last bits of fp32 with the batch. With less, or where 0 is given, it does not depend on the batch. */
+size_t eagle_op_attention_prompt_scratch_bytes(int R, int Rk, int nq, int nkv, int head_dim, int B);
 int eagle_op_attention_prompt(void* stream, const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v, int64_t ldv,
                               void* out, int64_t ldo, float* lse, int R, int Rk, int nq, int nkv, int head_dim, int B,
-                              const int32_t* q_start, const int32_t* k_start, float scale, int32_t* d_err);
+                              const int32_t* q_start, const int32_t* k_start, float scale, void* scratch, size_t scratch_bytes,
+                              int32_t* d_err);
 
 /* EAGLE-2 tree growth and rerank with injected draft confidences, for B sequences:
  * cand_tok/cand_logc [B][k]: the root's children (token, log confidence) in rank order;

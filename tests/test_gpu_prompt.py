@@ -269,17 +269,18 @@ def test_both_infinities_in_one_column():
 
 
 def test_results_do_not_depend_on_the_batch():
-    """A sequence alone and among others, first and last: the same bits."""
+    """A sequence alone and among others, first and last: the same bits (without scratch, so keys are not shared out)."""
     lens, before = [70, 300, 5, 129], [10, 0, 200, 0]
     p = Packed(lens, before, 8, 2, 128, seed=10)
-    out, lse = p.run()
+    none = torch.empty(0, dtype=torch.uint8, device=DEV)
+    out, lse = p.run(scratch=none)
     for b in range(4):
         r, c = slice(p.start[b], p.start[b + 1]), slice(p.kstart[b], p.kstart[b + 1])
         s = torch.empty(lens[b], 8, device=DEV)
-        o = api.attention_prompt(p.q[r], p.k[c], p.v[c], i32([0, lens[b]]), i32([0, lens[b] + before[b]]), lse=s)
+        o = api.attention_prompt(p.q[r], p.k[c], p.v[c], i32([0, lens[b]]), i32([0, lens[b] + before[b]]), lse=s, scratch=none)
         assert torch.equal(o, out[r]) and torch.equal(s, lse[r])
     for _ in range(3):
-        o2, l2 = p.run()
+        o2, l2 = p.run(scratch=none)
         assert torch.equal(o2, out) and torch.equal(l2, lse)
 
 
@@ -306,6 +307,48 @@ def test_joined_by_lse():
     o = o1.double() * torch.exp(l1 - l)[..., None] + o2.double() * torch.exp(l2 - l)[..., None]
     assert float((l - wlse.double()).abs().max()) < 1e-4
     assert float((o - want.double()).abs().max()) <= 2.0 ** -5 * float(p.v.abs().max())
+
+
+@pytest.mark.parametrize("lens,before,nq,nkv,d", [
+    ([1], [2000], 4, 1, 128), ([5, 1], [2800, 900], 28, 4, 128), ([300], [2200], 2, 2, 64), ([40, 2], [1500, 1700], 8, 2, 128),
+    ([1, 1], [4000, 0], 1, 1, 128), ([500], [2000], 4, 2, 128), ([0, 40, 0], [2500, 6500, 3], 64, 1, 64), ([3000], [0], 1, 1, 64),
+    ([1900], [-300], 1, 1, 128), ([130], [1700], 5, 5, 128), ([1], [20000], 2, 1, 64)])
+def test_few_rows_over_many_keys(lens, before, nq, nkv, d):
+    """Items cut into ranges of keys and joined; the same calls without scratch within the tolerances of both."""
+    p = Packed(lens, before, nq, nkv, d, seed=sum(lens) + nq)
+    api_bytes = api.L.lib().eagle_op_attention_prompt_scratch_bytes(p.R, p.K, nq, nkv, d, len(lens))
+    assert api_bytes > 0
+    out, lse = p.check()
+    again, _ = p.run(scratch=torch.full((max(api_bytes, 16),), 0xff, dtype=torch.uint8, device=DEV))
+    assert torch.equal(out, again)
+    rows = int(p.start[-1])
+    whole, wlse = p.run(scratch=torch.empty(0, dtype=torch.uint8, device=DEV))
+    assert float((whole[:rows].float() - out[:rows].float()).abs().max()) <= 2.0 ** -6 * float(p.v.abs().max())
+    short, _ = p.run(scratch=torch.empty(max(1, api_bytes // 2) // 16 * 16 + 16, dtype=torch.uint8, device=DEV))
+    assert torch.equal(short, whole)      # too little scratch: not split
+
+
+@pytest.mark.parametrize("fill", [float("nan"), float("inf")])
+def test_hidden_values_between_the_pieces_of_an_item(fill):
+    p = Packed([64, 3], [2500, 1500], 4, 2, 128, seed=17)
+    assert api.L.lib().eagle_op_attention_prompt_scratch_bytes(p.R, p.K, 4, 2, 128, 2) > 0
+    want, _ = p.run()
+    for at in (0, 700, 2499, 2500, 2530, 2563, 2564, 3200, 4066, 4068):
+        v = p.v[at].clone()
+        p.v[at, :, 9] = fill
+        out, _ = p.run()
+        p.v[at] = v
+        sees = torch.zeros(p.R, dtype=torch.bool, device=DEV)
+        for b in range(2):
+            if p.kstart[b] <= at < p.kstart[b + 1]:
+                first = p.start[b + 1] - (p.kstart[b + 1] - at)
+                sees[max(first, p.start[b]):p.start[b + 1]] = True
+        assert torch.equal(out[~sees], want[~sees])
+        rest = [c for c in range(128) if c != 9]
+        assert torch.equal(out[:, :, rest], want[:, :, rest])
+        if sees.any():
+            got = out[sees][:, :, 9].float()
+            assert (torch.isnan(got) | (got == fill)).all()
 
 
 def test_many_short_sequences():

@@ -100,8 +100,9 @@ def test_rope_refuses(lib):
 
 
 def prompt(lib, q=FAKE, ldq=1024, k=BIG, ldk=256, v=2 * BIG, ldv=256, out=3 * BIG, ldo=1024, lse=None, R=9, Rk=9, nq=8, nkv=2,
-           d=128, B=2, qs=FAKE, ks=FAKE):
-    return lib.eagle_op_attention_prompt(None, q, ldq, k, ldk, v, ldv, out, ldo, lse, R, Rk, nq, nkv, d, B, qs, ks, 0.0, None)
+           d=128, B=2, qs=FAKE, ks=FAKE, work=None, nb=0):
+    return lib.eagle_op_attention_prompt(None, q, ldq, k, ldk, v, ldv, out, ldo, lse, R, Rk, nq, nkv, d, B, qs, ks, 0.0, work, nb,
+                                         None)
 
 
 def test_prompt_attention_refuses(lib):
@@ -109,7 +110,7 @@ def test_prompt_attention_refuses(lib):
                dict(out=3 * BIG + 8), dict(ldq=1016), dict(ldq=1028), dict(ldk=248), dict(ldk=260), dict(ldv=128), dict(ldo=1000),
                dict(ldo=1 << 40), dict(R=-1), dict(Rk=-1), dict(nq=7), dict(nq=0), dict(nkv=0), dict(nq=130, ldq=1 << 15, ldo=1 << 15),
                dict(d=96), dict(d=256), dict(B=-1), dict(qs=None), dict(ks=None),
-               dict(out=FAKE), dict(out=FAKE + 1024), dict(out=BIG), dict(out=2 * BIG - 2048)):
+               dict(out=FAKE), dict(out=FAKE + 1024), dict(out=BIG), dict(out=2 * BIG - 2048), dict(work=FAKE + 8, nb=1 << 30)):
         assert prompt(lib, **kw) == L.EAGLE_EINVAL, kw
     assert prompt(lib, R=1 << 30, ldq=1024) == L.EAGLE_ECAPACITY and prompt(lib, Rk=2 ** 31 - 100) == L.EAGLE_ECAPACITY
     assert prompt(lib, R=0, q=None, out=None) == L.EAGLE_OK and prompt(lib, B=0) == L.EAGLE_OK

@@ -324,6 +324,15 @@ __device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
   return r;
 }
 
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 // Bounded wait of a converged warp for an mbarrier phase, looking at the abort flag and the clock every 64th time. Gives up as
 // mbar_wait does; every lane gets the same answer. (Short: it is inlined some twenty times, and the instruction cache is
 // what bounds the ends of items.)
@@ -458,7 +467,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
   extern __shared__ __align__(1024) uint8_t sm[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + Sh::OFF_BAR);
   uint64_t *full = bars, *empty = bars + ST, *looked = bars + 2 * ST /* ring */, *q_full = bars + 3 * ST /* [tile] */,
-           *q_empty = q_full + 2 /* [tile] */, *s_full = q_full + 4 /* [tile] */, *s_free = q_full + 6 /* [tile] */,
+           *s_full = q_full + 4 /* [tile] */, *s_free = q_full + 6 /* [tile] */,
            *p_full = q_full + 8 /* [tile] */, *p_free = q_full + 10 /* [tile] */, *o_done = q_full + 12 /* [tile] */,
            *o_free = q_full + 14 /* [tile] */, *l_full = q_full + 16 /* [tile] */, *l_free = q_full + 18 /* [tile] */,
            *item_full = q_full + 20 /* [slot] */, *item_empty = q_full + 22 /* [slot] */, *drain = q_full + 24 /* [tile] */;
@@ -478,7 +487,6 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(q_full + i), 1);
-      mbar_init(smem_u32(q_empty + i), 1);
       mbar_init(smem_u32(s_full + i), 1);
       mbar_init(smem_u32(s_free + i), 4);
       mbar_init(smem_u32(p_full + i), 4);
@@ -513,20 +521,48 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + Sh::T_S + mt * Sh::T_STEP + lane_off, tP = tS + KT, tO = tmem + mt * D + lane_off;
     uint32_t s_phase = 0, p_phase = 1, l_phase = 1;      // (1: a barrier's first wait passes, nobody holds what it guards)
+    // A tile's first warp brings its Q: the next item's as soon as the last S of this one is there, which no product reads Q
+    // for any more. (By the warp of the other copies these would wait for it: 64 ragged prompts MEASURED_Q.)
+    const bool brings = (warp & 3) == 0;
+    int q_next = 0, q_loads = 0;      // the first item whose Q is not under way yet; loads so far
+    auto bring = [&](const ApItem& x) {
+      if (x.n[mt] <= 0) return;
+      ++q_loads;
+      if (elect_one()) {
+        mbar_expect_tx(smem_u32(q_full + mt), (uint32_t)(Sh::HALVES * a.RB * a.G * 128));
+#pragma unroll
+        for (int y = 0; y < Sh::HALVES; ++y)
+          tma_load_3d(smem_u32(sm + mt * Sh::QB + y * Sh::QHALF), &tmQ, y * 64, x.h * a.G, x.row0 + mt * a.RB, smem_u32(q_full + mt));
+      }
+      __syncwarp();
+    };
     bool ok = true;
     for (int n = 0; ok; ++n) {
       ok = ap_wait(smem_u32(item_full + (n & 1)), (uint32_t)((n >> 1) & 1), abort_flag, a.err);
       if (!ok) break;
       const ApItem& it = items[n & 1];
       if (it.h < 0) break;
+      const bool late = brings && q_next <= n;
       const int nt = it.n[mt], first = it.lim0 + mt * a.RB;      // the last key that the tile's first row sees
       float m2 = -INFINITY, l = 0.f;
 #pragma unroll 1
-      for (int j = 0; j < nt; ++j) {
-        ok = ap_wait(smem_u32(s_full + mt), s_phase, abort_flag, a.err);
-        if (!ok) break;
-        s_phase ^= 1;
-        tc_fence_after();
+      for (int j = late ? -1 : 0; j < nt; ++j) {
+        // this item's Q if it was not known in time, the next one's behind the last S
+        if (j >= 0) {
+          ok = ap_wait(smem_u32(s_full + mt), s_phase, abort_flag, a.err);
+          if (!ok) break;
+          s_phase ^= 1;
+          tc_fence_after();
+        }
+        if (brings && (j < 0 || j + 1 == nt)) {
+          const int x = j < 0 ? n : n + 1;
+          if (j < 0 || __all_sync(0xffffffffu, mbar_test(smem_u32(item_full + (x & 1)), (uint32_t)((x >> 1) & 1)))) {
+            const ApItem& next = items[x & 1];
+            if (next.h >= 0) bring(next);
+            q_next = x + 1;
+          }
+        }
+        if (j < 0) continue;
         float s[KT];
 #pragma unroll
         for (int c = 0; c < KT / 32 * 32; c += 32) tmem_ld32_async(tS + c, s + c);
@@ -616,6 +652,8 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
       }
       warp_arrive(smem_u32(item_empty + (n & 1)));
     }
+    // a copy in flight lands before the CTA leaves
+    if (!ok && q_loads) ap_wait(smem_u32(q_full + mt), (uint32_t)((q_loads - 1) & 1), abort_flag, a.err, false);
   } else if (warp < AP_TMA) {
     // ---- results: both tiles' in turn, a quarter of the lanes a warp, while the softmax warps are at the next item ----
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Sh::R_OUT));
@@ -724,8 +762,6 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
       // ---- items, TMA ----
       ApList list{};
       ApStart at0{};      // split: where this CTA goes on
-      const uint32_t qbytes = (uint32_t)(Sh::HALVES * a.RB * a.G * 128);
-      uint32_t used = 0;                // loads of Q: of tile 0 in the low half, of tile 1 in the high half
       int s = 0;                        // stages of the ring so far
       ApItem it{}, next{};
       bool ok = true;
@@ -799,22 +835,6 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
           }
           __syncwarp();
           ++s;
-          if (x == 0)      // behind the first keys: Q, when the item before has done with its place
-#pragma unroll 1
-            for (int t = 0; ok && t < 2; ++t) {
-              if (!(t ? it.n[1] : it.n[0])) continue;
-              const uint32_t u = used >> 16 * t & 0xffff;
-              if (u) ok = ap_wait(smem_u32(q_empty + t), (u - 1) & 1, abort_flag, a.err);
-              if (!ok) break;
-              if (elect_one()) {
-                mbar_expect_tx(smem_u32(q_full + t), qbytes);
-                for (int y = 0; y < Sh::HALVES; ++y)
-                  tma_load_3d(smem_u32(sm + t * Sh::QB + y * Sh::QHALF), &tmQ, y * 64, it.h * a.G, it.row0 + t * a.RB,
-                              smem_u32(q_full + t));
-              }
-              __syncwarp();
-              used = (used & ~(0xffffu << 16 * t)) | (u + 1 == 0x10000 ? 2 : u + 1) << 16 * t;
-            }
         }
         if (ok && n >= 2) ok = ap_wait(smem_u32(item_empty + (n & 1)), (uint32_t)(((n >> 1) - 1) & 1), abort_flag, a.err);
         if (ok && next.h < 0 && n) {      // the end, unless warp 15 found something
@@ -838,14 +858,9 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
         if (next.h < 0) break;
         it = next;
       }
-      if (*abort_flag) {      // copies in flight land before the CTA leaves: the last ones of the ring and of Q
+      if (*abort_flag) {      // copies in flight land before the CTA leaves: the last ones of the ring
 #pragma unroll 1
-        for (int x = max(0, s - ST) - 2; x < s; ++x) {
-          const int t = x - (max(0, s - ST) - 2);
-          if (t < 2 && !(used >> 16 * t & 0xffff)) continue;
-          const uint32_t bar = t < 2 ? smem_u32(q_full + t) : smem_u32(full + x % ST);
-          ap_wait(bar, t < 2 ? ((used >> 16 * t & 0xffff) - 1) & 1 : (uint32_t)((x / ST) & 1), abort_flag, a.err, false);
-        }
+        for (int x = max(0, s - ST); x < s; ++x) ap_wait(smem_u32(full + x % ST), (uint32_t)((x / ST) & 1), abort_flag, a.err, false);
       }
     } else if (warp < AP_LOOK) {
       // ---- MMA: one warp a query tile ----
@@ -895,7 +910,6 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
                           IS, y ? 1u : 0u);
               tc_commit(smem_u32(s_full + mt));
               tc_commit(smem_u32(empty + st));
-              if (j + 1 == mine) tc_commit(smem_u32(q_empty + mt));
             }
             __syncwarp();
           } else {

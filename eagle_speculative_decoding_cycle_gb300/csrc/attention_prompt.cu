@@ -468,7 +468,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + Sh::OFF_BAR);
   uint64_t *full = bars, *empty = bars + ST, *looked = bars + 2 * ST /* ring */, *q_full = bars + 3 * ST /* [tile] */,
            *s_full = q_full + 4 /* [tile] */, *s_free = q_full + 6 /* [tile] */,
-           *p_full = q_full + 8 /* [tile] */, *p_free = q_full + 10 /* [tile] */, *o_done = q_full + 12 /* [tile] */,
+           *p_full = q_full + 8 /* [tile] */, *p_free = q_full + 10 /* [tile] */,
            *o_free = q_full + 14 /* [tile] */, *l_full = q_full + 16 /* [tile] */, *l_free = q_full + 18 /* [tile] */,
            *item_full = q_full + 20 /* [slot] */, *item_empty = q_full + 22 /* [slot] */, *drain = q_full + 24 /* [tile] */;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(q_full + 26);
@@ -482,7 +482,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < ST; ++i) {
       mbar_init(smem_u32(full + i), 1);
-      mbar_init(smem_u32(empty + i), 3);
+      mbar_init(smem_u32(empty + i), 3);      // either tile, warp 15
       mbar_init(smem_u32(looked + i), 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -491,7 +491,6 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
       mbar_init(smem_u32(s_free + i), 4);
       mbar_init(smem_u32(p_full + i), 4);
       mbar_init(smem_u32(p_free + i), 1);
-      mbar_init(smem_u32(o_done + i), 1);
       mbar_init(smem_u32(o_free + i), 4);
       mbar_init(smem_u32(l_full + i), 4);
       mbar_init(smem_u32(l_free + i), 4);
@@ -525,6 +524,9 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
     // for any more. (By the warp of the other copies these would wait for it: 64 ragged prompts MEASURED_Q.)
     const bool brings = (warp & 3) == 0;
     int q_next = 0, q_loads = 0;      // the first item whose Q is not under way yet; loads so far
+    // It gives the ring's stages back too: keys when their S is there, values when the product is done (an item's last ones: the
+    // warps that write the results).
+    int ring = 0;                     // stages before this item
     auto bring = [&](const ApItem& x) {
       if (x.n[mt] <= 0) return;
       ++q_loads;
@@ -543,7 +545,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
       const ApItem& it = items[n & 1];
       if (it.h < 0) break;
       const bool late = brings && q_next <= n;
-      const int nt = it.n[mt], first = it.lim0 + mt * a.RB;      // the last key that the tile's first row sees
+      const int nt = it.n[mt], both = max(it.n[0], it.n[1]), first = it.lim0 + mt * a.RB;      // the last key that the tile's first row sees
       float m2 = -INFINITY, l = 0.f;
 #pragma unroll 1
       for (int j = late ? -1 : 0; j < nt; ++j) {
@@ -553,6 +555,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
           if (!ok) break;
           s_phase ^= 1;
           tc_fence_after();
+          if (brings && elect_one()) mbar_arrive(smem_u32(empty + (ring + (j ? 2 * j - 1 : 0)) % ST));
         }
         if (brings && (j < 0 || j + 1 == nt)) {
           const int x = j < 0 ? n : n + 1;
@@ -596,6 +599,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
         ok = ap_wait(smem_u32(p_free + mt), p_phase, abort_flag, a.err);
         if (!ok) break;
         p_phase ^= 1;
+        if (brings && j > 0 && elect_one()) mbar_arrive(smem_u32(empty + (ring + 2 * j) % ST));
         tc_fence_after();
         if (j > 0 && __any_sync(0xffffffffu, raise)) {
 #pragma unroll 1
@@ -650,6 +654,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
           warp_arrive(smem_u32(l_full + mt));
         }
       }
+      ring += 2 * both;
       warp_arrive(smem_u32(item_empty + (n & 1)));
     }
     // a copy in flight lands before the CTA leaves
@@ -665,7 +670,8 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
       const int v = lane0 + x * 8 + (lane >> 2);
       at[x] = (uint32_t)(v / a.G) << 16 | (uint32_t)(v % a.G);
     }
-    uint32_t phase = 0;      // a bit a tile
+    uint32_t phase = 0, units = 0;      // a bit a tile: phase of l_full; whether its products so far are odd
+    int ring = 0;
     bool ok = true;
     for (int n = 0; ok; ++n) {
       ok = ap_wait(smem_u32(item_full + (n & 1)), (uint32_t)((n >> 1) & 1), abort_flag, a.err);
@@ -678,11 +684,15 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
         if (rows <= 0 || (SPLIT && it.slot >= 0 && !nt)) continue;
         __nv_bfloat16* base = a.out + (long long)(it.row0 + mt * a.RB) * a.ldo + (long long)it.h * a.G * D;
         if (nt) {
+          // the last product's phase of p_free: the one before is over, or l_full would not be
+          units ^= (uint32_t)(nt & 1) << mt;
           ok = ap_wait(smem_u32(l_full + mt), phase >> mt & 1, abort_flag, a.err) &&
-               ap_wait(smem_u32(o_done + mt), phase >> mt & 1, abort_flag, a.err);
+               ap_wait(smem_u32(p_free + mt), (units >> mt & 1) ^ 1, abort_flag, a.err);
           if (!ok) break;
           phase ^= 1u << mt;
           tc_fence_after();
+          if (warp == AP_SOFT && elect_one())
+            mbar_arrive(smem_u32(empty + (ring + (nt == max(it.n[0], it.n[1]) ? 2 * nt - 1 : 2 * nt)) % ST));
         }
         // Fragments of 16 rows, four threads a row, 64 columns at a time: a row's 64 bytes go out together. Rolled, as all
         // that runs once an item: what falls out of the instruction cache comes back at some ten clocks an instruction.
@@ -753,6 +763,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
           }
         }
       }
+      ring += 2 * max(it.n[0], it.n[1]);
       if (ok) warp_arrive(smem_u32(item_empty + (n & 1)));
     }
   } else {
@@ -883,7 +894,8 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
         const ApItem it = items[n & 1];
         if (it.h < 0) break;
         const int mine = mt ? it.n[1] : it.n[0], nt = max(it.n[0], it.n[1]);
-        // stage by stage: S of the keys in it, or O of the values in it; those of the other tile alone are given back
+        // Stage by stage: S of the keys in it, or O of the values in it; those of the other tile alone are given back. One commit
+        // each, which costs the issuing warp some 150 clocks: that a stage is free and O complete follows from the same.
 #pragma unroll 1
         for (int x = 0; ok && x < 2 * nt; ++x, ++s) {
           const int st = s % ST;
@@ -909,7 +921,6 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
                 ap_mma_ss(tS, dq + (((y >> 2) * Sh::QHALF + (y & 3) * 32) >> 4), k + (((y >> 2) * Sh::KHALF + (y & 3) * 32) >> 4),
                           IS, y ? 1u : 0u);
               tc_commit(smem_u32(s_full + mt));
-              tc_commit(smem_u32(empty + st));
             }
             __syncwarp();
           } else {
@@ -928,8 +939,6 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
               for (int y = 0; y < KT / 16; ++y)      // 16 keys a product
                 ap_mma_ts(tO, tP + y * 8, v + (y * 2048 >> 4), IO, y ? 1u : more);
               tc_commit(smem_u32(p_free + mt));
-              tc_commit(smem_u32(empty + st));
-              if (j + 1 == mine) tc_commit(smem_u32(o_done + mt));
             }
             __syncwarp();
           }

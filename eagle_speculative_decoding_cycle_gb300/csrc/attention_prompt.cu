@@ -20,7 +20,15 @@
 // S, softmax, P V, S ... has no overlap but the other tile's: 1.7 us for 128 keys of a pair, of them 1.06 of products and 0.54 of
 // softmax; the hand-overs between softmax and products, some 0.6 us a round, are in nobody's shadow. So P has columns of its
 // own: S of the next keys is computed as soon as the softmax warps hold this one in registers. For d = 128 that leaves
-// 80 keys a tile (S 80, P 40 of a tile's 128 columns beside O), for d = 64 128 keys (O 64, S 128, P 64 of 256).
+// 80 keys a tile (S 80, P 40 of a tile's 128 columns beside O), for d = 64 128 keys (O 64, S 128, P 64 of 256). A pair's 128 keys
+// then take 1.43 us (1.21 of products: of 80 columns they are bound by reading Q from shared memory); without any softmax
+// work 1.36: what is left is the way of S into the softmax warps and back, 1100 clocks beside its products.
+//
+// The tiles are not kept in step: each has its own warps throughout, and one runs ahead of the other as far as the ring
+// lets it. (In turn, key tile by key tile: 64 prompts of 128 to 2048 tokens of 32 heads over 8 928 us instead of 812.) What is left
+// of those, 730 us where the products take 404: 57 items a CTA, each with some 3 us until its products run and end without
+// a pause, part of it for instructions that the last item's loops have pushed out of the instruction cache (76 KB of code;
+// 110 KB of it took 893).
 // Weights are rounded to bf16 (2^-8 relative at most, as the values that they meet); maxima, sums and outputs are fp32, the
 // sum of the unrounded weights.
 //
@@ -521,7 +529,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
     const uint32_t tS = tmem + Sh::T_S + mt * Sh::T_STEP + lane_off, tP = tS + KT, tO = tmem + mt * D + lane_off;
     uint32_t s_phase = 0, p_phase = 1, l_phase = 1;      // (1: a barrier's first wait passes, nobody holds what it guards)
     // A tile's first warp brings its Q: the next item's as soon as the last S of this one is there, which no product reads Q
-    // for any more. (By the warp of the other copies these would wait for it: 64 ragged prompts MEASURED_Q.)
+    // for any more. (By the warp of the other copies these wait for it: 4096 tokens of 40 heads 157 us instead of 148.)
     const bool brings = (warp & 3) == 0;
     int q_next = 0, q_loads = 0;      // the first item whose Q is not under way yet; loads so far
     // It gives the ring's stages back too: keys when their S is there, values when the product is done (an item's last ones: the
@@ -574,7 +582,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
         tc_fence_before();
         warp_arrive(smem_u32(s_free + mt));      // S of the next keys may come
         const int last = first + pos - j * KT, all = first + low - j * KT;      // last keys seen by this row, by all of the warp's
-        // (one branch: tested 16 keys at a time, a pair's 128 keys took 1.67 us instead of MEASURED_MASK)
+        // (one branch: tested 16 keys at a time, a pair's 128 keys took 1.67 us instead of 1.43)
         if (KT - 1 > all)
 #pragma unroll
           for (int c = 0; c < KT; ++c) s[c] = c <= last ? s[c] : -INFINITY;

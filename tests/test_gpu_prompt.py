@@ -427,3 +427,49 @@ def test_rows_past_four_gigabytes():
     a, b = api.rope(plan, q, k, i32(np.arange(n)))
     api.rope(plan, view(0, 4), view(4096, 2), i32(np.arange(n)), out=(view(0, 4), view(4096, 2)))
     assert torch.equal(view(0, 4), a) and torch.equal(view(4096, 2), b)
+
+
+@pytest.mark.parametrize("nq,nkv,d,most", [(32, 8, 128, 300), (7, 7, 128, 700), (12, 12, 64, 500), (64, 4, 64, 90)])
+def test_several_items_a_cta(nq, nkv, d, most):
+    """More items than SMs, whole ones, with and without rows in their second tile: against 64 bits on the device."""
+    g = np.random.default_rng(nq)
+    lens = [int(x) for x in g.integers(0, most, 90)]
+    before = [int(x) if i % 3 == 0 else 0 for i, x in enumerate(g.integers(0, 200, 90))]
+    p = Packed(lens, before, nq, nkv, d, seed=18)
+    out, lse = p.run()
+    for b in range(90):
+        n, m = lens[b], lens[b] + before[b]
+        if n == 0:
+            continue
+        r, c = slice(p.start[b], p.start[b + 1]), slice(p.kstart[b], p.kstart[b + 1])
+        q = p.q[r].double().view(n, nkv, nq // nkv, d)
+        s = torch.einsum("nhgd,mhd->hgnm", q, p.k[c].double()) * d ** -0.5
+        reach = torch.einsum("nhgd,mhd->hgnm", q.abs(), p.k[c].double().abs()) * d ** -0.5
+        hidden = torch.ones(n, m, dtype=torch.bool, device=DEV).triu_(m - n + 1)
+        s, A = s.masked_fill(hidden, -math.inf), reach.masked_fill(hidden, 0).amax(-1)
+        P, v = torch.softmax(s, -1), p.v[c].double()
+        want, W = (torch.einsum("hgnm,mhd->nhgd", P, x).reshape(n, nq, d) for x in (v, v.abs()))
+        A = A.permute(2, 0, 1).reshape(n, nq)
+        tol = 2.0 ** -8 * want.abs() + W * (2.0 ** -8 + 2 * (d + 8) * 2.0 ** -23 * A[..., None] + (m + 64) * 2.0 ** -23)
+        assert ((out[r].double() - want).abs() <= tol).all(), b
+        wlse = torch.logsumexp(s, -1).permute(2, 0, 1).reshape(n, nq)
+        assert ((lse[r].double() - wlse).abs() <= (d + 8) * 2.0 ** -23 * A + (m + 64) * 2.0 ** -23 + 2.0 ** -22 * wlse.abs()).all(), b
+    again, _ = p.run()
+    assert torch.equal(out, again)
+
+
+def test_values_that_are_not_finite_among_many_items():
+    """The second pass over a CTA's items: results elsewhere keep their bits."""
+    g = np.random.default_rng(3)
+    lens = [int(x) for x in g.integers(1, 260, 80)]
+    p = Packed(lens, [0] * 80, 8, 8, 128, seed=19)
+    want, wlse = p.run()
+    at = [int(p.kstart[b]) + lens[b] // 2 for b in range(0, 80, 7)]
+    for i, x in enumerate(at):
+        p.v[x, i % 8, i] = (float("nan"), float("inf"), -float("inf"))[i % 3]
+    out, lse = p.run()
+    hit = torch.zeros(out.shape, dtype=torch.bool, device=DEV)
+    for i, (x, b) in enumerate(zip(at, range(0, 80, 7))):
+        hit[x:p.start[b + 1], i % 8, i] = True
+    assert torch.equal(out[~hit], want[~hit]) and torch.equal(lse, wlse)
+    assert not torch.isfinite(out[hit].float()).any()

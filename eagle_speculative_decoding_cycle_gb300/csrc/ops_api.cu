@@ -471,7 +471,7 @@ int eagle_op_rope(void* stream, int dtype_in, int dtype_out, const void* q, int6
     return EAGLE_EINVAL;
   if (R == 0) return EAGLE_OK;
   if (nq > 65536 || nkv > 65536) return EAGLE_ECAPACITY;
-  if (!pos || !turns) return EAGLE_EINVAL;
+  if (!pos || !turns || (reinterpret_cast<uintptr_t>(turns) & 7)) return EAGLE_EINVAL;
   const int64_t ei = dtype_in == EAGLE_DTYPE_F32 ? 4 : 2, eo = dtype_out == EAGLE_DTYPE_F32 ? 4 : 2;
   const struct { const void* p; int64_t ld, e, w; } rows[4] = {{q, ldq, ei, (int64_t)nq * head_dim}, {k, ldk, ei, (int64_t)nkv * head_dim},
                                                                {q_out, ldqo, eo, (int64_t)nq * head_dim}, {k_out, ldko, eo, (int64_t)nkv * head_dim}};
@@ -504,7 +504,8 @@ int eagle_op_rope(void* stream, int dtype_in, int dtype_out, const void* q, int6
 static int prompt_sizes(int R, int Rk, int nq, int nkv, int head_dim, int B) {
   if (R < 0 || Rk < 0 || nkv < 1 || nq < nkv || nq % nkv || nq / nkv > 64 || (head_dim != 64 && head_dim != 128) || B < 0)
     return EAGLE_EINVAL;
-  if ((double)R * nq >= 2147483648.0 || (double)Rk + 256 >= 2147483648.0 || nq > 65536 || B > (1 << 24)) return EAGLE_ECAPACITY;
+  // (2^27 keys keep a pair of tiles busy for 1.5 s; a wait's limit is 2 s)
+  if ((double)R * nq >= 2147483648.0 || Rk > (1 << 27) || nq > 65536 || B > (1 << 20)) return EAGLE_ECAPACITY;
   return EAGLE_OK;
 }
 
@@ -531,6 +532,15 @@ int eagle_op_attention_prompt(void* stream, const void* q, int64_t ldq, const vo
   if (rows_meet(out, ldo * 2, wq * 2, R, q, ldq * 2, wq * 2, R)) return EAGLE_EINVAL;
   if (Rk && (rows_meet(out, ldo * 2, wq * 2, R, k, ldk * 2, wk * 2, Rk) || rows_meet(out, ldo * 2, wq * 2, R, v, ldv * 2, wk * 2, Rk)))
     return EAGLE_EINVAL;
+  // the sums and the scratch memory lie outside all of them
+  const struct { const void* p; int64_t w; } own[2] = {{lse, (int64_t)R * nq * 4}, {scratch, scratch ? (int64_t)scratch_bytes : 0}};
+  for (const auto& x : own) {
+    if (!x.p || x.w <= 0) continue;
+    if (rows_meet(x.p, x.w, x.w, 1, q, ldq * 2, wq * 2, R) || rows_meet(x.p, x.w, x.w, 1, out, ldo * 2, wq * 2, R)) return EAGLE_EINVAL;
+    if (Rk && (rows_meet(x.p, x.w, x.w, 1, k, ldk * 2, wk * 2, Rk) || rows_meet(x.p, x.w, x.w, 1, v, ldv * 2, wk * 2, Rk)))
+      return EAGLE_EINVAL;
+  }
+  if (lse && scratch && rows_meet(lse, own[0].w, own[0].w, 1, scratch, own[1].w, own[1].w, own[1].w ? 1 : 0)) return EAGLE_EINVAL;
   PromptArgs a{};
   a.q = q; a.k = k; a.v = v; a.out = out; a.lse = lse;
   a.ldq = ldq; a.ldk = ldk; a.ldv = ldv; a.ldo = ldo;

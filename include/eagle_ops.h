@@ -267,7 +267,9 @@ int eagle_op_rope(void* stream, int dtype_in, int dtype_out, const void* q, int6
  * logarithm of each row's sum of exp(score), by which results over different keys can be joined. Scale =
  * 1/sqrt(head_dim) when scale <= 0. q_start, k_start: device [B + 1], read by the kernel, so that a captured call serves
  * any lengths; a sequence whose starts fall, or lie outside [0, R] or [0, Rk], is latched into *d_err (nullable) and
- * skipped. Rows of no sequence are left as they were. out meets none of q, k, v (refused).
+ * skipped (where starts fall back so often that sequences overlap, others may be skipped too). Rows of no
+ * sequence are left as they were. out meets none of q, k, v, and lse and scratch none of the others (refused). R * nq < 2^31, Rk <=
+ * 2^27, B <= 2^20 (EAGLE_ECAPACITY).
  * Products are bf16 with fp32 sums; weights enter the value product as bf16 (2^-8 relative, the type of the values);
  * maxima, sums and lse are fp32. Keys and values that a row does not see, of its own sequence too, may be anything,
  * NaN and infinities among it: its result is the same bits.

@@ -18,7 +18,7 @@ import numpy as np
 import pytest
 import torch
 
-from eagle_speculative_decoding_cycle_gb300 import api
+from eagle_speculative_decoding_cycle_gb300 import _lib as L, api
 from oracle import prompt as O
 
 pytestmark = pytest.mark.gpu
@@ -429,15 +429,9 @@ def test_rows_past_four_gigabytes():
     assert torch.equal(view(0, 4), a) and torch.equal(view(4096, 2), b)
 
 
-@pytest.mark.parametrize("nq,nkv,d,most", [(32, 8, 128, 300), (7, 7, 128, 700), (12, 12, 64, 500), (64, 4, 64, 90)])
-def test_several_items_a_cta(nq, nkv, d, most):
-    """More items than SMs, whole ones, with and without rows in their second tile: against 64 bits on the device."""
-    g = np.random.default_rng(nq)
-    lens = [int(x) for x in g.integers(0, most, 90)]
-    before = [int(x) if i % 3 == 0 else 0 for i, x in enumerate(g.integers(0, 200, 90))]
-    p = Packed(lens, before, nq, nkv, d, seed=18)
-    out, lse = p.run()
-    for b in range(90):
+def _agree_with_64_bits(p, lens, before, out, lse):
+    nq, nkv, d = p.q.shape[1], p.k.shape[1], p.q.shape[2]
+    for b in range(len(lens)):
         n, m = lens[b], lens[b] + before[b]
         if n == 0:
             continue
@@ -454,8 +448,49 @@ def test_several_items_a_cta(nq, nkv, d, most):
         assert ((out[r].double() - want).abs() <= tol).all(), b
         wlse = torch.logsumexp(s, -1).permute(2, 0, 1).reshape(n, nq)
         assert ((lse[r].double() - wlse).abs() <= (d + 8) * 2.0 ** -23 * A + (m + 64) * 2.0 ** -23 + 2.0 ** -22 * wlse.abs()).all(), b
+
+
+@pytest.mark.parametrize("nq,nkv,d,most", [(32, 8, 128, 300), (7, 7, 128, 700), (12, 12, 64, 500), (64, 4, 64, 90)])
+def test_several_items_a_cta(nq, nkv, d, most):
+    """More items than SMs, whole ones, with and without rows in their second tile: against 64 bits on the device."""
+    g = np.random.default_rng(nq)
+    lens = [int(x) for x in g.integers(0, most, 90)]
+    before = [int(x) if i % 3 == 0 else 0 for i, x in enumerate(g.integers(0, 200, 90))]
+    p = Packed(lens, before, nq, nkv, d, seed=18)
+    out, lse = p.run()
+    _agree_with_64_bits(p, lens, before, out, lse)
     again, _ = p.run()
     assert torch.equal(out, again)
+
+
+@pytest.mark.parametrize("nq,nkv,d", [(8, 1, 128), (4, 2, 64)])
+def test_lengths_far_apart(nq, nkv, d):
+    """A few rows behind many keys among many short sequences and empty ones: most levels have no pairs."""
+    g = np.random.default_rng(7)
+    lens = [int(x) for x in g.integers(0, 4, 1300)]
+    before = [0] * 1300
+    for i, (n, m) in {100: (70, 20000), 700: (1, 9000), 701: (33, 20000), 1299: (2, 40000)}.items():
+        lens[i], before[i] = n, m
+    p = Packed(lens, before, nq, nkv, d, seed=20)
+    out, lse = p.run()
+    _agree_with_64_bits(p, lens, before, out, lse)
+
+
+def test_starts_that_rise_and_fall_over_many_keys():
+    """Sequences that overlap seem to have more pairs than the rows do: latched, and nothing past the lists is touched."""
+    B, R, Rk, d = 100, 3840, 480000, 128
+    g = torch.Generator(device=DEV).manual_seed(3)
+    q = torch.randn(R, 1, d, device=DEV, generator=g).bfloat16()
+    k = torch.randn(Rk, 1, d, device=DEV, generator=g).bfloat16()
+    assert L.lib().eagle_op_attention_prompt_scratch_bytes(R, Rk, 1, 1, d, B) > 0
+    qs = torch.tensor([0, R] * (B // 2) + [0], dtype=torch.int32, device=DEV)
+    ks = torch.arange(0, Rk + 1, Rk // B, dtype=torch.int32, device=DEV)
+    for scratch in (None, torch.empty(0, dtype=torch.uint8, device=DEV)):
+        err = torch.zeros(1, dtype=torch.int32, device=DEV)
+        out = torch.zeros(R + 8, 1, d, dtype=torch.bfloat16, device=DEV)
+        api.attention_prompt(q, k, k, qs, ks, out=out[:R], err=err, scratch=scratch)
+        torch.cuda.synchronize()
+        assert err.item() == 2 and torch.isfinite(out.float()).all() and not out[R:].any()
 
 
 def test_values_that_are_not_finite_among_many_items():

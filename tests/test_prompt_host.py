@@ -112,6 +112,10 @@ def test_prompt_attention_refuses(lib):
                dict(d=96), dict(d=256), dict(B=-1), dict(qs=None), dict(ks=None),
                dict(out=FAKE), dict(out=FAKE + 1024), dict(out=BIG), dict(out=2 * BIG - 2048), dict(work=FAKE + 8, nb=1 << 30)):
         assert prompt(lib, **kw) == L.EAGLE_EINVAL, kw
+    for at in (FAKE + 1024, BIG + 512, 2 * BIG - 64, 3 * BIG):      # sums or scratch memory in the way
+        assert prompt(lib, lse=at) == L.EAGLE_EINVAL and prompt(lib, work=at, nb=4096) == L.EAGLE_EINVAL, at
+    assert prompt(lib, lse=5 * BIG, work=5 * BIG + 256, nb=64) == L.EAGLE_EINVAL
+    assert prompt(lib, Rk=(1 << 27) + 1) == L.EAGLE_ECAPACITY and prompt(lib, B=(1 << 20) + 1) == L.EAGLE_ECAPACITY
     assert prompt(lib, R=1 << 30, ldq=1024) == L.EAGLE_ECAPACITY and prompt(lib, Rk=2 ** 31 - 100) == L.EAGLE_ECAPACITY
     assert prompt(lib, R=0, q=None, out=None) == L.EAGLE_OK and prompt(lib, B=0) == L.EAGLE_OK
 

@@ -11,7 +11,8 @@ arithmetic of the method.
 Modules: philox (counter-based draws), model (target + drafters, fp64 with the
 model's rounding points), tree (EAGLE-2 policy), accept (acceptance and KV
 compaction), cycle (prefill, cycle, plain decode, planted mode), speedup (the
-tokens-per-step model).
+tokens-per-step model), ttt (the training-time-test forward), kv8 (the 8-bit cache),
+prompt (rotary positions, attention over packed prompts, blocks and accepted paths).
 
 Parity status: every function is pinned by a test against what the pages or
 mathematics fix (tests/test_oracle_*.py). The drafter's wiring (which feature and

@@ -22,13 +22,16 @@
 // own: S of the next keys is computed as soon as the softmax warps hold this one in registers. For d = 128 that leaves
 // 80 keys a tile (S 80, P 40 of a tile's 128 columns beside O), for d = 64 128 keys (O 64, S 128, P 64 of 256). A pair's 128 keys
 // then take 1.43 us (1.21 of products: of 80 columns they are bound by reading Q from shared memory); without any softmax
-// work 1.36: what is left is the way of S into the softmax warps and back, 1100 clocks beside its products.
+// work 1.36: what is left is the way of S into the softmax warps and back, 1100 clocks beside its products. (Tiles of 64 keys with two
+// P, so that no weights wait for a product: 1.79. A key tile takes its 0.9 us whatever its size.)
 //
 // The tiles are not kept in step: each has its own warps throughout, and one runs ahead of the other as far as the ring
-// lets it. (In turn, key tile by key tile: 64 prompts of 128 to 2048 tokens of 32 heads over 8 928 us instead of 812.) What is left
-// of those, 730 us where the products take 404: 57 items a CTA, each with some 3 us until its products run and end without
-// a pause, part of it for instructions that the last item's loops have pushed out of the instruction cache (76 KB of code;
-// 110 KB of it took 893).
+// lets it. (In turn, key tile by key tile: 64 prompts of 128 to 2048 tokens of 32 heads over 8 928 us instead of 812.) Those take
+// 740 us, the products of what rows see 404: 96 are for keys behind the diagonal, and 59 items a CTA have some 4 us each until
+// products follow without a pause: the last, masked softmax, then the issuing warp's way to the next item and its first S, 5100 clocks
+// where a key tile's period is 1700, and 0.9 us for results that the next item waits for. (A first S ahead of the last value
+// product: 852; what the issuing warp does besides slows every key tile. 110 KB of code instead of 80: 893.)
+//
 // Weights are rounded to bf16 (2^-8 relative at most, as the values that they meet); maxima, sums and outputs are fp32, the
 // sum of the unrounded weights.
 //

@@ -797,7 +797,7 @@ def attention_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_start:
     index, shape = q.get_device(), q.shape
     if index < 0 or q.dtype is not torch.bfloat16 or k.dtype is not torch.bfloat16 or v.dtype is not torch.bfloat16:
         raise ValueError("q, k and v must be bfloat16 tensors of a GPU")
-    d = shape[-1]
+    d = shape[-1] if len(shape) == 3 else 0
     ldq, ldk, ldv = _head_rows(q, index, d, "q"), _head_rows(k, index, d, "k"), _head_rows(v, index, d, "v")
     kshape = k.shape
     _need(kshape == v.shape, "k and v must have one shape")
@@ -837,6 +837,7 @@ def attention_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_start:
               "scratch must be a contiguous uint8 tensor on q's device")
         work, nb = scratch.data_ptr(), scratch.numel()
     rc = lib.eagle_op_attention_prompt(_stream_of(index, stream), q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv,
-                                           out.data_ptr(), ldo, _ptr(lse), R, kshape[0], nq, kshape[1], d, n - 1, q_start.data_ptr(), k_start.data_ptr(), scale, work, nb, _ptr(err))
+                                       out.data_ptr(), ldo, _ptr(lse), R, kshape[0], nq, kshape[1], d, n - 1,
+                                       q_start.data_ptr(), k_start.data_ptr(), scale, work, nb, _ptr(err))
     L.check(rc, "eagle_op_attention_prompt")
     return out

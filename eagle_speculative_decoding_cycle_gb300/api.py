@@ -742,8 +742,8 @@ def rope(plan: Rope, q: torch.Tensor, k: Optional[torch.Tensor], pos: torch.Tens
          out: Optional[Sequence[Optional[torch.Tensor]]] = None, inverse: bool = False,
          stream: Optional[torch.cuda.Stream] = None):
     """Rows q [R][nq][d] and k [R][nkv][d] (or None; fp32 or bf16, any row stride of whole 16 bytes) turned to positions
-    pos [R] (int32); inverse: turned back. Returns (q, k) of `dtype` (default: q's), contiguous, or written to `out`,
-    which may be (q, k) themselves."""
+    pos [R] (int32); inverse: turned back, and gradients of turned rows to those of the rows. Returns (q, k) of `dtype`
+    (default: q's), contiguous, or written to `out`, which may be (q, k) themselves."""
     d, index, qt = plan.head_dim, plan.index, q.dtype
     src = _KV_TYPES.get(qt)
     if src is None or index < 0:

@@ -248,9 +248,9 @@ int eagle_rope_turns(int n, const double* freq, uint64_t* turns);
 
 /* Turn the first `rot` entries of each head of R rows of q ([nq][head_dim]) and k ([nkv][head_dim]; either count may be
  * 0), row r by pos[r] * freq: pairs (x[i], x[i + rot / 2]), or (x[2i], x[2i + 1]) when interleaved, become
- * factor * (a cos - b sin, b cos + a sin), with `inverse` the same by the negative angle. Entries behind
- * `rot` are copied. head_dim 16..256 and rot 16..head_dim, multiples of 16. Types EAGLE_DTYPE_F32 or
- * _BF16, in and out independently; 16-byte aligned rows of free stride (elements, whole 16 bytes), so q
+ * factor * (a cos - b sin, b cos + a sin), with `inverse` the same by the negative angle: so a gradient with respect to
+ * turned rows becomes that with respect to the rows. Entries behind `rot` are copied. head_dim 16..256 and rot
+ * 16..head_dim, multiples of 16. Types EAGLE_DTYPE_F32 or _BF16, in and out independently; 16-byte aligned rows of free stride (elements, whole 16 bytes), so q
  * and k may be columns of a fused projection. An output may be the input it comes from (same type, rows
  * and stride); otherwise outputs meet neither an input nor each other (refused). turns: device [rot / 2].
  * Positions are any int32: the angle is taken modulo a turn without rounding, then rounded to fp32 (2^-24

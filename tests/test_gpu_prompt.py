@@ -92,6 +92,27 @@ def test_rope_back_far_and_negative_positions():
     assert float((z - x).abs().max()) < 2.0 ** -18      # two turns: each off by at most some 2^-20 of entries below 8
 
 
+@pytest.mark.parametrize("rule,d,rot,interleaved", [("plain", 128, 128, False), ("yarn", 64, 32, True), ("yarn-own", 96, 48, False)])
+def test_rope_back_is_the_gradient(rule, d, rot, interleaved):
+    """Of sum(w * rope(x)) with respect to x: against the formula in 64 bits, and against differences along some directions (the
+    map is linear: any step will do). An entry is off by at most 2^-20 m (|a| + |b|), by the arithmetic above for these
+    positions; a sum of products by the products' own sums of that."""
+    g = torch.Generator().manual_seed(d)
+    plan = api.Rope(d, rot=rot, interleaved=interleaved, scaling=RULES[rule], device=DEV)
+    pos = torch.randint(0, 100000, (50,), generator=g).numpy()
+    x, w = (torch.randn(50, 3, d, generator=g).to(DEV) for _ in range(2))
+    grad, _ = api.rope(plan, w, None, i32(pos), inverse=True)
+    check_rope(plan, RULES[rule], 1e4, w, grad, pos, interleaved, inverse=True)
+    slack = lambda t: O.rotate(host(t), pos, np.asarray(plan.freq), plan.factor, interleaved)[1]  # noqa: E731
+    for _ in range(4):
+        e = torch.randn(50, 3, d, generator=g).to(DEV)
+        up, down = x + e, x - e
+        step = host(up) - host(down)
+        rise = (host(w) * (host(api.rope(plan, up, None, i32(pos))[0]) - host(api.rope(plan, down, None, i32(pos))[0]))).sum()
+        off = 2.0 ** -20 * ((np.abs(host(w)) * (slack(up) + slack(down))).sum() + (np.abs(step) * slack(w)).sum())
+        assert abs(rise - (host(grad) * step).sum()) <= off
+
+
 def test_rope_own_frequencies_and_strides():
     g = torch.Generator().manual_seed(2)
     freq = [0.5, -1.25, 7.0, 0.0, 1e-9, 3.0, math.pi, 0.1]

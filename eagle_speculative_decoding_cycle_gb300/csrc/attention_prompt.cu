@@ -1121,8 +1121,9 @@ cudaError_t launch_prompt(cudaStream_t st, const CUtensorMap& q, const CUtensorM
 
 // Whether to split, from what the host knows, the rows and keys in all. A whole item takes its key tiles (1 us each), a range
 // its share of all items' and some AP_EXTRA more: the plan, the pieces' sums (up to 40 MB through L2) and the join. Heads of 128, 32
-// over 8, whole / split: 1 row behind 4096 keys 56 / 21 us, 61 rows 61 / 28, 512 rows behind 3584 64 / 49, 8 x 1 row behind 2048
-// (15 by the rule) 32 / 27; 4 x 200 rows behind 1800 (8) 39 / 52, a whole prompt of 1024 (2) 23 / 38.
+// over 8, whole / split: 1 row behind 4096 keys 51 / 21 us, 61 rows 55 / 27, 512 rows behind 3584 55 / 46, 8 x 1 row behind 2048
+// (15 by the rule) 30 / 27; on the other side 4 x 200 rows behind 1800 (8) 32 whole and a whole prompt of 1024 (2) 20 (split 13 and
+// 15 more).
 constexpr int AP_EXTRA = 14;
 static bool prompt_split(int R, int Rk, int G, int nkv, int d, int B, int sms) {
   const int RB = AT / G, KT = d == 128 ? ApShape<128>::KT : ApShape<64>::KT;

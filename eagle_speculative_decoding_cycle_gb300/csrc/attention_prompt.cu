@@ -101,21 +101,37 @@ __device__ __forceinline__ ApSeq ap_seq(const ApArgs& a, int b, bool& bad) {
   return bad ? ApSeq{0, 0, 0, 0} : ApSeq{r0, r1 - r0, k0, k1 - k0};
 }
 
-// The items' order. Pair t of a sequence has level t + off / (a pair's positions): proportional to its keys, nearly.
-// Items go by falling level, then sequence, then head: the last ones are the short ones, so the CTAs end together. A CTA goes
-// through the sequences twice a level that has pairs, however many items it takes: it goes on where its last one was. (From
+// The items' order. Pair t of a sequence has size t + off / (a pair's positions): proportional to its keys, nearly. A level
+// holds the sizes that agree in their highest `bits` bits: as a rule one size each. Items go by falling level, then sequence, then
+// falling size, then head: the last ones are the short ones, so the CTAs end together. A CTA goes through the sequences
+// twice a level that has pairs, however many items it takes: it goes on where its last one was. (From
 // the first sequence and the next level each time, 4096 prompts of 1 to 39 tokens of 32 heads took 5.7 ms instead of 0.93, 64 sequences
 // of which one is 512 rows behind 100000 keys 2.4 instead of 1.2.)
+//
+// One pass is B / 32 rounds of a warp, 0.43 us each. Between two of its items a CTA may go through every level, and its
+// other warps wait for that with a limit; so there are at most so many levels that their passes take AP_ROUNDS rounds, with
+// fewer bits where sequences are many and sizes far apart. (2048 single rows of 8 heads over one behind up to 16000 keys:
+// 2.1 ms, with a level for each of 1000 sizes 7.9. 2^20 sequences, all but 2000 empty, those of 2000 sizes: 42 ms, three passes.
+// Up to 64 sequences have 2048 levels, so one for each size up to some 100000 keys.)
+constexpr int AP_ROUNDS = 4096;
 struct ApList {
-  int level, next;             // the level at hand, the highest one below it that has pairs (-1: none)
+  int bits;
+  int lo, hi, next;            // the level at hand has sizes lo .. hi - 1; the largest size below it (-1: none)
   int above, upto;             // pairs of higher levels, of this and higher ones
   int b0, passed;              // the sequences that the search goes on from, pairs of this level before them
   int total;
 };
+constexpr int AP_MANY = 1 << 25;      // what sums over a lane's sequences stop at, so that a warp's stay in range
 __device__ __forceinline__ int ap_pairs(const ApArgs& a, int lq) { return (lq + 2 * a.RB - 1) / (2 * a.RB); }
 __device__ __forceinline__ int ap_first(const ApArgs& a, const ApSeq& s) { return s.lk > s.lq ? (s.lk - s.lq) / (2 * a.RB) : 0; }
 // The pairs that rows in order have at most. (Starts out of order may seem to have more; what is past this is left out.)
 __device__ __forceinline__ int ap_most(const ApArgs& a) { return a.R / (2 * a.RB) + a.B; }
+// The low bits of a size that its level leaves out, and the number of levels up to that of a size.
+__device__ __forceinline__ int ap_cut(int size, int bits) { return max(0, 32 - __clz(size) - bits); }
+__device__ __forceinline__ int ap_levels(int size, int bits) {
+  const int cut = ap_cut(size, bits);
+  return bits ? (cut << (bits - 1)) + (size >> cut) + 1 : 1;
+}
 __device__ __forceinline__ ApList ap_begin(const ApArgs& a, bool latch) {
   int total = 0, top = -1;
 #pragma unroll 1
@@ -124,25 +140,29 @@ __device__ __forceinline__ ApList ap_begin(const ApArgs& a, bool latch) {
     const ApSeq s = ap_seq(a, b, bad);
     if (bad && latch) latch_error(a.err, DEVERR_BOUNDS);
     const int T = ap_pairs(a, s.lq);
-    total = min(total + T, 1 << 25);
+    total = min(total + T, AP_MANY);
     if (T) top = max(top, ap_first(a, s) + T - 1);
   }
   ApList l{};
   l.total = min((int)__reduce_add_sync(0xffffffffu, total), ap_most(a));
   l.next = __reduce_max_sync(0xffffffffu, top);
+  const int most = max(1, AP_ROUNDS / ((a.B + 31) / 32));
+  l.bits = 30;
+#pragma unroll 1
+  while (l.next >= 0 && ap_levels(l.next, l.bits) > most) --l.bits;
   return l;
 }
 // The next level that has pairs (a converged warp).
 __device__ __forceinline__ void ap_descend(const ApArgs& a, ApList& l) {
-  const int e = l.level = l.next;
+  const int cut = ap_cut(l.next, l.bits), lo = l.lo = l.next >> cut << cut, hi = l.hi = l.next + 1;
   int n = 0, next = -1;
 #pragma unroll 1
   for (int b = threadIdx.x & 31; b < a.B; b += 32) {
     bool bad;
     const ApSeq s = ap_seq(a, b, bad);
     const int T = ap_pairs(a, s.lq), first = ap_first(a, s);
-    n += T && first <= e && e < first + T;
-    if (T && first < e) next = max(next, min(first + T, e) - 1);
+    n = min(n + max(0, min(first + T, hi) - max(first, lo)), AP_MANY);
+    if (T && first < lo) next = max(next, min(first + T, lo) - 1);
   }
   l.above = l.upto;
   l.upto += __reduce_add_sync(0xffffffffu, n);
@@ -169,14 +189,21 @@ __device__ __forceinline__ ApItem ap_item(const ApArgs& a, ApList& l, long long 
     ApSeq s{0, 0, 0, 0};
     bool bad;
     if (b < a.B) s = ap_seq(a, b, bad);
-    const int first = ap_first(a, s), t = l.level - first;
-    const unsigned who = __ballot_sync(0xffffffffu, t >= 0 && t < ap_pairs(a, s.lq));
-    const int n = __popc(who);
+    const int first = ap_first(a, s), end = min(first + ap_pairs(a, s.lq), l.hi);
+    const int here = min(max(0, end - max(first, l.lo)), AP_MANY);      // pairs of this level
+    const int n = __reduce_add_sync(0xffffffffu, here);
     if (k - l.passed >= n) {
       l.passed += n;
       continue;
     }
-    const int src = __fns(who, 0, k - l.passed + 1);
+    int upto = here;      // those of the sequences before this one with them
+#pragma unroll 1
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += y;
+    }
+    const int src = __ffs(__ballot_sync(0xffffffffu, upto > k - l.passed)) - 1;
+    const int t = end - 1 - (k - l.passed - (upto - here)) - first;      // (of that lane; the others' are of no account)
     const int p0 = t * 2 * a.RB, off = s.lk - s.lq;
     ApItem x;
     x.h = (int)(i - rank * a.nkv);

@@ -13,6 +13,7 @@ Attention: with W = sum p |v| / sum p and A the largest sum_i |q_i k_i| * scale 
   W * (n + 64) * 2^-23        n fp32 additions of the value product and of the sum, exp2 and the rescaling.
 lse: (d + 8) 2^-23 A for the scores, (n + 64) 2^-23 for the sum, and four roundings of a number of its size, 2^-22 |lse|."""
 import math
+from types import SimpleNamespace
 
 import numpy as np
 import pytest
@@ -529,3 +530,43 @@ def test_values_that_are_not_finite_among_many_items():
         hit[x:p.start[b + 1], i % 8, i] = True
     assert torch.equal(out[~hit], want[~hit]) and torch.equal(lse, wlse)
     assert not torch.isfinite(out[hit].float()).any()
+
+
+def _on_device(lens, before, nq, nkv, d, seed):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    start, kstart = np.cumsum([0] + list(lens)), np.cumsum([0] + [n + b for n, b in zip(lens, before)])
+    new = lambda rows, heads: torch.randn(int(rows), heads, d, device=DEV, dtype=torch.bfloat16, generator=g)  # noqa: E731
+    return SimpleNamespace(q=new(start[-1], nq), k=new(kstart[-1], nkv), v=new(kstart[-1], nkv), start=start, kstart=kstart)
+
+
+@pytest.mark.parametrize("nq,nkv,d", [(64, 1, 64), (8, 2, 128)])
+def test_thousands_of_lengths(nq, nkv, d):
+    """Sizes that differ from sequence to sequence, more of them than there are levels: each level holds several, of one sequence too."""
+    g = np.random.default_rng(nq)
+    before = (20000 * g.random(2500) ** 6).astype(int)
+    lens = np.where(g.random(2500) < 0.01, g.integers(1, 700, 2500), g.integers(0, 3, 2500))
+    p = _on_device(lens, before, nq, nkv, d, 21)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    lse = torch.empty(p.q.shape[:2], device=DEV)
+    out = api.attention_prompt(p.q, p.k, p.v, i32(p.start), i32(p.kstart), lse=lse, err=err)
+    assert int(err) == 0
+    _agree_with_64_bits(p, [int(x) for x in lens], [int(x) for x in before], out, lse)
+
+
+def test_a_million_sequences():
+    """As many sequences as are taken, nearly all empty, the others of as many sizes as there are of them. What a CTA goes through to
+    find its next item stays far below the limit of a wait: (levels + 2) passes, 32768 rounds each, of which one level at most
+    is taken here."""
+    B, n = 1 << 20, 2000
+    g = np.random.default_rng(22)
+    lens, before = np.zeros(B, dtype=int), np.zeros(B, dtype=int)
+    at = np.sort(g.choice(B, n, replace=False))
+    lens[at], before[at] = 1, 4 * g.permutation(n)
+    p = _on_device(lens, before, 64, 1, 64, 22)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    lse = torch.full((n, 64), math.nan, device=DEV)
+    out = torch.full((n, 64, 64), math.nan, dtype=torch.bfloat16, device=DEV)
+    api.attention_prompt(p.q, p.k, p.v, i32(p.start), i32(p.kstart), out=out, lse=lse, err=err)
+    assert int(err) == 0
+    few = SimpleNamespace(q=p.q, k=p.k, v=p.v, start=np.arange(n + 1), kstart=np.append(p.kstart[at], p.kstart[-1]))
+    _agree_with_64_bits(few, [1] * n, [int(x) for x in before[at]], out, lse)

@@ -55,6 +55,9 @@ constexpr int AP_SOFT = 8;           // softmax warps, four a tile; behind them 
 constexpr int AP_TMA = AP_SOFT + 4, AP_MMA = AP_TMA + 1, AP_LOOK = AP_TMA + 3;
 constexpr int AP_THREADS = (AP_SOFT + 8) * 32;
 constexpr float AP_LAZY = 8.f;       // binary orders that a maximum may pass its reference by
+// A wait gives up after EAGLE_WAIT_LIMIT_NS and this much for each key tile that there is: the warps that write results, and those
+// of a tile without rows, wait for a whole item. (A key tile takes 0.9 to 1.2 us at the clocks seen, so 2^27 keys of one item 1.5 to 1.9 s.)
+constexpr int AP_TILE_NS = 4000;
 constexpr uint32_t AP_NONE = 0x3fffffffu;      // three fields of ten bits, "no key"
 
 template <int D>
@@ -88,6 +91,7 @@ struct ApArgs {
   long long ldo;
   float* lse;
   int* err;
+  unsigned long long wait_ns;  // what a wait may take (AP_TILE_NS)
   float *part_o, *part_ml;     // split: [slot][2 tiles][128][D], [slot][2 tiles][128][2]
   struct ApStart* starts;      // split: [CTA]
   struct ApJoin* joins;        // split: [CTA]
@@ -385,7 +389,7 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
 // Bounded wait of a converged warp for an mbarrier phase, looking at the abort flag and the clock every 64th time. Gives up as
 // mbar_wait does; every lane gets the same answer. (Short: it is inlined some twenty times, and the instruction cache is
 // what bounds the ends of items.)
-__device__ __forceinline__ bool ap_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err, bool honor_abort = true) {
+__device__ __forceinline__ bool ap_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, const ApArgs& a, bool honor_abort = true) {
   uint64_t t0 = 0;
 #pragma unroll 1
   for (uint32_t tries = 1; !__all_sync(0xffffffffu, mbar_try(bar, parity)); ++tries) {
@@ -393,9 +397,9 @@ __device__ __forceinline__ bool ap_wait(uint32_t bar, uint32_t parity, volatile 
     if (honor_abort && __any_sync(0xffffffffu, *abort_flag)) return false;
     const uint64_t now = globaltimer();
     if (!t0) t0 = now;
-    if (__any_sync(0xffffffffu, now - t0 > EAGLE_WAIT_LIMIT_NS)) {
+    if (__any_sync(0xffffffffu, now - t0 > a.wait_ns)) {
       *abort_flag = 1;
-      latch_error(err, DEVERR_MBAR_TIMEOUT);
+      latch_error(a.err, DEVERR_MBAR_TIMEOUT);
       return false;
     }
   }
@@ -589,7 +593,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
     };
     bool ok = true;
     for (int n = 0; ok; ++n) {
-      ok = ap_wait(smem_u32(item_full + (n & 1)), (uint32_t)((n >> 1) & 1), abort_flag, a.err);
+      ok = ap_wait(smem_u32(item_full + (n & 1)), (uint32_t)((n >> 1) & 1), abort_flag, a);
       if (!ok) break;
       const ApItem& it = items[n & 1];
       if (it.h < 0) break;
@@ -600,7 +604,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
       for (int j = late ? -1 : 0; j < nt; ++j) {
         // this item's Q if it was not known in time, the next one's behind the last S
         if (j >= 0) {
-          ok = ap_wait(smem_u32(s_full + mt), s_phase, abort_flag, a.err);
+          ok = ap_wait(smem_u32(s_full + mt), s_phase, abort_flag, a);
           if (!ok) break;
           s_phase ^= 1;
           tc_fence_after();
@@ -644,7 +648,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
           l *= corr;
         }
         // the product into O before this one is done: P may be written, and O rescaled
-        ok = ap_wait(smem_u32(p_free + mt), p_phase, abort_flag, a.err);
+        ok = ap_wait(smem_u32(p_free + mt), p_phase, abort_flag, a);
         if (!ok) break;
         p_phase ^= 1;
         if (brings && j > 0 && elect_one()) mbar_arrive(smem_u32(empty + (ring + 2 * j) % ST));
@@ -695,7 +699,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
               l == 0.f ? -INFINITY : (ref + log2f(l)) * 0.693147180559945309f;
         }
         if (nt) {
-          ok = ap_wait(smem_u32(l_free + mt), l_phase, abort_flag, a.err);
+          ok = ap_wait(smem_u32(l_free + mt), l_phase, abort_flag, a);
           if (!ok) break;
           l_phase ^= 1;
           inv[mt * AT + qv] = piece ? 1.f : l == 0.f ? 0.f : 1.f / l;
@@ -706,7 +710,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
       warp_arrive(smem_u32(item_empty + (n & 1)));
     }
     // a copy in flight lands before the CTA leaves
-    if (!ok && q_loads) ap_wait(smem_u32(q_full + mt), (uint32_t)((q_loads - 1) & 1), abort_flag, a.err, false);
+    if (!ok && q_loads) ap_wait(smem_u32(q_full + mt), (uint32_t)((q_loads - 1) & 1), abort_flag, a, false);
   } else if (warp < AP_TMA) {
     // ---- results: both tiles' in turn, a quarter of the lanes a warp, while the softmax warps are at the next item ----
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Sh::R_OUT));
@@ -722,7 +726,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
     int ring = 0;
     bool ok = true;
     for (int n = 0; ok; ++n) {
-      ok = ap_wait(smem_u32(item_full + (n & 1)), (uint32_t)((n >> 1) & 1), abort_flag, a.err);
+      ok = ap_wait(smem_u32(item_full + (n & 1)), (uint32_t)((n >> 1) & 1), abort_flag, a);
       if (!ok) break;
       const ApItem& it = items[n & 1];
       if (it.h < 0) break;
@@ -734,8 +738,8 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
         if (nt) {
           // the last product's phase of p_free: the one before is over, or l_full would not be
           units ^= (uint32_t)(nt & 1) << mt;
-          ok = ap_wait(smem_u32(l_full + mt), phase >> mt & 1, abort_flag, a.err) &&
-               ap_wait(smem_u32(p_free + mt), (units >> mt & 1) ^ 1, abort_flag, a.err);
+          ok = ap_wait(smem_u32(l_full + mt), phase >> mt & 1, abort_flag, a) &&
+               ap_wait(smem_u32(p_free + mt), (units >> mt & 1) ^ 1, abort_flag, a);
           if (!ok) break;
           phase ^= 1u << mt;
           tc_fence_after();
@@ -884,7 +888,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
           if (nt == 0) break;
           const int st = s % ST;
           const bool is_v = x && (!(x & 1) || x + 1 == 2 * nt);
-          if (s >= ST) ok = ap_wait(smem_u32(empty + st), (uint32_t)((s / ST - 1) & 1), abort_flag, a.err);
+          if (s >= ST) ok = ap_wait(smem_u32(empty + st), (uint32_t)((s / ST - 1) & 1), abort_flag, a);
           if (!ok) break;
           if (elect_one()) {
             mbar_expect_tx(smem_u32(full + st), Sh::KB);
@@ -895,9 +899,9 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
           __syncwarp();
           ++s;
         }
-        if (ok && n >= 2) ok = ap_wait(smem_u32(item_empty + (n & 1)), (uint32_t)(((n >> 1) - 1) & 1), abort_flag, a.err);
+        if (ok && n >= 2) ok = ap_wait(smem_u32(item_empty + (n & 1)), (uint32_t)(((n >> 1) - 1) & 1), abort_flag, a);
         if (ok && next.h < 0 && n) {      // the end, unless warp 15 found something
-          ok = ap_wait(smem_u32(item_empty + (n - 1 & 1)), (uint32_t)((n - 1 >> 1) & 1), abort_flag, a.err);
+          ok = ap_wait(smem_u32(item_empty + (n - 1 & 1)), (uint32_t)((n - 1 >> 1) & 1), abort_flag, a);
           if (ok && *careful == 1) {
             __syncwarp();
             *careful = 2;
@@ -919,7 +923,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
       }
       if (*abort_flag) {      // copies in flight land before the CTA leaves: the last ones of the ring
 #pragma unroll 1
-        for (int x = max(0, s - ST); x < s; ++x) ap_wait(smem_u32(full + x % ST), (uint32_t)((x / ST) & 1), abort_flag, a.err, false);
+        for (int x = max(0, s - ST); x < s; ++x) ap_wait(smem_u32(full + x % ST), (uint32_t)((x / ST) & 1), abort_flag, a, false);
       }
     } else if (warp < AP_LOOK) {
       // ---- MMA: one warp a query tile ----
@@ -937,7 +941,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
       bool ok = true;
 #pragma unroll 1
       for (int n = 0; ok; ++n) {
-        ok = ap_wait(smem_u32(item_full + (n & 1)), (uint32_t)((n >> 1) & 1), abort_flag, a.err);
+        ok = ap_wait(smem_u32(item_full + (n & 1)), (uint32_t)((n >> 1) & 1), abort_flag, a);
         if (!ok) break;
         const ApItem it = items[n & 1];
         if (it.h < 0) break;
@@ -950,15 +954,15 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
           const bool is_v = x && (!(x & 1) || x + 1 == 2 * nt);
           const int j = x ? is_v ? (x - 1) >> 1 : (x + 1) >> 1 : 0;
           const uint32_t turn = (uint32_t)((s / ST) & 1);
-          ok = ap_wait(smem_u32(full + st), turn, abort_flag, a.err);
+          ok = ap_wait(smem_u32(full + st), turn, abort_flag, a);
           if (!ok) break;
           if (j >= mine) {
             if (elect_one()) mbar_arrive(smem_u32(empty + st));
             __syncwarp();
           } else if (!is_v) {
-            if (x == 0) ok = ap_wait(smem_u32(q_full + mt), (uint32_t)(used & 1), abort_flag, a.err);
+            if (x == 0) ok = ap_wait(smem_u32(q_full + mt), (uint32_t)(used & 1), abort_flag, a);
             // the softmax warps hold the S before
-            if (ok && units) ok = ap_wait(smem_u32(s_free + mt), (uint32_t)((units - 1) & 1), abort_flag, a.err);
+            if (ok && units) ok = ap_wait(smem_u32(s_free + mt), (uint32_t)((units - 1) & 1), abort_flag, a);
             if (!ok) break;
             ++units;
             tc_fence_after();
@@ -974,9 +978,9 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
           } else {
             int seen;
             if (*careful == 2 && ap_partial<KT>(it, a.RB, j, seen))      // (behind the wait for the stage: warp 15 has passed its use before)
-              ok = ap_wait(smem_u32(looked + st), turn, abort_flag, a.err);
-            if (ok && j == 0 && used) ok = ap_wait(smem_u32(o_free + mt), (uint32_t)((used - 1) & 1), abort_flag, a.err);
-            ok = ok && ap_wait(smem_u32(p_full + mt), p_phase, abort_flag, a.err);
+              ok = ap_wait(smem_u32(looked + st), turn, abort_flag, a);
+            if (ok && j == 0 && used) ok = ap_wait(smem_u32(o_free + mt), (uint32_t)((used - 1) & 1), abort_flag, a);
+            ok = ok && ap_wait(smem_u32(p_full + mt), p_phase, abort_flag, a);
             if (!ok) break;
             p_phase ^= 1;
             tc_fence_after();
@@ -998,14 +1002,14 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
       if (!ok) {      // products in flight end before the CTA frees its TMEM
         if (elect_one()) tc_commit(smem_u32(drain + mt));
         __syncwarp();
-        ap_wait(smem_u32(drain + mt), 0, abort_flag, a.err, false);
+        ap_wait(smem_u32(drain + mt), 0, abort_flag, a, false);
       }
     } else {
       // ---- value tiles that some rows see only in part ----
       int s = 0;
       bool ok = true;
       for (int n = 0; ok; ++n) {
-        ok = ap_wait(smem_u32(item_full + (n & 1)), (uint32_t)((n >> 1) & 1), abort_flag, a.err);
+        ok = ap_wait(smem_u32(item_full + (n & 1)), (uint32_t)((n >> 1) & 1), abort_flag, a);
         if (!ok) break;
         const ApItem it = items[n & 1];
         if (it.h < 0) break;
@@ -1014,7 +1018,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
         // every stage is waited for and given back, so that this warp is never a turn of the ring behind
 #pragma unroll 1
         for (int x = 0; ok && x < 2 * nt; ++x, ++s) {
-          ok = ap_wait(smem_u32(full + s % ST), (uint32_t)((s / ST) & 1), abort_flag, a.err);
+          ok = ap_wait(smem_u32(full + s % ST), (uint32_t)((s / ST) & 1), abort_flag, a);
           const bool is_v = x && (!(x & 1) || x + 1 == 2 * nt);
           const int j = (x - 1) >> 1;
           int seen;
@@ -1185,10 +1189,11 @@ int prompt_attention(cudaStream_t st, const PromptArgs& a) {
     p.joins = reinterpret_cast<ApJoin*>(p.starts + sms);
   }
   const int grid = split ? sms : (int)(most < sms ? most : sms);
+  const int KT = a.d == 128 ? ApShape<128>::KT : ApShape<64>::KT;
+  p.wait_ns = EAGLE_WAIT_LIMIT_NS + (unsigned long long)AP_TILE_NS * (a.Rk / KT + 1);
   CUtensorMap q, k, v;
   // without keys K and V are not read; their maps still need memory
   const bool none = a.Rk == 0;
-  const int KT = a.d == 128 ? ApShape<128>::KT : ApShape<64>::KT;
   if (!ap_map(&q, a.q, a.d, a.nq, a.R, a.ldq, p.G, p.RB) ||
       !ap_map(&k, none ? a.q : a.k, a.d, none ? a.nq : a.nkv, none ? a.R : a.Rk, none ? a.ldq : a.ldk, 1, KT) ||
       !ap_map(&v, none ? a.q : a.v, a.d, none ? a.nq : a.nkv, none ? a.R : a.Rk, none ? a.ldq : a.ldv, 1, KT))

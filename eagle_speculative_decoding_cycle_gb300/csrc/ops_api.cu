@@ -504,7 +504,7 @@ int eagle_op_rope(void* stream, int dtype_in, int dtype_out, const void* q, int6
 static int prompt_sizes(int R, int Rk, int nq, int nkv, int head_dim, int B) {
   if (R < 0 || Rk < 0 || nkv < 1 || nq < nkv || nq % nkv || nq / nkv > 64 || (head_dim != 64 && head_dim != 128) || B < 0)
     return EAGLE_EINVAL;
-  // (2^27 keys keep a pair of tiles busy for 1.5 s; a wait's limit is 2 s)
+  // (2^27 keys keep a pair of tiles busy for up to 2 s, which the waits' limit allows for)
   if ((double)R * nq >= 2147483648.0 || Rk > (1 << 27) || nq > 65536 || B > (1 << 20)) return EAGLE_ECAPACITY;
   return EAGLE_OK;
 }

@@ -269,7 +269,8 @@ int eagle_op_rope(void* stream, int dtype_in, int dtype_out, const void* q, int6
  * any lengths; a sequence whose starts fall, or lie outside [0, R] or [0, Rk], is latched into *d_err (nullable) and
  * skipped (where starts fall back so often that sequences overlap, others may be skipped too). Rows of no
  * sequence are left as they were. out meets none of q, k, v, and lse and scratch none of the others (refused). R * nq < 2^31, Rk <=
- * 2^27, B <= 2^20 (EAGLE_ECAPACITY).
+ * 2^27, B <= 2^20 (EAGLE_ECAPACITY). A wait inside the kernel that gives up (after 2 s and 4 us for every 80 keys of the call, 128
+ * for heads of 64) latches 1 into *d_err and leaves rows unwritten; without d_err nothing tells.
  * Products are bf16 with fp32 sums; weights enter the value product as bf16 (2^-8 relative, the type of the values);
  * maxima, sums and lse are fp32. Keys and values that a row does not see, of its own sequence too, may be anything,
  * NaN and infinities among it: its result is the same bits.

@@ -570,3 +570,24 @@ def test_a_million_sequences():
     assert int(err) == 0
     few = SimpleNamespace(q=p.q, k=p.k, v=p.v, start=np.arange(n + 1), kstart=np.append(p.kstart[at], p.kstart[-1]))
     _agree_with_64_bits(few, [1] * n, [int(x) for x in before[at]], out, lse)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_the_most_keys(d):
+    """One row behind 2^27 keys, not shared out: one CTA's item of a second or two, for which other warps wait. All keys are zero, so
+    weights are equal; a few values are 2^20, the others zero: their sum is exact and the result within its one rounding."""
+    n = 1 << 27
+    k = torch.zeros(n, 1, d, dtype=torch.bfloat16, device=DEV)
+    v = torch.zeros(n, 1, d, dtype=torch.bfloat16, device=DEV)
+    g = torch.Generator(device=DEV).manual_seed(d)
+    at = torch.randint(0, n, (3000,), device=DEV, generator=g)
+    at[:4] = torch.tensor([0, 1, n - 2, n - 1], device=DEV)
+    v[at, 0, torch.randint(0, d, (3000,), device=DEV, generator=g)] = 2.0 ** 20
+    q = torch.randn(1, 1, d, device=DEV, generator=g).bfloat16()
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    lse = torch.zeros(1, 1, device=DEV)
+    out = api.attention_prompt(q, k, v, i32([0, 1]), i32([0, n]), lse=lse, err=err, scratch=torch.empty(0, dtype=torch.uint8, device=DEV))
+    assert int(err) == 0
+    want = (v[:, 0] != 0).sum(0).double() * 2.0 ** 20 / n
+    assert want.sum() > 0 and torch.all((out[0, 0].double() - want).abs() <= 2.0 ** -8 * want)
+    assert abs(float(lse) - math.log(n)) <= 2.0 ** -22 * math.log(n)

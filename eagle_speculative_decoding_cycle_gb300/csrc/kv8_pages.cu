@@ -124,8 +124,13 @@ __global__ void __launch_bounds__(PLAN_THREADS, 1) kv8_plan_k(const PlanArgs a) 
         for (int j = lane; j < a.tab_w; j += 32) {
           const int e = __ldcg(row + j);
           if (j < nb) {
-            missing += e < 0;
-            last = j == end ? e : last;
+            if (e >= a.n_blocks) {      // no block: a missing entry
+              latch_error(a.err, DEVERR_BOUNDS);
+              row[j] = -1;
+            }
+            const bool there = e >= 0 && e < a.n_blocks;
+            missing += !there;
+            last = j == end && there ? e : last;
           } else if (e >= 0) {
             row[j] = -1;
             release(a, e);
@@ -168,9 +173,7 @@ __global__ void __launch_bounds__(PLAN_THREADS, 1) kv8_plan_k(const PlanArgs a) 
     if (b < a.B) {
       const int e = tail[b];
       v = need[b];
-      if (e >= a.n_blocks) {
-        latch_error(a.err, DEVERR_BOUNDS);
-      } else if (e >= 0 && __ldcg(a.refs + e) > 1) {
+      if (e >= 0 && __ldcg(a.refs + e) > 1) {
         state[b] = state[b] | PLAN_LAST;
         ++v;
       }

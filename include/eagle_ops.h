@@ -215,8 +215,9 @@ int eagle_op_kv8_compact(void* stream, const eagle_kv8* caches, int layers, int 
  * in all layers: what a sequence writes at length[b] and behind is never seen by another. A block
  * that loses its last holder by (d) is free from the next call on.
  * length[b] past cap, and a parent that is out of range, is b itself, takes part in the call or lacks a
- * block, are latched into *d_err (2) and leave b as it was; so is an entry outside the pool or a
- * count that does not match the table (the entry is cleared). Too few free blocks: latched (3); the entries that come
+ * block, are latched into *d_err (2) and leave b as it was. An entry outside the pool in a sequence that takes part is
+ * latched (2) and cleared, so a slot that is to have a block gets one by (c); so is an entry that is released while its
+ * block's count is zero already (counts of entries that stay are not looked at). Too few free blocks: latched (3); the entries that come
  * first in the order have theirs, the others stay -1, and a block that should have been copied
  * stays shared. scratch: no initial value, not shared with a call that may overlap on the GPU. */
 size_t eagle_op_kv8_resize_scratch_bytes(const eagle_kv8* cache);

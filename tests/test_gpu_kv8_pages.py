@@ -394,3 +394,28 @@ def test_a_run_from_prompts_to_cycles():
             live = [0, 1, 2, 4]
     flat = [e for t in table.tolist() for e in t if e >= 0]
     assert [flat.count(i) for i in range(n)] == ls.refs.tolist()
+
+
+@pytest.mark.parametrize("length,at", [([48, 20], (0, 1)), ([40, 20], (0, 2)), ([40, 20], (0, 0)), ([33, 32], (1, 1)), ([48, -1], (1, 0)),
+                                       ([16, 20], (0, 2))])
+@pytest.mark.parametrize("entry", [12, 99, 2 ** 31 - 1])
+def test_an_entry_outside_the_pool_among_those_that_stay(length, at, entry):
+    """It is latched and counts as missing: its slots get a block. (A sequence that takes no part keeps it, unnoticed.)"""
+    p = Pool(2, 3, 12)
+    p.step([48, 32])
+    p.table[at] = entry
+    takes_part = length[at[0]] >= 0
+    p.t[at[0]][at[1]] = -1 if takes_part else entry
+    p.step(length, code=2 if takes_part else 0)
+    p.step([48, 48] if takes_part else [48, -1])
+
+
+def test_an_entry_outside_the_pool_at_a_shared_end():
+    """The last entry, partly filled, of a fork that steps back: nothing is copied from it, and its block is a new one."""
+    p = Pool(3, 3, 12)
+    p.step([48, -1, -1])
+    p.step([-1, 48, 48], [-1, 0, 0])
+    p.table[1, 1] = 12
+    p.t[1][1] = -1
+    assert p.step([-1, 20, -1], code=2) == []
+    assert len(p.step([-1, -1, 20])) == 1

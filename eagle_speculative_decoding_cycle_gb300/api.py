@@ -707,11 +707,13 @@ class Rope:
                 names = {"linear": (), "ntk": (), "llama3": ("original", "low_freq_factor", "high_freq_factor"),
                          "yarn": ("original",)}[kind]
                 _need(all(k in x for k in ("factor",) + names), f"scaling {kind} needs factor " + " ".join(names))
-                if kind == "yarn":
-                    lo, hi = x.pop("beta_slow", 1.0), x.pop("beta_fast", 32.0)
-                else:
-                    lo, hi = x.pop("low_freq_factor", 0.0), x.pop("high_freq_factor", 0.0)
-                s = L.RopeScaling(L.ROPE_KINDS[kind], x.pop("factor"), x.pop("original", 0.0), lo, hi, x.pop("attention", 0.0))
+                by, original, lo, hi, attention = x.pop("factor"), 0.0, 0.0, 0.0, 0.0
+                if kind == "llama3":
+                    original, lo, hi = x.pop("original"), x.pop("low_freq_factor"), x.pop("high_freq_factor")
+                elif kind == "yarn":
+                    original, lo, hi = x.pop("original"), x.pop("beta_slow", 1.0), x.pop("beta_fast", 32.0)
+                    attention = x.pop("attention", 0.0)
+                s = L.RopeScaling(L.ROPE_KINDS[kind], by, original, lo, hi, attention)
                 _need(not x, "scaling has entries that the rule does not: " + ", ".join(map(str, x)))
             L.check(lib.eagle_rope_frequencies(self.rot, theta, None if s is None else C.byref(s), f, C.byref(m)),
                     "eagle_rope_frequencies")

@@ -198,3 +198,15 @@ def test_binding_refuses_layers(lib):
     for path in (torch.zeros(2, dtype=torch.int32), torch.zeros(3, 2, dtype=torch.int32), torch.zeros(2, 2)):
         with pytest.raises(ValueError):
             api.kv8_compact(paged, n, n, path)
+
+
+@pytest.mark.parametrize("kind,own", [("linear", {}), ("ntk", {}), ("llama3", dict(low_freq_factor=1.0, high_freq_factor=4.0, original=8192)),
+                                      ("yarn", dict(original=4096, beta_fast=32.0, beta_slow=1.0, attention=1.25))])
+@pytest.mark.parametrize("name", ["original", "attention", "low_freq_factor", "high_freq_factor", "beta_fast", "beta_slow"])
+def test_entries_of_another_rule_are_refused(lib, kind, own, name):
+    """A rule takes its own entries and no other rule's: what would be without effect is not taken in silence."""
+    rule = dict(kind=kind, factor=4.0, **own)
+    api.Rope(64, scaling=rule, device="cpu")
+    if name not in own:
+        with pytest.raises(ValueError):
+            api.Rope(64, scaling={**rule, name: 2.0}, device="cpu")

@@ -605,7 +605,7 @@ def attention_kv8(q: torch.Tensor, cache: KV8Cache, row_seq: torch.Tensor, row_s
 
 # ---- layers of an 8-bit cache: blocks and accepted paths -----------------------------------------------
 class KV8Layers:
-    """The 8-bit caches of a model's layers (KV8Cache, one shape), contiguous or over one block table. Paged: refs int32
+    """The 8-bit caches of a model's layers (KV8Cache, one shape, each in memory of its own), contiguous or over one block table. Paged: refs int32
     [n_blocks] counts the table entries that hold each block (None: counted from the table here)."""
 
     def __init__(self, caches: Sequence[KV8Cache], refs: Optional[torch.Tensor] = None):
@@ -614,6 +614,8 @@ class KV8Layers:
         for x in caches:
             _need(x.index == c.index and x.k.shape == c.k.shape and _ptr(x.table) == _ptr(c.table) and
                   x.max_batch == c.max_batch, "the layers must have one shape, device and block table")
+        spans = sorted((t.data_ptr(), t.data_ptr() + t.numel()) for x in caches for t in (x.k, x.v, x.k_exp, x.v_exp))
+        _need(all(end <= start for (_, end), (start, _) in zip(spans, spans[1:])), "the layers' arrays must not overlap")
         self.caches, self.n = list(caches), len(caches)
         self.device, self.index, self.max_batch, self.table, self.n_blocks = c.device, c.index, c.max_batch, c.table, c.n_blocks
         self.c = (L.KV8 * self.n)(*[x.c for x in caches])

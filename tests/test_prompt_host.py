@@ -210,3 +210,19 @@ def test_entries_of_another_rule_are_refused(lib, kind, own, name):
     if name not in own:
         with pytest.raises(ValueError):
             api.Rope(64, scaling={**rule, name: 2.0}, device="cpu")
+
+
+def test_layers_that_share_memory_are_refused(lib):
+    """Given twice, a layer's accepted paths would be moved twice, the second time from what the first one wrote."""
+    t = torch.full((2, 2), -1, dtype=torch.int32)
+    pool = [torch.zeros(2 * 64 * 48 * 2 * 16, dtype=torch.uint8) for _ in range(2)]
+    codes = lambda p, at: p[at:at + 3 * 2 * 16 * 64].view(3, 2, 16, 64)  # noqa: E731
+    exps = lambda: torch.zeros(3, 2, 16, dtype=torch.uint8)  # noqa: E731
+    one = api.KV8Cache(codes(pool[0], 0), codes(pool[1], 0), exps(), exps(), t)
+    beside = api.KV8Cache(codes(pool[0], 6144), codes(pool[1], 6144), exps(), exps(), t)
+    assert api.KV8Layers([beside, one]).n == 2
+    for bad in ([one, one], [beside, one, beside], [one, api.KV8Cache(codes(pool[0], 4096), codes(pool[1], 6144), exps(), exps(), t)],
+                [one, api.KV8Cache(codes(pool[0], 6144), codes(pool[1], 6144), exps(), one.v_exp, t)],
+                [api.KV8Cache(one.k, one.k, exps(), exps(), t)]):
+        with pytest.raises(ValueError):
+            api.KV8Layers(bad)

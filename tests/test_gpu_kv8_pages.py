@@ -419,3 +419,27 @@ def test_an_entry_outside_the_pool_at_a_shared_end():
     p.t[1][1] = -1
     assert p.step([-1, 20, -1], code=2) == []
     assert len(p.step([-1, -1, 20])) == 1
+
+
+@pytest.mark.parametrize("B", [2047, 2048, 2049, 5000])
+def test_thousands_of_sequences(B):
+    """Both sides of what the plan hands on in shared memory: forks, steps back into shared blocks, too few blocks, bad entries."""
+    g = np.random.default_rng(B)
+    p = Pool(B, 3, 3 * B, layers=2, nkv=1, d=64, block=16, seed=B)
+    p.step(g.integers(0, 49, B))
+    copies = 0
+    for _ in range(3):
+        have = np.asarray([sum(e >= 0 for e in t) for t in p.t]) * 16
+        forks = g.random(B) < 0.4
+        forks[-1] = True
+        parent = np.where(forks, g.choice(np.flatnonzero(~forks), B), -1)
+        length = np.where(forks, g.integers(0, 49, B) % (have[parent] + 1), -1)
+        p.scribble()
+        copies += len(p.step(length, parent))
+        p.scribble()
+        copies += len(p.step(np.where(g.random(B) < 0.5, g.integers(0, 49, B), -1)))
+    assert copies > B // 4
+    p.table[B - 1, 0] = 3 * B
+    p.t[B - 1][0] = -1
+    p.step(np.full(B, 40), code=2)
+    p.step(np.zeros(B))

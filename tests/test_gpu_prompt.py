@@ -591,3 +591,26 @@ def test_the_most_keys(d):
     want = (v[:, 0] != 0).sum(0).double() * 2.0 ** 20 / n
     assert want.sum() > 0 and torch.all((out[0, 0].double() - want).abs() <= 2.0 ** -8 * want)
     assert abs(float(lse) - math.log(n)) <= 2.0 ** -22 * math.log(n)
+
+
+def test_rows_of_skipped_sequences_are_left_alone():
+    """Starts that fall or lie outside, no two sequences over the same rows: only rows of the valid ones are written, sums too."""
+    p = Packed([30, 40, 20, 50], [0, 0, 0, 0], 4, 2, 128, seed=23, extra=0)
+    want, wlse = p.run()
+    s = p.start.tolist()
+    for qs, ks in ((s, s[:2] + [29] + s[3:]), (s, s[:4] + [141]), (s[:4] + [2 ** 31 - 1], s), ([-1] + s[1:], s), (s, [-2 ** 31] + s[1:]),
+                   (s, s[:2] + [-1] + s[3:])):
+        fine = [b for b in range(4) if 0 <= qs[b] <= qs[b + 1] <= p.R and 0 <= ks[b] <= ks[b + 1] <= p.K]
+        assert 2 <= len(fine) < 4
+        for scratch in (None, torch.empty(0, dtype=torch.uint8, device=DEV)):
+            out, lse = torch.full_like(want, 7.0), torch.full_like(wlse, 7.0)
+            err = torch.zeros(1, dtype=torch.int32, device=DEV)
+            api.attention_prompt(p.q, p.k, p.v, i32(qs), i32(ks), out=out, lse=lse, err=err, scratch=scratch)
+            assert int(err) == 2
+            valid = torch.zeros(p.R, dtype=torch.bool, device=DEV)
+            for b in fine:
+                valid[s[b]:s[b + 1]] = True
+            same = [b for b in fine if ks[b] == s[b] and ks[b + 1] == s[b + 1]]
+            assert torch.all(out[~valid] == 7) and torch.all(lse[~valid] == 7), (qs, ks)
+            for b in same:
+                assert torch.equal(out[s[b]:s[b + 1]], want[s[b]:s[b + 1]]) and torch.equal(lse[s[b]:s[b + 1]], wlse[s[b]:s[b + 1]])

@@ -375,9 +375,12 @@ int eagle_op_kv8_compact(void* stream, const eagle_kv8* caches, int layers, int 
   return EAGLE_ECAPACITY;
 }
 
+// Entries are counted in 32 bits.
+static bool kv8_table_fits(const Kv8& c) { return (int64_t)c.max_batch * c.tab_w <= 0x7fffffff; }
+
 size_t eagle_op_kv8_resize_scratch_bytes(const eagle_kv8* cache) {
   Kv8 c;
-  if (kv8_view(cache, c) != EAGLE_OK || !c.table) return 0;
+  if (kv8_view(cache, c) != EAGLE_OK || !c.table || !kv8_table_fits(c)) return 0;
   return kv8_resize_scratch(c);
 }
 
@@ -390,6 +393,7 @@ int eagle_op_kv8_resize(void* stream, const eagle_kv8* caches, int layers, int B
   if (!c.table || B < 0 || B > c.max_batch) return EAGLE_EINVAL;
   if (B == 0) return EAGLE_OK;
   if (!refs || !length) return EAGLE_EINVAL;
+  if (!kv8_table_fits(c)) return EAGLE_ECAPACITY;
   if (!scratch || !on16(scratch) || scratch_bytes < kv8_resize_scratch(c)) return EAGLE_ECAPACITY;
   r = kv8_resize(reinterpret_cast<cudaStream_t>(stream), c, l.data(), layers, B, refs, parent, length, scratch, d_err);
   return r == 0 ? EAGLE_OK : (r == -1 ? EAGLE_ECAPACITY : EAGLE_ECUDA);

@@ -219,7 +219,8 @@ int eagle_op_kv8_compact(void* stream, const eagle_kv8* caches, int layers, int 
  * latched (2) and cleared, so a slot that is to have a block gets one by (c); so is an entry that is released while its
  * block's count is zero already (counts of entries that stay are not looked at). Too few free blocks: latched (3); the entries that come
  * first in the order have theirs, the others stay -1, and a block that should have been copied
- * stays shared. scratch: no initial value, not shared with a call that may overlap on the GPU. */
+ * stays shared. scratch: no initial value, not shared with a call that may overlap on the GPU. A table of 2^31 entries and
+ * more is refused (EAGLE_ECAPACITY, scratch bytes 0). */
 size_t eagle_op_kv8_resize_scratch_bytes(const eagle_kv8* cache);
 int eagle_op_kv8_resize(void* stream, const eagle_kv8* caches, int layers, int B, int32_t* refs, const int32_t* parent,
                         const int32_t* length, void* scratch, size_t scratch_bytes, int32_t* d_err);

@@ -226,3 +226,13 @@ def test_layers_that_share_memory_are_refused(lib):
                 [api.KV8Cache(one.k, one.k, exps(), exps(), t)]):
         with pytest.raises(ValueError):
             api.KV8Layers(bad)
+
+
+def test_tables_of_too_many_entries_are_refused(lib):
+    """Missing entries are counted in 32 bits: a count that passed them would have assigned nothing and said nothing."""
+    wide = 2 ** 31 - 16      # slots of a sequence: 2^27 - 1 blocks of 16
+    for most, cap, fits in ((16, wide, True), (17, wide, False), (2 ** 27, 16 * 16, False), (2 ** 27 - 1, 16 * 16, True), (2 ** 20, wide, False)):
+        c = layers(max_batch=most, cap=cap)
+        assert (lib.eagle_op_kv8_resize_scratch_bytes(c) > 0) == fits, (most, cap)
+        if not fits:
+            assert resize(lib, c, nb=1 << 60) == L.EAGLE_ECAPACITY

@@ -443,3 +443,49 @@ def test_thousands_of_sequences(B):
     p.t[B - 1][0] = -1
     p.step(np.full(B, 40), code=2)
     p.step(np.zeros(B))
+
+
+def test_captured_forks_and_moves():
+    """A captured fork, moves in all layers and resize, replayed for other parents, lengths and paths."""
+    p = Pool(5, 6, 40, layers=3)
+    p.step([60, 40, -1, -1, -1])
+    parent, length, kept = i32([-1] * 5), i32([-1] * 5), i32([-1] * 5)
+    n_old, took, path = i32([0] * 5), i32([0] * 5), i32(np.zeros((5, 4)))
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        api.kv8_fork(p.layers, parent, length)
+        api.kv8_compact(p.layers, n_old, took, path)
+        api.kv8_resize(p.layers, kept)
+    p.same()
+    for par, n, moves in (([-1, -1, 0, 0, 1], [-1, -1, 60, 33, 40], {2: [50, 3, 8], 3: [20], 4: [30, 7]}),
+                          ([-1, -1, 1, -1, -1], [-1, -1, 17, 96, 50], {0: [5, 4], 2: [10], 3: [60, 70, 80, 90]})):
+        # places inside a sequence's last block, which is its own (sequence 0: a block that nobody holds any more)
+        at = [40 if b == 0 else 0 if m < 0 else max((m - 1) // 16 * 16, m - 5) for b, m in enumerate(n)]
+        paths = np.zeros((5, 4), dtype=int)
+        count = [0] * 5
+        for b, slots in moves.items():
+            paths[b, :len(slots)] = [s - at[b] for s in slots]
+            count[b] = len(slots)
+        keep = [-1 if b < 2 else at[b] + count[b] + 1 for b in range(5)]
+        for t, x in ((parent, par), (length, n), (kept, keep), (n_old, at), (took, count), (path, paths)):
+            t.copy_(i32(x))
+        p.scribble()
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        place = lambda b, s: (p.t[b][s // 16], s % 16)  # noqa: E731
+        copies = [O.resize(p.t, p.r, n, 16, par)[0]]
+        for src, dst, m in copies[0]:
+            for w in p.want:
+                w[:, dst, :, :m] = w[:, src, :, :m]
+        for w in p.want:
+            old = w.clone()
+            for b in range(5):
+                for j in range(1, count[b] + 1):
+                    (db, ds), (sb, ss) = place(b, at[b] + j), place(b, at[b] + paths[b, j - 1])
+                    w[:, db, :, ds] = old[:, sb, :, ss]
+        for src, dst, m in O.resize(p.t, p.r, keep, 16)[0]:
+            for w in p.want:
+                w[:, dst, :, :m] = w[:, src, :, :m]
+        p.same()

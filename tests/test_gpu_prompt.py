@@ -614,3 +614,32 @@ def test_rows_of_skipped_sequences_are_left_alone():
             assert torch.all(out[~valid] == 7) and torch.all(lse[~valid] == 7), (qs, ks)
             for b in same:
                 assert torch.equal(out[s[b]:s[b + 1]], want[s[b]:s[b + 1]]) and torch.equal(lse[s[b]:s[b + 1]], wlse[s[b]:s[b + 1]])
+
+
+def test_a_captured_call_of_few_rows_over_many_keys():
+    """Keys shared out, its scratch memory made during the capture: replayed for other lengths, beside a second graph with scratch
+    memory of its own, it gives what a call gives."""
+    p = Packed([60, 3], [2500, 3500], 8, 2, 128, seed=24, extra=0)
+    assert L.lib().eagle_op_attention_prompt_scratch_bytes(p.R, p.K, 8, 2, 128, 2) > 0
+    qs, ks = i32(p.start), i32(p.kstart)
+    outs, graphs, streams = [], [], [torch.cuda.Stream() for _ in range(2)]
+    for st in streams:
+        o, s = torch.zeros(63, 8, 128, dtype=torch.bfloat16, device=DEV), torch.zeros(63, 8, device=DEV)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=st):
+            api.attention_prompt(p.q, p.k, p.v, qs, ks, out=o, lse=s)
+        outs.append((o, s)), graphs.append(g)
+    for rows, keys in (([60, 3], [2560, 3503]), ([0, 63], [0, 6063]), ([62, 1], [63, 6000]), ([63, 0], [40, 6000]), ([1, 62], [6001, 62])):
+        a, b = i32(np.cumsum([0] + rows)), i32(np.cumsum([0] + keys))
+        qs.copy_(a), ks.copy_(b)
+        torch.cuda.synchronize()
+        for _ in range(3):
+            for g, st in zip(graphs, streams):
+                with torch.cuda.stream(st):
+                    g.replay()
+        torch.cuda.synchronize()
+        lse = torch.zeros(63, 8, device=DEV)
+        want = api.attention_prompt(p.q, p.k, p.v, a, b, lse=lse)
+        for o, s in outs:
+            assert torch.equal(o, want) and torch.equal(s, lse)

@@ -605,8 +605,8 @@ def attention_kv8(q: torch.Tensor, cache: KV8Cache, row_seq: torch.Tensor, row_s
 
 # ---- layers of an 8-bit cache: blocks and accepted paths -----------------------------------------------
 class KV8Layers:
-    """The 8-bit caches of a model's layers (KV8Cache, one shape, each in memory of its own), contiguous or over one block table. Paged: refs int32
-    [n_blocks] counts the table entries that hold each block (None: counted from the table here)."""
+    """The 8-bit caches of a model's layers (KV8Cache, one shape, each in memory of its own), contiguous or over one block
+    table. Paged: refs int32 [n_blocks] counts the table entries that hold each block (None: counted from the table here)."""
 
     def __init__(self, caches: Sequence[KV8Cache], refs: Optional[torch.Tensor] = None):
         _need(len(caches) > 0, "at least one layer")

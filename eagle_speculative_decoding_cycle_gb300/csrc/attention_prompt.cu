@@ -10,9 +10,10 @@
 // tiles (2 RB positions of one KV head) with all the keys that its rows see, KT at a time. A CTA an SM takes items in
 // turn, the ones with the most keys first. 16 warps:
 //   warps 0-3, 4-7  softmax of tile 0 / 1, one thread a query vector (TMEM lane): S row -> weights as bf16 in TMEM, running sum;
-//                   O is rescaled only when the maximum moves by more than 2^8;
+//                   O is rescaled only when the maximum moves by more than 2^8; a tile's first warp brings its Q by TMA and gives
+//                   the ring's stages back;
 //   warps 8-11      results: O of both tiles from TMEM, divided by the sums;
-//   warp 12         finds the items; TMA: Q of each tile, K and V tiles through one ring;
+//   warp 12         finds the items, brings the next one's Q into L2; TMA: K and V tiles through one ring;
 //   warps 13, 14    tcgen05.mma of tile 0 / 1: S = Q K^T (operands in shared memory), O += P V (P in TMEM, V read MN-major);
 //   warp 15         looks through value tiles that not all rows see (below).
 //
@@ -27,13 +28,15 @@
 //
 // The tiles are not kept in step: each has its own warps throughout, and one runs ahead of the other as far as the ring
 // lets it. (In turn, key tile by key tile: 64 prompts of 128 to 2048 tokens of 32 heads over 8 928 us instead of 812.) Those take
-// 740 us, the products of what rows see 404: 96 are for keys behind the diagonal, and 59 items a CTA have some 4 us each until
+// 740 us in a short burst (800 to 850 in a stream of calls, at the clocks of the power cap), the products of what rows see 404 (450):
+// 96 are for keys behind the diagonal, and 59 items a CTA have some 4 us each until
 // products follow without a pause: the last, masked softmax, then the issuing warp's way to the next item and its first S, 5100 clocks
 // where a key tile's period is 1700, and 0.9 us for results that the next item waits for. (A first S ahead of the last value
 // product: 852; what the issuing warp does besides slows every key tile. 110 KB of code instead of 80: 893.)
 //
 // Weights are rounded to bf16 (2^-8 relative at most, as the values that they meet); maxima, sums and outputs are fp32, the
-// sum of the unrounded weights.
+// sum of the unrounded weights. That rounding is what results are off by beyond their own: 64-bit arithmetic with weights rounded
+// as here is off the exact results by 0.0021 relative (1024 tokens of 32 heads; rounded results alone: 0.0016), the kernel off it by 0.00006.
 //
 // A weight of zero does not hide a value that is not finite (0 * inf = NaN). Warp 15 looks through the value tiles that some
 // rows see only in part, beside the products. Where it finds such a value the CTA takes all its items again, now with the
@@ -1151,10 +1154,16 @@ cudaError_t launch_prompt(cudaStream_t st, const CUtensorMap& q, const CUtensorM
 }  // namespace
 
 // Whether to split, from what the host knows, the rows and keys in all. A whole item takes its key tiles (1 us each), a range
-// its share of all items' and some AP_EXTRA more: the plan, the pieces' sums (up to 40 MB through L2) and the join. Heads of 128, 32
-// over 8, whole / split: 1 row behind 4096 keys 51 / 21 us, 61 rows 55 / 27, 512 rows behind 3584 55 / 46, 8 x 1 row behind 2048
-// (15 by the rule) 30 / 27; on the other side 4 x 200 rows behind 1800 (8) 32 whole and a whole prompt of 1024 (2) 20 (split 13 and
-// 15 more).
+// its share of all items' and some AP_EXTRA more: the plan, the pieces' sums (up to 40 MB through L2) and the join. Measured with
+// every case split, whole / split in us, behind the tiles that the rule compares with AP_EXTRA:
+//   heads of 128, 32 over 8 unless said: 1 row behind 4096 keys (48) 50 / 20, 61 rows (49) 56 / 27, 512 rows behind 3584 (30) 56 / 47,
+//   of 40 heads over 40 (24) 57 / 55, 8 x 1 row behind 2048 (14.8) 29 / 28, 1 row behind 1200 (14.2) 20 / 16, 700 rows behind 700 of 8 over
+//   1 (15.0) 24.6 / 25.4; below it 256 rows behind 1024
+//   (12.6) 23 / 25, 4 x 200 rows behind 1800 (8) 33 / 48, a whole prompt of 1024 (2) 21 / 42;
+//   heads of 64: 1 row behind 4096 (30) 38 / 18, 512 rows behind 3584 of 12 over 12 (27) 49 / 27, 1024 rows behind 2048 of 8 over 1 (19)
+//   40 / 29; below it 2 x 64 rows behind 1500 of 10 over 5 (11.4) 19 / 22, 1 row behind 1500 (11.3) 17.6 / 16.1, 8 x 1 row behind 2048 of
+//   32 over 8 (9) 23 / 24, a whole prompt of 1024 (1) 18 / 29, of 4096 of 12 over 12 (-8) 50 / 73.
+// The longest item is taken for the mean: one long sequence among short ones is not split.
 constexpr int AP_EXTRA = 14;
 static bool prompt_split(int R, int Rk, int G, int nkv, int d, int B, int sms) {
   const int RB = AT / G, KT = d == 128 ? ApShape<128>::KT : ApShape<64>::KT;

@@ -8,7 +8,7 @@
 // kv8_plan_k, one CTA, phases with a barrier between them:
 //   rows      a warp a sequence: which take part (a fork's parent keeps its entries during the call and has all that are
 //             shared); entries past the last block, and all that a fork held, released; a fork's taken from its parent's;
-//             counts down and up (integer atomics: any order). Entries that are missing are counted;
+//             counts down and up (integer atomics: any order). Entries that are missing, or lie outside the pool, are counted;
 //   last      a thread a sequence: its last block, if that is partly filled and others hold it too, is to be replaced: the
 //             sequence would write where they read. Exclusive sums of the entries wanted over the sequences;
 //   find      that many free blocks in rising order, 16 counts a thread at a time;

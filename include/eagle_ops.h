@@ -191,7 +191,8 @@ int eagle_op_attention_shared_kv8(void* stream, const eagle_kv8* cache, const vo
 
 /* ---- blocks and accepted paths of an 8-bit cache's layers -----------------------------------------
  * caches: HOST array of one eagle_kv8 a layer, read during the call; all layers have one shape and
- * one table, and each has arrays of its own (a layer given twice would be moved twice, in any order). Calls on one table (and writes of the cache) change it and are ordered by the caller.
+ * one table, and each has arrays of its own (a layer given twice would be moved twice, in any
+ * order). Calls on one table (and writes of the cache) change it and are ordered by the caller.
  *
  * Accepted paths to their committed slots, in all layers and heads: slot n_old[b] + j receives what
  * slot n_old[b] + acc_path[b][j - 1] held, j = 1..acc_len[b], for sequences b < B (n_old, acc_len [B],
